@@ -1,0 +1,601 @@
+// adj_lin.cu -- linear attention with a decay for each head in plain fp32 arithmetic: the
+// chunked forward and backward passes and the single-token step.  include/adj.h defines
+// the operators.
+//
+// Chunked form, chunks of C tokens.  With D_ij the decay from token j to token i >= j of a
+// chunk (LinDecay), f_i the decay from before the chunk to i, l_j from j to the chunk's end,
+// and S the state that enters the chunk:
+//     o_i = scale (sum_{j <= i} D_ij (q_i . k_j) v_j + f_i q_i S)
+//     S'  = f_{C-1} S + sum_j l_j k_j v_j^T
+// and with w_i = scale go_i and Z the adjoint state (the cotangent of S'):
+//     dq_i = sum_{j <= i} D_ij (w_i . v_j) k_j + f_i S w_i
+//     dk_j = sum_{i >= j} D_ij (w_i . v_j) q_i + l_j Z v_j
+//     dv_j = sum_{i >= j} D_ij (q_i . k_j) w_i + l_j Z^T k_j
+//     Z_before = f_{C-1} Z + sum_i f_i q_i w_i^T
+// dg_t is the sum of everything whose decay passes through token t: pairs j < t <= i inside
+// the chunk with W_ij = D_ij (w_i . v_j)(q_i . k_j), sources j < t that leave the chunk,
+// tokens i >= t that read the entering state, and the state that crosses the whole chunk:
+//     dg_t = sum_{i >= t > j} W_ij + sum_{j < t} l_j k_j . Z v_j + sum_{i >= t} f_i q_i . S w_i
+//            + f_{C-1} <Z, S>.
+// The first sum is taken as suffix sums of (row sums - column sums) of W without its
+// diagonal; no term is a difference of larger ones across chunks.
+//
+// Passes: (1) every chunk's own contribution to the state, in parallel; (2) a scan over the
+// chunks, element by element of the state; (3) every chunk's outputs, in parallel.
+#include <algorithm>
+
+#include "adj_lin.cuh"
+#include "adj_profile.cuh"
+
+namespace adj {
+namespace {
+
+constexpr int LC = 64;          // tokens of a chunk
+constexpr int LP = 132;         // row pitch of a [*][128] fp32 tile: rows 4 banks apart
+constexpr int PP = 68;          // row pitch of a [64][64] tile
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ void ld4(const float *p, float (&v)[4]) {
+    const float4 x = __ldg(reinterpret_cast<const float4 *>(p));
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+}
+__device__ __forceinline__ void ld4(const __nv_bfloat16 *p, float (&v)[4]) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void st1(float *p, float x) { *p = x; }
+__device__ __forceinline__ void st1(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+
+// tile[t][d] = mul * x[t * ld + d] for t < LC, d < D; rows past len are zeros
+template <class T>
+__device__ __forceinline__ void load_tile(float *tile, const void *x, int64_t ld, int D, int len, float mul = 1.f) {
+    const int n4 = D >> 2;
+    for (int i = threadIdx.x; i < LC * n4; i += blockDim.x) {
+        const int t = i / n4, d = (i - t * n4) << 2;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (t < len) ld4(static_cast<const T *>(x) + t * ld + d, v);
+        *reinterpret_cast<float4 *>(tile + t * LP + d) = make_float4(v[0] * mul, v[1] * mul, v[2] * mul, v[3] * mul);
+    }
+}
+
+// acc[r][c] += sum_k A(ty + 16 r, k) B(k, tx + 16 c) with A at a[row * AR + k * AK] and B at
+// b[k * BK + col * BC]; columns past `cols` are left out.
+template <int R, int NC, int AR, int AK, int BK, int BC>
+__device__ __forceinline__ void mm(float (&acc)[R][NC], const float *a, const float *b, int K, int cols) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    a += ty * AR;
+    b += tx * BC;
+#pragma unroll 2
+    for (int k = 0; k < K; k += 4) {
+        float x[R][4];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (AK == 1) {
+                const float4 f = *reinterpret_cast<const float4 *>(a + r * 16 * AR + k);
+                x[r][0] = f.x; x[r][1] = f.y; x[r][2] = f.z; x[r][3] = f.w;
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) x[r][u] = a[r * 16 * AR + (k + u) * AK];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            if (16 * c >= cols) break;
+            float y[4];
+            if (BK == 1) {
+                const float4 f = *reinterpret_cast<const float4 *>(b + c * 16 * BC + k);
+                y[0] = f.x; y[1] = f.y; y[2] = f.z; y[3] = f.w;
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) y[u] = b[(k + u) * BK + c * 16 * BC];
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) acc[r][c] = fmaf(x[r][u], y[u], acc[r][c]);
+        }
+    }
+}
+
+struct At {                     // one chunk of one head
+    int64_t b, h, hk, n, t0, seq;
+    int len;
+    __device__ At(const LinArgs &a) {
+        n = blockIdx.x;
+        h = blockIdx.y;
+        b = blockIdx.z;
+        hk = h / (a.H / a.Hk);
+        t0 = n * LC;
+        len = int(a.T - t0 < LC ? a.T - t0 : LC);
+        seq = b * a.T + t0;
+    }
+    __device__ int64_t state(const LinArgs &a) const { return ((b * a.H + h) * a.NC + n) * a.Dk * a.Dv; }
+};
+template <class T>
+__device__ __forceinline__ const T *row(const void *p, int64_t tok, int64_t ld, int64_t head, int D) {
+    return static_cast<const T *>(p) + tok * ld + head * D;
+}
+
+// Pass 1.  REV = false: S[n] = sum_j l_j k_j v_j^T; true: dS[n] = sum_i f_i q_i w_i^T.
+template <class T, bool REV>
+__global__ __launch_bounds__(256) void k_lin_chunk_state(const LinArgs a) {
+    extern __shared__ float sm[];
+    float *A = sm, *B = A + LC * LP;
+    __shared__ LinDecay<LC> D;
+    const At at(a);
+    if (threadIdx.x < 32) D.fill(a.g + at.seq * a.H + at.h, a.H, at.len);
+    if (REV) {
+        load_tile<T>(A, row<T>(a.q, at.seq, a.ldq, at.hk, a.Dk), a.ldq, a.Dk, at.len);
+        load_tile<T>(B, row<T>(a.go, at.seq, a.ldo, at.h, a.Dv), a.ldo, a.Dv, at.len, a.scale);
+    } else {
+        load_tile<T>(A, row<T>(a.k, at.seq, a.ldk, at.hk, a.Dk), a.ldk, a.Dk, at.len);
+        load_tile<T>(B, row<T>(a.v, at.seq, a.ldv, at.h, a.Dv), a.ldv, a.Dv, at.len);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < LC * a.Dv; i += 256) {
+        const int t = i / a.Dv, d = i - t * a.Dv;
+        B[t * LP + d] *= REV ? D.first(t) : D.last(t);
+    }
+    __syncthreads();
+    float acc[8][8] = {};
+    mm<8, 8, 1, LP, LP, 1>(acc, A, B, LC, a.Dv);
+    float *S = (REV ? a.dS : a.S) + at.state(a);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int d = ty + 16 * r, e = tx + 16 * c;
+            if (d < a.Dk && e < a.Dv) S[d * a.Dv + e] = acc[r][c];
+        }
+    if (threadIdx.x == 0) a.tot[(at.b * a.H + at.h) * a.NC + at.n] = D.total();
+}
+
+// Pass 2.  Every chunk's contribution is replaced by the state that enters it (REV: by the
+// adjoint state that its exit receives); one thread carries four elements through the chunks.
+template <bool REV>
+__global__ __launch_bounds__(128) void k_lin_scan(const LinArgs a) {
+    const int64_t n4 = int64_t(a.Dk) * a.Dv / 4, blocks = (n4 + 127) / 128, bh = blockIdx.x / blocks;
+    const int64_t i = (blockIdx.x - bh * blocks) * 128 + threadIdx.x;
+    if (i >= n4) return;
+    const float *init = REV ? a.ds1 : a.s0;
+    float *fin = REV ? a.ds0 : a.s1;
+    float4 c = init ? reinterpret_cast<const float4 *>(init)[bh * n4 + i] : f4(0.f);
+    float4 *S = reinterpret_cast<float4 *>(REV ? a.dS : a.S) + bh * a.NC * n4 + i;
+    const float *tot = a.tot + bh * a.NC;
+    constexpr int U = 8;        // loads in flight
+    for (int64_t m = 0; m < a.NC; m += U) {
+        float4 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (m + u < a.NC) x[u] = S[(REV ? a.NC - 1 - m - u : m + u) * n4];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (m + u < a.NC) {
+                const int64_t n = REV ? a.NC - 1 - m - u : m + u;
+                S[n * n4] = c;
+                c = fma4(f4(tot[n]), c, x[u]);
+            }
+    }
+    if (fin) reinterpret_cast<float4 *>(fin)[bh * n4 + i] = c;
+}
+
+__device__ __forceinline__ void load_state(float *tile, const float *S, int Dk, int Dv) {
+    const int n4 = Dv >> 2;
+    for (int i = threadIdx.x; i < Dk * n4; i += blockDim.x) {
+        const int d = i / n4, e = (i - d * n4) << 2;
+        *reinterpret_cast<float4 *>(tile + d * LP + e) = *reinterpret_cast<const float4 *>(S + int64_t(d) * Dv + e);
+    }
+}
+
+// Pass 3 of the forward pass.
+template <class T>
+__global__ __launch_bounds__(256) void k_lin_out(const LinArgs a) {
+    extern __shared__ float sm[];
+    float *Q = sm, *K = Q + LC * LP, *V = K + LC * LP, *S = V + LC * LP, *P = S + 128 * LP;
+    __shared__ LinDecay<LC> D;
+    const At at(a);
+    if (threadIdx.x < 32) D.fill(a.g + at.seq * a.H + at.h, a.H, at.len);
+    load_tile<T>(Q, row<T>(a.q, at.seq, a.ldq, at.hk, a.Dk), a.ldq, a.Dk, at.len);
+    load_tile<T>(K, row<T>(a.k, at.seq, a.ldk, at.hk, a.Dk), a.ldk, a.Dk, at.len);
+    load_tile<T>(V, row<T>(a.v, at.seq, a.ldv, at.h, a.Dv), a.ldv, a.Dv, at.len);
+    load_state(S, a.S + at.state(a), a.Dk, a.Dv);
+    __syncthreads();
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float p[4][4] = {};
+    mm<4, 4, LP, 1, 1, LP>(p, Q, K, a.Dk, LC);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int i = ty + 16 * r, j = tx + 16 * c;
+            P[i * PP + j] = j <= i ? p[r][c] * D.pair(i, j) : 0.f;
+        }
+    float acc[4][8] = {};
+    mm<4, 8, LP, 1, LP, 1>(acc, Q, S, a.Dk, a.Dv);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const float f = D.first(ty + 16 * r);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[r][c] *= f;
+    }
+    __syncthreads();
+    mm<4, 8, PP, 1, LP, 1>(acc, P, V, LC, a.Dv);
+    T *o = static_cast<T *>(a.o) + at.seq * a.ldo + at.h * a.Dv;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int i = ty + 16 * r, e = tx + 16 * c;
+            if (i < at.len && e < a.Dv) st1(o + i * a.ldo + e, acc[r][c] * a.scale);
+        }
+}
+
+// sum over the 16 threads of a row of the thread grid
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+    for (int d = 8; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
+    return x;
+}
+
+// dq or dk of one head: to the output, or (shared heads) to the fp32 partials
+template <class T>
+__device__ __forceinline__ void put_grad(const LinArgs &a, const At &at, const float (&acc)[4][8], void *out, float *part,
+                                         int64_t ld) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int i = ty + 16 * r, d = tx + 16 * c;
+            if (i >= at.len || d >= a.Dk) continue;
+            if (part) part[((at.seq + i) * a.H + at.h) * a.Dk + d] = acc[r][c];
+            else st1(static_cast<T *>(out) + (at.seq + i) * ld + at.hk * a.Dk + d, acc[r][c]);
+        }
+}
+
+// Pass 3 of the backward pass.
+template <class T>
+__global__ __launch_bounds__(256) void k_lin_grad(const LinArgs a) {
+    extern __shared__ float sm[];
+    float *Q = sm, *K = Q + LC * LP, *V = K + LC * LP, *W = V + LC * LP, *S = W + LC * LP, *P = S + 128 * LP;
+    __shared__ LinDecay<LC> D;
+    __shared__ float fs[LC], cs[LC], rs[LC], zs[8];
+    const At at(a);
+    if (threadIdx.x < 32) D.fill(a.g + at.seq * a.H + at.h, a.H, at.len);
+    load_tile<T>(Q, row<T>(a.q, at.seq, a.ldq, at.hk, a.Dk), a.ldq, a.Dk, at.len);
+    load_tile<T>(K, row<T>(a.k, at.seq, a.ldk, at.hk, a.Dk), a.ldk, a.Dk, at.len);
+    load_tile<T>(V, row<T>(a.v, at.seq, a.ldv, at.h, a.Dv), a.ldv, a.Dv, at.len);
+    load_tile<T>(W, row<T>(a.go, at.seq, a.ldo, at.h, a.Dv), a.ldo, a.Dv, at.len, a.scale);
+    load_state(S, a.S + at.state(a), a.Dk, a.Dv);
+    __syncthreads();
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+
+    // R_ij = D_ij (w_i . v_j), P_ij = D_ij (q_i . k_j); row and column sums of W = R (q . k)
+    float p[4][4] = {}, x[4][4] = {};
+    mm<4, 4, LP, 1, 1, LP>(p, Q, K, a.Dk, LC);
+    mm<4, 4, LP, 1, 1, LP>(x, W, V, a.Dv, LC);
+    float col[4] = {};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int i = ty + 16 * r, j = tx + 16 * c;
+            const float d = j <= i ? D.pair(i, j) : 0.f;
+            x[r][c] = j <= i ? x[r][c] * d : 0.f;
+            const float w = j < i ? x[r][c] * p[r][c] : 0.f;
+            p[r][c] = j <= i ? p[r][c] * d : 0.f;
+            sum += w;
+            col[c] += w;
+        }
+        sum = row_sum(sum);
+        if (tx == 0) rs[ty + 16 * r] = sum;
+    }
+    // column sums over the 16 thread rows, in a fixed order, through P
+#pragma unroll
+    for (int c = 0; c < 4; ++c) P[ty * PP + tx + 16 * c] = col[c];
+    __syncthreads();
+    if (threadIdx.x < LC) {
+        float s = 0.f;
+        for (int y = 0; y < 16; ++y) s += P[y * PP + threadIdx.x];
+        rs[threadIdx.x] -= s;
+    }
+    __syncthreads();
+    // dq
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) P[(ty + 16 * r) * PP + tx + 16 * c] = x[r][c];
+    {
+        float acc[4][8] = {};
+        mm<4, 8, LP, 1, 1, LP>(acc, W, S, a.Dv, a.Dk);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = ty + 16 * r;
+            const float f = D.first(i);
+            float dot = 0.f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                acc[r][c] *= f;
+                if (tx + 16 * c < a.Dk) dot = fmaf(acc[r][c], Q[i * LP + tx + 16 * c], dot);
+            }
+            dot = row_sum(dot);
+            if (tx == 0) fs[i] = dot;
+        }
+        __syncthreads();        // P holds R
+        mm<4, 8, PP, 1, LP, 1>(acc, P, K, LC, a.Dk);
+        put_grad<T>(a, at, acc, a.dq, a.pq, a.ldq);
+    }
+    // <Z, S>, then Z in S's place
+    {
+        const float *Z = a.dS + at.state(a);
+        const int n4 = a.Dv >> 2;
+        float dot = 0.f;
+        for (int i = threadIdx.x; i < a.Dk * n4; i += 256) {
+            const int d = i / n4, e = (i - d * n4) << 2;
+            float4 *s = reinterpret_cast<float4 *>(S + d * LP + e);
+            const float4 z = *reinterpret_cast<const float4 *>(Z + int64_t(d) * a.Dv + e), y = *s;
+            dot += z.x * y.x + z.y * y.y + z.z * y.z + z.w * y.w;
+            *s = z;             // every thread of the block is past its reads of S (the barrier above)
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(~0u, dot, d);
+        if ((threadIdx.x & 31) == 0) zs[threadIdx.x >> 5] = dot;
+        __syncthreads();
+    }
+    // dk
+    {
+        float acc[4][8] = {};
+        mm<4, 8, LP, 1, 1, LP>(acc, V, S, a.Dv, a.Dk);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int j = ty + 16 * r;
+            const float l = D.last(j);
+            float dot = 0.f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                acc[r][c] *= l;
+                if (tx + 16 * c < a.Dk) dot = fmaf(acc[r][c], K[j * LP + tx + 16 * c], dot);
+            }
+            dot = row_sum(dot);
+            if (tx == 0) cs[j] = dot;
+        }
+        mm<4, 8, 1, PP, LP, 1>(acc, P, Q, LC, a.Dk);
+        put_grad<T>(a, at, acc, a.dk, a.pk, a.ldk);
+    }
+    __syncthreads();            // P is free, cs is written
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) P[(ty + 16 * r) * PP + tx + 16 * c] = p[r][c];
+    // dv
+    {
+        float acc[4][8] = {};
+        mm<4, 8, LP, 1, LP, 1>(acc, K, S, a.Dk, a.Dv);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float l = D.last(ty + 16 * r);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[r][c] *= l;
+        }
+        __syncthreads();
+        mm<4, 8, 1, PP, LP, 1>(acc, P, W, LC, a.Dv);
+        T *dv = static_cast<T *>(a.dv) + at.seq * a.ldv + at.h * a.Dv;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const int j = ty + 16 * r, e = tx + 16 * c;
+                if (j < at.len && e < a.Dv) st1(dv + j * a.ldv + e, acc[r][c]);
+            }
+    }
+    // dg
+    if (threadIdx.x < LC) {
+        const int t = threadIdx.x;
+        float across = 0.f, reads = 0.f, inside = 0.f;
+        for (int w = 0; w < 8; ++w) across += zs[w];
+        across *= D.total();
+        for (int j = 0; j < t; ++j) across += cs[j];
+        for (int i = LC - 1; i >= t; --i) {
+            reads += fs[i];
+            inside += rs[i];
+        }
+        const int64_t n = (at.seq + t) * a.H + at.h;
+        if (t < at.len) {
+            const bool cut = t ? D.r[t] != D.r[t - 1] : D.r[0] != 0;
+            // no pair of the chunk crosses its first token
+            a.dg[n] = cut ? 0.f : across + reads + (t ? inside : 0.f);
+        }
+    }
+}
+
+// Shared heads: out[token][hk][d] = sum over the group's heads of part[token][h][d].
+template <class T>
+__global__ __launch_bounds__(256) void k_lin_share(const LinArgs a) {
+    const int n4 = a.Dk >> 2, rep = a.H / a.Hk;
+    const int64_t n = a.B * a.T * a.Hk * n4;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+        const int d = int(i % n4) << 2;
+        const int64_t r = i / n4, hk = r % a.Hk, tok = r / a.Hk;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const float *p = (w ? a.pk : a.pq) + (tok * a.H + hk * rep) * a.Dk + d;
+            float4 s = f4(0.f);
+            for (int h = 0; h < rep; ++h) s = s + ld_stream4(p + int64_t(h) * a.Dk);
+            st4(static_cast<T *>(w ? a.dk : a.dq) + tok * (w ? a.ldk : a.ldq) + hk * a.Dk + d, s);
+        }
+    }
+}
+
+// The step.  A block owns `cols` state columns (a multiple of 4) of one sequence's head;
+// thread (rg, cg) carries four columns of the rows rg, rg + RG, ...: S <- a S + k v^T and its
+// part of q S, whose sum over rg is taken through shared memory.  Bound by the state's 8 Dk Dv
+// bytes; columns are split further when there are few heads, to use more SMs.
+template <class T>
+__global__ __launch_bounds__(256) void k_lin_step(const LinArgs a, float *__restrict__ state, int64_t n_slots,
+                                                  const int32_t *__restrict__ slots, int cols) {
+    __shared__ float q[128], k[128];
+    __shared__ float4 part[256];
+    const int64_t bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
+    const int e0 = blockIdx.y * cols, w4 = min(cols, a.Dv - e0) >> 2, RG = 256 / w4;
+    const int cg = threadIdx.x % w4, rg = threadIdx.x / w4;
+    const int64_t slot = slots ? slots[b] : b;
+    T *o = static_cast<T *>(a.o) + b * a.ldo + h * a.Dv + e0 + 4 * cg;
+    if (slot < 0 || slot >= n_slots) {
+        if (rg == 0) st4(o, f4(0.f));
+        return;
+    }
+    float *S = state + ((slot * a.H + h) * a.Dk) * a.Dv + e0 + 4 * cg;
+    constexpr int U = 8;
+    float4 s[U];
+    if (rg < RG)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (rg + u * RG < a.Dk) s[u] = *reinterpret_cast<const float4 *>(S + int64_t(rg + u * RG) * a.Dv);
+    const float decay = expf(a.g[b * a.H + h]);
+    if (threadIdx.x < a.Dk) {
+        q[threadIdx.x] = float(row<T>(a.q, b, a.ldq, hk, a.Dk)[threadIdx.x]) * a.scale;
+        k[threadIdx.x] = float(row<T>(a.k, b, a.ldk, hk, a.Dk)[threadIdx.x]);
+    }
+    float v[4];
+    ld4(row<T>(a.v, b, a.ldv, h, a.Dv) + e0 + 4 * cg, v);
+    __syncthreads();
+    float4 acc = f4(0.f);
+    if (rg < RG) {
+        const float4 vv = make_float4(v[0], v[1], v[2], v[3]);
+        for (int d0 = rg; d0 < a.Dk; d0 += U * RG) {
+            if (d0 != rg)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (d0 + u * RG < a.Dk) s[u] = *reinterpret_cast<const float4 *>(S + int64_t(d0 + u * RG) * a.Dv);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int d = d0 + u * RG;
+                if (d >= a.Dk) break;
+                // a decay of zero drops the old state whatever it holds
+                s[u] = decay == 0.f ? f4(k[d]) * vv : fma4(f4(decay), s[u], f4(k[d]) * vv);
+                *reinterpret_cast<float4 *>(S + int64_t(d) * a.Dv) = s[u];
+                acc = fma4(f4(q[d]), s[u], acc);
+            }
+        }
+    }
+    part[threadIdx.x] = acc;
+    __syncthreads();
+    if (rg == 0) {
+        for (int r = 1; r < RG; ++r) acc = acc + part[r * w4 + cg];
+        st4(o, acc);
+    }
+}
+
+template <class K>
+cudaError_t big_smem(K kern, size_t bytes) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+}
+
+#define LIN_CUDA(x)                           \
+    do {                                      \
+        cudaError_t e_ = (x);                 \
+        if (e_ != cudaSuccess) return e_;     \
+    } while (0)
+
+constexpr size_t SM_STATE = size_t(2 * LC * LP) * 4, SM_OUT = size_t(3 * LC * LP + 128 * LP + LC * PP) * 4,
+                 SM_GRAD = size_t(4 * LC * LP + 128 * LP + LC * PP) * 4;
+
+template <class T, bool REV>
+cudaError_t states(const LinArgs &a, cudaStream_t st) {
+    const dim3 grid(unsigned(a.NC), a.H, unsigned(a.B));
+    if (a.NC) {
+        ProfScope ps(K_LIN_STATE, st);
+        LIN_CUDA(big_smem(k_lin_chunk_state<T, REV>, SM_STATE));
+        k_lin_chunk_state<T, REV><<<grid, 256, SM_STATE, st>>>(a);
+        LIN_CUDA(cudaGetLastError());
+    }
+    ProfScope ps(K_LIN_SCAN, st);
+    k_lin_scan<REV><<<unsigned(cdiv(int64_t(a.Dk) * a.Dv, 512) * a.B * a.H), 128, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t fwd(const LinArgs &a, cudaStream_t st) {
+    LIN_CUDA((states<T, false>(a, st)));
+    if (a.NC == 0) return cudaSuccess;
+    ProfScope ps(K_LIN_OUT, st);
+    LIN_CUDA(big_smem(k_lin_out<T>, SM_OUT));
+    k_lin_out<T><<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, SM_OUT, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t bwd(const LinArgs &a, cudaStream_t st) {
+    LIN_CUDA((states<T, false>(a, st)));
+    LIN_CUDA((states<T, true>(a, st)));
+    if (a.NC == 0) return cudaSuccess;
+    {
+        ProfScope ps(K_LIN_GRAD, st);
+        LIN_CUDA(big_smem(k_lin_grad<T>, SM_GRAD));
+        k_lin_grad<T><<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, SM_GRAD, st>>>(a);
+        LIN_CUDA(cudaGetLastError());
+    }
+    if (a.pq) {
+        ProfScope ps(K_LIN_SHARE, st);
+        const int64_t n = cdiv(a.B * a.T * a.Hk * (a.Dk / 4), 256);
+        k_lin_share<T><<<unsigned(std::min<int64_t>(n, 152 * 16)), 256, 0, st>>>(a);
+        LIN_CUDA(cudaGetLastError());
+    }
+    return cudaSuccess;
+}
+
+inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+int64_t lin_chunks(int64_t T, bool) { return cdiv(T, LC); }
+
+static size_t carve(LinArgs &a, bool bwd, bool, char *base) {
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        float *p = base ? reinterpret_cast<float *>(base + off) : nullptr;
+        off += al256(bytes);
+        return p;
+    };
+    const size_t st = size_t(a.B * a.H) * a.NC * a.Dk * a.Dv * 4;
+    a.S = take(st);
+    a.tot = take(size_t(a.B * a.H) * a.NC * 4);
+    a.dS = a.pq = a.pk = nullptr;
+    if (bwd) {
+        a.dS = take(st);
+        if (a.Hk < a.H) {
+            a.pq = take(size_t(a.B * a.T) * a.H * a.Dk * 4);
+            a.pk = take(size_t(a.B * a.T) * a.H * a.Dk * 4);
+        }
+    }
+    return off;
+}
+
+size_t lin_ws_bytes(const LinArgs &a, bool bwd, bool bf16) {
+    LinArgs t = a;
+    return carve(t, bwd, bf16, nullptr);
+}
+void lin_ws_carve(LinArgs &a, bool bwd, bool bf16, void *base) { carve(a, bwd, bf16, static_cast<char *>(base)); }
+
+cudaError_t launch_lin_fwd(const LinArgs &a, bool bf16, unsigned *, cudaStream_t st) {
+    return bf16 ? fwd<__nv_bfloat16>(a, st) : fwd<float>(a, st);
+}
+cudaError_t launch_lin_bwd(const LinArgs &a, bool bf16, unsigned *, cudaStream_t st) {
+    return bf16 ? bwd<__nv_bfloat16>(a, st) : bwd<float>(a, st);
+}
+cudaError_t launch_lin_step(const LinArgs &a, bool bf16, float *state, int64_t n_slots, const int32_t *slots,
+                            cudaStream_t st) {
+    ProfScope ps(K_LIN_STEP, st);
+    int cols = a.Dv;
+    while (cols % 8 == 0 && cols > 32 && a.B * a.H * cdiv(a.Dv, cols) < 152) cols /= 2;
+    const dim3 grid(unsigned(a.B * a.H), unsigned(cdiv(a.Dv, cols)));
+    if (bf16) k_lin_step<__nv_bfloat16><<<grid, 256, 0, st>>>(a, state, n_slots, slots, cols);
+    else k_lin_step<float><<<grid, 256, 0, st>>>(a, state, n_slots, slots, cols);
+    return cudaGetLastError();
+}
+
+}  // namespace adj

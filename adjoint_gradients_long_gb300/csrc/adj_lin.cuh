@@ -1,0 +1,103 @@
+// adj_lin.cuh -- linear attention with a decay for each head: what its kernels share.
+#pragma once
+#include "adj_internal.cuh"
+
+namespace adj {
+
+// One call, sizes and arrays resolved on the host.
+struct LinArgs {
+    int64_t B, T, NC;           // NC chunks a sequence
+    int H, Hk, Dk, Dv;
+    int64_t ldq, ldk, ldv, ldo; // elements between tokens
+    float scale;
+    const void *q, *k, *v, *go;
+    const float *g, *s0, *ds1;
+    void *o, *dq, *dk, *dv;
+    float *s1, *dg, *ds0;
+    float *S, *dS;              // [B,H,NC,Dk,Dv]: the states entering / adjoint states leaving each chunk
+    float *tot;                 // [B,H,NC]: the decay over each chunk
+    float *pq, *pk;             // Hk < H: dq, dk of every head [B,T,H,Dk] fp32, summed afterwards
+};
+
+// exp(g) below this is under half the smallest fp32: the decay is zero, a new start.
+constexpr float LIN_RESET = -104.f;
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The decays of one chunk.  With g_t the tokens' log decays in powers of two, G_t their
+// inclusive sum from the chunk's start and r_t the number of new starts up to t, the decay
+// from token j to token i >= j is 2^(G_i - G_j) where r_i = r_j, and zero otherwise.  G is kept
+// as a pair hi + lo, so that a difference of two long sums is as exact as a short sum.
+template <int C>
+struct LinDecay {
+    float hi[C], lo[C];
+    int r[C];
+
+    // from token j to token i; j <= i
+    __device__ __forceinline__ float pair(int i, int j) const {
+        return r[i] == r[j] ? fast_exp2((hi[i] - hi[j]) + (lo[i] - lo[j])) : 0.f;
+    }
+    // from before the chunk to token i, from token j to the chunk's end
+    __device__ __forceinline__ float first(int i) const { return r[i] == 0 ? fast_exp2(hi[i] + lo[i]) : 0.f; }
+    __device__ __forceinline__ float last(int j) const { return pair(C - 1, j); }
+    __device__ __forceinline__ float total() const { return first(C - 1); }
+
+    // by one whole warp: g[n * pitch], n < len (tokens past len have decay 1)
+    __device__ void fill(const float *g, int64_t pitch, int len) {
+        const int lane = threadIdx.x & 31;
+        constexpr int PER = C / 32;
+        double s[PER], sum = 0.0;
+        int c[PER], cnt = 0;
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            const int t = lane * PER + u;
+            const float x = t < len ? __ldg(g + t * pitch) : 0.f;
+            const bool cut = x < LIN_RESET;
+            sum += cut ? 0.0 : double(x) * 1.4426950408889634;
+            cnt += cut;
+            s[u] = sum;
+            c[u] = cnt;
+        }
+        double run = sum;
+        int rc = cnt;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const double a = __shfl_up_sync(~0u, run, d);
+            const int b = __shfl_up_sync(~0u, rc, d);
+            if (lane >= d) {
+                run += a;
+                rc += b;
+            }
+        }
+        double before = __shfl_up_sync(~0u, run, 1);
+        int cb = __shfl_up_sync(~0u, rc, 1);
+        if (lane == 0) {
+            before = 0.0;
+            cb = 0;
+        }
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            const double G = before + s[u];
+            const int t = lane * PER + u;
+            hi[t] = float(G);
+            lo[t] = float(G - double(hi[t]));
+            r[t] = cb + c[u];
+        }
+    }
+};
+
+// bytes of workspace after the header, and the arrays in it
+size_t lin_ws_bytes(const LinArgs &a, bool bwd, bool bf16);
+void lin_ws_carve(LinArgs &a, bool bwd, bool bf16, void *base);
+int64_t lin_chunks(int64_t T, bool bf16);
+
+cudaError_t launch_lin_fwd(const LinArgs &a, bool bf16, unsigned *status, cudaStream_t st);
+cudaError_t launch_lin_bwd(const LinArgs &a, bool bf16, unsigned *status, cudaStream_t st);
+cudaError_t launch_lin_step(const LinArgs &a, bool bf16, float *state, int64_t n_slots, const int32_t *slots,
+                            cudaStream_t st);
+
+}  // namespace adj

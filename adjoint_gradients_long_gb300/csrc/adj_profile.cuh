@@ -25,6 +25,15 @@ enum KernelId {
     K_SEL_BWD,
     K_SEL_DW,
     K_SEL_DX,
+    K_LIN_STATE,
+    K_LIN_SCAN,
+    K_LIN_OUT,
+    K_LIN_GRAD,
+    K_LIN_SHARE,
+    K_LIN_STEP,
+    K_LOGPROB,
+    K_CLIP_NORM,
+    K_CLIP_SCALE,
     K_COUNT
 };
 

@@ -15,13 +15,16 @@ LIB_PATH = os.path.join(_HERE, "_build", "libadj.so")
 F32, BF16 = 0, 1
 OP_FWD, OP_BWD_FULL, OP_BWD_TRUNC, OP_PARAM, OP_LOSS = 0, 1, 2, 3, 4
 OP_SEL_FWD, OP_SEL_BWD, OP_SEL_PARAM = 5, 6, 7
+OP_LIN_FWD, OP_LIN_BWD = 8, 9
+LOGPROB_MAX_TOP = 32
 STATUS = {0: "ADJ_OK", 1: "ADJ_EINVAL", 2: "ADJ_ESHAPE", 3: "ADJ_EALIGN", 4: "ADJ_EDTYPE",
           5: "ADJ_EWORKSPACE", 6: "ADJ_ECUDA", 7: "ADJ_ETIMEOUT"}
 EXPORTS = ("adj_workspace_bytes", "adj_fwd_scan", "adj_loss_mse", "adj_bwd_full", "adj_bwd_trunc",
            "adj_param_grad", "adj_stream_status", "adj_status_str", "adj_launch_count", "adj_profile_enable",
            "adj_profile_reset", "adj_profile_kernels", "adj_profile_name", "adj_profile_read", "adj_rms_norm",
            "adj_rms_norm_bwd", "adj_selftest_waits", "adj_selftest_ws_bytes", "adj_sel_fwd", "adj_sel_bwd",
-           "adj_sel_param_grad", "adj_sel_rowdot_cols")
+           "adj_sel_param_grad", "adj_sel_rowdot_cols", "adj_lin_workspace_bytes", "adj_lin_fwd", "adj_lin_bwd",
+           "adj_lin_step", "adj_logprob", "adj_clip_workspace_bytes", "adj_grad_clip")
 
 
 class AdjError(RuntimeError):
@@ -42,6 +45,24 @@ class Weights(ctypes.Structure):
 class SelWeights(ctypes.Structure):
     """adj_sel_weights: W_in [P, P+2N], b_dt [P], A [P,N]."""
     _fields_ = [("W_in", ctypes.c_void_p), ("b_dt", ctypes.c_void_p), ("A", ctypes.c_void_p)]
+
+
+class LinDims(ctypes.Structure):
+    """adj_lin_dims: ld* are element distances between tokens."""
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("H", ctypes.c_int32), ("Hk", ctypes.c_int32),
+                ("Dk", ctypes.c_int32), ("Dv", ctypes.c_int32), ("x_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64), ("ldo", ctypes.c_int64)]
+
+
+class LogprobDims(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("V", ctypes.c_int64), ("ld", ctypes.c_int64), ("ldd", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("top", ctypes.c_int32)]
+
+
+class GradSeg(ctypes.Structure):
+    """adj_grad_seg: one tensor of a clipping call."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -69,6 +90,16 @@ def load(path: str = LIB_PATH):
         lib.adj_sel_param_grad.argtypes = [_PD, _PS] + [_VP] * 8 + [ctypes.c_int, _VP, _SZ, _VP]
         lib.adj_sel_rowdot_cols.argtypes = [_PD]
         lib.adj_sel_rowdot_cols.restype = _SZ
+        _PL, _PG = ctypes.POINTER(LinDims), ctypes.POINTER(GradSeg)
+        lib.adj_lin_workspace_bytes.argtypes = [_PL, ctypes.c_int]
+        lib.adj_lin_workspace_bytes.restype = _SZ
+        lib.adj_lin_fwd.argtypes = [_PL] + [_VP] * 8 + [_SZ, _VP]
+        lib.adj_lin_bwd.argtypes = [_PL] + [_VP] * 13 + [_SZ, _VP]
+        lib.adj_lin_step.argtypes = [_PL] + [_VP] * 5 + [_I64] + [_VP] * 3
+        lib.adj_logprob.argtypes = [ctypes.POINTER(LogprobDims)] + [_VP] * 11
+        lib.adj_clip_workspace_bytes.argtypes = []
+        lib.adj_clip_workspace_bytes.restype = _SZ
+        lib.adj_grad_clip.argtypes = [_PG, _I64, ctypes.c_float, _VP, _VP, _SZ, _VP]
         lib.adj_selftest_waits.argtypes = [_VP, _SZ, ctypes.c_int, _VP]
         lib.adj_selftest_waits.restype = ctypes.c_int
         lib.adj_selftest_ws_bytes.argtypes = []
@@ -85,7 +116,7 @@ def load(path: str = LIB_PATH):
         lib.adj_profile_read.restype = ctypes.c_int
         for f in ("adj_fwd_scan", "adj_loss_mse", "adj_bwd_full", "adj_bwd_trunc", "adj_param_grad",
                   "adj_stream_status", "adj_rms_norm", "adj_rms_norm_bwd", "adj_sel_fwd", "adj_sel_bwd",
-                  "adj_sel_param_grad"):
+                  "adj_sel_param_grad", "adj_lin_fwd", "adj_lin_bwd", "adj_lin_step", "adj_logprob", "adj_grad_clip"):
             getattr(lib, f).restype = ctypes.c_int
         _lib = lib
     return _lib
@@ -228,3 +259,47 @@ def sel_param_grad(d, xhat, dz, dW_in, db_dt, accumulate, ws, ws_bytes, stream=N
     _check(load().adj_sel_param_grad(ctypes.byref(d), None if w is None else ctypes.byref(w), ptr(xhat), ptr(dz),
                                      ptr(dW_in), ptr(db_dt), ptr(r), ptr(gadd), ptr(rowdot), ptr(gy_prev),
                                      int(accumulate), ptr(ws), ws_bytes, _stream(stream)), "adj_sel_param_grad")
+
+
+# ---------------------------------------------------------------- operators of a language model
+def lin_dims(B, T, H, Hk, Dk, Dv, x_dtype=BF16, scale=1.0) -> LinDims:
+    """Dense arrays; the ld* fields may be raised for column slices of wider ones."""
+    return LinDims(B, T, H, Hk, Dk, Dv, x_dtype, scale, Hk * Dk, Hk * Dk, H * Dv, H * Dv)
+
+
+def lin_workspace_bytes(d, op) -> int:
+    return int(load().adj_lin_workspace_bytes(ctypes.byref(d), op))
+
+
+def lin_fwd(d, q, k, v, g, s0, o, s1, ws, ws_bytes, stream=None):
+    _check(load().adj_lin_fwd(ctypes.byref(d), ptr(q), ptr(k), ptr(v), ptr(g), ptr(s0), ptr(o), ptr(s1), ptr(ws),
+                              ws_bytes, _stream(stream)), "adj_lin_fwd")
+
+
+def lin_bwd(d, q, k, v, g, s0, go, ds1, dq, dk, dv, dg, ds0, ws, ws_bytes, stream=None):
+    _check(load().adj_lin_bwd(ctypes.byref(d), ptr(q), ptr(k), ptr(v), ptr(g), ptr(s0), ptr(go), ptr(ds1), ptr(dq),
+                              ptr(dk), ptr(dv), ptr(dg), ptr(ds0), ptr(ws), ws_bytes, _stream(stream)), "adj_lin_bwd")
+
+
+def lin_step(d, q, k, v, g, state, n_slots, slots, o, stream=None):
+    _check(load().adj_lin_step(ctypes.byref(d), ptr(q), ptr(k), ptr(v), ptr(g), ptr(state), n_slots, ptr(slots), ptr(o),
+                               _stream(stream)), "adj_lin_step")
+
+
+def logprob_dims(N, V, ld, ldd, x_dtype=BF16, top=0) -> LogprobDims:
+    return LogprobDims(N, V, ld, ldd, x_dtype, top)
+
+
+def logprob(d, logits, targets, logp, entropy, lse, top_id, top_logp, glp, gent, dlogits, stream=None):
+    _check(load().adj_logprob(ctypes.byref(d), ptr(logits), ptr(targets), ptr(logp), ptr(entropy), ptr(lse),
+                              ptr(top_id), ptr(top_logp), ptr(glp), ptr(gent), ptr(dlogits), _stream(stream)),
+           "adj_logprob")
+
+
+def clip_workspace_bytes() -> int:
+    return int(load().adj_clip_workspace_bytes())
+
+
+def grad_clip(segs, nseg, max_norm, out, ws, ws_bytes, stream=None):
+    """segs: a ctypes array of GradSeg."""
+    _check(load().adj_grad_clip(segs, nseg, max_norm, ptr(out), ptr(ws), ws_bytes, _stream(stream)), "adj_grad_clip")

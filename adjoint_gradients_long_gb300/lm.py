@@ -1,0 +1,235 @@
+"""Operators of a language model built of recurrent layers, through libadj.so.
+
+LinAttn, LinStep    linear attention with a decay for each head: chunked for prompts and
+                    training (with gradients), recurrent for single tokens
+TokenLogProbs       log probabilities of given tokens, entropy, top alternatives, gradient
+GradClip            clipping gradients by their global norm
+
+include/adj.h states each operator in full.  As the drivers of the layers do, an object holds
+the sizes, the workspace and the outputs of one shape: a call overwrites the outputs of the
+call before it, enqueues kernels on torch's current stream and synchronises nothing, and can
+be captured into a CUDA graph.  Calls on one object belong to one stream at a time (they share
+its buffers).  Tensors are checked for shape, type, device and layout (ValueError) before the
+library checks its own arguments (lib.AdjError).
+"""
+from __future__ import annotations
+
+from collections import namedtuple
+
+import torch
+
+from . import lib
+
+LogProbs = namedtuple("LogProbs", "logp entropy lse top_id top_logp dlogits")
+
+
+def _check(name, x, shape, dtype, device):
+    if x.dtype is not dtype or x.device != device or tuple(x.shape) != shape:
+        raise ValueError(f"{name}: expected {dtype} {shape} on {device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
+
+
+def _dense(name, x, shape, dtype, device):
+    _check(name, x, shape, dtype, device)
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor, got strides {x.stride()}")
+
+
+def _device(device):
+    d = torch.device(device)
+    return torch.device("cuda", torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
+
+
+def _workspace(nbytes, device):
+    ws = torch.empty((nbytes + 255) // 4, dtype=torch.int32, device=device)
+    ws[:64].zero_()             # the header: status word and tickets
+    return ws
+
+
+class _Lin:
+    """What LinAttn and LinStep share: sizes, and arrays [*lead, heads, width] whose heads lie
+    densely in a token and whose tokens lie a common distance apart."""
+
+    def __init__(self, lead, T, H, Dk, Dv, Hk, x_bf16, scale, device):
+        Hk = H if Hk is None else Hk
+        self.H, self.Hk, self.Dk, self.Dv = H, Hk, Dk, Dv
+        self.device = _device(device)
+        self.xt = torch.bfloat16 if x_bf16 else torch.float32
+        self.lead = lead
+        self.qk, self.vo = (*lead, Hk, Dk), (*lead, H, Dv)
+        self.dims = lib.lin_dims(lead[0], T, H, Hk, Dk, Dv, lib.BF16 if x_bf16 else lib.F32, scale)
+
+    def _pitch(self, name, x, shape):
+        _check(name, x, shape, self.xt, self.device)
+        s, least = x.stride(), shape[-2] * shape[-1]
+        if x.numel() == 0:
+            return least
+        ld = s[-3]
+        if s[-1] != 1 or s[-2] != shape[-1] or (len(shape) == 4 and shape[0] > 1 and s[0] != shape[1] * ld):
+            raise ValueError(f"{name}: heads must lie densely in a token and tokens evenly, got strides {s}")
+        return ld if x.numel() > least else least      # a token alone has no distance to the next one
+
+    def _inputs(self, q, k, v, g):
+        d = self.dims
+        d.ldq, d.ldk, d.ldv = self._pitch("q", q, self.qk), self._pitch("k", k, self.qk), self._pitch("v", v, self.vo)
+        d.ldo = self.H * self.Dv
+        _dense("g", g, (*self.lead, self.H), torch.float32, self.device)
+
+    def _state(self, name, s):
+        if s is not None:
+            _dense(name, s, (self.lead[0], self.H, self.Dk, self.Dv), torch.float32, self.device)
+
+    def _empty(self, shape, dtype=None):
+        return torch.empty(shape, dtype=dtype or self.xt, device=self.device)
+
+
+class LinAttn(_Lin):
+    """Linear attention over B rows of T tokens: S_t = e^{g_t} S_{t-1} + k_t v_t^T,
+    o_t = scale q_t S_t, q and k [B,T,Hk,Dk] shared by groups of H / Hk heads, v [B,T,H,Dv],
+    g [B,T,H] fp32 (at most 0; minus infinity starts a new document).  backward: also hold what
+    the gradients need."""
+
+    def __init__(self, B, T, H, Dk, Dv, Hk=None, x_bf16=True, scale=1.0, backward=False, device="cuda"):
+        super().__init__((B, T), T, H, Dk, Dv, Hk, x_bf16, scale, device)
+        need = lib.lin_workspace_bytes(self.dims, lib.OP_LIN_BWD if backward else lib.OP_LIN_FWD)
+        if need == 0:
+            raise ValueError("unsupported linear-attention sizes")
+        self.ws_bytes = int(need)
+        self.ws = _workspace(self.ws_bytes, self.device)
+        self.o = self._empty(self.vo)
+        self.s1 = self._empty((B, H, Dk, Dv), torch.float32)
+        self.has_backward = backward
+        if backward:
+            self.dq, self.dk, self.dv = self._empty(self.qk), self._empty(self.qk), self._empty(self.vo)
+            self.dg = self._empty((B, T, H), torch.float32)
+            self.ds0 = self._empty((B, H, Dk, Dv), torch.float32)
+
+    def forward(self, q, k, v, g, s0=None):
+        """(o [B,T,H,Dv], s1 [B,H,Dk,Dv]): the outputs and the state after the last token."""
+        self._inputs(q, k, v, g)
+        self._state("s0", s0)
+        lib.lin_fwd(self.dims, q, k, v, g, s0, self.o, self.s1, self.ws, self.ws_bytes)
+        return self.o, self.s1
+
+    def backward(self, q, k, v, g, go, s0=None, ds1=None):
+        """(dq, dk, dv, dg, ds0) for the cotangents go of o and ds1 of s1."""
+        if not self.has_backward:
+            raise ValueError("this LinAttn was made without backward=True")
+        self._inputs(q, k, v, g)
+        self._state("s0", s0)
+        self._state("ds1", ds1)
+        _dense("go", go, self.vo, self.xt, self.device)
+        for name, x, y in (("q", q, self.dq), ("k", k, self.dk), ("v", v, self.dv)):
+            if x.stride() != y.stride() and x.numel():
+                # the gradients have the layout of their inputs
+                setattr(self, "d" + name, torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=x.device))
+        lib.lin_bwd(self.dims, q, k, v, g, s0, go, ds1, self.dq, self.dk, self.dv, self.dg, self.ds0, self.ws,
+                    self.ws_bytes)
+        return self.dq, self.dk, self.dv, self.dg, self.ds0
+
+    def status(self, stream=None) -> int:
+        return lib.stream_status(self.ws, stream)
+
+
+class LinStep(_Lin):
+    """The same recurrence for one token of each of B sequences: q, k [B,Hk,Dk], v [B,H,Dv],
+    g [B,H] fp32, and a pool of states [n_slots,H,Dk,Dv] fp32 that is updated in place."""
+
+    def __init__(self, B, H, Dk, Dv, Hk=None, x_bf16=True, scale=1.0, device="cuda"):
+        super().__init__((B,), 1, H, Dk, Dv, Hk, x_bf16, scale, device)
+        if lib.lin_workspace_bytes(self.dims, lib.OP_LIN_FWD) == 0:
+            raise ValueError("unsupported linear-attention sizes")
+        self.o = self._empty(self.vo)
+
+    def step(self, q, k, v, g, state, slots=None):
+        """o [B,H,Dv].  slots [B] int32: sequence b's state is state[slots[b]] (a slot outside
+        the pool: padding, a row of zeros); None: state[b]."""
+        self._inputs(q, k, v, g)
+        _dense("state", state, (state.shape[0], self.H, self.Dk, self.Dv), torch.float32, self.device)
+        if slots is not None:
+            _dense("slots", slots, self.lead, torch.int32, self.device)
+        elif state.shape[0] < self.lead[0]:
+            raise ValueError(f"state: {state.shape[0]} slots for {self.lead[0]} sequences")
+        lib.lin_step(self.dims, q, k, v, g, state, state.shape[0], slots, self.o)
+        return self.o
+
+
+class TokenLogProbs:
+    """Log probabilities of given tokens over logits [N,V] (rows may be strided): targets [N]
+    int64 (outside [0,V): not scored), the row's entropy, its `top` best tokens, and the
+    gradient of both for the logits."""
+
+    def __init__(self, N, V, x_bf16=True, top=0, device="cuda"):
+        self.N, self.V, self.top = N, V, top
+        self.device = _device(device)
+        self.xt = torch.bfloat16 if x_bf16 else torch.float32
+        self.dims = lib.logprob_dims(N, V, V, V, lib.BF16 if x_bf16 else lib.F32, top)
+        if not (0 <= top <= min(V, lib.LOGPROB_MAX_TOP)):
+            raise ValueError(f"top: 0 to {min(V, lib.LOGPROB_MAX_TOP)}, got {top}")
+        f = lambda *s: torch.empty(*s, dtype=torch.float32, device=self.device)  # noqa: E731
+        self.logp, self.entropy, self.lse = f(N), f(N), f(N)
+        self.top_id = torch.empty(N, top, dtype=torch.int32, device=self.device) if top else None
+        self.top_logp = f(N, top) if top else None
+        self.dlogits = None
+
+    def _row(self, name, x):
+        _check(name, x, (self.N, self.V), self.xt, self.device)
+        if x.stride(1) != 1 and self.V > 1:
+            raise ValueError(f"{name}: rows must be contiguous, got strides {x.stride()}")
+        if self.N > 1 and x.stride(0) < self.V:
+            raise ValueError(f"{name}: rows must not overlap, got strides {x.stride()}")
+        return x.stride(0) if self.N > 1 else self.V
+
+    def _call(self, logits, targets, glp, gent, dlogits):
+        self.dims.ld = self._row("logits", logits)
+        _dense("targets", targets, (self.N,), torch.int64, self.device)
+        if dlogits is not None:
+            self.dims.ldd = self._row("dlogits", dlogits)
+        lib.logprob(self.dims, logits, targets, self.logp, self.entropy, self.lse, self.top_id, self.top_logp, glp,
+                    gent, dlogits)
+        return LogProbs(self.logp, self.entropy, self.lse, self.top_id, self.top_logp, dlogits)
+
+    def forward(self, logits, targets):
+        """LogProbs without a gradient."""
+        return self._call(logits, targets, None, None, None)
+
+    def gradient(self, logits, targets, glp, gent=None, dlogits=None):
+        """LogProbs with dlogits for the cotangents glp of logp and gent of the entropy, [N] fp32.
+        dlogits: the array to write, which may be the logits themselves; None: one of this
+        object's."""
+        _dense("glp", glp, (self.N,), torch.float32, self.device)
+        if gent is not None:
+            _dense("gent", gent, (self.N,), torch.float32, self.device)
+        if dlogits is None:
+            if self.dlogits is None:
+                self.dlogits = torch.empty(self.N, self.V, dtype=self.xt, device=self.device)
+            dlogits = self.dlogits
+        return self._call(logits, targets, glp, gent, dlogits)
+
+
+class GradClip:
+    """Clipping a fixed list of gradient tensors (fp32 or bf16, contiguous) by their global norm:
+    outs[i] = min(1, max_norm / (norm + 1e-6)) grads[i]; outs None clips in place."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError(f"{len(self.outs)} outputs for {len(self.grads)} gradients")
+        self.device = self.grads[0].device if self.grads else _device("cuda")
+        kinds = {torch.float32: lib.F32, torch.bfloat16: lib.BF16}
+        self.segs = (lib.GradSeg * max(1, len(self.grads)))()
+        for i, (x, y) in enumerate(zip(self.grads, self.outs)):
+            if x.dtype not in kinds:
+                raise ValueError(f"gradient {i}: fp32 or bf16, got {x.dtype}")
+            _dense(f"gradient {i}", x, tuple(x.shape), x.dtype, self.device)
+            _dense(f"output {i}", y, tuple(x.shape), x.dtype, self.device)
+            self.segs[i] = lib.GradSeg(x.data_ptr(), y.data_ptr(), x.numel(), kinds[x.dtype], 0)
+        self.ws_bytes = lib.clip_workspace_bytes()
+        self.ws = _workspace(self.ws_bytes, self.device)
+        self.result = torch.empty(2, dtype=torch.float32, device=self.device)
+        self.norm, self.coef = self.result[0], self.result[1]
+
+    def clip(self, max_norm):
+        """(norm, coefficient) as device scalars; the outputs hold the clipped gradients."""
+        lib.grad_clip(self.segs, len(self.grads), max_norm, self.result, self.ws, self.ws_bytes)
+        return self.norm, self.coef

@@ -76,7 +76,8 @@ typedef struct {
 
 enum {
     ADJ_OP_FWD = 0, ADJ_OP_BWD_FULL = 1, ADJ_OP_BWD_TRUNC = 2, ADJ_OP_PARAM = 3, ADJ_OP_LOSS = 4,
-    ADJ_OP_SEL_FWD = 5, ADJ_OP_SEL_BWD = 6, ADJ_OP_SEL_PARAM = 7   /* the general selective layer (below) */
+    ADJ_OP_SEL_FWD = 5, ADJ_OP_SEL_BWD = 6, ADJ_OP_SEL_PARAM = 7,  /* the general selective layer (below) */
+    ADJ_OP_LIN_FWD = 8, ADJ_OP_LIN_BWD = 9                         /* adj_lin_workspace_bytes only */
 };
 
 /* Workspace bytes that call `op` needs for these sizes (Tbar: the window of
@@ -248,6 +249,104 @@ adj_status adj_sel_bwd(const adj_dims *dims, const adj_sel_weights *w, const voi
 adj_status adj_sel_param_grad(const adj_dims *dims, const adj_sel_weights *w, const void *xhat, const void *dz,
                               float *dW_in, float *db_dt, const float *r, const float *gadd, const float *rowdot,
                               float *gy_prev, int accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators of a language model built of such layers (library facilities; the pages
+ * describe the gradient path only).
+ *
+ * Linear attention with a decay for each head: the selective recurrence with a matrix
+ * state per head.  Per head h of H, with q and k of head h / (H / Hk):
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T        S_t [Dk, Dv]
+ *     o_t = scale * q_t S_t
+ * Arrays (ld*: elements from one token to the next, so q, k and v may be column slices
+ * of one projection; sequences follow each other at T * ld*):
+ *   q [B,T,Hk,Dk], k [B,T,Hk,Dk], v [B,T,H,Dv], o [B,T,H,Dv]   x_dtype
+ *   g [B,T,H] fp32 (dense): the logarithm of the decay, expected <= 0.  exp(g) is taken as
+ *     zero below -104 (minus infinity included): the state starts afresh at that token, and
+ *     what came before leaves no trace in it, which packs several documents into one row
+ *   s0, s1 [B,H,Dk,Dv] fp32 (dense): the states before the first and after the last token
+ * A value that is not finite spreads to the outputs of its chunk of 128 tokens and onwards.
+ * Sizes: Dk and Dv multiples of 8 from 8 to 128; Hk divides H; H, B <= 65535; every ld* at
+ * least its row's heads times width and a multiple of 16 bytes.  x_dtype fp32: products in
+ * fp32.  x_dtype bf16: fp32 sums of products of bf16 operands; the decayed pair weights and
+ * the states that a token reads are rounded to bf16, the states themselves stay fp32.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int64_t B, T;
+    int32_t H, Hk, Dk, Dv;
+    int32_t x_dtype;
+    float scale;
+    int64_t ldq, ldk, ldv, ldo;
+} adj_lin_dims;
+
+/* Workspace bytes of ADJ_OP_LIN_FWD or ADJ_OP_LIN_BWD (0 for sizes the calls reject). */
+size_t adj_lin_workspace_bytes(const adj_lin_dims *dims, int op);
+
+/* Chunked form over T tokens.  s0 NULL: a state of zeros; s1 NULL: not written.  o may not
+ * alias an input.  B*T = 0 copies s0 (or zeros) to s1. */
+adj_status adj_lin_fwd(const adj_lin_dims *dims, const void *q, const void *k, const void *v, const float *g,
+                       const float *s0, void *o, float *s1, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients for the cotangents go [B,T,H,Dv] of o (x_dtype, pitch ldo) and ds1 of s1 (NULL:
+ * zeros).  dq, dk, dv have the layout of q, k, v; dg [B,T,H] and ds0 fp32 (ds0 NULL: not
+ * written).  q and k shared by several heads receive the sum over them, taken in a fixed
+ * order.  dg is zero where exp(g) is taken as zero.  No output may alias an input. */
+adj_status adj_lin_bwd(const adj_lin_dims *dims, const void *q, const void *k, const void *v, const float *g,
+                       const float *s0, const void *go, const float *ds1, void *dq, void *dk, void *dv, float *dg,
+                       float *ds0, void *ws, size_t ws_bytes, void *stream);
+
+/* One token for each of B sequences (dims->T is not read; ld* are the distances between
+ * sequences): state [n_slots,H,Dk,Dv] fp32 is updated in place, sequence b's in slot
+ * slots[b] (slots NULL: slot b, needs n_slots >= B).  A slot outside [0, n_slots) leaves
+ * the pool untouched and gives a row of zeros (the padding of a batch); a slot given twice is
+ * a race.  No workspace. */
+adj_status adj_lin_step(const adj_lin_dims *dims, const void *q, const void *k, const void *v, const float *g,
+                        float *state, int64_t n_slots, const int32_t *slots, void *o, void *stream);
+
+/* Log probabilities of given tokens.  Per row x = logits[n, :V] with lse = log sum_j e^x_j and
+ * p_j = e^(x_j - lse):
+ *   lse      [N] fp32
+ *   logp     [N] fp32 = x_target - lse; a target outside [0, V) is not scored: 0, no gradient
+ *   entropy  [N] fp32 = -sum_j p_j log p_j
+ *   top_id   [N,top] int32, top_logp [N,top] fp32: the `top` largest, largest first, equal
+ *            ones by the lower index (NaN counts as largest)
+ *   dlogits  [N,V] x_dtype (row pitch ldd) = glp_n (1[j = target] - p_j)
+ *                                            - gent_n p_j (log p_j + entropy_n),
+ *            the gradient for given cotangents glp of logp and gent of entropy [N] fp32
+ * Minus infinity in x is a masked token (p = 0, dlogits = 0).  A row masked altogether has
+ * lse = -inf, logp = -inf, entropy = 0 and dlogits = 0.  A NaN or +inf makes its row NaN.
+ * Any output may be NULL (top_id and top_logp both or neither; top = 0 for neither); dlogits
+ * needs glp or gent (a NULL one counts as zeros) and may be the logits array itself when
+ * ldd = ld.  logits and dlogits need only their type's alignment, ld, ldd >= V.  top <= V and
+ * top <= ADJ_LOGPROB_MAX_TOP; V < 2^31.  One launch, no workspace. */
+typedef struct {
+    int64_t N, V, ld, ldd;
+    int32_t x_dtype, top;
+} adj_logprob_dims;
+#define ADJ_LOGPROB_MAX_TOP 32
+adj_status adj_logprob(const adj_logprob_dims *dims, const void *logits, const int64_t *targets, float *logp,
+                       float *entropy, float *lse, int32_t *top_id, float *top_logp, const float *glp,
+                       const float *gent, void *dlogits, void *stream);
+
+/* Clipping gradients by their global norm: over all n values x of all tensors
+ *   norm = sqrt(sum x^2),  coef = min(1, max_norm / (norm + ADJ_CLIP_EPS)),  dst = coef * src.
+ * segs is a HOST array (copied at the call) of nseg tensors: src and dst device pointers of
+ * n values of `dtype`, aligned to that type; dst = src clips in place (and with coef = 1
+ * nothing is written then), any other overlap is an error of the caller; dst NULL: the tensor
+ * counts in the norm only.  out: two device floats, norm and coef.  An infinite norm gives
+ * coef 0, a NaN gives NaN (and NaN gradients): no call hides a step that has to be skipped.
+ * Sums are in a fixed order: the same inputs give the same bits. */
+typedef struct {
+    const void *src;
+    void *dst;
+    int64_t n;
+    int32_t dtype;
+    int32_t reserved;    /* zero */
+} adj_grad_seg;
+#define ADJ_CLIP_EPS 1e-6f
+size_t adj_clip_workspace_bytes(void);
+adj_status adj_grad_clip(const adj_grad_seg *segs, int64_t nseg, float max_norm, float *out, void *ws,
+                         size_t ws_bytes, void *stream);
 
 /* Synchronise `stream`, return and clear the sticky device status of `ws`
  * (ADJ_OK or ADJ_ETIMEOUT); ADJ_ECUDA if the stream reports an error. */
