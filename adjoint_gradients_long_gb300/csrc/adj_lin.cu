@@ -156,27 +156,27 @@ __global__ __launch_bounds__(256) void k_lin_chunk_state(const LinArgs a) {
 // Pass 2.  Every chunk's contribution is replaced by the state that enters it (REV: by the
 // adjoint state that its exit receives); one thread carries four elements through the chunks.
 template <bool REV>
-__global__ __launch_bounds__(128) void k_lin_scan(const LinArgs a) {
+__global__ __launch_bounds__(128) void k_lin_scan(const LinArgs a, int64_t NC) {
     const int64_t n4 = int64_t(a.Dk) * a.Dv / 4, blocks = (n4 + 127) / 128, bh = blockIdx.x / blocks;
     const int64_t i = (blockIdx.x - bh * blocks) * 128 + threadIdx.x;
     if (i >= n4) return;
     const float *init = REV ? a.ds1 : a.s0;
     float *fin = REV ? a.ds0 : a.s1;
     float4 c = init ? reinterpret_cast<const float4 *>(init)[bh * n4 + i] : f4(0.f);
-    float4 *S = reinterpret_cast<float4 *>(REV ? a.dS : a.S) + bh * a.NC * n4 + i;
-    const float *tot = a.tot + bh * a.NC;
+    float4 *S = reinterpret_cast<float4 *>(REV ? a.dS : a.S) + bh * NC * n4 + i;
+    const float *tot = a.tot + bh * NC;
     constexpr int U = 8;        // loads in flight
-    for (int64_t m = 0; m < a.NC; m += U) {
+    for (int64_t m = 0; m < NC; m += U) {
         float4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (m + u < a.NC) x[u] = S[(REV ? a.NC - 1 - m - u : m + u) * n4];
+            if (m + u < NC) x[u] = S[(REV ? NC - 1 - m - u : m + u) * n4];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (m + u < a.NC) {
-                const int64_t n = REV ? a.NC - 1 - m - u : m + u;
+            if (m + u < NC) {
+                const int64_t n = REV ? NC - 1 - m - u : m + u;
                 S[n * n4] = c;
-                c = fma4(f4(tot[n]), c, x[u]);
+                c = tot[n] == 0.f ? x[u] : fma4(f4(tot[n]), c, x[u]);   // a new start drops it whatever it holds
             }
     }
     if (fin) reinterpret_cast<float4 *>(fin)[bh * n4 + i] = c;
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(256) void k_lin_out(const LinArgs a) {
     for (int r = 0; r < 4; ++r) {
         const float f = D.first(ty + 16 * r);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) acc[r][c] *= f;
+        for (int c = 0; c < 8; ++c) acc[r][c] = f == 0.f ? 0.f : acc[r][c] * f;
     }
     __syncthreads();
     mm<4, 8, PP, 1, LP, 1>(acc, P, V, LC, a.Dv);
@@ -513,15 +513,12 @@ cudaError_t states(const LinArgs &a, cudaStream_t st) {
         k_lin_chunk_state<T, REV><<<grid, 256, SM_STATE, st>>>(a);
         LIN_CUDA(cudaGetLastError());
     }
-    ProfScope ps(K_LIN_SCAN, st);
-    k_lin_scan<REV><<<unsigned(cdiv(int64_t(a.Dk) * a.Dv, 512) * a.B * a.H), 128, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_lin_scan(a, a.NC, REV, st);
 }
 
 template <class T>
 cudaError_t fwd(const LinArgs &a, cudaStream_t st) {
     LIN_CUDA((states<T, false>(a, st)));
-    if (a.NC == 0) return cudaSuccess;
     ProfScope ps(K_LIN_OUT, st);
     LIN_CUDA(big_smem(k_lin_out<T>, SM_OUT));
     k_lin_out<T><<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, SM_OUT, st>>>(a);
@@ -554,16 +551,25 @@ inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 int64_t lin_chunks(int64_t T, bool) { return cdiv(T, LC); }
 
-static size_t carve(LinArgs &a, bool bwd, bool, char *base) {
+cudaError_t launch_lin_scan(const LinArgs &a, int64_t n, bool rev, cudaStream_t st) {
+    ProfScope ps(K_LIN_SCAN, st);
+    const unsigned grid = unsigned(cdiv(int64_t(a.Dk) * a.Dv, 512) * a.B * a.H);
+    if (rev) k_lin_scan<true><<<grid, 128, 0, st>>>(a, n);
+    else k_lin_scan<false><<<grid, 128, 0, st>>>(a, n);
+    return cudaGetLastError();
+}
+
+static size_t carve(LinArgs &a, bool bwd, bool bf16, char *base) {
     size_t off = 0;
     auto take = [&](size_t bytes) {
         float *p = base ? reinterpret_cast<float *>(base + off) : nullptr;
         off += al256(bytes);
         return p;
     };
-    const size_t st = size_t(a.B * a.H) * a.NC * a.Dk * a.Dv * 4;
+    const int64_t n = bf16 && !bwd ? lin_split(a).nseg : a.NC;
+    const size_t st = size_t(a.B * a.H) * n * a.Dk * a.Dv * 4;
     a.S = take(st);
-    a.tot = take(size_t(a.B * a.H) * a.NC * 4);
+    a.tot = take(size_t(a.B * a.H) * n * 4);
     a.dS = a.pq = a.pk = nullptr;
     if (bwd) {
         a.dS = take(st);
@@ -581,8 +587,9 @@ size_t lin_ws_bytes(const LinArgs &a, bool bwd, bool bf16) {
 }
 void lin_ws_carve(LinArgs &a, bool bwd, bool bf16, void *base) { carve(a, bwd, bf16, static_cast<char *>(base)); }
 
-cudaError_t launch_lin_fwd(const LinArgs &a, bool bf16, unsigned *, cudaStream_t st) {
-    return bf16 ? fwd<__nv_bfloat16>(a, st) : fwd<float>(a, st);
+cudaError_t launch_lin_fwd(const LinArgs &a, bool bf16, unsigned *status, cudaStream_t st) {
+    if (a.NC == 0) return launch_lin_scan(a, 0, false, st);      // s1 = s0
+    return bf16 ? launch_lin_tc_fwd(a, status, st) : fwd<float>(a, st);
 }
 cudaError_t launch_lin_bwd(const LinArgs &a, bool bf16, unsigned *, cudaStream_t st) {
     return bf16 ? bwd<__nv_bfloat16>(a, st) : bwd<float>(a, st);

@@ -97,6 +97,15 @@ int64_t lin_chunks(int64_t T, bool bf16);
 
 cudaError_t launch_lin_fwd(const LinArgs &a, bool bf16, unsigned *status, cudaStream_t st);
 cudaError_t launch_lin_bwd(const LinArgs &a, bool bf16, unsigned *status, cudaStream_t st);
+// The tensor-core forward pass (bf16 storage), and how it cuts a head's tokens: nseg segments of
+// cps chunks.  Its states are those of the segments: S [B,H,nseg,Dk,Dv], tot [B,H,nseg].
+struct LinSplit {
+    int nseg, cps;
+};
+LinSplit lin_split(const LinArgs &a);
+cudaError_t launch_lin_tc_fwd(const LinArgs &a, unsigned *status, cudaStream_t st);
+// every entry of S (rev: dS) [B,H,n,Dk,Dv] becomes the state before it (rev: after it)
+cudaError_t launch_lin_scan(const LinArgs &a, int64_t n, bool rev, cudaStream_t st);
 cudaError_t launch_lin_step(const LinArgs &a, bool bf16, float *state, int64_t n_slots, const int32_t *slots,
                             cudaStream_t st);
 

@@ -40,6 +40,12 @@ adj_status check_lin(const adj_lin_dims *d, bool step) {
     const int64_t vec = d->x_dtype == ADJ_BF16 ? 8 : 4, qk = int64_t(d->Hk) * d->Dk, vo = int64_t(d->H) * d->Dv;
     if (d->ldq < qk || d->ldk < qk || d->ldv < vo || d->ldo < vo) return ADJ_ESHAPE;
     if (d->ldq % vec || d->ldk % vec || d->ldv % vec || d->ldo % vec) return ADJ_EALIGN;
+    // tensor maps: 32-bit token coordinates, 40-bit byte strides
+    if (d->x_dtype == ADJ_BF16 && !step) {
+        if (d->T >= (int64_t(1) << 31)) return ADJ_ESHAPE;
+        for (int64_t ld : {d->ldq, d->ldk, d->ldv, d->ldo})
+            if (ld >= (int64_t(1) << 31) || d->T * ld >= (int64_t(1) << 39)) return ADJ_ESHAPE;
+    }
     // grids: a block for 512 state values of every head, and one for every chunk
     if (d->B * d->H >= (int64_t(1) << 26) || (!step && d->T >= (int64_t(1) << 36))) return ADJ_ESHAPE;
     if (!isfinite(d->scale)) return ADJ_EINVAL;

@@ -90,7 +90,9 @@ class LinAttn(_Lin):
 
     def __init__(self, B, T, H, Dk, Dv, Hk=None, x_bf16=True, scale=1.0, backward=False, device="cuda"):
         super().__init__((B, T), T, H, Dk, Dv, Hk, x_bf16, scale, device)
-        need = lib.lin_workspace_bytes(self.dims, lib.OP_LIN_BWD if backward else lib.OP_LIN_FWD)
+        need = lib.lin_workspace_bytes(self.dims, lib.OP_LIN_FWD)
+        if backward:
+            need = max(need, lib.lin_workspace_bytes(self.dims, lib.OP_LIN_BWD))
         if need == 0:
             raise ValueError("unsupported linear-attention sizes")
         self.ws_bytes = int(need)
