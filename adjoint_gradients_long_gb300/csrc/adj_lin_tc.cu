@@ -4,12 +4,11 @@
 // Chunks of 128 tokens: every product of a chunk is one tcgen05 accumulator of 128 rows.
 //     A  = Q K^T               (tokens x tokens)     exact operands
 //     O1 = Q S                 (tokens x Dv)         S rounded to bf16
-//     O2 = P V                 (tokens x Dv)         P = A . D rounded to bf16, in tensor memory
-//     U  = (l K)^T V           (Dk x Dv)             l K as a sum of two bf16, 2^-17 of a value
+//     O2 = P V                 (tokens x Dv)         P = A . D as a sum of two bf16, in tensor memory
+//     U  = (l K)^T V           (Dk x Dv)             l K as a sum of three bf16: exact to fp32
 //     o  = scale (f O1 + O2),  S <- f_last S + U     S in fp32 registers
-// with the decays D, f, l of adj_lin.cu.  O1 and O2 have one rounding to bf16 each, as large as
-// that of the output itself; U is held closer because the state is an fp32 result and errors
-// in it stay.
+// with the decays D, f, l of adj_lin.cu.  O1 has one rounding to bf16 before the output's own; U
+// has none, because the state is an fp32 result and errors in it stay.
 //
 // One block walks the chunks of a segment of one head's tokens.  When there are fewer heads
 // than SMs, the tokens of a head are cut into segments: k_lin_tc_state sums up each segment's own
@@ -27,9 +26,9 @@ namespace {
 using namespace tc5;
 
 constexpr int TCH = 128;                // tokens of a chunk
-constexpr int CW = 8;                   // computing warps: two groups of four, a group covers the 128 lanes
-constexpr int W_MMA = CW, W_TMA = CW + 1, W_DEC = CW + 2;
-constexpr int TC_BLOCK = (CW + 3) * 32;
+constexpr int CG = 4, CW = 4 * CG;      // computing warps: groups of four, a group covers the 128 lanes
+constexpr int W_MMA = CW, W_TMA = CW + 1, W_DEC = CW + 2, W_OUT = CW + 3;
+constexpr int TC_BLOCK = (CW + 4) * 32;
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -40,7 +39,7 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //   last[b]: from block b's end to the chunk's end; total: over the chunk
 // A decay between blocks is a product of such factors, each at most 1; only pairs inside one
 // block take an exponential each.
-struct ChunkDecay {
+struct alignas(16) ChunkDecay {
     float x[TCH], wb[TCH];
     uint8_t r[TCH];
     float Ehi[4], Elo[4], last[4];
@@ -115,38 +114,53 @@ struct StateMaps {
     CUtensorMap x, y;
 };
 
-enum { B_FULL0, B_FULL1, B_EMPTY0, B_EMPTY1, B_DEC0, B_DEC1, B_A, B_O1, B_P, B_K, B_U, B_S, B_OFREE, B_END, B_COUNT };
+enum { B_FULL0, B_FULL1, B_EMPTY0, B_EMPTY1, B_DEC0, B_DEC1, B_A, B_O1, B_PV, B_P, B_K, B_U, B_S, B_OFREE, B_OUT, B_END, B_COUNT };
 struct Ctl {
     uint64_t bar[B_COUNT];
     uint32_t tmem;
     int abort;
 };
 
-// Write 32 consecutive values (as bf16) of row r from column `col` on into a tile.
-__device__ __forceinline__ void put32(uint32_t tile, uint32_t panel, int r, int col, const float (&v)[32]) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-        sts(tile + unit_at(r, (col >> 3) + u, panel),
-            make_uint4(pack(v[8 * u], v[8 * u + 1]), pack(v[8 * u + 2], v[8 * u + 3]), pack(v[8 * u + 4], v[8 * u + 5]),
-                       pack(v[8 * u + 6], v[8 * u + 7])));
+// 8 values of row r (unit u) of a tile
+__device__ __forceinline__ void put8(uint32_t tile, uint32_t panel, int r, int u, const float *v) {
+    sts(tile + unit_at(r, u, panel), make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7])));
 }
 
-// Row r of a tile times w, as hi + lo: hi in place, lo into the other tile; units u0 .. u1.
-__device__ __forceinline__ void scale_row(uint32_t hi, uint32_t lo, uint32_t panel, int r, int u0, int u1, float w) {
-#pragma unroll 4
+// Row r of a tile times w as a sum of three bf16 (24 bits): the first in place, the others into
+// tiles of their own; units u0 .. u1.
+__device__ __forceinline__ void scale_row(uint32_t t0, uint32_t t1, uint32_t t2, uint32_t panel, int r, int u0, int u1,
+                                          float w) {
+#pragma unroll 2
     for (int u = u0; u < u1; ++u) {
         const uint32_t at = unit_at(r, u, panel);
-        const uint4 x = lds(hi + at);
+        uint4 x = lds(t0 + at);
+        if (w == 0.f) x = make_uint4(0u, 0u, 0u, 0u);    // drops a value whatever it is
         const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-        uint32_t h[4], l[4];
+        uint32_t h[4], l[4], ll[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float a = w == 0.f ? 0.f : lo_f(in[i]) * w, b = w == 0.f ? 0.f : hi_f(in[i]) * w;
+            float a = lo_f(in[i]) * w, b = hi_f(in[i]) * w;
             h[i] = pack(a, b);
-            l[i] = pack(a - lo_f(h[i]), b - hi_f(h[i]));
+            a -= lo_f(h[i]);
+            b -= hi_f(h[i]);
+            l[i] = pack(a, b);
+            ll[i] = pack(a - lo_f(l[i]), b - hi_f(l[i]));
         }
-        sts(hi + at, make_uint4(h[0], h[1], h[2], h[3]));
-        sts(lo + at, make_uint4(l[0], l[1], l[2], l[3]));
+        sts(t0 + at, make_uint4(h[0], h[1], h[2], h[3]));
+        sts(t1 + at, make_uint4(l[0], l[1], l[2], l[3]));
+        sts(t2 + at, make_uint4(ll[0], ll[1], ll[2], ll[3]));
+    }
+}
+
+// S <- tot S + U, for this thread's columns
+template <int VH>
+__device__ __forceinline__ void state_update(float (&S)[VH], uint32_t u, float tot) {
+#pragma unroll
+    for (int c = 0; c < VH; c += 16) {
+        float x[16];
+        ld16(u + c, x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[c + e] = tot == 0.f ? x[e] : fmaf(tot, S[c + e], x[e]);
     }
 }
 
@@ -197,20 +211,21 @@ __device__ __forceinline__ void store_part(const float (&S)[VH], float *p, int d
 // ---------------------------------------------------------------- forward
 // KW, VW: Dk and Dv rounded up to 64 or 128; the columns past them are zeros (the copies fill
 // them) and the store clips them.
+// The S tile also takes the third part of l K, between the last read of S and the next state.
 template <int KW, int VW>
 constexpr size_t fwd_smem() {
-    return 2 * size_t(2 * KW + VW) * 256 + size_t(KW) * VW * 2 + 2 * sizeof(ChunkDecay) + sizeof(Ctl);
+    return 2 * size_t(2 * KW + VW) * 256 + size_t(KW) * 256 + 2 * sizeof(ChunkDecay) + sizeof(Ctl);
 }
 
 template <int KW, int VW>
 __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constant__ FwdMaps m, const LinArgs a, int nseg,
                                                             int cps, unsigned *status) {
     constexpr uint32_t STAGE = (2 * KW + VW) * 256, TILE_K = KW * 256, PANEL = TCH * 128, SPANEL = KW * 128;
-    constexpr int VH = VW / 2;          // state and output columns of a thread
-    constexpr uint32_t T_A = 0, T_U = 128, T_O1 = 256, T_O2 = 384;
+    constexpr int VH = VW / CG;         // state and output columns of a thread
+    constexpr uint32_t T_A = 0, T_U = 128, T_P = T_U, T_O1 = 256, T_O2 = 384;
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t base = smem_u32(sm), S_AT = base + 2 * STAGE;
-    ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + 2 * STAGE + KW * VW * 2);
+    ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + 2 * STAGE + TILE_K);
     Ctl *ctl = reinterpret_cast<Ctl *>(dec + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Seg seg(a, nseg, cps);
@@ -218,7 +233,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < B_COUNT; ++i)
-            mbar_init(smem_u32(&ctl->bar[i]), i == B_P || i == B_K || i == B_S || i == B_OFREE ? CW : 1);
+            mbar_init(smem_u32(&ctl->bar[i]), i == B_P || i == B_K || i == B_S || i == B_OFREE || i == B_OUT ? CW : 1);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -257,49 +272,59 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_DEC0 + s));
         }
+    } else if (warp == W_OUT) {
+        if (lane == 0) {
+            // the outputs leave through V's tile, then the stage is free
+            for (int64_t n = 0; n < N; ++n) {
+                const int s = int(n & 1);
+                if (!wait(B_OUT, n)) break;
+                for (int p = 0; p < VW / 64; ++p)
+                    store4(&m.o, p * 64, int(seg.h), int((seg.n0 + n) * TCH), int(seg.b), base + s * STAGE + 2 * TILE_K + p * PANEL);
+                bulk_commit();
+                bulk_wait_read();
+                mbar_arrive(bar(B_EMPTY0 + s));
+            }
+            bulk_wait_all();
+        }
+        __syncwarp();
     } else if (warp == W_MMA) {
         if (lane == 0) {
-            const int kd = (a.Dk + 15) >> 4;
-            auto tiles = [&](int64_t n, Tile &q, Tile &k, Tile &v) {
-                const uint32_t at = base + uint32_t(n & 1) * STAGE;
-                q = Tile{at, PANEL, false};
-                k = Tile{at + TILE_K, PANEL, false};
-                v = Tile{at + 2 * TILE_K, PANEL, true};
-            };
-            Tile q, k, v;
-            tiles(0, q, k, v);
+            // a tile of one panel read across its rows gives its columns twice; the upper lanes of that
+            // product are not read
+            constexpr uint32_t WIDE = KW == 64 ? 0u : PANEL;
             bool ok = wait(B_FULL0, 0);
             if (ok) {
                 tc_fence_after();
-                product(tmem + T_A, q, k, TCH, kd, false);
+                product<TCH, KW / 16, false, false>(tmem + T_A, base, PANEL, base + TILE_K, PANEL, false);
                 commit(bar(B_A));
             }
             for (int64_t n = 0; ok && n < N; ++n) {
-                tiles(n, q, k, v);
-                ok = wait(B_S, n) && (n == 0 || wait(B_OFREE, n - 1));
-                if (!ok) break;
+                const uint32_t q = base + uint32_t(n & 1) * STAGE, k = q + TILE_K, v = k + TILE_K;
+                if (!(ok = wait(B_S, n) && (n == 0 || wait(B_OFREE, n - 1)))) break;
                 tc_fence_after();
-                product(tmem + T_O1, q, Tile{S_AT, SPANEL, true}, VW, kd, false);
+                product<VW, KW / 16, false, true>(tmem + T_O1, q, PANEL, S_AT, SPANEL, false);
                 commit(bar(B_O1));
                 if (!(ok = wait(B_P, n))) break;
                 tc_fence_after();
-                product_ts(tmem + T_O2, tmem + T_A, v, VW, TCH / 16, false);
-                if (!(ok = wait(B_K, n))) break;
-                tc_fence_after();
-                // a tile of one panel gives its columns twice; the upper lanes are not read
-                Tile khi{k.at, KW == 64 ? 0u : PANEL, true}, klo{q.at, KW == 64 ? 0u : PANEL, true};
-                product(tmem + T_U, khi, v, VW, TCH / 16, false);
-                product(tmem + T_U, klo, v, VW, TCH / 16, true);
-                commit(bar(B_U));
+                product_ts<VW, TCH / 16>(tmem + T_O2, tmem + T_P, v, PANEL, false);
+                product_ts<VW, TCH / 16>(tmem + T_O2, tmem + T_P + 64, v, PANEL, true);
+                commit(bar(B_PV));
                 if (n + 1 < N) {
+                    // every warp has read this chunk's A (B_P)
                     const int s = int((n + 1) & 1);
-                    // P lies where the next A goes
-                    if (!(ok = wait(B_FULL0 + s, (n + 1) >> 1) && wait(B_U, n))) break;
+                    if (!(ok = wait(B_FULL0 + s, (n + 1) >> 1))) break;
                     tc_fence_after();
-                    tiles(n + 1, q, k, v);
-                    product(tmem + T_A, q, k, TCH, kd, false);
+                    const uint32_t q1 = base + s * STAGE;
+                    product<TCH, KW / 16, false, false>(tmem + T_A, q1, PANEL, q1 + TILE_K, PANEL, false);
                     commit(bar(B_A));
                 }
+                // U goes where P was
+                if (!(ok = wait(B_K, n) && wait(B_PV, n))) break;
+                tc_fence_after();
+                product<VW, TCH / 16, true, true>(tmem + T_U, k, WIDE, v, PANEL, false);
+                product<VW, TCH / 16, true, true>(tmem + T_U, q, WIDE, v, PANEL, true);
+                product<VW, TCH / 16, true, true>(tmem + T_U, S_AT, WIDE, v, PANEL, true);
+                commit(bar(B_U));
             }
             int quiet = 0;
             commit(bar(B_END));
@@ -309,122 +334,114 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
     } else {
         const int wq = warp & 3, g = warp >> 2, i = wq * 32 + lane, c0 = g * VH;
         const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
+        auto arrive = [&](int b) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(b));
+        };
         float S[VH];
         const int64_t dd = int64_t(a.Dk) * a.Dv;
         load_part<VH>(S, nseg > 1 ? a.S + int64_t(blockIdx.x) * dd : a.s0 ? a.s0 + seg.bh * dd : nullptr, i, c0, a);
         auto put_state = [&]() {
             if (i < KW) {
 #pragma unroll
-                for (int u = 0; u < VH; u += 32) put32(S_AT, SPANEL, i, c0 + u, reinterpret_cast<const float(&)[32]>(S[u]));
+                for (int u = 0; u < VH; u += 8) put8(S_AT, SPANEL, i, (c0 + u) >> 3, S + u);
             }
             fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_S));
+            arrive(B_S);
         };
         put_state();
         for (int64_t n = 0; n < N; ++n) {
             const int s = int(n & 1);
             const uint32_t Q = base + s * STAGE, K = Q + TILE_K, V = K + TILE_K;
             const ChunkDecay &d = dec[s];
-            bool ok = all_ok(wait(B_DEC0 + s, n >> 1) && wait(B_A, n));
-            // P: this thread's row i, columns 16 g .. + 16 of every block of 32
-            float A[4][16];
-            if (ok) {
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c <= wq) ld16(lanes + T_A + 32 * c + 16 * g, A[c]);
-                tc_fence_before();
-            }
-            // P goes where A was: the warp that shares these lanes has read its columns
-            asm volatile("bar.sync %0, 64;" ::"r"(2 + wq) : "memory");
-            if (ok) {
-                tc_fence_after();
+            // P, 8 g .. + 8 of every block of 32 columns.  B_S of this chunk: every warp has read the last U,
+            // whose place P takes.
+            if (!all_ok(wait(B_DEC0 + s, n >> 1) && wait(B_A, n) && wait(B_S, n))) break;
+            tc_fence_after();
+            {
                 const float xi = d.x[i];
                 const int ri = d.r[i];
+                auto put_p = [&](int c, const float (&p)[8]) {
+                    uint32_t h[4], l[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t p[8];
-                    const int j0 = 32 * c + 16 * g;
-                    if (c < wq) {
-                        const float f = ri == d.re[c]
-                                            ? fast_exp2((d.Ehi[wq] - d.Ehi[c]) + (d.Elo[wq] - d.Elo[c]) + xi) : 0.f;
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float w0 = d.wb[j0 + e] * f, w1 = d.wb[j0 + e + 1] * f;
-                            p[e / 2] = pack(w0 == 0.f ? 0.f : A[c][e] * w0, w1 == 0.f ? 0.f : A[c][e + 1] * w1);
-                        }
-                    } else if (c == wq) {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            float y[2];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int j = j0 + e + h;
-                                y[h] = j <= i && ri == d.r[j] ? A[c][e + h] * fast_exp2(xi - d.x[j]) : 0.f;
-                            }
-                            p[e / 2] = pack(y[0], y[1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) p[e] = 0u;
+                    for (int e = 0; e < 4; ++e) {
+                        h[e] = pack(p[2 * e], p[2 * e + 1]);
+                        l[e] = pack(p[2 * e] - lo_f(h[e]), p[2 * e + 1] - hi_f(h[e]));
                     }
-                    st8(lanes + T_A + 16 * c + 8 * g, p);
+                    st4(lanes + T_P + 16 * c + 4 * g, h[0], h[1], h[2], h[3]);
+                    st4(lanes + T_P + 64 + 16 * c + 4 * g, l[0], l[1], l[2], l[3]);
+                };
+#pragma unroll 1
+                for (int c = 0; c < wq; ++c) {
+                    float A[8], w[8];
+                    ld8(lanes + T_A + 32 * c + 8 * g, A);
+                    const float f = ri == d.re[c] ? fast_exp2((d.Ehi[wq] - d.Ehi[c]) + (d.Elo[wq] - d.Elo[c]) + xi) : 0.f;
+                    *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(d.wb + 32 * c + 8 * g);
+                    *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(d.wb + 32 * c + 8 * g + 4);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float x = w[e] * f;
+                        A[e] = x == 0.f ? 0.f : A[e] * x;
+                    }
+                    put_p(c, A);
+                }
+                float A[8], x[8];
+                const int j0 = 32 * wq + 8 * g;
+                ld8(lanes + T_A + j0, A);
+                *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(d.x + j0);
+                *reinterpret_cast<float4 *>(x + 4) = *reinterpret_cast<const float4 *>(d.x + j0 + 4);
+                const uint2 rj = *reinterpret_cast<const uint2 *>(d.r + j0);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int r = int(((e < 4 ? rj.x : rj.y) >> (8 * (e & 3))) & 255u);
+                    A[e] = 8 * g + e <= lane && ri == r ? A[e] * fast_exp2(xi - x[e]) : 0.f;
+                }
+                put_p(wq, A);
+#pragma unroll 1
+                for (int c = wq + 1; c < 4; ++c) {
+                    st4(lanes + T_P + 16 * c + 4 * g, 0u, 0u, 0u, 0u);
+                    st4(lanes + T_P + 64 + 16 * c + 4 * g, 0u, 0u, 0u, 0u);
                 }
                 st_wait();
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_P));
+                arrive(B_P);
             }
-            // l K: the first products are done with Q and K, whose tiles take the two parts
-            ok = ok && all_ok(wait(B_O1, n));
-            if (ok) {
-                scale_row(K, Q, PANEL, i, g * (KW / 16), (g + 1) * (KW / 16), d.to_end(i));
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_K));
-            }
-            ok = ok && all_ok(wait(B_U, n));
-            if (ok) {
-                tc_fence_after();
-                const float tot = d.total;
-#pragma unroll
-                for (int u = 0; u < VH; u += 32) {
-                    float x[32];
-                    ld32(lanes + T_U + c0 + u, x);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) S[u + e] = tot == 0.f ? x[e] : fmaf(tot, S[u + e], x[e]);
-                }
-                tc_fence_before();
-                put_state();
-                // outputs, through V's tile
+            // l K: the products of Q, K and S are done, and their tiles take its three parts
+            if (!all_ok(wait(B_O1, n))) break;
+            scale_row(K, Q, S_AT, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG), d.to_end(i));
+            fence_proxy_async_smem();
+            arrive(B_K);
+            // the outputs, held until V has been read
+            if (!all_ok(wait(B_PV, n))) break;
+            tc_fence_after();
+            uint32_t o[VH / 2];
+            {
                 const float f = d.first(i);
 #pragma unroll
-                for (int u = 0; u < VH; u += 32) {
-                    float x[32], y[32];
-                    ld32(lanes + T_O1 + c0 + u, x);
-                    ld32(lanes + T_O2 + c0 + u, y);
+                for (int u = 0; u < VH; u += 16) {
+                    float x[16], y[16];
+                    ld16x2(lanes + T_O1 + c0 + u, lanes + T_O2 + c0 + u, x, y);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) y[e] = a.scale * (f == 0.f ? y[e] : fmaf(f, x[e], y[e]));
-                    put32(V, PANEL, i, c0 + u, y);
+                    for (int e = 0; e < 16; ++e) y[e] = a.scale * (f == 0.f ? y[e] : fmaf(f, x[e], y[e]));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[u / 2 + e] = pack(y[2 * e], y[2 * e + 1]);
                 }
                 tc_fence_before();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_OFREE));
+                arrive(B_OFREE);
             }
-            if (!bar_red_and(1, CW * 32, ok)) break;
-            if (threadIdx.x == 0) {
-                for (int p = 0; p < VW / 64; ++p)
-                    store4(&m.o, p * 64, int(seg.h), int((seg.n0 + n) * TCH), int(seg.b), V + p * PANEL);
-                bulk_commit();
-                bulk_wait_read();
-                mbar_arrive(bar(B_EMPTY0 + s));
-            }
+            const float tot = d.total;
+            if (!all_ok(wait(B_U, n))) break;
+            tc_fence_after();
+            state_update<VH>(S, lanes + T_U + c0, tot);
+            tc_fence_before();
+            put_state();
+#pragma unroll
+            for (int u = 0; u < VH / 8; ++u)
+                sts(V + unit_at(i, (c0 >> 3) + u, PANEL), make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
+            fence_proxy_async_smem();
+            arrive(B_OUT);
         }
         if (a.s1 && seg.n1 == a.NC) store_part<VH>(S, a.s1 + seg.bh * dd, i, c0, a);
-        if (threadIdx.x == 0) bulk_wait_all();
-        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -439,17 +456,17 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
 // over it.  REV: the adjoint state from q and scale go, walked from the last chunk back.
 template <int KW, int VW>
 constexpr size_t state_smem() {
-    return 2 * size_t(KW + VW) * 256 + size_t(KW) * 256 + 2 * sizeof(ChunkDecay) + sizeof(Ctl);
+    return 2 * size_t(KW + VW) * 256 + 2 * size_t(KW) * 256 + 2 * sizeof(ChunkDecay) + sizeof(Ctl);
 }
 
 template <int KW, int VW, bool REV>
 __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_constant__ StateMaps m, const LinArgs a, int nseg,
                                                               int cps, unsigned *status) {
     constexpr uint32_t STAGE = (KW + VW) * 256, TILE_K = KW * 256, PANEL = TCH * 128;
-    constexpr int VH = VW / 2;
+    constexpr int VH = VW / CG;
     extern __shared__ __align__(1024) uint8_t sm[];
-    const uint32_t base = smem_u32(sm), LO = base + 2 * STAGE;
-    ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + 2 * STAGE + TILE_K);
+    const uint32_t base = smem_u32(sm), L1 = base + 2 * STAGE, L2 = L1 + TILE_K;
+    ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + 2 * STAGE + 2 * TILE_K);
     Ctl *ctl = reinterpret_cast<Ctl *>(dec + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Seg seg(a, nseg, cps);
@@ -458,7 +475,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
     if (seg.seg == (REV ? 0 : nseg - 1)) return;     // no segment reads what this one leaves
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(smem_u32(&ctl->bar[i]), i == B_K ? CW : 1);
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(smem_u32(&ctl->bar[i]), i == B_K || i == B_EMPTY0 || i == B_EMPTY1 ? CW : 1);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -503,12 +520,13 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
         if (lane == 0) {
             for (int64_t n = 0; n < N; ++n) {
                 const int s = int(n & 1);
+                // B_K: the operands are there, and (n > 0) every warp has read the last product
                 if (!(wait(B_FULL0 + s, n >> 1) && wait(B_K, n))) break;
                 tc_fence_after();
                 const uint32_t at = base + s * STAGE, wide = KW == 64 ? 0u : PANEL;
-                const Tile y{at + TILE_K, PANEL, true};
-                product(tmem, Tile{at, wide, true}, y, VW, TCH / 16, false);
-                product(tmem, Tile{LO, wide, true}, y, VW, TCH / 16, true);
+                product<VW, TCH / 16, true, true>(tmem, at, wide, at + TILE_K, PANEL, false);
+                product<VW, TCH / 16, true, true>(tmem, L1, wide, at + TILE_K, PANEL, true);
+                product<VW, TCH / 16, true, true>(tmem, L2, wide, at + TILE_K, PANEL, true);
                 commit(bar(B_U));
             }
             int quiet = 0;
@@ -516,39 +534,30 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
             mbar_wait(bar(B_END), 0, &quiet, status);
         }
         __syncwarp();
-    } else {
+    } else if (warp < CW) {
         const int wq = warp & 3, g = warp >> 2, i = wq * 32 + lane, c0 = g * VH;
         const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
+        auto arrive = [&](int b) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(b));
+        };
         float S[VH];
 #pragma unroll
         for (int u = 0; u < VH; ++u) S[u] = 0.f;
         for (int64_t n = 0; n < N; ++n) {
             const int s = int(n & 1);
             const ChunkDecay &d = dec[s];
-            bool ok = all_ok(wait(B_FULL0 + s, n >> 1) && wait(B_DEC0 + s, n >> 1));
-            if (ok) {
-                scale_row(base + s * STAGE, LO, PANEL, i, g * (KW / 16), (g + 1) * (KW / 16),
-                          REV ? d.first(i) * a.scale : d.to_end(i));
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_K));
-            }
+            if (!all_ok(wait(B_FULL0 + s, n >> 1) && wait(B_DEC0 + s, n >> 1))) break;
+            scale_row(base + s * STAGE, L1, L2, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG),
+                      REV ? d.first(i) * a.scale : d.to_end(i));
+            fence_proxy_async_smem();
+            arrive(B_K);
             const float tot = d.total;
-            ok = ok && all_ok(wait(B_U, n));
-            if (ok) {
-                tc_fence_after();
-#pragma unroll
-                for (int u = 0; u < VH; u += 32) {
-                    float x[32];
-                    ld32(lanes + c0 + u, x);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) S[u + e] = tot == 0.f ? x[e] : fmaf(tot, S[u + e], x[e]);
-                }
-                tc_fence_before();
-            }
-            // every warp is done with the stage, its decays and the accumulator
-            if (!bar_red_and(1, CW * 32, ok)) break;
-            if (threadIdx.x == 0) mbar_arrive(bar(B_EMPTY0 + s));
+            if (!all_ok(wait(B_U, n))) break;
+            tc_fence_after();
+            state_update<VH>(S, lanes + c0, tot);
+            tc_fence_before();
+            arrive(B_EMPTY0 + s);       // done with the stage, its decays and the accumulator
         }
         float *out = (REV ? a.dS : a.S) + int64_t(blockIdx.x) * a.Dk * a.Dv;
         store_part<VH>(S, out, i, c0, a);

@@ -52,56 +52,76 @@ __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// One operand in shared memory: where it starts and how one k-step of 16 advances it.
+// One operand in shared memory: where it starts, the bytes of a panel, and whether K runs
+// across the rows.  The descriptor of k-step ks (16 of K) is the first one's plus an offset.
 struct Tile {
-    uint32_t at, panel;     // start; bytes of a panel
-    bool mn;                // K runs across the rows
+    uint32_t at, panel;
+    bool mn;
+    __device__ __forceinline__ uint64_t first() const { return mn ? desc_mn(at, panel) : desc_k(at); }
     __device__ __forceinline__ uint64_t step(int ks) const {
-        return mn ? desc_mn(at + uint32_t(ks) * 2048u, panel) : desc_k(at + uint32_t(ks >> 2) * panel + uint32_t(ks & 3) * 32u);
+        return uint64_t((mn ? uint32_t(ks) * 2048u : uint32_t(ks >> 2) * panel + uint32_t(ks & 3) * 32u) >> 4);
     }
 };
-// D[128, n] (+)= A B over k16 steps of 16
-__device__ __forceinline__ void product(uint32_t d, const Tile &a, const Tile &b, int n, int k16, bool acc) {
-    const uint32_t id = idesc(n, a.mn, b.mn);
-    for (int k = 0; k < k16; ++k) mma_ss(d, a.step(k), b.step(k), id, acc || k);
+// D[128, N] (+)= A B over K16 steps of 16
+template <int N, int K16, bool A_MN, bool B_MN>
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t a_panel, uint32_t b, uint32_t b_panel, bool acc) {
+    const Tile ta{a, a_panel, A_MN}, tb{b, b_panel, B_MN};
+    const uint64_t da = ta.first(), db = tb.first();
+#pragma unroll
+    for (int k = 0; k < K16; ++k) mma_ss(d, da + ta.step(k), db + tb.step(k), idesc(N, A_MN, B_MN), acc || k);
 }
-// A in tensor memory: bf16 pairs, 8 columns a step
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, const Tile &b, int n, int k16, bool acc) {
-    const uint32_t id = idesc(n, false, b.mn);
-    for (int k = 0; k < k16; ++k) mma_ts(d, a + uint32_t(k) * 8u, b.step(k), id, acc || k);
+// A in tensor memory: bf16 pairs, 8 columns a step; B across its rows
+template <int N, int K16>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_panel, bool acc) {
+    const Tile tb{b, b_panel, true};
+    const uint64_t db = tb.first();
+#pragma unroll
+    for (int k = 0; k < K16; ++k) mma_ts(d, a + uint32_t(k) * 8u, db + tb.step(k), idesc(N, false, true), acc || k);
 }
 
+// Columns of one warp's 32 lanes: thread t gets those of lane t.  The wait is part of the load,
+// so that no use of a register can come before it.
+__device__ __forceinline__ void ld8(uint32_t t, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(t)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void ld16(uint32_t t, float (&v)[16]) {
     uint32_t r[16];
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(t)
         : "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void ld32(uint32_t t, float (&v)[32]) {
-    uint32_t r[32];
+// two loads in flight
+__device__ __forceinline__ void ld16x2(uint32_t t, uint32_t u, float (&v)[16], float (&w)[16]) {
+    uint32_t r[16], q[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(t)
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7]), "=r"(q[8]), "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]), "=r"(q[14]), "=r"(q[15])
+        : "r"(t), "r"(u)
         : "memory");
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 16; ++i) {
+        v[i] = __uint_as_float(r[i]);
+        w[i] = __uint_as_float(q[i]);
+    }
 }
-__device__ __forceinline__ void st8(uint32_t t, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+__device__ __forceinline__ void st4(uint32_t t, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(t), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
 }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
