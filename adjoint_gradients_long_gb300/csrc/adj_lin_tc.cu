@@ -52,15 +52,18 @@ struct alignas(16) ChunkDecay {
     }
     __device__ __forceinline__ float to_end(int t) const { return wb[t] * last[t >> 5]; }
 
-    // by one whole warp: g[n * pitch], n < len (tokens past len have decay 1); the chunk's sum of
-    // logarithms is returned
-    __device__ double fill(const float *g, int64_t pitch, int len) {
+    // by one whole warp: this lane's four tokens of a chunk (tokens past len have decay 1) ...
+    static __device__ __forceinline__ float4 fetch(const float *g, int64_t pitch, int len) {
+        const int t = (threadIdx.x & 31) * 4;
+        return make_float4(t < len ? __ldg(g + t * pitch) : 0.f, t + 1 < len ? __ldg(g + (t + 1) * pitch) : 0.f,
+                           t + 2 < len ? __ldg(g + (t + 2) * pitch) : 0.f, t + 3 < len ? __ldg(g + (t + 3) * pitch) : 0.f);
+    }
+    // ... and their decays; the chunk's sum of logarithms is returned
+    __device__ double fill(float4 own) {
         const int lane = threadIdx.x & 31;
         double s[4], sum = 0.0;
         int c[4], cnt = 0;
-        float v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = lane * 4 + u < len ? __ldg(g + (lane * 4 + u) * pitch) : 0.f;
+        const float v[4] = {own.x, own.y, own.z, own.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const bool cut = v[u] < LIN_RESET;
@@ -114,7 +117,7 @@ struct StateMaps {
     CUtensorMap x, y;
 };
 
-enum { B_FULL0, B_FULL1, B_EMPTY0, B_EMPTY1, B_DEC0, B_DEC1, B_A, B_O1, B_PV, B_P, B_K, B_U, B_S, B_OFREE, B_OUT, B_END, B_COUNT };
+enum { B_FULL0, B_FULL1, B_EMPTY0, B_EMPTY1, B_DEC0, B_DEC1, B_A, B_PV, B_P, B_K, B_U, B_S, B_OUT, B_END, B_AR, B_COUNT = B_AR + 4 };
 struct Ctl {
     uint64_t bar[B_COUNT];
     uint32_t tmem;
@@ -152,15 +155,54 @@ __device__ __forceinline__ void scale_row(uint32_t t0, uint32_t t1, uint32_t t2,
     }
 }
 
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+// The same in two parts (2^-17 of a value), three instructions for a pair of values: with
+// w = w1 + w2 in bf16, x w1 has 16 bits, so h = bf16(x w1) and its remainder are exact, and x w2
+// joins the remainder.
+__device__ __forceinline__ void scale_row2(uint32_t t0, uint32_t t1, uint32_t panel, int r, int u0, int u1, float w) {
+    const uint32_t w1 = pack(w, w);
+    const float rest = w - lo_f(w1);
+    const uint32_t w2 = pack(rest, rest);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        const int u = u0 + v;
+        if (u >= u1) break;
+        const uint32_t at = unit_at(r, u, panel);
+        uint4 x = lds(t0 + at);
+        if (w == 0.f) x = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = mul2(in[i], w1);
+            l[i] = fma2(in[i], w2, fma2(in[i], w1, h[i] ^ 0x80008000u));
+        }
+        sts(t0 + at, make_uint4(h[0], h[1], h[2], h[3]));
+        sts(t1 + at, make_uint4(l[0], l[1], l[2], l[3]));
+    }
+}
+
 // S <- tot S + U, for this thread's columns
 template <int VH>
 __device__ __forceinline__ void state_update(float (&S)[VH], uint32_t u, float tot) {
+    float x[VH];
+    if (VH == 32) ld16x2(u, u + 16, reinterpret_cast<float(&)[16]>(x[0]), reinterpret_cast<float(&)[16]>(x[VH - 16]));
+    else ld16(u, reinterpret_cast<float(&)[16]>(x[0]));
+    if (tot == 0.f) {                   // a new start drops the state whatever it holds
 #pragma unroll
-    for (int c = 0; c < VH; c += 16) {
-        float x[16];
-        ld16(u + c, x);
+        for (int e = 0; e < VH; ++e) S[e] = x[e];
+    } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) S[c + e] = tot == 0.f ? x[e] : fmaf(tot, S[c + e], x[e]);
+        for (int e = 0; e < VH; ++e) S[e] = fmaf(tot, S[e], x[e]);
     }
 }
 
@@ -189,6 +231,11 @@ struct Seg {
         n1 = n0 + cps < a.NC ? n0 + cps : a.NC;
     }
 };
+
+__device__ __forceinline__ float4 gates(const LinArgs &a, const Seg &seg, int64_t chunk) {
+    const int64_t t = chunk * TCH;
+    return ChunkDecay::fetch(a.g + (seg.b * a.T + t) * a.H + seg.h, a.H, int(a.T - t < TCH ? a.T - t : TCH));
+}
 
 // This thread's part of a state: row d, columns c0 .. c0 + VH.
 template <int VH>
@@ -219,10 +266,13 @@ constexpr size_t fwd_smem() {
 
 template <int KW, int VW>
 __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constant__ FwdMaps m, const LinArgs a, int nseg,
-                                                            int cps, unsigned *status) {
+                                                            int cps, int parts, unsigned *status) {
     constexpr uint32_t STAGE = (2 * KW + VW) * 256, TILE_K = KW * 256, PANEL = TCH * 128, SPANEL = KW * 128;
     constexpr int VH = VW / CG;         // state and output columns of a thread
-    constexpr uint32_t T_A = 0, T_U = 128, T_P = T_U, T_O1 = 256, T_O2 = 384;
+    constexpr uint32_t T_A = 0, T_P = T_A, T_O2 = 384;
+    // O1 and U take turns: the next chunk's O1 goes where U was, as soon as the state has it
+    auto T_O1 = [](int64_t n) { return n & 1 ? 256u : 128u; };
+    auto T_U = [](int64_t n) { return n & 1 ? 128u : 256u; };
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t base = smem_u32(sm), S_AT = base + 2 * STAGE;
     ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + 2 * STAGE + TILE_K);
@@ -233,7 +283,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < B_COUNT; ++i)
-            mbar_init(smem_u32(&ctl->bar[i]), i == B_P || i == B_K || i == B_S || i == B_OFREE || i == B_OUT ? CW : 1);
+            mbar_init(smem_u32(&ctl->bar[i]), i >= B_AR ? CG : i == B_P || i == B_K || i == B_S || i == B_OUT ? CW : 1);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -264,11 +314,13 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
         }
         __syncwarp();
     } else if (warp == W_DEC) {
+        float4 own = gates(a, seg, seg.n0);
         for (int64_t n = 0; n < N; ++n) {
             const int s = int(n & 1);
+            const float4 now = own;
+            if (n + 1 < N) own = gates(a, seg, seg.n0 + n + 1);
             if (n >= 2 && !all_ok(wait(B_EMPTY0 + s, (n >> 1) - 1))) break;
-            const int64_t t = (seg.n0 + n) * TCH;
-            dec[s].fill(a.g + (seg.b * a.T + t) * a.H + seg.h, a.H, int(a.T - t < TCH ? a.T - t : TCH));
+            dec[s].fill(now);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_DEC0 + s));
         }
@@ -292,39 +344,28 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             // a tile of one panel read across its rows gives its columns twice; the upper lanes of that
             // product are not read
             constexpr uint32_t WIDE = KW == 64 ? 0u : PANEL;
-            bool ok = wait(B_FULL0, 0);
-            if (ok) {
-                tc_fence_after();
-                product<TCH, KW / 16, false, false>(tmem + T_A, base, PANEL, base + TILE_K, PANEL, false);
-                commit(bar(B_A));
-            }
-            for (int64_t n = 0; ok && n < N; ++n) {
+            for (int64_t n = 0; n < N; ++n) {
                 const uint32_t q = base + uint32_t(n & 1) * STAGE, k = q + TILE_K, v = k + TILE_K;
-                if (!(ok = wait(B_S, n) && (n == 0 || wait(B_OFREE, n - 1)))) break;
+                if (!(wait(B_FULL0 + int(n & 1), n >> 1) && wait(B_S, n))) break;
                 tc_fence_after();
-                product<VW, KW / 16, false, true>(tmem + T_O1, q, PANEL, S_AT, SPANEL, false);
-                commit(bar(B_O1));
-                if (!(ok = wait(B_P, n))) break;
+                product<VW, KW / 16, false, true>(tmem + T_O1(n), q, PANEL, S_AT, SPANEL, false);
+                // A goes where the last P was
+                if (n && !wait(B_PV, n - 1)) break;
+                tc_fence_after();
+                product<TCH, KW / 16, false, false>(tmem + T_A, q, PANEL, k, PANEL, false);
+                commit(bar(B_A));
+                // B_K, B_P: also every warp has read the last chunk's O1 and O2
+                if (!wait(B_K, n)) break;
+                tc_fence_after();
+                product<VW, TCH / 16, true, true>(tmem + T_U(n), k, WIDE, v, PANEL, false);
+                product<VW, TCH / 16, true, true>(tmem + T_U(n), q, WIDE, v, PANEL, true);
+                if (parts == 3) product<VW, TCH / 16, true, true>(tmem + T_U(n), S_AT, WIDE, v, PANEL, true);
+                commit(bar(B_U));
+                if (!wait(B_P, n)) break;
                 tc_fence_after();
                 product_ts<VW, TCH / 16>(tmem + T_O2, tmem + T_P, v, PANEL, false);
                 product_ts<VW, TCH / 16>(tmem + T_O2, tmem + T_P + 64, v, PANEL, true);
                 commit(bar(B_PV));
-                if (n + 1 < N) {
-                    // every warp has read this chunk's A (B_P)
-                    const int s = int((n + 1) & 1);
-                    if (!(ok = wait(B_FULL0 + s, (n + 1) >> 1))) break;
-                    tc_fence_after();
-                    const uint32_t q1 = base + s * STAGE;
-                    product<TCH, KW / 16, false, false>(tmem + T_A, q1, PANEL, q1 + TILE_K, PANEL, false);
-                    commit(bar(B_A));
-                }
-                // U goes where P was
-                if (!(ok = wait(B_K, n) && wait(B_PV, n))) break;
-                tc_fence_after();
-                product<VW, TCH / 16, true, true>(tmem + T_U, k, WIDE, v, PANEL, false);
-                product<VW, TCH / 16, true, true>(tmem + T_U, q, WIDE, v, PANEL, true);
-                product<VW, TCH / 16, true, true>(tmem + T_U, S_AT, WIDE, v, PANEL, true);
-                commit(bar(B_U));
             }
             int quiet = 0;
             commit(bar(B_END));
@@ -354,94 +395,93 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             const int s = int(n & 1);
             const uint32_t Q = base + s * STAGE, K = Q + TILE_K, V = K + TILE_K;
             const ChunkDecay &d = dec[s];
-            // P, 8 g .. + 8 of every block of 32 columns.  B_S of this chunk: every warp has read the last U,
-            // whose place P takes.
-            if (!all_ok(wait(B_DEC0 + s, n >> 1) && wait(B_A, n) && wait(B_S, n))) break;
+            // l K: the products of Q, K and S are done, and their tiles take its three parts
+            if (!all_ok(wait(B_DEC0 + s, n >> 1) && wait(B_A, n))) break;
             tc_fence_after();
+            if (parts == 3) scale_row(K, Q, S_AT, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG), d.to_end(i));
+            else scale_row2(K, Q, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG), d.to_end(i));
+            fence_proxy_async_smem();
+            arrive(B_K);
+            // P while U is formed: 8 g .. + 8 of every block of 32 columns, in place of A
             {
                 const float xi = d.x[i];
                 const int ri = d.r[i];
-                auto put_p = [&](int c, const float (&p)[8]) {
-                    uint32_t h[4], l[4];
+                uint32_t h[4][4], l[4][4];
+                auto split = [&](int c, const float (&p)[8]) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        h[e] = pack(p[2 * e], p[2 * e + 1]);
-                        l[e] = pack(p[2 * e] - lo_f(h[e]), p[2 * e + 1] - hi_f(h[e]));
+                        h[c][e] = pack(p[2 * e], p[2 * e + 1]);
+                        l[c][e] = pack(p[2 * e] - lo_f(h[c][e]), p[2 * e + 1] - hi_f(h[c][e]));
                     }
-                    st4(lanes + T_P + 16 * c + 4 * g, h[0], h[1], h[2], h[3]);
-                    st4(lanes + T_P + 64 + 16 * c + 4 * g, l[0], l[1], l[2], l[3]);
                 };
-#pragma unroll 1
-                for (int c = 0; c < wq; ++c) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
                     float A[8], w[8];
-                    ld8(lanes + T_A + 32 * c + 8 * g, A);
-                    const float f = ri == d.re[c] ? fast_exp2((d.Ehi[wq] - d.Ehi[c]) + (d.Elo[wq] - d.Elo[c]) + xi) : 0.f;
-                    *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(d.wb + 32 * c + 8 * g);
-                    *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(d.wb + 32 * c + 8 * g + 4);
+                    const int j0 = 32 * c + 8 * g;
+                    if (c < wq) {
+                        ld8(lanes + T_A + j0, A);
+                        const float f = ri == d.re[c] ? fast_exp2((d.Ehi[wq] - d.Ehi[c]) + (d.Elo[wq] - d.Elo[c]) + xi) : 0.f;
+                        *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(d.wb + j0);
+                        *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(d.wb + j0 + 4);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float x = w[e] * f;
-                        A[e] = x == 0.f ? 0.f : A[e] * x;
+                        for (int e = 0; e < 8; ++e) {
+                            const float x = w[e] * f;
+                            A[e] = x == 0.f ? 0.f : A[e] * x;
+                        }
+                        split(c, A);
+                    } else if (c == wq) {
+                        ld8(lanes + T_A + j0, A);
+                        *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(d.x + j0);
+                        *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(d.x + j0 + 4);
+                        const uint2 rj = *reinterpret_cast<const uint2 *>(d.r + j0);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int r = int(((e < 4 ? rj.x : rj.y) >> (8 * (e & 3))) & 255u);
+                            A[e] = 8 * g + e <= lane && ri == r ? A[e] * fast_exp2(xi - w[e]) : 0.f;
+                        }
+                        split(c, A);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) h[c][e] = l[c][e] = 0u;
                     }
-                    put_p(c, A);
                 }
-                float A[8], x[8];
-                const int j0 = 32 * wq + 8 * g;
-                ld8(lanes + T_A + j0, A);
-                *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(d.x + j0);
-                *reinterpret_cast<float4 *>(x + 4) = *reinterpret_cast<const float4 *>(d.x + j0 + 4);
-                const uint2 rj = *reinterpret_cast<const uint2 *>(d.r + j0);
+                tc_fence_before();
+                arrive(B_AR + wq);
+                // the warps of these lanes have read their columns
+                if (!all_ok(wait(B_AR + wq, n))) break;
+                tc_fence_after();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int r = int(((e < 4 ? rj.x : rj.y) >> (8 * (e & 3))) & 255u);
-                    A[e] = 8 * g + e <= lane && ri == r ? A[e] * fast_exp2(xi - x[e]) : 0.f;
-                }
-                put_p(wq, A);
-#pragma unroll 1
-                for (int c = wq + 1; c < 4; ++c) {
-                    st4(lanes + T_P + 16 * c + 4 * g, 0u, 0u, 0u, 0u);
-                    st4(lanes + T_P + 64 + 16 * c + 4 * g, 0u, 0u, 0u, 0u);
+                for (int c = 0; c < 4; ++c) {
+                    st4(lanes + T_P + 16 * c + 4 * g, h[c][0], h[c][1], h[c][2], h[c][3]);
+                    st4(lanes + T_P + 64 + 16 * c + 4 * g, l[c][0], l[c][1], l[c][2], l[c][3]);
                 }
                 st_wait();
                 tc_fence_before();
                 arrive(B_P);
             }
-            // l K: the products of Q, K and S are done, and their tiles take its three parts
-            if (!all_ok(wait(B_O1, n))) break;
-            scale_row(K, Q, S_AT, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG), d.to_end(i));
-            fence_proxy_async_smem();
-            arrive(B_K);
-            // the outputs, held until V has been read
-            if (!all_ok(wait(B_PV, n))) break;
-            tc_fence_after();
-            uint32_t o[VH / 2];
-            {
-                const float f = d.first(i);
-#pragma unroll
-                for (int u = 0; u < VH; u += 16) {
-                    float x[16], y[16];
-                    ld16x2(lanes + T_O1 + c0 + u, lanes + T_O2 + c0 + u, x, y);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) y[e] = a.scale * (f == 0.f ? y[e] : fmaf(f, x[e], y[e]));
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[u / 2 + e] = pack(y[2 * e], y[2 * e + 1]);
-                }
-                tc_fence_before();
-                arrive(B_OFREE);
-            }
-            const float tot = d.total;
             if (!all_ok(wait(B_U, n))) break;
             tc_fence_after();
-            state_update<VH>(S, lanes + T_U + c0, tot);
+            state_update<VH>(S, lanes + T_U(n) + c0, d.total);
             tc_fence_before();
             put_state();
+            // the outputs, through V's tile
+            const float f = d.first(i);
+            if (!all_ok(wait(B_PV, n))) break;
+            tc_fence_after();
 #pragma unroll
-            for (int u = 0; u < VH / 8; ++u)
-                sts(V + unit_at(i, (c0 >> 3) + u, PANEL), make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
+            for (int u = 0; u < VH; u += 16) {
+                float x[16], y[16];
+                ld16x2(lanes + T_O1(n) + c0 + u, lanes + T_O2 + c0 + u, x, y);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = a.scale * (f == 0.f ? y[e] : fmaf(f, x[e], y[e]));
+                put8(V, PANEL, i, (c0 + u) >> 3, y);
+                put8(V, PANEL, i, ((c0 + u) >> 3) + 1, y + 8);
+            }
+            tc_fence_before();
             fence_proxy_async_smem();
             arrive(B_OUT);
         }
-        if (a.s1 && seg.n1 == a.NC) store_part<VH>(S, a.s1 + seg.bh * dd, i, c0, a);
+        if (a.s1 && nseg == 1) store_part<VH>(S, a.s1 + seg.bh * dd, i, c0, a);
     }
     tc_fence_before();
     __syncthreads();
@@ -472,7 +512,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
     const Seg seg(a, nseg, cps);
     const int64_t N = seg.n1 - seg.n0;
     auto chunk = [&](int64_t n) { return REV ? seg.n1 - 1 - n : seg.n0 + n; };
-    if (seg.seg == (REV ? 0 : nseg - 1)) return;     // no segment reads what this one leaves
+    // no segment reads what the last one leaves: only the final state does
+    if (seg.seg == (REV ? 0 : nseg - 1) && !(REV ? a.ds0 : a.s1)) return;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < B_COUNT; ++i) mbar_init(smem_u32(&ctl->bar[i]), i == B_K || i == B_EMPTY0 || i == B_EMPTY1 ? CW : 1);
@@ -506,11 +547,13 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
     } else if (warp == W_DEC) {
         double sum = 0.0;
         int cuts = 0;
+        float4 own = gates(a, seg, chunk(0));
         for (int64_t n = 0; n < N; ++n) {
             const int s = int(n & 1);
+            const float4 now = own;
+            if (n + 1 < N) own = gates(a, seg, chunk(n + 1));
             if (n >= 2 && !all_ok(wait(B_EMPTY0 + s, (n >> 1) - 1))) break;
-            const int64_t t = chunk(n) * TCH;
-            sum += dec[s].fill(a.g + (seg.b * a.T + t) * a.H + seg.h, a.H, int(a.T - t < TCH ? a.T - t : TCH));
+            sum += dec[s].fill(now);
             __syncwarp();
             cuts += dec[s].n_cut;
             if (lane == 0) mbar_arrive(bar(B_DEC0 + s));
@@ -598,14 +641,14 @@ cudaError_t run_fwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cuda
         return cudaErrorInvalidValue;
     if (sp.nseg > 1) {
         LIN_CUDA((run_states<KW, VW, false>(a, sp, status, st)));
-        LinArgs b = a;
-        b.s1 = nullptr;                 // the last segment writes it
-        LIN_CUDA(launch_lin_scan(b, sp.nseg, false, st));
+        LIN_CUDA(launch_lin_scan(a, sp.nseg, false, st));
     }
     constexpr size_t smem = fwd_smem<KW, VW>();
     LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_fwd<KW, VW>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
     ProfScope ps(K_LIN_OUT, st);
-    k_lin_tc_fwd<KW, VW><<<unsigned(a.B * a.H * sp.nseg), TC_BLOCK, smem, st>>>(m, a, sp.nseg, sp.cps, status);
+    // the state is a result only where no segments' states were joined: otherwise it meets bf16 next
+    const int parts = sp.nseg == 1 && a.s1 ? 3 : 2;
+    k_lin_tc_fwd<KW, VW><<<unsigned(a.B * a.H * sp.nseg), TC_BLOCK, smem, st>>>(m, a, sp.nseg, sp.cps, parts, status);
     return cudaGetLastError();
 }
 
