@@ -26,11 +26,37 @@ namespace {
 using namespace tc5;
 
 constexpr int TCH = 128;                // tokens of a chunk
-constexpr int CG = 4, CW = 4 * CG;      // computing warps: groups of four, a group covers the 128 lanes
-constexpr int W_MMA = CW, W_TMA = CW + 1, W_DEC = CW + 2, W_OUT = CW + 3;
-constexpr int TC_BLOCK = (CW + 4) * 32;
+// Warps of a block.  Two sets of eight computing warps (two groups of four; a group covers the 128
+// lanes of tensor memory, a warp the lanes of its number modulo four), and one warp each that
+// issues products, copies in, copies out, and prepares the decays.
+constexpr int CG = 2, SET = 4 * CG;
+constexpr int W_MMA = 2 * SET, W_TMA = W_MMA + 1, W_DEC = W_MMA + 2, W_OUT = W_MMA + 3;
+constexpr int TC_BLOCK = (W_OUT + 1) * 32;
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A sum kept as hi + lo, 48 bits: the fp64 pipe is too slow for one warp to keep up with a chunk.
+struct Sum2 {
+    float hi, lo;
+    __device__ __forceinline__ static Sum2 two(float a, float b) {      // a + b exactly
+        const float s = a + b, t = s - a;
+        return Sum2{s, (a - (s - t)) + (b - t)};
+    }
+    __device__ __forceinline__ static Sum2 log2_of(float x) {           // x log2 e
+        constexpr float H = 1.44269502162933349609375f, L = 1.925963033500011079e-8f;
+        const float p = x * H;
+        return Sum2{p, fmaf(x, L, fmaf(x, H, -p))};
+    }
+    __device__ __forceinline__ Sum2 operator+(Sum2 o) const {
+        const Sum2 s = two(hi, o.hi);
+        const float l = s.lo + (lo + o.lo), h = s.hi + l;
+        return Sum2{h, l - (h - s.hi)};
+    }
+    __device__ __forceinline__ Sum2 operator-(Sum2 o) const { return *this + Sum2{-o.hi, -o.lo}; }
+    __device__ __forceinline__ float value() const { return hi + lo; }
+    __device__ __forceinline__ Sum2 up(int d) const { return Sum2{__shfl_up_sync(~0u, hi, d), __shfl_up_sync(~0u, lo, d)}; }
+    __device__ __forceinline__ Sum2 from(int l) const { return Sum2{__shfl_sync(~0u, hi, l), __shfl_sync(~0u, lo, l)}; }
+};
 
 // The decays of one chunk, by blocks of 32 tokens.  In powers of two, with G_t the sum of the
 // log decays from the chunk's start to t and E_b its value at block b's last token:
@@ -59,51 +85,56 @@ struct alignas(16) ChunkDecay {
                            t + 2 < len ? __ldg(g + (t + 2) * pitch) : 0.f, t + 3 < len ? __ldg(g + (t + 3) * pitch) : 0.f);
     }
     // ... and their decays; the chunk's sum of logarithms is returned
-    __device__ double fill(float4 own) {
+    __device__ Sum2 fill(float4 own) {
         const int lane = threadIdx.x & 31;
-        double s[4], sum = 0.0;
-        int c[4], cnt = 0;
         const float v[4] = {own.x, own.y, own.z, own.w};
+        Sum2 s[4], sum{0.f, 0.f};
+        int c[4], cnt = 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const bool cut = v[u] < LIN_RESET;
-            sum += cut ? 0.0 : double(v[u]) * 1.4426950408889634;
+            const float x = cut ? 0.f : v[u];
+            sum = sum + Sum2::log2_of(x);
             cnt += cut;
             s[u] = sum;
             c[u] = cnt;
         }
-        double run = sum;
+        Sum2 run = sum;
         int rc = cnt;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const double p = __shfl_up_sync(~0u, run, d);
+            const Sum2 p = run.up(d);
             const int q = __shfl_up_sync(~0u, rc, d);
             if (lane >= d) {
-                run += p;
+                run = p + run;
                 rc += q;
             }
         }
-        const double E = __shfl_sync(~0u, run, lane | 7), Eall = __shfl_sync(~0u, run, 31);
+        const Sum2 E = run.from(lane | 7), Eall = run.from(31);
         const int reb = __shfl_sync(~0u, rc, lane | 7), rall = __shfl_sync(~0u, rc, 31);
-        const double before = run - sum;
+        Sum2 before = run.up(1);
+        if (lane == 0) before = Sum2{0.f, 0.f};
         const int cb = rc - cnt;
+        float xs[4], ws[4];
+        uint32_t rs = 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int t = lane * 4 + u;
-            const float d = float((before + s[u]) - E);
-            x[t] = d;
-            r[t] = uint8_t(cb + c[u]);
-            wb[t] = cb + c[u] == reb ? fast_exp2(-d) : 0.f;
+            xs[u] = ((before + s[u]) - E).value();
+            ws[u] = cb + c[u] == reb ? fast_exp2(-xs[u]) : 0.f;
+            rs |= uint32_t(cb + c[u]) << (8 * u);
         }
+        reinterpret_cast<float4 *>(x)[lane] = make_float4(xs[0], xs[1], xs[2], xs[3]);
+        reinterpret_cast<float4 *>(wb)[lane] = make_float4(ws[0], ws[1], ws[2], ws[3]);
+        reinterpret_cast<uint32_t *>(r)[lane] = rs;
         if ((lane & 7) == 7) {
             const int b = lane >> 3;
-            Ehi[b] = float(E);
-            Elo[b] = float(E - double(float(E)));
+            Ehi[b] = E.hi;
+            Elo[b] = E.lo;
             re[b] = reb;
-            last[b] = reb == rall ? fast_exp2(float(Eall - E)) : 0.f;
+            last[b] = reb == rall ? fast_exp2((Eall - E).value()) : 0.f;
         }
         if (lane == 0) {
-            total = rall == 0 ? fast_exp2(float(Eall)) : 0.f;
+            total = rall == 0 ? fast_exp2(Eall.value()) : 0.f;
             n_cut = rall;
         }
         return Eall;
@@ -117,9 +148,18 @@ struct StateMaps {
     CUtensorMap x, y;
 };
 
-enum { B_FULL0, B_FULL1, B_EMPTY0, B_EMPTY1, B_DEC0, B_DEC1, B_A, B_PV, B_P, B_K, B_U, B_S, B_OUT, B_END, B_AR, B_COUNT = B_AR + 4 };
+struct Wait {
+    uint64_t *bar;
+    volatile int *abort;
+    unsigned *status;
+    // the n-th completion of barrier i
+    __device__ __forceinline__ bool operator()(int i, int64_t n) const {
+        return mbar_wait(smem_u32(bar + i), uint32_t(n & 1), abort, status);
+    }
+};
+template <int N>
 struct Ctl {
-    uint64_t bar[B_COUNT];
+    uint64_t bar[N];
     uint32_t tmem;
     int abort;
 };
@@ -172,10 +212,8 @@ __device__ __forceinline__ void scale_row2(uint32_t t0, uint32_t t1, uint32_t pa
     const uint32_t w1 = pack(w, w);
     const float rest = w - lo_f(w1);
     const uint32_t w2 = pack(rest, rest);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        const int u = u0 + v;
-        if (u >= u1) break;
+#pragma unroll 4
+    for (int u = u0; u < u1; ++u) {
         const uint32_t at = unit_at(r, u, panel);
         uint4 x = lds(t0 + at);
         if (w == 0.f) x = make_uint4(0u, 0u, 0u, 0u);
@@ -194,28 +232,21 @@ __device__ __forceinline__ void scale_row2(uint32_t t0, uint32_t t1, uint32_t pa
 // S <- tot S + U, for this thread's columns
 template <int VH>
 __device__ __forceinline__ void state_update(float (&S)[VH], uint32_t u, float tot) {
-    float x[VH];
-    if (VH == 32) ld16x2(u, u + 16, reinterpret_cast<float(&)[16]>(x[0]), reinterpret_cast<float(&)[16]>(x[VH - 16]));
-    else ld16(u, reinterpret_cast<float(&)[16]>(x[0]));
-    if (tot == 0.f) {                   // a new start drops the state whatever it holds
 #pragma unroll
-        for (int e = 0; e < VH; ++e) S[e] = x[e];
-    } else {
+    for (int c = 0; c < VH; c += 16) {
+        float x[16];
+        ld16(u + c, x);
+        if (tot == 0.f) {               // a new start drops the state whatever it holds
 #pragma unroll
-        for (int e = 0; e < VH; ++e) S[e] = fmaf(tot, S[e], x[e]);
+            for (int e = 0; e < 16; ++e) S[c + e] = x[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) S[c + e] = fmaf(tot, S[c + e], x[e]);
+        }
     }
 }
 
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(~0u, ok); }
-
-struct Wait {
-    uint64_t *bar;
-    volatile int *abort;
-    unsigned *status;
-    __device__ __forceinline__ bool operator()(int i, int64_t n) const {
-        return mbar_wait(smem_u32(bar + i), uint32_t(n & 1), abort, status);
-    }
-};
 
 // A segment of one head: blockIdx.x = (b * H + h) * nseg + seg, chunks [n0, n1).
 struct Seg {
@@ -259,16 +290,19 @@ __device__ __forceinline__ void store_part(const float (&S)[VH], float *p, int d
 // KW, VW: Dk and Dv rounded up to 64 or 128; the columns past them are zeros (the copies fill
 // them) and the store clips them.
 // The S tile also takes the third part of l K, between the last read of S and the next state.
+enum { F_FULL0, F_FULL1, F_EMPTY0, F_EMPTY1, F_DEC0, F_DEC1, F_A, F_PV, F_P, F_K, F_U, F_S, F_OUT, F_END, F_AR, F_COUNT = F_AR + 4 };
+
 template <int KW, int VW>
 constexpr size_t fwd_smem() {
-    return 2 * size_t(2 * KW + VW) * 256 + size_t(KW) * 256 + 2 * sizeof(ChunkDecay) + sizeof(Ctl);
+    return 2 * size_t(2 * KW + VW) * 256 + size_t(KW) * 256 + 2 * sizeof(ChunkDecay) + sizeof(Ctl<F_COUNT>);
 }
 
 template <int KW, int VW>
 __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constant__ FwdMaps m, const LinArgs a, int nseg,
                                                             int cps, int parts, unsigned *status) {
     constexpr uint32_t STAGE = (2 * KW + VW) * 256, TILE_K = KW * 256, PANEL = TCH * 128, SPANEL = KW * 128;
-    constexpr int VH = VW / CG;         // state and output columns of a thread
+    constexpr int FG = 2 * CG;          // both sets of warps take part in every step, as four groups
+    constexpr int VH = VW / FG;         // state and output columns of a thread
     constexpr uint32_t T_A = 0, T_P = T_A, T_O2 = 384;
     // O1 and U take turns: the next chunk's O1 goes where U was, as soon as the state has it
     auto T_O1 = [](int64_t n) { return n & 1 ? 256u : 128u; };
@@ -276,14 +310,14 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t base = smem_u32(sm), S_AT = base + 2 * STAGE;
     ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + 2 * STAGE + TILE_K);
-    Ctl *ctl = reinterpret_cast<Ctl *>(dec + 2);
+    auto *ctl = reinterpret_cast<Ctl<F_COUNT> *>(dec + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Seg seg(a, nseg, cps);
     const int64_t N = seg.n1 - seg.n0;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < B_COUNT; ++i)
-            mbar_init(smem_u32(&ctl->bar[i]), i >= B_AR ? CG : i == B_P || i == B_K || i == B_S || i == B_OUT ? CW : 1);
+        for (int i = 0; i < F_COUNT; ++i)
+            mbar_init(smem_u32(&ctl->bar[i]), i >= F_AR ? FG : i == F_P || i == F_K || i == F_S || i == F_OUT ? 2 * SET : 1);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -300,8 +334,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             int64_t n = 0;
             for (; n < N; ++n) {
                 const int s = int(n & 1);
-                if (n >= 2 && !wait(B_EMPTY0 + s, (n >> 1) - 1)) break;
-                const uint32_t at = base + s * STAGE, b = bar(B_FULL0 + s);
+                if (n >= 2 && !wait(F_EMPTY0 + s, (n >> 1) - 1)) break;
+                const uint32_t at = base + s * STAGE, b = bar(F_FULL0 + s);
                 const int t = int((seg.n0 + n) * TCH);
                 mbar_arrive_expect_tx(b, STAGE);
                 for (int p = 0; p < KW / 64; ++p) load4(at + p * PANEL, &m.q, p * 64, int(seg.hk), t, int(seg.b), b);
@@ -310,7 +344,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             }
             // nothing of an abandoned walk is in flight when the block leaves
             int quiet = 0;
-            for (int64_t i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait(bar(B_FULL0 + int(i & 1)), uint32_t((i >> 1) & 1), &quiet, status);
+            for (int64_t i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait(bar(F_FULL0 + int(i & 1)), uint32_t((i >> 1) & 1), &quiet, status);
         }
         __syncwarp();
     } else if (warp == W_DEC) {
@@ -319,22 +353,22 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             const int s = int(n & 1);
             const float4 now = own;
             if (n + 1 < N) own = gates(a, seg, seg.n0 + n + 1);
-            if (n >= 2 && !all_ok(wait(B_EMPTY0 + s, (n >> 1) - 1))) break;
+            if (n >= 2 && !all_ok(wait(F_EMPTY0 + s, (n >> 1) - 1))) break;
             dec[s].fill(now);
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_DEC0 + s));
+            if (lane == 0) mbar_arrive(bar(F_DEC0 + s));
         }
     } else if (warp == W_OUT) {
         if (lane == 0) {
             // the outputs leave through V's tile, then the stage is free
             for (int64_t n = 0; n < N; ++n) {
                 const int s = int(n & 1);
-                if (!wait(B_OUT, n)) break;
+                if (!wait(F_OUT, n)) break;
                 for (int p = 0; p < VW / 64; ++p)
                     store4(&m.o, p * 64, int(seg.h), int((seg.n0 + n) * TCH), int(seg.b), base + s * STAGE + 2 * TILE_K + p * PANEL);
                 bulk_commit();
                 bulk_wait_read();
-                mbar_arrive(bar(B_EMPTY0 + s));
+                mbar_arrive(bar(F_EMPTY0 + s));
             }
             bulk_wait_all();
         }
@@ -346,30 +380,30 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             constexpr uint32_t WIDE = KW == 64 ? 0u : PANEL;
             for (int64_t n = 0; n < N; ++n) {
                 const uint32_t q = base + uint32_t(n & 1) * STAGE, k = q + TILE_K, v = k + TILE_K;
-                if (!(wait(B_FULL0 + int(n & 1), n >> 1) && wait(B_S, n))) break;
+                if (!(wait(F_FULL0 + int(n & 1), n >> 1) && wait(F_S, n))) break;
                 tc_fence_after();
                 product<VW, KW / 16, false, true>(tmem + T_O1(n), q, PANEL, S_AT, SPANEL, false);
                 // A goes where the last P was
-                if (n && !wait(B_PV, n - 1)) break;
+                if (n && !wait(F_PV, n - 1)) break;
                 tc_fence_after();
                 product<TCH, KW / 16, false, false>(tmem + T_A, q, PANEL, k, PANEL, false);
-                commit(bar(B_A));
-                // B_K, B_P: also every warp has read the last chunk's O1 and O2
-                if (!wait(B_K, n)) break;
+                commit(bar(F_A));
+                // F_K, F_P: also every warp has read the last chunk's O1 and O2
+                if (!wait(F_K, n)) break;
                 tc_fence_after();
                 product<VW, TCH / 16, true, true>(tmem + T_U(n), k, WIDE, v, PANEL, false);
                 product<VW, TCH / 16, true, true>(tmem + T_U(n), q, WIDE, v, PANEL, true);
                 if (parts == 3) product<VW, TCH / 16, true, true>(tmem + T_U(n), S_AT, WIDE, v, PANEL, true);
-                commit(bar(B_U));
-                if (!wait(B_P, n)) break;
+                commit(bar(F_U));
+                if (!wait(F_P, n)) break;
                 tc_fence_after();
                 product_ts<VW, TCH / 16>(tmem + T_O2, tmem + T_P, v, PANEL, false);
                 product_ts<VW, TCH / 16>(tmem + T_O2, tmem + T_P + 64, v, PANEL, true);
-                commit(bar(B_PV));
+                commit(bar(F_PV));
             }
             int quiet = 0;
-            commit(bar(B_END));
-            mbar_wait(bar(B_END), 0, &quiet, status);
+            commit(bar(F_END));
+            mbar_wait(bar(F_END), 0, &quiet, status);
         }
         __syncwarp();
     } else {
@@ -388,7 +422,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
                 for (int u = 0; u < VH; u += 8) put8(S_AT, SPANEL, i, (c0 + u) >> 3, S + u);
             }
             fence_proxy_async_smem();
-            arrive(B_S);
+            arrive(F_S);
         };
         put_state();
         for (int64_t n = 0; n < N; ++n) {
@@ -396,12 +430,12 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             const uint32_t Q = base + s * STAGE, K = Q + TILE_K, V = K + TILE_K;
             const ChunkDecay &d = dec[s];
             // l K: the products of Q, K and S are done, and their tiles take its three parts
-            if (!all_ok(wait(B_DEC0 + s, n >> 1) && wait(B_A, n))) break;
+            if (!all_ok(wait(F_DEC0 + s, n >> 1) && wait(F_A, n))) break;
             tc_fence_after();
-            if (parts == 3) scale_row(K, Q, S_AT, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG), d.to_end(i));
-            else scale_row2(K, Q, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG), d.to_end(i));
+            if (parts == 3) scale_row(K, Q, S_AT, PANEL, i, g * (KW / 8 / FG), (g + 1) * (KW / 8 / FG), d.to_end(i));
+            else scale_row2(K, Q, PANEL, i, g * (KW / 8 / FG), (g + 1) * (KW / 8 / FG), d.to_end(i));
             fence_proxy_async_smem();
-            arrive(B_K);
+            arrive(F_K);
             // P while U is formed: 8 g .. + 8 of every block of 32 columns, in place of A
             {
                 const float xi = d.x[i];
@@ -420,14 +454,12 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
                     const int j0 = 32 * c + 8 * g;
                     if (c < wq) {
                         ld8(lanes + T_A + j0, A);
-                        const float f = ri == d.re[c] ? fast_exp2((d.Ehi[wq] - d.Ehi[c]) + (d.Elo[wq] - d.Elo[c]) + xi) : 0.f;
+                        const float f =
+                            ri == d.re[c] ? a.scale * fast_exp2((d.Ehi[wq] - d.Ehi[c]) + (d.Elo[wq] - d.Elo[c]) + xi) : 0.f;
                         *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(d.wb + j0);
                         *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(d.wb + j0 + 4);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float x = w[e] * f;
-                            A[e] = x == 0.f ? 0.f : A[e] * x;
-                        }
+                        for (int e = 0; e < 8; ++e) A[e] *= w[e] * f;
                         split(c, A);
                     } else if (c == wq) {
                         ld8(lanes + T_A + j0, A);
@@ -437,7 +469,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const int r = int(((e < 4 ? rj.x : rj.y) >> (8 * (e & 3))) & 255u);
-                            A[e] = 8 * g + e <= lane && ri == r ? A[e] * fast_exp2(xi - w[e]) : 0.f;
+                            A[e] = 8 * g + e <= lane && ri == r ? A[e] * (a.scale * fast_exp2(xi - w[e])) : 0.f;
                         }
                         split(c, A);
                     } else {
@@ -446,9 +478,9 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
                     }
                 }
                 tc_fence_before();
-                arrive(B_AR + wq);
+                arrive(F_AR + wq);
                 // the warps of these lanes have read their columns
-                if (!all_ok(wait(B_AR + wq, n))) break;
+                if (!all_ok(wait(F_AR + wq, n))) break;
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -457,29 +489,29 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
                 }
                 st_wait();
                 tc_fence_before();
-                arrive(B_P);
+                arrive(F_P);
             }
-            if (!all_ok(wait(B_U, n))) break;
+            if (!all_ok(wait(F_U, n))) break;
             tc_fence_after();
             state_update<VH>(S, lanes + T_U(n) + c0, d.total);
             tc_fence_before();
             put_state();
             // the outputs, through V's tile
-            const float f = d.first(i);
-            if (!all_ok(wait(B_PV, n))) break;
+            const float f = d.first(i) * a.scale;
+            if (!all_ok(wait(F_PV, n))) break;
             tc_fence_after();
 #pragma unroll
             for (int u = 0; u < VH; u += 16) {
                 float x[16], y[16];
                 ld16x2(lanes + T_O1(n) + c0 + u, lanes + T_O2 + c0 + u, x, y);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = a.scale * (f == 0.f ? y[e] : fmaf(f, x[e], y[e]));
+                for (int e = 0; e < 16; ++e) y[e] = f == 0.f ? y[e] : fmaf(f, x[e], y[e]);
                 put8(V, PANEL, i, (c0 + u) >> 3, y);
                 put8(V, PANEL, i, ((c0 + u) >> 3) + 1, y + 8);
             }
             tc_fence_before();
             fence_proxy_async_smem();
-            arrive(B_OUT);
+            arrive(F_OUT);
         }
         if (a.s1 && nseg == 1) store_part<VH>(S, a.s1 + seg.bh * dd, i, c0, a);
     }
@@ -494,20 +526,29 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
 // ---------------------------------------------------------------- segment states
 // The state that a segment's own tokens leave (zero before it): S[blockIdx.x], and the decay
 // over it.  REV: the adjoint state from q and scale go, walked from the last chunk back.
+//
+// A ring of three stages of half a chunk (64 tokens).  One set of warps multiplies x by its decays
+// to the chunk's end (two more tiles of a stage take the second and third part), the products of a
+// chunk's two halves add up in one of two accumulators, and the other set of warps folds them
+// into the state; only the state's own multiply-add is a chain.
+constexpr int SH = TCH / 2, RING = 3;
+enum { S_FULL, S_EMPTY = S_FULL + RING, S_K = S_EMPTY + RING, S_DEC = S_K + RING, S_DFREE = S_DEC + 2, S_U = S_DFREE + 2,
+       S_UFREE = S_U + 2, S_END = S_UFREE + 2, S_COUNT };
+
 template <int KW, int VW>
 constexpr size_t state_smem() {
-    return 2 * size_t(KW + VW) * 256 + 2 * size_t(KW) * 256 + 2 * sizeof(ChunkDecay) + sizeof(Ctl);
+    return RING * size_t(3 * KW + VW) * SH * 2 + 2 * sizeof(ChunkDecay) + sizeof(Ctl<S_COUNT>);
 }
 
 template <int KW, int VW, bool REV>
 __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_constant__ StateMaps m, const LinArgs a, int nseg,
                                                               int cps, unsigned *status) {
-    constexpr uint32_t STAGE = (KW + VW) * 256, TILE_K = KW * 256, PANEL = TCH * 128;
+    constexpr uint32_t TILE_K = KW * SH * 2, TILE_V = VW * SH * 2, STAGE = 3 * TILE_K + TILE_V, PANEL = SH * 128;
     constexpr int VH = VW / CG;
     extern __shared__ __align__(1024) uint8_t sm[];
-    const uint32_t base = smem_u32(sm), L1 = base + 2 * STAGE, L2 = L1 + TILE_K;
-    ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + 2 * STAGE + 2 * TILE_K);
-    Ctl *ctl = reinterpret_cast<Ctl *>(dec + 2);
+    const uint32_t base = smem_u32(sm);
+    ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + RING * STAGE);
+    auto *ctl = reinterpret_cast<Ctl<S_COUNT> *>(dec + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Seg seg(a, nseg, cps);
     const int64_t N = seg.n1 - seg.n0;
@@ -516,7 +557,10 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
     if (seg.seg == (REV ? 0 : nseg - 1) && !(REV ? a.ds0 : a.s1)) return;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(smem_u32(&ctl->bar[i]), i == B_K || i == B_EMPTY0 || i == B_EMPTY1 ? CW : 1);
+        for (int i = 0; i < S_COUNT; ++i)
+            mbar_init(smem_u32(&ctl->bar[i]), (i >= S_K && i < S_DEC) || (i >= S_UFREE && i < S_END) ? SET
+                                              : i >= S_DFREE && i < S_U                              ? 2 * SET
+                                                                                                     : 1);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -527,83 +571,106 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
     const uint32_t tmem = ctl->tmem;
     const Wait wait{ctl->bar, &ctl->abort, status};
     auto bar = [&](int i) { return smem_u32(&ctl->bar[i]); };
+    auto arrive = [&](int b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(b));
+    };
 
     if (warp == W_TMA) {
         if (lane == 0) {
-            int64_t n = 0;
-            for (; n < N; ++n) {
-                const int s = int(n & 1);
-                if (n >= 2 && !wait(B_EMPTY0 + s, (n >> 1) - 1)) break;
-                const uint32_t at = base + s * STAGE, b = bar(B_FULL0 + s);
-                const int t = int(chunk(n) * TCH);
-                mbar_arrive_expect_tx(b, STAGE);
+            int64_t h = 0, turn = 0;    // halves loaded; the ring's turn
+            int s = 0;
+            for (; h < 2 * N; ++h) {
+                if (turn && !wait(S_EMPTY + s, turn - 1)) break;
+                const uint32_t at = base + s * STAGE, b = bar(S_FULL + s);
+                const int t = int(chunk(h >> 1) * TCH + (h & 1) * SH);
+                mbar_arrive_expect_tx(b, TILE_K + TILE_V);
                 for (int p = 0; p < KW / 64; ++p) load4(at + p * PANEL, &m.x, p * 64, int(seg.hk), t, int(seg.b), b);
-                for (int p = 0; p < VW / 64; ++p) load4(at + TILE_K + p * PANEL, &m.y, p * 64, int(seg.h), t, int(seg.b), b);
+                for (int p = 0; p < VW / 64; ++p) load4(at + 3 * TILE_K + p * PANEL, &m.y, p * 64, int(seg.h), t, int(seg.b), b);
+                if (++s == RING) { s = 0; ++turn; }
             }
+            // nothing of an abandoned walk is in flight when the block leaves
             int quiet = 0;
-            for (int64_t i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait(bar(B_FULL0 + int(i & 1)), uint32_t((i >> 1) & 1), &quiet, status);
+            for (int64_t i = h > RING ? h - RING : 0; i < h; ++i)
+                mbar_wait(bar(S_FULL + int(i % RING)), uint32_t((i / RING) & 1), &quiet, status);
         }
         __syncwarp();
     } else if (warp == W_DEC) {
-        double sum = 0.0;
+        Sum2 sum{0.f, 0.f};
         int cuts = 0;
         float4 own = gates(a, seg, chunk(0));
         for (int64_t n = 0; n < N; ++n) {
             const int s = int(n & 1);
             const float4 now = own;
             if (n + 1 < N) own = gates(a, seg, chunk(n + 1));
-            if (n >= 2 && !all_ok(wait(B_EMPTY0 + s, (n >> 1) - 1))) break;
-            sum += dec[s].fill(now);
+            if (n >= 2 && !all_ok(wait(S_DFREE + s, (n >> 1) - 1))) break;
+            sum = sum + dec[s].fill(now);
             __syncwarp();
             cuts += dec[s].n_cut;
-            if (lane == 0) mbar_arrive(bar(B_DEC0 + s));
+            if (lane == 0) mbar_arrive(bar(S_DEC + s));
         }
-        if (lane == 0) a.tot[blockIdx.x] = cuts ? 0.f : fast_exp2(float(sum));
+        if (lane == 0) a.tot[blockIdx.x] = cuts ? 0.f : fast_exp2(sum.value());
     } else if (warp == W_MMA) {
         if (lane == 0) {
-            for (int64_t n = 0; n < N; ++n) {
-                const int s = int(n & 1);
-                // B_K: the operands are there, and (n > 0) every warp has read the last product
-                if (!(wait(B_FULL0 + s, n >> 1) && wait(B_K, n))) break;
+            constexpr uint32_t WIDE = KW == 64 ? 0u : PANEL;
+            int64_t turn = 0;
+            int s = 0;
+            for (int64_t h = 0; h < 2 * N; ++h) {
+                const int64_t n = h >> 1;
+                const int u = int(n & 1);
+                if (!wait(S_FULL + s, turn) || !wait(S_K + s, turn)) break;
+                if (!(h & 1) && n >= 2 && !wait(S_UFREE + u, (n >> 1) - 1)) break;
                 tc_fence_after();
-                const uint32_t at = base + s * STAGE, wide = KW == 64 ? 0u : PANEL;
-                product<VW, TCH / 16, true, true>(tmem, at, wide, at + TILE_K, PANEL, false);
-                product<VW, TCH / 16, true, true>(tmem, L1, wide, at + TILE_K, PANEL, true);
-                product<VW, TCH / 16, true, true>(tmem, L2, wide, at + TILE_K, PANEL, true);
-                commit(bar(B_U));
+                const uint32_t at = base + s * STAGE, y = at + 3 * TILE_K, d = tmem + u * 128;
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+                    product<VW, SH / 16, true, true>(d, at + p * TILE_K, WIDE, y, PANEL, p || (h & 1));
+                commit(bar(S_EMPTY + s));
+                if (h & 1) commit(bar(S_U + u));
+                if (++s == RING) { s = 0; ++turn; }
             }
             int quiet = 0;
-            commit(bar(B_END));
-            mbar_wait(bar(B_END), 0, &quiet, status);
+            commit(bar(S_END));
+            mbar_wait(bar(S_END), 0, &quiet, status);
         }
         __syncwarp();
-    } else if (warp < CW) {
-        const int wq = warp & 3, g = warp >> 2, i = wq * 32 + lane, c0 = g * VH;
+    } else if (warp < SET) {
+        // x times its decays: row r of the half, a quarter of the units
+        constexpr int UQ = KW / 8 / 4;
+        const int r = threadIdx.x & 63, q = threadIdx.x >> 6;
+        int64_t turn = 0;
+        int s = 0;
+        for (int64_t h = 0; h < 2 * N; ++h) {
+            const int64_t n = h >> 1;
+            const int e = int(n & 1);
+            if (!all_ok(wait(S_DEC + e, n >> 1) && wait(S_FULL + s, turn))) break;
+            const int i = int(h & 1) * SH + r;
+            const uint32_t at = base + s * STAGE;
+            scale_row(at, at + TILE_K, at + 2 * TILE_K, PANEL, r, q * UQ, (q + 1) * UQ,
+                      REV ? dec[e].first(i) * a.scale : dec[e].to_end(i));
+            fence_proxy_async_smem();
+            arrive(S_K + s);
+            if (h & 1) arrive(S_DFREE + e);
+            if (++s == RING) { s = 0; ++turn; }
+        }
+    } else if (warp < 2 * SET) {
+        const int wq = warp & 3, g = (warp >> 2) % CG, i = wq * 32 + lane, c0 = g * VH;
         const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
-        auto arrive = [&](int b) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(b));
-        };
         float S[VH];
 #pragma unroll
         for (int u = 0; u < VH; ++u) S[u] = 0.f;
         for (int64_t n = 0; n < N; ++n) {
-            const int s = int(n & 1);
-            const ChunkDecay &d = dec[s];
-            if (!all_ok(wait(B_FULL0 + s, n >> 1) && wait(B_DEC0 + s, n >> 1))) break;
-            scale_row(base + s * STAGE, L1, L2, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG),
-                      REV ? d.first(i) * a.scale : d.to_end(i));
-            fence_proxy_async_smem();
-            arrive(B_K);
-            const float tot = d.total;
-            if (!all_ok(wait(B_U, n))) break;
+            const int u = int(n & 1);
+            if (!all_ok(wait(S_DEC + u, n >> 1))) break;
+            const float tot = dec[u].total;
+            arrive(S_DFREE + u);
+            if (!all_ok(wait(S_U + u, n >> 1))) break;
             tc_fence_after();
-            state_update<VH>(S, lanes + c0, tot);
+            state_update<VH>(S, lanes + u * 128 + c0, tot);
             tc_fence_before();
-            arrive(B_EMPTY0 + s);       // done with the stage, its decays and the accumulator
+            arrive(S_UFREE + u);
         }
-        float *out = (REV ? a.dS : a.S) + int64_t(blockIdx.x) * a.Dk * a.Dv;
-        store_part<VH>(S, out, i, c0, a);
+        store_part<VH>(S, (REV ? a.dS : a.S) + int64_t(blockIdx.x) * a.Dk * a.Dv, i, c0, a);
     }
     tc_fence_before();
     __syncthreads();
@@ -622,8 +689,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
 template <int KW, int VW, bool REV>
 cudaError_t run_states(const LinArgs &a, const LinSplit &sp, unsigned *status, cudaStream_t st) {
     StateMaps m;
-    const bool ok = REV ? map_tokens(&m.x, a.q, a.Dk, a.Hk, a.T, a.B, a.ldq) && map_tokens(&m.y, a.go, a.Dv, a.H, a.T, a.B, a.ldo)
-                        : map_tokens(&m.x, a.k, a.Dk, a.Hk, a.T, a.B, a.ldk) && map_tokens(&m.y, a.v, a.Dv, a.H, a.T, a.B, a.ldv);
+    const bool ok = REV ? map_tokens(&m.x, a.q, a.Dk, a.Hk, a.T, a.B, a.ldq, SH) && map_tokens(&m.y, a.go, a.Dv, a.H, a.T, a.B, a.ldo, SH)
+                        : map_tokens(&m.x, a.k, a.Dk, a.Hk, a.T, a.B, a.ldk, SH) && map_tokens(&m.y, a.v, a.Dv, a.H, a.T, a.B, a.ldv, SH);
     if (!ok) return cudaErrorInvalidValue;
     constexpr size_t smem = state_smem<KW, VW>();
     LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_state<KW, VW, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));

@@ -124,6 +124,11 @@ __device__ __forceinline__ void st4(uint32_t t, uint32_t a, uint32_t b, uint32_t
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(t), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
 }
+__device__ __forceinline__ void st8(uint32_t t, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void alloc512(uint32_t *slot) {
@@ -169,13 +174,14 @@ __device__ __forceinline__ void sts(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// [B, T, heads, D] bf16 with token pitch ld: boxes of 64 values x 1 head x 128 tokens
-inline bool map_tokens(CUtensorMap *m, const void *p, int64_t D, int64_t heads, int64_t T, int64_t B, int64_t ld) {
+// [B, T, heads, D] bf16 with token pitch ld: boxes of 64 values x 1 head x `rows` tokens
+inline bool map_tokens(CUtensorMap *m, const void *p, int64_t D, int64_t heads, int64_t T, int64_t B, int64_t ld,
+                       int rows = 128) {
     auto enc = tmap_encoder();
     if (!enc) return false;
     const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(T), cuuint64_t(B)};
     const cuuint64_t strides[3] = {cuuint64_t(D) * 2, cuuint64_t(ld) * 2, cuuint64_t(T * ld) * 2};
-    const cuuint32_t box[4] = {64, 1, 128, 1}, one[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, 1, cuuint32_t(rows), 1}, one[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, one,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
