@@ -26,12 +26,13 @@ namespace {
 using namespace tc5;
 
 constexpr int TCH = 128;                // tokens of a chunk
-// Warps of a block.  Two sets of eight computing warps (two groups of four; a group covers the 128
-// lanes of tensor memory, a warp the lanes of its number modulo four), and one warp each that
-// issues products, copies in, copies out, and prepares the decays.
-constexpr int CG = 2, SET = 4 * CG;
-constexpr int W_MMA = 2 * SET, W_TMA = W_MMA + 1, W_DEC = W_MMA + 2, W_OUT = W_MMA + 3;
-constexpr int TC_BLOCK = (W_OUT + 1) * 32;
+// Warps of a block: sixteen computing warps (four groups of four; a group covers the 128 lanes
+// of tensor memory, a warp the lanes of its number modulo four), and one warp each that issues
+// products, copies in, and prepares the decays and copies out.  19 warps leave 104 registers a
+// thread; at 96 the state and the weights in flight spill, and the spills cost a fifth.
+constexpr int CG = 4, CW = 4 * CG;
+constexpr int W_MMA = CW, W_TMA = CW + 1, W_AUX = CW + 2;
+constexpr int TC_BLOCK = (CW + 3) * 32;
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -183,11 +184,11 @@ __device__ __forceinline__ void scale_row(uint32_t t0, uint32_t t1, uint32_t t2,
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float a = lo_f(in[i]) * w, b = hi_f(in[i]) * w;
-            h[i] = pack(a, b);
-            a -= lo_f(h[i]);
-            b -= hi_f(h[i]);
-            l[i] = pack(a, b);
-            ll[i] = pack(a - lo_f(l[i]), b - hi_f(l[i]));
+            h[i] = pack_top(a, b);
+            a -= top(a);
+            b -= top(b);
+            l[i] = pack_top(a, b);
+            ll[i] = pack_top(a - top(a), b - top(b));
         }
         sts(t0 + at, make_uint4(h[0], h[1], h[2], h[3]));
         sts(t1 + at, make_uint4(l[0], l[1], l[2], l[3]));
@@ -301,8 +302,7 @@ template <int KW, int VW>
 __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constant__ FwdMaps m, const LinArgs a, int nseg,
                                                             int cps, int parts, unsigned *status) {
     constexpr uint32_t STAGE = (2 * KW + VW) * 256, TILE_K = KW * 256, PANEL = TCH * 128, SPANEL = KW * 128;
-    constexpr int FG = 2 * CG;          // both sets of warps take part in every step, as four groups
-    constexpr int VH = VW / FG;         // state and output columns of a thread
+    constexpr int VH = VW / CG;         // state and output columns of a thread
     constexpr uint32_t T_A = 0, T_P = T_A, T_O2 = 384;
     // O1 and U take turns: the next chunk's O1 goes where U was, as soon as the state has it
     auto T_O1 = [](int64_t n) { return n & 1 ? 256u : 128u; };
@@ -317,7 +317,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < F_COUNT; ++i)
-            mbar_init(smem_u32(&ctl->bar[i]), i >= F_AR ? FG : i == F_P || i == F_K || i == F_S || i == F_OUT ? 2 * SET : 1);
+            mbar_init(smem_u32(&ctl->bar[i]), i >= F_AR ? CG : i == F_P || i == F_K || i == F_S || i == F_OUT ? CW : 1);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -347,31 +347,34 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             for (int64_t i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait(bar(F_FULL0 + int(i & 1)), uint32_t((i >> 1) & 1), &quiet, status);
         }
         __syncwarp();
-    } else if (warp == W_DEC) {
+    } else if (warp == W_AUX) {
+        // decays a chunk ahead; the outputs leave through V's tile, then the stage is free
         float4 own = gates(a, seg, seg.n0);
-        for (int64_t n = 0; n < N; ++n) {
+        bool ok = true;
+        auto out = [&](int64_t n) {
             const int s = int(n & 1);
-            const float4 now = own;
-            if (n + 1 < N) own = gates(a, seg, seg.n0 + n + 1);
-            if (n >= 2 && !all_ok(wait(F_EMPTY0 + s, (n >> 1) - 1))) break;
-            dec[s].fill(now);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(F_DEC0 + s));
-        }
-    } else if (warp == W_OUT) {
-        if (lane == 0) {
-            // the outputs leave through V's tile, then the stage is free
-            for (int64_t n = 0; n < N; ++n) {
-                const int s = int(n & 1);
-                if (!wait(F_OUT, n)) break;
+            if (!all_ok(wait(F_OUT, n))) return false;
+            if (lane == 0) {
                 for (int p = 0; p < VW / 64; ++p)
                     store4(&m.o, p * 64, int(seg.h), int((seg.n0 + n) * TCH), int(seg.b), base + s * STAGE + 2 * TILE_K + p * PANEL);
                 bulk_commit();
                 bulk_wait_read();
                 mbar_arrive(bar(F_EMPTY0 + s));
             }
-            bulk_wait_all();
+            __syncwarp();
+            return true;
+        };
+        for (int64_t n = 0; ok && n < N; ++n) {
+            const int s = int(n & 1);
+            const float4 now = own;
+            if (n + 1 < N) own = gates(a, seg, seg.n0 + n + 1);
+            if (n >= 2 && !(ok = out(n - 2))) break;
+            dec[s].fill(now);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(F_DEC0 + s));
         }
+        for (int64_t n = N > 2 ? N - 2 : 0; ok && n < N; ++n) ok = out(n);
+        if (lane == 0) bulk_wait_all();
         __syncwarp();
     } else if (warp == W_MMA) {
         if (lane == 0) {
@@ -432,8 +435,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             // l K: the products of Q, K and S are done, and their tiles take its three parts
             if (!all_ok(wait(F_DEC0 + s, n >> 1) && wait(F_A, n))) break;
             tc_fence_after();
-            if (parts == 3) scale_row(K, Q, S_AT, PANEL, i, g * (KW / 8 / FG), (g + 1) * (KW / 8 / FG), d.to_end(i));
-            else scale_row2(K, Q, PANEL, i, g * (KW / 8 / FG), (g + 1) * (KW / 8 / FG), d.to_end(i));
+            if (parts == 3) scale_row(K, Q, S_AT, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG), d.to_end(i));
+            else scale_row2(K, Q, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG), d.to_end(i));
             fence_proxy_async_smem();
             arrive(F_K);
             // P while U is formed: 8 g .. + 8 of every block of 32 columns, in place of A
@@ -444,8 +447,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
                 auto split = [&](int c, const float (&p)[8]) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        h[c][e] = pack(p[2 * e], p[2 * e + 1]);
-                        l[c][e] = pack(p[2 * e] - lo_f(h[c][e]), p[2 * e + 1] - hi_f(h[c][e]));
+                        h[c][e] = pack_top(p[2 * e], p[2 * e + 1]);
+                        l[c][e] = pack_top(p[2 * e] - top(p[2 * e]), p[2 * e + 1] - top(p[2 * e + 1]));
                     }
                 };
 #pragma unroll
@@ -527,10 +530,10 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
 // The state that a segment's own tokens leave (zero before it): S[blockIdx.x], and the decay
 // over it.  REV: the adjoint state from q and scale go, walked from the last chunk back.
 //
-// A ring of three stages of half a chunk (64 tokens).  One set of warps multiplies x by its decays
-// to the chunk's end (two more tiles of a stage take the second and third part), the products of a
-// chunk's two halves add up in one of two accumulators, and the other set of warps folds them
-// into the state; only the state's own multiply-add is a chain.
+// A ring of three stages of half a chunk (64 tokens).  The warps multiply x by its decays to the
+// chunk's end (two more tiles of a stage take the second and third part), the products of a
+// chunk's two halves add up in one of two accumulators, and the warps fold the chunk before into
+// the state meanwhile; only the state's own multiply-add is a chain.
 constexpr int SH = TCH / 2, RING = 3;
 enum { S_FULL, S_EMPTY = S_FULL + RING, S_K = S_EMPTY + RING, S_DEC = S_K + RING, S_DFREE = S_DEC + 2, S_U = S_DFREE + 2,
        S_UFREE = S_U + 2, S_END = S_UFREE + 2, S_COUNT };
@@ -558,9 +561,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S_COUNT; ++i)
-            mbar_init(smem_u32(&ctl->bar[i]), (i >= S_K && i < S_DEC) || (i >= S_UFREE && i < S_END) ? SET
-                                              : i >= S_DFREE && i < S_U                              ? 2 * SET
-                                                                                                     : 1);
+            mbar_init(smem_u32(&ctl->bar[i]), (i >= S_K && i < S_DEC) || (i >= S_DFREE && i < S_U) || (i >= S_UFREE && i < S_END) ? CW : 1);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -595,7 +596,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
                 mbar_wait(bar(S_FULL + int(i % RING)), uint32_t((i / RING) & 1), &quiet, status);
         }
         __syncwarp();
-    } else if (warp == W_DEC) {
+    } else if (warp == W_AUX) {
         Sum2 sum{0.f, 0.f};
         int cuts = 0;
         float4 own = gates(a, seg, chunk(0));
@@ -634,42 +635,48 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
             mbar_wait(bar(S_END), 0, &quiet, status);
         }
         __syncwarp();
-    } else if (warp < SET) {
-        // x times its decays: row r of the half, a quarter of the units
-        constexpr int UQ = KW / 8 / 4;
+    } else {
+        // x times its decays: row r of the half, an eighth of the units
+        constexpr int UQ = KW / 8 / 8;
         const int r = threadIdx.x & 63, q = threadIdx.x >> 6;
-        int64_t turn = 0;
-        int s = 0;
-        for (int64_t h = 0; h < 2 * N; ++h) {
-            const int64_t n = h >> 1;
-            const int e = int(n & 1);
-            if (!all_ok(wait(S_DEC + e, n >> 1) && wait(S_FULL + s, turn))) break;
-            const int i = int(h & 1) * SH + r;
-            const uint32_t at = base + s * STAGE;
-            scale_row(at, at + TILE_K, at + 2 * TILE_K, PANEL, r, q * UQ, (q + 1) * UQ,
-                      REV ? dec[e].first(i) * a.scale : dec[e].to_end(i));
-            fence_proxy_async_smem();
-            arrive(S_K + s);
-            if (h & 1) arrive(S_DFREE + e);
-            if (++s == RING) { s = 0; ++turn; }
-        }
-    } else if (warp < 2 * SET) {
-        const int wq = warp & 3, g = (warp >> 2) % CG, i = wq * 32 + lane, c0 = g * VH;
+        const int wq = warp & 3, g = warp >> 2, i = wq * 32 + lane, c0 = g * VH;
         const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
         float S[VH];
 #pragma unroll
         for (int u = 0; u < VH; ++u) S[u] = 0.f;
-        for (int64_t n = 0; n < N; ++n) {
+        auto fold = [&](int64_t n, float tot) {
             const int u = int(n & 1);
-            if (!all_ok(wait(S_DEC + u, n >> 1))) break;
-            const float tot = dec[u].total;
-            arrive(S_DFREE + u);
-            if (!all_ok(wait(S_U + u, n >> 1))) break;
+            if (!all_ok(wait(S_U + u, n >> 1))) return false;
             tc_fence_after();
             state_update<VH>(S, lanes + u * 128 + c0, tot);
             tc_fence_before();
             arrive(S_UFREE + u);
+            return true;
+        };
+        bool ok = true;
+        float tot = 0.f;
+        int64_t turn = 0;
+        int s = 0;
+        for (int64_t n = 0; ok && n < N; ++n) {
+            const int e = int(n & 1);
+            if (!(ok = all_ok(wait(S_DEC + e, n >> 1)))) break;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                if (!(ok = all_ok(wait(S_FULL + s, turn)))) break;
+                const uint32_t at = base + s * STAGE;
+                scale_row(at, at + TILE_K, at + 2 * TILE_K, PANEL, r, q * UQ, (q + 1) * UQ,
+                          REV ? dec[e].first(h * SH + r) * a.scale : dec[e].to_end(h * SH + r));
+                fence_proxy_async_smem();
+                arrive(S_K + s);
+                if (++s == RING) { s = 0; ++turn; }
+            }
+            const float now = dec[e].total;
+            if (!ok) break;
+            arrive(S_DFREE + e);
+            if (n && !(ok = fold(n - 1, tot))) break;
+            tot = now;
         }
+        if (ok) fold(N - 1, tot);
         store_part<VH>(S, (REV ? a.dS : a.S) + int64_t(blockIdx.x) * a.Dk * a.Dv, i, c0, a);
     }
     tc_fence_before();

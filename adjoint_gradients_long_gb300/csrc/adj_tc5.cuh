@@ -163,6 +163,13 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&v);
 }
+// the upper 16 bits of two values: bf16 by truncation, in one instruction where the rounding
+// conversion takes four issue slots.  For the parts of a sum, whose remainder the next part takes
+// up, it serves as well.
+__device__ __forceinline__ uint32_t pack_top(float a, float b) {
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float top(float a) { return __uint_as_float(__float_as_uint(a) & 0xFFFF0000u); }
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ uint4 lds(uint32_t a) {
