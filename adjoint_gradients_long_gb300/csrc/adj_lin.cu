@@ -46,7 +46,6 @@ __device__ __forceinline__ void ld4(const __nv_bfloat16 *p, float (&v)[4]) {
     v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
 }
 __device__ __forceinline__ void st1(float *p, float x) { *p = x; }
-__device__ __forceinline__ void st1(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
 // tile[t][d] = mul * x[t * ld + d] for t < LC, d < D; rows past len are zeros
 template <class T>
@@ -525,24 +524,21 @@ cudaError_t fwd(const LinArgs &a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+cudaError_t bwd_f32(const LinArgs &a, cudaStream_t st) {
+    LIN_CUDA((states<float, false>(a, st)));
+    LIN_CUDA((states<float, true>(a, st)));
+    ProfScope ps(K_LIN_GRAD, st);
+    LIN_CUDA(big_smem(k_lin_grad<float>, SM_GRAD));
+    k_lin_grad<float><<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, SM_GRAD, st>>>(a);
+    return cudaGetLastError();
+}
+
 template <class T>
-cudaError_t bwd(const LinArgs &a, cudaStream_t st) {
-    LIN_CUDA((states<T, false>(a, st)));
-    LIN_CUDA((states<T, true>(a, st)));
-    if (a.NC == 0) return cudaSuccess;
-    {
-        ProfScope ps(K_LIN_GRAD, st);
-        LIN_CUDA(big_smem(k_lin_grad<T>, SM_GRAD));
-        k_lin_grad<T><<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, SM_GRAD, st>>>(a);
-        LIN_CUDA(cudaGetLastError());
-    }
-    if (a.pq) {
-        ProfScope ps(K_LIN_SHARE, st);
-        const int64_t n = cdiv(a.B * a.T * a.Hk * (a.Dk / 4), 256);
-        k_lin_share<T><<<unsigned(std::min<int64_t>(n, 152 * 16)), 256, 0, st>>>(a);
-        LIN_CUDA(cudaGetLastError());
-    }
-    return cudaSuccess;
+cudaError_t share(const LinArgs &a, cudaStream_t st) {
+    ProfScope ps(K_LIN_SHARE, st);
+    const int64_t n = cdiv(a.B * a.T * a.Hk * (a.Dk / 4), 256);
+    k_lin_share<T><<<unsigned(std::min<int64_t>(n, 152 * 16)), 256, 0, st>>>(a);
+    return cudaGetLastError();
 }
 
 inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -562,20 +558,30 @@ cudaError_t launch_lin_scan(const LinArgs &a, int64_t n, bool rev, cudaStream_t 
 static size_t carve(LinArgs &a, bool bwd, bool bf16, char *base) {
     size_t off = 0;
     auto take = [&](size_t bytes) {
-        float *p = base ? reinterpret_cast<float *>(base + off) : nullptr;
+        char *p = base ? base + off : nullptr;
         off += al256(bytes);
         return p;
     };
-    const int64_t n = bf16 && !bwd ? lin_split(a).nseg : a.NC;
-    const size_t st = size_t(a.B * a.H) * n * a.Dk * a.Dv * 4;
-    a.S = take(st);
-    a.tot = take(size_t(a.B * a.H) * n * 4);
+    auto floats = [&](size_t n) { return reinterpret_cast<float *>(take(n * 4)); };
+    auto halves = [&](size_t n) { return reinterpret_cast<__nv_bfloat16 *>(take(n * 2)); };
+    const int64_t heads = a.B * a.H, n = heads * (bf16 ? lin_split(a).nseg : a.NC);
+    const size_t dd = size_t(a.Dk) * a.Dv;
+    a.S = floats(n * dd);
+    a.tot = floats(n);
     a.dS = a.pq = a.pk = nullptr;
+    a.shi = a.slo = a.zhi = a.zlo = nullptr;
     if (bwd) {
-        a.dS = take(st);
+        a.dS = floats(n * dd);
+        if (bf16) {
+            const size_t all = size_t(heads) * cdiv(a.T, 128) * dd;
+            a.shi = halves(all);
+            a.slo = halves(all);
+            a.zhi = halves(all);
+            a.zlo = halves(all);
+        }
         if (a.Hk < a.H) {
-            a.pq = take(size_t(a.B * a.T) * a.H * a.Dk * 4);
-            a.pk = take(size_t(a.B * a.T) * a.H * a.Dk * 4);
+            a.pq = floats(size_t(a.B * a.T) * a.H * a.Dk);
+            a.pk = floats(size_t(a.B * a.T) * a.H * a.Dk);
         }
     }
     return off;
@@ -591,8 +597,11 @@ cudaError_t launch_lin_fwd(const LinArgs &a, bool bf16, unsigned *status, cudaSt
     if (a.NC == 0) return launch_lin_scan(a, 0, false, st);      // s1 = s0
     return bf16 ? launch_lin_tc_fwd(a, status, st) : fwd<float>(a, st);
 }
-cudaError_t launch_lin_bwd(const LinArgs &a, bool bf16, unsigned *, cudaStream_t st) {
-    return bf16 ? bwd<__nv_bfloat16>(a, st) : bwd<float>(a, st);
+cudaError_t launch_lin_bwd(const LinArgs &a, bool bf16, unsigned *status, cudaStream_t st) {
+    if (a.NC == 0) return launch_lin_scan(a, 0, true, st);       // ds0 = ds1
+    LIN_CUDA(bf16 ? launch_lin_tc_bwd(a, status, st) : bwd_f32(a, st));
+    if (!a.pq) return cudaSuccess;
+    return bf16 ? share<__nv_bfloat16>(a, st) : share<float>(a, st);
 }
 cudaError_t launch_lin_step(const LinArgs &a, bool bf16, float *state, int64_t n_slots, const int32_t *slots,
                             cudaStream_t st) {

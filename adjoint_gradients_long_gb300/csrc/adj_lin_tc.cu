@@ -86,7 +86,8 @@ struct alignas(16) ChunkDecay {
                            t + 2 < len ? __ldg(g + (t + 2) * pitch) : 0.f, t + 3 < len ? __ldg(g + (t + 3) * pitch) : 0.f);
     }
     // ... and their decays; the chunk's sum of logarithms is returned
-    __device__ Sum2 fill(float4 own) {
+    // wa (may be null): 2^(G_t - E_{b-1}), from the block before to t, zero across a new start
+    __device__ Sum2 fill(float4 own, float *wa = nullptr) {
         const int lane = threadIdx.x & 31;
         const float v[4] = {own.x, own.y, own.z, own.w};
         Sum2 s[4], sum{0.f, 0.f};
@@ -127,6 +128,18 @@ struct alignas(16) ChunkDecay {
         reinterpret_cast<float4 *>(x)[lane] = make_float4(xs[0], xs[1], xs[2], xs[3]);
         reinterpret_cast<float4 *>(wb)[lane] = make_float4(ws[0], ws[1], ws[2], ws[3]);
         reinterpret_cast<uint32_t *>(r)[lane] = rs;
+        if (wa) {
+            Sum2 P = run.from((lane & 24) - 1);
+            int rp = __shfl_sync(~0u, rc, (lane & 24) - 1);
+            if (lane < 8) {
+                P = Sum2{0.f, 0.f};
+                rp = 0;
+            }
+            float w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) w[u] = cb + c[u] == rp ? fast_exp2(((before + s[u]) - P).value()) : 0.f;
+            reinterpret_cast<float4 *>(wa)[lane] = make_float4(w[0], w[1], w[2], w[3]);
+        }
         if ((lane & 7) == 7) {
             const int b = lane >> 3;
             Ehi[b] = E.hi;
@@ -409,7 +422,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             mbar_wait(bar(F_END), 0, &quiet, status);
         }
         __syncwarp();
-    } else {
+    } else if (warp < CW) {
         const int wq = warp & 3, g = warp >> 2, i = wq * 32 + lane, c0 = g * VH;
         const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
         auto arrive = [&](int b) {
@@ -543,7 +556,10 @@ constexpr size_t state_smem() {
     return RING * size_t(3 * KW + VW) * SH * 2 + 2 * sizeof(ChunkDecay) + sizeof(Ctl<S_COUNT>);
 }
 
-template <int KW, int VW, bool REV>
+// KEEP: the walk starts from the state that enters the segment (a.S / a.dS, or s0 / ds1 when the
+// segment is the whole head), and the state met before every chunk is kept as a sum of two bf16
+// (keep_hi, keep_lo [B,H,NC,Dk,Dv]), the operand of the backward pass.
+template <int KW, int VW, bool REV, bool KEEP>
 __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_constant__ StateMaps m, const LinArgs a, int nseg,
                                                               int cps, unsigned *status) {
     constexpr uint32_t TILE_K = KW * SH * 2, TILE_V = VW * SH * 2, STAGE = 3 * TILE_K + TILE_V, PANEL = SH * 128;
@@ -557,7 +573,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
     const int64_t N = seg.n1 - seg.n0;
     auto chunk = [&](int64_t n) { return REV ? seg.n1 - 1 - n : seg.n0 + n; };
     // no segment reads what the last one leaves: only the final state does
-    if (seg.seg == (REV ? 0 : nseg - 1) && !(REV ? a.ds0 : a.s1)) return;
+    if (!KEEP && seg.seg == (REV ? 0 : nseg - 1) && !(REV ? a.ds0 : a.s1)) return;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S_COUNT; ++i)
@@ -610,7 +626,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
             cuts += dec[s].n_cut;
             if (lane == 0) mbar_arrive(bar(S_DEC + s));
         }
-        if (lane == 0) a.tot[blockIdx.x] = cuts ? 0.f : fast_exp2(sum.value());
+        if (!KEEP && lane == 0) a.tot[blockIdx.x] = cuts ? 0.f : fast_exp2(sum.value());
     } else if (warp == W_MMA) {
         if (lane == 0) {
             constexpr uint32_t WIDE = KW == 64 ? 0u : PANEL;
@@ -635,15 +651,33 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
             mbar_wait(bar(S_END), 0, &quiet, status);
         }
         __syncwarp();
-    } else {
+    } else if (warp < CW) {
         // x times its decays: row r of the half, an eighth of the units
         constexpr int UQ = KW / 8 / 8;
         const int r = threadIdx.x & 63, q = threadIdx.x >> 6;
         const int wq = warp & 3, g = warp >> 2, i = wq * 32 + lane, c0 = g * VH;
         const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
         float S[VH];
+        const int64_t dd = int64_t(a.Dk) * a.Dv;
+        const float *init = REV ? a.ds1 : a.s0;
+        load_part<VH>(S, !KEEP ? nullptr : nseg > 1 ? (REV ? a.dS : a.S) + int64_t(blockIdx.x) * dd : init ? init + seg.bh * dd : nullptr,
+                      i, c0, a);
+        auto keep = [&](int64_t n) {
+            if (!KEEP || i >= a.Dk) return;
+            const int64_t at = (seg.bh * a.NC + chunk(n)) * dd + int64_t(i) * a.Dv;
 #pragma unroll
-        for (int u = 0; u < VH; ++u) S[u] = 0.f;
+            for (int u = 0; u < VH; u += 8) {
+                if (c0 + u >= a.Dv) break;
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h[e] = pack(S[u + 2 * e], S[u + 2 * e + 1]);
+                    l[e] = pack(S[u + 2 * e] - lo_f(h[e]), S[u + 2 * e + 1] - hi_f(h[e]));
+                }
+                *reinterpret_cast<uint4 *>((REV ? a.zhi : a.shi) + at + c0 + u) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>((REV ? a.zlo : a.slo) + at + c0 + u) = make_uint4(l[0], l[1], l[2], l[3]);
+            }
+        };
         auto fold = [&](int64_t n, float tot) {
             const int u = int(n & 1);
             if (!all_ok(wait(S_U + u, n >> 1))) return false;
@@ -674,10 +708,458 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
             if (!ok) break;
             arrive(S_DFREE + e);
             if (n && !(ok = fold(n - 1, tot))) break;
+            keep(n);
             tot = now;
         }
         if (ok) fold(N - 1, tot);
-        store_part<VH>(S, (REV ? a.dS : a.S) + int64_t(blockIdx.x) * a.Dk * a.Dv, i, c0, a);
+        if (!KEEP) store_part<VH>(S, (REV ? a.dS : a.S) + int64_t(blockIdx.x) * dd, i, c0, a);
+        else if (REV && a.ds0 && seg.seg == 0) store_part<VH>(S, a.ds0 + seg.bh * dd, i, c0, a);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W_MMA) {
+        tc_fence_after();
+        free512(tmem);
+    }
+}
+
+// ---------------------------------------------------------------- gradients of a chunk
+// One chunk of one head at a time, any order: the states around it are there (k_lin_tc_state).
+// With W = go, R = scale D . (W V^T) and P = scale D . (Q K^T) (tokens x tokens, lower triangle):
+//     dq = R K + scale f (W S^T)        dk = R^T Q + l (V Z^T)        dv = P^T W + l (K Z)
+// R, and R^T and P^T from products of their own (V W^T, K Q^T: a transpose is dearer than eight
+// instructions), are rounded to bf16 once, as the outputs are.  dg does not go through them:
+// its sums over W_ij = R_ij (q_i . k_j) are taken from the fp32 accumulators, by rows from R and by
+// columns from R^T, and S and Z come as sums of two bf16.
+// Tensor memory: four accumulators of 128 columns; R^T and P^T lie where their products were.
+struct GradMaps {
+    CUtensorMap q, k, v, w, shi, slo, zhi, zlo;
+};
+struct GradSums {
+    float r[CG][TCH], c[CG][TCH], f[CG][TCH], l[CG][TCH];  // rows and columns of W, reads of S, leavings to Z
+    float zs[CW];
+};
+enum { G_IN, G_S, G_Z, G_DEC, G_X1, G_G1, G_R, G_D1, G_X2, G_G2, G_RT, G_D2, G_D3, G_E1, G_E2, G_SC, G_DONE, G_DG,
+       G_END, G_AR, G_COUNT = G_AR + 8 };
+
+template <int KW, int VW>
+constexpr size_t grad_smem() {
+    return 2 * size_t(KW + VW) * 256 + 2 * size_t(KW) * VW * 2 + sizeof(ChunkDecay) + TCH * 4 + sizeof(GradSums) +
+           sizeof(Ctl<G_COUNT>);
+}
+
+// 16 columns of a row to an output of 16-byte aligned rows; columns past n are left out
+__device__ __forceinline__ void put16(__nv_bfloat16 *p, int n, const float (&v)[16]) {
+#pragma unroll
+    for (int u = 0; u < 16; u += 8)
+        if (u < n)
+            *reinterpret_cast<uint4 *>(p + u) =
+                make_uint4(pack(v[u], v[u + 1]), pack(v[u + 2], v[u + 3]), pack(v[u + 4], v[u + 5]), pack(v[u + 6], v[u + 7]));
+}
+__device__ __forceinline__ void put16(float *p, int n, const float (&v)[16]) {
+#pragma unroll
+    for (int u = 0; u < 16; u += 4)
+        if (u < n) *reinterpret_cast<float4 *>(p + u) = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+}
+
+template <int KW, int VW>
+__global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_constant__ GradMaps m, const LinArgs a,
+                                                             int64_t tasks, unsigned *status) {
+    constexpr uint32_t TILE_K = KW * 256, TILE_V = VW * 256, PANEL = TCH * 128, SPANEL = KW * 128, TILE_S = KW * VW * 2;
+    constexpr int KH = KW / CG, VH = VW / CG;   // columns of a thread
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t Q = smem_u32(sm), K = Q + TILE_K, V = K + TILE_K, W = V + TILE_V, SHI = W + TILE_V, SLO = SHI + TILE_S;
+    ChunkDecay &dec = *reinterpret_cast<ChunkDecay *>(sm + 2 * (TILE_K + TILE_V) + 2 * TILE_S);
+    float *wa = reinterpret_cast<float *>(&dec + 1);
+    GradSums &sums = *reinterpret_cast<GradSums *>(wa + TCH);
+    auto *ctl = reinterpret_cast<Ctl<G_COUNT> *>(&sums + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr uint32_t R0 = 0, R1 = 128, R2 = 256, R3 = 384;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < G_COUNT; ++i)
+            mbar_init(smem_u32(&ctl->bar[i]), i >= G_AR ? CG
+                                              : i == G_R || i == G_RT || i == G_E1 || i == G_E2 || i == G_SC || i == G_DONE ? CW : 1);
+        ctl->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == W_MMA) alloc512(&ctl->tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem;
+    const Wait wait{ctl->bar, &ctl->abort, status};
+    auto bar = [&](int i) { return smem_u32(&ctl->bar[i]); };
+    auto arrive = [&](int b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(b));
+    };
+    // the n-th task of this block
+    struct Task {
+        int64_t bh, b, h, hk, n;
+    };
+    auto task = [&](int64_t n) {
+        const int64_t t = int64_t(blockIdx.x) + n * gridDim.x;
+        Task k;
+        k.bh = t / a.NC;
+        k.n = t - k.bh * a.NC;
+        k.b = k.bh / a.H;
+        k.h = k.bh - k.b * a.H;
+        k.hk = k.h / (a.H / a.Hk);
+        return k;
+    };
+    const int64_t N = (tasks - blockIdx.x + gridDim.x - 1) / gridDim.x;
+
+    if (warp == W_TMA) {
+        if (lane == 0) {
+            int64_t n = 0;
+            int in = 0, ss = 0, zz = 0;         // copies begun
+            for (; n < N; ++n) {
+                // the last task's products (and the warps, G_DONE) are done with the tiles
+                if (n && !(wait(G_D3, n - 1) && wait(G_DONE, n - 1))) break;
+                const Task k = task(n);
+                const int t = int(k.n * TCH), z = int(k.bh * a.NC + k.n);
+                mbar_arrive_expect_tx(bar(G_IN), 2 * (TILE_K + TILE_V));
+                ++in;
+                for (int p = 0; p < VW / 64; ++p) {
+                    load4(W + p * PANEL, &m.w, p * 64, int(k.h), t, int(k.b), bar(G_IN));
+                    load4(V + p * PANEL, &m.v, p * 64, int(k.h), t, int(k.b), bar(G_IN));
+                }
+                for (int p = 0; p < KW / 64; ++p) {
+                    load4(Q + p * PANEL, &m.q, p * 64, int(k.hk), t, int(k.b), bar(G_IN));
+                    load4(K + p * PANEL, &m.k, p * 64, int(k.hk), t, int(k.b), bar(G_IN));
+                }
+                mbar_arrive_expect_tx(bar(G_S), 2 * TILE_S);
+                ++ss;
+                for (int p = 0; p < VW / 64; ++p) {
+                    load3(SHI + p * SPANEL, &m.shi, p * 64, 0, z, bar(G_S));
+                    load3(SLO + p * SPANEL, &m.slo, p * 64, 0, z, bar(G_S));
+                }
+                // Z in S's place
+                if (!(wait(G_G1, n) && wait(G_SC, n))) break;
+                mbar_arrive_expect_tx(bar(G_Z), 2 * TILE_S);
+                ++zz;
+                for (int p = 0; p < VW / 64; ++p) {
+                    load3(SHI + p * SPANEL, &m.zhi, p * 64, 0, z, bar(G_Z));
+                    load3(SLO + p * SPANEL, &m.zlo, p * 64, 0, z, bar(G_Z));
+                }
+            }
+            // nothing of an abandoned walk is in flight when the block leaves
+            int quiet = 0;
+            if (in) mbar_wait(bar(G_IN), uint32_t(in - 1) & 1, &quiet, status);
+            if (ss) mbar_wait(bar(G_S), uint32_t(ss - 1) & 1, &quiet, status);
+            if (zz) mbar_wait(bar(G_Z), uint32_t(zz - 1) & 1, &quiet, status);
+        }
+        __syncwarp();
+    } else if (warp == W_AUX) {
+        // decays, and the sums of dg when a task is done
+        for (int64_t n = 0; n < N; ++n) {
+            const Task k = task(n);
+            const int64_t t0 = k.n * TCH;
+            const int len = int(a.T - t0 < TCH ? a.T - t0 : TCH);
+            dec.fill(ChunkDecay::fetch(a.g + (k.b * a.T + t0) * a.H + k.h, a.H, len), wa);
+            arrive(G_DEC);
+            if (!all_ok(wait(G_DONE, n))) break;
+            float r[4], f[4], l[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int t = lane * 4 + u;
+                r[u] = f[u] = l[u] = 0.f;
+#pragma unroll
+                for (int g = 0; g < CG; ++g) {
+                    r[u] += sums.r[g][t] - sums.c[g][t];
+                    f[u] += sums.f[g][t];
+                    l[u] += sums.l[g][t];
+                }
+            }
+            float zs = lane < CW ? sums.zs[lane] : 0.f;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) zs += __shfl_xor_sync(~0u, zs, d);
+            // suffix sums of r and f, prefix sums of l, within the lane and then across the warp
+            const float lt = (l[0] + l[1]) + (l[2] + l[3]);
+            r[2] += r[3]; r[1] += r[2]; r[0] += r[1];
+            f[2] += f[3]; f[1] += f[2]; f[0] += f[1];
+            float rr = r[0], ff = f[0], ll = lt;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const float x = __shfl_down_sync(~0u, rr, d), y = __shfl_down_sync(~0u, ff, d), z = __shfl_up_sync(~0u, ll, d);
+                if (lane + d < 32) {
+                    rr += x;
+                    ff += y;
+                }
+                if (lane >= d) ll += z;
+            }
+            const float after_r = rr - r[0], after_f = ff - f[0];
+            float across = (ll - lt) + (dec.total == 0.f ? 0.f : dec.total * zs);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int t = lane * 4 + u;
+                const bool cut = t ? dec.r[t] != dec.r[t - 1] : dec.r[0] != 0;
+                // no pair of the chunk crosses its first token
+                if (t < len)
+                    a.dg[(k.b * a.T + t0 + t) * a.H + k.h] = cut ? 0.f : across + (f[u] + after_f) + (t ? r[u] + after_r : 0.f);
+                across += l[u];
+            }
+            arrive(G_DG);
+        }
+    } else if (warp == W_MMA) {
+        if (lane == 0) {
+            constexpr int KS = KW / 16, VS = VW / 16, TS = TCH / 16;
+            for (int64_t n = 0; n < N; ++n) {
+                if (!wait(G_IN, n)) break;
+                tc_fence_after();
+                product<TCH, VS, false, false>(tmem + R0, W, PANEL, V, PANEL, false);
+                product<TCH, KS, false, false>(tmem + R1, Q, PANEL, K, PANEL, false);
+                commit(bar(G_X1));
+                if (!wait(G_S, n)) break;
+                tc_fence_after();
+                product<KW, VS, false, false>(tmem + R2, W, PANEL, SHI, SPANEL, false);
+                product<KW, VS, false, false>(tmem + R2, W, PANEL, SLO, SPANEL, true);
+                commit(bar(G_G1));
+                if (!wait(G_R, n)) break;
+                tc_fence_after();
+                product_ts<KW, TS>(tmem + R3, tmem + R0, K, PANEL, false);
+                commit(bar(G_D1));
+                product<TCH, KS, false, false>(tmem + R1, K, PANEL, Q, PANEL, false);
+                if (!wait(G_D1, n)) break;              // R0 has been read
+                tc_fence_after();
+                product<TCH, VS, false, false>(tmem + R0, V, PANEL, W, PANEL, false);
+                commit(bar(G_X2));
+                if (!(wait(G_Z, n) && wait(G_E1, n))) break;
+                tc_fence_after();
+                product<KW, VS, false, false>(tmem + R2, V, PANEL, SHI, SPANEL, false);
+                product<KW, VS, false, false>(tmem + R2, V, PANEL, SLO, SPANEL, true);
+                if (!wait(G_RT, n)) break;
+                tc_fence_after();
+                product_ts<KW, TS>(tmem + R3, tmem + R0, Q, PANEL, false);
+                commit(bar(G_D2));
+                if (!wait(G_E2, n)) break;
+                tc_fence_after();
+                product<VW, KS, false, true>(tmem + R2, K, PANEL, SHI, SPANEL, false);
+                product_ts<VW, TS>(tmem + R3, tmem + R1, W, PANEL, false);
+                commit(bar(G_D3));
+            }
+            int quiet = 0;
+            commit(bar(G_END));
+            mbar_wait(bar(G_END), 0, &quiet, status);
+        }
+        __syncwarp();
+    } else if (warp < CW) {
+        const int wq = warp & 3, g = warp >> 2, i = wq * 32 + lane;
+        const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
+        for (int64_t n = 0; n < N; ++n) {
+            const Task k = task(n);
+            const int64_t t0 = k.n * TCH;
+            const bool live = t0 + i < a.T;
+            const int64_t tok = k.b * a.T + t0 + i;
+            if (!all_ok(wait(G_DEC, n) && (n == 0 || wait(G_DG, n - 1)) && wait(G_X1, n))) break;
+            tc_fence_after();
+            const float xi = dec.x[i];
+            const int ri = dec.r[i], j8 = 8 * g;
+            // R, 8 columns of every block of 32, and the row sums of W
+            {
+                uint32_t h[4][4];
+                float sum = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c > wq) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) h[c][e] = 0u;
+                        continue;
+                    }
+                    float x[8], y[8], w[8];
+                    ld8(lanes + R0 + 32 * c + j8, x);
+                    ld8(lanes + R1 + 32 * c + j8, y);
+                    const float *src = (c < wq ? dec.wb : dec.x) + 32 * c + j8;
+                    *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(src);
+                    *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(src + 4);
+                    if (c < wq) {
+                        const float f = ri == dec.re[c]
+                                            ? a.scale * fast_exp2((dec.Ehi[wq] - dec.Ehi[c]) + (dec.Elo[wq] - dec.Elo[c]) + xi) : 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            x[e] *= w[e] * f;
+                            sum = fmaf(x[e], y[e], sum);
+                        }
+                    } else {
+                        const uint2 rj = *reinterpret_cast<const uint2 *>(dec.r + 32 * c + j8);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int r = int(((e < 4 ? rj.x : rj.y) >> (8 * (e & 3))) & 255u);
+                            x[e] = j8 + e <= lane && ri == r ? x[e] * (a.scale * fast_exp2(xi - w[e])) : 0.f;
+                            if (j8 + e < lane) sum = fmaf(x[e], y[e], sum);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[c][e] = pack(x[2 * e], x[2 * e + 1]);
+                }
+                sums.r[g][i] = sum;
+                tc_fence_before();
+                arrive(G_AR + wq);
+                // the warps of these lanes have read their columns
+                if (!all_ok(wait(G_AR + wq, n))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) st4(lanes + R0 + 16 * c + 4 * g, h[c][0], h[c][1], h[c][2], h[c][3]);
+                st_wait();
+                tc_fence_before();
+                arrive(G_R);
+            }
+            // this thread's part of S, for <Z, S>
+            uint32_t sh[VH / 2], sl[VH / 2];
+            if (!all_ok(wait(G_S, n))) break;
+#pragma unroll
+            for (int u = 0; u < VH / 8; ++u) {
+                const uint32_t at = i < KW ? unit_at(i, g * (VH / 8) + u, SPANEL) : 0u;
+                const uint4 x = lds(SHI + at), y = lds(SLO + at);
+                sh[4 * u] = x.x; sh[4 * u + 1] = x.y; sh[4 * u + 2] = x.z; sh[4 * u + 3] = x.w;
+                sl[4 * u] = y.x; sl[4 * u + 1] = y.y; sl[4 * u + 2] = y.z; sl[4 * u + 3] = y.w;
+            }
+            fence_proxy_async_smem();
+            arrive(G_SC);
+            // an output of one phase: s R2 + t R3, and s R2 . x with x this row's tile
+            auto out = [&](float s, float t, uint32_t tile, int c0, int W_, auto put, float *dot) {
+                float d = 0.f;
+#pragma unroll 1
+                for (int u = 0; u < W_; u += 16) {
+                    float x[16], y[16];
+                    ld16x2(lanes + R2 + c0 + u, lanes + R3 + c0 + u, x, y);
+                    if (dot) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const uint4 v = lds(tile + unit_at(i, ((c0 + u) >> 3) + q, PANEL));
+                            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                d = fmaf(x[8 * q + 2 * e], lo_f(in[e]), d);
+                                d = fmaf(x[8 * q + 2 * e + 1], hi_f(in[e]), d);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) y[e] = s == 0.f ? t * y[e] : fmaf(s, x[e], t * y[e]);
+                    put(c0 + u, y);
+                }
+                if (dot) *dot = s == 0.f ? 0.f : s * d;
+            };
+            // dq
+            const float fi = dec.first(i) * a.scale;
+            if (!all_ok(wait(G_D1, n))) break;
+            tc_fence_after();
+            out(fi, 1.f, Q, g * KH, KH, [&](int c, const float (&y)[16]) {
+                if (!live) return;
+                if (a.pq) put16(a.pq + (tok * a.H + k.h) * a.Dk + c, a.Dk - c, y);
+                else put16(static_cast<__nv_bfloat16 *>(a.dq) + tok * a.ldq + k.hk * a.Dk + c, a.Dk - c, y);
+            }, &sums.f[g][i]);
+            tc_fence_before();
+            arrive(G_E1);
+            // R^T and P^T: this thread's row is token j = i, its columns the later tokens
+            if (!all_ok(wait(G_X2, n))) break;
+            tc_fence_after();
+            const float wbj = dec.wb[i];
+            {
+                uint32_t h[4][4], p[4][4];
+                float sum = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c < wq) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) h[c][e] = p[c][e] = 0u;
+                        continue;
+                    }
+                    float x[8], y[8], w[8];
+                    ld8(lanes + R0 + 32 * c + j8, x);
+                    ld8(lanes + R1 + 32 * c + j8, y);
+                    const float *src = (c > wq ? wa : dec.x) + 32 * c + j8;
+                    *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(src);
+                    *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(src + 4);
+                    if (c > wq) {
+                        const float f = dec.re[c - 1 < 0 ? 0 : c - 1] == dec.re[wq]
+                                            ? a.scale * wbj *
+                                                  fast_exp2((dec.Ehi[c - 1 < 0 ? 0 : c - 1] - dec.Ehi[wq]) +
+                                                            (dec.Elo[c - 1 < 0 ? 0 : c - 1] - dec.Elo[wq]))
+                                            : 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float d = w[e] * f;
+                            x[e] *= d;
+                            sum = fmaf(x[e], y[e], sum);
+                            y[e] *= d;
+                        }
+                    } else {
+                        const uint2 rj = *reinterpret_cast<const uint2 *>(dec.r + 32 * c + j8);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int r = int(((e < 4 ? rj.x : rj.y) >> (8 * (e & 3))) & 255u);
+                            const bool in = j8 + e >= lane && ri == r;
+                            const float d = in ? a.scale * fast_exp2(w[e] - xi) : 0.f;
+                            x[e] = in ? x[e] * d : 0.f;
+                            if (j8 + e > lane) sum = fmaf(x[e], y[e], sum);
+                            y[e] = in ? y[e] * d : 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        h[c][e] = pack(x[2 * e], x[2 * e + 1]);
+                        p[c][e] = pack(y[2 * e], y[2 * e + 1]);
+                    }
+                }
+                sums.c[g][i] = sum;
+                tc_fence_before();
+                arrive(G_AR + 4 + wq);
+                if (!all_ok(wait(G_AR + 4 + wq, n))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    st4(lanes + R0 + 16 * c + 4 * g, h[c][0], h[c][1], h[c][2], h[c][3]);
+                    st4(lanes + R1 + 16 * c + 4 * g, p[c][0], p[c][1], p[c][2], p[c][3]);
+                }
+                st_wait();
+                tc_fence_before();
+                arrive(G_RT);
+            }
+            // <Z, S>
+            if (!all_ok(wait(G_Z, n))) break;
+            {
+                float d = 0.f;
+#pragma unroll
+                for (int u = 0; u < VH / 8; ++u) {
+                    const uint32_t at = i < KW ? unit_at(i, g * (VH / 8) + u, SPANEL) : 0u;
+                    const uint4 x = lds(SHI + at), y = lds(SLO + at);
+                    const uint32_t zh[4] = {x.x, x.y, x.z, x.w}, zl[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t s = sh[4 * u + e], t = sl[4 * u + e];
+                        d = fmaf(lo_f(zh[e]) + lo_f(zl[e]), lo_f(s) + lo_f(t), d);
+                        d = fmaf(hi_f(zh[e]) + hi_f(zl[e]), hi_f(s) + hi_f(t), d);
+                    }
+                }
+                if (i >= KW) d = 0.f;
+#pragma unroll
+                for (int e = 16; e; e >>= 1) d += __shfl_xor_sync(~0u, d, e);
+                if (lane == 0) sums.zs[warp] = d;
+            }
+            // dk
+            const float lj = dec.to_end(i);
+            if (!all_ok(wait(G_D2, n))) break;
+            tc_fence_after();
+            out(lj, 1.f, K, g * KH, KH, [&](int c, const float (&y)[16]) {
+                if (!live) return;
+                if (a.pk) put16(a.pk + (tok * a.H + k.h) * a.Dk + c, a.Dk - c, y);
+                else put16(static_cast<__nv_bfloat16 *>(a.dk) + tok * a.ldk + k.hk * a.Dk + c, a.Dk - c, y);
+            }, &sums.l[g][i]);
+            tc_fence_before();
+            arrive(G_E2);
+            // dv
+            if (!all_ok(wait(G_D3, n))) break;
+            tc_fence_after();
+            out(lj, 1.f, 0u, g * VH, VH, [&](int c, const float (&y)[16]) {
+                if (live) put16(static_cast<__nv_bfloat16 *>(a.dv) + tok * a.ldv + k.h * a.Dv + c, a.Dv - c, y);
+            }, static_cast<float *>(nullptr));
+            tc_fence_before();
+            fence_proxy_async_smem();
+            arrive(G_DONE);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -693,16 +1175,16 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
         if (e_ != cudaSuccess) return e_;     \
     } while (0)
 
-template <int KW, int VW, bool REV>
+template <int KW, int VW, bool REV, bool KEEP>
 cudaError_t run_states(const LinArgs &a, const LinSplit &sp, unsigned *status, cudaStream_t st) {
     StateMaps m;
     const bool ok = REV ? map_tokens(&m.x, a.q, a.Dk, a.Hk, a.T, a.B, a.ldq, SH) && map_tokens(&m.y, a.go, a.Dv, a.H, a.T, a.B, a.ldo, SH)
                         : map_tokens(&m.x, a.k, a.Dk, a.Hk, a.T, a.B, a.ldk, SH) && map_tokens(&m.y, a.v, a.Dv, a.H, a.T, a.B, a.ldv, SH);
     if (!ok) return cudaErrorInvalidValue;
     constexpr size_t smem = state_smem<KW, VW>();
-    LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_state<KW, VW, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+    LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_state<KW, VW, REV, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
     ProfScope ps(K_LIN_STATE, st);
-    k_lin_tc_state<KW, VW, REV><<<unsigned(a.B * a.H * sp.nseg), TC_BLOCK, smem, st>>>(m, a, sp.nseg, sp.cps, status);
+    k_lin_tc_state<KW, VW, REV, KEEP><<<unsigned(a.B * a.H * sp.nseg), TC_BLOCK, smem, st>>>(m, a, sp.nseg, sp.cps, status);
     return cudaGetLastError();
 }
 
@@ -714,7 +1196,7 @@ cudaError_t run_fwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cuda
         !map_tokens(&m.v, a.v, a.Dv, a.H, a.T, a.B, a.ldv) || !map_tokens(&m.o, a.o, a.Dv, a.H, a.T, a.B, a.ldo))
         return cudaErrorInvalidValue;
     if (sp.nseg > 1) {
-        LIN_CUDA((run_states<KW, VW, false>(a, sp, status, st)));
+        LIN_CUDA((run_states<KW, VW, false, false>(a, sp, status, st)));
         LIN_CUDA(launch_lin_scan(a, sp.nseg, false, st));
     }
     constexpr size_t smem = fwd_smem<KW, VW>();
@@ -723,6 +1205,36 @@ cudaError_t run_fwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cuda
     // the state is a result only where no segments' states were joined: otherwise it meets bf16 next
     const int parts = sp.nseg == 1 && a.s1 ? 3 : 2;
     k_lin_tc_fwd<KW, VW><<<unsigned(a.B * a.H * sp.nseg), TC_BLOCK, smem, st>>>(m, a, sp.nseg, sp.cps, parts, status);
+    return cudaGetLastError();
+}
+
+template <int KW, int VW>
+cudaError_t run_bwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cudaStream_t st) {
+    static_assert(grad_smem<128, 128>() <= 232448, "shared memory of an SM");
+    GradMaps m;
+    const int64_t n = a.B * a.H * a.NC;
+    if (!map_tokens(&m.q, a.q, a.Dk, a.Hk, a.T, a.B, a.ldq) || !map_tokens(&m.k, a.k, a.Dk, a.Hk, a.T, a.B, a.ldk) ||
+        !map_tokens(&m.v, a.v, a.Dv, a.H, a.T, a.B, a.ldv) || !map_tokens(&m.w, a.go, a.Dv, a.H, a.T, a.B, a.ldo) ||
+        !map_states(&m.shi, a.shi, a.Dv, a.Dk, n, KW) || !map_states(&m.slo, a.slo, a.Dv, a.Dk, n, KW) ||
+        !map_states(&m.zhi, a.zhi, a.Dv, a.Dk, n, KW) || !map_states(&m.zlo, a.zlo, a.Dv, a.Dk, n, KW))
+        return cudaErrorInvalidValue;
+    // the states around every chunk: by segments where the heads alone would leave SMs idle
+    LinArgs b = a;
+    b.s1 = b.ds0 = nullptr;
+    if (sp.nseg > 1) {
+        LIN_CUDA((run_states<KW, VW, false, false>(b, sp, status, st)));
+        LIN_CUDA(launch_lin_scan(b, sp.nseg, false, st));
+    }
+    LIN_CUDA((run_states<KW, VW, false, true>(a, sp, status, st)));
+    if (sp.nseg > 1) {
+        LIN_CUDA((run_states<KW, VW, true, false>(b, sp, status, st)));
+        LIN_CUDA(launch_lin_scan(b, sp.nseg, true, st));
+    }
+    LIN_CUDA((run_states<KW, VW, true, true>(a, sp, status, st)));
+    constexpr size_t smem = grad_smem<KW, VW>();
+    LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_grad<KW, VW>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+    ProfScope ps(K_LIN_GRAD, st);
+    k_lin_tc_grad<KW, VW><<<unsigned(std::min<int64_t>(n, 152)), TC_BLOCK, smem, st>>>(m, a, n, status);
     return cudaGetLastError();
 }
 
@@ -749,6 +1261,14 @@ cudaError_t launch_lin_tc_fwd(const LinArgs &args, unsigned *status, cudaStream_
     const LinSplit sp = lin_split(a);
     if (a.Dk <= 64) return a.Dv <= 64 ? run_fwd<64, 64>(a, sp, status, st) : run_fwd<64, 128>(a, sp, status, st);
     return a.Dv <= 64 ? run_fwd<128, 64>(a, sp, status, st) : run_fwd<128, 128>(a, sp, status, st);
+}
+
+cudaError_t launch_lin_tc_bwd(const LinArgs &args, unsigned *status, cudaStream_t st) {
+    LinArgs a = args;
+    a.NC = cdiv(a.T, TCH);
+    const LinSplit sp = lin_split(a);
+    if (a.Dk <= 64) return a.Dv <= 64 ? run_bwd<64, 64>(a, sp, status, st) : run_bwd<64, 128>(a, sp, status, st);
+    return a.Dv <= 64 ? run_bwd<128, 64>(a, sp, status, st) : run_bwd<128, 128>(a, sp, status, st);
 }
 
 }  // namespace adj

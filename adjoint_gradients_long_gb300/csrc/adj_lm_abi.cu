@@ -42,7 +42,7 @@ adj_status check_lin(const adj_lin_dims *d, bool step) {
     if (d->ldq % vec || d->ldk % vec || d->ldv % vec || d->ldo % vec) return ADJ_EALIGN;
     // tensor maps: 32-bit token coordinates, 40-bit byte strides
     if (d->x_dtype == ADJ_BF16 && !step) {
-        if (d->T >= (int64_t(1) << 31)) return ADJ_ESHAPE;
+        if (d->T >= (int64_t(1) << 31) || d->B * d->H * (d->T / 128 + 1) >= (int64_t(1) << 31)) return ADJ_ESHAPE;
         for (int64_t ld : {d->ldq, d->ldk, d->ldv, d->ldo})
             if (ld >= (int64_t(1) << 31) || d->T * ld >= (int64_t(1) << 39)) return ADJ_ESHAPE;
     }
