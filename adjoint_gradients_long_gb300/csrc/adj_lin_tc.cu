@@ -28,11 +28,10 @@ using namespace tc5;
 constexpr int TCH = 128;                // tokens of a chunk
 // Warps of a block: sixteen computing warps (four groups of four; a group covers the 128 lanes
 // of tensor memory, a warp the lanes of its number modulo four), and one warp each that issues
-// products, copies in, and prepares the decays and copies out.  19 warps leave 104 registers a
-// thread; at 96 the state and the weights in flight spill, and the spills cost a fifth.
+// products, copies in, prepares the decays, and copies out.
 constexpr int CG = 4, CW = 4 * CG;
-constexpr int W_MMA = CW, W_TMA = CW + 1, W_AUX = CW + 2;
-constexpr int TC_BLOCK = (CW + 3) * 32;
+constexpr int W_MMA = CW, W_TMA = CW + 1, W_AUX = CW + 2, W_OUT = CW + 3;
+constexpr int TC_BLOCK = (CW + 4) * 32;
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -159,7 +158,7 @@ struct FwdMaps {
     CUtensorMap q, k, v, o;
 };
 struct StateMaps {
-    CUtensorMap x, y;
+    CUtensorMap x, y, hi, lo;   // hi, lo: the kept states
 };
 
 struct Wait {
@@ -548,25 +547,28 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
 // chunk's two halves add up in one of two accumulators, and the warps fold the chunk before into
 // the state meanwhile; only the state's own multiply-add is a chain.
 constexpr int SH = TCH / 2, RING = 3;
-enum { S_FULL, S_EMPTY = S_FULL + RING, S_K = S_EMPTY + RING, S_DEC = S_K + RING, S_DFREE = S_DEC + 2, S_U = S_DFREE + 2,
-       S_UFREE = S_U + 2, S_END = S_UFREE + 2, S_COUNT };
+enum { S_FULL, S_EMPTY = S_FULL + RING, S_K = S_EMPTY + RING, S_DEC = S_K + RING, S_DFREE = S_DEC + 2,
+       S_U = S_DFREE + 2, S_UFREE = S_U + 2, S_KEPT = S_UFREE + 2, S_END, S_LEFT, S_COUNT };
 
-template <int KW, int VW>
+template <int KW, int VW, bool KEEP>
 constexpr size_t state_smem() {
-    return RING * size_t(3 * KW + VW) * SH * 2 + 2 * sizeof(ChunkDecay) + sizeof(Ctl<S_COUNT>);
+    return RING * size_t(3 * KW + VW) * SH * 2 + (KEEP ? size_t(KW) * VW * 2 : 0) + 2 * sizeof(ChunkDecay) + sizeof(Ctl<S_COUNT>);
 }
 
 // KEEP: the walk starts from the state that enters the segment (a.S / a.dS, or s0 / ds1 when the
 // segment is the whole head), and the state met before every chunk is kept as a sum of two bf16
-// (keep_hi, keep_lo [B,H,NC,Dk,Dv]), the operand of the backward pass.
+// [B,H,NC,Dk,Dv], the operand of the backward pass.  The parts leave one after the other through
+// one tile, the second while the next chunk is being scaled; with a tile each and a ring of two
+// stages the walk waited for its copies in (86 us against @@ us for 64 chunks of 32 heads).
 template <int KW, int VW, bool REV, bool KEEP>
 __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_constant__ StateMaps m, const LinArgs a, int nseg,
                                                               int cps, unsigned *status) {
     constexpr uint32_t TILE_K = KW * SH * 2, TILE_V = VW * SH * 2, STAGE = 3 * TILE_K + TILE_V, PANEL = SH * 128;
+    constexpr uint32_t TILE_S = KW * VW * 2, SPANEL = KW * 128;
     constexpr int VH = VW / CG;
     extern __shared__ __align__(1024) uint8_t sm[];
-    const uint32_t base = smem_u32(sm);
-    ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + RING * STAGE);
+    const uint32_t base = smem_u32(sm), KEPT = base + RING * STAGE;
+    ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + RING * STAGE + (KEEP ? TILE_S : 0));
     auto *ctl = reinterpret_cast<Ctl<S_COUNT> *>(dec + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Seg seg(a, nseg, cps);
@@ -577,7 +579,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S_COUNT; ++i)
-            mbar_init(smem_u32(&ctl->bar[i]), (i >= S_K && i < S_DEC) || (i >= S_DFREE && i < S_U) || (i >= S_UFREE && i < S_END) ? CW : 1);
+            mbar_init(smem_u32(&ctl->bar[i]), (i >= S_K && i < S_DEC) || (i >= S_DFREE && i < S_U) || (i >= S_UFREE && i <= S_KEPT) ? CW : 1);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -627,6 +629,19 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
             if (lane == 0) mbar_arrive(bar(S_DEC + s));
         }
         if (!KEEP && lane == 0) a.tot[blockIdx.x] = cuts ? 0.f : fast_exp2(sum.value());
+    } else if (warp == W_OUT) {
+        if (KEEP && lane == 0) {
+            for (int64_t k = 0; k < 2 * N; ++k) {
+                if (!wait(S_KEPT, k)) break;
+                for (int p = 0; p < VW / 64; ++p)
+                    store3(k & 1 ? &m.lo : &m.hi, p * 64, 0, int(seg.bh * a.NC + chunk(k >> 1)), KEPT + p * SPANEL);
+                bulk_commit();
+                bulk_wait_read();
+                mbar_arrive(bar(S_LEFT));
+            }
+            bulk_wait_all();
+        }
+        __syncwarp();
     } else if (warp == W_MMA) {
         if (lane == 0) {
             constexpr uint32_t WIDE = KW == 64 ? 0u : PANEL;
@@ -662,21 +677,25 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
         const float *init = REV ? a.ds1 : a.s0;
         load_part<VH>(S, !KEEP ? nullptr : nseg > 1 ? (REV ? a.dS : a.S) + int64_t(blockIdx.x) * dd : init ? init + seg.bh * dd : nullptr,
                       i, c0, a);
-        auto keep = [&](int64_t n) {
-            if (!KEEP || i >= a.Dk) return;
-            const int64_t at = (seg.bh * a.NC + chunk(n)) * dd + int64_t(i) * a.Dv;
+        // the first (k even) or second part of the state; k counts the parts
+        auto keep = [&](int64_t k) {
+            if (!KEEP) return true;
+            if (k && !all_ok(wait(S_LEFT, k - 1))) return false;
+            if (i < KW)
 #pragma unroll
-            for (int u = 0; u < VH; u += 8) {
-                if (c0 + u >= a.Dv) break;
-                uint32_t h[4], l[4];
+                for (int u = 0; u < VH; u += 8) {
+                    uint32_t h[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    h[e] = pack(S[u + 2 * e], S[u + 2 * e + 1]);
-                    l[e] = pack(S[u + 2 * e] - lo_f(h[e]), S[u + 2 * e + 1] - hi_f(h[e]));
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = S[u + 2 * e], y = S[u + 2 * e + 1];
+                        h[e] = pack(x, y);
+                        if (k & 1) h[e] = pack(x - lo_f(h[e]), y - hi_f(h[e]));
+                    }
+                    sts(KEPT + unit_at(i, (c0 + u) >> 3, SPANEL), make_uint4(h[0], h[1], h[2], h[3]));
                 }
-                *reinterpret_cast<uint4 *>((REV ? a.zhi : a.shi) + at + c0 + u) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4 *>((REV ? a.zlo : a.slo) + at + c0 + u) = make_uint4(l[0], l[1], l[2], l[3]);
-            }
+            fence_proxy_async_smem();
+            arrive(S_KEPT);
+            return true;
         };
         auto fold = [&](int64_t n, float tot) {
             const int u = int(n & 1);
@@ -703,15 +722,16 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
                 fence_proxy_async_smem();
                 arrive(S_K + s);
                 if (++s == RING) { s = 0; ++turn; }
+                if (h == 0 && n && !(ok = keep(2 * n - 1))) break;
             }
             const float now = dec[e].total;
             if (!ok) break;
             arrive(S_DFREE + e);
             if (n && !(ok = fold(n - 1, tot))) break;
-            keep(n);
+            if (!(ok = keep(2 * n))) break;
             tot = now;
         }
-        if (ok) fold(N - 1, tot);
+        if (ok && keep(2 * N - 1)) fold(N - 1, tot);
         if (!KEEP) store_part<VH>(S, (REV ? a.dS : a.S) + int64_t(blockIdx.x) * dd, i, c0, a);
         else if (REV && a.ds0 && seg.seg == 0) store_part<VH>(S, a.ds0 + seg.bh * dd, i, c0, a);
     }
@@ -732,15 +752,17 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
 // its sums over W_ij = R_ij (q_i . k_j) are taken from the fp32 accumulators, by rows from R and by
 // columns from R^T, and S and Z come as sums of two bf16.
 // Tensor memory: four accumulators of 128 columns; R^T and P^T lie where their products were.
+// The outputs leave through tiles whose last product is done: dq through S's, dk through Q's, dv
+// through V's.  (fp32 parts of shared heads are stored by the lanes.)
 struct GradMaps {
-    CUtensorMap q, k, v, w, shi, slo, zhi, zlo;
+    CUtensorMap q, k, v, w, shi, slo, zhi, zlo, dq, dk, dv;
 };
 struct GradSums {
-    float r[CG][TCH], c[CG][TCH], f[CG][TCH], l[CG][TCH];  // rows and columns of W, reads of S, leavings to Z
+    float r[CG][TCH], f[CG][TCH], l[CG][TCH];   // W: rows less columns; reads of S; leavings to Z
     float zs[CW];
 };
 enum { G_IN, G_S, G_Z, G_DEC, G_X1, G_G1, G_R, G_D1, G_X2, G_G2, G_RT, G_D2, G_D3, G_E1, G_E2, G_SC, G_DONE, G_DG,
-       G_END, G_AR, G_COUNT = G_AR + 8 };
+       G_OQ, G_OK, G_OV, G_SFREE, G_LEFT, G_END, G_AR, G_COUNT = G_AR + 8 };
 
 template <int KW, int VW>
 constexpr size_t grad_smem() {
@@ -748,14 +770,7 @@ constexpr size_t grad_smem() {
            sizeof(Ctl<G_COUNT>);
 }
 
-// 16 columns of a row to an output of 16-byte aligned rows; columns past n are left out
-__device__ __forceinline__ void put16(__nv_bfloat16 *p, int n, const float (&v)[16]) {
-#pragma unroll
-    for (int u = 0; u < 16; u += 8)
-        if (u < n)
-            *reinterpret_cast<uint4 *>(p + u) =
-                make_uint4(pack(v[u], v[u + 1]), pack(v[u + 2], v[u + 3]), pack(v[u + 4], v[u + 5]), pack(v[u + 6], v[u + 7]));
-}
+// 16 columns of a row to an fp32 array of 16-byte aligned rows; columns past n are left out
 __device__ __forceinline__ void put16(float *p, int n, const float (&v)[16]) {
 #pragma unroll
     for (int u = 0; u < 16; u += 4)
@@ -779,7 +794,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
     if (threadIdx.x == 0) {
         for (int i = 0; i < G_COUNT; ++i)
             mbar_init(smem_u32(&ctl->bar[i]), i >= G_AR ? CG
-                                              : i == G_R || i == G_RT || i == G_E1 || i == G_E2 || i == G_SC || i == G_DONE ? CW : 1);
+                                              : i == G_R || i == G_RT || (i >= G_E1 && i <= G_DONE) || (i >= G_OQ && i <= G_OV) ? CW : 1);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -815,8 +830,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
             int64_t n = 0;
             int in = 0, ss = 0, zz = 0;         // copies begun
             for (; n < N; ++n) {
-                // the last task's products (and the warps, G_DONE) are done with the tiles
-                if (n && !(wait(G_D3, n - 1) && wait(G_DONE, n - 1))) break;
+                // the last task is done with the tiles: its products, the warps, its outputs
+                if (n && !(wait(G_D3, n - 1) && wait(G_DONE, n - 1) && wait(G_LEFT, n - 1))) break;
                 const Task k = task(n);
                 const int t = int(k.n * TCH), z = int(k.bh * a.NC + k.n);
                 mbar_arrive_expect_tx(bar(G_IN), 2 * (TILE_K + TILE_V));
@@ -835,8 +850,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                     load3(SHI + p * SPANEL, &m.shi, p * 64, 0, z, bar(G_S));
                     load3(SLO + p * SPANEL, &m.slo, p * 64, 0, z, bar(G_S));
                 }
-                // Z in S's place
-                if (!(wait(G_G1, n) && wait(G_SC, n))) break;
+                // Z in S's place, once dq has left through it
+                if (!wait(G_SFREE, n)) break;
                 mbar_arrive_expect_tx(bar(G_Z), 2 * TILE_S);
                 ++zz;
                 for (int p = 0; p < VW / 64; ++p) {
@@ -849,6 +864,32 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
             if (in) mbar_wait(bar(G_IN), uint32_t(in - 1) & 1, &quiet, status);
             if (ss) mbar_wait(bar(G_S), uint32_t(ss - 1) & 1, &quiet, status);
             if (zz) mbar_wait(bar(G_Z), uint32_t(zz - 1) & 1, &quiet, status);
+        }
+        __syncwarp();
+    } else if (warp == W_OUT) {
+        if (lane == 0) {
+            for (int64_t n = 0; n < N; ++n) {
+                const Task k = task(n);
+                const int t = int(k.n * TCH);
+                if (!wait(G_OQ, n)) break;
+                if (!a.pq) {
+                    for (int p = 0; p < KW / 64; ++p) store4(&m.dq, p * 64, int(k.hk), t, int(k.b), SHI + p * PANEL);
+                    bulk_commit();
+                    bulk_wait_read();
+                }
+                mbar_arrive(bar(G_SFREE));
+                if (!wait(G_OK, n)) break;
+                if (!a.pq) {
+                    for (int p = 0; p < KW / 64; ++p) store4(&m.dk, p * 64, int(k.hk), t, int(k.b), Q + p * PANEL);
+                    bulk_commit();
+                }
+                if (!wait(G_OV, n)) break;
+                for (int p = 0; p < VW / 64; ++p) store4(&m.dv, p * 64, int(k.h), t, int(k.b), V + p * PANEL);
+                bulk_commit();
+                bulk_wait_read();
+                mbar_arrive(bar(G_LEFT));
+            }
+            bulk_wait_all();
         }
         __syncwarp();
     } else if (warp == W_AUX) {
@@ -867,7 +908,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 r[u] = f[u] = l[u] = 0.f;
 #pragma unroll
                 for (int g = 0; g < CG; ++g) {
-                    r[u] += sums.r[g][t] - sums.c[g][t];
+                    r[u] += sums.r[g][t];
                     f[u] += sums.f[g][t];
                     l[u] += sums.l[g][t];
                 }
@@ -1015,10 +1056,14 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 sh[4 * u] = x.x; sh[4 * u + 1] = x.y; sh[4 * u + 2] = x.z; sh[4 * u + 3] = x.w;
                 sl[4 * u] = y.x; sl[4 * u + 1] = y.y; sl[4 * u + 2] = y.z; sl[4 * u + 3] = y.w;
             }
-            fence_proxy_async_smem();
+            // dq takes S's place: every warp has its part, and W S^T is formed
             arrive(G_SC);
-            // an output of one phase: s R2 + t R3, and s R2 . x with x this row's tile
-            auto out = [&](float s, float t, uint32_t tile, int c0, int W_, auto put, float *dot) {
+            auto stage = [&](uint32_t tile, int c, const float (&y)[16]) {
+                put8(tile, PANEL, i, c >> 3, y);
+                put8(tile, PANEL, i, (c >> 3) + 1, y + 8);
+            };
+            // an output of one phase: s R2 + R3, and s R2 . x with x this row's tile
+            auto out = [&](float s, uint32_t tile, int c0, int W_, auto put, float *dot) {
                 float d = 0.f;
 #pragma unroll 1
                 for (int u = 0; u < W_; u += 16) {
@@ -1037,22 +1082,23 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                         }
                     }
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) y[e] = s == 0.f ? t * y[e] : fmaf(s, x[e], t * y[e]);
+                    for (int e = 0; e < 16; ++e) y[e] = s == 0.f ? y[e] : fmaf(s, x[e], y[e]);
                     put(c0 + u, y);
                 }
                 if (dot) *dot = s == 0.f ? 0.f : s * d;
             };
             // dq
             const float fi = dec.first(i) * a.scale;
-            if (!all_ok(wait(G_D1, n))) break;
+            if (!all_ok(wait(G_SC, n) && wait(G_D1, n))) break;
             tc_fence_after();
-            out(fi, 1.f, Q, g * KH, KH, [&](int c, const float (&y)[16]) {
-                if (!live) return;
-                if (a.pq) put16(a.pq + (tok * a.H + k.h) * a.Dk + c, a.Dk - c, y);
-                else put16(static_cast<__nv_bfloat16 *>(a.dq) + tok * a.ldq + k.hk * a.Dk + c, a.Dk - c, y);
+            out(fi, Q, g * KH, KH, [&](int c, const float (&y)[16]) {
+                if (!a.pq) stage(SHI, c, y);
+                else if (live) put16(a.pq + (tok * a.H + k.h) * a.Dk + c, a.Dk - c, y);
             }, &sums.f[g][i]);
             tc_fence_before();
             arrive(G_E1);
+            fence_proxy_async_smem();
+            arrive(G_OQ);
             // R^T and P^T: this thread's row is token j = i, its columns the later tokens
             if (!all_ok(wait(G_X2, n))) break;
             tc_fence_after();
@@ -1104,7 +1150,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                         p[c][e] = pack(y[2 * e], y[2 * e + 1]);
                     }
                 }
-                sums.c[g][i] = sum;
+                sums.r[g][i] -= sum;
                 tc_fence_before();
                 arrive(G_AR + 4 + wq);
                 if (!all_ok(wait(G_AR + 4 + wq, n))) break;
@@ -1143,21 +1189,23 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
             const float lj = dec.to_end(i);
             if (!all_ok(wait(G_D2, n))) break;
             tc_fence_after();
-            out(lj, 1.f, K, g * KH, KH, [&](int c, const float (&y)[16]) {
-                if (!live) return;
-                if (a.pk) put16(a.pk + (tok * a.H + k.h) * a.Dk + c, a.Dk - c, y);
-                else put16(static_cast<__nv_bfloat16 *>(a.dk) + tok * a.ldk + k.hk * a.Dk + c, a.Dk - c, y);
+            out(lj, K, g * KH, KH, [&](int c, const float (&y)[16]) {
+                if (!a.pk) stage(Q, c, y);
+                else if (live) put16(a.pk + (tok * a.H + k.h) * a.Dk + c, a.Dk - c, y);
             }, &sums.l[g][i]);
             tc_fence_before();
             arrive(G_E2);
+            fence_proxy_async_smem();
+            arrive(G_OK);
             // dv
             if (!all_ok(wait(G_D3, n))) break;
             tc_fence_after();
-            out(lj, 1.f, 0u, g * VH, VH, [&](int c, const float (&y)[16]) {
-                if (live) put16(static_cast<__nv_bfloat16 *>(a.dv) + tok * a.ldv + k.h * a.Dv + c, a.Dv - c, y);
+            out(lj, 0u, g * VH, VH, [&](int c, const float (&y)[16]) {
+                stage(V, c, y);
             }, static_cast<float *>(nullptr));
             tc_fence_before();
             fence_proxy_async_smem();
+            arrive(G_OV);
             arrive(G_DONE);
         }
     }
@@ -1181,7 +1229,10 @@ cudaError_t run_states(const LinArgs &a, const LinSplit &sp, unsigned *status, c
     const bool ok = REV ? map_tokens(&m.x, a.q, a.Dk, a.Hk, a.T, a.B, a.ldq, SH) && map_tokens(&m.y, a.go, a.Dv, a.H, a.T, a.B, a.ldo, SH)
                         : map_tokens(&m.x, a.k, a.Dk, a.Hk, a.T, a.B, a.ldk, SH) && map_tokens(&m.y, a.v, a.Dv, a.H, a.T, a.B, a.ldv, SH);
     if (!ok) return cudaErrorInvalidValue;
-    constexpr size_t smem = state_smem<KW, VW>();
+    if (KEEP && (!map_states(&m.hi, REV ? a.zhi : a.shi, a.Dv, a.Dk, a.B * a.H * a.NC, KW) ||
+                 !map_states(&m.lo, REV ? a.zlo : a.slo, a.Dv, a.Dk, a.B * a.H * a.NC, KW)))
+        return cudaErrorInvalidValue;
+    constexpr size_t smem = state_smem<KW, VW, KEEP>();
     LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_state<KW, VW, REV, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
     ProfScope ps(K_LIN_STATE, st);
     k_lin_tc_state<KW, VW, REV, KEEP><<<unsigned(a.B * a.H * sp.nseg), TC_BLOCK, smem, st>>>(m, a, sp.nseg, sp.cps, status);
@@ -1190,7 +1241,8 @@ cudaError_t run_states(const LinArgs &a, const LinSplit &sp, unsigned *status, c
 
 template <int KW, int VW>
 cudaError_t run_fwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cudaStream_t st) {
-    static_assert(fwd_smem<128, 128>() <= 232448 && state_smem<128, 128>() <= 232448, "shared memory of an SM");
+    static_assert(fwd_smem<128, 128>() <= 232448 && state_smem<128, 128, false>() <= 232448 &&
+                      state_smem<128, 128, true>() <= 232448, "shared memory of an SM");
     FwdMaps m;
     if (!map_tokens(&m.q, a.q, a.Dk, a.Hk, a.T, a.B, a.ldq) || !map_tokens(&m.k, a.k, a.Dk, a.Hk, a.T, a.B, a.ldk) ||
         !map_tokens(&m.v, a.v, a.Dv, a.H, a.T, a.B, a.ldv) || !map_tokens(&m.o, a.o, a.Dv, a.H, a.T, a.B, a.ldo))
@@ -1216,7 +1268,8 @@ cudaError_t run_bwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cuda
     if (!map_tokens(&m.q, a.q, a.Dk, a.Hk, a.T, a.B, a.ldq) || !map_tokens(&m.k, a.k, a.Dk, a.Hk, a.T, a.B, a.ldk) ||
         !map_tokens(&m.v, a.v, a.Dv, a.H, a.T, a.B, a.ldv) || !map_tokens(&m.w, a.go, a.Dv, a.H, a.T, a.B, a.ldo) ||
         !map_states(&m.shi, a.shi, a.Dv, a.Dk, n, KW) || !map_states(&m.slo, a.slo, a.Dv, a.Dk, n, KW) ||
-        !map_states(&m.zhi, a.zhi, a.Dv, a.Dk, n, KW) || !map_states(&m.zlo, a.zlo, a.Dv, a.Dk, n, KW))
+        (!a.pq && (!map_tokens(&m.dq, a.dq, a.Dk, a.Hk, a.T, a.B, a.ldq) || !map_tokens(&m.dk, a.dk, a.Dk, a.Hk, a.T, a.B, a.ldk))) ||
+        !map_tokens(&m.dv, a.dv, a.Dv, a.H, a.T, a.B, a.ldv) || !map_states(&m.zhi, a.zhi, a.Dv, a.Dk, n, KW) || !map_states(&m.zlo, a.zlo, a.Dv, a.Dk, n, KW))
         return cudaErrorInvalidValue;
     // the states around every chunk: by segments where the heads alone would leave SMs idle
     LinArgs b = a;

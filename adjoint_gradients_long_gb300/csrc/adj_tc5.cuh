@@ -152,6 +152,12 @@ __device__ __forceinline__ void store4(const CUtensorMap *m, int x, int head, in
                  "r"(x), "r"(head), "r"(t), "r"(b), "r"(src)
                  : "memory");
 }
+__device__ __forceinline__ void store3(const CUtensorMap *m, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
 __device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
