@@ -149,33 +149,35 @@ __global__ __launch_bounds__(256) void k_lin_chunk_state(const LinArgs a) {
             const int d = ty + 16 * r, e = tx + 16 * c;
             if (d < a.Dk && e < a.Dv) S[d * a.Dv + e] = acc[r][c];
         }
-    if (threadIdx.x == 0) a.tot[(at.b * a.H + at.h) * a.NC + at.n] = D.total();
+    if (threadIdx.x == 0) (REV ? a.dtot : a.tot)[(at.b * a.H + at.h) * a.NC + at.n] = D.total();
 }
 
-// Pass 2.  Every chunk's contribution is replaced by the state that enters it (REV: by the
+// Pass 2.  Every chunk's contribution is replaced by the state that enters it (in reverse: by the
 // adjoint state that its exit receives); one thread carries four elements through the chunks.
-template <bool REV>
-__global__ __launch_bounds__(128) void k_lin_scan(const LinArgs a, int64_t NC) {
-    const int64_t n4 = int64_t(a.Dk) * a.Dv / 4, blocks = (n4 + 127) / 128, bh = blockIdx.x / blocks;
-    const int64_t i = (blockIdx.x - bh * blocks) * 128 + threadIdx.x;
+// rev0: the direction of the first half of the grid, the other half (if any) goes the other way.
+__global__ __launch_bounds__(128) void k_lin_scan(const LinArgs a, int64_t NC, int64_t half, bool rev0) {
+    const bool rev = blockIdx.x < half ? rev0 : !rev0;
+    const int64_t block = blockIdx.x < half ? blockIdx.x : blockIdx.x - half;
+    const int64_t n4 = int64_t(a.Dk) * a.Dv / 4, blocks = (n4 + 127) / 128, bh = block / blocks;
+    const int64_t i = (block - bh * blocks) * 128 + threadIdx.x;
     if (i >= n4) return;
-    const float *init = REV ? a.ds1 : a.s0;
-    float *fin = REV ? a.ds0 : a.s1;
+    const float *init = rev ? a.ds1 : a.s0;
+    float *fin = rev ? a.ds0 : a.s1;
     float4 c = init ? reinterpret_cast<const float4 *>(init)[bh * n4 + i] : f4(0.f);
-    float4 *S = reinterpret_cast<float4 *>(REV ? a.dS : a.S) + bh * NC * n4 + i;
-    const float *tot = a.tot + bh * NC;
+    float4 *S = reinterpret_cast<float4 *>(rev ? a.dS : a.S) + bh * NC * n4 + i;
+    const float *tot = (rev ? a.dtot : a.tot) + bh * NC;
     constexpr int U = 8;        // loads in flight
     for (int64_t m = 0; m < NC; m += U) {
         float4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (m + u < NC) x[u] = S[(REV ? NC - 1 - m - u : m + u) * n4];
+            if (m + u < NC) x[u] = S[(rev ? NC - 1 - m - u : m + u) * n4];
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (m + u < NC) {
-                const int64_t n = REV ? NC - 1 - m - u : m + u;
+                const int64_t n = rev ? NC - 1 - m - u : m + u;
                 S[n * n4] = c;
-                c = tot[n] == 0.f ? x[u] : fma4(f4(tot[n]), c, x[u]);   // a new start drops it whatever it holds
+                c = tot[n] == 0.f ? x[u] : fma4(f4(tot[n]), c, x[u]);    // a new start drops it whatever it holds
             }
     }
     if (fin) reinterpret_cast<float4 *>(fin)[bh * n4 + i] = c;
@@ -512,7 +514,7 @@ cudaError_t states(const LinArgs &a, cudaStream_t st) {
         k_lin_chunk_state<T, REV><<<grid, 256, SM_STATE, st>>>(a);
         LIN_CUDA(cudaGetLastError());
     }
-    return launch_lin_scan(a, a.NC, REV, st);
+    return launch_lin_scan(a, a.NC, REV ? 2 : 1, st);
 }
 
 template <class T>
@@ -547,11 +549,10 @@ inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 int64_t lin_chunks(int64_t T, bool) { return cdiv(T, LC); }
 
-cudaError_t launch_lin_scan(const LinArgs &a, int64_t n, bool rev, cudaStream_t st) {
+cudaError_t launch_lin_scan(const LinArgs &a, int64_t n, int dirs, cudaStream_t st) {
     ProfScope ps(K_LIN_SCAN, st);
-    const unsigned grid = unsigned(cdiv(int64_t(a.Dk) * a.Dv, 512) * a.B * a.H);
-    if (rev) k_lin_scan<true><<<grid, 128, 0, st>>>(a, n);
-    else k_lin_scan<false><<<grid, 128, 0, st>>>(a, n);
+    const int64_t half = cdiv(int64_t(a.Dk) * a.Dv, 512) * a.B * a.H;
+    k_lin_scan<<<unsigned(half * (dirs == 3 ? 2 : 1)), 128, 0, st>>>(a, n, half, dirs == 2);
     return cudaGetLastError();
 }
 
@@ -564,14 +565,15 @@ static size_t carve(LinArgs &a, bool bwd, bool bf16, char *base) {
     };
     auto floats = [&](size_t n) { return reinterpret_cast<float *>(take(n * 4)); };
     auto halves = [&](size_t n) { return reinterpret_cast<__nv_bfloat16 *>(take(n * 2)); };
-    const int64_t heads = a.B * a.H, n = heads * (bf16 ? lin_split(a).nseg : a.NC);
+    const int64_t heads = a.B * a.H, n = heads * (bf16 ? lin_split(a, bwd).nseg : a.NC);
     const size_t dd = size_t(a.Dk) * a.Dv;
     a.S = floats(n * dd);
     a.tot = floats(n);
-    a.dS = a.pq = a.pk = nullptr;
+    a.dS = a.dtot = a.pq = a.pk = nullptr;
     a.shi = a.slo = a.zhi = a.zlo = nullptr;
     if (bwd) {
         a.dS = floats(n * dd);
+        a.dtot = floats(n);
         if (bf16) {
             const size_t all = size_t(heads) * cdiv(a.T, 128) * dd;
             a.shi = halves(all);
@@ -594,11 +596,11 @@ size_t lin_ws_bytes(const LinArgs &a, bool bwd, bool bf16) {
 void lin_ws_carve(LinArgs &a, bool bwd, bool bf16, void *base) { carve(a, bwd, bf16, static_cast<char *>(base)); }
 
 cudaError_t launch_lin_fwd(const LinArgs &a, bool bf16, unsigned *status, cudaStream_t st) {
-    if (a.NC == 0) return launch_lin_scan(a, 0, false, st);      // s1 = s0
+    if (a.NC == 0) return launch_lin_scan(a, 0, 1, st);      // s1 = s0
     return bf16 ? launch_lin_tc_fwd(a, status, st) : fwd<float>(a, st);
 }
 cudaError_t launch_lin_bwd(const LinArgs &a, bool bf16, unsigned *status, cudaStream_t st) {
-    if (a.NC == 0) return launch_lin_scan(a, 0, true, st);       // ds0 = ds1
+    if (a.NC == 0) return launch_lin_scan(a, 0, 2, st);       // ds0 = ds1
     LIN_CUDA(bf16 ? launch_lin_tc_bwd(a, status, st) : bwd_f32(a, st));
     if (!a.pq) return cudaSuccess;
     return bf16 ? share<__nv_bfloat16>(a, st) : share<float>(a, st);

@@ -15,7 +15,7 @@ struct LinArgs {
     void *o, *dq, *dk, *dv;
     float *s1, *dg, *ds0;
     float *S, *dS;              // [B,H,NC,Dk,Dv]: the states entering / adjoint states leaving each chunk
-    float *tot;                 // [B,H,NC]: the decay over each chunk
+    float *tot, *dtot;          // [B,H,NC]: the decay over each chunk (dtot: beside dS, where both are in flight)
     // bf16: S and dS of every chunk as sums of two bf16 instead; S, dS, tot are then those of segments
     __nv_bfloat16 *shi, *slo, *zhi, *zlo;
     float *pq, *pk;             // Hk < H: dq, dk of every head [B,T,H,Dk] fp32, summed afterwards
@@ -104,12 +104,13 @@ cudaError_t launch_lin_bwd(const LinArgs &a, bool bf16, unsigned *status, cudaSt
 struct LinSplit {
     int nseg, cps;
 };
-LinSplit lin_split(const LinArgs &a);
+LinSplit lin_split(const LinArgs &a, bool bwd);
 cudaError_t launch_lin_tc_fwd(const LinArgs &a, unsigned *status, cudaStream_t st);
 // the tensor-core backward pass but for the sum over shared heads
 cudaError_t launch_lin_tc_bwd(const LinArgs &a, unsigned *status, cudaStream_t st);
-// every entry of S (rev: dS) [B,H,n,Dk,Dv] becomes the state before it (rev: after it)
-cudaError_t launch_lin_scan(const LinArgs &a, int64_t n, bool rev, cudaStream_t st);
+// Every entry of S [B,H,n,Dk,Dv] becomes the state before it (dirs & 1), every entry of dS the
+// adjoint state after it (dirs & 2).
+cudaError_t launch_lin_scan(const LinArgs &a, int64_t n, int dirs, cudaStream_t st);
 cudaError_t launch_lin_step(const LinArgs &a, bool bf16, float *state, int64_t n_slots, const int32_t *slots,
                             cudaStream_t st);
 

@@ -157,8 +157,11 @@ struct alignas(16) ChunkDecay {
 struct FwdMaps {
     CUtensorMap q, k, v, o;
 };
-struct StateMaps {
+struct StateMaps {              // of one direction
     CUtensorMap x, y, hi, lo;   // hi, lo: the kept states
+};
+struct BothMaps {
+    StateMaps dir[2];
 };
 
 struct Wait {
@@ -261,13 +264,13 @@ __device__ __forceinline__ void state_update(float (&S)[VH], uint32_t u, float t
 
 __device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(~0u, ok); }
 
-// A segment of one head: blockIdx.x = (b * H + h) * nseg + seg, chunks [n0, n1).
+// A segment of one head: block (b * H + h) * nseg + seg, chunks [n0, n1).
 struct Seg {
     int64_t bh, b, h, hk, n0, n1;
     int seg;
-    __device__ Seg(const LinArgs &a, int nseg, int cps) {
-        bh = blockIdx.x / nseg;
-        seg = int(blockIdx.x - bh * nseg);
+    __device__ Seg(const LinArgs &a, int nseg, int cps, int64_t block) {
+        bh = block / nseg;
+        seg = int(block - bh * nseg);
         b = bh / a.H;
         h = bh - b * a.H;
         hk = h / (a.H / a.Hk);
@@ -324,7 +327,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
     ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + 2 * STAGE + TILE_K);
     auto *ctl = reinterpret_cast<Ctl<F_COUNT> *>(dec + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Seg seg(a, nseg, cps);
+    const Seg seg(a, nseg, cps, blockIdx.x);
     const int64_t N = seg.n1 - seg.n0;
 
     if (threadIdx.x == 0) {
@@ -540,7 +543,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
 
 // ---------------------------------------------------------------- segment states
 // The state that a segment's own tokens leave (zero before it): S[blockIdx.x], and the decay
-// over it.  REV: the adjoint state from q and scale go, walked from the last chunk back.
+// over it; in the second half of a grid for both directions, the adjoint state from q and scale go,
+// walked from the last chunk back.
 //
 // A ring of three stages of half a chunk (64 tokens).  The warps multiply x by its decays to the
 // chunk's end (two more tiles of a stage take the second and third part), the products of a
@@ -560,9 +564,9 @@ constexpr size_t state_smem() {
 // [B,H,NC,Dk,Dv], the operand of the backward pass.  The parts leave one after the other through
 // one tile, the second while the next chunk is being scaled; with a tile each and a ring of two
 // stages the walk waited for its copies in (86 us against @@ us for 64 chunks of 32 heads).
-template <int KW, int VW, bool REV, bool KEEP>
-__global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_constant__ StateMaps m, const LinArgs a, int nseg,
-                                                              int cps, unsigned *status) {
+template <int KW, int VW, bool KEEP>
+__global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_constant__ BothMaps maps, const LinArgs a,
+                                                              int nseg, int cps, unsigned *status) {
     constexpr uint32_t TILE_K = KW * SH * 2, TILE_V = VW * SH * 2, STAGE = 3 * TILE_K + TILE_V, PANEL = SH * 128;
     constexpr uint32_t TILE_S = KW * VW * 2, SPANEL = KW * 128;
     constexpr int VH = VW / CG;
@@ -571,11 +575,14 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
     ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + RING * STAGE + (KEEP ? TILE_S : 0));
     auto *ctl = reinterpret_cast<Ctl<S_COUNT> *>(dec + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Seg seg(a, nseg, cps);
+    const int64_t per = a.B * a.H * nseg, block = blockIdx.x % per;
+    const bool rev = blockIdx.x >= per;
+    const StateMaps &m = maps.dir[rev];
+    const Seg seg(a, nseg, cps, block);
     const int64_t N = seg.n1 - seg.n0;
-    auto chunk = [&](int64_t n) { return REV ? seg.n1 - 1 - n : seg.n0 + n; };
+    auto chunk = [&](int64_t n) { return rev ? seg.n1 - 1 - n : seg.n0 + n; };
     // no segment reads what the last one leaves: only the final state does
-    if (!KEEP && seg.seg == (REV ? 0 : nseg - 1) && !(REV ? a.ds0 : a.s1)) return;
+    if (!KEEP && seg.seg == (rev ? 0 : nseg - 1) && !(rev ? a.ds0 : a.s1)) return;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S_COUNT; ++i)
@@ -628,7 +635,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
             cuts += dec[s].n_cut;
             if (lane == 0) mbar_arrive(bar(S_DEC + s));
         }
-        if (!KEEP && lane == 0) a.tot[blockIdx.x] = cuts ? 0.f : fast_exp2(sum.value());
+        if (!KEEP && lane == 0) (rev ? a.dtot : a.tot)[block] = cuts ? 0.f : fast_exp2(sum.value());
     } else if (warp == W_OUT) {
         if (KEEP && lane == 0) {
             for (int64_t k = 0; k < 2 * N; ++k) {
@@ -674,8 +681,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
         const uint32_t lanes = tmem + (uint32_t(wq * 32) << 16);
         float S[VH];
         const int64_t dd = int64_t(a.Dk) * a.Dv;
-        const float *init = REV ? a.ds1 : a.s0;
-        load_part<VH>(S, !KEEP ? nullptr : nseg > 1 ? (REV ? a.dS : a.S) + int64_t(blockIdx.x) * dd : init ? init + seg.bh * dd : nullptr,
+        const float *init = rev ? a.ds1 : a.s0;
+        load_part<VH>(S, !KEEP ? nullptr : nseg > 1 ? (rev ? a.dS : a.S) + block * dd : init ? init + seg.bh * dd : nullptr,
                       i, c0, a);
         // the first (k even) or second part of the state; k counts the parts
         auto keep = [&](int64_t k) {
@@ -718,7 +725,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
                 if (!(ok = all_ok(wait(S_FULL + s, turn)))) break;
                 const uint32_t at = base + s * STAGE;
                 scale_row(at, at + TILE_K, at + 2 * TILE_K, PANEL, r, q * UQ, (q + 1) * UQ,
-                          REV ? dec[e].first(h * SH + r) * a.scale : dec[e].to_end(h * SH + r));
+                          rev ? dec[e].first(h * SH + r) * a.scale : dec[e].to_end(h * SH + r));
                 fence_proxy_async_smem();
                 arrive(S_K + s);
                 if (++s == RING) { s = 0; ++turn; }
@@ -732,8 +739,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
             tot = now;
         }
         if (ok && keep(2 * N - 1)) fold(N - 1, tot);
-        if (!KEEP) store_part<VH>(S, (REV ? a.dS : a.S) + int64_t(blockIdx.x) * dd, i, c0, a);
-        else if (REV && a.ds0 && seg.seg == 0) store_part<VH>(S, a.ds0 + seg.bh * dd, i, c0, a);
+        if (!KEEP) store_part<VH>(S, (rev ? a.dS : a.S) + block * dd, i, c0, a);
+        else if (rev && a.ds0 && seg.seg == 0) store_part<VH>(S, a.ds0 + seg.bh * dd, i, c0, a);
     }
     tc_fence_before();
     __syncthreads();
@@ -1223,19 +1230,22 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
         if (e_ != cudaSuccess) return e_;     \
     } while (0)
 
-template <int KW, int VW, bool REV, bool KEEP>
-cudaError_t run_states(const LinArgs &a, const LinSplit &sp, unsigned *status, cudaStream_t st) {
-    StateMaps m;
-    const bool ok = REV ? map_tokens(&m.x, a.q, a.Dk, a.Hk, a.T, a.B, a.ldq, SH) && map_tokens(&m.y, a.go, a.Dv, a.H, a.T, a.B, a.ldo, SH)
-                        : map_tokens(&m.x, a.k, a.Dk, a.Hk, a.T, a.B, a.ldk, SH) && map_tokens(&m.y, a.v, a.Dv, a.H, a.T, a.B, a.ldv, SH);
+// dirs: 1 forward, 2 both
+template <int KW, int VW, bool KEEP>
+cudaError_t run_states(const LinArgs &a, const LinSplit &sp, int dirs, unsigned *status, cudaStream_t st) {
+    BothMaps m;
+    const int64_t n = a.B * a.H * a.NC;
+    bool ok = map_tokens(&m.dir[0].x, a.k, a.Dk, a.Hk, a.T, a.B, a.ldk, SH) && map_tokens(&m.dir[0].y, a.v, a.Dv, a.H, a.T, a.B, a.ldv, SH);
+    if (dirs == 2)
+        ok = ok && map_tokens(&m.dir[1].x, a.q, a.Dk, a.Hk, a.T, a.B, a.ldq, SH) && map_tokens(&m.dir[1].y, a.go, a.Dv, a.H, a.T, a.B, a.ldo, SH);
+    if (KEEP)
+        ok = ok && map_states(&m.dir[0].hi, a.shi, a.Dv, a.Dk, n, KW) && map_states(&m.dir[0].lo, a.slo, a.Dv, a.Dk, n, KW) &&
+             map_states(&m.dir[1].hi, a.zhi, a.Dv, a.Dk, n, KW) && map_states(&m.dir[1].lo, a.zlo, a.Dv, a.Dk, n, KW);
     if (!ok) return cudaErrorInvalidValue;
-    if (KEEP && (!map_states(&m.hi, REV ? a.zhi : a.shi, a.Dv, a.Dk, a.B * a.H * a.NC, KW) ||
-                 !map_states(&m.lo, REV ? a.zlo : a.slo, a.Dv, a.Dk, a.B * a.H * a.NC, KW)))
-        return cudaErrorInvalidValue;
     constexpr size_t smem = state_smem<KW, VW, KEEP>();
-    LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_state<KW, VW, REV, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+    LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_state<KW, VW, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
     ProfScope ps(K_LIN_STATE, st);
-    k_lin_tc_state<KW, VW, REV, KEEP><<<unsigned(a.B * a.H * sp.nseg), TC_BLOCK, smem, st>>>(m, a, sp.nseg, sp.cps, status);
+    k_lin_tc_state<KW, VW, KEEP><<<unsigned(a.B * a.H * sp.nseg * dirs), TC_BLOCK, smem, st>>>(m, a, sp.nseg, sp.cps, status);
     return cudaGetLastError();
 }
 
@@ -1248,8 +1258,8 @@ cudaError_t run_fwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cuda
         !map_tokens(&m.v, a.v, a.Dv, a.H, a.T, a.B, a.ldv) || !map_tokens(&m.o, a.o, a.Dv, a.H, a.T, a.B, a.ldo))
         return cudaErrorInvalidValue;
     if (sp.nseg > 1) {
-        LIN_CUDA((run_states<KW, VW, false, false>(a, sp, status, st)));
-        LIN_CUDA(launch_lin_scan(a, sp.nseg, false, st));
+        LIN_CUDA((run_states<KW, VW, false>(a, sp, 1, status, st)));
+        LIN_CUDA(launch_lin_scan(a, sp.nseg, 1, st));
     }
     constexpr size_t smem = fwd_smem<KW, VW>();
     LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_fwd<KW, VW>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
@@ -1275,15 +1285,10 @@ cudaError_t run_bwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cuda
     LinArgs b = a;
     b.s1 = b.ds0 = nullptr;
     if (sp.nseg > 1) {
-        LIN_CUDA((run_states<KW, VW, false, false>(b, sp, status, st)));
-        LIN_CUDA(launch_lin_scan(b, sp.nseg, false, st));
+        LIN_CUDA((run_states<KW, VW, false>(b, sp, 2, status, st)));
+        LIN_CUDA(launch_lin_scan(b, sp.nseg, 3, st));
     }
-    LIN_CUDA((run_states<KW, VW, false, true>(a, sp, status, st)));
-    if (sp.nseg > 1) {
-        LIN_CUDA((run_states<KW, VW, true, false>(b, sp, status, st)));
-        LIN_CUDA(launch_lin_scan(b, sp.nseg, true, st));
-    }
-    LIN_CUDA((run_states<KW, VW, true, true>(a, sp, status, st)));
+    LIN_CUDA((run_states<KW, VW, true>(a, sp, 2, status, st)));
     constexpr size_t smem = grad_smem<KW, VW>();
     LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_grad<KW, VW>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
     ProfScope ps(K_LIN_GRAD, st);
@@ -1293,8 +1298,9 @@ cudaError_t run_bwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cuda
 
 }  // namespace
 
-LinSplit lin_split(const LinArgs &a) {
-    const int64_t heads = a.B * a.H, NC = cdiv(a.T, TCH);
+LinSplit lin_split(const LinArgs &a, bool bwd) {
+    // the backward pass walks both directions side by side
+    const int64_t heads = a.B * a.H * (bwd ? 2 : 1), NC = cdiv(a.T, TCH);
     LinSplit s{1, int(NC)};
     // One block an SM: split the tokens when that fills SMs that would stay idle; a segment is at
     // least four chunks, below which its start costs more than it saves.
@@ -1311,7 +1317,7 @@ LinSplit lin_split(const LinArgs &a) {
 cudaError_t launch_lin_tc_fwd(const LinArgs &args, unsigned *status, cudaStream_t st) {
     LinArgs a = args;
     a.NC = cdiv(a.T, TCH);
-    const LinSplit sp = lin_split(a);
+    const LinSplit sp = lin_split(a, false);
     if (a.Dk <= 64) return a.Dv <= 64 ? run_fwd<64, 64>(a, sp, status, st) : run_fwd<64, 128>(a, sp, status, st);
     return a.Dv <= 64 ? run_fwd<128, 64>(a, sp, status, st) : run_fwd<128, 128>(a, sp, status, st);
 }
@@ -1319,7 +1325,7 @@ cudaError_t launch_lin_tc_fwd(const LinArgs &args, unsigned *status, cudaStream_
 cudaError_t launch_lin_tc_bwd(const LinArgs &args, unsigned *status, cudaStream_t st) {
     LinArgs a = args;
     a.NC = cdiv(a.T, TCH);
-    const LinSplit sp = lin_split(a);
+    const LinSplit sp = lin_split(a, true);
     if (a.Dk <= 64) return a.Dv <= 64 ? run_bwd<64, 64>(a, sp, status, st) : run_bwd<64, 128>(a, sp, status, st);
     return a.Dv <= 64 ? run_bwd<128, 64>(a, sp, status, st) : run_bwd<128, 128>(a, sp, status, st);
 }
