@@ -24,6 +24,19 @@ struct Vec;
 template <>
 struct Vec<float> {
     static constexpr int N = 4;
+    static constexpr uint32_t LOW = 0xFF800000u;         // minus infinity, N of them
+    static __device__ __forceinline__ float largest(uint4 u) {
+        return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+    }
+    // values below -1e38 as -1e38 (NaN stays)
+    static __device__ __forceinline__ uint32_t floor1(uint32_t w) {
+        float y;
+        asm("max.NaN.f32 %0, %1, 0fFE967699;" : "=f"(y) : "f"(__uint_as_float(w)));
+        return __float_as_uint(y);
+    }
+    static __device__ __forceinline__ uint4 floored(uint4 u) {
+        return make_uint4(floor1(u.x), floor1(u.y), floor1(u.z), floor1(u.w));
+    }
     static __device__ __forceinline__ void unpack(uint4 u, float (&x)[4]) {
         x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y); x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
     }
@@ -36,6 +49,24 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
+    static constexpr uint32_t LOW = 0xFF80FF80u;
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+    static __device__ __forceinline__ float largest(uint4 u) {
+        const uint32_t m = max2(max2(u.x, u.y), max2(u.z, u.w));
+        return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ uint32_t floor2(uint32_t w) {
+        uint32_t d;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(0xFE96FE96u));
+        return d;
+    }
+    static __device__ __forceinline__ uint4 floored(uint4 u) {
+        return make_uint4(floor2(u.x), floor2(u.y), floor2(u.z), floor2(u.w));
+    }
     static __device__ __forceinline__ void unpack(uint4 u, float (&x)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -94,14 +125,24 @@ struct Ragged {
 };
 
 // ---------------------------------------------------------------- log probabilities
-constexpr int LPT = 512;        // threads of a row
-constexpr int CAND = 1024;      // candidates for the top list
+// One pass over the row with the running maximum, sum and entropy sum of its softmax; bound by
+// the row's bytes.  A row is cut over a cluster of 1 to 8 blocks: when it is too long for one
+// block's shared memory (the gradient's second pass reads the row from there), and when there are
+// too few rows to fill the SMs.  The blocks' statistics and top lists are joined through
+// distributed shared memory, in rank order.
+constexpr int LPT = 512;        // threads of a block
+constexpr int CAND = 512;       // candidates for the top list
+constexpr int LPU = 4;          // vectors in flight a thread
+constexpr int64_t ROW_KEEP = 72 * 1024;     // bytes of a row that a block keeps: three blocks an SM
 
 // Order of the top list as unsigned integers: NaN above +inf, the zeros equal.
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (x != x) return 0xFFFFFFFFu;
     const uint32_t u = __float_as_uint(x + 0.f);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return k == 0xFFFFFFFFu ? NAN : __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 // (key, index) as one number: larger is better, among equal keys the lower index
 __device__ __forceinline__ uint64_t rank_key(uint32_t key, uint32_t idx) { return (uint64_t(key) << 32) | uint32_t(~idx); }
@@ -112,13 +153,14 @@ struct Stat {
     float m, s, t;
 };
 // Distances from m in powers of two.  One multiply-add each, on the rounded m log2 e, which
-// every use of the same m shares; beyond 2^127 that product would overflow and the difference is
-// taken first.  A row with nothing but masked values is measured from zero.
+// every use of the same m shares; near the ends of the range (far) that product would overflow and
+// the difference is taken first.  A row with nothing but masked values is measured from zero.
 struct Ref {
     float m, m2;
     bool far;
-    __device__ __forceinline__ explicit Ref(float m_) : m(m_ == -INFINITY ? 0.f : m_), m2(m * LOG2E), far(fabsf(m) > 1.7e38f) {}
-    __device__ __forceinline__ float operator()(float x) const { return far ? (x - m) * LOG2E : fmaf(x, LOG2E, -m2); }
+    __device__ __forceinline__ explicit Ref(float m_) : m(m_ == -INFINITY ? 0.f : m_), m2(m * LOG2E), far(fabsf(m) > 9e37f) {}
+    template <bool FAR>
+    __device__ __forceinline__ float at(float x) const { return FAR ? (x - m) * LOG2E : fmaf(x, LOG2E, -m2); }
     __device__ __forceinline__ float from(const Ref &o) const { return far || o.far ? (o.m - m) * LOG2E : o.m2 - m2; }
     // log(sum) of a sum s = 2^l2s measured from m, and a value's logarithm less that
     __device__ __forceinline__ float natural(float l2s) const { return far ? m + l2s * LN2 : (m2 + l2s) * LN2; }
@@ -141,145 +183,301 @@ __device__ __forceinline__ Stat join(Stat a, Stat b) {
     return o;
 }
 
-template <class T, bool GRAD>
-__global__ __launch_bounds__(LPT) void k_logprob(const LogprobArgs a) {
-    constexpr int N = Vec<T>::N;
-    __shared__ Stat red[LPT / 32];
-    __shared__ Stat all;
-    __shared__ uint64_t cand[CAND];
-    __shared__ int n_cand;
-    const int tid = threadIdx.x;
-    const int64_t row = blockIdx.x;
-    const Ragged<T> x(const_cast<T *>(static_cast<const T *>(a.logits)) + row * a.ld, a.V);
-    const int64_t nv = x.vectors();
+__device__ __forceinline__ uint32_t rank_in_cluster() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void meet(int blocks) {
+    if (blocks == 1) __syncthreads();
+    else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// another block's copy of an object in shared memory
+template <class X>
+__device__ __forceinline__ X peer(const X *own, uint32_t rank) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(own)), b;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(a), "r"(rank));
+    union {
+        X x;
+        uint32_t w[sizeof(X) / 4];
+    } u;
+#pragma unroll
+    for (int i = 0; i < int(sizeof(X) / 4); ++i)
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(u.w[i]) : "r"(b + 4 * i) : "memory");
+    return u.x;
+}
 
-    Stat st{-INFINITY, 0.f, 0.f};
-    for (int64_t i = tid; i < nv; i += LPT) {
-        float v[N];
-        x.load(i, v, -INFINITY);
-        float m = v[0];
+// The statistics of a whole warp, in every lane: the largest maximum, then plain sums.
+__device__ __forceinline__ Stat warp_join(Stat x) {
+    float m = x.m;
 #pragma unroll
-        for (int e = 1; e < N; ++e) m = fmaxf(m, v[e]);
-        if (m > st.m) {
-            if (st.s != 0.f) {
-                const float d = Ref(m).from(Ref(st.m)), f = ex2(d);
-                st.t = f == 0.f ? 0.f : f * fmaf(st.s, d, st.t);
-                st.s *= f;
-            }
-            st.m = m;
-        }
-        const Ref r(st.m);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float d = r(v[e]), p = ex2(d);
-            st.s += p;
-            if (p != 0.f) st.t = fmaf(p, d, st.t);       // a masked value has d = -inf
-        }
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    if (x.s != 0.f) {
+        const float d = Ref(m).from(Ref(x.m)), f = ex2(d);
+        x.t = f == 0.f ? 0.f : f * fmaf(x.s, d, x.t);
+        x.s *= f;
     }
-    const float own_max = st.m;
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
-        Stat o;
-        o.m = __shfl_xor_sync(~0u, st.m, d);
-        o.s = __shfl_xor_sync(~0u, st.s, d);
-        o.t = __shfl_xor_sync(~0u, st.t, d);
-        st = join(st, o);
+        x.s += __shfl_xor_sync(~0u, x.s, d);
+        x.t += __shfl_xor_sync(~0u, x.t, d);
     }
+    x.m = m;
+    return x;
+}
+
+// 2^distance times the distance is zero for a masked value, but minus infinity times zero would
+// be NaN.  Values are raised to -1e38 first (half an instruction each in bf16); where the largest
+// itself lies that low (FAR) the distance is held to -200, below which its power of two is zero.
+template <class T, bool FAR>
+__device__ __forceinline__ void distances(uint4 raw, const Ref &r, float (&d)[Vec<T>::N], float (&p)[Vec<T>::N]) {
+    Vec<T>::unpack(FAR ? raw : Vec<T>::floored(raw), d);
+#pragma unroll
+    for (int e = 0; e < Vec<T>::N; ++e) {
+        d[e] = r.at<FAR>(d[e]);
+        p[e] = ex2(d[e]);
+        if (FAR) d[e] = fmaxf(d[e], -200.f);
+    }
+}
+
+template <class T, bool FAR, int U>
+__device__ __forceinline__ void add_up(Stat &st, const uint4 (&raw)[U]) {
+    constexpr int N = Vec<T>::N;
+    const Ref r(st.m);
+    float s[2] = {0.f, 0.f}, t[2] = {0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float d[N], p[N];
+        distances<T, FAR>(raw[u], r, d, p);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            s[e & 1] += p[e];
+            t[e & 1] = fmaf(p[e], d[e], t[e & 1]);
+        }
+    }
+    st.s += s[0] + s[1];
+    st.t += t[0] + t[1];
+}
+
+template <class T, int U>
+__device__ __forceinline__ void take(Stat &st, const uint4 (&raw)[U]) {
+    float m = Vec<T>::largest(raw[0]);
+#pragma unroll
+    for (int u = 1; u < U; ++u) m = fmaxf(m, Vec<T>::largest(raw[u]));
+    if (m > st.m) {
+        if (st.s != 0.f) {
+            const float d = Ref(m).from(Ref(st.m)), f = ex2(d);
+            st.t = f == 0.f ? 0.f : f * fmaf(st.s, d, st.t);
+            st.s *= f;
+        }
+        st.m = m;
+    }
+    if (Ref(st.m).far) add_up<T, true>(st, raw);
+    else add_up<T, false>(st, raw);
+}
+
+// g = p (c0 + c1 d) of one vector, p = 2^d
+template <class T, bool FAR>
+__device__ __forceinline__ uint4 slope(uint4 raw, const Ref &ref, float c0, float c1) {
+    float d[Vec<T>::N], p[Vec<T>::N];
+    distances<T, FAR>(raw, ref, d, p);
+#pragma unroll
+    for (int e = 0; e < Vec<T>::N; ++e) d[e] = p[e] * fmaf(c1, d[e], c0);
+    return Vec<T>::pack(d);
+}
+
+template <class T, bool GRAD>
+__global__ __launch_bounds__(LPT, 3) void k_logprob(const LogprobArgs a) {
+    constexpr int N = Vec<T>::N;
+    extern __shared__ uint4 kept[];                      // GRAD: this block's part of the row
+    __shared__ Stat red[LPT / 32], mine;
+    __shared__ uint64_t cand[CAND], best_of[ADJ_LOGPROB_MAX_TOP];
+    __shared__ uint32_t keys[LPT], bound_;
+    __shared__ int n_cand;
+    const int tid = threadIdx.x, blocks = a.blocks;
+    const uint32_t rank = blocks > 1 ? rank_in_cluster() : 0u;
+    const int64_t row = blockIdx.x / blocks;
+    const Ragged<T> x(const_cast<T *>(static_cast<const T *>(a.logits)) + row * a.ld, a.V);
+    // this block's vectors v0 .. v0 + nv of the row; the first and the last of a row may lie partly
+    // outside it and are fetched value by value
+    const int all_v = int(x.vectors()), per = (all_v + blocks - 1) / blocks, v0 = int(rank) * per, nv = max(0, min(all_v - v0, per));
+    const bool odd_first = nv > 0 && !x.whole(v0), odd_last = nv > 1 && !x.whole(v0 + nv - 1);
+    const int w0 = odd_first ? 1 : 0, w1 = nv - (odd_last ? 1 : 0);
+    const uint4 *src = reinterpret_cast<const uint4 *>(x.p - x.shift) + v0;
+    const int64_t y = a.targets ? a.targets[row] : -1;
+    const bool scored = y >= 0 && y < a.V;
+    // before any block of the row may write its gradient over it
+    const float at_y = scored ? Vec<T>::get(x.p[y]) : 0.f;
+    auto fetch = [&](int i) {                            // any vector of this block
+        if (i >= w0 && i < w1) return __ldg(src + i);
+        float v[N];
+        x.load(v0 + i, v, -INFINITY);
+        return Vec<T>::pack(v);
+    };
+
+    Stat st{-INFINITY, 0.f, 0.f};
+    int i = w0 + tid;
+    for (; i + (LPU - 1) * LPT < w1; i += LPU * LPT) {
+        uint4 raw[LPU];
+#pragma unroll
+        for (int u = 0; u < LPU; ++u) raw[u] = __ldg(src + i + u * LPT);
+        if (GRAD)
+#pragma unroll
+            for (int u = 0; u < LPU; ++u)
+                if (i + u * LPT < a.keep) kept[i + u * LPT] = raw[u];
+        take<T, LPU>(st, raw);
+    }
+    // the rest, then the vectors at the row's ends (threads 0 and 1)
+    const int end = tid == 0 && odd_first ? 0 : tid == 1 && odd_last ? nv - 1 : nv;
+    for (i = i < w1 ? i : end; i < nv; i = i + LPT < w1 && i != end ? i + LPT : i == end ? nv : end) {
+        const uint4 raw[1] = {fetch(i)};
+        if (GRAD && i < a.keep) kept[i] = raw[0];
+        take<T, 1>(st, raw);
+    }
+    const float own_max = st.m;
+    st = warp_join(st);
     if ((tid & 31) == 0) red[tid >> 5] = st;
     if (tid == 0) n_cand = 0;
     __syncthreads();
-    if (tid == 0) {
-        Stat s = red[0];
-        for (int w = 1; w < LPT / 32; ++w) s = join(s, red[w]);
-        all = s;
-    }
-    __syncthreads();
-    const Ref ref(all.m);
-    const float s = all.s, l2s = log2f(s);
-    const bool empty = s == 0.f;
-    const float lse = empty ? -INFINITY : ref.natural(l2s), ent = empty ? 0.f : (l2s - all.t / s) * LN2;
-    const int64_t y = a.targets ? a.targets[row] : -1;
-    const bool scored = y >= 0 && y < a.V;
-    if (tid == 0) {
-        if (a.lse) a.lse[row] = lse;
-        if (a.entropy) a.entropy[row] = ent;
-        if (a.logp)
-            a.logp[row] = !scored ? 0.f : empty ? -INFINITY : ref.logp(Vec<T>::get(x.p[y]), l2s);
+    if (tid < 32) {
+        st = warp_join(tid < LPT / 32 ? red[tid] : Stat{-INFINITY, 0.f, 0.f});
+        if (tid == 0) mine = st;
     }
     if (a.top) {
-        // Lower bound of the top-th largest: the top-th largest of the threads' own maxima, to 16
-        // bits of its key.  Only threads at or above it read their values again.
-        const bool slow_row = s != s;                    // NaN or +inf: own_max says too little
+        // This block's part of the top list.  A lower bound of its top-th largest value: the top-th
+        // largest of the threads' own maxima, to 12 bits of its key (an eighth of a power of two).  Only
+        // threads at or above it read their values again.
         const uint32_t key = order_key(own_max);
-        uint32_t bound = 0;
-        for (int b = 31; b >= 16; --b) {
-            const uint32_t c = bound | (1u << b);
-            if (__syncthreads_count(key >= c) >= a.top) bound = c;
+        keys[tid] = key;
+        __syncthreads();
+        const bool odd = mine.s != mine.s;               // NaN or +inf: own_max says too little
+        if (tid < 32) {
+            uint32_t k[LPT / 32], bound = 0;
+#pragma unroll
+            for (int w = 0; w < LPT / 32; ++w) k[w] = keys[w * 32 + tid];
+            for (int b = 31; b >= 20; --b) {
+                const uint32_t c = bound | (1u << b);
+                int n = 0;
+#pragma unroll
+                for (int w = 0; w < LPT / 32; ++w) n += k[w] >= c;
+                if (__reduce_add_sync(~0u, n) >= a.top) bound = c;
+            }
+            if (tid == 0) bound_ = bound;
         }
-        if (!slow_row && key >= bound)
-            for (int64_t i = tid; i < nv; i += LPT)
-                for (int e = 0; e < N; ++e) {
-                    const int64_t j = i * N - x.shift + e;
-                    if (j < 0 || j >= a.V) continue;
-                    const uint32_t k = order_key(Vec<T>::get(x.p[j]));
-                    if (k < bound) continue;
-                    const int at = atomicAdd(&n_cand, 1);
-                    if (at < CAND) cand[at] = rank_key(k, uint32_t(j));
-                }
+        __syncthreads();
+        const uint32_t bound = bound_;
+        auto offer = [&](int i) {
+            float v[N];
+            Vec<T>::unpack(fetch(i), v);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const int64_t j = int64_t(v0 + i) * N - x.shift + e;
+                const uint32_t k = order_key(v[e]);
+                if (k < bound || j < 0 || j >= a.V) continue;
+                const int at = atomicAdd(&n_cand, 1);
+                if (at < CAND) cand[at] = rank_key(k, uint32_t(j));
+            }
+        };
+        if (!odd) {
+            // a thread's values are read again by its whole warp: few threads qualify
+            for (uint32_t m = __ballot_sync(~0u, key >= bound); m; m &= m - 1) {
+                const int t = (tid & ~31) + __ffs(m) - 1;
+                for (int i = w0 + t + (tid & 31) * LPT; i < w1; i += 32 * LPT) offer(i);
+                if (t == tid && tid == 0 && odd_first) offer(0);
+                if (t == tid && tid == 1 && odd_last) offer(nv - 1);
+            }
+        }
+        if (tid < a.top) best_of[tid] = 0;               // fewer values than places
         __syncthreads();
         const int n = n_cand;
-        int32_t *id = a.top_id + row * a.top;
-        float *lp = a.top_logp + row * a.top;
-        auto put = [&](int r, uint64_t c) {
-            const uint32_t j = ~uint32_t(c);
-            id[r] = int32_t(j);
-            lp[r] = empty ? -INFINITY : ref.logp(Vec<T>::get(x.p[j]), l2s);
-        };
-        if (!slow_row && n <= CAND) {
+        if (!odd && n <= CAND) {
+            // the order of the candidates is the threads'; their ranks are not
             for (int i = tid; i < n; i += LPT) {
                 int r = 0;
                 for (int k = 0; k < n; ++k) r += cand[k] > cand[i];
-                if (r < a.top) put(r, cand[i]);
+                if (r < a.top) best_of[r] = cand[i];
             }
         } else {
             // many equal values, or NaN: the best of those after the last one taken, `top` times
             uint64_t last = ~uint64_t(0);
             for (int r = 0; r < a.top; ++r) {
                 uint64_t best = 0;
-                for (int64_t j = tid; j < a.V; j += LPT) {
-                    const uint64_t c = rank_key(order_key(Vec<T>::get(x.p[j])), uint32_t(j));
-                    if (c < last && c > best) best = c;
+                for (int i = tid; i < nv; i += LPT) {
+                    float v[N];
+                    Vec<T>::unpack(fetch(i), v);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const int64_t j = int64_t(v0 + i) * N - x.shift + e;
+                        const uint64_t c = rank_key(order_key(v[e]), uint32_t(j));
+                        if (j >= 0 && j < a.V && c < last && c > best) best = c;
+                    }
                 }
 #pragma unroll
                 for (int d = 16; d; d >>= 1) best = max(best, __shfl_xor_sync(~0u, best, d));
+                __syncthreads();
                 if ((tid & 31) == 0) cand[tid >> 5] = best;
                 __syncthreads();
                 for (int w = 0; w < LPT / 32; ++w) best = max(best, cand[w]);
-                __syncthreads();
-                if (tid == 0) put(r, best);
+                if (tid == 0) best_of[r] = best;
                 last = best;
             }
         }
     }
-    if (GRAD) {
-        const float gl = scored && !empty && a.glp ? a.glp[row] : 0.f, ge = a.gent ? a.gent[row] : 0.f;
-        const float inv = empty ? 0.f : 1.f / s;
-        const Ragged<T> out(static_cast<T *>(a.dlogits) + row * a.ldd, a.V);
-        if (a.top) __syncthreads();                      // in place: the top list has been read
-        for (int64_t i = tid; i < nv; i += LPT) {
-            float v[N];
-            x.load(i, v, -INFINITY);
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float d = ref(v[e]), p = ex2(d) * inv;
-                float g = -gl * p;
-                if (p != 0.f) g -= ge * p * fmaf(d - l2s, LN2, ent);
-                if (i * N - x.shift + e == y && scored) g += gl;
-                v[e] = g;
-            }
-            out.store(i, x.shift, v);
+    meet(blocks);
+    Stat all = mine;
+    if (blocks > 1) {
+        all = peer(&mine, 0);
+        for (int b = 1; b < blocks; ++b) all = join(all, peer(&mine, b));
+    }
+    const Ref ref(all.m);
+    const float s = all.s, l2s = log2f(s);
+    const bool empty = s == 0.f;
+    const float lse = empty ? -INFINITY : ref.natural(l2s), ent = empty ? 0.f : (l2s - all.t / s) * LN2;
+    if (rank == 0 && tid == 0) {
+        if (a.lse) a.lse[row] = lse;
+        if (a.entropy) a.entropy[row] = ent;
+        if (a.logp) a.logp[row] = !scored ? 0.f : empty ? -INFINITY : ref.logp(at_y, l2s);
+    }
+    if (a.top && rank == 0) {
+        // the blocks' lists, by rank among all of them
+        const int n = a.top * blocks;
+        for (int i = tid; i < n; i += LPT) cand[i] = blocks > 1 ? peer(best_of + i % a.top, i / a.top) : best_of[i];
+        __syncthreads();
+        for (int i = tid; i < n; i += LPT) {
+            const uint64_t c = cand[i];
+            int r = 0;
+            for (int k = 0; k < n; ++k) r += cand[k] > c;
+            if (c == 0 || r >= a.top) continue;          // 0: a place that a short part left free
+            a.top_id[row * a.top + r] = int32_t(~uint32_t(c));
+            a.top_logp[row * a.top + r] = empty ? -INFINITY : ref.logp(key_value(uint32_t(c >> 32)), l2s);
         }
     }
+    if (GRAD) {
+        const float gl = scored && !empty && a.glp ? a.glp[row] : 0.f, ge = a.gent ? a.gent[row] : 0.f;
+        // g = -gl p - ge p (ln p + entropy), with ln p = (d - l2s) ln 2
+        const float c0 = empty ? 0.f : fmaf(-ge, ent - l2s * LN2, -gl) / s, c1 = empty ? 0.f : -ge * LN2 / s;
+        const Ragged<T> out(static_cast<T *>(a.dlogits) + row * a.ldd, a.V);
+        const int hot = scored ? int((y + x.shift) / N) - v0 : -1;
+        uint4 *dst = reinterpret_cast<uint4 *>(out.p - x.shift) + v0;
+        const bool same = out.shift == x.shift;          // whole vectors of one are whole vectors of the other
+        for (int i = tid; i < nv; i += LPT) {
+            const uint4 raw = i < a.keep ? kept[i] : fetch(i);
+            const uint4 g = ref.far ? slope<T, true>(raw, ref, c0, c1) : slope<T, false>(raw, ref, c0, c1);
+            if (same && i >= w0 && i < w1) {
+                __stcs(dst + i, g);
+            } else {
+                float v[N];
+                Vec<T>::unpack(g, v);
+                out.store(v0 + i, x.shift, v);
+            }
+        }
+        // the target's own value, over what this thread stored for its vector
+        if (hot >= 0 && hot < nv && tid == hot % LPT) {
+            const float d = ref.far ? ref.at<true>(at_y) : ref.at<false>(at_y);
+            out.p[y] = Vec<T>::put(fmaf(ex2(d), fmaf(c1, fmaxf(d, -200.f), c0), gl));
+        }
+    }
+    if (blocks > 1) meet(blocks);                        // no block leaves while another reads its statistics
 }
 
 // ---------------------------------------------------------------- clipping
@@ -447,17 +645,40 @@ cudaError_t clip(const adj_grad_seg *segs, int64_t nseg, float max_norm, float *
 
 }  // namespace
 
+namespace {
+template <class T, bool GRAD>
+cudaError_t logprob(LogprobArgs a, cudaStream_t st) {
+    const int64_t row = a.V * int64_t(sizeof(T)) + 16;
+    a.blocks = 1;
+    // a part of the row has to fit where the gradient reads it again ...
+    while (GRAD && a.blocks < 8 && row > a.blocks * ROW_KEEP) a.blocks *= 2;
+    // ... and idle SMs are put to use while a part is at least one turn of the block's loads
+    while (a.blocks < 8 && a.N * a.blocks * 2 <= 152 && row >= a.blocks * 2 * int64_t(LPU * LPT * 16)) a.blocks *= 2;
+    const int64_t part = cdiv(cdiv(row, 16), a.blocks);
+    a.keep = GRAD ? int(std::min<int64_t>(part, (a.blocks == 8 ? 200 * 1024 : ROW_KEEP) / 16)) : 0;
+    const size_t smem = size_t(a.keep) * 16;
+    cudaError_t e = cudaFuncSetAttribute(k_logprob<T, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(a.N * a.blocks));
+    cfg.blockDim = dim3(LPT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = unsigned(a.blocks);
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = a.blocks > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, k_logprob<T, GRAD>, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+}  // namespace
+
 cudaError_t launch_logprob(const LogprobArgs &a, bool bf16, cudaStream_t st) {
     ProfScope ps(K_LOGPROB, st);
-    const unsigned grid = unsigned(a.N);
-    if (bf16) {
-        if (a.dlogits) k_logprob<__nv_bfloat16, true><<<grid, LPT, 0, st>>>(a);
-        else k_logprob<__nv_bfloat16, false><<<grid, LPT, 0, st>>>(a);
-    } else {
-        if (a.dlogits) k_logprob<float, true><<<grid, LPT, 0, st>>>(a);
-        else k_logprob<float, false><<<grid, LPT, 0, st>>>(a);
-    }
-    return cudaGetLastError();
+    if (bf16) return a.dlogits ? logprob<__nv_bfloat16, true>(a, st) : logprob<__nv_bfloat16, false>(a, st);
+    return a.dlogits ? logprob<float, true>(a, st) : logprob<float, false>(a, st);
 }
 
 size_t clip_ws_bytes() { return WS_HEADER + (CLIP_GRID + 1) * sizeof(double); }

@@ -14,6 +14,8 @@ struct LogprobArgs {
     float *top_logp;
     const float *glp, *gent;
     void *dlogits;
+    // set by the launcher: blocks of a row, 16-byte units that each keeps for the gradient
+    int blocks, keep;
 };
 
 cudaError_t launch_logprob(const LogprobArgs &a, bool bf16, cudaStream_t st);

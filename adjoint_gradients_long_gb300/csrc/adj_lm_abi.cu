@@ -124,7 +124,7 @@ adj_status adj_logprob(const adj_logprob_dims *d, const void *logits, const int6
                        const float *gent, void *dlogits, void *stream) {
     if (!d) return ADJ_EINVAL;
     if (d->x_dtype != ADJ_F32 && d->x_dtype != ADJ_BF16) return ADJ_EDTYPE;
-    if (d->N < 0 || d->N >= (int64_t(1) << 31) || d->V < 1 || d->V >= (int64_t(1) << 31) || d->ld < d->V) return ADJ_ESHAPE;
+    if (d->N < 0 || d->N >= (int64_t(1) << 28) || d->V < 1 || d->V >= (int64_t(1) << 31) || d->ld < d->V) return ADJ_ESHAPE;
     if (d->top < 0 || d->top > ADJ_LOGPROB_MAX_TOP || d->top > d->V) return ADJ_ESHAPE;
     if (dlogits && d->ldd < d->V) return ADJ_ESHAPE;
     if (d->N == 0) return ADJ_OK;
@@ -138,7 +138,7 @@ adj_status adj_logprob(const adj_logprob_dims *d, const void *logits, const int6
     for (const void *p : {(const void *)logp, (const void *)entropy, (const void *)lse, (const void *)top_id,
                           (const void *)top_logp, (const void *)glp, (const void *)gent})
         if (!aligned(p, 4)) return ADJ_EALIGN;
-    LogprobArgs a{d->N, d->V, d->ld, d->ldd, d->top, logits, targets, logp, entropy, lse, top_id, top_logp, glp, gent, dlogits};
+    LogprobArgs a{d->N, d->V, d->ld, d->ldd, d->top, logits, targets, logp, entropy, lse, top_id, top_logp, glp, gent, dlogits, 1, 0};
     return done(launch_logprob(a, d->x_dtype == ADJ_BF16, static_cast<cudaStream_t>(stream)));
 }
 

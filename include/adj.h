@@ -318,7 +318,7 @@ adj_status adj_lin_step(const adj_lin_dims *dims, const void *q, const void *k, 
  * Any output may be NULL (top_id and top_logp both or neither; top = 0 for neither); dlogits
  * needs glp or gent (a NULL one counts as zeros) and may be the logits array itself when
  * ldd = ld.  logits and dlogits need only their type's alignment, ld, ldd >= V.  top <= V and
- * top <= ADJ_LOGPROB_MAX_TOP; V < 2^31.  One launch, no workspace. */
+ * top <= ADJ_LOGPROB_MAX_TOP; N < 2^28, V < 2^31.  One launch, no workspace. */
 typedef struct {
     int64_t N, V, ld, ldd;
     int32_t x_dtype, top;
