@@ -125,15 +125,22 @@ struct Ragged {
 };
 
 // ---------------------------------------------------------------- log probabilities
-// One pass over the row with the running maximum, sum and entropy sum of its softmax; bound by
-// the row's bytes.  A row is cut over a cluster of 1 to 8 blocks: when it is too long for one
-// block's shared memory (the gradient's second pass reads the row from there), and when there are
-// too few rows to fill the SMs.  The blocks' statistics and top lists are joined through
-// distributed shared memory, in rank order.
-constexpr int LPT = 512;        // threads of a block
+// One pass over the row with the running maximum, sum and entropy sum of its softmax; the
+// gradient's second pass finds the row in L2.  Bound by the row's bytes, then by the instructions
+// of a value (12 for both passes in bf16).  A row is cut over a cluster of 1 to 8 blocks: when the
+// rows in flight would not stay in L2 otherwise, and when there are too few rows to fill the SMs.
+// The blocks' statistics and top lists are joined through distributed shared memory, in rank order.
+//
+// Measured, loss with gradient of 8192 x 32768 bf16 (1.07 GB): 179 us, 0.89 of the
+// copy bandwidth; with the row kept in shared memory, three blocks of 512 an SM, 227 us (the
+// occupancy is worth more than the L2 reads).  Scoring 2048 x 50001 fp32: 86 us, 0.70.
+constexpr int LPT = 256;        // threads of a block
+constexpr int LPB = 6;          // blocks an SM
 constexpr int CAND = 512;       // candidates for the top list
 constexpr int LPU = 4;          // vectors in flight a thread
-constexpr int64_t ROW_KEEP = 72 * 1024;     // bytes of a row that a block keeps: three blocks an SM
+// bytes of a row that one block takes when the gradient reads them again: 152 x 6 such parts are
+// 64 MB, half of L2
+constexpr int64_t ROW_PART = 72 * 1024;
 
 // Order of the top list as unsigned integers: NaN above +inf, the zeros equal.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -287,20 +294,19 @@ __device__ __forceinline__ uint4 slope(uint4 raw, const Ref &ref, float c0, floa
 }
 
 template <class T, bool GRAD>
-__global__ __launch_bounds__(LPT, 3) void k_logprob(const LogprobArgs a) {
+__global__ __launch_bounds__(LPT, LPB) void k_logprob(const LogprobArgs a) {
     constexpr int N = Vec<T>::N;
-    extern __shared__ uint4 kept[];                      // GRAD: this block's part of the row
     __shared__ Stat red[LPT / 32], mine;
     __shared__ uint64_t cand[CAND], best_of[ADJ_LOGPROB_MAX_TOP];
     __shared__ uint32_t keys[LPT], bound_;
     __shared__ int n_cand;
     const int tid = threadIdx.x, blocks = a.blocks;
     const uint32_t rank = blocks > 1 ? rank_in_cluster() : 0u;
-    const int64_t row = blockIdx.x / blocks;
+    const int64_t row = blockIdx.x >> a.log_blocks;
     const Ragged<T> x(const_cast<T *>(static_cast<const T *>(a.logits)) + row * a.ld, a.V);
     // this block's vectors v0 .. v0 + nv of the row; the first and the last of a row may lie partly
     // outside it and are fetched value by value
-    const int all_v = int(x.vectors()), per = (all_v + blocks - 1) / blocks, v0 = int(rank) * per, nv = max(0, min(all_v - v0, per));
+    const int all_v = int(x.vectors()), per = (all_v + blocks - 1) >> a.log_blocks, v0 = int(rank) * per, nv = max(0, min(all_v - v0, per));
     const bool odd_first = nv > 0 && !x.whole(v0), odd_last = nv > 1 && !x.whole(v0 + nv - 1);
     const int w0 = odd_first ? 1 : 0, w1 = nv - (odd_last ? 1 : 0);
     const uint4 *src = reinterpret_cast<const uint4 *>(x.p - x.shift) + v0;
@@ -321,17 +327,12 @@ __global__ __launch_bounds__(LPT, 3) void k_logprob(const LogprobArgs a) {
         uint4 raw[LPU];
 #pragma unroll
         for (int u = 0; u < LPU; ++u) raw[u] = __ldg(src + i + u * LPT);
-        if (GRAD)
-#pragma unroll
-            for (int u = 0; u < LPU; ++u)
-                if (i + u * LPT < a.keep) kept[i + u * LPT] = raw[u];
         take<T, LPU>(st, raw);
     }
     // the rest, then the vectors at the row's ends (threads 0 and 1)
     const int end = tid == 0 && odd_first ? 0 : tid == 1 && odd_last ? nv - 1 : nv;
     for (i = i < w1 ? i : end; i < nv; i = i + LPT < w1 && i != end ? i + LPT : i == end ? nv : end) {
         const uint4 raw[1] = {fetch(i)};
-        if (GRAD && i < a.keep) kept[i] = raw[0];
         take<T, 1>(st, raw);
     }
     const float own_max = st.m;
@@ -457,22 +458,29 @@ __global__ __launch_bounds__(LPT, 3) void k_logprob(const LogprobArgs a) {
         // g = -gl p - ge p (ln p + entropy), with ln p = (d - l2s) ln 2
         const float c0 = empty ? 0.f : fmaf(-ge, ent - l2s * LN2, -gl) / s, c1 = empty ? 0.f : -ge * LN2 / s;
         const Ragged<T> out(static_cast<T *>(a.dlogits) + row * a.ldd, a.V);
-        const int hot = scored ? int((y + x.shift) / N) - v0 : -1;
+        const int hot = scored ? int(unsigned(y + x.shift) / N) - v0 : -1;
         uint4 *dst = reinterpret_cast<uint4 *>(out.p - x.shift) + v0;
         const bool same = out.shift == x.shift;          // whole vectors of one are whole vectors of the other
-        for (int i = tid; i < nv; i += LPT) {
-            const uint4 raw = i < a.keep ? kept[i] : fetch(i);
-            const uint4 g = ref.far ? slope<T, true>(raw, ref, c0, c1) : slope<T, false>(raw, ref, c0, c1);
-            if (same && i >= w0 && i < w1) {
-                __stcs(dst + i, g);
-            } else {
-                float v[N];
-                Vec<T>::unpack(g, v);
-                out.store(v0 + i, x.shift, v);
+        auto grad = [&](uint4 raw) { return ref.far ? slope<T, true>(raw, ref, c0, c1) : slope<T, false>(raw, ref, c0, c1); };
+        auto odd = [&](int i) {
+            float v[N];
+            Vec<T>::unpack(grad(fetch(i)), v);
+            out.store(v0 + i, x.shift, v);
+        };
+        if (same) {
+            int i = w0 + tid;
+            for (; i + LPT < w1; i += 2 * LPT) {
+                const uint4 r0 = __ldcs(src + i), r1 = __ldcs(src + i + LPT);
+                __stcs(dst + i, grad(r0));
+                __stcs(dst + i + LPT, grad(r1));
             }
+            if (i < w1) __stcs(dst + i, grad(__ldcs(src + i)));
+        } else {
+            for (int i = w0 + tid; i < w1; i += LPT) odd(i);
         }
+        if (end < nv) odd(end);
         // the target's own value, over what this thread stored for its vector
-        if (hot >= 0 && hot < nv && tid == hot % LPT) {
+        if (hot >= 0 && hot < nv && tid == (hot == 0 && odd_first ? 0 : hot == nv - 1 && odd_last ? 1 : (hot - w0) % LPT)) {
             const float d = ref.far ? ref.at<true>(at_y) : ref.at<false>(at_y);
             out.p[y] = Vec<T>::put(fmaf(ex2(d), fmaf(c1, fmaxf(d, -200.f), c0), gl));
         }
@@ -650,19 +658,15 @@ template <class T, bool GRAD>
 cudaError_t logprob(LogprobArgs a, cudaStream_t st) {
     const int64_t row = a.V * int64_t(sizeof(T)) + 16;
     a.blocks = 1;
-    // a part of the row has to fit where the gradient reads it again ...
-    while (GRAD && a.blocks < 8 && row > a.blocks * ROW_KEEP) a.blocks *= 2;
-    // ... and idle SMs are put to use while a part is at least one turn of the block's loads
-    while (a.blocks < 8 && a.N * a.blocks * 2 <= 152 && row >= a.blocks * 2 * int64_t(LPU * LPT * 16)) a.blocks *= 2;
-    const int64_t part = cdiv(cdiv(row, 16), a.blocks);
-    a.keep = GRAD ? int(std::min<int64_t>(part, (a.blocks == 8 ? 200 * 1024 : ROW_KEEP) / 16)) : 0;
-    const size_t smem = size_t(a.keep) * 16;
-    cudaError_t e = cudaFuncSetAttribute(k_logprob<T, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
+    a.log_blocks = 0;
+    // a row that the gradient reads again has to stay in L2 with the others in flight ...
+    while (GRAD && a.blocks < 8 && row > a.blocks * ROW_PART) a.blocks = 1 << ++a.log_blocks;
+    // ... and idle SMs are put to use while a part is at least one turn of the block's loads.  More
+    // parts than that cost more than they even out (2048 x 50001 fp32: 86 us in one part, 128 in four).
+    while (a.blocks < 8 && a.N * a.blocks * 2 <= 152 && row >= a.blocks * 2 * int64_t(LPU * LPT * 16)) a.blocks = 1 << ++a.log_blocks;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(a.N * a.blocks));
     cfg.blockDim = dim3(LPT);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
@@ -670,7 +674,7 @@ cudaError_t logprob(LogprobArgs a, cudaStream_t st) {
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = a.blocks > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, k_logprob<T, GRAD>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_logprob<T, GRAD>, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 }  // namespace

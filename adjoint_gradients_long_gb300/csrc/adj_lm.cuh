@@ -14,8 +14,7 @@ struct LogprobArgs {
     float *top_logp;
     const float *glp, *gent;
     void *dlogits;
-    // set by the launcher: blocks of a row, 16-byte units that each keeps for the gradient
-    int blocks, keep;
+    int blocks, log_blocks;     // of a row, set by the launcher
 };
 
 cudaError_t launch_logprob(const LogprobArgs &a, bool bf16, cudaStream_t st);
