@@ -356,6 +356,7 @@ __global__ __launch_bounds__(LPT, LPB) void k_logprob(const LogprobArgs a) {
             uint32_t k[LPT / 32], bound = 0;
 #pragma unroll
             for (int w = 0; w < LPT / 32; ++w) k[w] = keys[w * 32 + tid];
+#pragma unroll 1
             for (int b = 31; b >= 20; --b) {
                 const uint32_t c = bound | (1u << b);
                 int n = 0;
@@ -370,9 +371,10 @@ __global__ __launch_bounds__(LPT, LPB) void k_logprob(const LogprobArgs a) {
         auto offer = [&](int i) {
             float v[N];
             Vec<T>::unpack(fetch(i), v);
+            const int64_t j0 = int64_t(v0 + i) * N - x.shift;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const int64_t j = int64_t(v0 + i) * N - x.shift + e;
+                const int64_t j = j0 + e;
                 const uint32_t k = order_key(v[e]);
                 if (k < bound || j < 0 || j >= a.V) continue;
                 const int at = atomicAdd(&n_cand, 1);
@@ -381,8 +383,10 @@ __global__ __launch_bounds__(LPT, LPB) void k_logprob(const LogprobArgs a) {
         };
         if (!odd) {
             // a thread's values are read again by its whole warp: few threads qualify
+#pragma unroll 1
             for (uint32_t m = __ballot_sync(~0u, key >= bound); m; m &= m - 1) {
                 const int t = (tid & ~31) + __ffs(m) - 1;
+#pragma unroll 1
                 for (int i = w0 + t + (tid & 31) * LPT; i < w1; i += 32 * LPT) offer(i);
                 if (t == tid && tid == 0 && odd_first) offer(0);
                 if (t == tid && tid == 1 && odd_last) offer(nv - 1);
@@ -395,6 +399,7 @@ __global__ __launch_bounds__(LPT, LPB) void k_logprob(const LogprobArgs a) {
             // the order of the candidates is the threads'; their ranks are not
             for (int i = tid; i < n; i += LPT) {
                 int r = 0;
+#pragma unroll 1
                 for (int k = 0; k < n; ++k) r += cand[k] > cand[i];
                 if (r < a.top) best_of[r] = cand[i];
             }
@@ -447,6 +452,7 @@ __global__ __launch_bounds__(LPT, LPB) void k_logprob(const LogprobArgs a) {
         for (int i = tid; i < n; i += LPT) {
             const uint64_t c = cand[i];
             int r = 0;
+#pragma unroll 1
             for (int k = 0; k < n; ++k) r += cand[k] > c;
             if (c == 0 || r >= a.top) continue;          // 0: a place that a short part left free
             a.top_id[row * a.top + r] = int32_t(~uint32_t(c));
@@ -489,19 +495,30 @@ __global__ __launch_bounds__(LPT, LPB) void k_logprob(const LogprobArgs a) {
 }
 
 // ---------------------------------------------------------------- clipping
+// Bound by bytes: one read for the norm, one read and one write for the scaling.  Up to 1000
+// tensors (their table travels as the kernel's parameters) take one cooperative launch: every block
+// sums its chunks, the blocks meet, and each goes back over its chunks from the last one, whose
+// values are still in L2.  More tensors take one launch a group for the norm and one for the
+// scaling.
 constexpr int CT = 256;         // threads of a block
-constexpr int CLIP_CHUNK = 16384;   // bytes of a chunk
+constexpr int CB = 4;           // blocks an SM
+constexpr int CLIP_GRID = 152 * CB;
 
 template <int MAXS>
 struct ClipSegs {
     int n, first_group;         // first_group: the total starts with this group of tensors
     float max_norm;
+    int chunk;                  // 16-byte units of a chunk, a multiple of CT
     int64_t chunks;
     const void *src[MAXS];
     void *dst[MAXS];
     int64_t len[MAXS];
     int first[MAXS];            // a tensor's first chunk
     uint8_t bf16[MAXS];
+};
+struct ClipWs {                 // in the workspace
+    unsigned *status, *ticket, *turn;
+    double *part, *total;
 };
 
 template <int MAXS>
@@ -515,99 +532,204 @@ __device__ __forceinline__ int seg_of(const ClipSegs<MAXS> &g, int64_t c) {
     return lo;
 }
 
+// The part i0 .. i1 (16-byte units) of a tensor: its sum of squares, or its values times f.  Whole
+// units eight at a time a thread; the ends of a tensor, and outputs aligned otherwise, value by value.
+constexpr int CU = 8;
 template <class T>
-__device__ __forceinline__ float chunk_square(const void *src, int64_t n, int64_t c) {
-    constexpr int N = Vec<T>::N, PER = CLIP_CHUNK / 16 / CT;
+__device__ __forceinline__ float part_square(const void *src, int64_t n, int64_t i0, int64_t i1) {
+    constexpr int N = Vec<T>::N;
     const Ragged<T> x(const_cast<T *>(static_cast<const T *>(src)), n);
-    const int64_t nv = x.vectors(), i0 = c * (CLIP_CHUNK / 16) + threadIdx.x;
-    float s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int u = 0; u < PER; ++u) {
-        const int64_t i = i0 + u * CT;
-        if (i >= nv) break;
+    const uint4 *p = reinterpret_cast<const uint4 *>(x.p - x.shift);
+    i1 = min(i1, x.vectors());
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](uint4 raw) {
         float v[N];
-        x.load(i, v, 0.f);
+        Vec<T>::unpack(raw, v);
 #pragma unroll
-        for (int e = 0; e < N; ++e) s[e & 1] = fmaf(v[e], v[e], s[e & 1]);
+        for (int e = 0; e < N; ++e) s[e & 3] = fmaf(v[e], v[e], s[e & 3]);
+    };
+    const int64_t w0 = i0 + !x.whole(i0), w1 = max(w0, i1 - !x.whole(i1 - 1));
+    const int len = int(w1 - w0);
+    p += w0;
+    int i = threadIdx.x;
+#pragma unroll 1
+    for (; i + (CU - 1) * CT < len; i += CU * CT) {
+        uint4 raw[CU];
+#pragma unroll
+        for (int u = 0; u < CU; ++u) raw[u] = __ldg(p + i + u * CT);
+#pragma unroll
+        for (int u = 0; u < CU; ++u) add(raw[u]);
     }
-    return s[0] + s[1];
+#pragma unroll 1
+    for (; i < len; i += CT) add(__ldg(p + i));
+    const int64_t end = threadIdx.x == 0 && w0 > i0 ? i0 : threadIdx.x == 1 && w1 < i1 && w1 >= w0 && i1 - 1 > i0 ? i1 - 1 : -1;
+    if (end >= 0) {
+        float v[N];
+        x.load(end, v, 0.f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e & 3] = fmaf(v[e], v[e], s[e & 3]);
+    }
+    return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 template <class T>
-__device__ __forceinline__ void chunk_scale(const void *src, void *dst, int64_t n, int64_t c, float f) {
-    constexpr int N = Vec<T>::N, PER = CLIP_CHUNK / 16 / CT;
+__device__ __forceinline__ void part_scale(const void *src, void *dst, int64_t n, int64_t i0, int64_t i1, float f) {
+    constexpr int N = Vec<T>::N;
     const Ragged<T> x(const_cast<T *>(static_cast<const T *>(src)), n), y(static_cast<T *>(dst), n);
-    const int64_t nv = x.vectors(), i0 = c * (CLIP_CHUNK / 16) + threadIdx.x;
+    const uint4 *p = reinterpret_cast<const uint4 *>(x.p - x.shift);
+    uint4 *q = reinterpret_cast<uint4 *>(y.p - y.shift);
+    i1 = min(i1, x.vectors());
+    auto scaled = [&](uint4 raw) {
+        float v[N];
+        Vec<T>::unpack(raw, v);
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-        const int64_t i = i0 + u * CT;
-        if (i >= nv) break;
+        for (int e = 0; e < N; ++e) v[e] *= f;
+        return Vec<T>::pack(v);
+    };
+    auto slowly = [&](int64_t i) {
         float v[N];
         x.load(i, v, 0.f);
 #pragma unroll
         for (int e = 0; e < N; ++e) v[e] *= f;
         y.store(i, x.shift, v);
+    };
+    if (x.shift != y.shift) {
+        for (int64_t i = i0 + threadIdx.x; i < i1; i += CT) slowly(i);
+        return;
     }
+    const int64_t w0 = i0 + !x.whole(i0), w1 = max(w0, i1 - !x.whole(i1 - 1));
+    const int len = int(w1 - w0);
+    p += w0;
+    q += w0;
+    // backwards: what was read last is read first
+    int i = len - 1 - int(threadIdx.x);
+#pragma unroll 1
+    for (; i - (CU / 2 - 1) * CT >= 0; i -= CU / 2 * CT) {
+        uint4 raw[CU / 2];
+#pragma unroll
+        for (int u = 0; u < CU / 2; ++u) raw[u] = __ldcs(p + i - u * CT);
+#pragma unroll
+        for (int u = 0; u < CU / 2; ++u) __stcs(q + i - u * CT, scaled(raw[u]));
+    }
+#pragma unroll 1
+    for (; i >= 0; i -= CT) __stcs(q + i, scaled(__ldcs(p + i)));
+    if (threadIdx.x == 0 && w0 > i0) slowly(i0);
+    if (threadIdx.x == 1 && w1 < i1 && i1 - 1 > i0) slowly(i1 - 1);
 }
 
-// Sum of squares: a block takes the chunks blockIdx.x, + gridDim.x, ...; the last block to
-// finish adds the blocks' sums in their order.
-template <int MAXS>
-__global__ __launch_bounds__(CT) void k_clip_norm(const __grid_constant__ ClipSegs<MAXS> g, double *part, double *total,
-                                                  unsigned *ticket, float *out) {
-    __shared__ double red[CT / 32];
-    __shared__ bool last;
-    double sum = 0.0;
-    for (int64_t c = blockIdx.x; c < g.chunks; c += gridDim.x) {
-        const int s = seg_of(g, c);
-        const int64_t k = c - g.first[s];
-        sum += g.bf16[s] ? chunk_square<__nv_bfloat16>(g.src[s], g.len[s], k) : chunk_square<float>(g.src[s], g.len[s], k);
-    }
-    auto block_sum = [&](double v) {
+__device__ __forceinline__ double block_sum(double v, double *red) {
 #pragma unroll
-        for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-        __syncthreads();
-        double r = 0.0;
-        for (int w = 0; w < CT / 32; ++w) r += red[w];
-        __syncthreads();
-        return r;
-    };
-    sum = block_sum(sum);
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double r = 0.0;
+    for (int w = 0; w < CT / 32; ++w) r += red[w];
+    __syncthreads();
+    return r;
+}
+
+// A block takes a contiguous range of chunks, so that it looks its tensor up once.
+template <int MAXS>
+__device__ __forceinline__ int64_t range(const ClipSegs<MAXS> &g, int64_t block) {
+    return g.chunks * block / gridDim.x;
+}
+
+// The block's part of the sum of squares.  A thread's tensors add up as a sum and what its
+// roundings lost: the fp64 pipe would take as long as the loads.
+template <int MAXS>
+__device__ __forceinline__ double sum_chunks(const ClipSegs<MAXS> &g) {
+    float sum = 0.f, lost = 0.f;
+    const int64_t c1 = range(g, int64_t(blockIdx.x) + 1);
+    int64_t c = range(g, blockIdx.x);
+    for (int s = seg_of(g, c); c < c1; ++s) {
+        const int64_t next = s + 1 < g.n ? min(c1, int64_t(g.first[s + 1])) : c1;
+        const int64_t i0 = (c - g.first[s]) * g.chunk, i1 = (next - g.first[s]) * g.chunk;
+        const float x = g.bf16[s] ? part_square<__nv_bfloat16>(g.src[s], g.len[s], i0, i1)
+                                  : part_square<float>(g.src[s], g.len[s], i0, i1);
+        const float t = sum + x, y = t - sum, z = (sum - (t - y)) + (x - y);
+        if (z == z) lost += z;                           // not where the sum is infinite
+        sum = t;
+        c = next;
+    }
+    return double(sum) + double(lost);
+}
+
+// Hands in the block's sum; true in the last block to do so, which then has added all of them in the
+// blocks' order and written the norm and the coefficient.
+template <int MAXS>
+__device__ __forceinline__ bool hand_in(const ClipSegs<MAXS> &g, double sum, const ClipWs &ws, float *out, double *red) {
+    __shared__ bool last;
+    sum = block_sum(sum, red);
     if (threadIdx.x == 0) {
-        part[blockIdx.x] = sum;
+        ws.part[blockIdx.x] = sum;
         __threadfence();
-        last = atomicInc(ticket, gridDim.x - 1) == gridDim.x - 1;
+        last = atomicInc(ws.ticket, gridDim.x - 1) == gridDim.x - 1;
     }
     __syncthreads();
-    if (!last) return;
+    if (!last) return false;
     __threadfence();
     double v = 0.0;
-    for (int b = threadIdx.x; b < int(gridDim.x); b += CT) v += __ldcg(part + b);
-    v = block_sum(v);
+    for (int b = threadIdx.x; b < int(gridDim.x); b += CT) v += __ldcg(ws.part + b);
+    v = block_sum(v, red);
     if (threadIdx.x == 0) {
-        if (!g.first_group) v += *total;
-        *total = v;
+        if (!g.first_group) v += *ws.total;
+        *ws.total = v;
         const float norm = float(sqrt(v)), c = g.max_norm / (norm + ADJ_CLIP_EPS);
         out[0] = norm;
         out[1] = c > 1.f ? 1.f : c;                      // NaN stays NaN
     }
+    return true;
 }
 
+// The block's chunks, the last one first: its values were read last.
 template <int MAXS>
-__global__ __launch_bounds__(CT) void k_clip_scale(const __grid_constant__ ClipSegs<MAXS> g, const float *out) {
-    const float f = out[1];
-    for (int64_t c = blockIdx.x; c < g.chunks; c += gridDim.x) {
-        const int s = seg_of(g, c);
-        if (!g.dst[s] || (g.dst[s] == g.src[s] && f == 1.f)) continue;
-        const int64_t k = c - g.first[s];
-        if (g.bf16[s]) chunk_scale<__nv_bfloat16>(g.src[s], g.dst[s], g.len[s], k, f);
-        else chunk_scale<float>(g.src[s], g.dst[s], g.len[s], k, f);
+__device__ __forceinline__ void scale_chunks(const ClipSegs<MAXS> &g, float f) {
+    const int64_t c0 = range(g, blockIdx.x);
+    int64_t c1 = range(g, int64_t(blockIdx.x) + 1);
+    for (int s = seg_of(g, c1 - 1); c1 > c0; --s) {
+        const int64_t c = max(c0, int64_t(g.first[s]));
+        if (g.dst[s] && !(g.dst[s] == g.src[s] && f == 1.f)) {
+            const int64_t i0 = (c - g.first[s]) * g.chunk, i1 = (c1 - g.first[s]) * g.chunk;
+            if (g.bf16[s]) part_scale<__nv_bfloat16>(g.src[s], g.dst[s], g.len[s], i0, i1, f);
+            else part_scale<float>(g.src[s], g.dst[s], g.len[s], i0, i1, f);
+        }
+        c1 = c;
     }
 }
 
-constexpr int CLIP_GRID = 152 * 8;
+template <int MAXS>
+__global__ __launch_bounds__(CT, CB) void k_clip_norm(const __grid_constant__ ClipSegs<MAXS> g, const ClipWs ws, float *out) {
+    __shared__ double red[CT / 32];
+    hand_in(g, sum_chunks(g), ws, out, red);
+}
+template <int MAXS>
+__global__ __launch_bounds__(CT, CB) void k_clip_scale(const __grid_constant__ ClipSegs<MAXS> g, const float *out) {
+    scale_chunks(g, out[1]);
+}
+// Both, with all blocks resident (cooperative launch).
+template <int MAXS>
+__global__ __launch_bounds__(CT, CB) void k_clip(const __grid_constant__ ClipSegs<MAXS> g, const ClipWs ws, float *out) {
+    __shared__ double red[CT / 32];
+    __shared__ float coef;
+    const unsigned turn = threadIdx.x == 0 ? ld_acquire(ws.turn) : 0u;     // before this block hands in
+    const double sum = sum_chunks(g);
+    const bool last = hand_in(g, sum, ws, out, red);
+    if (threadIdx.x == 0) {
+        if (last) {
+            __threadfence();
+            st_release(ws.turn, turn + 1);
+        } else {
+            int it = 0;
+            while (ld_acquire(ws.turn) == turn && ++it < SPIN_LIMIT) __nanosleep(32);
+            if (it == SPIN_LIMIT) record_timeout(ws.status);
+        }
+        coef = __ldcg(out + 1);
+    }
+    __syncthreads();
+    scale_chunks(g, coef);
+}
 
+// The next tensors from i on, as many as fit; returns where the next group starts.
 template <int MAXS>
 int64_t fill(ClipSegs<MAXS> &t, const adj_grad_seg *segs, int64_t i, int64_t nseg) {
     t.n = 0;
@@ -616,38 +738,61 @@ int64_t fill(ClipSegs<MAXS> &t, const adj_grad_seg *segs, int64_t i, int64_t nse
         if (segs[i].n == 0) continue;
         const bool bf = segs[i].dtype == ADJ_BF16;
         const int64_t bytes = (reinterpret_cast<uintptr_t>(segs[i].src) & 15u) + segs[i].n * (bf ? 2 : 4);
-        if (t.chunks + cdiv(bytes, CLIP_CHUNK) >= (int64_t(1) << 31)) break;
+        const int64_t chunks = cdiv(bytes, 16 * int64_t(t.chunk));
+        if (t.chunks + chunks >= (int64_t(1) << 31)) break;
         t.src[t.n] = segs[i].src;
         t.dst[t.n] = segs[i].dst;
         t.len[t.n] = segs[i].n;
         t.first[t.n] = int(t.chunks);
         t.bf16[t.n] = bf;
-        t.chunks += cdiv(bytes, CLIP_CHUNK);
+        t.chunks += chunks;
         ++t.n;
     }
+    while (i < nseg && segs[i].n == 0) ++i;
     return i;
 }
 
 template <int MAXS>
-cudaError_t clip(const adj_grad_seg *segs, int64_t nseg, float max_norm, float *out, char *ws, cudaStream_t st) {
-    double *part = reinterpret_cast<double *>(ws + WS_HEADER), *total = part + CLIP_GRID;
-    unsigned *ticket = reinterpret_cast<unsigned *>(ws) + 2;
+cudaError_t clip(const adj_grad_seg *segs, int64_t nseg, float max_norm, float *out, char *base, cudaStream_t st) {
+    ClipWs ws;
+    ws.status = reinterpret_cast<unsigned *>(base);
+    ws.ticket = ws.status + 2;
+    ws.turn = ws.status + 3;
+    ws.part = reinterpret_cast<double *>(base + WS_HEADER);
+    ws.total = ws.part + CLIP_GRID;
     ClipSegs<MAXS> t;
     t.max_norm = max_norm;
-    for (int pass = 0; pass < 2; ++pass) {
-        int64_t i = 0;
-        t.first_group = 1;
-        do {
+    t.first_group = 1;
+    // chunks of 16 KB, four loads in flight a thread; of 4 KB where those would leave SMs idle
+    int64_t bytes = 0;
+    for (int64_t i = 0; i < nseg; ++i) bytes += segs[i].n * (segs[i].dtype == ADJ_BF16 ? 2 : 4);
+    t.chunk = bytes < int64_t(152) * 16384 ? CT : 4 * CT;
+    auto grid = [&] { return unsigned(std::max<int64_t>(1, std::min<int64_t>(t.chunks, CLIP_GRID))); };
+    int64_t i = fill(t, segs, 0, nseg);
+    if (i >= nseg) {
+        ProfScope ps(K_CLIP_NORM, st);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(grid());
+        cfg.blockDim = dim3(CT);
+        cfg.stream = st;
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeCooperative;
+        at.val.cooperative = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, k_clip<MAXS>, t, ws, out);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
+    for (int pass = 0; pass < 2; ++pass)
+        for (i = 0; i < nseg;) {
             i = fill(t, segs, i, nseg);
-            const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(t.chunks, CLIP_GRID)));
             ProfScope ps(pass ? K_CLIP_SCALE : K_CLIP_NORM, st);
-            if (pass == 0) k_clip_norm<MAXS><<<grid, CT, 0, st>>>(t, part, total, ticket, out);
-            else k_clip_scale<MAXS><<<grid, CT, 0, st>>>(t, out);
+            if (pass == 0) k_clip_norm<MAXS><<<grid(), CT, 0, st>>>(t, ws, out);
+            else k_clip_scale<MAXS><<<grid(), CT, 0, st>>>(t, out);
             const cudaError_t e = cudaGetLastError();
             if (e != cudaSuccess) return e;
             t.first_group = 0;
-        } while (i < nseg);
-    }
+        }
     return cudaSuccess;
 }
 

@@ -24,14 +24,16 @@ LogProbs = namedtuple("LogProbs", "logp entropy lse top_id top_logp dlogits")
 
 
 def _check(name, x, shape, dtype, device):
-    if x.dtype is not dtype or x.device != device or tuple(x.shape) != shape:
-        raise ValueError(f"{name}: expected {dtype} {shape} on {device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
+    if x.dtype is not dtype or x.shape != shape or x.device != device:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
 
 
 def _dense(name, x, shape, dtype, device):
+    """The address of a dense tensor."""
     _check(name, x, shape, dtype, device)
     if not x.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor, got strides {x.stride()}")
+    return x.data_ptr()
 
 
 def _device(device):
