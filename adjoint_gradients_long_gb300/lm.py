@@ -57,28 +57,28 @@ class _Lin:
         self.device = _device(device)
         self.xt = torch.bfloat16 if x_bf16 else torch.float32
         self.lead = lead
-        self.qk, self.vo = (*lead, Hk, Dk), (*lead, H, Dv)
+        self.qk, self.vo, self.gates, self.states = (*lead, Hk, Dk), (*lead, H, Dv), (*lead, H), (lead[0], H, Dk, Dv)
         self.dims = lib.lin_dims(lead[0], T, H, Hk, Dk, Dv, lib.BF16 if x_bf16 else lib.F32, scale)
 
     def _pitch(self, name, x, shape):
+        """The distance of two tokens in x."""
         _check(name, x, shape, self.xt, self.device)
-        s, least = x.stride(), shape[-2] * shape[-1]
-        if x.numel() == 0:
+        least = shape[-2] * shape[-1]
+        if x.is_contiguous():
             return least
+        s = x.stride()
         ld = s[-3]
-        if s[-1] != 1 or s[-2] != shape[-1] or (len(shape) == 4 and shape[0] > 1 and s[0] != shape[1] * ld):
+        if s[-1] != 1 or s[-2] != shape[-1] or ld < least or (len(shape) == 4 and shape[0] > 1 and s[0] != shape[1] * ld):
             raise ValueError(f"{name}: heads must lie densely in a token and tokens evenly, got strides {s}")
-        return ld if x.numel() > least else least      # a token alone has no distance to the next one
+        return ld
 
     def _inputs(self, q, k, v, g):
         d = self.dims
         d.ldq, d.ldk, d.ldv = self._pitch("q", q, self.qk), self._pitch("k", k, self.qk), self._pitch("v", v, self.vo)
-        d.ldo = self.H * self.Dv
-        _dense("g", g, (*self.lead, self.H), torch.float32, self.device)
+        return q.data_ptr(), k.data_ptr(), v.data_ptr(), _dense("g", g, self.gates, torch.float32, self.device)
 
     def _state(self, name, s):
-        if s is not None:
-            _dense(name, s, (self.lead[0], self.H, self.Dk, self.Dv), torch.float32, self.device)
+        return None if s is None else _dense(name, s, self.states, torch.float32, self.device)
 
     def _empty(self, shape, dtype=None):
         return torch.empty(shape, dtype=dtype or self.xt, device=self.device)
@@ -109,25 +109,20 @@ class LinAttn(_Lin):
 
     def forward(self, q, k, v, g, s0=None):
         """(o [B,T,H,Dv], s1 [B,H,Dk,Dv]): the outputs and the state after the last token."""
-        self._inputs(q, k, v, g)
-        self._state("s0", s0)
-        lib.lin_fwd(self.dims, q, k, v, g, s0, self.o, self.s1, self.ws, self.ws_bytes)
+        lib.lin_fwd(self.dims, *self._inputs(q, k, v, g), self._state("s0", s0), self.o, self.s1, self.ws, self.ws_bytes)
         return self.o, self.s1
 
     def backward(self, q, k, v, g, go, s0=None, ds1=None):
         """(dq, dk, dv, dg, ds0) for the cotangents go of o and ds1 of s1."""
         if not self.has_backward:
             raise ValueError("this LinAttn was made without backward=True")
-        self._inputs(q, k, v, g)
-        self._state("s0", s0)
-        self._state("ds1", ds1)
-        _dense("go", go, self.vo, self.xt, self.device)
+        at = self._inputs(q, k, v, g)
+        at += self._state("s0", s0), _dense("go", go, self.vo, self.xt, self.device), self._state("ds1", ds1)
         for name, x, y in (("q", q, self.dq), ("k", k, self.dk), ("v", v, self.dv)):
             if x.stride() != y.stride() and x.numel():
                 # the gradients have the layout of their inputs
                 setattr(self, "d" + name, torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=x.device))
-        lib.lin_bwd(self.dims, q, k, v, g, s0, go, ds1, self.dq, self.dk, self.dv, self.dg, self.ds0, self.ws,
-                    self.ws_bytes)
+        lib.lin_bwd(self.dims, *at, self.dq, self.dk, self.dv, self.dg, self.ds0, self.ws, self.ws_bytes)
         return self.dq, self.dk, self.dv, self.dg, self.ds0
 
     def status(self, stream=None) -> int:
@@ -147,13 +142,13 @@ class LinStep(_Lin):
     def step(self, q, k, v, g, state, slots=None):
         """o [B,H,Dv].  slots [B] int32: sequence b's state is state[slots[b]] (a slot outside
         the pool: padding, a row of zeros); None: state[b]."""
-        self._inputs(q, k, v, g)
-        _dense("state", state, (state.shape[0], self.H, self.Dk, self.Dv), torch.float32, self.device)
+        n = state.shape[0]
+        pool = _dense("state", state, (n, self.H, self.Dk, self.Dv), torch.float32, self.device)
         if slots is not None:
-            _dense("slots", slots, self.lead, torch.int32, self.device)
-        elif state.shape[0] < self.lead[0]:
-            raise ValueError(f"state: {state.shape[0]} slots for {self.lead[0]} sequences")
-        lib.lin_step(self.dims, q, k, v, g, state, state.shape[0], slots, self.o)
+            slots = _dense("slots", slots, self.lead, torch.int32, self.device)
+        elif n < self.lead[0]:
+            raise ValueError(f"state: {n} slots for {self.lead[0]} sequences")
+        lib.lin_step(self.dims, *self._inputs(q, k, v, g), pool, n, slots, self.o)
         return self.o
 
 
@@ -164,6 +159,7 @@ class TokenLogProbs:
 
     def __init__(self, N, V, x_bf16=True, top=0, device="cuda"):
         self.N, self.V, self.top = N, V, top
+        self.rows, self.shape = (N,), (N, V)
         self.device = _device(device)
         self.xt = torch.bfloat16 if x_bf16 else torch.float32
         self.dims = lib.logprob_dims(N, V, V, V, lib.BF16 if x_bf16 else lib.F32, top)
@@ -176,7 +172,9 @@ class TokenLogProbs:
         self.dlogits = None
 
     def _row(self, name, x):
-        _check(name, x, (self.N, self.V), self.xt, self.device)
+        _check(name, x, self.shape, self.xt, self.device)
+        if x.is_contiguous():
+            return self.V
         if x.stride(1) != 1 and self.V > 1:
             raise ValueError(f"{name}: rows must be contiguous, got strides {x.stride()}")
         if self.N > 1 and x.stride(0) < self.V:
@@ -185,11 +183,10 @@ class TokenLogProbs:
 
     def _call(self, logits, targets, glp, gent, dlogits):
         self.dims.ld = self._row("logits", logits)
-        _dense("targets", targets, (self.N,), torch.int64, self.device)
         if dlogits is not None:
             self.dims.ldd = self._row("dlogits", dlogits)
-        lib.logprob(self.dims, logits, targets, self.logp, self.entropy, self.lse, self.top_id, self.top_logp, glp,
-                    gent, dlogits)
+        lib.logprob(self.dims, logits, _dense("targets", targets, self.rows, torch.int64, self.device), self.logp,
+                    self.entropy, self.lse, self.top_id, self.top_logp, glp, gent, dlogits)
         return LogProbs(self.logp, self.entropy, self.lse, self.top_id, self.top_logp, dlogits)
 
     def forward(self, logits, targets):
@@ -200,9 +197,9 @@ class TokenLogProbs:
         """LogProbs with dlogits for the cotangents glp of logp and gent of the entropy, [N] fp32.
         dlogits: the array to write, which may be the logits themselves; None: one of this
         object's."""
-        _dense("glp", glp, (self.N,), torch.float32, self.device)
+        _dense("glp", glp, self.rows, torch.float32, self.device)
         if gent is not None:
-            _dense("gent", gent, (self.N,), torch.float32, self.device)
+            _dense("gent", gent, self.rows, torch.float32, self.device)
         if dlogits is None:
             if self.dlogits is None:
                 self.dlogits = torch.empty(self.N, self.V, dtype=self.xt, device=self.device)
