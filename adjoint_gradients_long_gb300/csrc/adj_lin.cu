@@ -45,17 +45,33 @@ __device__ __forceinline__ void ld4(const __nv_bfloat16 *p, float (&v)[4]) {
     v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xFFFF0000u);
     v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
 }
-__device__ __forceinline__ void st1(float *p, float x) { *p = x; }
 
-// tile[t][d] = mul * x[t * ld + d] for t < LC, d < D; rows past len are zeros
-template <class T>
-__device__ __forceinline__ void load_tile(float *tile, const void *x, int64_t ld, int D, int len, float mul = 1.f) {
-    const int n4 = D >> 2;
-    for (int i = threadIdx.x; i < LC * n4; i += blockDim.x) {
-        const int t = i / n4, d = (i - t * n4) << 2;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (t < len) ld4(static_cast<const T *>(x) + t * ld + d, v);
-        *reinterpret_cast<float4 *>(tile + t * LP + d) = make_float4(v[0] * mul, v[1] * mul, v[2] * mul, v[3] * mul);
+// tile[t * pitch + d] = x[t * ld + d] for t < LC, d < D, rows past len zeros; sixteen threads a row.
+// Asynchronous: all of a block's tiles are in flight together, until loaded().
+__device__ __forceinline__ void load_tile(float *tile, int pitch, const float *x, int64_t ld, int D, int len) {
+#pragma unroll
+    for (int t = threadIdx.x >> 4; t < LC; t += 16)
+#pragma unroll
+        for (int d = (threadIdx.x & 15) << 2; d < 128; d += 64) {
+            if (d >= D) break;
+            const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(tile + t * pitch + d));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(x + (t < len ? t * ld + d : 0)),
+                         "r"(t < len ? 16 : 0)
+                         : "memory");
+        }
+}
+__device__ __forceinline__ void loaded() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+}
+// rows times w[t] * mul (w null: mul alone); a weight of zero drops a row whatever it holds
+__device__ __forceinline__ void scale_tile(float *tile, int pitch, int D, float mul, const float *w = nullptr) {
+    for (int t = threadIdx.x >> 4; t < LC; t += 16) {
+        const float m = w ? w[t] * mul : mul;
+        for (int d = (threadIdx.x & 15) << 2; d < D; d += 64) {
+            float4 *p = reinterpret_cast<float4 *>(tile + t * pitch + d);
+            *p = m == 0.f ? f4(0.f) : f4(m) * *p;
+        }
     }
 }
 
@@ -98,6 +114,53 @@ __device__ __forceinline__ void mm(float (&acc)[R][NC], const float *a, const fl
     }
 }
 
+// Outer-product forms: this thread's rows are 4 ty + q (and + 64), its columns 4 tx + q (and + 64),
+// so that 256 FMAs take 16 to 24 shared-memory wavefronts.  `cols`: columns in use.
+//   A_K: A(row, k) = a[row * ap + k], else a[k * ap + row];  B(k, col) = b[k * bp + col].
+template <int R, bool A_K>
+__device__ __forceinline__ void mm_outer(float (&acc)[R][8], const float *a, int ap, const float *b, int bp, int K, int cols) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    a += A_K ? 4 * ty * ap : 4 * ty;
+    b += 4 * tx;
+    const bool two = cols > 64;
+#pragma unroll 2
+    for (int k = 0; k < K; k += 4) {
+        float x[R][4];          // [row][k]
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (A_K) {
+                const float4 f = *reinterpret_cast<const float4 *>(a + ((r & 3) + 64 * (r >> 2)) * ap + k);
+                x[r][0] = f.x; x[r][1] = f.y; x[r][2] = f.z; x[r][3] = f.w;
+            } else if ((r & 3) == 0) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float4 f = *reinterpret_cast<const float4 *>(a + (k + u) * ap + 16 * r);
+                    x[r][u] = f.x; x[r + 1][u] = f.y; x[r + 2][u] = f.z; x[r + 3][u] = f.w;
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float4 y = *reinterpret_cast<const float4 *>(b + (k + u) * bp);
+            const float4 z = two ? *reinterpret_cast<const float4 *>(b + (k + u) * bp + 64) : f4(0.f);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                acc[r][0] = fmaf(x[r][u], y.x, acc[r][0]);
+                acc[r][1] = fmaf(x[r][u], y.y, acc[r][1]);
+                acc[r][2] = fmaf(x[r][u], y.z, acc[r][2]);
+                acc[r][3] = fmaf(x[r][u], y.w, acc[r][3]);
+            }
+            if (two)
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    acc[r][4] = fmaf(x[r][u], z.x, acc[r][4]);
+                    acc[r][5] = fmaf(x[r][u], z.y, acc[r][5]);
+                    acc[r][6] = fmaf(x[r][u], z.z, acc[r][6]);
+                    acc[r][7] = fmaf(x[r][u], z.w, acc[r][7]);
+                }
+        }
+    }
+}
+
 struct At {                     // one chunk of one head
     int64_t b, h, hk, n, t0, seq;
     int len;
@@ -117,38 +180,50 @@ __device__ __forceinline__ const T *row(const void *p, int64_t tok, int64_t ld, 
     return static_cast<const T *>(p) + tok * ld + head * D;
 }
 
+// Pitches of tiles D wide: rows an odd multiple of 16 bytes apart, so that 16-byte reads down a
+// column of rows meet no bank twice.
+__host__ __device__ __forceinline__ int pitch_of(int D) { return D + 4; }
+
 // Pass 1.  REV = false: S[n] = sum_j l_j k_j v_j^T; true: dS[n] = sum_i f_i q_i w_i^T.
-template <class T, bool REV>
-__global__ __launch_bounds__(256) void k_lin_chunk_state(const LinArgs a) {
+template <bool REV>
+__global__ __launch_bounds__(256, 3) void k_lin_chunk_state(const LinArgs a) {
     extern __shared__ float sm[];
-    float *A = sm, *B = A + LC * LP;
+    const int pk = pitch_of(a.Dk), pv = pitch_of(a.Dv);
+    // 64 rows more than a.Dk may be read across A's rows: they lie in B
+    float *A = sm, *B = A + LC * pk;
     __shared__ LinDecay<LC> D;
     const At at(a);
-    if (threadIdx.x < 32) D.fill(a.g + at.seq * a.H + at.h, a.H, at.len);
+    __shared__ float w[LC];
     if (REV) {
-        load_tile<T>(A, row<T>(a.q, at.seq, a.ldq, at.hk, a.Dk), a.ldq, a.Dk, at.len);
-        load_tile<T>(B, row<T>(a.go, at.seq, a.ldo, at.h, a.Dv), a.ldo, a.Dv, at.len, a.scale);
+        load_tile(A, pk, row<float>(a.q, at.seq, a.ldq, at.hk, a.Dk), a.ldq, a.Dk, at.len);
+        load_tile(B, pv, row<float>(a.go, at.seq, a.ldo, at.h, a.Dv), a.ldo, a.Dv, at.len);
     } else {
-        load_tile<T>(A, row<T>(a.k, at.seq, a.ldk, at.hk, a.Dk), a.ldk, a.Dk, at.len);
-        load_tile<T>(B, row<T>(a.v, at.seq, a.ldv, at.h, a.Dv), a.ldv, a.Dv, at.len);
+        load_tile(A, pk, row<float>(a.k, at.seq, a.ldk, at.hk, a.Dk), a.ldk, a.Dk, at.len);
+        load_tile(B, pv, row<float>(a.v, at.seq, a.ldv, at.h, a.Dv), a.ldv, a.Dv, at.len);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < LC * a.Dv; i += 256) {
-        const int t = i / a.Dv, d = i - t * a.Dv;
-        B[t * LP + d] *= REV ? D.first(t) : D.last(t);
+    if (threadIdx.x < 32) {
+        D.fill(a.g + at.seq * a.H + at.h, a.H, at.len);
+        __syncwarp();
+        for (int t = threadIdx.x; t < LC; t += 32) w[t] = REV ? D.first(t) : D.last(t);
     }
+    loaded();
+    scale_tile(A, pk, a.Dk, REV ? a.scale : 1.f, w);
     __syncthreads();
-    float acc[8][8] = {};
-    mm<8, 8, 1, LP, LP, 1>(acc, A, B, LC, a.Dv);
     float *S = (REV ? a.dS : a.S) + at.state(a);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    // 64 rows of the state at a time
+    for (int d0 = 0; d0 < a.Dk; d0 += 64) {
+        float acc[4][8] = {};
+        mm_outer<4, false>(acc, A + d0, pk, B, pv, LC, a.Dv);
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const int d = ty + 16 * r, e = tx + 16 * c;
-            if (d < a.Dk && e < a.Dv) S[d * a.Dv + e] = acc[r][c];
-        }
+            for (int c = 0; c < 8; c += 4) {
+                const int d = d0 + 4 * ty + r, e = 4 * tx + 16 * c;
+                if (d < a.Dk && e < a.Dv)
+                    *reinterpret_cast<float4 *>(S + d * a.Dv + e) = make_float4(acc[r][c], acc[r][c + 1], acc[r][c + 2], acc[r][c + 3]);
+            }
+    }
     if (threadIdx.x == 0) (REV ? a.dtot : a.tot)[(at.b * a.H + at.h) * a.NC + at.n] = D.total();
 }
 
@@ -183,54 +258,72 @@ __global__ __launch_bounds__(128) void k_lin_scan(const LinArgs a, int64_t NC, i
     if (fin) reinterpret_cast<float4 *>(fin)[bh * n4 + i] = c;
 }
 
-__device__ __forceinline__ void load_state(float *tile, const float *S, int Dk, int Dv) {
-    const int n4 = Dv >> 2;
-    for (int i = threadIdx.x; i < Dk * n4; i += blockDim.x) {
-        const int d = i / n4, e = (i - d * n4) << 2;
-        *reinterpret_cast<float4 *>(tile + d * LP + e) = *reinterpret_cast<const float4 *>(S + int64_t(d) * Dv + e);
-    }
+__device__ __forceinline__ void load_state(float *tile, int pitch, const float *S, int Dk, int Dv) {
+    for (int d = threadIdx.x >> 4; d < Dk; d += 16)
+#pragma unroll
+        for (int e = (threadIdx.x & 15) << 2; e < 128; e += 64) {
+            if (e >= Dv) break;
+            const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(tile + d * pitch + e));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(S + int64_t(d) * Dv + e) : "memory");
+        }
 }
 
 // Pass 3 of the forward pass.
-template <class T>
-__global__ __launch_bounds__(256) void k_lin_out(const LinArgs a) {
+__global__ __launch_bounds__(256, 2) void k_lin_out(const LinArgs a) {
     extern __shared__ float sm[];
-    float *Q = sm, *K = Q + LC * LP, *V = K + LC * LP, *S = V + LC * LP, *P = S + 128 * LP;
+    const int pk = pitch_of(a.Dk), pv = pitch_of(a.Dv);
+    float *Q = sm, *V = Q + LC * pk, *S = V + LC * pv, *K = S + a.Dk * pv, *P = K;       // P in K's place
     __shared__ LinDecay<LC> D;
     const At at(a);
+    load_tile(Q, pk, row<float>(a.q, at.seq, a.ldq, at.hk, a.Dk), a.ldq, a.Dk, at.len);
+    load_tile(K, pk, row<float>(a.k, at.seq, a.ldk, at.hk, a.Dk), a.ldk, a.Dk, at.len);
+    load_tile(V, pv, row<float>(a.v, at.seq, a.ldv, at.h, a.Dv), a.ldv, a.Dv, at.len);
+    load_state(S, pv, a.S + at.state(a), a.Dk, a.Dv);
     if (threadIdx.x < 32) D.fill(a.g + at.seq * a.H + at.h, a.H, at.len);
-    load_tile<T>(Q, row<T>(a.q, at.seq, a.ldq, at.hk, a.Dk), a.ldq, a.Dk, at.len);
-    load_tile<T>(K, row<T>(a.k, at.seq, a.ldk, at.hk, a.Dk), a.ldk, a.Dk, at.len);
-    load_tile<T>(V, row<T>(a.v, at.seq, a.ldv, at.h, a.Dv), a.ldv, a.Dv, at.len);
-    load_state(S, a.S + at.state(a), a.Dk, a.Dv);
-    __syncthreads();
+    loaded();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    // rows 4 ty + r, columns tx + 16 c
     float p[4][4] = {};
-    mm<4, 4, LP, 1, 1, LP>(p, Q, K, a.Dk, LC);
+#pragma unroll 2
+    for (int k = 0; k < a.Dk; k += 4) {
+        float4 x[4], y[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r) x[r] = *reinterpret_cast<const float4 *>(Q + (4 * ty + r) * pk + k);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int i = ty + 16 * r, j = tx + 16 * c;
-            P[i * PP + j] = j <= i ? p[r][c] * D.pair(i, j) : 0.f;
-        }
+        for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4 *>(K + (tx + 16 * c) * pk + k);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                p[r][c] = fmaf(x[r].x, y[c].x, fmaf(x[r].y, y[c].y, fmaf(x[r].z, y[c].z, fmaf(x[r].w, y[c].w, p[r][c]))));
+    }
     float acc[4][8] = {};
-    mm<4, 8, LP, 1, LP, 1>(acc, Q, S, a.Dk, a.Dv);
+    mm_outer<4, true>(acc, Q, pk, S, pv, a.Dk, a.Dv);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const float f = D.first(ty + 16 * r);
+        const float f = D.first(4 * ty + r);
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[r][c] = f == 0.f ? 0.f : acc[r][c] * f;
     }
     __syncthreads();
-    mm<4, 8, PP, 1, LP, 1>(acc, P, V, LC, a.Dv);
-    T *o = static_cast<T *>(a.o) + at.seq * a.ldo + at.h * a.Dv;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const int i = ty + 16 * r, e = tx + 16 * c;
-            if (i < at.len && e < a.Dv) st1(o + i * a.ldo + e, acc[r][c] * a.scale);
+        for (int c = 0; c < 4; ++c) {
+            const int i = 4 * ty + r, j = tx + 16 * c;
+            P[i * PP + j] = j <= i ? p[r][c] * D.pair(i, j) : 0.f;
+        }
+    __syncthreads();
+    // the warp's last row bounds its sums
+    mm_outer<4, true>(acc, P, PP, V, pv, 8 * (ty >> 1) + 8, a.Dv);
+    float *o = static_cast<float *>(a.o) + at.seq * a.ldo + at.h * a.Dv;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 8; c += 4) {
+            const int i = 4 * ty + r, e = 4 * tx + 16 * c;
+            if (i < at.len && e < a.Dv)
+                st4(o + i * a.ldo + e, make_float4(acc[r][c] * a.scale, acc[r][c + 1] * a.scale, acc[r][c + 2] * a.scale, acc[r][c + 3] * a.scale));
         }
 }
 
@@ -242,7 +335,6 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 // dq or dk of one head: to the output, or (shared heads) to the fp32 partials
-template <class T>
 __device__ __forceinline__ void put_grad(const LinArgs &a, const At &at, const float (&acc)[4][8], void *out, float *part,
                                          int64_t ld) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -253,24 +345,25 @@ __device__ __forceinline__ void put_grad(const LinArgs &a, const At &at, const f
             const int i = ty + 16 * r, d = tx + 16 * c;
             if (i >= at.len || d >= a.Dk) continue;
             if (part) part[((at.seq + i) * a.H + at.h) * a.Dk + d] = acc[r][c];
-            else st1(static_cast<T *>(out) + (at.seq + i) * ld + at.hk * a.Dk + d, acc[r][c]);
+            else static_cast<float *>(out)[(at.seq + i) * ld + at.hk * a.Dk + d] = acc[r][c];
         }
 }
 
 // Pass 3 of the backward pass.
-template <class T>
 __global__ __launch_bounds__(256) void k_lin_grad(const LinArgs a) {
     extern __shared__ float sm[];
     float *Q = sm, *K = Q + LC * LP, *V = K + LC * LP, *W = V + LC * LP, *S = W + LC * LP, *P = S + 128 * LP;
     __shared__ LinDecay<LC> D;
     __shared__ float fs[LC], cs[LC], rs[LC], zs[8];
     const At at(a);
+    load_tile(Q, LP, row<float>(a.q, at.seq, a.ldq, at.hk, a.Dk), a.ldq, a.Dk, at.len);
+    load_tile(K, LP, row<float>(a.k, at.seq, a.ldk, at.hk, a.Dk), a.ldk, a.Dk, at.len);
+    load_tile(V, LP, row<float>(a.v, at.seq, a.ldv, at.h, a.Dv), a.ldv, a.Dv, at.len);
+    load_tile(W, LP, row<float>(a.go, at.seq, a.ldo, at.h, a.Dv), a.ldo, a.Dv, at.len);
+    load_state(S, LP, a.S + at.state(a), a.Dk, a.Dv);
     if (threadIdx.x < 32) D.fill(a.g + at.seq * a.H + at.h, a.H, at.len);
-    load_tile<T>(Q, row<T>(a.q, at.seq, a.ldq, at.hk, a.Dk), a.ldq, a.Dk, at.len);
-    load_tile<T>(K, row<T>(a.k, at.seq, a.ldk, at.hk, a.Dk), a.ldk, a.Dk, at.len);
-    load_tile<T>(V, row<T>(a.v, at.seq, a.ldv, at.h, a.Dv), a.ldv, a.Dv, at.len);
-    load_tile<T>(W, row<T>(a.go, at.seq, a.ldo, at.h, a.Dv), a.ldo, a.Dv, at.len, a.scale);
-    load_state(S, a.S + at.state(a), a.Dk, a.Dv);
+    loaded();
+    scale_tile(W, LP, a.Dv, a.scale);
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 
@@ -328,7 +421,7 @@ __global__ __launch_bounds__(256) void k_lin_grad(const LinArgs a) {
         }
         __syncthreads();        // P holds R
         mm<4, 8, PP, 1, LP, 1>(acc, P, K, LC, a.Dk);
-        put_grad<T>(a, at, acc, a.dq, a.pq, a.ldq);
+        put_grad(a, at, acc, a.dq, a.pq, a.ldq);
     }
     // <Z, S>, then Z in S's place
     {
@@ -365,7 +458,7 @@ __global__ __launch_bounds__(256) void k_lin_grad(const LinArgs a) {
             if (tx == 0) cs[j] = dot;
         }
         mm<4, 8, 1, PP, LP, 1>(acc, P, Q, LC, a.Dk);
-        put_grad<T>(a, at, acc, a.dk, a.pk, a.ldk);
+        put_grad(a, at, acc, a.dk, a.pk, a.ldk);
     }
     __syncthreads();            // P is free, cs is written
 #pragma unroll
@@ -384,13 +477,13 @@ __global__ __launch_bounds__(256) void k_lin_grad(const LinArgs a) {
         }
         __syncthreads();
         mm<4, 8, 1, PP, LP, 1>(acc, P, W, LC, a.Dv);
-        T *dv = static_cast<T *>(a.dv) + at.seq * a.ldv + at.h * a.Dv;
+        float *dv = static_cast<float *>(a.dv) + at.seq * a.ldv + at.h * a.Dv;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const int j = ty + 16 * r, e = tx + 16 * c;
-                if (j < at.len && e < a.Dv) st1(dv + j * a.ldv + e, acc[r][c]);
+                if (j < at.len && e < a.Dv) dv[j * a.ldv + e] = acc[r][c];
             }
     }
     // dg
@@ -502,36 +595,35 @@ cudaError_t big_smem(K kern, size_t bytes) {
         if (e_ != cudaSuccess) return e_;     \
     } while (0)
 
-constexpr size_t SM_STATE = size_t(2 * LC * LP) * 4, SM_OUT = size_t(3 * LC * LP + 128 * LP + LC * PP) * 4,
-                 SM_GRAD = size_t(4 * LC * LP + 128 * LP + LC * PP) * 4;
+constexpr size_t SM_GRAD = size_t(4 * LC * LP + 128 * LP + LC * PP) * 4;
 
-template <class T, bool REV>
+template <bool REV>
 cudaError_t states(const LinArgs &a, cudaStream_t st) {
-    const dim3 grid(unsigned(a.NC), a.H, unsigned(a.B));
-    if (a.NC) {
+    {
         ProfScope ps(K_LIN_STATE, st);
-        LIN_CUDA(big_smem(k_lin_chunk_state<T, REV>, SM_STATE));
-        k_lin_chunk_state<T, REV><<<grid, 256, SM_STATE, st>>>(a);
+        const size_t smem = size_t(LC) * (pitch_of(a.Dk) + pitch_of(a.Dv)) * 4 + 256;
+        LIN_CUDA(big_smem(k_lin_chunk_state<REV>, smem));
+        k_lin_chunk_state<REV><<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, smem, st>>>(a);
         LIN_CUDA(cudaGetLastError());
     }
     return launch_lin_scan(a, a.NC, REV ? 2 : 1, st);
 }
 
-template <class T>
-cudaError_t fwd(const LinArgs &a, cudaStream_t st) {
-    LIN_CUDA((states<T, false>(a, st)));
+cudaError_t fwd_f32(const LinArgs &a, cudaStream_t st) {
+    LIN_CUDA(states<false>(a, st));
     ProfScope ps(K_LIN_OUT, st);
-    LIN_CUDA(big_smem(k_lin_out<T>, SM_OUT));
-    k_lin_out<T><<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, SM_OUT, st>>>(a);
+    const size_t smem = (size_t(LC + a.Dk) * pitch_of(a.Dv) + LC * (pitch_of(a.Dk) + std::max(pitch_of(a.Dk), PP))) * 4;
+    LIN_CUDA(big_smem(k_lin_out, smem));
+    k_lin_out<<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 cudaError_t bwd_f32(const LinArgs &a, cudaStream_t st) {
-    LIN_CUDA((states<float, false>(a, st)));
-    LIN_CUDA((states<float, true>(a, st)));
+    LIN_CUDA(states<false>(a, st));
+    LIN_CUDA(states<true>(a, st));
     ProfScope ps(K_LIN_GRAD, st);
-    LIN_CUDA(big_smem(k_lin_grad<float>, SM_GRAD));
-    k_lin_grad<float><<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, SM_GRAD, st>>>(a);
+    LIN_CUDA(big_smem(k_lin_grad, SM_GRAD));
+    k_lin_grad<<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, SM_GRAD, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -597,7 +689,7 @@ void lin_ws_carve(LinArgs &a, bool bwd, bool bf16, void *base) { carve(a, bwd, b
 
 cudaError_t launch_lin_fwd(const LinArgs &a, bool bf16, unsigned *status, cudaStream_t st) {
     if (a.NC == 0) return launch_lin_scan(a, 0, 1, st);      // s1 = s0
-    return bf16 ? launch_lin_tc_fwd(a, status, st) : fwd<float>(a, st);
+    return bf16 ? launch_lin_tc_fwd(a, status, st) : fwd_f32(a, st);
 }
 cudaError_t launch_lin_bwd(const LinArgs &a, bool bf16, unsigned *status, cudaStream_t st) {
     if (a.NC == 0) return launch_lin_scan(a, 0, 2, st);       // ds0 = ds1

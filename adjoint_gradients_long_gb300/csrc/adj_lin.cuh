@@ -30,6 +30,29 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// A sum kept as hi + lo, 48 bits: the fp64 pipe is too slow for one warp to keep up with a chunk.
+struct Sum2 {
+    float hi, lo;
+    __device__ __forceinline__ static Sum2 two(float a, float b) {      // a + b exactly
+        const float s = a + b, t = s - a;
+        return Sum2{s, (a - (s - t)) + (b - t)};
+    }
+    __device__ __forceinline__ static Sum2 log2_of(float x) {           // x log2 e
+        constexpr float H = 1.44269502162933349609375f, L = 1.925963033500011079e-8f;
+        const float p = x * H;
+        return Sum2{p, fmaf(x, L, fmaf(x, H, -p))};
+    }
+    __device__ __forceinline__ Sum2 operator+(Sum2 o) const {
+        const Sum2 s = two(hi, o.hi);
+        const float l = s.lo + (lo + o.lo), h = s.hi + l;
+        return Sum2{h, l - (h - s.hi)};
+    }
+    __device__ __forceinline__ Sum2 operator-(Sum2 o) const { return *this + Sum2{-o.hi, -o.lo}; }
+    __device__ __forceinline__ float value() const { return hi + lo; }
+    __device__ __forceinline__ Sum2 up(int d) const { return Sum2{__shfl_up_sync(~0u, hi, d), __shfl_up_sync(~0u, lo, d)}; }
+    __device__ __forceinline__ Sum2 from(int l) const { return Sum2{__shfl_sync(~0u, hi, l), __shfl_sync(~0u, lo, l)}; }
+};
+
 // The decays of one chunk.  With g_t the tokens' log decays in powers of two, G_t their
 // inclusive sum from the chunk's start and r_t the number of new starts up to t, the decay
 // from token j to token i >= j is 2^(G_i - G_j) where r_i = r_j, and zero otherwise.  G is kept
@@ -52,42 +75,38 @@ struct LinDecay {
     __device__ void fill(const float *g, int64_t pitch, int len) {
         const int lane = threadIdx.x & 31;
         constexpr int PER = C / 32;
-        double s[PER], sum = 0.0;
+        Sum2 s[PER], sum{0.f, 0.f};
         int c[PER], cnt = 0;
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
             const int t = lane * PER + u;
             const float x = t < len ? __ldg(g + t * pitch) : 0.f;
             const bool cut = x < LIN_RESET;
-            sum += cut ? 0.0 : double(x) * 1.4426950408889634;
+            sum = sum + Sum2::log2_of(cut ? 0.f : x);
             cnt += cut;
             s[u] = sum;
             c[u] = cnt;
         }
-        double run = sum;
+        Sum2 run = sum;
         int rc = cnt;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const double a = __shfl_up_sync(~0u, run, d);
+            const Sum2 a = run.up(d);
             const int b = __shfl_up_sync(~0u, rc, d);
             if (lane >= d) {
-                run += a;
+                run = a + run;
                 rc += b;
             }
         }
-        double before = __shfl_up_sync(~0u, run, 1);
-        int cb = __shfl_up_sync(~0u, rc, 1);
-        if (lane == 0) {
-            before = 0.0;
-            cb = 0;
-        }
+        Sum2 before = run.up(1);
+        if (lane == 0) before = Sum2{0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
-            const double G = before + s[u];
+            const Sum2 G = before + s[u];
             const int t = lane * PER + u;
-            hi[t] = float(G);
-            lo[t] = float(G - double(hi[t]));
-            r[t] = cb + c[u];
+            hi[t] = G.hi;
+            lo[t] = G.lo;
+            r[t] = rc - cnt + c[u];
         }
     }
 };

@@ -35,29 +35,6 @@ constexpr int TC_BLOCK = (CW + 4) * 32;
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// A sum kept as hi + lo, 48 bits: the fp64 pipe is too slow for one warp to keep up with a chunk.
-struct Sum2 {
-    float hi, lo;
-    __device__ __forceinline__ static Sum2 two(float a, float b) {      // a + b exactly
-        const float s = a + b, t = s - a;
-        return Sum2{s, (a - (s - t)) + (b - t)};
-    }
-    __device__ __forceinline__ static Sum2 log2_of(float x) {           // x log2 e
-        constexpr float H = 1.44269502162933349609375f, L = 1.925963033500011079e-8f;
-        const float p = x * H;
-        return Sum2{p, fmaf(x, L, fmaf(x, H, -p))};
-    }
-    __device__ __forceinline__ Sum2 operator+(Sum2 o) const {
-        const Sum2 s = two(hi, o.hi);
-        const float l = s.lo + (lo + o.lo), h = s.hi + l;
-        return Sum2{h, l - (h - s.hi)};
-    }
-    __device__ __forceinline__ Sum2 operator-(Sum2 o) const { return *this + Sum2{-o.hi, -o.lo}; }
-    __device__ __forceinline__ float value() const { return hi + lo; }
-    __device__ __forceinline__ Sum2 up(int d) const { return Sum2{__shfl_up_sync(~0u, hi, d), __shfl_up_sync(~0u, lo, d)}; }
-    __device__ __forceinline__ Sum2 from(int l) const { return Sum2{__shfl_sync(~0u, hi, l), __shfl_sync(~0u, lo, l)}; }
-};
-
 // The decays of one chunk, by blocks of 32 tokens.  In powers of two, with G_t the sum of the
 // log decays from the chunk's start to t and E_b its value at block b's last token:
 //   x[t] = G_t - E_b (b the block of t), E as hi + lo; r counts new starts
