@@ -584,11 +584,6 @@ __global__ __launch_bounds__(256) void k_lin_step(const LinArgs a, float *__rest
     }
 }
 
-template <class K>
-cudaError_t big_smem(K kern, size_t bytes) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-}
-
 #define LIN_CUDA(x)                           \
     do {                                      \
         cudaError_t e_ = (x);                 \
@@ -602,7 +597,7 @@ cudaError_t states(const LinArgs &a, cudaStream_t st) {
     {
         ProfScope ps(K_LIN_STATE, st);
         const size_t smem = size_t(LC) * (pitch_of(a.Dk) + pitch_of(a.Dv)) * 4 + 256;
-        LIN_CUDA(big_smem(k_lin_chunk_state<REV>, smem));
+        LIN_CUDA(allow_smem<k_lin_chunk_state<REV>>());
         k_lin_chunk_state<REV><<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, smem, st>>>(a);
         LIN_CUDA(cudaGetLastError());
     }
@@ -613,7 +608,7 @@ cudaError_t fwd_f32(const LinArgs &a, cudaStream_t st) {
     LIN_CUDA(states<false>(a, st));
     ProfScope ps(K_LIN_OUT, st);
     const size_t smem = (size_t(LC + a.Dk) * pitch_of(a.Dv) + LC * (pitch_of(a.Dk) + std::max(pitch_of(a.Dk), PP))) * 4;
-    LIN_CUDA(big_smem(k_lin_out, smem));
+    LIN_CUDA(allow_smem<k_lin_out>());
     k_lin_out<<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, smem, st>>>(a);
     return cudaGetLastError();
 }
@@ -622,7 +617,7 @@ cudaError_t bwd_f32(const LinArgs &a, cudaStream_t st) {
     LIN_CUDA(states<false>(a, st));
     LIN_CUDA(states<true>(a, st));
     ProfScope ps(K_LIN_GRAD, st);
-    LIN_CUDA(big_smem(k_lin_grad, SM_GRAD));
+    LIN_CUDA(allow_smem<k_lin_grad>());
     k_lin_grad<<<dim3(unsigned(a.NC), a.H, unsigned(a.B)), 256, SM_GRAD, st>>>(a);
     return cudaGetLastError();
 }

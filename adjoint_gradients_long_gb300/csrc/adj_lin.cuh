@@ -1,8 +1,25 @@
 // adj_lin.cuh -- linear attention with a decay for each head: what its kernels share.
 #pragma once
+#include <atomic>
+
 #include "adj_internal.cuh"
 
 namespace adj {
+
+// The kernel's limit of dynamic shared memory, raised once a device (the call costs as much as a
+// launch): to the most that any launch of it may ask for.
+template <auto Kern>
+cudaError_t allow_smem(size_t most = 232448 - 8192) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // One call, sizes and arrays resolved on the host.
 struct LinArgs {

@@ -1220,7 +1220,7 @@ cudaError_t run_states(const LinArgs &a, const LinSplit &sp, int dirs, unsigned 
              map_states(&m.dir[1].hi, a.zhi, a.Dv, a.Dk, n, KW) && map_states(&m.dir[1].lo, a.zlo, a.Dv, a.Dk, n, KW);
     if (!ok) return cudaErrorInvalidValue;
     constexpr size_t smem = state_smem<KW, VW, KEEP>();
-    LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_state<KW, VW, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+    LIN_CUDA((allow_smem<k_lin_tc_state<KW, VW, KEEP>>(smem)));
     ProfScope ps(K_LIN_STATE, st);
     k_lin_tc_state<KW, VW, KEEP><<<unsigned(a.B * a.H * sp.nseg * dirs), TC_BLOCK, smem, st>>>(m, a, sp.nseg, sp.cps, status);
     return cudaGetLastError();
@@ -1239,7 +1239,7 @@ cudaError_t run_fwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cuda
         LIN_CUDA(launch_lin_scan(a, sp.nseg, 1, st));
     }
     constexpr size_t smem = fwd_smem<KW, VW>();
-    LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_fwd<KW, VW>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+    LIN_CUDA((allow_smem<k_lin_tc_fwd<KW, VW>>(smem)));
     ProfScope ps(K_LIN_OUT, st);
     // the state is a result only where no segments' states were joined: otherwise it meets bf16 next
     const int parts = sp.nseg == 1 && a.s1 ? 3 : 2;
@@ -1267,7 +1267,7 @@ cudaError_t run_bwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cuda
     }
     LIN_CUDA((run_states<KW, VW, true>(a, sp, 2, status, st)));
     constexpr size_t smem = grad_smem<KW, VW>();
-    LIN_CUDA(cudaFuncSetAttribute(k_lin_tc_grad<KW, VW>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+    LIN_CUDA((allow_smem<k_lin_tc_grad<KW, VW>>(smem)));
     ProfScope ps(K_LIN_GRAD, st);
     k_lin_tc_grad<KW, VW><<<unsigned(std::min<int64_t>(n, 152)), TC_BLOCK, smem, st>>>(m, a, n, status);
     return cudaGetLastError();

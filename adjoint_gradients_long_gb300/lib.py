@@ -138,6 +138,24 @@ def _stream(stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def bind(name, *first):
+    """The C entry point `name` with its first arguments fixed, as a function of the rest (addresses
+    as ints or None), for callers that make the same call many times; raises like the others."""
+    f = getattr(load(), name)
+
+    def call(*rest):
+        st = f(*first, *rest)
+        if st != 0:
+            raise AdjError(name, st)
+    return call
+
+
+def raw_stream(device) -> int:
+    """torch's current stream of a CUDA device, as an address."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index) if device.index is not None else 0
+
+
 def _check(st: int, what: str):
     if st != 0:
         raise AdjError(what, st)

@@ -14,11 +14,13 @@ library checks its own arguments (lib.AdjError).
 """
 from __future__ import annotations
 
+import ctypes
 from collections import namedtuple
 
 import torch
 
 from . import lib
+from .lib import raw_stream
 
 LogProbs = namedtuple("LogProbs", "logp entropy lse top_id top_logp dlogits")
 
@@ -59,6 +61,7 @@ class _Lin:
         self.lead = lead
         self.qk, self.vo, self.gates, self.states = (*lead, Hk, Dk), (*lead, H, Dv), (*lead, H), (lead[0], H, Dk, Dv)
         self.dims = lib.lin_dims(lead[0], T, H, Hk, Dk, Dv, lib.BF16 if x_bf16 else lib.F32, scale)
+        self._pd = ctypes.byref(self.dims)
 
     def _pitch(self, name, x, shape):
         """The distance of two tokens in x."""
@@ -102,6 +105,8 @@ class LinAttn(_Lin):
         self.o = self._empty(self.vo)
         self.s1 = self._empty((B, H, Dk, Dv), torch.float32)
         self.has_backward = backward
+        self._fwd, self._bwd = lib.bind("adj_lin_fwd", self._pd), lib.bind("adj_lin_bwd", self._pd)
+        self._out = self.o.data_ptr(), self.s1.data_ptr(), self.ws.data_ptr(), self.ws_bytes
         if backward:
             self.dq, self.dk, self.dv = self._empty(self.qk), self._empty(self.qk), self._empty(self.vo)
             self.dg = self._empty((B, T, H), torch.float32)
@@ -109,7 +114,7 @@ class LinAttn(_Lin):
 
     def forward(self, q, k, v, g, s0=None):
         """(o [B,T,H,Dv], s1 [B,H,Dk,Dv]): the outputs and the state after the last token."""
-        lib.lin_fwd(self.dims, *self._inputs(q, k, v, g), self._state("s0", s0), self.o, self.s1, self.ws, self.ws_bytes)
+        self._fwd(*self._inputs(q, k, v, g), self._state("s0", s0), *self._out, raw_stream(self.device))
         return self.o, self.s1
 
     def backward(self, q, k, v, g, go, s0=None, ds1=None):
@@ -122,7 +127,8 @@ class LinAttn(_Lin):
             if x.stride() != y.stride() and x.numel():
                 # the gradients have the layout of their inputs
                 setattr(self, "d" + name, torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=x.device))
-        lib.lin_bwd(self.dims, *at, self.dq, self.dk, self.dv, self.dg, self.ds0, self.ws, self.ws_bytes)
+        self._bwd(*at, self.dq.data_ptr(), self.dk.data_ptr(), self.dv.data_ptr(), self.dg.data_ptr(), self.ds0.data_ptr(),
+                  *self._out[2:], raw_stream(self.device))
         return self.dq, self.dk, self.dv, self.dg, self.ds0
 
     def status(self, stream=None) -> int:
@@ -138,6 +144,7 @@ class LinStep(_Lin):
         if lib.lin_workspace_bytes(self.dims, lib.OP_LIN_FWD) == 0:
             raise ValueError("unsupported linear-attention sizes")
         self.o = self._empty(self.vo)
+        self._step, self._out = lib.bind("adj_lin_step", self._pd), self.o.data_ptr()
 
     def step(self, q, k, v, g, state, slots=None):
         """o [B,H,Dv].  slots [B] int32: sequence b's state is state[slots[b]] (a slot outside
@@ -148,7 +155,7 @@ class LinStep(_Lin):
             slots = _dense("slots", slots, self.lead, torch.int32, self.device)
         elif n < self.lead[0]:
             raise ValueError(f"state: {n} slots for {self.lead[0]} sequences")
-        lib.lin_step(self.dims, *self._inputs(q, k, v, g), pool, n, slots, self.o)
+        self._step(*self._inputs(q, k, v, g), pool, n, slots, self._out, raw_stream(self.device))
         return self.o
 
 
@@ -170,6 +177,10 @@ class TokenLogProbs:
         self.top_id = torch.empty(N, top, dtype=torch.int32, device=self.device) if top else None
         self.top_logp = f(N, top) if top else None
         self.dlogits = None
+        self._logprob = lib.bind("adj_logprob", ctypes.byref(self.dims))
+        self._out = tuple(None if x is None else x.data_ptr()
+                          for x in (self.logp, self.entropy, self.lse, self.top_id, self.top_logp))
+        self._plain = LogProbs(self.logp, self.entropy, self.lse, self.top_id, self.top_logp, None)
 
     def _row(self, name, x):
         _check(name, x, self.shape, self.xt, self.device)
@@ -181,30 +192,28 @@ class TokenLogProbs:
             raise ValueError(f"{name}: rows must not overlap, got strides {x.stride()}")
         return x.stride(0) if self.N > 1 else self.V
 
-    def _call(self, logits, targets, glp, gent, dlogits):
-        self.dims.ld = self._row("logits", logits)
-        if dlogits is not None:
-            self.dims.ldd = self._row("dlogits", dlogits)
-        lib.logprob(self.dims, logits, _dense("targets", targets, self.rows, torch.int64, self.device), self.logp,
-                    self.entropy, self.lse, self.top_id, self.top_logp, glp, gent, dlogits)
-        return LogProbs(self.logp, self.entropy, self.lse, self.top_id, self.top_logp, dlogits)
-
     def forward(self, logits, targets):
         """LogProbs without a gradient."""
-        return self._call(logits, targets, None, None, None)
+        self.dims.ld = self._row("logits", logits)
+        y = _dense("targets", targets, self.rows, torch.int64, self.device)
+        self._logprob(logits.data_ptr(), y, *self._out, None, None, None, raw_stream(self.device))
+        return self._plain
 
     def gradient(self, logits, targets, glp, gent=None, dlogits=None):
         """LogProbs with dlogits for the cotangents glp of logp and gent of the entropy, [N] fp32.
         dlogits: the array to write, which may be the logits themselves; None: one of this
         object's."""
-        _dense("glp", glp, self.rows, torch.float32, self.device)
-        if gent is not None:
-            _dense("gent", gent, self.rows, torch.float32, self.device)
+        self.dims.ld = self._row("logits", logits)
+        y = _dense("targets", targets, self.rows, torch.int64, self.device)
+        cot = (_dense("glp", glp, self.rows, torch.float32, self.device),
+               None if gent is None else _dense("gent", gent, self.rows, torch.float32, self.device))
         if dlogits is None:
             if self.dlogits is None:
                 self.dlogits = torch.empty(self.N, self.V, dtype=self.xt, device=self.device)
             dlogits = self.dlogits
-        return self._call(logits, targets, glp, gent, dlogits)
+        self.dims.ldd = self._row("dlogits", dlogits)
+        self._logprob(logits.data_ptr(), y, *self._out, *cot, dlogits.data_ptr(), raw_stream(self.device))
+        return self._plain._replace(dlogits=dlogits)
 
 
 class GradClip:
@@ -229,8 +238,10 @@ class GradClip:
         self.ws = _workspace(self.ws_bytes, self.device)
         self.result = torch.empty(2, dtype=torch.float32, device=self.device)
         self.norm, self.coef = self.result[0], self.result[1]
+        self._clip = lib.bind("adj_grad_clip", self.segs, len(self.grads))
+        self._out = self.result.data_ptr(), self.ws.data_ptr(), self.ws_bytes
 
     def clip(self, max_norm):
         """(norm, coefficient) as device scalars; the outputs hold the clipped gradients."""
-        lib.grad_clip(self.segs, len(self.grads), max_norm, self.result, self.ws, self.ws_bytes)
+        self._clip(max_norm, *self._out, raw_stream(self.device))
         return self.norm, self.coef
