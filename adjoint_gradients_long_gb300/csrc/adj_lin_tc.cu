@@ -375,7 +375,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             constexpr uint32_t WIDE = KW == 64 ? 0u : PANEL;
             for (int64_t n = 0; n < N; ++n) {
                 const uint32_t q = base + uint32_t(n & 1) * STAGE, k = q + TILE_K, v = k + TILE_K;
-                if (!(wait(F_FULL0 + int(n & 1), n >> 1) && wait(F_S, n))) break;
+                // the decays too: the warps take them as there once A is
+                if (!(wait(F_FULL0 + int(n & 1), n >> 1) && wait(F_DEC0 + int(n & 1), n >> 1) && wait(F_S, n))) break;
                 tc_fence_after();
                 product<VW, KW / 16, false, true>(tmem + T_O1(n), q, PANEL, S_AT, SPANEL, false);
                 // A goes where the last P was
@@ -425,7 +426,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             const uint32_t Q = base + s * STAGE, K = Q + TILE_K, V = K + TILE_K;
             const ChunkDecay &d = dec[s];
             // l K: the products of Q, K and S are done, and their tiles take its three parts
-            if (!all_ok(wait(F_DEC0 + s, n >> 1) && wait(F_A, n))) break;
+            if (!all_ok(wait(F_A, n))) break;
             tc_fence_after();
             if (parts == 3) scale_row(K, Q, S_AT, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG), d.to_end(i));
             else scale_row2(K, Q, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG), d.to_end(i));

@@ -518,7 +518,7 @@ struct ClipSegs {
 };
 struct ClipWs {                 // in the workspace
     unsigned *status, *ticket, *turn;
-    double *part, *total;
+    float *part, *total;
 };
 
 template <int MAXS>
@@ -617,13 +617,16 @@ __device__ __forceinline__ void part_scale(const void *src, void *dst, int64_t n
     if (threadIdx.x == 1 && w1 < i1 && i1 - 1 > i0) slowly(i1 - 1);
 }
 
-__device__ __forceinline__ double block_sum(double v, double *red) {
+// Sums over a block and over the blocks are plain fp32 trees: at most 12 roundings, 4e-7 of the
+// norm's square.  (The fp64 pipe takes 2 us for them, as long as the rest of a small call.)
+__device__ __forceinline__ float block_sum(float v, float *red) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    double r = 0.0;
-    for (int w = 0; w < CT / 32; ++w) r += red[w];
+    float r = red[threadIdx.x & (CT / 32 - 1)];
+#pragma unroll
+    for (int d = CT / 64; d; d >>= 1) r += __shfl_xor_sync(~0u, r, d);
     __syncthreads();
     return r;
 }
@@ -637,7 +640,7 @@ __device__ __forceinline__ int64_t range(const ClipSegs<MAXS> &g, int64_t block)
 // The block's part of the sum of squares.  A thread's tensors add up as a sum and what its
 // roundings lost: the fp64 pipe would take as long as the loads.
 template <int MAXS>
-__device__ __forceinline__ double sum_chunks(const ClipSegs<MAXS> &g) {
+__device__ __forceinline__ float sum_chunks(const ClipSegs<MAXS> &g) {
     float sum = 0.f, lost = 0.f;
     const int64_t c1 = range(g, int64_t(blockIdx.x) + 1);
     int64_t c = range(g, blockIdx.x);
@@ -651,13 +654,13 @@ __device__ __forceinline__ double sum_chunks(const ClipSegs<MAXS> &g) {
         sum = t;
         c = next;
     }
-    return double(sum) + double(lost);
+    return sum + lost;
 }
 
 // Hands in the block's sum; true in the last block to do so, which then has added all of them in the
 // blocks' order and written the norm and the coefficient.
 template <int MAXS>
-__device__ __forceinline__ bool hand_in(const ClipSegs<MAXS> &g, double sum, const ClipWs &ws, float *out, double *red) {
+__device__ __forceinline__ bool hand_in(const ClipSegs<MAXS> &g, float sum, const ClipWs &ws, float *out, float *red) {
     __shared__ bool last;
     sum = block_sum(sum, red);
     if (threadIdx.x == 0) {
@@ -668,13 +671,13 @@ __device__ __forceinline__ bool hand_in(const ClipSegs<MAXS> &g, double sum, con
     __syncthreads();
     if (!last) return false;
     __threadfence();
-    double v = 0.0;
+    float v = 0.f;
     for (int b = threadIdx.x; b < int(gridDim.x); b += CT) v += __ldcg(ws.part + b);
     v = block_sum(v, red);
     if (threadIdx.x == 0) {
         if (!g.first_group) v += *ws.total;
         *ws.total = v;
-        const float norm = float(sqrt(v)), c = g.max_norm / (norm + ADJ_CLIP_EPS);
+        const float norm = sqrtf(v), c = g.max_norm / (norm + ADJ_CLIP_EPS);
         out[0] = norm;
         out[1] = c > 1.f ? 1.f : c;                      // NaN stays NaN
     }
@@ -699,7 +702,7 @@ __device__ __forceinline__ void scale_chunks(const ClipSegs<MAXS> &g, float f) {
 
 template <int MAXS>
 __global__ __launch_bounds__(CT, CB) void k_clip_norm(const __grid_constant__ ClipSegs<MAXS> g, const ClipWs ws, float *out) {
-    __shared__ double red[CT / 32];
+    __shared__ float red[CT / 32];
     hand_in(g, sum_chunks(g), ws, out, red);
 }
 template <int MAXS>
@@ -709,10 +712,10 @@ __global__ __launch_bounds__(CT, CB) void k_clip_scale(const __grid_constant__ C
 // Both, with all blocks resident (cooperative launch).
 template <int MAXS>
 __global__ __launch_bounds__(CT, CB) void k_clip(const __grid_constant__ ClipSegs<MAXS> g, const ClipWs ws, float *out) {
-    __shared__ double red[CT / 32];
+    __shared__ float red[CT / 32];
     __shared__ float coef;
     const unsigned turn = threadIdx.x == 0 ? ld_acquire(ws.turn) : 0u;     // before this block hands in
-    const double sum = sum_chunks(g);
+    const float sum = sum_chunks(g);
     const bool last = hand_in(g, sum, ws, out, red);
     if (threadIdx.x == 0) {
         if (last) {
@@ -720,7 +723,8 @@ __global__ __launch_bounds__(CT, CB) void k_clip(const __grid_constant__ ClipSeg
             st_release(ws.turn, turn + 1);
         } else {
             int it = 0;
-            while (ld_acquire(ws.turn) == turn && ++it < SPIN_LIMIT) __nanosleep(32);
+            while (ld_acquire(ws.turn) == turn && ++it < SPIN_LIMIT) {
+            }
             if (it == SPIN_LIMIT) record_timeout(ws.status);
         }
         coef = __ldcg(out + 1);
@@ -758,7 +762,7 @@ cudaError_t clip(const adj_grad_seg *segs, int64_t nseg, float max_norm, float *
     ws.status = reinterpret_cast<unsigned *>(base);
     ws.ticket = ws.status + 2;
     ws.turn = ws.status + 3;
-    ws.part = reinterpret_cast<double *>(base + WS_HEADER);
+    ws.part = reinterpret_cast<float *>(base + WS_HEADER);
     ws.total = ws.part + CLIP_GRID;
     ClipSegs<MAXS> t;
     t.max_norm = max_norm;
@@ -830,7 +834,7 @@ cudaError_t launch_logprob(const LogprobArgs &a, bool bf16, cudaStream_t st) {
     return a.dlogits ? logprob<float, true>(a, st) : logprob<float, false>(a, st);
 }
 
-size_t clip_ws_bytes() { return WS_HEADER + (CLIP_GRID + 1) * sizeof(double); }
+size_t clip_ws_bytes() { return WS_HEADER + (CLIP_GRID + 1) * sizeof(float); }
 
 cudaError_t launch_grad_clip(const adj_grad_seg *segs, int64_t nseg, float max_norm, float *out, char *ws,
                              cudaStream_t st) {
