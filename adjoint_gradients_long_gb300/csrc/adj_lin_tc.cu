@@ -738,7 +738,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
 // columns from R^T, and S and Z come as sums of two bf16.
 // Tensor memory: four accumulators of 128 columns; R^T and P^T lie where their products were.
 // The outputs leave through tiles whose last product is done: dq through S's, dk through Q's, dv
-// through V's.  (fp32 parts of shared heads are stored by the lanes.)
+// through Z's (fp32 parts of shared heads are stored by the lanes), so that the next task's Q, K, V
+// and W come in while dv is formed.  The decays are a task ahead.
 struct GradMaps {
     CUtensorMap q, k, v, w, shi, slo, zhi, zlo, dq, dk, dv;
 };
@@ -746,12 +747,12 @@ struct GradSums {
     float r[CG][TCH], f[CG][TCH], l[CG][TCH];   // W: rows less columns; reads of S; leavings to Z
     float zs[CW];
 };
-enum { G_IN, G_S, G_Z, G_DEC, G_X1, G_G1, G_R, G_D1, G_X2, G_G2, G_RT, G_D2, G_D3, G_E1, G_E2, G_SC, G_DONE, G_DG,
-       G_OQ, G_OK, G_OV, G_SFREE, G_LEFT, G_END, G_AR, G_COUNT = G_AR + 8 };
+enum { G_IN, G_S, G_Z, G_DEC0, G_DEC1, G_X1, G_G1, G_R, G_D1, G_X2, G_G2, G_RT, G_D2, G_D3, G_E1, G_E2, G_SC, G_DONE, G_DG,
+       G_OQ, G_OK, G_OV, G_SFREE, G_QFREE, G_LEFT, G_END, G_AR, G_COUNT = G_AR + 8 };
 
 template <int KW, int VW>
 constexpr size_t grad_smem() {
-    return 2 * size_t(KW + VW) * 256 + 2 * size_t(KW) * VW * 2 + sizeof(ChunkDecay) + TCH * 4 + sizeof(GradSums) +
+    return 2 * size_t(KW + VW) * 256 + 2 * size_t(KW) * VW * 2 + 2 * (sizeof(ChunkDecay) + TCH * 4) + sizeof(GradSums) +
            sizeof(Ctl<G_COUNT>);
 }
 
@@ -769,9 +770,9 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
     constexpr int KH = KW / CG, VH = VW / CG;   // columns of a thread
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t Q = smem_u32(sm), K = Q + TILE_K, V = K + TILE_K, W = V + TILE_V, SHI = W + TILE_V, SLO = SHI + TILE_S;
-    ChunkDecay &dec = *reinterpret_cast<ChunkDecay *>(sm + 2 * (TILE_K + TILE_V) + 2 * TILE_S);
-    float *wa = reinterpret_cast<float *>(&dec + 1);
-    GradSums &sums = *reinterpret_cast<GradSums *>(wa + TCH);
+    ChunkDecay *decs = reinterpret_cast<ChunkDecay *>(sm + 2 * (TILE_K + TILE_V) + 2 * TILE_S);
+    float *was = reinterpret_cast<float *>(decs + 2);
+    GradSums &sums = *reinterpret_cast<GradSums *>(was + 2 * TCH);
     auto *ctl = reinterpret_cast<Ctl<G_COUNT> *>(&sums + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr uint32_t R0 = 0, R1 = 128, R2 = 256, R3 = 384;
@@ -799,14 +800,10 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
         int64_t bh, b, h, hk, n;
     };
     auto task = [&](int64_t n) {
-        const int64_t t = int64_t(blockIdx.x) + n * gridDim.x;
-        Task k;
-        k.bh = t / a.NC;
-        k.n = t - k.bh * a.NC;
-        k.b = k.bh / a.H;
-        k.h = k.bh - k.b * a.H;
-        k.hk = k.h / (a.H / a.Hk);
-        return k;
+        // below 2^31, as the map of the states wants it
+        const uint32_t t = blockIdx.x + uint32_t(n) * gridDim.x, nc = uint32_t(a.NC), H = uint32_t(a.H);
+        const uint32_t bh = t / nc, b = bh / H, h = bh - b * H;
+        return Task{bh, b, h, h / (H / uint32_t(a.Hk)), t - bh * nc};
     };
     const int64_t N = (tasks - blockIdx.x + gridDim.x - 1) / gridDim.x;
 
@@ -815,8 +812,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
             int64_t n = 0;
             int in = 0, ss = 0, zz = 0;         // copies begun
             for (; n < N; ++n) {
-                // the last task is done with the tiles: its products, the warps, its outputs
-                if (n && !(wait(G_D3, n - 1) && wait(G_DONE, n - 1) && wait(G_LEFT, n - 1))) break;
+                // the last task is done with the tiles: its products, and dk has left
+                if (n && !(wait(G_D3, n - 1) && wait(G_QFREE, n - 1))) break;
                 const Task k = task(n);
                 const int t = int(k.n * TCH), z = int(k.bh * a.NC + k.n);
                 mbar_arrive_expect_tx(bar(G_IN), 2 * (TILE_K + TILE_V));
@@ -829,6 +826,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                     load4(Q + p * PANEL, &m.q, p * 64, int(k.hk), t, int(k.b), bar(G_IN));
                     load4(K + p * PANEL, &m.k, p * 64, int(k.hk), t, int(k.b), bar(G_IN));
                 }
+                if (n && !wait(G_LEFT, n - 1)) break;         // dv too
                 mbar_arrive_expect_tx(bar(G_S), 2 * TILE_S);
                 ++ss;
                 for (int p = 0; p < VW / 64; ++p) {
@@ -867,9 +865,11 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 if (!a.pq) {
                     for (int p = 0; p < KW / 64; ++p) store4(&m.dk, p * 64, int(k.hk), t, int(k.b), Q + p * PANEL);
                     bulk_commit();
+                    bulk_wait_read();
                 }
+                mbar_arrive(bar(G_QFREE));
                 if (!wait(G_OV, n)) break;
-                for (int p = 0; p < VW / 64; ++p) store4(&m.dv, p * 64, int(k.h), t, int(k.b), V + p * PANEL);
+                for (int p = 0; p < VW / 64; ++p) store4(&m.dv, p * 64, int(k.h), t, int(k.b), SHI + p * PANEL);
                 bulk_commit();
                 bulk_wait_read();
                 mbar_arrive(bar(G_LEFT));
@@ -878,13 +878,23 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
         }
         __syncwarp();
     } else if (warp == W_AUX) {
-        // decays, and the sums of dg when a task is done
+        // decays a task ahead, and the sums of dg when a task is done
+        auto fetch = [&](int64_t n) {
+            const Task k = task(n);
+            const int64_t t0 = k.n * TCH;
+            return ChunkDecay::fetch(a.g + (k.b * a.T + t0) * a.H + k.h, a.H, int(a.T - t0 < TCH ? a.T - t0 : TCH));
+        };
+        auto fill = [&](int64_t n, float4 own) {
+            decs[n & 1].fill(own, was + (n & 1) * TCH);
+            arrive(G_DEC0 + int(n & 1));
+        };
+        fill(0, fetch(0));
         for (int64_t n = 0; n < N; ++n) {
             const Task k = task(n);
             const int64_t t0 = k.n * TCH;
             const int len = int(a.T - t0 < TCH ? a.T - t0 : TCH);
-            dec.fill(ChunkDecay::fetch(a.g + (k.b * a.T + t0) * a.H + k.h, a.H, len), wa);
-            arrive(G_DEC);
+            if (n + 1 < N) fill(n + 1, fetch(n + 1));    // its buffer's last task was done before this one
+            const ChunkDecay &dec = decs[n & 1];
             if (!all_ok(wait(G_DONE, n))) break;
             float r[4], f[4], l[4];
 #pragma unroll
@@ -978,7 +988,9 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
             const int64_t t0 = k.n * TCH;
             const bool live = t0 + i < a.T;
             const int64_t tok = k.b * a.T + t0 + i;
-            if (!all_ok(wait(G_DEC, n) && (n == 0 || wait(G_DG, n - 1)) && wait(G_X1, n))) break;
+            const ChunkDecay &dec = decs[n & 1];
+            const float *wa = was + (n & 1) * TCH;
+            if (!all_ok(wait(G_DEC0 + int(n & 1), n >> 1) && (n == 0 || wait(G_DG, n - 1)) && wait(G_X1, n))) break;
             tc_fence_after();
             const float xi = dec.x[i];
             const int ri = dec.r[i], j8 = 8 * g;
@@ -1186,7 +1198,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
             if (!all_ok(wait(G_D3, n))) break;
             tc_fence_after();
             out(lj, 0u, g * VH, VH, [&](int c, const float (&y)[16]) {
-                stage(V, c, y);
+                stage(SHI, c, y);            // Z has been read: <Z, S> by all warps (G_E2), K Z (G_D3)
             }, static_cast<float *>(nullptr));
             tc_fence_before();
             fence_proxy_async_smem();
