@@ -5,10 +5,11 @@
 //     A  = Q K^T               (tokens x tokens)     exact operands
 //     O1 = Q S                 (tokens x Dv)         S rounded to bf16
 //     O2 = P V                 (tokens x Dv)         P = A . D as a sum of two bf16, in tensor memory
-//     U  = (l K)^T V           (Dk x Dv)             l K as a sum of three bf16: exact to fp32
+//     U  = (l K)^T V           (Dk x Dv)             l K as a sum of three bf16 where the state is
+//                                                    a result, of two where it meets bf16 next
 //     o  = scale (f O1 + O2),  S <- f_last S + U     S in fp32 registers
-// with the decays D, f, l of adj_lin.cu.  O1 has one rounding to bf16 before the output's own; U
-// has none, because the state is an fp32 result and errors in it stay.
+// with the decays D, f, l of adj_lin.cu.  O1 has one rounding to bf16 before the output's own; three
+// parts hold l K to fp32, because errors in a state that is a result stay.
 //
 // One block walks the chunks of a segment of one head's tokens.  When there are fewer heads
 // than SMs, the tokens of a head are cut into segments: k_lin_tc_state sums up each segment's own
@@ -283,11 +284,11 @@ __device__ __forceinline__ void store_part(const float (&S)[VH], float *p, int d
 // KW, VW: Dk and Dv rounded up to 64 or 128; the columns past them are zeros (the copies fill
 // them) and the store clips them.
 //
-// Measured, 131072 tokens x 16 heads of 128 (2.15 GB): 500 to 515 us, 0.62 of the copy bandwidth
-// with 250 us for the segments' states before it.  What bounds a chunk of 128 columns is shared
-// memory: its 48 products read 350 KB, the copies, the scaled keys, the state and the output
-// tile move 250 KB more, 4,700 cycles at 128 bytes a cycle of the 8,700 that it takes; the rest
-// is the chain A -> l K -> U -> S and A -> P -> O2 -> o that one block an SM cannot fill.
+// Measured, 131072 tokens x 16 heads of 128 (2.15 GB): 514 us, 0.62 of the copy bandwidth, with
+// 247 us for the segments' states before it.  A block takes 4.5 us a chunk.  By count the operands of
+// the products, the copies, the scaled keys, the state and the output tile move 600 KB through
+// shared memory, 4,700 cycles at 128 bytes a cycle: about half of that time.  The rest is taken to be
+// the chain A -> l K -> U -> S and A -> P -> O2 -> o, which one block an SM cannot fill.
 // The S tile also takes the third part of l K, between the last read of S and the next state.
 enum { F_FULL0, F_FULL1, F_EMPTY0, F_EMPTY1, F_DEC0, F_DEC1, F_A, F_PV, F_P, F_K, F_U, F_S, F_OUT, F_END, F_AR, F_COUNT = F_AR + 4 };
 
@@ -526,8 +527,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
 }
 
 // ---------------------------------------------------------------- segment states
-// Measured, 131072 tokens x 16 heads of 128 in 9 segments (1.07 GB): 240 us; 3,000 of a chunk's
-// 4,200 cycles are shared memory's (three parts of l K written and read).
+// Measured, 131072 tokens x 16 heads of 128 in 9 segments (1.07 GB): 247 us.
 //
 // The state that a segment's own tokens leave (zero before it): S[blockIdx.x], and the decay
 // over it; in the second half of a grid for both directions, the adjoint state from q and scale go,
@@ -550,7 +550,8 @@ constexpr size_t state_smem() {
 // segment is the whole head), and the state met before every chunk is kept as a sum of two bf16
 // [B,H,NC,Dk,Dv], the operand of the backward pass.  The parts leave one after the other through
 // one tile, the second while the next chunk is being scaled; with a tile each and a ring of two
-// stages the walk waited for its copies in (86 us against 70 us for 64 chunks of 32 heads).
+// stages the walk waited for its copies in (all state launches of 2 x 8192 tokens x 16 heads of
+// 128: 241 us so, 208 us with one tile and three stages).
 template <int KW, int VW, bool KEEP>
 __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_constant__ BothMaps maps, const LinArgs a,
                                                               int nseg, int cps, unsigned *status) {
@@ -745,8 +746,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
 // instructions), are rounded to bf16 once, as the outputs are.  dg does not go through them:
 // its sums over W_ij = R_ij (q_i . k_j) are taken from the fp32 accumulators, by rows from R and by
 // columns from R^T, and S and Z come as sums of two bf16.
-// Measured, 2 x 8192 tokens x 16 heads of 128 (2048 chunks): 190 us, 14 us a chunk and SM; the
-// states before it 184 us in two launches.  Bound by the chain of a chunk: eleven products and four
+// Measured, 2 x 8192 tokens x 16 heads of 128 (2048 chunks): 192 us, 14 us a chunk and SM; the
+// states before it 185 us in two launches.  Bound by the chain of a chunk: eleven products and four
 // passes of the registers, each waiting for the one before.
 // Tensor memory: four accumulators of 128 columns; R^T and P^T lie where their products were.
 // The outputs leave through tiles whose last product is done: dq through S's, dk through Q's, dv
