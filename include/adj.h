@@ -270,8 +270,9 @@ adj_status adj_sel_param_grad(const adj_dims *dims, const adj_sel_weights *w, co
  * least its row's heads times width and a multiple of 16 bytes.  x_dtype fp32: products in
  * fp32.  x_dtype bf16: fp32 sums of products of bf16 operands; the states that a token reads
  * and, in the backward pass, the decayed pair weights are rounded to bf16 (the forward pass keeps
- * those as a sum of two); the states themselves stay fp32.  dg and ds0 take states and keys as
- * sums of two bf16: relative errors of 1e-6 as a rule, 1.2e-5 the largest seen.
+ * those as a sum of two); the states themselves stay fp32.  dg takes the states around a chunk
+ * as sums of two bf16.  Relative errors: dg 1e-6 and ds0 8e-7 as a rule, 1.2e-5 and 5.7e-6 the
+ * largest seen.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int64_t B, T;
