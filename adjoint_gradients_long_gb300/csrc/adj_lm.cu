@@ -159,16 +159,23 @@ __device__ __forceinline__ uint64_t rank_key(uint32_t key, uint32_t idx) { retur
 struct Stat {
     float m, s, t;
 };
-// Distances from m in powers of two.  One multiply-add each, on the rounded m log2 e, which
-// every use of the same m shares; near the ends of the range (far) that product would overflow and
-// the difference is taken first.  A row with nothing but masked values is measured from zero.
+// Distances from m in powers of two.  One multiply-add each, on m2 = m log2 e as rounded, which
+// every use of the same m shares: the distance of m itself is m2's rounding error, off().  It grows with
+// m (and 2^off overflows from 1e10 on), so past FAR_FROM, where it may reach 0.003, the difference is
+// taken before the product.  A row with nothing but masked values is measured from zero.
+constexpr float FAR_FROM = 65536.f;
 struct Ref {
     float m, m2;
     bool far;
-    __device__ __forceinline__ explicit Ref(float m_) : m(m_ == -INFINITY ? 0.f : m_), m2(m * LOG2E), far(fabsf(m) > 9e37f) {}
+    __device__ __forceinline__ explicit Ref(float m_) : m(m_ == -INFINITY ? 0.f : m_), m2(m * LOG2E), far(fabsf(m) > FAR_FROM) {}
     template <bool FAR>
     __device__ __forceinline__ float at(float x) const { return FAR ? (x - m) * LOG2E : fmaf(x, LOG2E, -m2); }
-    __device__ __forceinline__ float from(const Ref &o) const { return far || o.far ? (o.m - m) * LOG2E : o.m2 - m2; }
+    // what a distance from here exceeds (x - m) log2 e by
+    __device__ __forceinline__ float off() const { return far ? 0.f : fmaf(m, LOG2E, -m2); }
+    // from here to another reference, at most at this one
+    __device__ __forceinline__ float from(const Ref &o) const {
+        return far || o.far ? fmaf(o.m - m, LOG2E, off() - o.off()) : o.m2 - m2;
+    }
     // log(sum) of a sum s = 2^l2s measured from m, and a value's logarithm less that
     __device__ __forceinline__ float natural(float l2s) const { return far ? m + l2s * LN2 : (m2 + l2s) * LN2; }
     __device__ __forceinline__ float logp(float x, float l2s) const {
