@@ -176,11 +176,10 @@ struct Ref {
     __device__ __forceinline__ float from(const Ref &o) const {
         return far || o.far ? fmaf(o.m - m, LOG2E, off() - o.off()) : o.m2 - m2;
     }
-    // log(sum) of a sum s = 2^l2s measured from m, and a value's logarithm less that
-    __device__ __forceinline__ float natural(float l2s) const { return far ? m + l2s * LN2 : (m2 + l2s) * LN2; }
-    __device__ __forceinline__ float logp(float x, float l2s) const {
-        return far ? (x - m) - l2s * LN2 : (fmaf(x, LOG2E, -m2) - l2s) * LN2;
-    }
+    // log(sum) of a sum s = 2^l2s measured from m, and a value's logarithm less that: the difference
+    // first, which no value of fp32 overflows but where the result does
+    __device__ __forceinline__ float natural(float l2s) const { return m + (l2s - off()) * LN2; }
+    __device__ __forceinline__ float logp(float x, float l2s) const { return (x - m) - (l2s - off()) * LN2; }
 };
 __device__ __forceinline__ Stat join(Stat a, Stat b) {
     const float m = fmaxf(a.m, b.m);

@@ -17,6 +17,7 @@ from oracle import lm as olm  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
+LOWEST = {True: torch.finfo(torch.bfloat16).min, False: torch.finfo(torch.float32).min}
 SHAPES = [(6, 700), (6, 4099), (6, 12001), (6, 70007)]         # one block a row, then clusters of 2 to 8
 
 
@@ -70,10 +71,11 @@ def logits(N, V, bf16, seed):
 
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("N,V", SHAPES)
-@pytest.mark.parametrize("fill", [-1e4, -65504.0, -1e9, -5e9, -1e10, -1e12, -1e15, -1e20, -1e30])
+@pytest.mark.parametrize("fill", [-1e4, -65504.0, -1e9, -5e9, -1e10, -1e12, -1e15, -1e20, -1e30, "lowest"])
 def test_finite_masks(fill, N, V, bf16):
     """A fill in place of minus infinity: at the head of the row, in all of it, in most of it at
     random, around one value left, at the tail, and in the target."""
+    fill = LOWEST[bf16] if fill == "lowest" else fill
     x, y, glp, gent, gen = logits(N, V, bf16, V)
     x[0, :V * 6 // 10] = fill
     x[1] = fill
