@@ -28,10 +28,10 @@ struct Vec<float> {
     static __device__ __forceinline__ float largest(uint4 u) {
         return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
     }
-    // values below -1e38 as -1e38 (NaN stays)
+    // values below -2^18 as -2^18 (NaN stays)
     static __device__ __forceinline__ uint32_t floor1(uint32_t w) {
         float y;
-        asm("max.NaN.f32 %0, %1, 0fFE967699;" : "=f"(y) : "f"(__uint_as_float(w)));
+        asm("max.NaN.f32 %0, %1, 0fC8800000;" : "=f"(y) : "f"(__uint_as_float(w)));
         return __float_as_uint(y);
     }
     static __device__ __forceinline__ uint4 floored(uint4 u) {
@@ -61,7 +61,7 @@ struct Vec<__nv_bfloat16> {
     }
     static __device__ __forceinline__ uint32_t floor2(uint32_t w) {
         uint32_t d;
-        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(0xFE96FE96u));
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(0xC880C880u));
         return d;
     }
     static __device__ __forceinline__ uint4 floored(uint4 u) {
@@ -240,8 +240,10 @@ __device__ __forceinline__ Stat warp_join(Stat x) {
 }
 
 // 2^distance times the distance is zero for a masked value, but minus infinity times zero would
-// be NaN.  Values are raised to -1e38 first (half an instruction each in bf16); where the largest
-// itself lies that low (FAR) the distance is held to -200, below which its power of two is zero.
+// be NaN.  Values are raised to -2^18 first (half an instruction each in bf16), whose power of two is
+// zero from every reference that is not far: distances stay above -5e5, so that the gradient's
+// c0 + c1 distance is finite for cotangents up to 7e32 times the row's sum.  From a far one (FAR) the
+// distance is held to -200, below which its power of two is zero.
 template <class T, bool FAR>
 __device__ __forceinline__ void distances(uint4 raw, const Ref &r, float (&d)[Vec<T>::N], float (&p)[Vec<T>::N]) {
     Vec<T>::unpack(FAR ? raw : Vec<T>::floored(raw), d);

@@ -1,5 +1,5 @@
 """Log probabilities over logits far from zero (GPU, against the fp64 oracle): large finite values
-that stand for masked tokens, rows with nothing else, large maxima.
+that stand for masked tokens, rows with nothing else, large maxima, large cotangents of the entropy.
 
 Tolerances, row by row:
   lse       3e-7 of it (one rounding of a sum with the largest logit, 2^-24, and one of its storage)
@@ -120,3 +120,20 @@ def test_maxima_around_one_scale(bf16):
         x = x.to(torch.bfloat16 if bf16 else torch.float32)
         y = torch.tensor([5, V - 2, 17, 4], device="cuda")
         check(x, y, bf16, torch.ones(4, device="cuda"), torch.full((4,), 0.5, device="cuda"))
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("gent", [4.0, -8.0, 1e4, -1e4, 1e20])
+@pytest.mark.parametrize("N,V", [(6, 700), (6, 12001)])
+def test_large_entropy_cotangent(N, V, gent, bf16):
+    """Masked tokens of a confident row get no gradient, whatever the cotangent."""
+    x, y, glp, ge, _ = logits(N, V, bf16, V + 2)
+    x[:3, 5] = 40
+    ge[:] = gent
+    for n, low in enumerate((float("-inf"), LOWEST[bf16], -1e30)):
+        x[n, V // 2:] = low
+        x[3 + n, 1::2] = low
+    y[:] = torch.tensor([5, 7, -1, 0, 2, 4], device="cuda")
+    r = check(x, y, bf16, glp, ge)
+    for n in range(3):
+        assert (r.dlogits[n, V // 2:] == 0).all() and (r.dlogits[3 + n, 1::2] == 0).all()
