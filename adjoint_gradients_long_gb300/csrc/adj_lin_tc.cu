@@ -382,8 +382,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             constexpr uint32_t WIDE = KW == 64 ? 0u : PANEL;
             for (int64_t n = 0; n < N; ++n) {
                 const uint32_t q = base + uint32_t(n & 1) * STAGE, k = q + TILE_K, v = k + TILE_K;
-                // the decays too: the warps take them as there once A is
-                if (!(wait(F_FULL0 + int(n & 1), n >> 1) && wait(F_DEC0 + int(n & 1), n >> 1) && wait(F_S, n))) break;
+                if (!(wait(F_FULL0 + int(n & 1), n >> 1) && wait(F_S, n))) break;
                 tc_fence_after();
                 product<VW, KW / 16, false, true>(tmem + T_O1(n), q, PANEL, S_AT, SPANEL, false);
                 // A goes where the last P was
@@ -432,8 +431,10 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             const int s = int(n & 1);
             const uint32_t Q = base + s * STAGE, K = Q + TILE_K, V = K + TILE_K;
             const ChunkDecay &d = dec[s];
-            // l K: the products of Q, K and S are done, and their tiles take its three parts
-            if (!all_ok(wait(F_A, n))) break;
+            // l K: the products of Q, K and S are done, and their tiles take its three parts.  K and the
+            // decays are waited for too: A's barrier orders the products alone, not what other warps and
+            // the copies have written
+            if (!all_ok(wait(F_FULL0 + s, n >> 1) && wait(F_DEC0 + s, n >> 1) && wait(F_A, n))) break;
             tc_fence_after();
             if (parts == 3) scale_row(K, Q, S_AT, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG), d.to_end(i));
             else scale_row2(K, Q, PANEL, i, g * (KW / 8 / CG), (g + 1) * (KW / 8 / CG), d.to_end(i));
@@ -1003,7 +1004,9 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
             const int64_t tok = k.b * a.T + t0 + i;
             const ChunkDecay &dec = decs[n & 1];
             const float *wa = was + (n & 1) * TCH;
-            if (!all_ok(wait(G_DEC0 + int(n & 1), n >> 1) && (n == 0 || wait(G_DG, n - 1)) && wait(G_X1, n))) break;
+            // the tiles too, whose rows are read below: the products' barriers do not order the copies
+            if (!all_ok(wait(G_DEC0 + int(n & 1), n >> 1) && wait(G_IN, n) && (n == 0 || wait(G_DG, n - 1)) && wait(G_X1, n)))
+                break;
             tc_fence_after();
             const float xi = dec.x[i];
             const int ri = dec.r[i], j8 = 8 * g;
