@@ -40,21 +40,29 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // log decays from the chunk's start to t and E_b its value at block b's last token:
 //   x[t] = G_t - E_b (b the block of t), E as hi + lo; r counts new starts
 //   wb[t] = 2^(E_b - G_t): from t to its block's end, zero across a new start
-//   last[b]: from block b's end to the chunk's end; total: over the chunk
+//   wa[t] = 2^(G_t - E_{b-1}): from the end of the block before to t, zero across a new start (kept
+//           beside this where it is used)
+//   last[b]: from block b's end to the chunk's end; start[b]: from before the chunk to block b's
+//           start, start[4]: over the chunk
 // A decay between blocks is a product of such factors, each at most 1; only pairs inside one
-// block take an exponential each.
+// block take an exponential each.  x is hundreds to thousands where strong decays follow t in its
+// block, and rounded to fp32 there (2e-4 of a decay at most): good enough for outputs of bf16
+// alone.  Fp32 states and gradients take first() from wa, and pairs of a block from x with what its
+// rounding lost.
 struct alignas(16) ChunkDecay {
     float x[TCH], wb[TCH];
     uint8_t r[TCH];
     float Ehi[4], Elo[4], last[4];
     int re[4];
-    float total;
+    float start[5];
     int n_cut;
 
     __device__ __forceinline__ float first(int t) const {
         return r[t] == 0 ? fast_exp2((Ehi[t >> 5] + Elo[t >> 5]) + x[t]) : 0.f;
     }
+    __device__ __forceinline__ float first(int t, const float *wa) const { return wa[t] * start[t >> 5]; }
     __device__ __forceinline__ float to_end(int t) const { return wb[t] * last[t >> 5]; }
+    __device__ __forceinline__ float total() const { return start[4]; }
 
     // by one whole warp: this lane's four tokens of a chunk (tokens past len have decay 1) ...
     static __device__ __forceinline__ float4 fetch(const float *g, int64_t pitch, int len) {
@@ -63,8 +71,8 @@ struct alignas(16) ChunkDecay {
                            t + 2 < len ? __ldg(g + (t + 2) * pitch) : 0.f, t + 3 < len ? __ldg(g + (t + 3) * pitch) : 0.f);
     }
     // ... and their decays; the chunk's sum of logarithms is returned
-    // wa (may be null): 2^(G_t - E_{b-1}), from the block before to t, zero across a new start
-    __device__ Sum2 fill(float4 own, float *wa = nullptr) {
+    // wa (may be null, and x itself): as above; xl (may be null): what the rounding of x lost
+    __device__ Sum2 fill(float4 own, float *wa = nullptr, float *xl = nullptr) {
         const int lane = threadIdx.x & 31;
         const float v[4] = {own.x, own.y, own.z, own.w};
         Sum2 s[4], sum{0.f, 0.f};
@@ -94,17 +102,20 @@ struct alignas(16) ChunkDecay {
         Sum2 before = run.up(1);
         if (lane == 0) before = Sum2{0.f, 0.f};
         const int cb = rc - cnt;
-        float xs[4], ws[4];
+        float xs[4], ls[4], ws[4];
         uint32_t rs = 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            xs[u] = ((before + s[u]) - E).value();
+            const Sum2 d = (before + s[u]) - E;
+            xs[u] = d.value();
+            ls[u] = d.lo - (xs[u] - d.hi);
             ws[u] = cb + c[u] == reb ? fast_exp2(-xs[u]) : 0.f;
             rs |= uint32_t(cb + c[u]) << (8 * u);
         }
         reinterpret_cast<float4 *>(x)[lane] = make_float4(xs[0], xs[1], xs[2], xs[3]);
         reinterpret_cast<float4 *>(wb)[lane] = make_float4(ws[0], ws[1], ws[2], ws[3]);
         reinterpret_cast<uint32_t *>(r)[lane] = rs;
+        if (xl) reinterpret_cast<float4 *>(xl)[lane] = make_float4(ls[0], ls[1], ls[2], ls[3]);
         if (wa) {
             Sum2 P = run.from((lane & 24) - 1);
             int rp = __shfl_sync(~0u, rc, (lane & 24) - 1);
@@ -123,9 +134,10 @@ struct alignas(16) ChunkDecay {
             Elo[b] = E.lo;
             re[b] = reb;
             last[b] = reb == rall ? fast_exp2((Eall - E).value()) : 0.f;
+            start[b + 1] = reb == 0 ? fast_exp2(E.value()) : 0.f;
         }
         if (lane == 0) {
-            total = rall == 0 ? fast_exp2(Eall.value()) : 0.f;
+            start[0] = 1.f;
             n_cut = rall;
         }
         return Eall;
@@ -497,7 +509,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             }
             if (!all_ok(wait(F_U, n))) break;
             tc_fence_after();
-            state_update<VH>(S, lanes + T_U(n) + c0, d.total);
+            state_update<VH>(S, lanes + T_U(n) + c0, d.total());
             tc_fence_before();
             put_state();
             // the outputs, through V's tile
@@ -619,7 +631,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
             const float4 now = own;
             if (n + 1 < N) own = gates(a, seg, chunk(n + 1));
             if (n >= 2 && !all_ok(wait(S_DFREE + s, (n >> 1) - 1))) break;
-            sum = sum + dec[s].fill(now);
+            sum = sum + dec[s].fill(now, rev ? dec[s].x : nullptr);     // x itself is not read
             __syncwarp();
             cuts += dec[s].n_cut;
             if (lane == 0) mbar_arrive(bar(S_DEC + s));
@@ -714,13 +726,13 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
                 if (!(ok = all_ok(wait(S_FULL + s, turn)))) break;
                 const uint32_t at = base + s * STAGE;
                 scale_row(at, at + TILE_K, at + 2 * TILE_K, PANEL, r, q * UQ, (q + 1) * UQ,
-                          rev ? dec[e].first(h * SH + r) * a.scale : dec[e].to_end(h * SH + r));
+                          rev ? dec[e].first(h * SH + r, dec[e].x) * a.scale : dec[e].to_end(h * SH + r));
                 fence_proxy_async_smem();
                 arrive(S_K + s);
                 if (++s == RING) { s = 0; ++turn; }
                 if (h == 0 && n && !(ok = keep(2 * n - 1))) break;
             }
-            const float now = dec[e].total;
+            const float now = dec[e].total();
             if (!ok) break;
             arrive(S_DFREE + e);
             if (n && !(ok = fold(n - 1, tot))) break;
@@ -766,7 +778,7 @@ enum { G_IN, G_S, G_Z, G_DEC0, G_DEC1, G_X1, G_G1, G_R, G_D1, G_X2, G_G2, G_RT, 
 
 template <int KW, int VW>
 constexpr size_t grad_smem() {
-    return 2 * size_t(KW + VW) * 256 + 2 * size_t(KW) * VW * 2 + 2 * (sizeof(ChunkDecay) + TCH * 4) + sizeof(GradSums) +
+    return 2 * size_t(KW + VW) * 256 + 2 * size_t(KW) * VW * 2 + 2 * (sizeof(ChunkDecay) + TCH * 8) + sizeof(GradSums) +
            sizeof(Ctl<G_COUNT>);
 }
 
@@ -785,8 +797,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t Q = smem_u32(sm), K = Q + TILE_K, V = K + TILE_K, W = V + TILE_V, SHI = W + TILE_V, SLO = SHI + TILE_S;
     ChunkDecay *decs = reinterpret_cast<ChunkDecay *>(sm + 2 * (TILE_K + TILE_V) + 2 * TILE_S);
-    float *was = reinterpret_cast<float *>(decs + 2);
-    GradSums &sums = *reinterpret_cast<GradSums *>(was + 2 * TCH);
+    float *was = reinterpret_cast<float *>(decs + 2);   // wa and xl of both
+    GradSums &sums = *reinterpret_cast<GradSums *>(was + 4 * TCH);
     auto *ctl = reinterpret_cast<Ctl<G_COUNT> *>(&sums + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr uint32_t R0 = 0, R1 = 128, R2 = 256, R3 = 384;
@@ -899,7 +911,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
             return ChunkDecay::fetch(a.g + (k.b * a.T + t0) * a.H + k.h, a.H, int(a.T - t0 < TCH ? a.T - t0 : TCH));
         };
         auto fill = [&](int64_t n, float4 own) {
-            decs[n & 1].fill(own, was + (n & 1) * TCH);
+            decs[n & 1].fill(own, was + (n & 1) * 2 * TCH, was + (n & 1) * 2 * TCH + TCH);
             arrive(G_DEC0 + int(n & 1));
         };
         fill(0, fetch(0));
@@ -940,7 +952,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 if (lane >= d) ll += z;
             }
             const float after_r = rr - r[0], after_f = ff - f[0];
-            float across = (ll - lt) + (dec.total == 0.f ? 0.f : dec.total * zs);
+            float across = (ll - lt) + (dec.total() == 0.f ? 0.f : dec.total() * zs);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int t = lane * 4 + u;
@@ -1003,13 +1015,18 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
             const bool live = t0 + i < a.T;
             const int64_t tok = k.b * a.T + t0 + i;
             const ChunkDecay &dec = decs[n & 1];
-            const float *wa = was + (n & 1) * TCH;
+            const float *wa = was + (n & 1) * 2 * TCH, *xl = wa + TCH;
             // the tiles too, whose rows are read below: the products' barriers do not order the copies
             if (!all_ok(wait(G_DEC0 + int(n & 1), n >> 1) && wait(G_IN, n) && (n == 0 || wait(G_DG, n - 1)) && wait(G_X1, n)))
                 break;
             tc_fence_after();
-            const float xi = dec.x[i];
+            const float xi = dec.x[i], xli = xl[i], wai = wa[i];
             const int ri = dec.r[i], j8 = 8 * g;
+            // what x's rounding lost at this thread's 8 columns of its own block
+            auto lost = [&](float (&w)[8]) {
+                *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(xl + 32 * wq + j8);
+                *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(xl + 32 * wq + j8 + 4);
+            };
             // R, 8 columns of every block of 32, and the row sums of W
             {
                 uint32_t h[4][4];
@@ -1028,8 +1045,10 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                     *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(src);
                     *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(src + 4);
                     if (c < wq) {
-                        const float f = ri == dec.re[c]
-                                            ? a.scale * fast_exp2((dec.Ehi[wq] - dec.Ehi[c]) + (dec.Elo[wq] - dec.Elo[c]) + xi) : 0.f;
+                        // c < wq: the block before this row's exists
+                        const int p = wq ? wq - 1 : 0;
+                        const float f = dec.re[p] == dec.re[c]
+                                            ? a.scale * wai * fast_exp2((dec.Ehi[p] - dec.Ehi[c]) + (dec.Elo[p] - dec.Elo[c])) : 0.f;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             x[e] *= w[e] * f;
@@ -1037,10 +1056,12 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                         }
                     } else {
                         const uint2 rj = *reinterpret_cast<const uint2 *>(dec.r + 32 * c + j8);
+                        float l[8];
+                        lost(l);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const int r = int(((e < 4 ? rj.x : rj.y) >> (8 * (e & 3))) & 255u);
-                            x[e] = j8 + e <= lane && ri == r ? x[e] * (a.scale * fast_exp2(xi - w[e])) : 0.f;
+                            x[e] = j8 + e <= lane && ri == r ? x[e] * (a.scale * fast_exp2((xi - w[e]) + (xli - l[e]))) : 0.f;
                             if (j8 + e < lane) sum = fmaf(x[e], y[e], sum);
                         }
                     }
@@ -1101,7 +1122,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 if (dot) *dot = s == 0.f ? 0.f : s * d;
             };
             // dq
-            const float fi = dec.first(i) * a.scale;
+            const float fi = dec.first(i, wa) * a.scale;
             if (!all_ok(wait(G_SC, n) && wait(G_D1, n))) break;
             tc_fence_after();
             out(fi, Q, g * KH, KH, [&](int c, const float (&y)[16]) {
@@ -1147,11 +1168,13 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                         }
                     } else {
                         const uint2 rj = *reinterpret_cast<const uint2 *>(dec.r + 32 * c + j8);
+                        float l[8];
+                        lost(l);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const int r = int(((e < 4 ? rj.x : rj.y) >> (8 * (e & 3))) & 255u);
                             const bool in = j8 + e >= lane && ri == r;
-                            const float d = in ? a.scale * fast_exp2(w[e] - xi) : 0.f;
+                            const float d = in ? a.scale * fast_exp2((w[e] - xi) + (l[e] - xli)) : 0.f;
                             x[e] = in ? x[e] * d : 0.f;
                             if (j8 + e > lane) sum = fmaf(x[e], y[e], sum);
                             y[e] = in ? y[e] * d : 0.f;
