@@ -151,9 +151,14 @@ def bind(name, *first):
 
 
 def raw_stream(device) -> int:
-    """torch's current stream of a CUDA device, as an address."""
+    """torch's current stream of a CUDA device, as an address.  The library launches on the current
+    device, and the address of a default stream names none: any other device is refused."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(device.index) if device.index is not None else 0
+    if device.type != "cuda":
+        raise ValueError(f"the library runs on CUDA devices, got {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"{device} is not the current device; call inside torch.cuda.device({device.index})")
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _check(st: int, what: str):

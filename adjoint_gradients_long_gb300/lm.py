@@ -9,8 +9,9 @@ include/adj.h states each operator in full.  As the drivers of the layers do, an
 the sizes, the workspace and the outputs of one shape: a call overwrites the outputs of the
 call before it, enqueues kernels on torch's current stream and synchronises nothing, and can
 be captured into a CUDA graph.  Calls on one object belong to one stream at a time (they share
-its buffers).  Tensors are checked for shape, type, device and layout (ValueError) before the
-library checks its own arguments (lib.AdjError).
+its buffers).  An object's device has to be the current one during a call.  Tensors are checked for
+shape, type, device and layout (ValueError) before the library checks its own arguments
+(lib.AdjError).
 """
 from __future__ import annotations
 

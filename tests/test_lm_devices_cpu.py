@@ -1,0 +1,37 @@
+"""The language-model objects launch on the current CUDA device alone (nothing is launched here)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from adjoint_gradients_long_gb300 import build as adj_build, lib, lm  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    adj_build.build()
+
+
+def test_host_tensors_are_refused():
+    """Valid calls on host tensors: refused before the library gets a host address."""
+    z = torch.zeros
+    before = lib.launch_count()
+    a = lm.LinAttn(1, 8, 4, 16, 16, Hk=2, x_bf16=False, backward=True, device="cpu")
+    q, v, g = z(1, 8, 2, 16), z(1, 8, 4, 16), z(1, 8, 4)
+    s, x = lm.LinStep(2, 4, 16, 16, x_bf16=False, device="cpu"), z(2, 4, 16)
+    t = lm.TokenLogProbs(4, 100, x_bf16=False, device="cpu")
+    y = z(4, dtype=torch.int64)
+    c = lm.GradClip([z(4)])
+    for call in (lambda: a.forward(q, q, v, g), lambda: a.backward(q, q, v, g, v),
+                 lambda: s.step(x, x, x, z(2, 4), z(2, 4, 16, 16)), lambda: t.forward(z(4, 100), y),
+                 lambda: t.gradient(z(4, 100), y, z(4)), lambda: c.clip(1.0)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    assert lib.launch_count() == before
+
+
+def test_another_device_is_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
+    assert lib.raw_stream(torch.device("cuda", 0)) == 0
+    with pytest.raises(ValueError, match="current device"):
+        lib.raw_stream(torch.device("cuda", 1))
