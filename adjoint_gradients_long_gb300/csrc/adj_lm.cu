@@ -724,10 +724,12 @@ template <int MAXS>
 __global__ __launch_bounds__(CT, CB) void k_clip(const __grid_constant__ ClipSegs<MAXS> g, const ClipWs ws, float *out) {
     __shared__ float red[CT / 32];
     __shared__ float coef;
+    __shared__ bool met;
     const unsigned turn = threadIdx.x == 0 ? ld_acquire(ws.turn) : 0u;     // before this block hands in
     const float sum = sum_chunks(g);
     const bool last = hand_in(g, sum, ws, out, red);
     if (threadIdx.x == 0) {
+        met = true;
         if (last) {
             __threadfence();
             st_release(ws.turn, turn + 1);
@@ -735,12 +737,16 @@ __global__ __launch_bounds__(CT, CB) void k_clip(const __grid_constant__ ClipSeg
             int it = 0;
             while (ld_acquire(ws.turn) == turn && ++it < SPIN_LIMIT) {
             }
-            if (it == SPIN_LIMIT) record_timeout(ws.status);
+            if (it == SPIN_LIMIT) {                      // no coefficient: nothing is scaled, and the result says so
+                record_timeout(ws.status);
+                out[0] = out[1] = NAN;
+                met = false;
+            }
         }
         coef = __ldcg(out + 1);
     }
     __syncthreads();
-    scale_chunks(g, coef);
+    if (met) scale_chunks(g, coef);
 }
 
 // The next tensors from i on, as many as fit; returns where the next group starts.

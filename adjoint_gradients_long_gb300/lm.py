@@ -246,3 +246,12 @@ class GradClip:
         """(norm, coefficient) as device scalars; the outputs hold the clipped gradients."""
         self._clip(max_norm, *self._out, raw_stream(self.device))
         return self.norm, self.coef
+
+    def status(self, stream=None) -> int:
+        """Waits for `stream`: 0, or the status (lib.STATUS) of a call whose blocks did not meet in
+        time.  Such a call leaves (NaN, NaN) and what it has not scaled as it was; the object is
+        ready for the next call afterwards."""
+        st = lib.stream_status(self.ws, stream)
+        if st:
+            self.ws[:64].zero_()
+        return st

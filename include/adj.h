@@ -338,7 +338,10 @@ adj_status adj_logprob(const adj_logprob_dims *dims, const void *logits, const i
  * nothing is written then), any other overlap is an error of the caller; dst NULL: the tensor
  * counts in the norm only.  out: two device floats, norm and coef.  An infinite norm gives
  * coef 0, a NaN gives NaN (and NaN gradients): no call hides a step that has to be skipped.
- * Sums are in a fixed order: the same inputs give the same bits. */
+ * Sums are in a fixed order: the same inputs give the same bits.  Up to 1000 tensors the blocks wait
+ * for one another, with a limit: past it the status word is set, norm and coef are NaN, and what
+ * has not been scaled stays as it was.  The first 256 bytes of ws have to be zero before the first
+ * call, and before the next one after ADJ_ETIMEOUT. */
 typedef struct {
     const void *src;
     void *dst;
