@@ -153,7 +153,7 @@ adj_status adj_grad_clip(const adj_grad_seg *segs, int64_t nseg, float max_norm,
     if (ws_bytes < clip_ws_bytes()) return ADJ_EWORKSPACE;
     for (int64_t i = 0; i < nseg; ++i) {
         const adj_grad_seg &s = segs[i];
-        if (s.n < 0 || s.n >= (int64_t(1) << 43)) return ADJ_ESHAPE;
+        if (s.n < 0 || s.n >= (int64_t(1) << 40)) return ADJ_ESHAPE;     // its chunks fit 31 bits
         if (s.dtype != ADJ_F32 && s.dtype != ADJ_BF16) return ADJ_EDTYPE;
         if (s.n && !s.src) return ADJ_EINVAL;
         const uintptr_t el = s.dtype == ADJ_BF16 ? 2 : 4;

@@ -345,7 +345,7 @@ adj_status adj_logprob(const adj_logprob_dims *dims, const void *logits, const i
 typedef struct {
     const void *src;
     void *dst;
-    int64_t n;
+    int64_t n;           /* below 2^40 */
     int32_t dtype;
     int32_t reserved;    /* zero */
 } adj_grad_seg;

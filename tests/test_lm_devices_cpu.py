@@ -35,3 +35,10 @@ def test_another_device_is_refused(monkeypatch):
     assert lib.raw_stream(torch.device("cuda", 0)) == 0
     with pytest.raises(ValueError, match="current device"):
         lib.raw_stream(torch.device("cuda", 1))
+
+
+def test_clip_refuses_what_no_launch_can_cover():
+    """A tensor of more chunks than a launch counts: refused by its size (nothing is launched)."""
+    for n in (1 << 40, 1 << 42, (1 << 43) - 1):
+        segs = (lib.GradSeg * 1)(lib.GradSeg(1 << 40, 1 << 40, n, lib.F32, 0))
+        assert lib.load().adj_grad_clip(segs, 1, 1.0, 1 << 40, 1 << 40, 1 << 50, None) == 2
