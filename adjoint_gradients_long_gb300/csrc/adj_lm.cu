@@ -1,6 +1,7 @@
 // adj_lm.cu -- log probabilities of given tokens (with entropy, top alternatives and the
 // gradient) and clipping gradients by their global norm.  include/adj.h defines them.
 #include <algorithm>
+#include <atomic>
 
 #include "adj_lm.cuh"
 #include "adj_profile.cuh"
@@ -512,7 +513,7 @@ __global__ __launch_bounds__(LPT, LPB) void k_logprob(const LogprobArgs a) {
 // call, 232 us in the first form with two launches.
 constexpr int CT = 256;         // threads of a block
 constexpr int CB = 4;           // blocks an SM
-constexpr int CLIP_GRID = 152 * CB;
+constexpr int CLIP_GRID = 152 * CB; // at most: as many as are resident together
 
 template <int MAXS>
 struct ClipSegs {
@@ -772,6 +773,18 @@ int64_t fill(ClipSegs<MAXS> &t, const adj_grad_seg *segs, int64_t i, int64_t nse
     return i;
 }
 
+// Blocks that are resident together on the current device.
+int clip_blocks() {
+    static std::atomic<int> seen[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return CLIP_GRID;
+    if (dev < 64 && (sms = seen[dev].load(std::memory_order_relaxed)) == 0) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return CLIP_GRID;
+        seen[dev].store(sms, std::memory_order_relaxed);
+    }
+    return sms > 0 ? std::min(CLIP_GRID, sms * CB) : CLIP_GRID;
+}
+
 template <int MAXS>
 cudaError_t clip(const adj_grad_seg *segs, int64_t nseg, float max_norm, float *out, char *base, cudaStream_t st) {
     ClipWs ws;
@@ -787,7 +800,8 @@ cudaError_t clip(const adj_grad_seg *segs, int64_t nseg, float max_norm, float *
     int64_t bytes = 0;
     for (int64_t i = 0; i < nseg; ++i) bytes += segs[i].n * (segs[i].dtype == ADJ_BF16 ? 2 : 4);
     t.chunk = bytes < int64_t(152) * 16384 ? CT : 4 * CT;
-    auto grid = [&] { return unsigned(std::max<int64_t>(1, std::min<int64_t>(t.chunks, CLIP_GRID))); };
+    const int most = clip_blocks();
+    auto grid = [&] { return unsigned(std::max<int64_t>(1, std::min<int64_t>(t.chunks, most))); };
     int64_t i = fill(t, segs, 0, nseg);
     if (i >= nseg) {
         ProfScope ps(K_CLIP_NORM, st);
