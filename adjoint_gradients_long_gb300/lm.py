@@ -110,6 +110,7 @@ class LinAttn(_Lin):
         self._out = self.o.data_ptr(), self.s1.data_ptr(), self.ws.data_ptr(), self.ws_bytes
         if backward:
             self.dq, self.dk, self.dv = self._empty(self.qk), self._empty(self.qk), self._empty(self.vo)
+            self._strided = {("q", None): self.dq, ("k", None): self.dk, ("v", None): self.dv}
             self.dg = self._empty((B, T, H), torch.float32)
             self.ds0 = self._empty((B, H, Dk, Dv), torch.float32)
 
@@ -118,16 +119,23 @@ class LinAttn(_Lin):
         self._fwd(*self._inputs(q, k, v, g), self._state("s0", s0), *self._out, raw_stream(self.device))
         return self.o, self.s1
 
+    def _like(self, name, x):
+        """The gradient of x, in x's layout: one array for each layout that has been met, kept with
+        the object, as a captured graph goes on writing to the one that it was captured with."""
+        at = name, None if x.is_contiguous() else x.stride()
+        if at not in self._strided:
+            self._strided[at] = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if at[1] is None
+                                 else torch.empty_strided(x.shape, at[1], dtype=x.dtype, device=x.device))
+        return self._strided[at]
+
     def backward(self, q, k, v, g, go, s0=None, ds1=None):
-        """(dq, dk, dv, dg, ds0) for the cotangents go of o and ds1 of s1."""
+        """(dq, dk, dv, dg, ds0) for the cotangents go of o and ds1 of s1; dq, dk and dv have the
+        layout of q, k and v."""
         if not self.has_backward:
             raise ValueError("this LinAttn was made without backward=True")
         at = self._inputs(q, k, v, g)
         at += self._state("s0", s0), _dense("go", go, self.vo, self.xt, self.device), self._state("ds1", ds1)
-        for name, x, y in (("q", q, self.dq), ("k", k, self.dk), ("v", v, self.dv)):
-            if x.stride() != y.stride() and x.numel():
-                # the gradients have the layout of their inputs
-                setattr(self, "d" + name, torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=x.device))
+        self.dq, self.dk, self.dv = self._like("q", q), self._like("k", k), self._like("v", v)
         self._bwd(*at, self.dq.data_ptr(), self.dk.data_ptr(), self.dv.data_ptr(), self.dg.data_ptr(), self.ds0.data_ptr(),
                   *self._out[2:], raw_stream(self.device))
         return self.dq, self.dk, self.dv, self.dg, self.ds0

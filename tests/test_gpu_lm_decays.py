@@ -97,3 +97,26 @@ def test_same_bits_again_and_on_another_stream(B, T, H, Hk, D, bf16):
         for y, z in zip(outs, first):
             assert torch.equal(y, z)
     assert a.status() == 0
+
+
+def test_graph_outlives_another_layout():
+    """A captured backward pass replays into its own arrays after a call in another layout."""
+    from adjoint_gradients_long_gb300 import lm
+    B, T, H, D = 2, 200, 2, 64
+    gate = lambda gen, s: torch.log(torch.sigmoid(torch.randn(s, generator=gen) + 3))  # noqa: E731
+    x = inputs(B, T, H, H, D, D, True, 5, gate)
+    wide = torch.cat([x[n].flatten(2) for n in "qkv"], -1)
+    apart = [wide[..., i * H * D:(i + 1) * H * D].unflatten(-1, (H, D)) for i in range(3)]
+    a = lm.LinAttn(B, T, H, D, D, backward=True)
+    first = [y.clone() for y in a.backward(x["q"], x["k"], x["v"], x["g"], x["go"])[:4]]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.backward(x["q"], x["k"], x["v"], x["g"], x["go"])
+    at = [a.dq.data_ptr(), a.dk.data_ptr(), a.dv.data_ptr()]
+    outs = a.backward(*apart, x["g"], x["go"])[:4]
+    assert [y.stride() for y in outs[:3]] == [y.stride() for y in apart]
+    assert all(torch.equal(y, z) for y, z in zip(outs, first))
+    g.replay()                                   # into the arrays that the object still holds
+    again = a.backward(x["q"], x["k"], x["v"], x["g"], x["go"])
+    assert [y.data_ptr() for y in again[:3]] == at
+    assert all(torch.equal(y, z) for y, z in zip(again, first))
