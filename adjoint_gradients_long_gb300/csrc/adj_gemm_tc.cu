@@ -1527,15 +1527,24 @@ static bool ro_enabled() {
     return g_ro_mode == 1;
 }
 
-// Whether pair GEMMs with a long K (a mainloop bound by operand delivery) run as quads.
+// Whether pair GEMMs with a long K (a mainloop bound by operand delivery) run as quads.  Their
+// multicast loads are for a process that works alone on the one GPU that it sees: a rank of several
+// (WORLD_SIZE, as the launchers of distributed programs set it) or a process with more GPUs takes the
+// pairs.
 static int g_quad_mode = -1;
 static bool quad_enabled() {
     if (g_quad_mode < 0) {
-        const char *v = getenv("ADJ_GEMM_QUAD");
-        g_quad_mode = (v && v[0] == '0') ? 0 : 1;
+        const char *v = getenv("ADJ_GEMM_QUAD"), *w = getenv("WORLD_SIZE");
+        int gpus = 0;
+        if (cudaGetDeviceCount(&gpus) != cudaSuccess) {
+            gpus = 0;
+            cudaGetLastError();
+        }
+        g_quad_mode = (v && v[0] == '0') || (w && atoi(w) > 1) || gpus > 1 ? 0 : 1;
     }
     return g_quad_mode == 1;
 }
+extern "C" int adj_gemm_multicast(void) { return quad_enabled() ? 1 : 0; }
 
 // Whether GEMMs whose operands are both bf16 and both loaded by TMA run as CTA pairs.
 static int g_pair_mode = -1;   // -1: not read yet

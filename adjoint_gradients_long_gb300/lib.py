@@ -24,7 +24,7 @@ EXPORTS = ("adj_workspace_bytes", "adj_fwd_scan", "adj_loss_mse", "adj_bwd_full"
            "adj_profile_reset", "adj_profile_kernels", "adj_profile_name", "adj_profile_read", "adj_rms_norm",
            "adj_rms_norm_bwd", "adj_selftest_waits", "adj_selftest_ws_bytes", "adj_sel_fwd", "adj_sel_bwd",
            "adj_sel_param_grad", "adj_sel_rowdot_cols", "adj_lin_workspace_bytes", "adj_lin_fwd", "adj_lin_bwd",
-           "adj_lin_step", "adj_logprob", "adj_clip_workspace_bytes", "adj_grad_clip")
+           "adj_lin_step", "adj_logprob", "adj_clip_workspace_bytes", "adj_grad_clip", "adj_gemm_multicast")
 
 
 class AdjError(RuntimeError):
@@ -109,6 +109,8 @@ def load(path: str = LIB_PATH):
         lib.adj_status_str.argtypes = [ctypes.c_int]
         lib.adj_status_str.restype = ctypes.c_char_p
         lib.adj_launch_count.restype = ctypes.c_ulonglong
+        lib.adj_gemm_multicast.argtypes = []
+        lib.adj_gemm_multicast.restype = ctypes.c_int
         lib.adj_profile_enable.argtypes = [ctypes.c_int]
         lib.adj_profile_name.argtypes = [ctypes.c_int]
         lib.adj_profile_name.restype = ctypes.c_char_p

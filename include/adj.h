@@ -389,6 +389,11 @@ adj_status adj_fwd_scan_noalloc(const adj_dims *dims, const adj_weights *w, cons
 size_t adj_selftest_ws_bytes(void);
 adj_status adj_selftest_waits(void *ws, size_t ws_bytes, int which, void *stream);
 
+/* 1 if this process's GEMMs may take the four-CTA layout, whose loads are multicast inside the
+ * cluster: in a process that is no rank of several (WORLD_SIZE unset or 1) and sees one GPU at most,
+ * unless ADJ_GEMM_QUAD=0.  Read once a process. */
+int adj_gemm_multicast(void);
+
 /* ---- Launch accounting and per-kernel timing (a library facility; the pages
  * describe no implementation, so these have no counterpart there).
  * adj_launch_count: kernels launched by this library since it was loaded.
