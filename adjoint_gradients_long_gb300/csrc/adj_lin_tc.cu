@@ -405,9 +405,10 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
                 // F_K, F_P: also every warp has read the last chunk's O1 and O2
                 if (!wait(F_K, n)) break;
                 tc_fence_after();
-                product<VW, TCH / 16, true, true>(tmem + T_U(n), k, WIDE, v, PANEL, false);
-                product<VW, TCH / 16, true, true>(tmem + T_U(n), q, WIDE, v, PANEL, true);
-                if (parts == 3) product<VW, TCH / 16, true, true>(tmem + T_U(n), S_AT, WIDE, v, PANEL, true);
+                // the accumulator truncates: the smaller parts first, while it is small
+                if (parts == 3) product<VW, TCH / 16, true, true>(tmem + T_U(n), S_AT, WIDE, v, PANEL, false);
+                product<VW, TCH / 16, true, true>(tmem + T_U(n), q, WIDE, v, PANEL, parts == 3);
+                product<VW, TCH / 16, true, true>(tmem + T_U(n), k, WIDE, v, PANEL, true);
                 commit(bar(F_U));
                 if (!wait(F_P, n)) break;
                 tc_fence_after();
@@ -662,9 +663,10 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
                 if (!(h & 1) && n >= 2 && !wait(S_UFREE + u, (n >> 1) - 1)) break;
                 tc_fence_after();
                 const uint32_t at = base + s * STAGE, y = at + 3 * TILE_K, d = tmem + u * 128;
+                // the accumulator truncates: the smaller parts first
 #pragma unroll
-                for (int p = 0; p < 3; ++p)
-                    product<VW, SH / 16, true, true>(d, at + p * TILE_K, WIDE, y, PANEL, p || (h & 1));
+                for (int p = 2; p >= 0; --p)
+                    product<VW, SH / 16, true, true>(d, at + p * TILE_K, WIDE, y, PANEL, p < 2 || (h & 1));
                 commit(bar(S_EMPTY + s));
                 if (h & 1) commit(bar(S_U + u));
                 if (++s == RING) { s = 0; ++turn; }
@@ -975,8 +977,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 commit(bar(G_X1));
                 if (!wait(G_S, n)) break;
                 tc_fence_after();
-                product<KW, VS, false, false>(tmem + R2, W, PANEL, SHI, SPANEL, false);
-                product<KW, VS, false, false>(tmem + R2, W, PANEL, SLO, SPANEL, true);
+                product<KW, VS, false, false>(tmem + R2, W, PANEL, SLO, SPANEL, false);
+                product<KW, VS, false, false>(tmem + R2, W, PANEL, SHI, SPANEL, true);
                 commit(bar(G_G1));
                 if (!wait(G_R, n)) break;
                 tc_fence_after();
@@ -989,8 +991,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 commit(bar(G_X2));
                 if (!(wait(G_Z, n) && wait(G_E1, n))) break;
                 tc_fence_after();
-                product<KW, VS, false, false>(tmem + R2, V, PANEL, SHI, SPANEL, false);
-                product<KW, VS, false, false>(tmem + R2, V, PANEL, SLO, SPANEL, true);
+                product<KW, VS, false, false>(tmem + R2, V, PANEL, SLO, SPANEL, false);
+                product<KW, VS, false, false>(tmem + R2, V, PANEL, SHI, SPANEL, true);
                 if (!wait(G_RT, n)) break;
                 tc_fence_after();
                 product_ts<KW, TS>(tmem + R3, tmem + R0, Q, PANEL, false);

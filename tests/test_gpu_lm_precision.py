@@ -1,0 +1,53 @@
+"""How far linear attention of bf16 layers is from the fp64 oracle (GPU): as far as the storage of its
+results and sums in 32 bits make it, and no further.
+
+Bounds (relative, Frobenius):
+  s1        2.5e-7: the tensor cores' accumulator drops what is below its last bit.  A sum over a chunk
+            grows over 8 steps of 16 tokens, each of which loses half of a last bit of what is there on
+            average, half of 8.5e-8 of it; the smaller parts of the keys add up before.  And the fp32
+            roundings of the state.
+  ds0       6.5e-7: the same with a chunk in two halves, whose smaller parts also meet the larger one
+            of the half before: 16 steps
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from conftest import rel_fro  # noqa: E402
+from oracle import lm as olm  # noqa: E402
+from test_gpu_lm_decays import inputs, np64  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+STATE, ADJOINT = 2.5e-7, 6.5e-7
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from adjoint_gradients_long_gb300 import build
+    build.build()
+
+
+def errors(B, T, H, Hk, Dk, Dv, seed):
+    from adjoint_gradients_long_gb300 import lm
+    x = inputs(B, T, H, Hk, Dk, Dv, True, seed, lambda gen, s: torch.log(torch.sigmoid(torch.randn(s, generator=gen) + 3)))
+    a = lm.LinAttn(B, T, H, Dk, Dv, Hk=Hk, scale=Dk ** -0.5, backward=True)
+    got = [y.clone() for y in a.forward(x["q"], x["k"], x["v"], x["g"], x["s0"])]
+    got += a.backward(x["q"], x["k"], x["v"], x["g"], x["go"], x["s0"], x["ds1"])
+    h = {m: np64(y) for m, y in x.items()}
+    ref = [*olm.lin_forward(h["q"], h["k"], h["v"], h["g"], Dk ** -0.5, h["s0"]),
+           *olm.lin_backward(h["q"], h["k"], h["v"], h["g"], Dk ** -0.5, h["go"], h["s0"], h["ds1"])]
+    e = {m: rel_fro(np64(y), r) for m, y, r in zip(("o", "s1", "dq", "dk", "dv", "dg", "ds0"), got, ref)}
+    print(f"{B}x{T}, {H}/{Hk} heads of {Dk} and {Dv}: " + " ".join(f"{m}={v:.2e}" for m, v in e.items()))
+    return e
+
+
+SIZES = [(1, 77, 4, 4, 64, 64), (2, 128, 4, 4, 128, 128), (1, 300, 4, 2, 64, 64), (2, 500, 8, 2, 96, 64), (1, 1100, 2, 1, 64, 128)]
+
+
+@pytest.mark.parametrize("size", SIZES)
+def test_states(size):
+    e = errors(*size, seed=size[1])
+    assert e["s1"] <= STATE and e["ds0"] <= ADJOINT, e
