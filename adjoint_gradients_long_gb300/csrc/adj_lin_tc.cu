@@ -758,11 +758,13 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
 // With W = go, R = scale D . (W V^T) and P = scale D . (Q K^T) (tokens x tokens, lower triangle):
 //     dq = R K + scale f (W S^T)        dk = R^T Q + l (V Z^T)        dv = P^T W + l (K Z)
 // R, and R^T and P^T from products of their own (V W^T, K Q^T: a transpose is dearer than eight
-// instructions), are rounded to bf16 once, as the outputs are.  dg does not go through them:
-// its sums over W_ij = R_ij (q_i . k_j) are taken from the fp32 accumulators, by rows from R and by
-// columns from R^T, and S and Z come as sums of two bf16.
-// Measured, 2 x 8192 tokens x 16 heads of 128 (2048 chunks): 192 us, 14 us a chunk and SM; the
-// states before it 185 us in two launches.  Bound by the chain of a chunk: eleven products and four
+// instructions), are sums of two bf16 that take the columns of the fp32 values they come from, so that
+// no warp waits for another's reads.  dg does not go through them: its sums over
+// W_ij = R_ij (q_i . k_j) are taken from the fp32 accumulators, by rows from R and by columns from R^T,
+// and S and Z come as sums of two bf16 (dv takes two of Z's).  The accumulators drop what is below
+// their last bit: smaller parts are multiplied first.
+// Measured, 2 x 8192 tokens x 16 heads of 128 (2048 chunks): 204 us, 15 us a chunk and SM; the
+// states before it 183 us in two launches.  Bound by the chain of a chunk: eleven products and four
 // passes of the registers, each waiting for the one before.
 // Tensor memory: four accumulators of 128 columns; R^T and P^T lie where their products were.
 // The outputs leave through tiles whose last product is done: dq through S's, dk through Q's, dv
@@ -776,7 +778,7 @@ struct GradSums {
     float zs[CW];
 };
 enum { G_IN, G_S, G_Z, G_DEC0, G_DEC1, G_X1, G_G1, G_R, G_D1, G_X2, G_G2, G_RT, G_D2, G_D3, G_E1, G_E2, G_SC, G_DONE, G_DG,
-       G_OQ, G_OK, G_OV, G_SFREE, G_QFREE, G_LEFT, G_END, G_AR, G_COUNT = G_AR + 8 };
+       G_OQ, G_OK, G_OV, G_SFREE, G_QFREE, G_LEFT, G_END, G_COUNT };
 
 template <int KW, int VW>
 constexpr size_t grad_smem() {
@@ -807,8 +809,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < G_COUNT; ++i)
-            mbar_init(smem_u32(&ctl->bar[i]), i >= G_AR ? CG
-                                              : i == G_R || i == G_RT || (i >= G_E1 && i <= G_DONE) || (i >= G_OQ && i <= G_OV) ? CW : 1);
+            mbar_init(smem_u32(&ctl->bar[i]), i == G_R || i == G_RT || (i >= G_E1 && i <= G_DONE) || (i >= G_OQ && i <= G_OV) ? CW : 1);
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -968,7 +969,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
         }
     } else if (warp == W_MMA) {
         if (lane == 0) {
-            constexpr int KS = KW / 16, VS = VW / 16, TS = TCH / 16;
+            constexpr int KS = KW / 16, VS = VW / 16, T8 = TCH / 8;
             for (int64_t n = 0; n < N; ++n) {
                 if (!wait(G_IN, n)) break;
                 tc_fence_after();
@@ -982,7 +983,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 commit(bar(G_G1));
                 if (!wait(G_R, n)) break;
                 tc_fence_after();
-                product_ts<KW, TS>(tmem + R3, tmem + R0, K, PANEL, false);
+                product_ts2<KW, T8>(tmem + R3, tmem + R0, K, PANEL);
                 commit(bar(G_D1));
                 product<TCH, KS, false, false>(tmem + R1, K, PANEL, Q, PANEL, false);
                 if (!wait(G_D1, n)) break;              // R0 has been read
@@ -995,12 +996,13 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 product<KW, VS, false, false>(tmem + R2, V, PANEL, SHI, SPANEL, true);
                 if (!wait(G_RT, n)) break;
                 tc_fence_after();
-                product_ts<KW, TS>(tmem + R3, tmem + R0, Q, PANEL, false);
+                product_ts2<KW, T8>(tmem + R3, tmem + R0, Q, PANEL);
                 commit(bar(G_D2));
                 if (!wait(G_E2, n)) break;
                 tc_fence_after();
-                product<VW, KS, false, true>(tmem + R2, K, PANEL, SHI, SPANEL, false);
-                product_ts<VW, TS>(tmem + R3, tmem + R1, W, PANEL, false);
+                product<VW, KS, false, true>(tmem + R2, K, PANEL, SLO, SPANEL, false);
+                product<VW, KS, false, true>(tmem + R2, K, PANEL, SHI, SPANEL, true);
+                product_ts2<VW, T8>(tmem + R3, tmem + R1, W, PANEL);
                 commit(bar(G_D3));
             }
             int quiet = 0;
@@ -1031,13 +1033,12 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
             };
             // R, 8 columns of every block of 32, and the row sums of W
             {
-                uint32_t h[4][4];
                 float sum = 0.f;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
+                    uint32_t h[8] = {};
                     if (c > wq) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) h[c][e] = 0u;
+                        st8(lanes + R0 + 32 * c + j8, h);
                         continue;
                     }
                     float x[8], y[8], w[8];
@@ -1067,17 +1068,10 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                             if (j8 + e < lane) sum = fmaf(x[e], y[e], sum);
                         }
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[c][e] = pack(x[2 * e], x[2 * e + 1]);
+                    split8(x, h);
+                    st8(lanes + R0 + 32 * c + j8, h);
                 }
                 sums.r[g][i] = sum;
-                tc_fence_before();
-                arrive(G_AR + wq);
-                // the warps of these lanes have read their columns
-                if (!all_ok(wait(G_AR + wq, n))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) st4(lanes + R0 + 16 * c + 4 * g, h[c][0], h[c][1], h[c][2], h[c][3]);
                 st_wait();
                 tc_fence_before();
                 arrive(G_R);
@@ -1140,13 +1134,13 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
             tc_fence_after();
             const float wbj = dec.wb[i];
             {
-                uint32_t h[4][4], p[4][4];
                 float sum = 0.f;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
+                    uint32_t h[8] = {};
                     if (c < wq) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) h[c][e] = p[c][e] = 0u;
+                        st8(lanes + R0 + 32 * c + j8, h);
+                        st8(lanes + R1 + 32 * c + j8, h);
                         continue;
                     }
                     float x[8], y[8], w[8];
@@ -1182,22 +1176,12 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                             y[e] = in ? y[e] * d : 0.f;
                         }
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        h[c][e] = pack(x[2 * e], x[2 * e + 1]);
-                        p[c][e] = pack(y[2 * e], y[2 * e + 1]);
-                    }
+                    split8(x, h);
+                    st8(lanes + R0 + 32 * c + j8, h);
+                    split8(y, h);
+                    st8(lanes + R1 + 32 * c + j8, h);
                 }
                 sums.r[g][i] -= sum;
-                tc_fence_before();
-                arrive(G_AR + 4 + wq);
-                if (!all_ok(wait(G_AR + 4 + wq, n))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    st4(lanes + R0 + 16 * c + 4 * g, h[c][0], h[c][1], h[c][2], h[c][3]);
-                    st4(lanes + R1 + 16 * c + 4 * g, p[c][0], p[c][1], p[c][2], p[c][3]);
-                }
                 st_wait();
                 tc_fence_before();
                 arrive(G_RT);

@@ -24,9 +24,9 @@ __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
     return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
            (uint64_t(2) << 61);
 }
-// rows are K, M or N runs along a row; panel: distance of the 64-column panels
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t panel) {
-    return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(panel >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+// rows are K, M or N runs along a row; panel: distance of the 64-column panels; rows8: of 8-row groups
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t panel, uint32_t rows8 = 1024) {
+    return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(panel >> 4) << 16) | (uint64_t(rows8 >> 4) << 32) |
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 // bf16 x bf16 -> fp32, M = 128
@@ -77,6 +77,16 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t b, u
     const uint64_t db = tb.first();
 #pragma unroll
     for (int k = 0; k < K16; ++k) mma_ts(d, a + uint32_t(k) * 8u, db + tb.step(k), idesc(N, false, true), acc || k);
+}
+
+// A in tensor memory as sums of two bf16, in the columns of the fp32 values that they come from: of
+// every 8 columns the first four hold the values rounded down to bf16, the others what that lost.  A
+// step of 16 takes the same 8 rows of B twice: its 8-row groups lie a distance of zero apart.
+template <int N, int K8>
+__device__ __forceinline__ void product_ts2(uint32_t d, uint32_t a, uint32_t b, uint32_t b_panel) {
+    const uint64_t db = desc_mn(b, b_panel, 0u);
+#pragma unroll
+    for (int k = 0; k < K8; ++k) mma_ts(d, a + uint32_t(k) * 8u, db + uint64_t(k * 64), idesc(N, false, true), k != 0);
 }
 
 // Columns of one warp's 32 lanes: thread t gets those of lane t.  The wait is part of the load,
@@ -176,6 +186,14 @@ __device__ __forceinline__ uint32_t pack_top(float a, float b) {
     return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
 __device__ __forceinline__ float top(float a) { return __uint_as_float(__float_as_uint(a) & 0xFFFF0000u); }
+// 8 values as sums of two bf16, for product_ts2
+__device__ __forceinline__ void split8(const float (&p)[8], uint32_t (&r)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        r[e] = pack_top(p[2 * e], p[2 * e + 1]);
+        r[4 + e] = pack_top(p[2 * e] - top(p[2 * e]), p[2 * e + 1] - top(p[2 * e + 1]));
+    }
+}
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ uint4 lds(uint32_t a) {

@@ -8,6 +8,7 @@ Bounds (relative, Frobenius):
             roundings of the state.
   ds0       6.5e-7: the same with a chunk in two halves, whose smaller parts also meet the larger one
             of the half before: 16 steps
+  dq dk dv  2.0e-3: one rounding to bf16 of a normal value is 1.66e-3, two are 2.35e-3
 """
 import pytest
 
@@ -19,7 +20,7 @@ from test_gpu_lm_decays import inputs, np64  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
-STATE, ADJOINT = 2.5e-7, 6.5e-7
+STATE, ADJOINT, ONE_ROUNDING = 2.5e-7, 6.5e-7, 2.0e-3
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -51,3 +52,9 @@ SIZES = [(1, 77, 4, 4, 64, 64), (2, 128, 4, 4, 128, 128), (1, 300, 4, 2, 64, 64)
 def test_states(size):
     e = errors(*size, seed=size[1])
     assert e["s1"] <= STATE and e["ds0"] <= ADJOINT, e
+
+
+@pytest.mark.parametrize("size", SIZES)
+def test_gradients_of_tokens(size):
+    e = errors(*size, seed=size[1] + 1)
+    assert max(e["dq"], e["dk"], e["dv"]) <= ONE_ROUNDING, e
