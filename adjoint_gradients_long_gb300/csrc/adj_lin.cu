@@ -663,16 +663,19 @@ static size_t carve(LinArgs &a, bool bwd, bool bf16, char *base) {
     a.S = floats(n * dd);
     a.tot = floats(n);
     a.dS = a.dtot = a.pq = a.pk = nullptr;
-    a.shi = a.slo = a.zhi = a.zlo = nullptr;
+    a.shi = a.slo = a.s3 = a.zhi = a.zlo = a.z3 = nullptr;
     if (bwd) {
         a.dS = floats(n * dd);
         a.dtot = floats(n);
         if (bf16) {
-            const size_t all = size_t(heads) * cdiv(a.T, 128) * dd;
+            const size_t chunks = size_t(heads) * cdiv(a.T, 128), all = chunks * dd;
+            const size_t wide = chunks * lin_wide(a.Dk) * lin_wide(a.Dv);
             a.shi = halves(all);
             a.slo = halves(all);
+            a.s3 = halves(wide);
             a.zhi = halves(all);
             a.zlo = halves(all);
+            a.z3 = halves(wide);
         }
         if (a.Hk < a.H) {
             a.pq = floats(size_t(a.B * a.T) * a.H * a.Dk);

@@ -33,10 +33,14 @@ struct LinArgs {
     float *s1, *dg, *ds0;
     float *S, *dS;              // [B,H,NC,Dk,Dv]: the states entering / adjoint states leaving each chunk
     float *tot, *dtot;          // [B,H,NC]: the decay over each chunk (dtot: beside dS, where both are in flight)
-    // bf16: S and dS of every chunk as sums of two bf16 instead; S, dS, tot are then those of segments
-    __nv_bfloat16 *shi, *slo, *zhi, *zlo;
+    // bf16: S and dS of every chunk as sums of three bf16 instead; S, dS, tot are then those of segments.
+    // The third parts lie in pieces of 32 columns, [B,H,NC] x [columns / 32][rows][32], with rows and
+    // columns rounded up to lin_wide
+    __nv_bfloat16 *shi, *slo, *s3, *zhi, *zlo, *z3;
     float *pq, *pk;             // Hk < H: dq, dk of every head [B,T,H,Dk] fp32, summed afterwards
 };
+
+constexpr int lin_wide(int d) { return d <= 64 ? 64 : 128; }
 
 // exp(g) below this is under half the smallest fp32: the decay is zero, a new start.
 constexpr float LIN_RESET = -104.f;

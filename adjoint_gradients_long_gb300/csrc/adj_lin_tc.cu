@@ -560,12 +560,16 @@ constexpr size_t state_smem() {
     return RING * size_t(3 * KW + VW) * SH * 2 + (KEEP ? size_t(KW) * VW * 2 : 0) + 2 * sizeof(ChunkDecay) + sizeof(Ctl<S_COUNT>);
 }
 
+// Columns of a piece of a kept state's third part, which lies as [piece][row][32].
+constexpr int PIECE = 32;
 // KEEP: the walk starts from the state that enters the segment (a.S / a.dS, or s0 / ds1 when the
-// segment is the whole head), and the state met before every chunk is kept as a sum of two bf16
-// [B,H,NC,Dk,Dv], the operand of the backward pass.  The parts leave one after the other through
+// segment is the whole head), and the state met before every chunk is kept as a sum of three bf16
+// [B,H,NC,Dk,Dv], the operand of the backward pass.  The first two leave one after the other through
 // one tile, the second while the next chunk is being scaled; with a tile each and a ring of two
 // stages the walk waited for its copies in (all state launches of 2 x 8192 tokens x 16 heads of
-// 128: 241 us so, 208 us with one tile and three stages).
+// 128: 241 us so, 208 us with one tile and three stages).  The third leaves from the registers with the
+// second, 32 bytes a store in a layout of its own (the same launches now: 198 us, 183 us without a
+// third part, 310 us with it through the tile as well).
 template <int KW, int VW, bool KEEP>
 __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_constant__ BothMaps maps, const LinArgs a,
                                                               int nseg, int cps, unsigned *status) {
@@ -688,21 +692,36 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
         load_part<VH>(S, !KEEP ? nullptr : nseg > 1 ? (rev ? a.dS : a.S) + block * dd : init ? init + seg.bh * dd : nullptr,
                       i, c0, a);
         // the first (k even) or second part of the state; k counts the parts
+        // and the third with it
         auto keep = [&](int64_t k) {
             if (!KEEP) return true;
             if (k && !all_ok(wait(S_LEFT, k - 1))) return false;
-            if (i < KW)
+            if (i < KW) {
+                __nv_bfloat16 *third = (rev ? a.z3 : a.s3) + (seg.bh * a.NC + chunk(k >> 1)) * (KW * VW);
+                uint4 before = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int u = 0; u < VH; u += 8) {
-                    uint32_t h[4];
+                    uint32_t h[4], t[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float x = S[u + 2 * e], y = S[u + 2 * e + 1];
+                        float x = S[u + 2 * e], y = S[u + 2 * e + 1];
                         h[e] = pack(x, y);
-                        if (k & 1) h[e] = pack(x - lo_f(h[e]), y - hi_f(h[e]));
+                        if (k & 1) {
+                            x -= lo_f(h[e]);
+                            y -= hi_f(h[e]);
+                            h[e] = pack(x, y);
+                            t[e] = pack_top(x - lo_f(h[e]), y - hi_f(h[e]));
+                        }
                     }
                     sts(KEPT + unit_at(i, (c0 + u) >> 3, SPANEL), make_uint4(h[0], h[1], h[2], h[3]));
+                    if (k & 1) {
+                        const uint4 now = make_uint4(t[0], t[1], t[2], t[3]);
+                        const int e = c0 + u - 8;
+                        if (u & 8) stg32(third + (e / PIECE * KW + i) * PIECE + e % PIECE, before, now);
+                        before = now;
+                    }
                 }
+            }
             fence_proxy_async_smem();
             arrive(S_KEPT);
             return true;
@@ -761,28 +780,30 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
 // instructions), are sums of two bf16 that take the columns of the fp32 values they come from, so that
 // no warp waits for another's reads.  dg does not go through them: its sums over
 // W_ij = R_ij (q_i . k_j) are taken from the fp32 accumulators, by rows from R and by columns from R^T,
-// and S and Z come as sums of two bf16 (dv takes two of Z's).  The accumulators drop what is below
+// and S and Z come as sums of three bf16 (dv takes two of Z's).  The accumulators drop what is below
 // their last bit: smaller parts are multiplied first.
-// Measured, 2 x 8192 tokens x 16 heads of 128 (2048 chunks): 204 us, 15 us a chunk and SM; the
-// states before it 183 us in two launches.  Bound by the chain of a chunk: eleven products and four
+// The third parts come in pieces of 32 columns beside the tiles.  Without them the training batch below
+// takes 389 us for 429, and dg is off by 1e-6 to 2.6e-6 for 3e-7 to 5e-7.
+// Measured, 2 x 8192 tokens x 16 heads of 128 (2048 chunks): 230 us, 16 us a chunk and SM; the
+// states before it 198 us in two launches.  Bound by the chain of a chunk: eleven products and four
 // passes of the registers, each waiting for the one before.
 // Tensor memory: four accumulators of 128 columns; R^T and P^T lie where their products were.
 // The outputs leave through tiles whose last product is done: dq through S's, dk through Q's, dv
 // through Z's (fp32 parts of shared heads are stored by the lanes), so that the next task's Q, K, V
 // and W come in while dv is formed.  The decays are a task ahead.
 struct GradMaps {
-    CUtensorMap q, k, v, w, shi, slo, zhi, zlo, dq, dk, dv;
+    CUtensorMap q, k, v, w, shi, slo, s3, zhi, zlo, z3, dq, dk, dv;
 };
 struct GradSums {
     float r[CG][TCH], f[CG][TCH], l[CG][TCH];   // W: rows less columns; reads of S; leavings to Z
     float zs[CW];
 };
-enum { G_IN, G_S, G_Z, G_DEC0, G_DEC1, G_X1, G_G1, G_R, G_D1, G_X2, G_G2, G_RT, G_D2, G_D3, G_E1, G_E2, G_SC, G_DONE, G_DG,
-       G_OQ, G_OK, G_OV, G_SFREE, G_QFREE, G_LEFT, G_END, G_COUNT };
+enum { G_IN, G_S, G_Z, G_DEC0, G_DEC1, G_X1, G_R, G_D1, G_X2, G_RT, G_D2, G_D3, G_E1, G_E2, G_SC, G_DONE, G_DG,
+       G_OQ, G_OK, G_OV, G_SFREE, G_QFREE, G_LEFT, G_END, G_T, G_TFREE = G_T + 3, G_COUNT = G_TFREE + 3 };
 
 template <int KW, int VW>
 constexpr size_t grad_smem() {
-    return 2 * size_t(KW + VW) * 256 + 2 * size_t(KW) * VW * 2 + 2 * (sizeof(ChunkDecay) + TCH * 8) + sizeof(GradSums) +
+    return 2 * size_t(KW + VW) * 256 + 2 * size_t(KW) * VW * 2 + 3 * size_t(KW) * PIECE * 2 + 2 * (sizeof(ChunkDecay) + TCH * 8) + sizeof(GradSums) +
            sizeof(Ctl<G_COUNT>);
 }
 
@@ -799,8 +820,11 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
     constexpr uint32_t TILE_K = KW * 256, TILE_V = VW * 256, PANEL = TCH * 128, SPANEL = KW * 128, TILE_S = KW * VW * 2;
     constexpr int KH = KW / CG, VH = VW / CG;   // columns of a thread
     extern __shared__ __align__(1024) uint8_t sm[];
-    const uint32_t Q = smem_u32(sm), K = Q + TILE_K, V = K + TILE_K, W = V + TILE_V, SHI = W + TILE_V, SLO = SHI + TILE_S;
-    ChunkDecay *decs = reinterpret_cast<ChunkDecay *>(sm + 2 * (TILE_K + TILE_V) + 2 * TILE_S);
+    const uint32_t Q = smem_u32(sm), K = Q + TILE_K, V = K + TILE_K, W = V + TILE_V, SHI = W + TILE_V, SLO = SHI + TILE_S,
+                   THIRD = SLO + TILE_S;
+    constexpr int PN = VW / PIECE;
+    constexpr uint32_t TILE_P = KW * PIECE * 2;
+    ChunkDecay *decs = reinterpret_cast<ChunkDecay *>(sm + 2 * (TILE_K + TILE_V) + 2 * TILE_S + 3 * TILE_P);
     float *was = reinterpret_cast<float *>(decs + 2);   // wa and xl of both
     GradSums &sums = *reinterpret_cast<GradSums *>(was + 4 * TCH);
     auto *ctl = reinterpret_cast<Ctl<G_COUNT> *>(&sums + 1);
@@ -840,6 +864,19 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
         if (lane == 0) {
             int64_t n = 0;
             int in = 0, ss = 0, zz = 0;         // copies begun
+            int64_t turn = 0;                   // the ring's turn
+            int at = 0;
+            // pieces p0 .. p1 of a state's third part, as the products with those before are done
+            auto load_third = [&](const CUtensorMap *x, int p0, int p1, int z) {
+                for (int p = p0; p < p1; ++p) {
+                    if (turn && !wait(G_TFREE + at, turn - 1)) return false;
+                    mbar_arrive_expect_tx(bar(G_T + at), TILE_P);
+                    load2(THIRD + at * TILE_P, x, 0, (z * PN + p) * KW, bar(G_T + at));
+                    if (++at == 3) { at = 0; ++turn; }
+                }
+                return true;
+            };
+            constexpr int PA = PN < 3 ? PN : 3;
             for (; n < N; ++n) {
                 // the last task is done with the tiles: its products, and dk has left
                 if (n && !(wait(G_D3, n - 1) && wait(G_QFREE, n - 1))) break;
@@ -855,6 +892,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                     load4(Q + p * PANEL, &m.q, p * 64, int(k.hk), t, int(k.b), bar(G_IN));
                     load4(K + p * PANEL, &m.k, p * 64, int(k.hk), t, int(k.b), bar(G_IN));
                 }
+                if (!load_third(&m.s3, 0, PA, z)) break;
                 if (n && !wait(G_LEFT, n - 1)) break;         // dv too
                 mbar_arrive_expect_tx(bar(G_S), 2 * TILE_S);
                 ++ss;
@@ -862,6 +900,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                     load3(SHI + p * SPANEL, &m.shi, p * 64, 0, z, bar(G_S));
                     load3(SLO + p * SPANEL, &m.slo, p * 64, 0, z, bar(G_S));
                 }
+                if (!(load_third(&m.s3, PA, PN, z) && load_third(&m.z3, 0, PA, z))) break;
                 // Z in S's place, once dq has left through it
                 if (!wait(G_SFREE, n)) break;
                 mbar_arrive_expect_tx(bar(G_Z), 2 * TILE_S);
@@ -870,12 +909,15 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                     load3(SHI + p * SPANEL, &m.zhi, p * 64, 0, z, bar(G_Z));
                     load3(SLO + p * SPANEL, &m.zlo, p * 64, 0, z, bar(G_Z));
                 }
+                if (!load_third(&m.z3, PA, PN, z)) break;
             }
             // nothing of an abandoned walk is in flight when the block leaves
             int quiet = 0;
             if (in) mbar_wait(bar(G_IN), uint32_t(in - 1) & 1, &quiet, status);
             if (ss) mbar_wait(bar(G_S), uint32_t(ss - 1) & 1, &quiet, status);
             if (zz) mbar_wait(bar(G_Z), uint32_t(zz - 1) & 1, &quiet, status);
+            for (int i = 0; i < 3; ++i)
+                if (turn + (i < at)) mbar_wait(bar(G_T + i), uint32_t(turn + (i < at) - 1) & 1, &quiet, status);
         }
         __syncwarp();
     } else if (warp == W_OUT) {
@@ -970,17 +1012,30 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
     } else if (warp == W_MMA) {
         if (lane == 0) {
             constexpr int KS = KW / 16, VS = VW / 16, T8 = TCH / 8;
+            int64_t turn = 0;
+            int at = 0;
+            // R2 = x times the third part of a state
+            auto thirds = [&](uint32_t x) {
+                for (int p = 0; p < PN; ++p) {
+                    if (!wait(G_T + at, turn)) return false;
+                    tc_fence_after();
+                    product32<KW>(tmem + R2, x + (p >> 1) * PANEL + (p & 1) * (PIECE * 2), THIRD + at * TILE_P, p != 0);
+                    commit(bar(G_TFREE + at));
+                    if (++at == 3) { at = 0; ++turn; }
+                }
+                return true;
+            };
             for (int64_t n = 0; n < N; ++n) {
                 if (!wait(G_IN, n)) break;
                 tc_fence_after();
                 product<TCH, VS, false, false>(tmem + R0, W, PANEL, V, PANEL, false);
                 product<TCH, KS, false, false>(tmem + R1, Q, PANEL, K, PANEL, false);
                 commit(bar(G_X1));
-                if (!wait(G_S, n)) break;
+                // the accumulator truncates: the smaller parts first.  R2 has been read (dv)
+                if (!((n == 0 || wait(G_DONE, n - 1)) && thirds(W) && wait(G_S, n))) break;
                 tc_fence_after();
-                product<KW, VS, false, false>(tmem + R2, W, PANEL, SLO, SPANEL, false);
+                product<KW, VS, false, false>(tmem + R2, W, PANEL, SLO, SPANEL, true);
                 product<KW, VS, false, false>(tmem + R2, W, PANEL, SHI, SPANEL, true);
-                commit(bar(G_G1));
                 if (!wait(G_R, n)) break;
                 tc_fence_after();
                 product_ts2<KW, T8>(tmem + R3, tmem + R0, K, PANEL);
@@ -990,9 +1045,9 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 tc_fence_after();
                 product<TCH, VS, false, false>(tmem + R0, V, PANEL, W, PANEL, false);
                 commit(bar(G_X2));
-                if (!(wait(G_Z, n) && wait(G_E1, n))) break;
+                if (!(wait(G_E1, n) && thirds(V) && wait(G_Z, n))) break;
                 tc_fence_after();
-                product<KW, VS, false, false>(tmem + R2, V, PANEL, SLO, SPANEL, false);
+                product<KW, VS, false, false>(tmem + R2, V, PANEL, SLO, SPANEL, true);
                 product<KW, VS, false, false>(tmem + R2, V, PANEL, SHI, SPANEL, true);
                 if (!wait(G_RT, n)) break;
                 tc_fence_after();
@@ -1296,6 +1351,8 @@ cudaError_t run_bwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cuda
         (!a.pq && (!map_tokens(&m.dq, a.dq, a.Dk, a.Hk, a.T, a.B, a.ldq) || !map_tokens(&m.dk, a.dk, a.Dk, a.Hk, a.T, a.B, a.ldk))) ||
         !map_tokens(&m.dv, a.dv, a.Dv, a.H, a.T, a.B, a.ldv) || !map_states(&m.zhi, a.zhi, a.Dv, a.Dk, n, KW) || !map_states(&m.zlo, a.zlo, a.Dv, a.Dk, n, KW))
         return cudaErrorInvalidValue;
+    const int64_t pieces = n * (VW / PIECE);
+    if (!map_rows32(&m.s3, a.s3, pieces * KW, KW) || !map_rows32(&m.z3, a.z3, pieces * KW, KW)) return cudaErrorInvalidValue;
     // the states around every chunk: by segments where the heads alone would leave SMs idle
     LinArgs b = a;
     b.s1 = b.ds0 = nullptr;

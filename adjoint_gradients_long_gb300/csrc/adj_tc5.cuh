@@ -29,6 +29,11 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t panel, uint
     return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(panel >> 4) << 16) | (uint64_t(rows8 >> 4) << 32) |
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
+// rows of 32 values in the 64-byte swizzle, K along a row: unit u of row r lies at r * 64 + ((u ^ (r >> 1) & 3) << 4)
+__device__ __forceinline__ uint64_t desc_k64(uint32_t saddr) {
+    return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t(512 >> 4) << 32) | (uint64_t(1) << 46) |
+           (uint64_t(4) << 61);
+}
 // bf16 x bf16 -> fp32, M = 128
 __device__ __forceinline__ uint32_t idesc(int n, bool a_mn, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) | (uint32_t(n >> 3) << 17) |
@@ -69,6 +74,13 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t a_panel
     const uint64_t da = ta.first(), db = tb.first();
 #pragma unroll
     for (int k = 0; k < K16; ++k) mma_ss(d, da + ta.step(k), db + tb.step(k), idesc(N, A_MN, B_MN), acc || k);
+}
+// the same over 32 of K, with B [N][32] in the 64-byte swizzle
+template <int N>
+__device__ __forceinline__ void product32(uint32_t d, uint32_t a, uint32_t b, bool acc) {
+    const uint64_t da = desc_k(a), db = desc_k64(b);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) mma_ss(d, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc(N, false, false), acc || k);
 }
 // A in tensor memory: bf16 pairs, 8 columns a step; B across its rows
 template <int N, int K16>
@@ -175,6 +187,13 @@ __device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap *m, int x,
         : "memory");
 }
 
+__device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&v);
@@ -201,6 +220,12 @@ __device__ __forceinline__ uint4 lds(uint32_t a) {
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
+// 32 bytes to global memory, on 32
+__device__ __forceinline__ void stg32(void *p, uint4 a, uint4 b) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x),
+                 "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
 __device__ __forceinline__ void sts(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -226,6 +251,16 @@ inline bool map_states(CUtensorMap *m, const void *p, int64_t Dv, int64_t Dk, in
     const cuuint32_t box[3] = {64, cuuint32_t(rows), 1}, one[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, one,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// [n, 32] bf16, dense: boxes of `rows` rows, in the 64-byte swizzle
+inline bool map_rows32(CUtensorMap *m, const void *p, int64_t n, int rows) {
+    auto enc = tmap_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {32, cuuint64_t(n)}, strides[1] = {64};
+    const cuuint32_t box[2] = {32, cuuint32_t(rows)}, one[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -9,6 +9,8 @@ Bounds (relative, Frobenius):
   ds0       6.5e-7: the same with a chunk in two halves, whose smaller parts also meet the larger one
             of the half before: 16 steps
   dq dk dv  2.0e-3: one rounding to bf16 of a normal value is 1.66e-3, two are 2.35e-3
+  dg        1e-6: sums of products of two such accumulators each, 2 x 2.4e-7 and 2.4e-7 + 4.5e-7 in the
+            terms with a state; the states themselves to 2^-24
 """
 import pytest
 
@@ -20,7 +22,7 @@ from test_gpu_lm_decays import inputs, np64  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
-STATE, ADJOINT, ONE_ROUNDING = 2.5e-7, 6.5e-7, 2.0e-3
+STATE, ADJOINT, ONE_ROUNDING, DECAY = 2.5e-7, 6.5e-7, 2.0e-3, 1e-6
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -58,3 +60,9 @@ def test_states(size):
 def test_gradients_of_tokens(size):
     e = errors(*size, seed=size[1] + 1)
     assert max(e["dq"], e["dk"], e["dv"]) <= ONE_ROUNDING, e
+
+
+@pytest.mark.parametrize("size", SIZES)
+def test_gradients_of_decays(size):
+    e = errors(*size, seed=size[1] + 2)
+    assert e["dg"] <= DECAY, e
