@@ -152,15 +152,22 @@ def bind(name, *first):
     return call
 
 
+_torch_c = None
+
+
 def raw_stream(device) -> int:
     """torch's current stream of a CUDA device, as an address.  The library launches on the current
     device, and the address of a default stream names none: any other device is refused."""
-    import torch
-    if device.type != "cuda":
+    global _torch_c
+    if _torch_c is None:
+        import torch
+        _torch_c = torch._C
+    i = device.index
+    if i is None or device.type != "cuda":
         raise ValueError(f"the library runs on CUDA devices, got {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"{device} is not the current device; call inside torch.cuda.device({device.index})")
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    if i != _torch_c._cuda_getDevice():
+        raise ValueError(f"{device} is not the current device; call inside torch.cuda.device({i})")
+    return _torch_c._cuda_getCurrentRawStream(i)
 
 
 def _check(st: int, what: str):

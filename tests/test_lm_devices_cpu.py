@@ -30,7 +30,7 @@ def test_host_tensors_are_refused():
 
 
 def test_another_device_is_refused(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
     assert lib.raw_stream(torch.device("cuda", 0)) == 0
     with pytest.raises(ValueError, match="current device"):
