@@ -669,13 +669,13 @@ static size_t carve(LinArgs &a, bool bwd, bool bf16, char *base) {
         a.dtot = floats(n);
         if (bf16) {
             const size_t chunks = size_t(heads) * cdiv(a.T, 128), all = chunks * dd;
-            const size_t wide = chunks * lin_wide(a.Dk) * lin_wide(a.Dv);
+            const size_t third = chunks * lin_pieces(a.Dv) * 32 * a.Dk;
             a.shi = halves(all);
             a.slo = halves(all);
-            a.s3 = halves(wide);
+            a.s3 = halves(third);
             a.zhi = halves(all);
             a.zlo = halves(all);
-            a.z3 = halves(wide);
+            a.z3 = halves(third);
         }
         if (a.Hk < a.H) {
             a.pq = floats(size_t(a.B * a.T) * a.H * a.Dk);

@@ -34,13 +34,12 @@ struct LinArgs {
     float *S, *dS;              // [B,H,NC,Dk,Dv]: the states entering / adjoint states leaving each chunk
     float *tot, *dtot;          // [B,H,NC]: the decay over each chunk (dtot: beside dS, where both are in flight)
     // bf16: S and dS of every chunk as sums of three bf16 instead; S, dS, tot are then those of segments.
-    // The third parts lie in pieces of 32 columns, [B,H,NC] x [columns / 32][rows][32], with rows and
-    // columns rounded up to lin_wide
+    // The third parts lie in pieces of 32 columns, [B,H,NC] x [lin_pieces(Dv)][Dk][32]
     __nv_bfloat16 *shi, *slo, *s3, *zhi, *zlo, *z3;
     float *pq, *pk;             // Hk < H: dq, dk of every head [B,T,H,Dk] fp32, summed afterwards
 };
 
-constexpr int lin_wide(int d) { return d <= 64 ? 64 : 128; }
+__host__ __device__ constexpr int lin_pieces(int Dv) { return (Dv + 31) / 32; }
 
 // exp(g) below this is under half the smallest fp32: the decay is zero, a new start.
 constexpr float LIN_RESET = -104.f;

@@ -560,7 +560,7 @@ constexpr size_t state_smem() {
     return RING * size_t(3 * KW + VW) * SH * 2 + (KEEP ? size_t(KW) * VW * 2 : 0) + 2 * sizeof(ChunkDecay) + sizeof(Ctl<S_COUNT>);
 }
 
-// Columns of a piece of a kept state's third part, which lies as [piece][row][32].
+// Columns of a piece of a kept state's third part.
 constexpr int PIECE = 32;
 // KEEP: the walk starts from the state that enters the segment (a.S / a.dS, or s0 / ds1 when the
 // segment is the whole head), and the state met before every chunk is kept as a sum of three bf16
@@ -697,7 +697,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
             if (!KEEP) return true;
             if (k && !all_ok(wait(S_LEFT, k - 1))) return false;
             if (i < KW) {
-                __nv_bfloat16 *third = (rev ? a.z3 : a.s3) + (seg.bh * a.NC + chunk(k >> 1)) * (KW * VW);
+                const int pieces = lin_pieces(a.Dv);
+                __nv_bfloat16 *third = (rev ? a.z3 : a.s3) + ((seg.bh * a.NC + chunk(k >> 1)) * pieces * a.Dk + i) * PIECE;
                 uint4 before = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                 for (int u = 0; u < VH; u += 8) {
@@ -717,7 +718,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
                     if (k & 1) {
                         const uint4 now = make_uint4(t[0], t[1], t[2], t[3]);
                         const int e = c0 + u - 8;
-                        if (u & 8) stg32(third + (e / PIECE * KW + i) * PIECE + e % PIECE, before, now);
+                        if ((u & 8) && i < a.Dk && e / PIECE < pieces) stg32(third + e / PIECE * a.Dk * PIECE + e % PIECE, before, now);
                         before = now;
                     }
                 }
@@ -871,7 +872,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 for (int p = p0; p < p1; ++p) {
                     if (turn && !wait(G_TFREE + at, turn - 1)) return false;
                     mbar_arrive_expect_tx(bar(G_T + at), TILE_P);
-                    load2(THIRD + at * TILE_P, x, 0, (z * PN + p) * KW, bar(G_T + at));
+                    load4(THIRD + at * TILE_P, x, 0, 0, p, z, bar(G_T + at));   // past the state: zeros
                     if (++at == 3) { at = 0; ++turn; }
                 }
                 return true;
@@ -1351,8 +1352,8 @@ cudaError_t run_bwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cuda
         (!a.pq && (!map_tokens(&m.dq, a.dq, a.Dk, a.Hk, a.T, a.B, a.ldq) || !map_tokens(&m.dk, a.dk, a.Dk, a.Hk, a.T, a.B, a.ldk))) ||
         !map_tokens(&m.dv, a.dv, a.Dv, a.H, a.T, a.B, a.ldv) || !map_states(&m.zhi, a.zhi, a.Dv, a.Dk, n, KW) || !map_states(&m.zlo, a.zlo, a.Dv, a.Dk, n, KW))
         return cudaErrorInvalidValue;
-    const int64_t pieces = n * (VW / PIECE);
-    if (!map_rows32(&m.s3, a.s3, pieces * KW, KW) || !map_rows32(&m.z3, a.z3, pieces * KW, KW)) return cudaErrorInvalidValue;
+    const int pieces = lin_pieces(a.Dv);
+    if (!map_pieces(&m.s3, a.s3, a.Dk, pieces, n, KW) || !map_pieces(&m.z3, a.z3, a.Dk, pieces, n, KW)) return cudaErrorInvalidValue;
     // the states around every chunk: by segments where the heads alone would leave SMs idle
     LinArgs b = a;
     b.s1 = b.ds0 = nullptr;

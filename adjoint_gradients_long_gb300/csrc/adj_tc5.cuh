@@ -187,12 +187,6 @@ __device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap *m, int x,
         : "memory");
 }
 
-__device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
 
 __device__ __forceinline__ uint32_t pack(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -253,13 +247,14 @@ inline bool map_states(CUtensorMap *m, const void *p, int64_t Dv, int64_t Dk, in
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// [n, 32] bf16, dense: boxes of `rows` rows, in the 64-byte swizzle
-inline bool map_rows32(CUtensorMap *m, const void *p, int64_t n, int rows) {
+// [n, pieces, Dk, 32] bf16, dense: boxes of one piece, `rows` rows of it, in the 64-byte swizzle
+inline bool map_pieces(CUtensorMap *m, const void *p, int64_t Dk, int64_t pieces, int64_t n, int rows) {
     auto enc = tmap_encoder();
     if (!enc) return false;
-    const cuuint64_t dims[2] = {32, cuuint64_t(n)}, strides[1] = {64};
-    const cuuint32_t box[2] = {32, cuuint32_t(rows)}, one[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, one,
+    const cuuint64_t dims[4] = {32, cuuint64_t(Dk), cuuint64_t(pieces), cuuint64_t(n)};
+    const cuuint64_t strides[3] = {64, cuuint64_t(Dk) * 64, cuuint64_t(Dk * pieces) * 64};
+    const cuuint32_t box[4] = {32, cuuint32_t(rows), 1, 1}, one[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, one,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

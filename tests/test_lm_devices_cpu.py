@@ -42,3 +42,14 @@ def test_clip_refuses_what_no_launch_can_cover():
     for n in (1 << 40, 1 << 42, (1 << 43) - 1):
         segs = (lib.GradSeg * 1)(lib.GradSeg(1 << 40, 1 << 40, n, lib.F32, 0))
         assert lib.load().adj_grad_clip(segs, 1, 1.0, 1 << 40, 1 << 40, 1 << 50, None) == 2
+
+
+def test_backward_workspace_follows_the_heads():
+    """Small heads keep small states: what the gradients need beyond the forward pass is the kept
+    states of both directions, two dense parts and a third in pieces of 32 columns."""
+    def need(Dk, Dv, op, T=131072, H=64):
+        return lib.lin_workspace_bytes(lib.lin_dims(1, T, H, H, Dk, Dv), op)
+    for Dk, Dv in ((8, 8), (64, 64), (128, 128), (72, 40), (8, 128)):
+        parts = 2 * Dk * Dv + Dk * ((Dv + 31) // 32 * 32)          # values of a state, both directions alike
+        growth = need(Dk, Dv, lib.OP_LIN_BWD) - need(Dk, Dv, lib.OP_LIN_FWD)
+        assert growth <= 1.2 * 2 * 2 * (131072 // 128) * 64 * parts + 2 ** 20, (Dk, Dv)
