@@ -25,6 +25,12 @@ __device__ __forceinline__ void record_timeout(unsigned *status) {
     atomicOr(status, ST_TIMEOUT);
 }
 
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // ---------------------------------------------------------------- memory ops
 __device__ __forceinline__ unsigned ld_acquire(const unsigned *p) {
     unsigned v;

@@ -35,11 +35,9 @@
 namespace adj {
 namespace {
 
-constexpr int LC = 64;          // tokens of a chunk
+constexpr int LC = LIN_CHUNK;   // tokens of a chunk
 constexpr int LP = 132;         // row pitch of a [*][128] fp32 tile: rows 4 banks apart
 constexpr int PP = 68;          // row pitch of a [64][64] tile
-
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 __device__ __forceinline__ void ld4(const float *p, float (&v)[4]) {
     const float4 x = __ldg(reinterpret_cast<const float4 *>(p));
@@ -590,12 +588,6 @@ __global__ __launch_bounds__(256) void k_lin_step(const LinArgs a, float *__rest
     }
 }
 
-#define LIN_CUDA(x)                           \
-    do {                                      \
-        cudaError_t e_ = (x);                 \
-        if (e_ != cudaSuccess) return e_;     \
-    } while (0)
-
 constexpr size_t SM_GRAD = size_t(4 * LC * LP + 128 * LP + LC * PP) * 4;
 
 template <bool REV>
@@ -631,7 +623,7 @@ cudaError_t bwd_f32(const LinArgs &a, cudaStream_t st) {
 template <class T>
 cudaError_t share(const LinArgs &a, cudaStream_t st) {
     ProfScope ps(K_LIN_SHARE, st);
-    const int64_t n = cdiv(a.B * a.T * a.Hk * (a.Dk / 4), 256);
+    const int64_t n = lin_div(a.B * a.T * a.Hk * (a.Dk / 4), 256);
     k_lin_share<T><<<unsigned(std::min<int64_t>(n, 152 * 16)), 256, 0, st>>>(a);
     return cudaGetLastError();
 }
@@ -640,11 +632,9 @@ inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
-int64_t lin_chunks(int64_t T, bool) { return cdiv(T, LC); }
-
 cudaError_t launch_lin_scan(const LinArgs &a, int64_t n, int dirs, cudaStream_t st) {
     ProfScope ps(K_LIN_SCAN, st);
-    const int64_t half = cdiv(int64_t(a.Dk) * a.Dv, 512) * a.B * a.H;
+    const int64_t half = lin_div(int64_t(a.Dk) * a.Dv, 512) * a.B * a.H;
     k_lin_scan<<<unsigned(half * (dirs == 3 ? 2 : 1)), 128, 0, st>>>(a, n, half, dirs == 2);
     return cudaGetLastError();
 }
@@ -668,7 +658,7 @@ static size_t carve(LinArgs &a, bool bwd, bool bf16, char *base) {
         a.dS = floats(n * dd);
         a.dtot = floats(n);
         if (bf16) {
-            const size_t chunks = size_t(heads) * cdiv(a.T, 128), all = chunks * dd;
+            const size_t chunks = size_t(heads) * a.NC, all = chunks * dd;
             const size_t third = chunks * lin_pieces(a.Dv) * 32 * a.Dk;
             a.shi = halves(all);
             a.slo = halves(all);
@@ -705,8 +695,8 @@ cudaError_t launch_lin_step(const LinArgs &a, bool bf16, float *state, int64_t n
                             cudaStream_t st) {
     ProfScope ps(K_LIN_STEP, st);
     int cols = a.Dv;
-    while (cols % 8 == 0 && cols > 32 && a.B * a.H * cdiv(a.Dv, cols) < 152) cols /= 2;
-    const dim3 grid(unsigned(a.B * a.H), unsigned(cdiv(a.Dv, cols)));
+    while (cols % 8 == 0 && cols > 32 && a.B * a.H * lin_div(a.Dv, cols) < 152) cols /= 2;
+    const dim3 grid(unsigned(a.B * a.H), unsigned(lin_div(a.Dv, cols)));
     if (bf16) k_lin_step<__nv_bfloat16><<<grid, 256, 0, st>>>(a, state, n_slots, slots, cols);
     else k_lin_step<float><<<grid, 256, 0, st>>>(a, state, n_slots, slots, cols);
     return cudaGetLastError();

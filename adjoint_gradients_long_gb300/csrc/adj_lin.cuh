@@ -4,7 +4,17 @@
 
 #include "adj_internal.cuh"
 
+#define LIN_CUDA(x)                           \
+    do {                                      \
+        cudaError_t e_ = (x);                 \
+        if (e_ != cudaSuccess) return e_;     \
+    } while (0)
+
 namespace adj {
+
+inline int64_t lin_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+constexpr int LIN_CHUNK = 64, LIN_TC_CHUNK = 128;       // tokens of a chunk: fp32, bf16
+inline int64_t lin_chunks(int64_t T, bool bf16) { return lin_div(T, bf16 ? LIN_TC_CHUNK : LIN_CHUNK); }
 
 // The kernel's limit of dynamic shared memory, raised once a device (the call costs as much as a
 // launch): to the most that any launch of it may ask for.
@@ -43,12 +53,6 @@ __host__ __device__ constexpr int lin_pieces(int Dv) { return (Dv + 31) / 32; }
 
 // exp(g) below this is under half the smallest fp32: the decay is zero, a new start.
 constexpr float LIN_RESET = -104.f;
-
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // A sum kept as hi + lo, 48 bits: the fp64 pipe is too slow for one warp to keep up with a chunk.
 struct Sum2 {
@@ -134,7 +138,6 @@ struct LinDecay {
 // bytes of workspace after the header, and the arrays in it
 size_t lin_ws_bytes(const LinArgs &a, bool bwd, bool bf16);
 void lin_ws_carve(LinArgs &a, bool bwd, bool bf16, void *base);
-int64_t lin_chunks(int64_t T, bool bf16);
 
 cudaError_t launch_lin_fwd(const LinArgs &a, bool bf16, unsigned *status, cudaStream_t st);
 cudaError_t launch_lin_bwd(const LinArgs &a, bool bf16, unsigned *status, cudaStream_t st);

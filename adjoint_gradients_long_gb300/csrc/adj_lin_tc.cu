@@ -26,15 +26,13 @@ namespace {
 
 using namespace tc5;
 
-constexpr int TCH = 128;                // tokens of a chunk
+constexpr int TCH = LIN_TC_CHUNK;       // tokens of a chunk
 // Warps of a block: sixteen computing warps (four groups of four; a group covers the 128 lanes
 // of tensor memory, a warp the lanes of its number modulo four), and one warp each that issues
 // products, copies in, prepares the decays, and copies out.
 constexpr int CG = 4, CW = 4 * CG;
 constexpr int W_MMA = CW, W_TMA = CW + 1, W_AUX = CW + 2, W_OUT = CW + 3;
 constexpr int TC_BLOCK = (CW + 4) * 32;
-
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The decays of one chunk, by blocks of 32 tokens.  In powers of two, with G_t the sum of the
 // log decays from the chunk's start to t and E_b its value at block b's last token:
@@ -1295,12 +1293,6 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
     }
 }
 
-#define LIN_CUDA(x)                           \
-    do {                                      \
-        cudaError_t e_ = (x);                 \
-        if (e_ != cudaSuccess) return e_;     \
-    } while (0)
-
 // dirs: 1 forward, 2 both
 template <int KW, int VW, bool KEEP>
 cudaError_t run_states(const LinArgs &a, const LinSplit &sp, int dirs, unsigned *status, cudaStream_t st) {
@@ -1373,31 +1365,27 @@ cudaError_t run_bwd(const LinArgs &a, const LinSplit &sp, unsigned *status, cuda
 
 LinSplit lin_split(const LinArgs &a, bool bwd) {
     // the backward pass walks both directions side by side
-    const int64_t heads = a.B * a.H * (bwd ? 2 : 1), NC = cdiv(a.T, TCH);
+    const int64_t heads = a.B * a.H * (bwd ? 2 : 1), NC = a.NC;
     LinSplit s{1, int(NC)};
     // One block an SM: split the tokens when that fills SMs that would stay idle; a segment is at
     // least four chunks, below which its start costs more than it saves.
     if (heads < 152 && NC >= 8) {
         int64_t n = std::min<int64_t>(152 / heads, NC / 4);
         if (n > 1) {
-            s.cps = int(cdiv(NC, n));
-            s.nseg = int(cdiv(NC, s.cps));
+            s.cps = int(lin_div(NC, n));
+            s.nseg = int(lin_div(NC, s.cps));
         }
     }
     return s;
 }
 
-cudaError_t launch_lin_tc_fwd(const LinArgs &args, unsigned *status, cudaStream_t st) {
-    LinArgs a = args;
-    a.NC = cdiv(a.T, TCH);
+cudaError_t launch_lin_tc_fwd(const LinArgs &a, unsigned *status, cudaStream_t st) {
     const LinSplit sp = lin_split(a, false);
     if (a.Dk <= 64) return a.Dv <= 64 ? run_fwd<64, 64>(a, sp, status, st) : run_fwd<64, 128>(a, sp, status, st);
     return a.Dv <= 64 ? run_fwd<128, 64>(a, sp, status, st) : run_fwd<128, 128>(a, sp, status, st);
 }
 
-cudaError_t launch_lin_tc_bwd(const LinArgs &args, unsigned *status, cudaStream_t st) {
-    LinArgs a = args;
-    a.NC = cdiv(a.T, TCH);
+cudaError_t launch_lin_tc_bwd(const LinArgs &a, unsigned *status, cudaStream_t st) {
     const LinSplit sp = lin_split(a, true);
     if (a.Dk <= 64) return a.Dv <= 64 ? run_bwd<64, 64>(a, sp, status, st) : run_bwd<64, 128>(a, sp, status, st);
     return a.Dv <= 64 ? run_bwd<128, 64>(a, sp, status, st) : run_bwd<128, 128>(a, sp, status, st);

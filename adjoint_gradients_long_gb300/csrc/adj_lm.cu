@@ -13,12 +13,6 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // 16 bytes of T as floats
 template <class T>
 struct Vec;
@@ -190,7 +184,7 @@ __device__ __forceinline__ Stat join(Stat a, Stat b) {
     for (int k = 0; k < 2; ++k) {
         const Stat &x = k ? b : a;
         if (x.s == 0.f) continue;                        // nothing, or only masked values
-        const float d = r.from(Ref(x.m)), e = ex2(d);
+        const float d = r.from(Ref(x.m)), e = fast_exp2(d);
         o.s = fmaf(x.s, e, o.s);
         if (e != 0.f) o.t += e * fmaf(x.s, d, x.t);
     }
@@ -227,7 +221,7 @@ __device__ __forceinline__ Stat warp_join(Stat x) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
     if (x.s != 0.f) {
-        const float d = Ref(m).from(Ref(x.m)), f = ex2(d);
+        const float d = Ref(m).from(Ref(x.m)), f = fast_exp2(d);
         x.t = f == 0.f ? 0.f : f * fmaf(x.s, d, x.t);
         x.s *= f;
     }
@@ -251,7 +245,7 @@ __device__ __forceinline__ void distances(uint4 raw, const Ref &r, float (&d)[Ve
 #pragma unroll
     for (int e = 0; e < Vec<T>::N; ++e) {
         d[e] = r.at<FAR>(d[e]);
-        p[e] = ex2(d[e]);
+        p[e] = fast_exp2(d[e]);
         if (FAR) d[e] = fmaxf(d[e], -200.f);
     }
 }
@@ -282,7 +276,7 @@ __device__ __forceinline__ void take(Stat &st, const uint4 (&raw)[U]) {
     for (int u = 1; u < U; ++u) m = fmaxf(m, Vec<T>::largest(raw[u]));
     if (m > st.m) {
         if (st.s != 0.f) {
-            const float d = Ref(m).from(Ref(st.m)), f = ex2(d);
+            const float d = Ref(m).from(Ref(st.m)), f = fast_exp2(d);
             st.t = f == 0.f ? 0.f : f * fmaf(st.s, d, st.t);
             st.s *= f;
         }
@@ -497,7 +491,7 @@ __global__ __launch_bounds__(LPT, LPB) void k_logprob(const LogprobArgs a) {
         // the target's own value, over what this thread stored for its vector
         if (hot >= 0 && hot < nv && tid == (hot == 0 && odd_first ? 0 : hot == nv - 1 && odd_last ? 1 : (hot - w0) % LPT)) {
             const float d = ref.far ? ref.at<true>(at_y) : ref.at<false>(at_y);
-            out.p[y] = Vec<T>::put(fmaf(ex2(d), fmaf(c1, fmaxf(d, -200.f), c0), gl));
+            out.p[y] = Vec<T>::put(fmaf(fast_exp2(d), fmaf(c1, fmaxf(d, -200.f), c0), gl));
         }
     }
     if (blocks > 1) meet(blocks);                        // no block leaves while another reads its statistics
