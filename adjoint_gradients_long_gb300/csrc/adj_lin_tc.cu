@@ -1130,16 +1130,29 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 tc_fence_before();
                 arrive(G_R);
             }
-            // this thread's part of S, for <Z, S>
-            uint32_t sh[VH / 2], sl[VH / 2];
+            // 8 values of row i of the state in the tiles, from column 8 u of this thread's; <Z, S> takes the
+            // third part where at least 1 / 64 of it crosses the chunk
+            const bool deep = dec.total() >= 1.f / 64;
+            auto state8 = [&](int u, const __nv_bfloat16 *third, float (&v)[8]) {
+                const int c = g * VH + 8 * u;
+                const uint32_t at = i < KW ? unit_at(i, c >> 3, SPANEL) : 0u;
+                const uint4 x = lds(SHI + at), y = lds(SLO + at);
+                uint4 t = make_uint4(0u, 0u, 0u, 0u);
+                if (deep && i < a.Dk && c < a.Dv)
+                    t = __ldg(reinterpret_cast<const uint4 *>(
+                        third + (((k.bh * a.NC + k.n) * lin_pieces(a.Dv) + c / PIECE) * a.Dk + i) * PIECE + c % PIECE));
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w}, ts[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[2 * e] = (lo_f(xs[e]) + lo_f(ys[e])) + lo_f(ts[e]);
+                    v[2 * e + 1] = (hi_f(xs[e]) + hi_f(ys[e])) + hi_f(ts[e]);
+                }
+            };
+            // this thread's part of S
+            float S[VH / 8][8];
             if (!all_ok(wait(G_S, n))) break;
 #pragma unroll
-            for (int u = 0; u < VH / 8; ++u) {
-                const uint32_t at = i < KW ? unit_at(i, g * (VH / 8) + u, SPANEL) : 0u;
-                const uint4 x = lds(SHI + at), y = lds(SLO + at);
-                sh[4 * u] = x.x; sh[4 * u + 1] = x.y; sh[4 * u + 2] = x.z; sh[4 * u + 3] = x.w;
-                sl[4 * u] = y.x; sl[4 * u + 1] = y.y; sl[4 * u + 2] = y.z; sl[4 * u + 3] = y.w;
-            }
+            for (int u = 0; u < VH / 8; ++u) state8(u, a.s3, S[u]);
             // dq takes S's place: every warp has its part, and W S^T is formed
             arrive(G_SC);
             auto stage = [&](uint32_t tile, int c, const float (&y)[16]) {
@@ -1246,15 +1259,10 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_grad(const __grid_consta
                 float d = 0.f;
 #pragma unroll
                 for (int u = 0; u < VH / 8; ++u) {
-                    const uint32_t at = i < KW ? unit_at(i, g * (VH / 8) + u, SPANEL) : 0u;
-                    const uint4 x = lds(SHI + at), y = lds(SLO + at);
-                    const uint32_t zh[4] = {x.x, x.y, x.z, x.w}, zl[4] = {y.x, y.y, y.z, y.w};
+                    float z[8];
+                    state8(u, a.z3, z);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t s = sh[4 * u + e], t = sl[4 * u + e];
-                        d = fmaf(lo_f(zh[e]) + lo_f(zl[e]), lo_f(s) + lo_f(t), d);
-                        d = fmaf(hi_f(zh[e]) + hi_f(zl[e]), hi_f(s) + hi_f(t), d);
-                    }
+                    for (int e = 0; e < 8; ++e) d = fmaf(z[e], S[u][e], d);
                 }
                 if (i >= KW) d = 0.f;
 #pragma unroll

@@ -33,9 +33,10 @@ def _built():
     build.build()
 
 
-def errors(B, T, H, Hk, Dk, Dv, seed):
+def errors(B, T, H, Hk, Dk, Dv, seed, mean=3.0):
+    """mean: of the gates' arguments (3: decays around 0.95 a token; 12: hardly any)."""
     from adjoint_gradients_long_gb300 import lm
-    x = inputs(B, T, H, Hk, Dk, Dv, True, seed, lambda gen, s: torch.log(torch.sigmoid(torch.randn(s, generator=gen) + 3)))
+    x = inputs(B, T, H, Hk, Dk, Dv, True, seed, lambda gen, s: torch.log(torch.sigmoid(torch.randn(s, generator=gen) + mean)))
     a = lm.LinAttn(B, T, H, Dk, Dv, Hk=Hk, scale=Dk ** -0.5, backward=True)
     got = [y.clone() for y in a.forward(x["q"], x["k"], x["v"], x["g"], x["s0"])]
     got += a.backward(x["q"], x["k"], x["v"], x["g"], x["go"], x["s0"], x["ds1"])
@@ -65,4 +66,18 @@ def test_gradients_of_tokens(size):
 @pytest.mark.parametrize("size", SIZES)
 def test_gradients_of_decays(size):
     e = errors(*size, seed=size[1] + 2)
+    assert e["dg"] <= DECAY, e
+
+
+@pytest.mark.parametrize("size", [(2, 2, 3, 1, 16, 24), (4, 1, 8, 4, 64, 64), (2, 7, 4, 4, 128, 128), (1, 40, 4, 2, 72, 104)])
+def test_gradients_of_decays_where_the_state_counts(size):
+    """Few tokens between a state and its cotangent: dg is little else than their product."""
+    e = errors(*size, seed=size[1] + 3)
+    assert e["dg"] <= DECAY, e
+
+
+@pytest.mark.parametrize("size", [(2, 200, 4, 2, 64, 64), (1, 1000, 2, 2, 128, 128)])
+def test_gradients_of_weak_decays(size):
+    """States that cross whole chunks."""
+    e = errors(*size, seed=size[1] + 4, mean=12.0)
     assert e["dg"] <= DECAY, e
