@@ -156,17 +156,17 @@ _torch_c = None
 
 
 def raw_stream(device) -> int:
-    """torch's current stream of a CUDA device, as an address.  The library launches on the current
-    device, and the address of a default stream names none: any other device is refused."""
+    """torch's current stream of a CUDA device (with its index), as an address.  The library launches on
+    the current device, and the address of a default stream names none: any other device is
+    refused, and the host (a device without an index)."""
     global _torch_c
     if _torch_c is None:
         import torch
         _torch_c = torch._C
     i = device.index
-    if i is None or device.type != "cuda":
-        raise ValueError(f"the library runs on CUDA devices, got {device}")
-    if i != _torch_c._cuda_getDevice():
-        raise ValueError(f"{device} is not the current device; call inside torch.cuda.device({i})")
+    if i is None or i != _torch_c._cuda_getDevice():
+        raise ValueError(f"the library runs on the current CUDA device, got {device}" +
+                         ("" if i is None else f"; call inside torch.cuda.device({i})"))
     return _torch_c._cuda_getCurrentRawStream(i)
 
 

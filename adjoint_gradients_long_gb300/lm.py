@@ -40,8 +40,11 @@ def _dense(name, x, shape, dtype, device):
 
 
 def _device(device):
+    """The device as tensors name it: CUDA ones with an index, any other without."""
     d = torch.device(device)
-    return torch.device("cuda", torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
+    if d.type != "cuda":
+        return torch.device(d.type)
+    return d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
 def _workspace(nbytes, device):
@@ -234,7 +237,7 @@ class GradClip:
         self.outs = self.grads if outs is None else list(outs)
         if len(self.outs) != len(self.grads):
             raise ValueError(f"{len(self.outs)} outputs for {len(self.grads)} gradients")
-        self.device = self.grads[0].device if self.grads else _device("cuda")
+        self.device = _device(self.grads[0].device if self.grads else "cuda")
         kinds = {torch.float32: lib.F32, torch.bfloat16: lib.BF16}
         self.segs = (lib.GradSeg * max(1, len(self.grads)))()
         for i, (x, y) in enumerate(zip(self.grads, self.outs)):

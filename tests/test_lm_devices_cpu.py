@@ -26,6 +26,8 @@ def test_host_tensors_are_refused():
                  lambda: t.gradient(z(4, 100), y, z(4)), lambda: c.clip(1.0)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+    with pytest.raises(ValueError):
+        lm.TokenLogProbs(4, 100, x_bf16=False, device="cpu:0").forward(z(4, 100), y)
     assert lib.launch_count() == before
 
 
@@ -33,7 +35,7 @@ def test_another_device_is_refused(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
     assert lib.raw_stream(torch.device("cuda", 0)) == 0
-    with pytest.raises(ValueError, match="current device"):
+    with pytest.raises(ValueError, match="cuda:1"):
         lib.raw_stream(torch.device("cuda", 1))
 
 
