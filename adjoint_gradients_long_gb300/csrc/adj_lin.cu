@@ -23,10 +23,11 @@
 // Passes: (1) every chunk's own contribution to the state, in parallel; (2) a scan over the
 // chunks, element by element of the state; (3) every chunk's outputs, in parallel.
 //
-// fp32 storage keeps to the fp32 pipe: products of three bf16 parts would be six to one on the
-// tensor cores and still short of fp32.  Measured, 4 x 2000 tokens x 16 heads of 64 and 128: 69 us,
+// fp32 storage keeps to the fp32 pipe; on the tensor cores three bf16 parts would hold its operands, at
+// six products for one (not built).  Measured, 4 x 2000 tokens x 16 heads of 64 and 128: 68 us,
 // 35 us and 134 us for the passes (7.4 Gflop; the first version, one block an SM and scalar reads of
-// shared memory, took 586 us).
+// shared memory, took 586 us).  The gradients' last pass, k_lin_grad, still has that form: 807 us for
+// all passes of the gradients at the same sizes.
 #include <algorithm>
 
 #include "adj_lin.cuh"

@@ -1,5 +1,5 @@
 // adj_lin_tc.cu -- linear attention with a decay for each head on the tensor cores: the chunked
-// forward pass for bf16 storage.  adj_lin.cu states the formulas.
+// forward and backward passes for bf16 storage.  adj_lin.cu states the formulas.
 //
 // Chunks of 128 tokens: every product of a chunk is one tcgen05 accumulator of 128 rows.
 //     A  = Q K^T               (tokens x tokens)     exact operands
@@ -8,8 +8,12 @@
 //     U  = (l K)^T V           (Dk x Dv)             l K as a sum of three bf16 where the state is
 //                                                    a result, of two where it meets bf16 next
 //     o  = scale (f O1 + O2),  S <- f_last S + U     S in fp32 registers
-// with the decays D, f, l of adj_lin.cu.  O1 has one rounding to bf16 before the output's own; three
-// parts hold l K to fp32, because errors in a state that is a result stay.
+// with the decays D, f, l of adj_lin.cu.  Three parts hold l K to fp32, because errors in a state that is
+// a result stay.  O1 has one rounding to bf16 before the output's own, whose 1.66e-3 (relative, 2-norm)
+// grow to 1.70e-3 over the long prompt below and to 2.0e-3 to 2.4e-3 where little but the state is
+// read.  S in two parts was built and gives 1.66e-3 throughout: with a tile each, where heads leave
+// room for it, prompts took 4 to 8% longer, and at 128 columns of both, where the parts take turns
+// in one tile, 849 us for 764.  Outputs that are rounded to bf16 anyway were not worth that.
 //
 // One block walks the chunks of a segment of one head's tokens.  When there are fewer heads
 // than SMs, the tokens of a head are cut into segments: k_lin_tc_state sums up each segment's own
@@ -294,7 +298,7 @@ __device__ __forceinline__ void store_part(const float (&S)[VH], float *p, int d
 // KW, VW: Dk and Dv rounded up to 64 or 128; the columns past them are zeros (the copies fill
 // them) and the store clips them.
 //
-// Measured, 131072 tokens x 16 heads of 128 (2.15 GB): 514 us, 0.62 of the copy bandwidth, with
+// Measured, 131072 tokens x 16 heads of 128 (2.15 GB): 511 us, 0.62 of the copy bandwidth, with
 // 247 us for the segments' states before it.  A block takes 4.5 us a chunk.  By count the operands of
 // the products, the copies, the scaled keys, the state and the output tile move 600 KB through
 // shared memory, 4,700 cycles at 128 bytes a cycle: about half of that time.  The rest is taken to be
@@ -782,9 +786,9 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_state(const __grid_const
 // and S and Z come as sums of three bf16 (dv takes two of Z's).  The accumulators drop what is below
 // their last bit: smaller parts are multiplied first.
 // The third parts come in pieces of 32 columns beside the tiles.  Without them the training batch below
-// takes 389 us for 429, and dg is off by 1e-6 to 2.6e-6 for 3e-7 to 5e-7.
-// Measured, 2 x 8192 tokens x 16 heads of 128 (2048 chunks): 230 us, 16 us a chunk and SM; the
-// states before it 198 us in two launches.  Bound by the chain of a chunk: eleven products and four
+// takes 389 us for 433, and dg is off by 1e-6 to 4.5e-6 for 0.8e-7 to 4.9e-7.
+// Measured, 2 x 8192 tokens x 16 heads of 128 (2048 chunks): 225 us, 16 us a chunk and SM; the
+// states before it 200 us in two launches.  Bound by the chain of a chunk: its products and four
 // passes of the registers, each waiting for the one before.
 // Tensor memory: four accumulators of 128 columns; R^T and P^T lie where their products were.
 // The outputs leave through tiles whose last product is done: dq through S's, dk through Q's, dv

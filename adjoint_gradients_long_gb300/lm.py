@@ -230,7 +230,9 @@ class TokenLogProbs:
 
 class GradClip:
     """Clipping a fixed list of gradient tensors (fp32 or bf16, contiguous) by their global norm:
-    outs[i] = min(1, max_norm / (norm + 1e-6)) grads[i]; outs None clips in place."""
+    outs[i] = min(1, max_norm / (norm + 1e-6)) grads[i]; outs None clips in place.  The object keeps
+    these tensors and clips them at every call: a program that frees its gradients and makes
+    others needs another object for those."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)

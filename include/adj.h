@@ -268,11 +268,11 @@ adj_status adj_sel_param_grad(const adj_dims *dims, const adj_sel_weights *w, co
  * A value that is not finite spreads to the outputs of its chunk of 128 tokens and onwards.
  * Sizes: Dk and Dv multiples of 8 from 8 to 128; Hk divides H; H, B <= 65535; every ld* at
  * least its row's heads times width and a multiple of 16 bytes.  x_dtype fp32: products in
- * fp32.  x_dtype bf16: fp32 sums of products of bf16 operands; the states that a token reads
- * and, in the backward pass, the decayed pair weights are rounded to bf16 (the forward pass keeps
- * those as a sum of two); the states themselves stay fp32.  dg takes the states around a chunk
- * as sums of two bf16.  Relative errors: dg 1e-6 and ds0 8e-7 as a rule, 1.2e-5 and 5.7e-6 the
- * largest seen.
+ * fp32.  x_dtype bf16: fp32 sums of products of bf16 operands; states are fp32.  The states that
+ * a token reads in the forward pass are rounded to bf16: o has 1.7e-3 to 2.4e-3 as a rule (2-norm),
+ * of which its own rounding is 1.66e-3.  Every other value between is a sum of two or three bf16: dq, dk
+ * and dv have their own rounding alone; s1, ds0 and dg are fp32 sums on tensor cores, 4e-7, 6e-7
+ * and 7e-7 the largest seen.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int64_t B, T;
@@ -316,8 +316,11 @@ adj_status adj_lin_step(const adj_lin_dims *dims, const void *q, const void *k, 
  *   dlogits  [N,V] x_dtype (row pitch ldd) = glp_n (1[j = target] - p_j)
  *                                            - gent_n p_j (log p_j + entropy_n),
  *            the gradient for given cotangents glp of logp and gent of entropy [N] fp32
- * Minus infinity in x is a masked token (p = 0, dlogits = 0).  A row masked altogether has
- * lse = -inf, logp = -inf, entropy = 0 and dlogits = 0.  A NaN or +inf makes its row NaN.
+ * Minus infinity in x is a masked token (p = 0, dlogits = 0, or glp_n where it is the target), and so in
+ * effect is any value far below the row's largest; every finite value of the type is in range.  A row of
+ * minus infinity alone has lse = -inf, logp = -inf, entropy = 0 and dlogits = 0; a row of one
+ * finite value, however low, is uniform.  A NaN or +inf makes its row NaN.  Cotangents of the
+ * entropy up to 7e32 leave masked tokens without a gradient.
  * Any output may be NULL (top_id and top_logp both or neither; top = 0 for neither); dlogits
  * needs glp or gent (a NULL one counts as zeros) and may be the logits array itself when
  * ldd = ld.  logits and dlogits need only their type's alignment, ld, ldd >= V.  top <= V and
@@ -336,7 +339,8 @@ adj_status adj_logprob(const adj_logprob_dims *dims, const void *logits, const i
  * segs is a HOST array (copied at the call) of nseg tensors: src and dst device pointers of
  * n values of `dtype`, aligned to that type; dst = src clips in place (and with coef = 1
  * nothing is written then), any other overlap is an error of the caller; dst NULL: the tensor
- * counts in the norm only.  out: two device floats, norm and coef.  An infinite norm gives
+ * counts in the norm only.  out: two device floats, norm and coef.  Sums are fp32: squares past
+ * 3.4e38 make the norm infinite.  An infinite norm gives
  * coef 0, a NaN gives NaN (and NaN gradients): no call hides a step that has to be skipped.
  * Sums are in a fixed order: the same inputs give the same bits.  Up to 1000 tensors the blocks wait
  * for one another, with a limit: past it the status word is set, norm and coef are NaN, and what
