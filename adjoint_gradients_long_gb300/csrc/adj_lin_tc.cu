@@ -3,17 +3,15 @@
 //
 // Chunks of 128 tokens: every product of a chunk is one tcgen05 accumulator of 128 rows.
 //     A  = Q K^T               (tokens x tokens)     exact operands
-//     O1 = Q S                 (tokens x Dv)         S rounded to bf16
+//     O1 = Q S                 (tokens x Dv)         S as a sum of two bf16
 //     O2 = P V                 (tokens x Dv)         P = A . D as a sum of two bf16, in tensor memory
 //     U  = (l K)^T V           (Dk x Dv)             l K as a sum of three bf16 where the state is
 //                                                    a result, of two where it meets bf16 next
 //     o  = scale (f O1 + O2),  S <- f_last S + U     S in fp32 registers
 // with the decays D, f, l of adj_lin.cu.  Three parts hold l K to fp32, because errors in a state that is
-// a result stay.  O1 has one rounding to bf16 before the output's own, whose 1.66e-3 (relative, 2-norm)
-// grow to 1.70e-3 over the long prompt below and to 2.0e-3 to 2.4e-3 where little but the state is
-// read.  S in two parts was built and gives 1.66e-3 throughout: with a tile each, where heads leave
-// room for it, prompts took 4 to 8% longer, and at 128 columns of both, where the parts take turns
-// in one tile, 849 us for 764.  Outputs that are rounded to bf16 anyway were not worth that.
+// a result stay.  With S in one part o was off by 1.70e-3 (relative, 2-norm) over the long prompt below
+// and by 2.0e-3 to 2.4e-3 where little but the state is read, for the 1.66e-3 of its own rounding; the
+// second part costs that prompt 832 us for 763, and 1 to 6% where heads are smaller.
 //
 // One block walks the chunks of a segment of one head's tokens.  When there are fewer heads
 // than SMs, the tokens of a head are cut into segments: k_lin_tc_state sums up each segment's own
@@ -298,11 +296,12 @@ __device__ __forceinline__ void store_part(const float (&S)[VH], float *p, int d
 // KW, VW: Dk and Dv rounded up to 64 or 128; the columns past them are zeros (the copies fill
 // them) and the store clips them.
 //
-// Measured, 131072 tokens x 16 heads of 128 (2.15 GB): 511 us, 0.62 of the copy bandwidth, with
-// 247 us for the segments' states before it.  A block takes 4.5 us a chunk.  By count the operands of
-// the products, the copies, the scaled keys, the state and the output tile move 600 KB through
-// shared memory, 4,700 cycles at 128 bytes a cycle: about half of that time.  The rest is taken to be
+// Measured, 131072 tokens x 16 heads of 128 (2.15 GB): 581 us, 0.55 of the copy bandwidth, with
+// 248 us for the segments' states before it.  A block takes 5.1 us a chunk.  By count the operands of
+// the products, the copies, the scaled keys, the state and the output tile move 700 KB through
+// shared memory, 5,500 cycles at 128 bytes a cycle: about half of that time.  The rest is taken to be
 // the chain A -> l K -> U -> S and A -> P -> O2 -> o, which one block an SM cannot fill.
+// The second part of S lies where the keys of the chunk before were: their product U is what S came of.
 // The S tile also takes the third part of l K, between the last read of S and the next state.
 enum { F_FULL0, F_FULL1, F_EMPTY0, F_EMPTY1, F_DEC0, F_DEC1, F_A, F_PV, F_P, F_K, F_U, F_S, F_OUT, F_END, F_AR, F_COUNT = F_AR + 4 };
 
@@ -322,6 +321,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
     auto T_U = [](int64_t n) { return n & 1 ? 128u : 256u; };
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t base = smem_u32(sm), S_AT = base + 2 * STAGE;
+    // the second part of the state that enters chunk n: where the keys of the chunk before were
+    auto S_LO = [&](int64_t n) { return base + uint32_t(~n & 1) * STAGE + TILE_K; };
     ChunkDecay *dec = reinterpret_cast<ChunkDecay *>(sm + 2 * STAGE + TILE_K);
     auto *ctl = reinterpret_cast<Ctl<F_COUNT> *>(dec + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -347,7 +348,8 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             int64_t n = 0;
             for (; n < N; ++n) {
                 const int s = int(n & 1);
-                if (n >= 2 && !wait(F_EMPTY0 + s, (n >> 1) - 1)) break;
+                // the last chunk's O1 has read the state's second part in this stage
+                if ((n >= 2 && !wait(F_EMPTY0 + s, (n >> 1) - 1)) || (n && !wait(F_A, n - 1))) break;
                 const uint32_t at = base + s * STAGE, b = bar(F_FULL0 + s);
                 const int t = int((seg.n0 + n) * TCH);
                 mbar_arrive_expect_tx(b, STAGE);
@@ -396,13 +398,14 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             constexpr uint32_t WIDE = KW == 64 ? 0u : PANEL;
             for (int64_t n = 0; n < N; ++n) {
                 const uint32_t q = base + uint32_t(n & 1) * STAGE, k = q + TILE_K, v = k + TILE_K;
-                if (!(wait(F_FULL0 + int(n & 1), n >> 1) && wait(F_S, n))) break;
-                tc_fence_after();
-                product<VW, KW / 16, false, true>(tmem + T_O1(n), q, PANEL, S_AT, SPANEL, false);
                 // A goes where the last P was
-                if (n && !wait(F_PV, n - 1)) break;
+                if (!wait(F_FULL0 + int(n & 1), n >> 1) || (n && !wait(F_PV, n - 1))) break;
                 tc_fence_after();
                 product<TCH, KW / 16, false, false>(tmem + T_A, q, PANEL, k, PANEL, false);
+                if (!wait(F_S, n)) break;
+                tc_fence_after();
+                product<VW, KW / 16, false, true>(tmem + T_O1(n), q, PANEL, S_LO(n), SPANEL, false);
+                product<VW, KW / 16, false, true>(tmem + T_O1(n), q, PANEL, S_AT, SPANEL, true);
                 commit(bar(F_A));
                 // F_K, F_P: also every warp has read the last chunk's O1 and O2
                 if (!wait(F_K, n)) break;
@@ -433,15 +436,27 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
         float S[VH];
         const int64_t dd = int64_t(a.Dk) * a.Dv;
         load_part<VH>(S, nseg > 1 ? a.S + int64_t(blockIdx.x) * dd : a.s0 ? a.s0 + seg.bh * dd : nullptr, i, c0, a);
-        auto put_state = [&]() {
+        auto put_state = [&](int64_t n) {
             if (i < KW) {
+                const uint32_t lo = S_LO(n);
 #pragma unroll
-                for (int u = 0; u < VH; u += 8) put8(S_AT, SPANEL, i, (c0 + u) >> 3, S + u);
+                for (int u = 0; u < VH; u += 8) {
+                    const uint32_t at = unit_at(i, (c0 + u) >> 3, SPANEL);
+                    uint32_t h[4], l[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = S[u + 2 * e], y = S[u + 2 * e + 1];
+                        h[e] = pack_top(x, y);
+                        l[e] = pack(x - top(x), y - top(y));
+                    }
+                    sts(S_AT + at, make_uint4(h[0], h[1], h[2], h[3]));
+                    sts(lo + at, make_uint4(l[0], l[1], l[2], l[3]));
+                }
             }
             fence_proxy_async_smem();
             arrive(F_S);
         };
-        put_state();
+        put_state(0);
         for (int64_t n = 0; n < N; ++n) {
             const int s = int(n & 1);
             const uint32_t Q = base + s * STAGE, K = Q + TILE_K, V = K + TILE_K;
@@ -514,7 +529,7 @@ __global__ __launch_bounds__(TC_BLOCK, 1) void k_lin_tc_fwd(const __grid_constan
             tc_fence_after();
             state_update<VH>(S, lanes + T_U(n) + c0, d.total());
             tc_fence_before();
-            put_state();
+            put_state(n + 1);
             // the outputs, through V's tile
             const float f = d.first(i) * a.scale;
             if (!all_ok(wait(F_PV, n))) break;

@@ -268,11 +268,9 @@ adj_status adj_sel_param_grad(const adj_dims *dims, const adj_sel_weights *w, co
  * A value that is not finite spreads to the outputs of its chunk of 128 tokens and onwards.
  * Sizes: Dk and Dv multiples of 8 from 8 to 128; Hk divides H; H, B <= 65535; every ld* at
  * least its row's heads times width and a multiple of 16 bytes.  x_dtype fp32: products in
- * fp32.  x_dtype bf16: fp32 sums of products of bf16 operands; states are fp32.  The states that
- * a token reads in the forward pass are rounded to bf16: o has 1.7e-3 to 2.4e-3 as a rule (2-norm),
- * of which its own rounding is 1.66e-3.  Every other value between is a sum of two or three bf16: dq, dk
- * and dv have their own rounding alone; s1, ds0 and dg are fp32 sums on tensor cores, 4e-7, 6e-7
- * and 7e-7 the largest seen.
+ * fp32.  x_dtype bf16: fp32 sums of products of bf16 operands, in which every value between is a
+ * sum of two or three bf16; states are fp32.  o, dq, dk and dv have their own rounding alone; s1, ds0
+ * and dg are fp32 sums on tensor cores, off by 4e-7, 6e-7 and 7e-7 (2-norm) the largest seen.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int64_t B, T;

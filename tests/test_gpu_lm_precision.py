@@ -8,7 +8,7 @@ Bounds (relative, Frobenius):
             roundings of the state.
   ds0       6.5e-7: the same with a chunk in two halves, whose smaller parts also meet the larger one
             of the half before: 16 steps
-  dq dk dv  2.0e-3: one rounding to bf16 of a normal value is 1.66e-3, two are 2.35e-3
+  o dq dk dv  2.0e-3: one rounding to bf16 of a normal value is 1.66e-3, two are 2.35e-3
   dg        1e-6: sums of products of two such accumulators each, 2 x 2.4e-7 and 2.4e-7 + 4.5e-7 in the
             terms with a state; the states themselves to 2^-24
 """
@@ -55,6 +55,12 @@ SIZES = [(1, 77, 4, 4, 64, 64), (2, 128, 4, 4, 128, 128), (1, 300, 4, 2, 64, 64)
 def test_states(size):
     e = errors(*size, seed=size[1])
     assert e["s1"] <= STATE and e["ds0"] <= ADJOINT, e
+
+
+@pytest.mark.parametrize("size", SIZES + [(2, 7, 4, 4, 128, 128), (1, 40, 4, 2, 72, 104), (2, 300, 2, 2, 128, 128)])
+def test_outputs(size):
+    e = errors(*size, seed=size[1] + 5)
+    assert e["o"] <= ONE_ROUNDING, e
 
 
 @pytest.mark.parametrize("size", SIZES)
