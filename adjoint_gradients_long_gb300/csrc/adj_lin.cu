@@ -26,7 +26,7 @@
 // fp32 storage keeps to the fp32 pipe; on the tensor cores three bf16 parts would hold its operands, at
 // six products for one (not built).  Measured, 4 x 2000 tokens x 16 heads of 64 and 128: 68 us,
 // 35 us and 134 us for the passes (7.4 Gflop; the first version, one block an SM and scalar reads of
-// shared memory, took 586 us).  The gradients' last pass, k_lin_grad, still has that form: 807 us for
+// shared memory, took 586 us).  The gradients' last pass, k_lin_grad, still has that form: 806 us for
 // all passes of the gradients at the same sizes.
 #include <algorithm>
 
