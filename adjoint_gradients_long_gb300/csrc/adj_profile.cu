@@ -26,7 +26,8 @@ const char *g_names[K_COUNT] = {"proj_in", "fwd_scan", "proj_out", "loss", "cot_
                                 "input_grad", "rms_norm", "rms_norm_bwd", "weight_prep",
                                 "sel_proj", "sel_fwd", "sel_bwd", "sel_dW", "sel_dx",
                                 "lin_state", "lin_scan", "lin_out", "lin_grad", "lin_share", "lin_step",
-                                "logprob", "clip_norm", "clip_scale"};
+                                "logprob", "clip_norm", "clip_scale", "conv_fwd", "conv_bwd", "conv_step",
+                                "ssm_state", "ssm_carry", "ssm_out", "ssm_grad", "ssm_join", "ssm_step", "sample"};
 
 cudaEvent_t take() {
     if (!g_pool.empty()) {

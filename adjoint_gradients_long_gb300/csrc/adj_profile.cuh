@@ -34,6 +34,16 @@ enum KernelId {
     K_LOGPROB,
     K_CLIP_NORM,
     K_CLIP_SCALE,
+    K_CONV_FWD,
+    K_CONV_BWD,
+    K_CONV_STEP,
+    K_SSM_STATE,
+    K_SSM_CARRY,
+    K_SSM_OUT,
+    K_SSM_GRAD,
+    K_SSM_JOIN,
+    K_SSM_STEP,
+    K_SAMPLE,
     K_COUNT
 };
 

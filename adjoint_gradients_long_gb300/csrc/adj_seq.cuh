@@ -1,0 +1,195 @@
+// adj_seq.cuh -- what the short convolution and the selective scan share: sequences in a run of
+// tokens, vectors of eight channels, packed pairs of fp32, and the launchers.
+#pragma once
+#include <type_traits>
+
+#include "adj_internal.cuh"
+
+namespace adj {
+
+inline int64_t seq_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The sequences of a call (include/adj.h, "Sequences").  Offsets are held to [0, rows], and an index
+// that a search returns to [0, B), whatever the array holds.
+struct Seqs {
+    const int64_t *off;         // null: B sequences of T tokens each
+    int64_t B, T, rows;
+
+    __device__ __forceinline__ int64_t at(int64_t i) const {
+        const int64_t v = __ldg(off + i);
+        return v < 0 ? 0 : v > rows ? rows : v;
+    }
+    __device__ __forceinline__ int64_t begin(int64_t b) const { return off ? at(b) : b * T; }
+    __device__ __forceinline__ int64_t end(int64_t b) const { return off ? at(b + 1) : (b + 1) * T; }
+    // the sequence that holds token t, or -1
+    __device__ __forceinline__ int64_t find(int64_t t) const {
+        if (!off) return t < rows ? t / T : -1;
+        int64_t lo = 0, hi = B + 1;                     // entries at most t lie below lo, larger ones from hi on
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (at(mid) <= t) lo = mid + 1;
+            else hi = mid;
+        }
+        return lo <= B ? lo - 1 : -1;
+    }
+};
+
+// ---------------------------------------------------------------- eight channels
+template <class T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = __ldg(reinterpret_cast<const float4 *>(p));
+        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+    __device__ __forceinline__ static Raw8 of(const float (&x)[8]) {
+        return Raw8{make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7])};
+    }
+    __device__ __forceinline__ void store(float *p) const {
+        reinterpret_cast<float4 *>(p)[0] = a;
+        reinterpret_cast<float4 *>(p)[1] = b;
+    }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ static Raw8 of(const float (&x)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<uint32_t *>(&v);
+        }
+        return Raw8{make_uint4(w[0], w[1], w[2], w[3])};
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = u; }
+};
+// eight consecutive fp32
+__device__ __forceinline__ void ld8(const float *p, float (&x)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
+// ---------------------------------------------------------------- functions of one value
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float SEQ_LOG2E = 1.4426950408889634f, SEQ_LN2 = 0.6931471805599453f;
+// 1 / (1 + e^-x): the exponential overflows to infinity below -88, whose reciprocal is zero
+__device__ __forceinline__ float sigmoid_f(float x) { return fast_rcp(1.f + fast_exp2(-x * SEQ_LOG2E)); }
+
+// log(1 + e^v) = max(v, 0) + 2 atanh(s), s = e / (2 + e), e = e^-|v|: s is at most 1/3, where a polynomial
+// of degree 4 in s^2 gives atanh(s) / s to 4e-9 (interpolated at Chebyshev nodes).  The rounding of the
+// exponent's product is made up for, so that small steps keep 23 bits.
+__device__ __forceinline__ float softplus_f(float v) {
+    const float u = -fabsf(v), p = u * SEQ_LOG2E;
+    const float r = fmaf(u, 1.925963033500011e-8f, fmaf(u, SEQ_LOG2E, -p));
+    float e = fast_exp2(p);
+    e = fmaf(e, r * SEQ_LN2, e);
+    e = u < -100.f ? 0.f : e;                           // r is not finite where v is not
+    const float s = e * fast_rcp(2.f + e), q = s * s;
+    float c = fmaf(q, 0.14078889787197113f, 0.13982579112052917f);
+    c = fmaf(q, c, 0.20012298226356506f);
+    c = fmaf(q, c, 0.3333316147327423f);
+    return fmaxf(v, 0.f) + 2.f * fmaf(s * q, c, s);
+}
+
+// ---------------------------------------------------------------- pairs of fp32 in one instruction
+typedef unsigned long long pair_t;
+__device__ __forceinline__ pair_t pk(float x, float y) {
+    pair_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void upk(pair_t v, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) {
+    pair_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c) {
+    pair_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ pair_t add2(pair_t a, pair_t b) {
+    pair_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ pair_t exp2_2(pair_t v) {
+    float x, y;
+    upk(v, x, y);
+    return pk(fast_exp2(x), fast_exp2(y));
+}
+
+// ---------------------------------------------------------------- calls, resolved on the host
+struct ConvArgs {
+    Seqs q;
+    int64_t ldx, ldy;
+    int P, W, act;
+    const void *x, *s0, *go, *ds1;
+    const float *w, *bias;
+    void *y, *s1, *dx, *ds0;
+    float *dw, *dbias;
+    float *part;                // backward: [blocks of tokens][W+1][P]
+};
+size_t conv_ws_bytes(const ConvArgs &a);
+cudaError_t launch_conv_fwd(const ConvArgs &a, bool bf16, cudaStream_t st);
+cudaError_t launch_conv_bwd(const ConvArgs &a, bool bf16, cudaStream_t st);
+cudaError_t launch_conv_step(const ConvArgs &a, bool bf16, void *state, int64_t n_slots, const int32_t *slots,
+                             cudaStream_t st);
+
+struct SsmArgs {
+    Seqs q;
+    int64_t ldx, lddt, ldz, ldB, ldC, ldy;
+    int P, N;
+    const void *x, *dt, *Bm, *Cm, *z, *go;
+    const float *A, *D, *bias, *s0, *ds1;
+    void *y, *dx, *ddt, *dB, *dC, *dz;
+    float *s1, *dA, *dD, *dbias, *ds0;
+    // workspace
+    int64_t nseg, seglen;       // the tokens are cut into nseg segments of seglen (the last may be shorter)
+    float *seg;                 // [nseg][P][N]: the state a segment makes from nothing, then the one that enters it
+    float *step;                // [nseg][P]: sum of its steps; -1: a sequence begins in it
+    float *adj;                 // [nseg][P][N]: the same of the adjoint state, from the right
+    float *tile, *tstep;        // [tiles][P][N], [tiles][P]: state and steps from the segment's start to each tile
+    float *bc;                  // [blocks of channels][rows][2 N]: partial sums of dB and dC
+    float *par;                 // [nseg][P][N+2]: partial sums of dA, then of dD and ddt_bias
+};
+// cuts the tokens, and lays out the workspace from `base` (null: sizes alone); its bytes
+size_t ssm_plan(SsmArgs &a, bool bwd, void *base);
+cudaError_t launch_ssm_fwd(const SsmArgs &a, bool bf16, cudaStream_t st);
+cudaError_t launch_ssm_bwd(const SsmArgs &a, bool bf16, cudaStream_t st);
+cudaError_t launch_ssm_step(const SsmArgs &a, bool bf16, float *state, int64_t n_slots, const int32_t *slots,
+                            cudaStream_t st);
+
+struct SampleArgs {
+    int64_t N, V, ld;
+    const void *logits;
+    const float *u, *temperature, *top_p, *min_p;
+    const int32_t *top_k;
+    int64_t *token;
+    float *logp;
+};
+cudaError_t launch_sample(const SampleArgs &a, bool bf16, cudaStream_t st);
+
+}  // namespace adj

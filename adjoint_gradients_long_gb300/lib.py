@@ -16,6 +16,7 @@ F32, BF16 = 0, 1
 OP_FWD, OP_BWD_FULL, OP_BWD_TRUNC, OP_PARAM, OP_LOSS = 0, 1, 2, 3, 4
 OP_SEL_FWD, OP_SEL_BWD, OP_SEL_PARAM = 5, 6, 7
 OP_LIN_FWD, OP_LIN_BWD = 8, 9
+OP_SSM_FWD, OP_SSM_BWD = 10, 11
 LOGPROB_MAX_TOP = 32
 STATUS = {0: "ADJ_OK", 1: "ADJ_EINVAL", 2: "ADJ_ESHAPE", 3: "ADJ_EALIGN", 4: "ADJ_EDTYPE",
           5: "ADJ_EWORKSPACE", 6: "ADJ_ECUDA", 7: "ADJ_ETIMEOUT"}
@@ -24,7 +25,9 @@ EXPORTS = ("adj_workspace_bytes", "adj_fwd_scan", "adj_loss_mse", "adj_bwd_full"
            "adj_profile_reset", "adj_profile_kernels", "adj_profile_name", "adj_profile_read", "adj_rms_norm",
            "adj_rms_norm_bwd", "adj_selftest_waits", "adj_selftest_ws_bytes", "adj_sel_fwd", "adj_sel_bwd",
            "adj_sel_param_grad", "adj_sel_rowdot_cols", "adj_lin_workspace_bytes", "adj_lin_fwd", "adj_lin_bwd",
-           "adj_lin_step", "adj_logprob", "adj_clip_workspace_bytes", "adj_grad_clip", "adj_gemm_multicast")
+           "adj_lin_step", "adj_logprob", "adj_clip_workspace_bytes", "adj_grad_clip", "adj_gemm_multicast",
+           "adj_conv_workspace_bytes", "adj_conv_fwd", "adj_conv_bwd", "adj_conv_step", "adj_ssm_workspace_bytes",
+           "adj_ssm_fwd", "adj_ssm_bwd", "adj_ssm_step", "adj_sample")
 
 
 class AdjError(RuntimeError):
@@ -65,6 +68,26 @@ class GradSeg(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class ConvDims(ctypes.Structure):
+    """adj_conv_dims: ld* are element distances between tokens."""
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("P", ctypes.c_int32), ("W", ctypes.c_int32), ("x_dtype", ctypes.c_int32), ("packed", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class SsmDims(ctypes.Structure):
+    """adj_ssm_dims: ld* are element distances between tokens."""
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("ldx", ctypes.c_int64), ("lddt", ctypes.c_int64),
+                ("ldz", ctypes.c_int64), ("ldB", ctypes.c_int64), ("ldC", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("P", ctypes.c_int32), ("N", ctypes.c_int32), ("x_dtype", ctypes.c_int32), ("packed", ctypes.c_int32)]
+
+
+class SampleDims(ctypes.Structure):
+    """adj_sample_dims."""
+    _fields_ = [("N", ctypes.c_int64), ("V", ctypes.c_int64), ("ld", ctypes.c_int64), ("x_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 _VP, _SZ, _I64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64
 _PD, _PW, _PS = ctypes.POINTER(Dims), ctypes.POINTER(Weights), ctypes.POINTER(SelWeights)
@@ -100,6 +123,18 @@ def load(path: str = LIB_PATH):
         lib.adj_clip_workspace_bytes.argtypes = []
         lib.adj_clip_workspace_bytes.restype = _SZ
         lib.adj_grad_clip.argtypes = [_PG, _I64, ctypes.c_float, _VP, _VP, _SZ, _VP]
+        _PV, _PM = ctypes.POINTER(ConvDims), ctypes.POINTER(SsmDims)
+        lib.adj_conv_workspace_bytes.argtypes = [_PV]
+        lib.adj_conv_workspace_bytes.restype = _SZ
+        lib.adj_conv_fwd.argtypes = [_PV] + [_VP] * 8
+        lib.adj_conv_bwd.argtypes = [_PV] + [_VP] * 12 + [_SZ, _VP]
+        lib.adj_conv_step.argtypes = [_PV] + [_VP] * 4 + [_I64] + [_VP] * 3
+        lib.adj_ssm_workspace_bytes.argtypes = [_PM, ctypes.c_int]
+        lib.adj_ssm_workspace_bytes.restype = _SZ
+        lib.adj_ssm_fwd.argtypes = [_PM] + [_VP] * 13 + [_SZ, _VP]
+        lib.adj_ssm_bwd.argtypes = [_PM] + [_VP] * 22 + [_SZ, _VP]
+        lib.adj_ssm_step.argtypes = [_PM] + [_VP] * 9 + [_I64] + [_VP] * 3
+        lib.adj_sample.argtypes = [ctypes.POINTER(SampleDims)] + [_VP] * 9
         lib.adj_selftest_waits.argtypes = [_VP, _SZ, ctypes.c_int, _VP]
         lib.adj_selftest_waits.restype = ctypes.c_int
         lib.adj_selftest_ws_bytes.argtypes = []
@@ -118,7 +153,9 @@ def load(path: str = LIB_PATH):
         lib.adj_profile_read.restype = ctypes.c_int
         for f in ("adj_fwd_scan", "adj_loss_mse", "adj_bwd_full", "adj_bwd_trunc", "adj_param_grad",
                   "adj_stream_status", "adj_rms_norm", "adj_rms_norm_bwd", "adj_sel_fwd", "adj_sel_bwd",
-                  "adj_sel_param_grad", "adj_lin_fwd", "adj_lin_bwd", "adj_lin_step", "adj_logprob", "adj_grad_clip"):
+                  "adj_sel_param_grad", "adj_lin_fwd", "adj_lin_bwd", "adj_lin_step", "adj_logprob", "adj_grad_clip",
+                  "adj_conv_fwd", "adj_conv_bwd", "adj_conv_step", "adj_ssm_fwd", "adj_ssm_bwd", "adj_ssm_step",
+                  "adj_sample"):
             getattr(lib, f).restype = ctypes.c_int
         _lib = lib
     return _lib
@@ -335,3 +372,62 @@ def clip_workspace_bytes() -> int:
 def grad_clip(segs, nseg, max_norm, out, ws, ws_bytes, stream=None):
     """segs: a ctypes array of GradSeg."""
     _check(load().adj_grad_clip(segs, nseg, max_norm, ptr(out), ptr(ws), ws_bytes, _stream(stream)), "adj_grad_clip")
+
+
+def conv_dims(B, T, P, W, x_dtype=BF16, packed=0, act=1) -> ConvDims:
+    """Dense arrays; the ld* fields may be raised for column slices of wider ones."""
+    return ConvDims(B, T, P, P, P, W, x_dtype, packed, act, 0)
+
+
+def conv_workspace_bytes(d) -> int:
+    return int(load().adj_conv_workspace_bytes(ctypes.byref(d)))
+
+
+def conv_fwd(d, x, w, bias, s0, offsets, y, s1, stream=None):
+    _check(load().adj_conv_fwd(ctypes.byref(d), ptr(x), ptr(w), ptr(bias), ptr(s0), ptr(offsets), ptr(y), ptr(s1),
+                               _stream(stream)), "adj_conv_fwd")
+
+
+def conv_bwd(d, x, w, bias, s0, offsets, go, ds1, dx, dw, dbias, ds0, ws, ws_bytes, stream=None):
+    _check(load().adj_conv_bwd(ctypes.byref(d), ptr(x), ptr(w), ptr(bias), ptr(s0), ptr(offsets), ptr(go), ptr(ds1),
+                               ptr(dx), ptr(dw), ptr(dbias), ptr(ds0), ptr(ws), ws_bytes, _stream(stream)), "adj_conv_bwd")
+
+
+def conv_step(d, x, w, bias, state, n_slots, slots, y, stream=None):
+    _check(load().adj_conv_step(ctypes.byref(d), ptr(x), ptr(w), ptr(bias), ptr(state), n_slots, ptr(slots), ptr(y),
+                                _stream(stream)), "adj_conv_step")
+
+
+def ssm_dims(B, T, P, N, x_dtype=BF16, packed=0) -> SsmDims:
+    """Dense arrays; the ld* fields may be raised for column slices of wider ones."""
+    return SsmDims(B, T, P, P, P, N, N, P, P, N, x_dtype, packed)
+
+
+def ssm_workspace_bytes(d, op) -> int:
+    return int(load().adj_ssm_workspace_bytes(ctypes.byref(d), op))
+
+
+def ssm_fwd(d, x, dt, A, Bm, Cm, D, z, dt_bias, s0, offsets, y, s1, ws, ws_bytes, stream=None):
+    _check(load().adj_ssm_fwd(ctypes.byref(d), ptr(x), ptr(dt), ptr(A), ptr(Bm), ptr(Cm), ptr(D), ptr(z), ptr(dt_bias),
+                              ptr(s0), ptr(offsets), ptr(y), ptr(s1), ptr(ws), ws_bytes, _stream(stream)), "adj_ssm_fwd")
+
+
+def ssm_bwd(d, x, dt, A, Bm, Cm, D, z, dt_bias, s0, offsets, go, ds1, dx, ddt, dA, dB, dC, dD, dz, ddt_bias, ds0, ws,
+            ws_bytes, stream=None):
+    _check(load().adj_ssm_bwd(ctypes.byref(d), ptr(x), ptr(dt), ptr(A), ptr(Bm), ptr(Cm), ptr(D), ptr(z), ptr(dt_bias),
+                              ptr(s0), ptr(offsets), ptr(go), ptr(ds1), ptr(dx), ptr(ddt), ptr(dA), ptr(dB), ptr(dC),
+                              ptr(dD), ptr(dz), ptr(ddt_bias), ptr(ds0), ptr(ws), ws_bytes, _stream(stream)), "adj_ssm_bwd")
+
+
+def ssm_step(d, x, dt, A, Bm, Cm, D, z, dt_bias, state, n_slots, slots, y, stream=None):
+    _check(load().adj_ssm_step(ctypes.byref(d), ptr(x), ptr(dt), ptr(A), ptr(Bm), ptr(Cm), ptr(D), ptr(z), ptr(dt_bias),
+                               ptr(state), n_slots, ptr(slots), ptr(y), _stream(stream)), "adj_ssm_step")
+
+
+def sample_dims(N, V, ld, x_dtype=BF16) -> SampleDims:
+    return SampleDims(N, V, ld, x_dtype, 0)
+
+
+def sample(d, logits, u, temperature, top_k, top_p, min_p, token, logp, stream=None):
+    _check(load().adj_sample(ctypes.byref(d), ptr(logits), ptr(u), ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p),
+                             ptr(token), ptr(logp), _stream(stream)), "adj_sample")

@@ -77,7 +77,8 @@ typedef struct {
 enum {
     ADJ_OP_FWD = 0, ADJ_OP_BWD_FULL = 1, ADJ_OP_BWD_TRUNC = 2, ADJ_OP_PARAM = 3, ADJ_OP_LOSS = 4,
     ADJ_OP_SEL_FWD = 5, ADJ_OP_SEL_BWD = 6, ADJ_OP_SEL_PARAM = 7,  /* the general selective layer (below) */
-    ADJ_OP_LIN_FWD = 8, ADJ_OP_LIN_BWD = 9                         /* adj_lin_workspace_bytes only */
+    ADJ_OP_LIN_FWD = 8, ADJ_OP_LIN_BWD = 9,                        /* adj_lin_workspace_bytes only */
+    ADJ_OP_SSM_FWD = 10, ADJ_OP_SSM_BWD = 11                       /* adj_ssm_workspace_bytes only */
 };
 
 /* Workspace bytes that call `op` needs for these sizes (Tbar: the window of
@@ -355,6 +356,123 @@ typedef struct {
 size_t adj_clip_workspace_bytes(void);
 adj_status adj_grad_clip(const adj_grad_seg *segs, int64_t nseg, float max_norm, float *out, void *ws,
                          size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * What stands around a selective recurrence in such a model: a short causal convolution
+ * before it, and the recurrence itself with states that come in and go out.
+ *
+ * Sequences.  packed = 0: B sequences of T tokens, one behind the other (arrays [B,T,..]).
+ * packed = 1: B sequences of any lengths in T tokens together (arrays [T,..]); `offsets`
+ * [B+1] int64 on the DEVICE, 0 <= offsets[0] <= .. <= offsets[B] <= T: sequence b is the
+ * tokens offsets[b] to offsets[b+1], none if they are equal.  Tokens before offsets[0] and
+ * from offsets[B] on belong to no sequence: their inputs count for nothing, and their rows of
+ * the outputs stay as they were.  Offsets that break this rule give unspecified values, but
+ * no access out of bounds.  A sequence without tokens passes its state through.  Nothing
+ * reaches from one sequence into another, values that are not finite included (but for
+ * gradients of parameters, which sum over all).
+ * ld*: elements from one token to the next (so that arrays may be column slices of one
+ * projection), multiples of 16 bytes.  A pool of states has n_slots entries; slots [B] int32
+ * gives the entry of each sequence (NULL: entry b, needs n_slots >= B).  A slot outside
+ * [0, n_slots) leaves the pool untouched and gives a row of zeros (the padding of a batch); a
+ * slot given twice is a race.
+ * ------------------------------------------------------------------------- */
+
+/* Short causal convolution, each channel with its own W taps.  With the list
+ * c = s0[b,0..W-1), x_0, x_1, .. of a sequence:
+ *     p_t = bias + sum_j w[p,j] c_{t+j},    y_t = p_t, or p_t sigmoid(p_t) with act = 1
+ *   x, y [rows,P] x_dtype; w [P,W], bias [P] fp32 (bias NULL: zeros)
+ *   s0, s1 [B,W-1,P] x_dtype: the last W-1 entries of the list before and after the tokens
+ * P a multiple of 8, W 2 to 4; sums in fp32. */
+typedef struct {
+    int64_t B, T;
+    int64_t ldx, ldy;
+    int32_t P, W;
+    int32_t x_dtype, packed, act;
+    int32_t reserved;            /* zero */
+} adj_conv_dims;
+
+/* s0 NULL: zeros; s1 NULL: not written.  y may not alias an input.  No workspace. */
+adj_status adj_conv_fwd(const adj_conv_dims *dims, const void *x, const float *w, const float *bias, const void *s0,
+                        const int64_t *offsets, void *y, void *s1, void *stream);
+
+/* Workspace bytes of adj_conv_bwd (0 for sizes it rejects). */
+size_t adj_conv_workspace_bytes(const adj_conv_dims *dims);
+
+/* Gradients for the cotangents go [rows,P] of y (pitch ldy) and ds1 [B,W-1,P] of s1 (both
+ * x_dtype; ds1 NULL: zeros): dx (pitch ldx), dw [P,W] fp32, dbias [P] fp32 (NULL: not written),
+ * ds0 [B,W-1,P] x_dtype (NULL: not written).  No output may alias an input.  Sums in a fixed order. */
+adj_status adj_conv_bwd(const adj_conv_dims *dims, const void *x, const float *w, const float *bias, const void *s0,
+                        const int64_t *offsets, const void *go, const void *ds1, void *dx, float *dw, float *dbias,
+                        void *ds0, void *ws, size_t ws_bytes, void *stream);
+
+/* One token for each of B sequences (dims->T and packed are not read; ld* are the distances
+ * between sequences): state [n_slots,W-1,P] x_dtype is updated in place.  No workspace. */
+adj_status adj_conv_step(const adj_conv_dims *dims, const void *x, const float *w, const float *bias, void *state,
+                         int64_t n_slots, const int32_t *slots, void *y, void *stream);
+
+/* Selective scan, per channel p and state n:
+ *     d_t = softplus(dt_t + dt_bias),   h_t = exp(d_t A) h_{t-1} + d_t x_t B_t
+ *     v_t = sum_n C_t h_t + D x_t,      y_t = v_t, or v_t z_t sigmoid(z_t) with z
+ *   x, dt, z, y [rows,P], Bm, Cm [rows,N] x_dtype; A [P,N], D, dt_bias [P] fp32
+ *   s0, s1 [B,P,N] fp32: the states before the first and after the last token
+ * A is expected <= 0; larger ones are allowed as long as products of exp(d A) over a sequence stay
+ * finite.  dt of minus infinity is a step of zero: the token leaves the state as it is.
+ * P a multiple of 8; N 8, 16, 32 or 64; states and sums in fp32. */
+typedef struct {
+    int64_t B, T;
+    int64_t ldx, lddt, ldz, ldB, ldC, ldy;
+    int32_t P, N;
+    int32_t x_dtype, packed;
+} adj_ssm_dims;
+
+/* Workspace bytes of ADJ_OP_SSM_FWD or ADJ_OP_SSM_BWD (0 for sizes the calls reject). */
+size_t adj_ssm_workspace_bytes(const adj_ssm_dims *dims, int op);
+
+/* D, z, dt_bias, s0 NULL: zeros (z: no gate); s1 NULL: not written.  y may not alias an input. */
+adj_status adj_ssm_fwd(const adj_ssm_dims *dims, const void *x, const void *dt, const float *A, const void *Bm,
+                       const void *Cm, const float *D, const void *z, const float *dt_bias, const float *s0,
+                       const int64_t *offsets, void *y, float *s1, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients for the cotangents go [rows,P] of y (x_dtype, pitch ldy) and ds1 of s1 (NULL: zeros).
+ * dx, ddt, dz, dB, dC have the type and pitch of x, dt, z, Bm, Cm; dA, dD, ddt_bias, ds0 are fp32.
+ * dD, ddt_bias, ds0 NULL: not written; dz is needed where z is given, and NULL without.  No output
+ * may alias an input.  Sums in a fixed order. */
+adj_status adj_ssm_bwd(const adj_ssm_dims *dims, const void *x, const void *dt, const float *A, const void *Bm,
+                       const void *Cm, const float *D, const void *z, const float *dt_bias, const float *s0,
+                       const int64_t *offsets, const void *go, const float *ds1, void *dx, void *ddt, float *dA,
+                       void *dB, void *dC, float *dD, void *dz, float *ddt_bias, float *ds0, void *ws,
+                       size_t ws_bytes, void *stream);
+
+/* One token for each of B sequences (dims->T and packed are not read; ld* are the distances
+ * between sequences): state [n_slots,P,N] fp32 is updated in place.  No workspace. */
+adj_status adj_ssm_step(const adj_ssm_dims *dims, const void *x, const void *dt, const float *A, const void *Bm,
+                        const void *Cm, const float *D, const void *z, const float *dt_bias, float *state,
+                        int64_t n_slots, const int32_t *slots, void *y, void *stream);
+
+/* Sampling a token from logits, by given random numbers.  Per row x = logits[n, :V] with its largest
+ * value m, and the row's settings (fp32, top_k int32; a NULL array: the value in brackets):
+ *   weights   w_i = round(2^40 e^((x_i - m) / temperature)), whole numbers  [1]
+ *   kept      a prefix of the order by x descending, then i ascending: those with
+ *             w_i >= min_p 2^40 [0], of these the first top_k (<= 0: all) [0], of these the
+ *             shortest prefix that holds at least top_p of their weight, and one at least [1]
+ *   token     the first kept j, by index, with sum of the kept w_i, i <= j, > u[n] * their total
+ *   logp      log(w_j / total), from (x_j - m) / temperature itself
+ * u [N] fp32 in [0, 1) (others are taken as the nearest such number, NaN as 0).  Temperature 0 takes
+ * the largest logit, the lowest index first; top_p >= 1 and min_p <= 0 keep all, min_p > 1 and top_p <= 0
+ * the largest alone.  Minus infinity is a masked token.  Weights are off by a few units of 2^-40; as they
+ * are whole numbers the result does not depend on the order of sums, and equal rows give equal tokens.
+ * token [N] int64 and logp [N] fp32 (NULL: not written).  Without a finite value a row gives token -1 and
+ * logp -inf; with a NaN or +inf in it, or a setting that is NaN or a negative temperature, token -1 and
+ * logp NaN.  logits need only their type's alignment, ld >= V; N < 2^28, 1 <= V < 2^22.  One launch, no
+ * workspace. */
+typedef struct {
+    int64_t N, V, ld;
+    int32_t x_dtype;
+    int32_t reserved;            /* zero */
+} adj_sample_dims;
+adj_status adj_sample(const adj_sample_dims *dims, const void *logits, const float *u, const float *temperature,
+                      const int32_t *top_k, const float *top_p, const float *min_p, int64_t *token, float *logp,
+                      void *stream);
 
 /* Synchronise `stream`, return and clear the sticky device status of `ws`
  * (ADJ_OK or ADJ_ETIMEOUT); ADJ_ECUDA if the stream reports an error. */
