@@ -41,8 +41,8 @@ template <int N>
 struct Tile {
     static constexpr int NQ = N / 4, CQ = 32 / NQ, CW = 4 * CQ;
     static constexpr int TT = N == 8 ? 8 : 16;
-    static constexpr int VT = CW / 8;                               // vectors of eight channels a token
-    static constexpr int VPL = TT * VT >= 32 ? TT * VT / 32 : 1;    // of a tile, a lane
+    static constexpr int QPL = TT * CQ / 32;                        // a lane's quads of channels in a tile
+    static constexpr int MAPS = TT * N / 8, MPL = (MAPS + 31) / 32; // vectors of eight of B (or C); a lane's
     static constexpr int X = TT * CW;                               // floats of a tile of channels
     static constexpr int S = TT * N * 2;                            // floats of a tile of B or C, doubled
 };
@@ -157,106 +157,119 @@ struct Marks {
     __device__ __forceinline__ int64_t of(int i) const { return __shfl_sync(~0u, seq, i); }
 };
 
-// A lane's vectors of a tile: vector j is token (lane + 32 j) / VT, channels 8 ((lane + 32 j) % VT)
-template <class T, int N>
-struct Vecs {
-    typedef Tile<N> K;
-    int tok[K::VPL];
-    int c;                              // first channel (the same for every j)
-    int cl;                             // the same inside the warp's
-    bool in;
-    __device__ Vecs(const Lane<N> &l, int P) {
-        cl = l.lane % K::VT * 8;
-        c = l.c0 + cl;
-#pragma unroll
-        for (int j = 0; j < K::VPL; ++j) tok[j] = (l.lane + 32 * j) / K::VT;
-        in = c < P && tok[0] < K::TT;
+// Four channels as they are stored
+template <class T>
+struct Raw4;
+template <>
+struct Raw4<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float *p) { v = __ldg(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void zero() { v = f4(0.f); }
+    __device__ __forceinline__ float4 get() const { return v; }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldg(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
+    __device__ __forceinline__ float4 get() const {
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xFFFF0000u));
     }
+};
+
+// What a lane stages and finishes: quad j is token row + NQ j of the tile, always the same channels
+template <class T, int N>
+struct Mine {
+    typedef Tile<N> K;
+    int row, cl, c;                     // cl: channel inside the warp's, c: in the array
+    bool in;
+    float4 bias, D;
+    __device__ Mine(const SsmArgs &a, const Lane<N> &l) {
+        row = l.lane / K::CQ;
+        cl = l.lane % K::CQ * 4;
+        c = l.c0 + cl;
+        in = c < a.P;
+        bias = a.bias && in ? __ldg(reinterpret_cast<const float4 *>(a.bias + c)) : f4(0.f);
+        D = a.D && in ? __ldg(reinterpret_cast<const float4 *>(a.D + c)) : f4(0.f);
+    }
+    __device__ __forceinline__ int tok(int j) const { return row + K::NQ * j; }
     __device__ __forceinline__ bool ok(const Lane<N> &l, int64_t t, int j) const {
-        const int64_t x = t + tok[j];
+        const int64_t x = t + tok(j);
         return in && x >= l.lo && x < l.hi;
     }
-    __device__ __forceinline__ void load(Raw8<T> (&r)[K::VPL], const void *p, int64_t ld, const Lane<N> &l, int64_t t) const {
+    __device__ __forceinline__ void load(Raw4<T> (&r)[K::QPL], const void *p, int64_t ld, const Lane<N> &l, int64_t t) const {
 #pragma unroll
-        for (int j = 0; j < K::VPL; ++j) {
-            if (ok(l, t, j)) r[j].load(static_cast<const T *>(p) + (t + tok[j]) * ld + c);
+        for (int j = 0; j < K::QPL; ++j) {
+            if (ok(l, t, j)) r[j].load(static_cast<const T *>(p) + (t + tok(j)) * ld + c);
             else r[j].zero();
         }
     }
 };
 
-__device__ __forceinline__ void put8(float *p, const float (&x)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ float4 softplus4(float4 v) {
+    return make_float4(softplus_f(v.x), softplus_f(v.y), softplus_f(v.z), softplus_f(v.w));
 }
+__device__ __forceinline__ float4 sigmoid4(float4 v) {
+    return make_float4(sigmoid_f(v.x), sigmoid_f(v.y), sigmoid_f(v.z), sigmoid_f(v.w));
+}
+__device__ __forceinline__ void put4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ float4 get4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
 // steps and inputs of a tile: d and u = d x (zeros where there is no token)
 template <class T, int N>
-__device__ __forceinline__ void stage_steps(const SsmArgs &a, const Lane<N> &l, const Vecs<T, N> &v, int64_t t,
-                                            const Raw8<T> (&rx)[Tile<N>::VPL], const Raw8<T> (&rdt)[Tile<N>::VPL],
-                                            float *ds, float *us) {
+__device__ __forceinline__ void stage_steps(const Lane<N> &l, const Mine<T, N> &v, int64_t t, const Raw4<T> (&rx)[Tile<N>::QPL],
+                                            const Raw4<T> (&rdt)[Tile<N>::QPL], float *ds, float *us) {
     typedef Tile<N> K;
-    if (v.tok[0] >= K::TT) return;
 #pragma unroll
-    for (int j = 0; j < K::VPL; ++j) {
-        float x[8], d[8], b[8];
-        rx[j].get(x);
-        rdt[j].get(d);
-        if (a.bias && v.in) {
-            ld8(a.bias + v.c, b);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) b[e] = 0.f;
-        }
-        const bool ok = v.ok(l, t, j);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            d[e] = ok ? softplus_f(d[e] + b[e]) : 0.f;
-            x[e] *= d[e];
-        }
-        put8(ds + v.tok[j] * K::CW + v.cl, d);
-        put8(us + v.tok[j] * K::CW + v.cl, x);
+    for (int j = 0; j < K::QPL; ++j) {
+        const float4 d = v.ok(l, t, j) ? softplus4(rdt[j].get() + v.bias) : f4(0.f);
+        put4(ds + v.tok(j) * K::CW + v.cl, d);
+        put4(us + v.tok(j) * K::CW + v.cl, d * rx[j].get());
     }
 }
 
 // the cotangent g of v: go, times z sigmoid(z) with a gate
 template <class T, int N>
-__device__ __forceinline__ void stage_cotangent(const SsmArgs &a, const Lane<N> &l, const Vecs<T, N> &v, int64_t t, float *gs) {
+__device__ __forceinline__ void stage_cotangent(const SsmArgs &a, const Mine<T, N> &v, const Raw4<T> (&rg)[Tile<N>::QPL],
+                                                const Raw4<T> (&rz)[Tile<N>::QPL], float *gs) {
     typedef Tile<N> K;
-    if (v.tok[0] >= K::TT) return;
-    Raw8<T> rg[K::VPL], rz[K::VPL];
-    v.load(rg, a.go, a.ldy, l, t);
-    if (a.z) v.load(rz, a.z, a.ldz, l, t);
 #pragma unroll
-    for (int j = 0; j < K::VPL; ++j) {
-        float g[8], z[8];
-        rg[j].get(g);
+    for (int j = 0; j < K::QPL; ++j) {
+        float4 g = rg[j].get();
         if (a.z) {
-            rz[j].get(z);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] *= z[e] * sigmoid_f(z[e]);
+            const float4 z = rz[j].get();
+            g = g * (z * sigmoid4(z));
         }
-        put8(gs + v.tok[j] * K::CW + v.cl, g);
+        put4(gs + v.tok(j) * K::CW + v.cl, g);
     }
 }
 
-// B or C of a tile, each value twice
+// B or C of a tile: fetched, and staged with each value twice
 template <class T, int N>
-__device__ __forceinline__ void stage_maps(const void *p, int64_t ld, const Lane<N> &l, int64_t t, float *s) {
+struct Maps {
     typedef Tile<N> K;
+    Raw8<T> r[K::MPL];
+    __device__ __forceinline__ void load(const void *p, int64_t ld, const Lane<N> &l, int64_t t) {
 #pragma unroll
-    for (int i = l.lane; i < K::TT * N / 8; i += 32) {
-        const int tok = i / (N / 8), n = i % (N / 8) * 8;
-        Raw8<T> r;
-        if (t + tok >= l.lo && t + tok < l.hi) r.load(static_cast<const T *>(p) + (t + tok) * ld + n);
-        else r.zero();
-        float x[8];
-        r.get(x);
-#pragma unroll
-        for (int e = 0; e < 8; e += 2)
-            *reinterpret_cast<float4 *>(s + (tok * N + n + e) * 2) = make_float4(x[e], x[e], x[e + 1], x[e + 1]);
+        for (int j = 0; j < K::MPL; ++j) {
+            const int i = l.lane + 32 * j, tok = i / (N / 8), n = i % (N / 8) * 8;
+            if (tok < K::TT && t + tok >= l.lo && t + tok < l.hi) r[j].load(static_cast<const T *>(p) + (t + tok) * ld + n);
+            else r[j].zero();
+        }
     }
-}
+    __device__ __forceinline__ void stage(const Lane<N> &l, float *s) const {
+#pragma unroll
+        for (int j = 0; j < K::MPL; ++j) {
+            const int i = l.lane + 32 * j;
+            float x[8];
+            r[j].get(x);
+            if (i < K::MAPS)
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) put4(s + (i * 8 + e) * 2, make_float4(x[e], x[e], x[e + 1], x[e + 1]));
+        }
+    }
+};
 
 template <int N>
 __device__ __forceinline__ Quad decays(const SsmArgs &a, const Lane<N> &l) {
@@ -270,28 +283,48 @@ __device__ __forceinline__ Quad decays(const SsmArgs &a, const Lane<N> &l) {
     return A;
 }
 
+// The exponential unit's results lie low by 2e-8 on average where the exponent is near zero (measured over
+// 0 to -1; 0.3 to 0.8 units of the last place at worst either way).  States that last for a
+// thousand tokens would show it, so exponents are raised by that much in the multiply-add that forms them.
+constexpr float EXP_UP = 2.5e-8f;
+
+// what a thread reads of a token: its channels' steps and inputs, its states' B (or C)
+template <int N>
+struct Token {
+    pair_t d[2], u[2], B[4];
+    __device__ __forceinline__ void load(const float *ds, const float *us, const float *Bs, const Lane<N> &l, int i) {
+        const ulonglong2 x = lds2(ds + i * Tile<N>::CW + l.cq * 4), y = lds2(us + i * Tile<N>::CW + l.cq * 4);
+        d[0] = x.x; d[1] = x.y;
+        u[0] = y.x; u[1] = y.y;
+        maps(B, Bs, l, i);
+    }
+    __device__ __forceinline__ static void maps(pair_t (&b)[4], const float *s, const Lane<N> &l, int i) {
+        const ulonglong2 x = lds2(s + (i * N + l.nq * 4) * 2), y = lds2(s + (i * N + l.nq * 4) * 2 + 4);
+        b[0] = x.x; b[1] = x.y; b[2] = y.x; b[3] = y.y;
+    }
+};
+
 // h = exp(d A) h + u B for one token
-template <bool KEEP>
-__device__ __forceinline__ void advance(const Quad &A, Quad &h, Quad *keep, ulonglong2 d, ulonglong2 u, const float *B) {
-    const ulonglong2 b0 = lds2(B), b1 = lds2(B + 4);
-    const pair_t b[4] = {b0.x, b0.y, b1.x, b1.y}, dd[2] = {d.x, d.y}, uu[2] = {u.x, u.y};
+template <bool KEEP, int N>
+__device__ __forceinline__ void advance(const Quad &A, Quad &h, Quad *keep, const Token<N> &k) {
+    const pair_t up = pk(EXP_UP, EXP_UP);
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const pair_t e = exp2_2(mul2(dd[k], A.v[n][k]));
-            if (KEEP) keep->v[n][k] = e;
-            h.v[n][k] = fma2(e, h.v[n][k], mul2(uu[k], b[n]));
+        for (int c = 0; c < 2; ++c) {
+            const pair_t e = exp2_2(fma2(k.d[c], A.v[n][c], up));
+            if (KEEP) keep->v[n][c] = e;
+            h.v[n][c] = fma2(e, h.v[n][c], mul2(k.u[c], k.B[n]));
         }
 }
 
 // ---------------------------------------------------------------- segments from a state of zero
 template <class T, int N, bool BWD>
-__global__ __launch_bounds__(32 * WPB) void k_ssm_state(const SsmArgs a, int64_t cols) {
+__global__ __launch_bounds__(32 * WPB, 3) void k_ssm_state(const SsmArgs a, int64_t cols) {
     typedef Tile<N> K;
     extern __shared__ __align__(16) float sm[];
     const Lane<N> l(a, blockIdx.x, cols);
-    const Vecs<T, N> v(l, a.P);
+    const Mine<T, N> v(a, l);
     float *ds = sm + l.warp * ((BWD ? 3 : 2) * K::X + (BWD ? 2 : 1) * K::S), *us = ds + K::X, *Bs = us + K::X;
     float *Cs = Bs + K::S, *gs = Cs + K::S;                         // BWD
     const Quad A = decays<N>(a, l);
@@ -302,15 +335,17 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_state(const SsmArgs a, int64_t
     pair_t sum[2] = {pk(0.f, 0.f), pk(0.f, 0.f)};
     bool fresh = false;                                             // a sequence has begun in this segment
     Marks mk;
-    Raw8<T> rx[K::VPL], rdt[K::VPL];
+    Raw4<T> rx[K::QPL], rdt[K::QPL];
+    Maps<T, N> rB;
     v.load(rx, a.x, a.ldx, l, l.t0);
     v.load(rdt, a.dt, a.lddt, l, l.t0);
+    rB.load(a.Bm, a.ldB, l, l.t0);
     auto steps = [&](float *p) {                                    // [P] of the sums of steps
         if (l.nq != 0 || !l.in) return;
         float4 s;
         upk(sum[0], s.x, s.y);
         upk(sum[1], s.z, s.w);
-        *reinterpret_cast<float4 *>(p + l.c0 + l.cq * 4) = fresh ? make_float4(-1.f, -1.f, -1.f, -1.f) : s;
+        put4(p + l.c0 + l.cq * 4, fresh ? f4(-1.f) : s);
     };
     for (int64_t t = l.t0; t < l.t1; t += K::TT) {
         if (BWD) {
@@ -320,48 +355,64 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_state(const SsmArgs a, int64_t
         }
         mk.at<K::TT>(a.q, t, l.lo, l.hi, true);
         __syncwarp();
-        stage_steps<T, N>(a, l, v, t, rx, rdt, ds, us);
-        stage_maps<T, N>(a.Bm, a.ldB, l, t, Bs);
+        stage_steps<T, N>(l, v, t, rx, rdt, ds, us);
+        rB.stage(l, Bs);
         if (BWD) {
-            stage_maps<T, N>(a.Cm, a.ldC, l, t, Cs);
-            stage_cotangent<T, N>(a, l, v, t, gs);
+            Raw4<T> rg[K::QPL], rz[K::QPL];
+            Maps<T, N> rC;
+            v.load(rg, a.go, a.ldy, l, t);
+            if (a.z) v.load(rz, a.z, a.ldz, l, t);
+            rC.load(a.Cm, a.ldC, l, t);
+            stage_cotangent<T, N>(a, v, rg, rz, gs);
+            rC.stage(l, Cs);
         }
         __syncwarp();
         v.load(rx, a.x, a.ldx, l, t + K::TT);
         v.load(rdt, a.dt, a.lddt, l, t + K::TT);
-#pragma unroll 2
-        for (int i = 0; i < K::TT; ++i) {
-            const ulonglong2 d = lds2(ds + i * K::CW + l.cq * 4), u = lds2(us + i * K::CW + l.cq * 4);
-            if (mk.first >> i & 1u) {
-                const int64_t b = mk.of(i);
-                if (a.s0) h.load<N>(l.of(a, a.s0, b), l.in);
-                else h.fill(0.f);
-                fresh = true;
-            }
-            sum[0] = add2(sum[0], d.x);
-            sum[1] = add2(sum[1], d.y);
-            Quad e;
-            advance<BWD>(A, h, &e, d, u, Bs + (i * N + l.nq * 4) * 2);
-            if (BWD && !fresh) {
-                const ulonglong2 g = lds2(gs + i * K::CW + l.cq * 4);
-                const ulonglong2 c0 = lds2(Cs + (i * N + l.nq * 4) * 2), c1 = lds2(Cs + (i * N + l.nq * 4) * 2 + 4);
-                const pair_t c[4] = {c0.x, c0.y, c1.x, c1.y}, gg[2] = {g.x, g.y};
+        rB.load(a.Bm, a.ldB, l, t + K::TT);
+        auto walk = [&](auto events, int i0) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        P.v[n][k] = mul2(P.v[n][k], e.v[n][k]);
-                        m.v[n][k] = fma2(P.v[n][k], mul2(gg[k], c[n]), m.v[n][k]);
-                    }
-                if (a.ds1 && (mk.last >> i & 1u)) {
-                    Quad s;
-                    s.load<N>(l.of(a, a.ds1, mk.of(i)), l.in);
+            for (int j = 0; j < G; ++j) {
+                const int i = i0 + j;
+                Token<N> k;
+                k.load(ds, us, Bs, l, i);
+                if (events && (mk.first >> i & 1u)) {
+                    const int64_t b = mk.of(i);
+                    if (a.s0) h.load<N>(l.of(a, a.s0, b), l.in);
+                    else h.fill(0.f);
+                    fresh = true;
+                }
+                sum[0] = add2(sum[0], k.d[0]);
+                sum[1] = add2(sum[1], k.d[1]);
+                Quad e;
+                advance<BWD>(A, h, &e, k);
+                if (BWD && !(events && fresh)) {
+                    const ulonglong2 g = lds2(gs + i * K::CW + l.cq * 4);
+                    const pair_t gg[2] = {g.x, g.y};
+                    pair_t C[4];
+                    Token<N>::maps(C, Cs, l, i);
 #pragma unroll
                     for (int n = 0; n < 4; ++n)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) m.v[n][k] = fma2(P.v[n][k], s.v[n][k], m.v[n][k]);
+                        for (int c = 0; c < 2; ++c) {
+                            P.v[n][c] = mul2(P.v[n][c], e.v[n][c]);
+                            m.v[n][c] = fma2(P.v[n][c], mul2(gg[c], C[n]), m.v[n][c]);
+                        }
+                    if (events && a.ds1 && (mk.last >> i & 1u)) {
+                        Quad s;
+                        s.load<N>(l.of(a, a.ds1, mk.of(i)), l.in);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) m.v[n][c] = fma2(P.v[n][c], s.v[n][c], m.v[n][c]);
+                    }
                 }
             }
+        };
+#pragma unroll 1
+        for (int i = 0; i < K::TT; i += G) {
+            if (((mk.first | mk.last) >> i & ((1u << G) - 1)) || (BWD && fresh)) walk(std::true_type(), i);
+            else walk(std::false_type(), i);
         }
     }
     h.store<N>(l.of(a, a.seg, l.seg), l.in);
@@ -414,7 +465,7 @@ __device__ void pass_through(const SsmArgs &a, float *out, const float *in, int6
 
 // ---------------------------------------------------------------- outputs
 template <class T, int N>
-__global__ __launch_bounds__(32 * WPB) void k_ssm_out(const SsmArgs a, int64_t cols) {
+__global__ __launch_bounds__(32 * WPB, 3) void k_ssm_out(const SsmArgs a, int64_t cols) {
     typedef Tile<N> K;
     extern __shared__ __align__(16) float sm[];
     const int64_t work = a.nseg * cols;
@@ -423,7 +474,7 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_out(const SsmArgs a, int64_t c
         return;
     }
     const Lane<N> l(a, blockIdx.x, cols);
-    const Vecs<T, N> v(l, a.P);
+    const Mine<T, N> v(a, l);
     float *ds = sm + l.warp * (2 * K::X + 2 * K::S + K::TT * 128), *us = ds + K::X, *Bs = us + K::X, *Cs = Bs + K::S;
     float *ys = Cs + K::S;                                          // [TT][NQ][CW]: sums over a quad of states
     const Quad A = decays<N>(a, l);
@@ -431,71 +482,78 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_out(const SsmArgs a, int64_t c
     h.fill(0.f);
     if (a.nseg > 1) h.load<N>(l.of(a, a.seg, l.seg), l.in);
     Marks mk;
-    Raw8<T> rx[K::VPL], rdt[K::VPL], rz[K::VPL], cx[K::VPL];
-    v.load(rx, a.x, a.ldx, l, l.t0);
-    v.load(rdt, a.dt, a.lddt, l, l.t0);
+    Raw4<T> rx[K::QPL], rdt[K::QPL], rz[K::QPL], cx[K::QPL];
+    Maps<T, N> rB, rC;
+    auto fetch = [&](int64_t t) {
+        v.load(rx, a.x, a.ldx, l, t);
+        v.load(rdt, a.dt, a.lddt, l, t);
+        rB.load(a.Bm, a.ldB, l, t);
+        rC.load(a.Cm, a.ldC, l, t);
+    };
+    fetch(l.t0);
     for (int64_t t = l.t0; t < l.t1; t += K::TT) {
         mk.at<K::TT>(a.q, t, l.lo, l.hi, true);
         __syncwarp();
-        stage_steps<T, N>(a, l, v, t, rx, rdt, ds, us);
-        stage_maps<T, N>(a.Bm, a.ldB, l, t, Bs);
-        stage_maps<T, N>(a.Cm, a.ldC, l, t, Cs);
+        stage_steps<T, N>(l, v, t, rx, rdt, ds, us);
+        rB.stage(l, Bs);
+        rC.stage(l, Cs);
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < K::VPL; ++j) cx[j] = rx[j];
+        for (int j = 0; j < K::QPL; ++j) cx[j] = rx[j];
         if (a.z) v.load(rz, a.z, a.ldz, l, t);
-        v.load(rx, a.x, a.ldx, l, t + K::TT);
-        v.load(rdt, a.dt, a.lddt, l, t + K::TT);
-#pragma unroll 2
-        for (int i = 0; i < K::TT; ++i) {
-            const ulonglong2 d = lds2(ds + i * K::CW + l.cq * 4), u = lds2(us + i * K::CW + l.cq * 4);
-            if (mk.first >> i & 1u) {
-                const int64_t b = mk.of(i);
-                if (a.s0) h.load<N>(l.of(a, a.s0, b), l.in);
-                else h.fill(0.f);
-            }
-            advance<false>(A, h, nullptr, d, u, Bs + (i * N + l.nq * 4) * 2);
-            const ulonglong2 c0 = lds2(Cs + (i * N + l.nq * 4) * 2), c1 = lds2(Cs + (i * N + l.nq * 4) * 2 + 4);
-            const pair_t c[4] = {c0.x, c0.y, c1.x, c1.y};
-            ulonglong2 y;
-            y.x = mul2(c[0], h.v[0][0]);
-            y.y = mul2(c[0], h.v[0][1]);
+        fetch(t + K::TT);
+        // the sums of a group stay in registers until its end: a store to shared memory would hold up
+        // the next token's loads
+        auto walk = [&](auto events, int i0) {
+            ulonglong2 y[G];
 #pragma unroll
-            for (int n = 1; n < 4; ++n) {
-                y.x = fma2(c[n], h.v[n][0], y.x);
-                y.y = fma2(c[n], h.v[n][1], y.y);
+            for (int j = 0; j < G; ++j) {
+                const int i = i0 + j;
+                Token<N> k;
+                pair_t C[4];
+                k.load(ds, us, Bs, l, i);
+                Token<N>::maps(C, Cs, l, i);
+                if (events && (mk.first >> i & 1u)) {
+                    const int64_t b = mk.of(i);
+                    if (a.s0) h.load<N>(l.of(a, a.s0, b), l.in);
+                    else h.fill(0.f);
+                }
+                advance<false>(A, h, nullptr, k);
+                y[j].x = mul2(C[0], h.v[0][0]);
+                y[j].y = mul2(C[0], h.v[0][1]);
+#pragma unroll
+                for (int n = 1; n < 4; ++n) {
+                    y[j].x = fma2(C[n], h.v[n][0], y[j].x);
+                    y[j].y = fma2(C[n], h.v[n][1], y[j].y);
+                }
+                if (events && a.s1 && (mk.last >> i & 1u)) {
+                    const int64_t b = mk.of(i);
+                    h.store<N>(l.of(a, a.s1, b), l.in);
+                }
             }
-            *reinterpret_cast<ulonglong2 *>(ys + (i * K::NQ + l.nq) * K::CW + l.cq * 4) = y;
-            if (a.s1 && (mk.last >> i & 1u)) {
-                const int64_t b = mk.of(i);
-                h.store<N>(l.of(a, a.s1, b), l.in);
-            }
+#pragma unroll
+            for (int j = 0; j < G; ++j)
+                *reinterpret_cast<ulonglong2 *>(ys + ((i0 + j) * K::NQ + l.nq) * K::CW + l.cq * 4) = y[j];
+        };
+#pragma unroll 1
+        for (int i = 0; i < K::TT; i += G) {
+            if ((mk.first | mk.last) >> i & ((1u << G) - 1)) walk(std::true_type(), i);
+            else walk(std::false_type(), i);
         }
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < K::VPL; ++j) {
+        for (int j = 0; j < K::QPL; ++j) {
             if (!v.ok(l, t, j)) continue;
-            const float *p = ys + v.tok[j] * K::NQ * K::CW + v.cl;
-            float y[8], x[8], z[8];
+            const float *p = ys + v.tok(j) * 128 + v.cl;
+            float4 y = get4(p);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = p[e];
-#pragma unroll
-            for (int q = 1; q < K::NQ; ++q)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] += p[q * K::CW + e];
-            if (a.D) {
-                float D[8];
-                ld8(a.D + v.c, D);
-                cx[j].get(x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = fmaf(D[e], x[e], y[e]);
-            }
+            for (int q = 1; q < K::NQ; ++q) y = y + get4(p + q * K::CW);
+            y = fma4(v.D, cx[j].get(), y);
             if (a.z) {
-                rz[j].get(z);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] *= z[e] * sigmoid_f(z[e]);
+                const float4 z = rz[j].get();
+                y = y * (z * sigmoid4(z));
             }
-            Raw8<T>::of(y).store(static_cast<T *>(a.y) + (t + v.tok[j]) * a.ldy + v.c);
+            st4(static_cast<T *>(a.y) + (t + v.tok(j)) * a.ldy + v.c, y);
         }
     }
 }
@@ -521,16 +579,14 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_grad(const SsmArgs a, int64_t 
         return;
     }
     const Lane<N> l(a, blockIdx.x, cols);
-    const Vecs<T, N> v(l, a.P);
+    const Mine<T, N> v(a, l);
     float *ds = sm + l.warp * M::ALL, *us = ds + K::X, *gs = us + K::X, *Bs = gs + K::X, *Cs = Bs + K::S;
     float *ck = Cs + K::S, *bc = ck + M::CK, *ch = bc + M::BC, *ws = ch + M::CH;
     const Quad A = decays<N>(a, l);
     Quad e, dA;                                                     // e: what reaches the state before
     e.load<N>(l.of(a, a.adj, l.seg), l.in);
     dA.fill(0.f);
-    float dD[8], db[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dD[i] = db[i] = 0.f;
+    float4 dD = f4(0.f), db = f4(0.f);
     Marks mk;
     const int tiles = int((l.t1 - l.t0 + K::TT - 1) / K::TT);
     for (int ti = tiles - 1; ti >= 0; --ti) {
@@ -553,14 +609,19 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_grad(const SsmArgs a, int64_t 
             }
         }
         {
-            Raw8<T> rx[K::VPL], rdt[K::VPL];
+            Raw4<T> rx[K::QPL], rdt[K::QPL], rg[K::QPL], rz[K::QPL];
+            Maps<T, N> rB, rC;
             v.load(rx, a.x, a.ldx, l, t);
             v.load(rdt, a.dt, a.lddt, l, t);
+            v.load(rg, a.go, a.ldy, l, t);
+            if (a.z) v.load(rz, a.z, a.ldz, l, t);
+            rB.load(a.Bm, a.ldB, l, t);
+            rC.load(a.Cm, a.ldC, l, t);
             __syncwarp();
-            stage_steps<T, N>(a, l, v, t, rx, rdt, ds, us);
-            stage_cotangent<T, N>(a, l, v, t, gs);
-            stage_maps<T, N>(a.Bm, a.ldB, l, t, Bs);
-            stage_maps<T, N>(a.Cm, a.ldC, l, t, Cs);
+            stage_steps<T, N>(l, v, t, rx, rdt, ds, us);
+            stage_cotangent<T, N>(a, v, rg, rz, gs);
+            rB.stage(l, Bs);
+            rC.stage(l, Cs);
             __syncwarp();
         }
         auto begin = [&](int i, Quad &x) {                          // the state before a sequence's first token
@@ -579,8 +640,9 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_grad(const SsmArgs a, int64_t 
             for (int j = 0; j < G; ++j) {
                 const int i = (g - 1) * G + j;
                 if (mk.first >> i & 1u) begin(i, h);
-                advance<false>(A, h, nullptr, lds2(ds + i * K::CW + l.cq * 4), lds2(us + i * K::CW + l.cq * 4),
-                               Bs + (i * N + l.nq * 4) * 2);
+                Token<N> k;
+                k.load(ds, us, Bs, l, i);
+                advance<false>(A, h, nullptr, k);
             }
             keep(g, h);
         }
@@ -597,8 +659,9 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_grad(const SsmArgs a, int64_t 
                 const int i = g * G + j;
                 if (mk.first >> i & 1u) begin(i, h);
                 hp[j] = h;
-                advance<true>(A, h, &ea[j], lds2(ds + i * K::CW + l.cq * 4), lds2(us + i * K::CW + l.cq * 4),
-                              Bs + (i * N + l.nq * 4) * 2);
+                Token<N> k;
+                k.load(ds, us, Bs, l, i);
+                advance<true>(A, h, &ea[j], k);
             }
 #pragma unroll
             for (int j = G - 1; j >= 0; --j) {
@@ -673,45 +736,29 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_grad(const SsmArgs a, int64_t 
         }
         // the tile's gradients of what each channel reads
         {
-            Raw8<T> rx[K::VPL], rdt[K::VPL], rz[K::VPL], rg[K::VPL];
+            Raw4<T> rx[K::QPL], rdt[K::QPL], rz[K::QPL], rg[K::QPL];
             v.load(rx, a.x, a.ldx, l, t);
             v.load(rdt, a.dt, a.lddt, l, t);
             v.load(rg, a.go, a.ldy, l, t);
             if (a.z) v.load(rz, a.z, a.ldz, l, t);
 #pragma unroll
-            for (int j = 0; j < K::VPL; ++j) {
+            for (int j = 0; j < K::QPL; ++j) {
                 if (!v.ok(l, t, j)) continue;
-                float x[8], dt[8], g[8], z[8], D[8], b[8], dx[8];
-                rx[j].get(x);
-                rdt[j].get(dt);
-                rg[j].get(g);
-                const int64_t at = t + v.tok[j];
-                const float *mb = ds + v.tok[j] * K::CW + v.cl, *sa = us + v.tok[j] * K::CW + v.cl, *vv = gs + v.tok[j] * K::CW + v.cl;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) D[i] = b[i] = 0.f;
-                if (a.D) ld8(a.D + v.c, D);
-                if (a.bias) ld8(a.bias + v.c, b);
+                const int64_t at = t + v.tok(j);
+                const int sh = v.tok(j) * K::CW + v.cl;
+                const float4 x = rx[j].get(), raw = rdt[j].get() + v.bias, mb = get4(ds + sh);
+                float4 g = rg[j].get();
                 if (a.z) {
-                    float dz[8];
-                    rz[j].get(z);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float s = sigmoid_f(z[i]), val = fmaf(D[i], x[i], vv[i]);
-                        dz[i] = g[i] * val * s * fmaf(z[i], 1.f - s, 1.f);
-                        g[i] *= z[i] * s;
-                    }
-                    Raw8<T>::of(dz).store(static_cast<T *>(a.dz) + at * a.ldz + v.c);
+                    // v z s: its derivative for z is v s (1 + z (1 - s))
+                    const float4 z = rz[j].get(), s = sigmoid4(z), val = fma4(v.D, x, get4(gs + sh));
+                    st4(static_cast<T *>(a.dz) + at * a.ldz + v.c, g * val * s * fma4(z, f4(1.f) - s, f4(1.f)));
+                    g = g * (z * s);
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float raw = dt[i] + b[i];
-                    dx[i] = fmaf(softplus_f(raw), mb[i], D[i] * g[i]);
-                    dt[i] = fmaf(x[i], mb[i], SEQ_LN2 * sa[i]) * sigmoid_f(raw);
-                    dD[i] = fmaf(g[i], x[i], dD[i]);
-                    db[i] += dt[i];
-                }
-                Raw8<T>::of(dx).store(static_cast<T *>(a.dx) + at * a.ldx + v.c);
-                Raw8<T>::of(dt).store(static_cast<T *>(a.ddt) + at * a.lddt + v.c);
+                const float4 ddt = fma4(x, mb, f4(SEQ_LN2) * get4(us + sh)) * sigmoid4(raw);
+                st4(static_cast<T *>(a.dx) + at * a.ldx + v.c, fma4(softplus4(raw), mb, v.D * g));
+                st4(static_cast<T *>(a.ddt) + at * a.lddt + v.c, ddt);
+                dD = fma4(g, x, dD);
+                db = db + ddt;
             }
         }
         // dB and dC over the block's warps
@@ -729,16 +776,17 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_grad(const SsmArgs a, int64_t 
     float *par = a.par + l.seg * a.P * (N + 2);
     dA.store<N>(par + l.state(a), l.in);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int w = K::VT; w < 32; w <<= 1) {
-            dD[i] += __shfl_xor_sync(~0u, dD[i], w);
-            db[i] += __shfl_xor_sync(~0u, db[i], w);
-        }
+    for (int w = K::CQ; w < 32; w <<= 1) {
+        auto join = [&](float4 &x) {
+            x = x + make_float4(__shfl_xor_sync(~0u, x.x, w), __shfl_xor_sync(~0u, x.y, w), __shfl_xor_sync(~0u, x.z, w),
+                                __shfl_xor_sync(~0u, x.w, w));
+        };
+        join(dD);
+        join(db);
     }
-    if (l.lane < K::VT && v.c < a.P) {
-        put8(par + int64_t(a.P) * N + v.c, dD);
-        put8(par + int64_t(a.P) * (N + 1) + v.c, db);
+    if (l.lane < K::CQ && v.in) {
+        put4(par + int64_t(a.P) * N + v.c, dD);
+        put4(par + int64_t(a.P) * (N + 1) + v.c, db);
     }
 }
 
