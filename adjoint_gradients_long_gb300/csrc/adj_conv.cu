@@ -1,12 +1,13 @@
 // adj_conv.cu -- the short causal convolution of a selective layer: prompts, gradients and single
 // tokens.  include/adj.h defines it.
 //
-// A thread walks a run of consecutive tokens for eight channels (16 bytes of bf16), with the last W-1
-// inputs, the weights and the sums of a token in registers, so each value is read once (and W-1 of
-// them again by the run after it, mostly from L2) and written once.  Bound by HBM: the arithmetic is
-// W multiply-adds and one sigmoid a value.  A block holds VG vectors of channels side by side and
-// 256 / VG runs, VG the power of two that covers the channels, 32 at most: neighbouring threads
-// read neighbouring vectors.
+// A thread walks a run of consecutive tokens for four channels, with the last W-1 inputs, the weights and
+// the sums of a token in registers, so each value is read once (and W-1 of them again by the run
+// after it, mostly from L2) and written once.  Bound by HBM: the arithmetic is W multiply-adds and
+// one sigmoid a value.  Four channels, not eight: eight took 162 registers forwards and 255 backwards,
+// too few warps to cover HBM's latency.  A block holds VG quads of channels side by side and
+// 256 / VG runs, VG the power of two that covers the channels, 64 at most: neighbouring threads
+// read neighbouring quads.
 //
 // Gradient: with dp_t = go_t act'(p_t),
 //     dc_i = sum_j w_j dp_{i-j},    dw_j = sum_t dp_t c_{t+j},
@@ -19,28 +20,33 @@ namespace adj {
 namespace {
 
 constexpr int CT = 256;         // threads of a block
-constexpr int CU = 4;           // tokens in flight a thread
+// tokens that a thread fetches together (and as many are on their way behind them)
+template <class T>
+constexpr int FETCH = sizeof(T) == 2 ? 4 : 2;
 
 template <class T>
 __device__ __forceinline__ const T *row(const void *p, int64_t i, int64_t ld, int c) {
     return static_cast<const T *>(p) + i * ld + c;
 }
 
-// weights [W][8] and bias of eight channels; w is [P][W]
+// Weights and bias of four channels; w is [P][W], so theirs are W vectors in a row
 template <int W>
-__device__ __forceinline__ void load_taps(const ConvArgs &a, int c, float (&w)[W][8], float (&bias)[8]) {
+__device__ __forceinline__ void load_taps(const ConvArgs &a, int c, float4 (&w)[W], float4 &bias) {
+    union {
+        float4 v[W];
+        float f[4 * W];
+    } u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int j = 0; j < W; ++j) u.v[j] = __ldg(reinterpret_cast<const float4 *>(a.w + int64_t(c) * W) + j);
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][e] = __ldg(a.w + int64_t(c + e) * W + j);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) bias[e] = a.bias ? __ldg(a.bias + c + e) : 0.f;
+    for (int j = 0; j < W; ++j) w[j] = make_float4(u.f[j], u.f[W + j], u.f[2 * W + j], u.f[3 * W + j]);
+    bias = a.bias ? __ldg(reinterpret_cast<const float4 *>(a.bias + c)) : f4(0.f);
 }
 
 // Entry i of sequence b's list (its state, then its tokens from `begin` on)
 template <class T, int W>
-__device__ __forceinline__ Raw8<T> entry(const ConvArgs &a, int64_t b, int64_t begin, int64_t i, int c) {
-    Raw8<T> r;
+__device__ __forceinline__ Raw4<T> entry(const ConvArgs &a, int64_t b, int64_t begin, int64_t i, int c) {
+    Raw4<T> r;
     if (i >= W - 1) r.load(row<T>(a.x, begin + i - (W - 1), a.ldx, c));
     else if (a.s0) r.load(row<T>(a.s0, b * (W - 1) + i, a.P, c));
     else r.zero();
@@ -48,20 +54,20 @@ __device__ __forceinline__ Raw8<T> entry(const ConvArgs &a, int64_t b, int64_t b
 }
 
 struct Place {
-    int c;                      // first of the thread's eight channels
+    int c;                      // first of the thread's four channels
     int run;                    // of the block's runs
     bool in;
     __device__ Place(int vg, int P) {
         const int v = int(blockIdx.y) * vg + int(threadIdx.x) % vg;
         run = int(threadIdx.x) / vg;
-        c = v * 8;
+        c = v * 4;
         in = c < P;
     }
 };
 
 // Blocks below `runs` take tokens, those above write the states after the last tokens.
 template <class T, int W>
-__global__ __launch_bounds__(CT) void k_conv_fwd(const ConvArgs a, int vg, int tr, int64_t runs) {
+__global__ __launch_bounds__(CT, 3) void k_conv_fwd(const ConvArgs a, int vg, int tr, int64_t runs) {
     const Place at(vg, a.P);
     if (!at.in) return;
     const int c = at.c, rg = CT / vg;
@@ -76,7 +82,7 @@ __global__ __launch_bounds__(CT) void k_conv_fwd(const ConvArgs a, int vg, int t
     int64_t t = (int64_t(blockIdx.x) * rg + at.run) * tr;
     const int64_t stop = min(t + tr, a.q.rows);
     if (t >= stop) return;
-    float w[W][8], bias[8], x[W][8];
+    float4 w[W], bias, x[W];
     load_taps<W>(a, c, w, bias);
     if (a.q.off) t = max(t, a.q.at(0));
     while (t < stop) {
@@ -85,36 +91,35 @@ __global__ __launch_bounds__(CT) void k_conv_fwd(const ConvArgs a, int vg, int t
         const int64_t begin = a.q.begin(b), end = min(a.q.end(b), stop);
         // x[1..W-1]: the W-1 entries before token t
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) entry<T, W>(a, b, begin, t - begin + j, c).get(x[j + 1]);
-        Raw8<T> next[CU];
+        for (int j = 0; j < W - 1; ++j) x[j + 1] = entry<T, W>(a, b, begin, t - begin + j, c).get();
+        // pointers and counts inside the run: 64-bit comparisons a token cost more than its arithmetic
+        const T *px = row<T>(a.x, t, a.ldx, c);
+        T *py = static_cast<T *>(a.y) + t * a.ldy + c;
+        const int n = int(end - t);
+        constexpr int FU = FETCH<T>;
+        Raw4<T> next[FU];
 #pragma unroll
-        for (int u = 0; u < CU; ++u)
-            if (t + u < end) next[u].load(row<T>(a.x, t + u, a.ldx, c));
-        for (; t < end; t += CU) {
-            Raw8<T> now[CU];
+        for (int u = 0; u < FU; ++u)
+            if (u < n) next[u].load(px + u * a.ldx);
+        for (int i = 0; i < n; i += FU) {
+            Raw4<T> now[FU];
 #pragma unroll
-            for (int u = 0; u < CU; ++u) now[u] = next[u];
+            for (int u = 0; u < FU; ++u) now[u] = next[u];
+            px += FU * a.ldx;
 #pragma unroll
-            for (int u = 0; u < CU; ++u)
-                if (t + CU + u < end) next[u].load(row<T>(a.x, t + CU + u, a.ldx, c));
+            for (int u = 0; u < FU; ++u)
+                if (i + FU + u < n) next[u].load(px + u * a.ldx);
 #pragma unroll
-            for (int u = 0; u < CU; ++u) {
-                if (t + u >= end) break;
-                float y[8];
+            for (int u = 0; u < FU; ++u) {
+                if (i + u >= n) break;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int j = 0; j < W - 1; ++j) x[j] = x[j + 1];
+                x[W - 1] = now[u].get();
+                float4 p = bias;
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) x[j][e] = x[j + 1][e];
-                }
-                now[u].get(x[W - 1]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float p = bias[e];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) p = fmaf(w[j][e], x[j][e], p);
-                    y[e] = a.act ? p * sigmoid_f(p) : p;
-                }
-                Raw8<T>::of(y).store(static_cast<T *>(a.y) + (t + u) * a.ldy + c);
+                for (int j = 0; j < W; ++j) p = fma4(w[j], x[j], p);
+                st4(py, a.act ? p * sigmoid4(p) : p);
+                py += a.ldy;
             }
         }
         t = end;
@@ -123,43 +128,33 @@ __global__ __launch_bounds__(CT) void k_conv_fwd(const ConvArgs a, int vg, int t
 
 // Blocks below `runs` take tokens, those above write ds0.
 template <class T, int W>
-__global__ __launch_bounds__(CT) void k_conv_bwd(const ConvArgs a, int vg, int tr, int64_t runs) {
-    __shared__ float sum[CT * 8];
+__global__ __launch_bounds__(CT, 2) void k_conv_bwd(const ConvArgs a, int vg, int tr, int64_t runs) {
+    __shared__ float4 sum[CT];
     const Place at(vg, a.P);
     const int c = at.c, rg = CT / vg;
-    float w[W][8], bias[8], x[W][8], dp[W][8], dw[W][8], db[8];
+    float4 w[W], bias, x[W], dp[W], dw[W], db = f4(0.f);
     if (at.in) load_taps<W>(a, c, w, bias);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        db[e] = 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][e] = dp[j][e] = 0.f;
-    }
+    for (int j = 0; j < W; ++j) dw[j] = dp[j] = f4(0.f);
     // one token: its entry joins x[W-1], the cotangent of its sum dp[W-1]
-    auto token = [&](const Raw8<T> &in, const Raw8<T> &cot) {
-        float g[8];
-        in.get(x[W - 1]);
-        cot.get(g);
+    auto token = [&](const Raw4<T> &in, const Raw4<T> &cot) {
+        x[W - 1] = in.get();
+        float4 g = cot.get();
+        if (a.act) {
+            float4 p = bias;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (a.act) {
-                float p = bias[e];
-#pragma unroll
-                for (int j = 0; j < W; ++j) p = fmaf(w[j][e], x[j][e], p);
-                const float s = sigmoid_f(p);
-                g[e] *= s * fmaf(p, 1.f - s, 1.f);
-            }
-            dp[W - 1][e] = g[e];
+            for (int j = 0; j < W; ++j) p = fma4(w[j], x[j], p);
+            const float4 s = sigmoid4(p);
+            g = g * s * fma4(p, f4(1.f) - s, f4(1.f));
         }
+        dp[W - 1] = g;
     };
     auto shift = [&]() {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) {
-                x[j][e] = x[j + 1][e];
-                dp[j][e] = dp[j + 1][e];
-            }
+        for (int j = 0; j < W - 1; ++j) {
+            x[j] = x[j + 1];
+            dp[j] = dp[j + 1];
+        }
     };
     if (int64_t(blockIdx.x) >= runs) {
         // dc of the entries of the state: from the first W-1 tokens, and from ds1 where a sequence is shorter
@@ -167,30 +162,28 @@ __global__ __launch_bounds__(CT) void k_conv_bwd(const ConvArgs a, int vg, int t
         if (!at.in || b >= a.q.B) return;
         const int64_t begin = a.q.begin(b), n = max(int64_t(0), a.q.end(b) - begin);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) entry<T, W>(a, b, begin, j, c).get(x[j + 1]);
-        float ds[W - 1][8];
+        for (int j = 0; j < W - 1; ++j) x[j + 1] = entry<T, W>(a, b, begin, j, c).get();
+        float4 ds[W - 1];
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
-            Raw8<T> r;
+            Raw4<T> r;
             r.zero();
             if (a.ds1 && i >= n) r.load(row<T>(a.ds1, b * (W - 1) + (i - n), a.P, c));
-            r.get(ds[i]);
+            ds[i] = r.get();
         }
 #pragma unroll
         for (int t = 0; t < W - 1; ++t) {
             if (t >= n) break;
             shift();
-            Raw8<T> in, cot;
+            Raw4<T> in, cot;
             in.load(row<T>(a.x, begin + t, a.ldx, c));
             cot.load(row<T>(a.go, begin + t, a.ldy, c));
             token(in, cot);
 #pragma unroll
-            for (int j = 0; j < W - 1 - t; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ds[t + j][e] = fmaf(w[j][e], dp[W - 1][e], ds[t + j][e]);
+            for (int j = 0; j < W - 1 - t; ++j) ds[t + j] = fma4(w[j], dp[W - 1], ds[t + j]);
         }
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) Raw8<T>::of(ds[i]).store(static_cast<T *>(a.ds0) + (b * (W - 1) + i) * a.P + c);
+        for (int i = 0; i < W - 1; ++i) st4(static_cast<T *>(a.ds0) + (b * (W - 1) + i) * a.P + c, ds[i]);
         return;
     }
     int64_t t = (int64_t(blockIdx.x) * rg + at.run) * tr;
@@ -199,86 +192,77 @@ __global__ __launch_bounds__(CT) void k_conv_bwd(const ConvArgs a, int vg, int t
     while (t < stop) {
         const int64_t b = a.q.find(t);
         if (b < 0) break;
-        const int64_t begin = a.q.begin(b), end = a.q.end(b), from = t, last = min(end, stop), until = last + W - 1;
+        const int64_t begin = a.q.begin(b), end = a.q.end(b), last = min(end, stop), until = last + W - 1;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
-            entry<T, W>(a, b, begin, t - begin + j, c).get(x[j + 1]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dp[j + 1][e] = 0.f;
+            x[j + 1] = entry<T, W>(a, b, begin, t - begin + j, c).get();
+            dp[j + 1] = f4(0.f);
         }
-        Raw8<T> nx[CU], ng[CU];
-        auto fetch = [&](int64_t t0) {
+        const T *px = row<T>(a.x, t, a.ldx, c), *pg = row<T>(a.go, t, a.ldy, c);
+        T *pd = static_cast<T *>(a.dx) + t * a.ldx + c;
+        // counted from the first token here: tokens that exist, that this run sums up and emits, that it walks
+        const int left = int(min(end - t, int64_t(tr + W))), own = int(last - t), all = int(until - t);
+        const int64_t tail = end - (W - 1) - t;                     // the first token that s1 holds
+        constexpr int CU = FETCH<T> / 2;
+        Raw4<T> nx[CU], ng[CU];
+        auto fetch = [&](int i) {
 #pragma unroll
             for (int u = 0; u < CU; ++u)
-                if (t0 + u < min(end, until)) {
-                    nx[u].load(row<T>(a.x, t0 + u, a.ldx, c));
-                    ng[u].load(row<T>(a.go, t0 + u, a.ldy, c));
+                if (i + u < left && i + u < all) {
+                    nx[u].load(px + u * a.ldx);
+                    ng[u].load(pg + u * a.ldy);
                 }
+            px += CU * a.ldx;
+            pg += CU * a.ldy;
         };
-        fetch(t);
-        for (; t < until; t += CU) {
-            Raw8<T> px[CU], pg[CU];
+        fetch(0);
+        for (int i = 0; i < all; i += CU) {
+            Raw4<T> cx[CU], cg[CU];
 #pragma unroll
             for (int u = 0; u < CU; ++u) {
-                px[u] = nx[u];
-                pg[u] = ng[u];
+                cx[u] = nx[u];
+                cg[u] = ng[u];
             }
-            fetch(t + CU);
+            fetch(i + CU);
 #pragma unroll
             for (int u = 0; u < CU; ++u) {
-                const int64_t tt = t + u, s = tt - (W - 1);
-                if (tt >= until) break;
+                const int k = i + u, s = k - (W - 1);               // dx of token s is complete after token k
+                if (k >= all) break;
                 shift();
-                if (tt < end) {
-                    token(px[u], pg[u]);
-                } else {
+                if (k < left) token(cx[u], cg[u]);
+                else dp[W - 1] = f4(0.f);
+                if (k < own) {
+                    db = db + dp[W - 1];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dp[W - 1][e] = 0.f;
+                    for (int j = 0; j < W; ++j) dw[j] = fma4(dp[W - 1], x[j], dw[j]);
                 }
-                if (tt < last) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        db[e] += dp[W - 1][e];
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][e] = fmaf(dp[W - 1][e], x[j][e], dw[j][e]);
-                    }
-                }
-                if (s >= from) {
-                    float d[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) d[e] = 0.f;
-                    if (a.ds1 && s >= end - (W - 1)) {
-                        Raw8<T> r;
-                        r.load(row<T>(a.ds1, b * (W - 1) + (s - end + W - 1), a.P, c));
-                        r.get(d);
+                if (s >= 0) {
+                    float4 d = f4(0.f);
+                    if (a.ds1 && s >= tail) {
+                        Raw4<T> r;
+                        r.load(row<T>(a.ds1, b * (W - 1) + (s - tail), a.P, c));
+                        d = r.get();
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-#pragma unroll
-                        for (int j = 0; j < W; ++j) d[e] = fmaf(w[W - 1 - j][e], dp[j][e], d[e]);
-                    Raw8<T>::of(d).store(static_cast<T *>(a.dx) + s * a.ldx + c);
+                    for (int j = 0; j < W; ++j) d = fma4(w[W - 1 - j], dp[j], d);
+                    st4(pd, d);
+                    pd += a.ldx;
                 }
             }
         }
         t = last;
     }
     // the block's sums over its runs, in their order
-    const int width = vg * 8, col = int(threadIdx.x) % vg * 8;
+#pragma unroll
     for (int k = 0; k <= W; ++k) {
         __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float v = db[e];
-#pragma unroll
-            for (int j = 0; j < W; ++j) v = k == j ? dw[j][e] : v;
-            sum[at.run * width + col + e] = v;
-        }
+        sum[threadIdx.x] = k < W ? dw[k < W ? k : 0] : db;          // thread = run vg + quad
         __syncthreads();
-        const int p = int(blockIdx.y) * width + int(threadIdx.x);
-        if (int(threadIdx.x) < width && p < a.P) {
-            float v = 0.f;
-            for (int r = 0; r < rg; ++r) v += sum[r * width + threadIdx.x];
-            a.part[(int64_t(blockIdx.x) * (W + 1) + k) * a.P + p] = v;
+        const int p = (int(blockIdx.y) * vg + int(threadIdx.x)) * 4;
+        if (int(threadIdx.x) < vg && p < a.P) {
+            float4 v = f4(0.f);
+            for (int r = 0; r < rg; ++r) v = v + sum[r * vg + threadIdx.x];
+            *reinterpret_cast<float4 *>(a.part + (int64_t(blockIdx.x) * (W + 1) + k) * a.P + p) = v;
         }
     }
 }
@@ -297,42 +281,31 @@ __global__ __launch_bounds__(CT) void k_conv_join(const ConvArgs a, int64_t bloc
 
 template <class T, int W>
 __global__ __launch_bounds__(CT) void k_conv_step(const ConvArgs a, T *state, int64_t n_slots, const int32_t *slots) {
-    const int pv = a.P / 8;
+    const int pv = a.P / 4;
     const int64_t i = int64_t(blockIdx.x) * CT + threadIdx.x, b = i / pv;
     if (b >= a.q.B) return;
-    const int c = int(i - b * pv) * 8;
+    const int c = int(i - b * pv) * 4;
     const int64_t slot = slots ? int64_t(__ldg(slots + b)) : b;
     T *y = static_cast<T *>(a.y) + b * a.ldy + c;
     if (slot < 0 || slot >= n_slots) {
-        Raw8<T> r;
-        r.zero();
-        r.store(y);
+        st4(y, f4(0.f));
         return;
     }
-    Raw8<T> r[W];
+    Raw4<T> r[W];
     T *s = state + slot * (W - 1) * a.P + c;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) r[j] = *reinterpret_cast<const Raw8<T> *>(s + int64_t(j) * a.P);
+    for (int j = 0; j < W - 1; ++j) r[j].load_own(s + int64_t(j) * a.P);
     r[W - 1].load(row<T>(a.x, b, a.ldx, c));
-    float w[W][8], p[8];
+    float4 w[W], p;
     load_taps<W>(a, c, w, p);
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-        float x[8];
-        r[j].get(x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = fmaf(w[j][e], x[e], p[e]);
-    }
+    for (int j = 0; j < W; ++j) p = fma4(w[j], r[j].get(), p);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) r[j + 1].store(s + int64_t(j) * a.P);
-    if (a.act) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] *= sigmoid_f(p[e]);
-    }
-    Raw8<T>::of(p).store(y);
+    st4(y, a.act ? p * sigmoid4(p) : p);
 }
 
-// vectors side by side in a block, runs of `tr` tokens, blocks of runs
+// quads side by side in a block, runs of `tr` tokens, blocks of runs
 struct ConvGrid {
     int vg, tr;
     int64_t runs;
@@ -340,9 +313,9 @@ struct ConvGrid {
 // The longest runs (the fewest tokens read twice) of which there are still `want` threads' worth for
 // the loads in flight to cover HBM's latency.
 ConvGrid conv_grid(const ConvArgs &a, int longest, int shortest, int64_t want) {
-    const int pv = a.P / 8;
+    const int pv = a.P / 4;
     ConvGrid g{1, longest, 0};
-    while (g.vg < pv && g.vg < 32) g.vg *= 2;
+    while (g.vg < pv && g.vg < 64) g.vg *= 2;
     while (g.tr > shortest && seq_div(a.q.rows, g.tr) * pv < want) g.tr /= 2;
     g.runs = seq_div(a.q.rows, int64_t(g.tr) * (CT / g.vg));
     return g;
@@ -371,7 +344,7 @@ cudaError_t launch_conv_fwd(const ConvArgs &a, bool bf16, cudaStream_t st) {
     const ConvGrid g = fwd_grid(a);
     const int64_t blocks = g.runs + (a.s1 ? seq_div(a.q.B, CT / g.vg) : 0);
     if (blocks == 0) return cudaSuccess;
-    const dim3 grid(unsigned(blocks), unsigned(seq_div(a.P / 8, g.vg)));
+    const dim3 grid(unsigned(blocks), unsigned(seq_div(a.P / 4, g.vg)));
     ProfScope p(K_CONV_FWD, st);
     pick(a, bf16, [&](auto t, auto w) { k_conv_fwd<decltype(t), decltype(w)::value><<<grid, CT, 0, st>>>(a, g.vg, g.tr, g.runs); });
     return cudaGetLastError();
@@ -381,7 +354,7 @@ cudaError_t launch_conv_bwd(const ConvArgs &a, bool bf16, cudaStream_t st) {
     const ConvGrid g = bwd_grid(a);
     const int64_t blocks = g.runs + (a.ds0 ? seq_div(a.q.B, CT / g.vg) : 0);
     if (blocks) {
-        const dim3 grid(unsigned(blocks), unsigned(seq_div(a.P / 8, g.vg)));
+        const dim3 grid(unsigned(blocks), unsigned(seq_div(a.P / 4, g.vg)));
         ProfScope p(K_CONV_BWD, st);
         pick(a, bf16, [&](auto t, auto w) { k_conv_bwd<decltype(t), decltype(w)::value><<<grid, CT, 0, st>>>(a, g.vg, g.tr, g.runs); });
         const cudaError_t e = cudaGetLastError();
@@ -394,7 +367,7 @@ cudaError_t launch_conv_bwd(const ConvArgs &a, bool bf16, cudaStream_t st) {
 
 cudaError_t launch_conv_step(const ConvArgs &a, bool bf16, void *state, int64_t n_slots, const int32_t *slots,
                              cudaStream_t st) {
-    const unsigned blocks = unsigned(seq_div(a.q.B * (a.P / 8), CT));
+    const unsigned blocks = unsigned(seq_div(a.q.B * (a.P / 4), CT));
     ProfScope p(K_CONV_STEP, st);
     pick(a, bf16, [&](auto t, auto w) {
         typedef decltype(t) T;

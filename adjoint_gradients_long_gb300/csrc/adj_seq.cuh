@@ -48,13 +48,6 @@ struct Raw8<float> {
     __device__ __forceinline__ void get(float (&x)[8]) const {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
-    __device__ __forceinline__ static Raw8 of(const float (&x)[8]) {
-        return Raw8{make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7])};
-    }
-    __device__ __forceinline__ void store(float *p) const {
-        reinterpret_cast<float4 *>(p)[0] = a;
-        reinterpret_cast<float4 *>(p)[1] = b;
-    }
 };
 template <>
 struct Raw8<__nv_bfloat16> {
@@ -69,22 +62,31 @@ struct Raw8<__nv_bfloat16> {
             x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
     }
-    __device__ __forceinline__ static Raw8 of(const float (&x)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<uint32_t *>(&v);
-        }
-        return Raw8{make_uint4(w[0], w[1], w[2], w[3])};
-    }
-    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint4 *>(p) = u; }
 };
-// eight consecutive fp32
-__device__ __forceinline__ void ld8(const float *p, float (&x)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+// ---------------------------------------------------------------- four channels, as they are stored
+template <class T>
+struct Raw4;
+template <>
+struct Raw4<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float *p) { v = __ldg(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void load_own(const float *p) { v = *reinterpret_cast<const float4 *>(p); }   // written by this launch too
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float4 *>(p) = v; }
+    __device__ __forceinline__ void zero() { v = f4(0.f); }
+    __device__ __forceinline__ float4 get() const { return v; }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldg(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ void load_own(const __nv_bfloat16 *p) { v = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint2 *>(p) = v; }
+    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
+    __device__ __forceinline__ float4 get() const {
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xFFFF0000u));
+    }
+};
 
 // ---------------------------------------------------------------- functions of one value
 __device__ __forceinline__ float fast_rcp(float x) {
@@ -95,6 +97,10 @@ __device__ __forceinline__ float fast_rcp(float x) {
 constexpr float SEQ_LOG2E = 1.4426950408889634f, SEQ_LN2 = 0.6931471805599453f;
 // 1 / (1 + e^-x): the exponential overflows to infinity below -88, whose reciprocal is zero
 __device__ __forceinline__ float sigmoid_f(float x) { return fast_rcp(1.f + fast_exp2(-x * SEQ_LOG2E)); }
+
+__device__ __forceinline__ float4 sigmoid4(float4 v) {
+    return make_float4(sigmoid_f(v.x), sigmoid_f(v.y), sigmoid_f(v.z), sigmoid_f(v.w));
+}
 
 // log(1 + e^v) = max(v, 0) + 2 atanh(s), s = e / (2 + e), e = e^-|v|: s is at most 1/3, where a polynomial
 // of degree 4 in s^2 gives atanh(s) / s to 4e-9 (interpolated at Chebyshev nodes).  The rounding of the

@@ -72,8 +72,8 @@ adj_status check_conv(const adj_conv_dims *d, bool step, ConvArgs &a) {
     a.q = Seqs{nullptr, d->B, step ? 1 : d->T, rows};
     a.ldx = d->ldx; a.ldy = d->ldy;
     a.P = d->P; a.W = d->W; a.act = d->act;
-    // grids: a thread for every vector of a step, blocks of 32 vectors in their second dimension
-    return !step || rows * (d->P / 8) < (int64_t(1) << 38) ? ADJ_OK : ADJ_ESHAPE;
+    // grids: a thread for every four channels of a step, blocks of 64 quads in their second dimension
+    return !step || rows * (d->P / 4) < (int64_t(1) << 38) ? ADJ_OK : ADJ_ESHAPE;
 }
 
 adj_status check_ssm(const adj_ssm_dims *d, bool step, SsmArgs &a) {

@@ -157,27 +157,6 @@ struct Marks {
     __device__ __forceinline__ int64_t of(int i) const { return __shfl_sync(~0u, seq, i); }
 };
 
-// Four channels as they are stored
-template <class T>
-struct Raw4;
-template <>
-struct Raw4<float> {
-    float4 v;
-    __device__ __forceinline__ void load(const float *p) { v = __ldg(reinterpret_cast<const float4 *>(p)); }
-    __device__ __forceinline__ void zero() { v = f4(0.f); }
-    __device__ __forceinline__ float4 get() const { return v; }
-};
-template <>
-struct Raw4<__nv_bfloat16> {
-    uint2 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldg(reinterpret_cast<const uint2 *>(p)); }
-    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
-    __device__ __forceinline__ float4 get() const {
-        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                           __uint_as_float(v.y & 0xFFFF0000u));
-    }
-};
-
 // What a lane stages and finishes: quad j is token row + NQ j of the tile, always the same channels
 template <class T, int N>
 struct Mine {
@@ -209,9 +188,6 @@ struct Mine {
 
 __device__ __forceinline__ float4 softplus4(float4 v) {
     return make_float4(softplus_f(v.x), softplus_f(v.y), softplus_f(v.z), softplus_f(v.w));
-}
-__device__ __forceinline__ float4 sigmoid4(float4 v) {
-    return make_float4(sigmoid_f(v.x), sigmoid_f(v.y), sigmoid_f(v.z), sigmoid_f(v.w));
 }
 __device__ __forceinline__ void put4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
 __device__ __forceinline__ float4 get4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
@@ -818,48 +794,53 @@ __global__ __launch_bounds__(256) void k_ssm_join(const SsmArgs a, int64_t cols,
 }
 
 // ---------------------------------------------------------------- single tokens
-// A thread takes four states of one channel; the state is read and written once, bound by HBM.
+// A thread takes four states of each of K channels, K the number of quads of states, 4 at most: its K loads of
+// the state are in flight together, and the steps of the K channels are formed by one lane each.
+// The state is read and written once, bound by HBM.
 template <class T, int N>
 __global__ __launch_bounds__(256) void k_ssm_step(const SsmArgs a, float *state, int64_t n_slots, const int32_t *slots) {
-    constexpr int NQ = N / 4;
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, per = int64_t(a.P) * NQ, b = i / per;
-    const bool in = b < a.q.B;                                      // whole groups of NQ lanes
-    const int64_t r = in ? i - b * per : 0;
-    const int p = int(r / NQ), nq = int(r % NQ);
-    float y = 0.f, x = 0.f;
-    bool held = false;
-    if (in) {
-        const int64_t slot = slots ? int64_t(__ldg(slots + b)) : b;
-        held = slot >= 0 && slot < n_slots;
-        if (held) {
-            float4 *s = reinterpret_cast<float4 *>(state + (slot * a.P + p) * N) + nq, h = *s;
-            x = float(static_cast<const T *>(a.x)[b * a.ldx + p]);
-            const float raw = float(static_cast<const T *>(a.dt)[b * a.lddt + p]);
-            const float d = softplus_f(raw + (a.bias ? __ldg(a.bias + p) : 0.f)), u = d * x;
-            const float4 A = f4(SEQ_LOG2E * d) * __ldg(reinterpret_cast<const float4 *>(a.A + int64_t(p) * N) + nq);
-            float B[4], C[4];
+    constexpr int NQ = N / 4, K = NQ < 4 ? NQ : 4;
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, per = int64_t(a.P) / K * NQ, b = i / per;
+    if (b >= a.q.B) return;                                         // whole groups of NQ lanes
+    const int r = int(i - b * per), nq = r % NQ, c0 = r / NQ * K, k0 = nq % K, p = c0 + k0;
+    const uint32_t group = (NQ == 32 ? ~0u : (1u << NQ) - 1) << (threadIdx.x & 31 & ~(NQ - 1));
+    T *y = static_cast<T *>(a.y) + b * a.ldy + p;
+    const int64_t slot = slots ? int64_t(__ldg(slots + b)) : b;
+    if (slot < 0 || slot >= n_slots) {                              // the whole group
+        if (nq < K) *y = T(0.f);
+        return;
+    }
+    float4 *s = reinterpret_cast<float4 *>(state + (slot * a.P + c0) * N) + nq, h[K];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                B[n] = float(static_cast<const T *>(a.Bm)[b * a.ldB + nq * 4 + n]);
-                C[n] = float(static_cast<const T *>(a.Cm)[b * a.ldC + nq * 4 + n]);
-            }
-            h = make_float4(fmaf(fast_exp2(A.x), h.x, u * B[0]), fmaf(fast_exp2(A.y), h.y, u * B[1]),
-                            fmaf(fast_exp2(A.z), h.z, u * B[2]), fmaf(fast_exp2(A.w), h.w, u * B[3]));
-            *s = h;
-            y = fmaf(C[0], h.x, fmaf(C[1], h.y, fmaf(C[2], h.z, C[3] * h.w)));
-        }
+    for (int k = 0; k < K; ++k) h[k] = s[k * NQ];
+    const float x = float(static_cast<const T *>(a.x)[b * a.ldx + p]);
+    const float raw = float(static_cast<const T *>(a.dt)[b * a.lddt + p]);
+    const float z = a.z ? float(static_cast<const T *>(a.z)[b * a.ldz + p]) : 0.f;
+    Raw4<T> rB, rC;
+    rB.load(static_cast<const T *>(a.Bm) + b * a.ldB + nq * 4);
+    rC.load(static_cast<const T *>(a.Cm) + b * a.ldC + nq * 4);
+    const float4 B = rB.get(), C = rC.get(), up = f4(EXP_UP);
+    const float d0 = softplus_f(raw + (a.bias ? __ldg(a.bias + p) : 0.f)), u0 = d0 * x;
+    float v[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const float d = __shfl_sync(group, d0, k, NQ), u = __shfl_sync(group, u0, k, NQ);
+        const float4 A = f4(SEQ_LOG2E) * __ldg(reinterpret_cast<const float4 *>(a.A + int64_t(c0 + k) * N) + nq), t = fma4(f4(d), A, up);
+        h[k] = fma4(make_float4(fast_exp2(t.x), fast_exp2(t.y), fast_exp2(t.z), fast_exp2(t.w)), h[k], f4(u) * B);
+        s[k * NQ] = h[k];
+        v[k] = fmaf(C.x, h[k].x, fmaf(C.y, h[k].y, fmaf(C.z, h[k].z, C.w * h[k].w)));
     }
 #pragma unroll
-    for (int d = 1; d < NQ; d <<= 1) y += __shfl_xor_sync(~0u, y, d);
-    if (!in || nq != 0) return;
-    if (held) {
-        if (a.D) y = fmaf(__ldg(a.D + p), x, y);
-        if (a.z) {
-            const float z = float(static_cast<const T *>(a.z)[b * a.ldz + p]);
-            y *= z * sigmoid_f(z);
-        }
-    }
-    static_cast<T *>(a.y)[b * a.ldy + p] = T(y);
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int w = 1; w < NQ; w <<= 1) v[k] += __shfl_xor_sync(group, v[k], w);
+    if (nq >= K) return;
+    float out = v[0];
+#pragma unroll
+    for (int k = 1; k < K; ++k) out = k0 == k ? v[k] : out;
+    if (a.D) out = fmaf(__ldg(a.D + p), x, out);
+    if (a.z) out *= z * sigmoid_f(z);
+    *y = T(out);
 }
 
 // ---------------------------------------------------------------- launches
@@ -970,7 +951,7 @@ cudaError_t launch_ssm_step(const SsmArgs &a, bool bf16, float *state, int64_t n
         typedef decltype(t) T;
         constexpr int N = decltype(n)::value;
         ProfScope p(K_SSM_STEP, st);
-        k_ssm_step<T, N><<<unsigned(seq_div(a.q.B * a.P * (N / 4), 256)), 256, 0, st>>>(a, state, n_slots, slots);
+        k_ssm_step<T, N><<<unsigned(seq_div(a.q.B * (a.P / std::min(4, N / 4)) * (N / 4), 256)), 256, 0, st>>>(a, state, n_slots, slots);
         return cudaGetLastError();
     });
 }
