@@ -8,16 +8,18 @@
 //
 // The kept tokens are a prefix of the order by x, so a limit is a key (the order of the fp32 values as
 // unsigned integers) and a number of tokens that equal it.  Top-k and top-p are found without sorting:
-// counts and weights over 2048 bins of distance from the maximum say in which bin a limit lies; the keys
-// of that bin are cut into 2048 parts again until one key is left, at most three times (one distinct
-// value in a bin, as often with bf16, ends it at once).  The token is then found by index: sums of the
-// kept weights of every warp's part, of every thread's share of the part that holds it, and along
-// that share.
+// counts or weights over bins of the distance from the maximum, 24 to a power of two, say in which bin
+// a limit lies.  One value alone there (as often with bf16) is the limit; up to 512 tokens are compared
+// with one another; the keys of more are cut into 1024 parts again until one is left, three
+// times at most.  Top-k goes first and counts only, so that weights are formed for what it keeps.
+// The token is then found by index: sums of the kept weights of every warp's part, of every thread's
+// share of the part that holds it, and along that share.
 //
-// One cluster of 1 to 8 blocks a row; the first pass over the logits comes from HBM and the others
-// find them in L2.
+// One cluster of 1 to 8 blocks a row, each with its part of the row in shared memory: the logits are
+// read once, and every later pass finds them there.
 #include <algorithm>
 
+#include "adj_lin.cuh"
 #include "adj_profile.cuh"
 #include "adj_row.cuh"
 #include "adj_seq.cuh"
@@ -27,10 +29,11 @@ namespace {
 
 constexpr int ST = 512;                 // threads of a block
 constexpr int SW = ST / 32;
-constexpr int BINS = 2048;
+constexpr int BINS = 1024;
+constexpr int LIST = 512;               // tokens of a bin that are compared one by one
 constexpr uint64_t ONE = uint64_t(1) << 40;
 constexpr float DEAD = 41.5f;           // 2^-41.5 is less than half a unit
-constexpr float PARTS = 48.f;           // bins a power of two: DEAD of them fit
+constexpr float PARTS = 24.f;           // bins a power of two: DEAD of them fit
 
 // 2^(-i / 256): as a whole number of 2^-42, and as a pair of fp32
 struct alignas(16) Step {
@@ -60,10 +63,19 @@ struct Weigh {
     bool greedy;
     const Step *steps;
 
-    // a part of the distances from the largest: never falls as x does; -1: too far
+    uint64_t least;                     // the smallest weight that min-p keeps, one unit at least
+    float sure, never;                  // distances up to which a weight is above `least`, from which below
+
+    // a part of the distances from the largest: never falls as x does; -1: not kept by min-p, or too far
     __device__ __forceinline__ int bin(float x) const {
+        if (x == m) return 0;
         const float t = (m - x) * hi;
-        return x == m ? 0 : t < DEAD ? int(t * PARTS) : -1;
+        if (greedy || !(t < never) || (t > sure && (*this)(x) < least)) return -1;
+        return int(t * PARTS);
+    }
+    __device__ __forceinline__ uint64_t kept(float x) const {
+        const uint64_t w = (*this)(x);
+        return w < least ? 0 : w;
     }
     __device__ __forceinline__ uint64_t operator()(float x) const {
         if (x == m) return ONE;
@@ -92,20 +104,27 @@ struct Weigh {
 
 struct Shared {
     Step steps[256];
-    unsigned long long weight[BINS];
-    uint32_t count[BINS];
+    uint32_t count[BINS], low[BINS], high[BINS];        // tokens of a bin; the halves of their weights' sum
     // what the blocks of a cluster read of one another
     float top;
-    uint32_t bad, kmin, kmax;
+    uint32_t bad, kmin, kmax, listed, list[LIST];
     unsigned long long part[SW];
     uint32_t ties[SW];
     // scratch of a block
-    unsigned long long red64[SW];
-    uint32_t red32[SW];
-    // a crossing: its bin, what lies before it
-    uint32_t bin, before_c, owner, owner_ties;
+    unsigned long long red64[SW], list_w[LIST];
+    uint32_t red32[SW], all_list[LIST];
+    // a crossing: its bin, what it holds and what lies before it
+    uint32_t bin, here_c, before_c, owner, owner_ties, limit;
     unsigned long long before_w, owner_w, total;
 };
+
+// A 64-bit sum in two native 32-bit additions (64 bits in shared memory are a loop of compare and
+// exchange, which tokens of one bin hold up); few weights reach 2^32, so the second is rare.
+__device__ __forceinline__ void add_weight(Shared &s, int bin, uint64_t w) {
+    const uint32_t lo = uint32_t(w), old = atomicAdd(&s.low[bin], lo);
+    const uint32_t hi = uint32_t(w >> 32) + (old + lo < old ? 1u : 0u);
+    if (hi) atomicAdd(&s.high[bin], hi);
+}
 
 // Exclusive sums over the block's threads, in their order; totals in every thread.
 __device__ void block_scan(Shared &s, uint32_t c, uint64_t w, uint32_t &ec, uint64_t &ew, uint32_t &tc, uint64_t &tw) {
@@ -153,22 +172,15 @@ struct Level {
         uint32_t sc = 0;
         uint64_t sw = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int bin = int(threadIdx.x) * PER + i;
-            c[i] = s.count[bin];
-            w[i] = s.weight[bin];
-        }
-        if (blocks > 1) {
+        for (int i = 0; i < PER; ++i) c[i] = 0, w[i] = 0;
+        for (int b = 0; b < blocks; ++b)
 #pragma unroll
-            for (int i = 0; i < PER; ++i) c[i] = 0, w[i] = 0;
-            for (int b = 0; b < blocks; ++b)
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int bin = int(threadIdx.x) * PER + i;
-                    c[i] += peer(s.count + bin, b);
-                    w[i] += peer(s.weight + bin, b);
-                }
-        }
+            for (int i = 0; i < PER; ++i) {
+                const int bin = int(threadIdx.x) * PER + i;
+                const bool own = blocks == 1;
+                c[i] += own ? s.count[bin] : peer(s.count + bin, b);
+                w[i] += (uint64_t(own ? s.high[bin] : peer(s.high + bin, b)) << 32) + (own ? s.low[bin] : peer(s.low + bin, b));
+            }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             sc += c[i];
@@ -195,6 +207,7 @@ __device__ void cross(Shared &s, const Level &l, const Goal &g, uint32_t over_c,
     for (int i = 0; i < Level::PER; ++i) {
         if (l.c[i] && g.inside(c, w) && !g.inside(c + l.c[i], w + l.w[i])) {
             s.bin = threadIdx.x * Level::PER + i;
+            s.here_c = l.c[i];
             s.before_c = c;
             s.before_w = w;
         }
@@ -204,64 +217,81 @@ __device__ void cross(Shared &s, const Level &l, const Goal &g, uint32_t over_c,
     __syncthreads();
 }
 
-// A limit: tokens above `key`, and the first `ties` of those that equal it, hold `weight`
+// A limit: tokens above `key`, and the first `ties` of those that equal it
 struct Cut {
     uint32_t key, ties;
-    uint64_t weight;
 };
 
+// A block's part of a row: 16-byte vectors in shared memory, minus infinity where they reach over the row
 template <class T>
 struct Row {
     static constexpr int N = Vec<T>::N;
-    Ragged<T> x;
-    int v0, nv;                         // this block's vectors
-    __device__ Row(const SampleArgs &a, int64_t row, int blocks, uint32_t rank)
-        : x(const_cast<T *>(static_cast<const T *>(a.logits)) + row * a.ld, a.V) {
-        const int all = int(x.vectors()), per = (all + blocks - 1) / blocks;
-        v0 = int(rank) * per;
+    uint4 *v;
+    int nv;                             // vectors
+    int64_t j0;                         // index of the first value
+    __device__ Row(const SampleArgs &a, int64_t row, int blocks, uint32_t rank, uint4 *to) : v(to) {
+        const Ragged<T> x(const_cast<T *>(static_cast<const T *>(a.logits)) + row * a.ld, a.V);
+        const int all = int(x.vectors()), per = (all + blocks - 1) / blocks, v0 = int(rank) * per;
         nv = max(0, min(all - v0, per));
-    }
-    __device__ __forceinline__ void load(int i, float (&v)[N]) const { x.load(v0 + i, v, -INFINITY); }
-    __device__ __forceinline__ int64_t index(int i, int e) const { return int64_t(v0 + i) * N - x.shift + e; }
-    template <class F>
-    __device__ __forceinline__ void each(F f) const {
+        j0 = int64_t(v0) * N - x.shift;
+        const uint4 *from = reinterpret_cast<const uint4 *>(x.p - x.shift) + v0;
         for (int i = threadIdx.x; i < nv; i += ST) {
-            float v[N];
-            load(i, v);
+            if (x.whole(v0 + i)) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(v + i))),
+                             "l"(from + i)
+                             : "memory");
+            } else {
+                float f[N];
+                x.load(v0 + i, f, -INFINITY);
+                v[i] = Vec<T>::pack(f);
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    __device__ __forceinline__ int64_t index(int i, int e) const { return j0 + int64_t(i) * N + e; }
+    template <class F>
+    __device__ __forceinline__ void each_of(int i, int end, int step, F f) const {
+        for (; i < end; i += step) {
+            float x[N];
+            Vec<T>::unpack(v[i], x);
 #pragma unroll
-            for (int e = 0; e < N; ++e) f(v[e]);
+            for (int e = 0; e < N; ++e) f(x[e]);
         }
     }
+    template <class F>
+    __device__ __forceinline__ void each(F f) const { each_of(threadIdx.x, nv, ST, f); }
 };
 
 __device__ __forceinline__ void clear(Shared &s) {
     for (int i = threadIdx.x; i < BINS; i += ST) {
-        s.count[i] = 0;
-        s.weight[i] = 0;
+        s.count[i] = s.low[i] = s.high[i] = 0;
     }
 }
 
-// The limit in bin s.bin of the distances: the keys there, cut again until one is left.
+// The limit in bin s.bin of the distances, among tokens with keys of at least `floor`.
 template <class T>
-__device__ Cut narrow(Shared &s, const Row<T> &row, const Weigh &weigh, uint64_t least, const Goal &g, int blocks) {
-    const int bin = int(s.bin);
+__device__ Cut narrow(Shared &s, const Row<T> &row, const Weigh &weigh, const Goal &g, uint32_t floor, int blocks) {
+    const int tid = threadIdx.x, bin = int(s.bin);
+    const bool few = s.here_c <= LIST;
     uint32_t over_c = s.before_c, lo = ~0u, hi = 0;
     uint64_t over_w = s.before_w;
     meet(blocks);                                                   // everyone has read what a call before left
+    if (tid == 0) {
+        s.kmin = ~0u;
+        s.kmax = s.listed = 0;
+    }
+    __syncthreads();
     row.each([&](float x) {
-        if (weigh.bin(x) != bin || weigh(x) < least) return;
+        if (weigh.bin(x) != bin) return;
         const uint32_t k = order_key(x);
+        if (k < floor) return;
         lo = min(lo, k);
         hi = max(hi, k);
+        if (few) s.list[atomicAdd(&s.listed, 1u)] = k;              // here_c of them over all blocks
     });
     lo = __reduce_min_sync(~0u, lo);
     hi = __reduce_max_sync(~0u, hi);
-    if (threadIdx.x == 0) {
-        s.kmin = ~0u;
-        s.kmax = 0;
-    }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
+    if ((tid & 31) == 0) {
         atomicMin(&s.kmin, lo);
         atomicMax(&s.kmax, hi);
     }
@@ -272,18 +302,52 @@ __device__ Cut narrow(Shared &s, const Row<T> &row, const Weigh &weigh, uint64_t
         lo = min(lo, peer(&s.kmin, b));
         hi = max(hi, peer(&s.kmax, b));
     }
+    if (few && lo < hi) {
+        // every token of the bin with all others: what lies above it; the lowest one inside the goal
+        int n = 0;
+        for (int b = 0; b < blocks; ++b) {
+            const int m = int(blocks > 1 ? peer(&s.listed, b) : s.listed);
+            if (tid < m && n + tid < LIST) s.all_list[n + tid] = blocks > 1 ? peer(s.list + tid, b) : s.list[tid];
+            n += m;
+        }
+        n = min(n, LIST);
+        if (tid == 0) s.limit = ~0u;
+        __syncthreads();
+        const uint32_t mine = tid < n ? s.all_list[tid] : 0u;
+        if (tid < n) s.list_w[tid] = g.by_count ? 0 : weigh(key_value(mine));
+        __syncthreads();
+        uint32_t c = over_c;
+        uint64_t w = over_w;
+        if (tid < n) {
+            for (int i = 0; i < n; ++i)
+                if (s.all_list[i] > mine) {
+                    ++c;
+                    w += s.list_w[i];
+                }
+            if (g.inside(c, w)) atomicMin(&s.limit, mine);
+        }
+        __syncthreads();
+        if (tid < n && mine == s.limit) {                           // equal tokens write the same
+            s.before_c = c;
+            s.before_w = w;
+        }
+        __syncthreads();
+        lo = hi = s.limit;
+        over_c = s.before_c;
+        over_w = s.before_w;
+    }
     while (lo < hi) {
-        const int shift = max(0, 21 - __clz(hi - lo));              // the range in at most 2048 parts
+        const int shift = max(0, 22 - __clz(hi - lo));              // the range in at most 1024 parts
         meet(blocks);                                               // everyone has read the bins before
         clear(s);
         __syncthreads();
         row.each([&](float x) {
             const uint32_t k = order_key(x);
             if (k < lo || k > hi) return;
-            const uint64_t w = weigh(x);
-            if (w < least) return;
+            const uint64_t w = weigh.kept(x);
+            if (w == 0) return;
             atomicAdd(&s.count[(hi - k) >> shift], 1u);
-            atomicAdd(&s.weight[(hi - k) >> shift], (unsigned long long)w);
+            if (!g.by_count) add_weight(s, (hi - k) >> shift, w);
         });
         meet(blocks);
         Level l;
@@ -294,7 +358,7 @@ __device__ Cut narrow(Shared &s, const Row<T> &row, const Weigh &weigh, uint64_t
         hi -= s.bin << shift;
         lo = max(lo, hi - ((1u << shift) - 1));
     }
-    Cut c{hi, 0, over_w};
+    Cut c{hi, 0};
     const uint64_t w = weigh(key_value(hi));
     if (w == 0) return c;                                           // not reached: a bin that is crossed holds a token
     if (g.by_count) {
@@ -305,35 +369,34 @@ __device__ Cut narrow(Shared &s, const Row<T> &row, const Weigh &weigh, uint64_t
         while (n > 1 && !(double(over_w + (n - 1) * w) < g.mass)) --n;
         c.ties = uint32_t(n);
     }
-    c.weight += c.ties * w;
     return c;
 }
 
 template <class T>
-__global__ __launch_bounds__(ST, 2) void k_sample(const SampleArgs a, int blocks) {
+__global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
     constexpr int N = Vec<T>::N;
     extern __shared__ __align__(16) char raw[];
     Shared &s = *reinterpret_cast<Shared *>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = blocks > 1 ? rank_in_cluster() : 0u;
     const int64_t n = int64_t(blockIdx.x) / blocks;
-    const Row<T> row(a, n, blocks, rank);
 
     const float temperature = a.temperature ? a.temperature[n] : 1.f;
     const float top_p = a.top_p ? a.top_p[n] : 1.f, min_p = a.min_p ? a.min_p[n] : 0.f;
     const int32_t top_k = a.top_k ? a.top_k[n] : 0;
-    float top = -INFINITY;
-    bool bad = !(temperature >= 0.f) || top_p != top_p || min_p != min_p;
     if (tid < 256) s.steps[tid] = g_steps.s[tid];
     clear(s);
     if (tid == 0) s.bad = 0;
+    const Row<T> row(a, n, blocks, rank, reinterpret_cast<uint4 *>(raw + sizeof(Shared)));
+    __syncthreads();
+    float top = -INFINITY;
+    bool bad = !(temperature >= 0.f) || top_p != top_p || min_p != min_p;
     row.each([&](float x) {
         bad |= !(x < INFINITY);                                     // NaN or +inf
         top = fmaxf(top, x);
     });
 #pragma unroll
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-    __syncthreads();
     if (lane == 0) s.red32[warp] = __float_as_uint(top);
     if (bad) s.bad = 1;
     __syncthreads();
@@ -363,57 +426,74 @@ __global__ __launch_bounds__(ST, 2) void k_sample(const SampleArgs a, int blocks
         weigh.hi = float(c);
         weigh.lo = float(c - double(weigh.hi));
     }
-    const uint64_t least = !(min_p > 0.f) ? 1 : min_p >= 1.f ? ONE : max(uint64_t(1), uint64_t(ceil(double(min_p) * double(ONE))));
-    Cut cut{0, 0, 0};                                               // everything
+    weigh.least = 1;
+    weigh.sure = 40.5f;                                             // half a unit is at 41
+    weigh.never = DEAD;
+    if (min_p > 0.f) {
+        const float p = fminf(min_p, 1.f), t = -log2f(p);
+        weigh.least = max(uint64_t(1), uint64_t(ceil(double(p) * double(ONE))));
+        const float out = weigh.least < 1024 ? 2.f : 0.01f;         // outside log2f's error and the weights' rounding
+        weigh.sure = fminf(weigh.sure, t - out);
+        weigh.never = fminf(weigh.never, t + out);
+    }
+    Cut cut{0, 0};                                                  // everything
     const bool by_k = top_k > 0 && top_k < a.V, by_p = top_p < 1.f;
     if (weigh.greedy || (by_k && top_k == 1)) {
-        cut = Cut{order_key(top), 1, ONE};
-    } else if (by_k || by_p) {
-        row.each([&](float x) {
-            const uint64_t w = weigh(x);
-            if (w < least) return;
-            const int bin = weigh.bin(x);
-            atomicAdd(&s.count[bin], 1u);
-            atomicAdd(&s.weight[bin], (unsigned long long)w);
-        });
-        meet(blocks);
-        Level l;
-        l.read(s, blocks);
-        uint64_t Z = l.all_w;
-        if (by_k && uint32_t(top_k) < l.all_c) {
-            const Goal g{true, uint32_t(top_k), 0.0};
-            cross(s, l, g, 0, 0);
-            cut = narrow(s, row, weigh, least, g, blocks);
-            Z = cut.weight;
+        cut = Cut{order_key(top), 1};
+    } else {
+        if (by_k) {
+            row.each([&](float x) {
+                const int bin = weigh.bin(x);
+                if (bin >= 0) atomicAdd(&s.count[bin], 1u);
+            });
+            meet(blocks);
+            Level l;
+            l.read(s, blocks);
+            if (uint32_t(top_k) < l.all_c) {
+                const Goal g{true, uint32_t(top_k), 0.0};
+                cross(s, l, g, 0, 0);
+                cut = narrow(s, row, weigh, g, 0, blocks);
+            }
         }
         if (by_p) {
+            // tokens that equal top-k's limit count in full here, which moves nothing: what top_p asks
+            // for lies within the kept ones
+            if (by_k) {
+                meet(blocks);                                       // everyone has read the bins
+                clear(s);
+                __syncthreads();
+            }
+            row.each([&](float x) {
+                const uint32_t k = order_key(x);
+                const int bin = k >= cut.key ? weigh.bin(x) : -1;
+                if (bin < 0) return;
+                const uint64_t w = weigh(x);
+                atomicAdd(&s.count[bin], 1u);
+                add_weight(s, bin, w);
+            });
+            meet(blocks);
+            Level l;
+            l.read(s, blocks);
+            uint64_t Z = l.all_w;
+            if (cut.ties) Z -= (uint64_t(l.all_c) - uint32_t(top_k)) * weigh(key_value(cut.key));
             // one token at least: the first begins below one unit
             const Goal g{false, 0, fmax(double(top_p) * double(Z), 1.0)};
             cross(s, l, g, 0, 0);
-            cut = narrow(s, row, weigh, least, g, blocks);
+            cut = narrow(s, row, weigh, g, cut.key, blocks);
         }
     }
 
     // The token, by index: this warp's vectors, their kept weight and the number that equal the limit
     const uint64_t tie_w = cut.ties ? weigh(key_value(cut.key)) : 0;
     const int per = (row.nv + SW - 1) / SW, i0 = min(row.nv, warp * per), i1 = min(row.nv, i0 + per);
-    auto add = [&](int i, uint64_t &w, uint32_t &t) {
-        float v[N];
-        row.load(i, v);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const uint32_t k = order_key(v[e]);
-            if (k > cut.key) {
-                const uint64_t x = weigh(v[e]);
-                w += x < least ? 0 : x;
-            } else {
-                t += k == cut.key;
-            }
-        }
-    };
     uint64_t w = 0;
     uint32_t t = 0;
-    for (int i = i0 + lane; i < i1; i += 32) add(i, w, t);
+    auto add = [&](float x) {
+        const uint32_t k = order_key(x);
+        if (k > cut.key) w += weigh.kept(x);
+        else t += k == cut.key;
+    };
+    row.each_of(i0 + lane, i1, 32, add);
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
         w += __shfl_xor_sync(~0u, w, d);
@@ -457,7 +537,7 @@ __global__ __launch_bounds__(ST, 2) void k_sample(const SampleArgs a, int blocks
         const int share = (last - first + ST - 1) / ST, j0 = min(last, first + tid * share), j1 = min(last, j0 + share);
         w = 0;
         t = 0;
-        for (int i = j0; i < j1; ++i) add(i, w, t);
+        row.each_of(j0, j1, 1, add);
         uint32_t bt, at, u32;
         uint64_t bw, aw;
         block_scan(s, t, 0, bt, bw, at, aw);
@@ -471,13 +551,12 @@ __global__ __launch_bounds__(ST, 2) void k_sample(const SampleArgs a, int blocks
             float value = 0.f;
             for (int i = j0; i < j1; ++i) {
                 float v[N];
-                row.load(i, v);
+                Vec<T>::unpack(row.v[i], v);
                 for (int e = 0; e < N; ++e) {
                     const uint32_t k = order_key(v[e]);
                     uint64_t x = 0;
                     if (k > cut.key) {
-                        x = weigh(v[e]);
-                        x = x < least ? 0 : x;
+                        x = weigh.kept(v[e]);
                     } else if (k == cut.key) {
                         x = bt < cut.ties ? tie_w : 0;
                         ++bt;
@@ -501,15 +580,22 @@ __global__ __launch_bounds__(ST, 2) void k_sample(const SampleArgs a, int blocks
     }
 }
 
+constexpr size_t MOST_SMEM = 232448 - sizeof(Shared) - 64;          // for a part of a row
+static_assert(int64_t(ADJ_SAMPLE_MAX_V) / 8 * 4 + 32 <= int64_t(MOST_SMEM), "a row has to fit eight blocks");
+
 template <class T>
 cudaError_t launch(const SampleArgs &a, cudaStream_t st) {
-    // the blocks of a row: as many as still leave every block 4096 values, while rows alone do not fill the SMs
+    // the fewest blocks whose parts fit; then more, while every block keeps 4096 values and there are SMs for all
+    auto part = [&](int blocks) { return size_t((a.V * sizeof(T) / 16 + 2 + blocks - 1) / blocks) * 16; };
     int blocks = 1;
-    while (blocks < 8 && a.N * blocks * 2 <= 152 * 2 && a.V / (blocks * 2) >= 4096) blocks *= 2;
+    while (blocks < 8 && part(blocks) > MOST_SMEM) blocks *= 2;
+    while (blocks < 8 && a.N * blocks * 2 <= 152 && a.V / (blocks * 2) >= 4096) blocks *= 2;
+    const cudaError_t e = allow_smem<k_sample<T>>(232448);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.N * blocks));
     cfg.blockDim = dim3(ST);
-    cfg.dynamicSmemBytes = sizeof(Shared);
+    cfg.dynamicSmemBytes = sizeof(Shared) + part(blocks);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

@@ -209,7 +209,7 @@ adj_status adj_sample(const adj_sample_dims *d, const void *logits, const float 
                       void *stream) {
     if (!d) return ADJ_EINVAL;
     if (d->x_dtype != ADJ_F32 && d->x_dtype != ADJ_BF16) return ADJ_EDTYPE;
-    if (d->N < 0 || d->N >= (int64_t(1) << 28) || d->V < 1 || d->V >= (int64_t(1) << 22) || d->ld < d->V) return ADJ_ESHAPE;
+    if (d->N < 0 || d->N >= (int64_t(1) << 28) || d->V < 1 || d->V > ADJ_SAMPLE_MAX_V || d->ld < d->V) return ADJ_ESHAPE;
     if (d->reserved) return ADJ_EINVAL;
     if (d->N == 0) return ADJ_OK;
     if (!logits || !u || !token) return ADJ_EINVAL;

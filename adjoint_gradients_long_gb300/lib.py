@@ -18,6 +18,7 @@ OP_SEL_FWD, OP_SEL_BWD, OP_SEL_PARAM = 5, 6, 7
 OP_LIN_FWD, OP_LIN_BWD = 8, 9
 OP_SSM_FWD, OP_SSM_BWD = 10, 11
 LOGPROB_MAX_TOP = 32
+SAMPLE_MAX_V = 393216
 STATUS = {0: "ADJ_OK", 1: "ADJ_EINVAL", 2: "ADJ_ESHAPE", 3: "ADJ_EALIGN", 4: "ADJ_EDTYPE",
           5: "ADJ_EWORKSPACE", 6: "ADJ_ECUDA", 7: "ADJ_ETIMEOUT"}
 EXPORTS = ("adj_workspace_bytes", "adj_fwd_scan", "adj_loss_mse", "adj_bwd_full", "adj_bwd_trunc",

@@ -505,8 +505,8 @@ class Sampler:
         self.rows, self.shape = (N,), (N, V)
         self.device = _device(device)
         self.xt = torch.bfloat16 if x_bf16 else torch.float32
-        if N < 0 or not 1 <= V < 1 << 22:
-            raise ValueError(f"Sampler: N at least 0 and V 1 to {(1 << 22) - 1}, got {N} and {V}")
+        if N < 0 or not 1 <= V <= lib.SAMPLE_MAX_V:
+            raise ValueError(f"Sampler: N at least 0 and V 1 to {lib.SAMPLE_MAX_V}, got {N} and {V}")
         self.dims = lib.sample_dims(N, V, V, lib.BF16 if x_bf16 else lib.F32)
         self.token = torch.empty(N, dtype=torch.int64, device=self.device)
         self.logp = torch.empty(N, dtype=torch.float32, device=self.device)

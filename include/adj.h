@@ -463,8 +463,9 @@ adj_status adj_ssm_step(const adj_ssm_dims *dims, const void *x, const void *dt,
  * are whole numbers the result does not depend on the order of sums, and equal rows give equal tokens.
  * token [N] int64 and logp [N] fp32 (NULL: not written).  Without a finite value a row gives token -1 and
  * logp -inf; with a NaN or +inf in it, or a setting that is NaN or a negative temperature, token -1 and
- * logp NaN.  logits need only their type's alignment, ld >= V; N < 2^28, 1 <= V < 2^22.  One launch, no
- * workspace. */
+ * logp NaN.  logits need only their type's alignment, ld >= V; N < 2^28, 1 <= V <= ADJ_SAMPLE_MAX_V.  One
+ * launch, no workspace. */
+#define ADJ_SAMPLE_MAX_V 393216
 typedef struct {
     int64_t N, V, ld;
     int32_t x_dtype;
