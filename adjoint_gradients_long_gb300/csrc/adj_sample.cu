@@ -27,11 +27,9 @@
 namespace adj {
 namespace {
 
-constexpr int ST = 512;                 // threads of a block
-constexpr int SW = ST / 32;
+constexpr int MOST_WARPS = 32;
 constexpr int BINS = 1024;
 constexpr int LIST = 512;               // tokens of a bin that are compared one by one
-constexpr uint64_t ONE = uint64_t(1) << 40;
 constexpr float DEAD = 41.5f;           // 2^-41.5 is less than half a unit
 constexpr float PARTS = 24.f;           // bins a power of two: DEAD of them fit
 
@@ -59,28 +57,15 @@ __device__ const StepTable g_steps = make_steps();
 
 // A row's weights
 struct Weigh {
-    float m, hi, lo;                    // the largest logit; log2 e / temperature as a pair
-    bool greedy;
+    float m, hi, lo;                    // the largest logit; log2 e / temperature as a pair, finite
     const Step *steps;
-
     uint64_t least;                     // the smallest weight that min-p keeps, one unit at least
     float sure, never;                  // distances up to which a weight is above `least`, from which below
 
-    // a part of the distances from the largest: never falls as x does; -1: not kept by min-p, or too far
-    __device__ __forceinline__ int bin(float x) const {
-        if (x == m) return 0;
-        const float t = (m - x) * hi;
-        if (greedy || !(t < never) || (t > sure && (*this)(x) < least)) return -1;
-        return int(t * PARTS);
-    }
-    __device__ __forceinline__ uint64_t kept(float x) const {
-        const uint64_t w = (*this)(x);
-        return w < least ? 0 : w;
-    }
+    // Without a branch: values at all distances go the same way, and those too far are zero at the end (NaN is
+    // too far: minus infinity at an infinite temperature).
     __device__ __forceinline__ uint64_t operator()(float x) const {
-        if (x == m) return ONE;
         const float d = m - x, t = d * hi;
-        if (greedy || !(t < DEAD)) return 0;            // NaN: minus infinity at an infinite temperature
         const float b = d - m, dl = (m - (d - b)) - (x + b);
         const float e = fmaf(d, hi, -t) + fmaf(d, lo, dl * hi);
         const float MAGIC = 12582912.f;                 // 1.5 2^23: rounds to whole numbers
@@ -97,8 +82,19 @@ struct Weigh {
         const float qb = fmaf(rest, 4398046511104.f, MAGIC);    // 2^42, below 2^22 of it
         const long long whole = (long long)s.fixed + ((long long)(__float_as_int(qa) - __float_as_int(MAGIC)) << 22) +
                                 (__float_as_int(qb) - __float_as_int(MAGIC));
-        const int n = (k >> 8) + 2;
-        return uint64_t(whole + (1ll << (n - 1))) >> n;
+        const int n = ((k >> 8) + 2) & 63;
+        const uint64_t w = uint64_t(whole + (1ll << (n - 1))) >> n;
+        return t < DEAD ? w : 0;
+    }
+    // a part of the distances from the largest: never falls as x does; -1: not kept by min-p, or too far
+    __device__ __forceinline__ int bin(float x) const {
+        const float t = (m - x) * hi;
+        if (!(t < never) || (t > sure && (*this)(x) < least)) return -1;
+        return int(t * PARTS);
+    }
+    __device__ __forceinline__ uint64_t kept(float x) const {
+        const uint64_t w = (*this)(x);
+        return w < least ? 0 : w;
     }
 };
 
@@ -108,14 +104,14 @@ struct Shared {
     // what the blocks of a cluster read of one another
     float top;
     uint32_t bad, kmin, kmax, listed, list[LIST];
-    unsigned long long part[SW];
-    uint32_t ties[SW];
+    unsigned long long part[MOST_WARPS];
+    uint32_t ties[MOST_WARPS];
     // scratch of a block
-    unsigned long long red64[SW], list_w[LIST];
-    uint32_t red32[SW], all_list[LIST];
+    unsigned long long red64[MOST_WARPS], list_w[LIST];
+    uint32_t red32[MOST_WARPS], all_list[LIST];
     // a crossing: its bin, what it holds and what lies before it
     uint32_t bin, here_c, before_c, owner, owner_ties, limit;
-    unsigned long long before_w, owner_w, total;
+    unsigned long long before_w, owner_w, total, mass;
 };
 
 // A 64-bit sum in two native 32-bit additions (64 bits in shared memory are a loop of compare and
@@ -127,6 +123,7 @@ __device__ __forceinline__ void add_weight(Shared &s, int bin, uint64_t w) {
 }
 
 // Exclusive sums over the block's threads, in their order; totals in every thread.
+template <int ST>
 __device__ void block_scan(Shared &s, uint32_t c, uint64_t w, uint32_t &ec, uint64_t &ew, uint32_t &tc, uint64_t &tw) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t ic = c;
@@ -151,7 +148,7 @@ __device__ void block_scan(Shared &s, uint32_t c, uint64_t w, uint32_t &ec, uint
     tc = 0;
     tw = 0;
 #pragma unroll
-    for (int i = 0; i < SW; ++i) {
+    for (int i = 0; i < ST / 32; ++i) {
         if (i < warp) {
             bc += s.red32[i];
             bw += s.red64[i];
@@ -163,7 +160,8 @@ __device__ void block_scan(Shared &s, uint32_t c, uint64_t w, uint32_t &ec, uint
     ew = bw + iw - w;
 }
 
-// Four bins of a thread over all blocks, with what lies in the bins before them
+// A thread's bins over all blocks, with what lies in the bins before them
+template <int ST>
 struct Level {
     static constexpr int PER = BINS / ST;
     uint32_t c[PER], before_c, all_c;
@@ -186,7 +184,7 @@ struct Level {
             sc += c[i];
             sw += w[i];
         }
-        block_scan(s, sc, sw, before_c, before_w, all_c, all_w);
+        block_scan<ST>(s, sc, sw, before_c, before_w, all_c, all_w);
     }
 };
 
@@ -194,19 +192,20 @@ struct Level {
 struct Goal {
     bool by_count;
     uint32_t k;
-    double mass;
-    __device__ __forceinline__ bool inside(uint32_t c, uint64_t w) const { return by_count ? c < k : double(w) < mass; }
+    uint64_t mass;
+    __device__ __forceinline__ bool inside(uint32_t c, uint64_t w) const { return by_count ? c < k : w < mass; }
 };
 
 // The last bin whose beginning is inside the goal, given what lies before the whole level.
-__device__ void cross(Shared &s, const Level &l, const Goal &g, uint32_t over_c, uint64_t over_w) {
+template <int ST>
+__device__ void cross(Shared &s, const Level<ST> &l, const Goal &g, uint32_t over_c, uint64_t over_w) {
     uint32_t c = over_c + l.before_c;
     uint64_t w = over_w + l.before_w;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < Level::PER; ++i) {
+    for (int i = 0; i < Level<ST>::PER; ++i) {
         if (l.c[i] && g.inside(c, w) && !g.inside(c + l.c[i], w + l.w[i])) {
-            s.bin = threadIdx.x * Level::PER + i;
+            s.bin = threadIdx.x * Level<ST>::PER + i;
             s.here_c = l.c[i];
             s.before_c = c;
             s.before_w = w;
@@ -217,13 +216,14 @@ __device__ void cross(Shared &s, const Level &l, const Goal &g, uint32_t over_c,
     __syncthreads();
 }
 
-// A limit: tokens above `key`, and the first `ties` of those that equal it
+// A limit: tokens above `x`, and the first `ties` of those that equal it
 struct Cut {
-    uint32_t key, ties;
+    float x;
+    uint32_t ties;
 };
 
 // A block's part of a row: 16-byte vectors in shared memory, minus infinity where they reach over the row
-template <class T>
+template <class T, int ST>
 struct Row {
     static constexpr int N = Vec<T>::N;
     uint4 *v;
@@ -235,16 +235,17 @@ struct Row {
         nv = max(0, min(all - v0, per));
         j0 = int64_t(v0) * N - x.shift;
         const uint4 *from = reinterpret_cast<const uint4 *>(x.p - x.shift) + v0;
-        for (int i = threadIdx.x; i < nv; i += ST) {
-            if (x.whole(v0 + i)) {
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(v + i))),
-                             "l"(from + i)
-                             : "memory");
-            } else {
-                float f[N];
-                x.load(v0 + i, f, -INFINITY);
-                v[i] = Vec<T>::pack(f);
-            }
+        // the first and the last vector of the row may lie partly outside it
+        const int w0 = nv > 0 && !x.whole(v0) ? 1 : 0, w1 = nv > w0 && !x.whole(v0 + nv - 1) ? nv - 1 : nv;
+        for (int i = w0 + int(threadIdx.x); i < w1; i += ST)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(v + i))),
+                         "l"(from + i)
+                         : "memory");
+        if (threadIdx.x < 2 && (threadIdx.x == 0 ? w0 == 1 : w1 < nv)) {
+            const int i = threadIdx.x == 0 ? 0 : nv - 1;
+            float f[N];
+            x.load(v0 + i, f, -INFINITY);
+            v[i] = Vec<T>::pack(f);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -262,15 +263,16 @@ struct Row {
     __device__ __forceinline__ void each(F f) const { each_of(threadIdx.x, nv, ST, f); }
 };
 
+template <int ST>
 __device__ __forceinline__ void clear(Shared &s) {
     for (int i = threadIdx.x; i < BINS; i += ST) {
         s.count[i] = s.low[i] = s.high[i] = 0;
     }
 }
 
-// The limit in bin s.bin of the distances, among tokens with keys of at least `floor`.
-template <class T>
-__device__ Cut narrow(Shared &s, const Row<T> &row, const Weigh &weigh, const Goal &g, uint32_t floor, int blocks) {
+// The limit in bin s.bin of the distances, among tokens of at least `floor`.
+template <class T, int ST>
+__device__ Cut narrow(Shared &s, const Row<T, ST> &row, const Weigh &weigh, const Goal &g, float floor, int blocks) {
     const int tid = threadIdx.x, bin = int(s.bin);
     const bool few = s.here_c <= LIST;
     uint32_t over_c = s.before_c, lo = ~0u, hi = 0;
@@ -282,9 +284,8 @@ __device__ Cut narrow(Shared &s, const Row<T> &row, const Weigh &weigh, const Go
     }
     __syncthreads();
     row.each([&](float x) {
-        if (weigh.bin(x) != bin) return;
+        if (!(x >= floor) || weigh.bin(x) != bin) return;
         const uint32_t k = order_key(x);
-        if (k < floor) return;
         lo = min(lo, k);
         hi = max(hi, k);
         if (few) s.list[atomicAdd(&s.listed, 1u)] = k;              // here_c of them over all blocks
@@ -339,7 +340,7 @@ __device__ Cut narrow(Shared &s, const Row<T> &row, const Weigh &weigh, const Go
     while (lo < hi) {
         const int shift = max(0, 22 - __clz(hi - lo));              // the range in at most 1024 parts
         meet(blocks);                                               // everyone has read the bins before
-        clear(s);
+        clear<ST>(s);
         __syncthreads();
         row.each([&](float x) {
             const uint32_t k = order_key(x);
@@ -350,7 +351,7 @@ __device__ Cut narrow(Shared &s, const Row<T> &row, const Weigh &weigh, const Go
             if (!g.by_count) add_weight(s, (hi - k) >> shift, w);
         });
         meet(blocks);
-        Level l;
+        Level<ST> l;
         l.read(s, blocks);
         cross(s, l, g, over_c, over_w);
         over_c = s.before_c;
@@ -358,23 +359,15 @@ __device__ Cut narrow(Shared &s, const Row<T> &row, const Weigh &weigh, const Go
         hi -= s.bin << shift;
         lo = max(lo, hi - ((1u << shift) - 1));
     }
-    Cut c{hi, 0};
-    const uint64_t w = weigh(key_value(hi));
-    if (w == 0) return c;                                           // not reached: a bin that is crossed holds a token
-    if (g.by_count) {
-        c.ties = g.k - over_c;
-    } else {
-        uint64_t n = uint64_t(fmax((g.mass - double(over_w)) / double(w), 1.0));
-        while (double(over_w + n * w) < g.mass) ++n;
-        while (n > 1 && !(double(over_w + (n - 1) * w) < g.mass)) --n;
-        c.ties = uint32_t(n);
-    }
+    Cut c{key_value(hi), 0};
+    const uint64_t w = weigh(c.x);
+    if (w) c.ties = g.by_count ? g.k - over_c : uint32_t((g.mass - over_w + w - 1) / w);    // the limit holds a token: w > 0
     return c;
 }
 
-template <class T>
+template <class T, int ST>
 __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
-    constexpr int N = Vec<T>::N;
+    constexpr int N = Vec<T>::N, SW = ST / 32;
     extern __shared__ __align__(16) char raw[];
     Shared &s = *reinterpret_cast<Shared *>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -385,9 +378,9 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
     const float top_p = a.top_p ? a.top_p[n] : 1.f, min_p = a.min_p ? a.min_p[n] : 0.f;
     const int32_t top_k = a.top_k ? a.top_k[n] : 0;
     if (tid < 256) s.steps[tid] = g_steps.s[tid];
-    clear(s);
+    clear<ST>(s);
     if (tid == 0) s.bad = 0;
-    const Row<T> row(a, n, blocks, rank, reinterpret_cast<uint4 *>(raw + sizeof(Shared)));
+    const Row<T, ST> row(a, n, blocks, rank, reinterpret_cast<uint4 *>(raw + sizeof(Shared)));
     __syncthreads();
     float top = -INFINITY;
     bool bad = !(temperature >= 0.f) || top_p != top_p || min_p != min_p;
@@ -419,79 +412,74 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
     }
     Weigh weigh;
     weigh.m = top;
-    weigh.greedy = temperature == 0.f;
     weigh.steps = s.steps;
     {
-        const double c = 1.4426950408889634074 / double(temperature);
-        weigh.hi = float(c);
-        weigh.lo = float(c - double(weigh.hi));
+        // log2 e / temperature as a pair: the quotient, and the quotient of what it leaves
+        constexpr float H = 1.44269502162933349609375f, L = 1.925963033500011079e-8f;
+        weigh.hi = fminf(H / temperature, 3.402823466e38f);
+        // none for an infinite temperature, nor for one near zero (a difference of logits is far there)
+        weigh.lo = weigh.hi == 0.f || weigh.hi > 1e37f ? 0.f : (fmaf(-weigh.hi, temperature, H) + L) / temperature;
     }
     weigh.least = 1;
     weigh.sure = 40.5f;                                             // half a unit is at 41
     weigh.never = DEAD;
     if (min_p > 0.f) {
         const float p = fminf(min_p, 1.f), t = -log2f(p);
-        weigh.least = max(uint64_t(1), uint64_t(ceil(double(p) * double(ONE))));
+        weigh.least = max(uint64_t(1), uint64_t(ceilf(p * 1099511627776.f)))      /* 2^40: exact */;
         const float out = weigh.least < 1024 ? 2.f : 0.01f;         // outside log2f's error and the weights' rounding
         weigh.sure = fminf(weigh.sure, t - out);
         weigh.never = fminf(weigh.never, t + out);
     }
-    Cut cut{0, 0};                                                  // everything
+    Cut cut{-INFINITY, 0};                                          // everything
     const bool by_k = top_k > 0 && top_k < a.V, by_p = top_p < 1.f;
-    if (weigh.greedy || (by_k && top_k == 1)) {
-        cut = Cut{order_key(top), 1};
+    if (temperature == 0.f || (by_k && top_k == 1)) {
+        cut = Cut{top, 1};
     } else {
-        if (by_k) {
-            row.each([&](float x) {
-                const int bin = weigh.bin(x);
-                if (bin >= 0) atomicAdd(&s.count[bin], 1u);
-            });
-            meet(blocks);
-            Level l;
-            l.read(s, blocks);
-            if (uint32_t(top_k) < l.all_c) {
-                const Goal g{true, uint32_t(top_k), 0.0};
-                cross(s, l, g, 0, 0);
-                cut = narrow(s, row, weigh, g, 0, blocks);
-            }
-        }
-        if (by_p) {
-            // tokens that equal top-k's limit count in full here, which moves nothing: what top_p asks
-            // for lies within the kept ones
-            if (by_k) {
+        // Top-k first, then top-p among what is left.  Tokens that equal top-k's limit count in full there,
+        // which moves nothing: what top_p asks for lies within the kept ones.
+#pragma unroll 1
+        for (int phase = by_k ? 0 : 1; phase < (by_p ? 2 : 1); ++phase) {
+            const bool mass = phase == 1;
+            if (mass && by_k) {
                 meet(blocks);                                       // everyone has read the bins
-                clear(s);
+                clear<ST>(s);
                 __syncthreads();
             }
             row.each([&](float x) {
-                const uint32_t k = order_key(x);
-                const int bin = k >= cut.key ? weigh.bin(x) : -1;
+                const int bin = x >= cut.x ? weigh.bin(x) : -1;
                 if (bin < 0) return;
-                const uint64_t w = weigh(x);
                 atomicAdd(&s.count[bin], 1u);
-                add_weight(s, bin, w);
+                if (mass) add_weight(s, bin, weigh(x));
             });
             meet(blocks);
-            Level l;
+            Level<ST> l;
             l.read(s, blocks);
-            uint64_t Z = l.all_w;
-            if (cut.ties) Z -= (uint64_t(l.all_c) - uint32_t(top_k)) * weigh(key_value(cut.key));
-            // one token at least: the first begins below one unit
-            const Goal g{false, 0, fmax(double(top_p) * double(Z), 1.0)};
+            Goal g{!mass, uint32_t(top_k), 0};
+            if (mass) {
+                // one token at least: the first begins below one unit.  One thread alone in 64-bit floating point.
+                if (tid == 0) {
+                    uint64_t Z = l.all_w;
+                    if (cut.ties) Z -= (uint64_t(l.all_c) - uint32_t(top_k)) * weigh(cut.x);
+                    s.mass = uint64_t(ceil(fmax(double(top_p) * double(Z), 1.0)));
+                }
+                __syncthreads();
+                g.mass = s.mass;
+            } else if (uint32_t(top_k) >= l.all_c) {
+                continue;
+            }
             cross(s, l, g, 0, 0);
-            cut = narrow(s, row, weigh, g, cut.key, blocks);
+            cut = narrow(s, row, weigh, g, cut.x, blocks);
         }
     }
 
     // The token, by index: this warp's vectors, their kept weight and the number that equal the limit
-    const uint64_t tie_w = cut.ties ? weigh(key_value(cut.key)) : 0;
+    const uint64_t tie_w = cut.ties ? weigh(cut.x) : 0;
     const int per = (row.nv + SW - 1) / SW, i0 = min(row.nv, warp * per), i1 = min(row.nv, i0 + per);
     uint64_t w = 0;
     uint32_t t = 0;
     auto add = [&](float x) {
-        const uint32_t k = order_key(x);
-        if (k > cut.key) w += weigh.kept(x);
-        else t += k == cut.key;
+        if (x > cut.x) w += weigh.kept(x);
+        else t += x == cut.x;
     };
     row.each_of(i0 + lane, i1, 32, add);
 #pragma unroll
@@ -515,12 +503,15 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
             pw = blocks > 1 ? peer(s.part + tid % SW, tid / SW) : s.part[tid];
             pt = blocks > 1 ? peer(s.ties + tid % SW, tid / SW) : s.ties[tid];
         }
-        block_scan(s, pt, 0, bt, bw, at, aw);
+        block_scan<ST>(s, pt, 0, bt, bw, at, aw);
         const uint64_t mine = pw + kept(bt, pt) * tie_w;
-        block_scan(s, 0, mine, u32, bw, at, aw);
-        const float u = a.u[n];
-        const double goal = double(u > 0.f ? fminf(u, 0.99999994f) : 0.f) * double(aw);
-        if (mine && !(double(bw) > goal) && double(bw + mine) > goal) {
+        block_scan<ST>(s, 0, mine, u32, bw, at, aw);
+        if (tid == 0) {
+            const float u = a.u[n];
+            s.mass = uint64_t(double(u > 0.f ? fminf(u, 0.99999994f) : 0.f) * double(aw));
+        }
+        __syncthreads();
+        if (mine && bw <= s.mass && bw + mine > s.mass) {
             s.owner = uint32_t(tid);
             s.owner_w = bw;
             s.owner_ties = bt;
@@ -531,8 +522,7 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
     meet(blocks);                                                   // all have read what they need of the others
     if (s.owner / SW != rank) return;
     {
-        const float u = a.u[n];
-        const double goal = double(u > 0.f ? fminf(u, 0.99999994f) : 0.f) * double(s.total);
+        const uint64_t goal = s.mass;
         const int first = min(row.nv, int(s.owner % SW) * per), last = min(row.nv, first + per);
         const int share = (last - first + ST - 1) / ST, j0 = min(last, first + tid * share), j1 = min(last, j0 + share);
         w = 0;
@@ -540,24 +530,22 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
         row.each_of(j0, j1, 1, add);
         uint32_t bt, at, u32;
         uint64_t bw, aw;
-        block_scan(s, t, 0, bt, bw, at, aw);
+        block_scan<ST>(s, t, 0, bt, bw, at, aw);
         bt += s.owner_ties;
         const uint64_t mine = w + kept(bt, t) * tie_w;
-        block_scan(s, 0, mine, u32, bw, at, aw);
+        block_scan<ST>(s, 0, mine, u32, bw, at, aw);
         bw += s.owner_w;
-        if (mine && !(double(bw) > goal) && double(bw + mine) > goal) {
-            // along this thread's share; the last kept token where rounding passes over the goal
+        if (mine && bw <= goal && bw + mine > goal) {                // along this thread's share
             int64_t token = -1;
             float value = 0.f;
             for (int i = j0; i < j1; ++i) {
                 float v[N];
                 Vec<T>::unpack(row.v[i], v);
                 for (int e = 0; e < N; ++e) {
-                    const uint32_t k = order_key(v[e]);
                     uint64_t x = 0;
-                    if (k > cut.key) {
+                    if (v[e] > cut.x) {
                         x = weigh.kept(v[e]);
-                    } else if (k == cut.key) {
+                    } else if (v[e] == cut.x) {
                         x = bt < cut.ties ? tie_w : 0;
                         ++bt;
                     }
@@ -565,7 +553,7 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
                     bw += x;
                     token = row.index(i, e);
                     value = v[e];
-                    if (double(bw) > goal) {
+                    if (bw > goal) {
                         i = j1;
                         break;
                     }
@@ -574,7 +562,7 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
             a.token[n] = token;
             if (a.logp) {
                 const float far = value == top ? 0.f : (value - top) / temperature;
-                a.logp[n] = far - logf(float(double(s.total) / double(ONE)));
+                a.logp[n] = far - logf(__ull2float_rn(s.total) * (1.f / 1099511627776.f));
             }
         }
     }
@@ -583,19 +571,14 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
 constexpr size_t MOST_SMEM = 232448 - sizeof(Shared) - 64;          // for a part of a row
 static_assert(int64_t(ADJ_SAMPLE_MAX_V) / 8 * 4 + 32 <= int64_t(MOST_SMEM), "a row has to fit eight blocks");
 
-template <class T>
-cudaError_t launch(const SampleArgs &a, cudaStream_t st) {
-    // the fewest blocks whose parts fit; then more, while every block keeps 4096 values and there are SMs for all
-    auto part = [&](int blocks) { return size_t((a.V * sizeof(T) / 16 + 2 + blocks - 1) / blocks) * 16; };
-    int blocks = 1;
-    while (blocks < 8 && part(blocks) > MOST_SMEM) blocks *= 2;
-    while (blocks < 8 && a.N * blocks * 2 <= 152 && a.V / (blocks * 2) >= 4096) blocks *= 2;
-    const cudaError_t e = allow_smem<k_sample<T>>(232448);
+template <class T, int ST>
+cudaError_t launch_as(const SampleArgs &a, int blocks, size_t smem, cudaStream_t st) {
+    const cudaError_t e = allow_smem<k_sample<T, ST>>(232448);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.N * blocks));
     cfg.blockDim = dim3(ST);
-    cfg.dynamicSmemBytes = sizeof(Shared) + part(blocks);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -604,7 +587,19 @@ cudaError_t launch(const SampleArgs &a, cudaStream_t st) {
     cfg.attrs = at;
     cfg.numAttrs = blocks > 1 ? 1 : 0;
     ProfScope p(K_SAMPLE, st);
-    return cudaLaunchKernelEx(&cfg, k_sample<T>, a, blocks);
+    return cudaLaunchKernelEx(&cfg, k_sample<T, ST>, a, blocks);
+}
+
+template <class T>
+cudaError_t launch(const SampleArgs &a, cudaStream_t st) {
+    // the fewest blocks whose parts fit; then more, while every block keeps 4096 values and there are SMs for all
+    auto part = [&](int blocks) { return size_t((a.V * sizeof(T) / 16 + 2 + blocks - 1) / blocks) * 16; };
+    int blocks = 1;
+    while (blocks < 8 && part(blocks) > MOST_SMEM) blocks *= 2;
+    while (blocks < 8 && a.N * blocks * 2 <= 152 && a.V / (blocks * 2) >= 4096) blocks *= 2;
+    const size_t smem = sizeof(Shared) + part(blocks);
+    // a part that leaves no room for a second block beside it gets all the SM's threads
+    return smem > 113 * 1024 ? launch_as<T, 1024>(a, blocks, smem, st) : launch_as<T, 512>(a, blocks, smem, st);
 }
 
 }  // namespace
