@@ -7,13 +7,14 @@
 //     dB_t = sum_p u m_t      dC_t = sum_p g h_t        dA = sum_t d e_t h_{t-1}
 //     dx_t = d sum_n m_t B + D g                        dd_t = x sum_n m_t B + sum_n A e_t h_{t-1}
 //
-// A warp owns a segment of consecutive tokens for CW = 512 / N channels; a thread owns four
-// channels and four states of each, sixteen states in registers.  Lane = quad of states +
-// (N / 4) quad of channels.  Pairs of channels go through the packed fp32 instructions; the exponential
-// of every state and token, one a lane, is what the pipes have most of.  The inputs of a tile of TT
-// tokens are staged in the warp's own part of shared memory, converted to fp32 once (B and C twice
-// over, as pairs); sums over states or channels leave through shared memory too, one 16-byte store
-// a thread and token, and are added up by whole tiles: a butterfly of shuffles costs three times that.
+// A warp owns a segment of consecutive tokens for CW channels; a thread owns 2 NP channels and four states
+// of each in registers (NP 2; 1 for short prompts).  Lane = quad of states + (N / 4) group of channels.
+// Pairs of channels go through the packed fp32 instructions.  The inputs of a tile of TT tokens are
+// staged in the warp's own part of shared memory, converted to fp32 once.  A 16-byte load of it takes four of
+// its cycles whether lanes read the same bytes or not, which was 85% of the forward pass with B and C
+// stored twice over, as pairs, and sums left through it; now they are paired in registers, and sums over
+// the quads of states go by exchanges that halve the values a lane holds.  Neighbouring lanes hold their
+// pairs of channels in opposite order, so that the first exchange needs no selection.
 //
 // The tokens are cut into segments, as many as fill the machine.  k_ssm_state walks every segment from
 // a state of zero; k_ssm_carry goes over the segments in order and leaves the state that enters each;
@@ -34,68 +35,56 @@
 namespace adj {
 namespace {
 
-constexpr int WPB = 4;                  // warps of a block, side by side in channels
-constexpr int G = 4;                    // tokens whose states the backward pass keeps in registers
+constexpr int WPB = 4;                  // warps of a block, side by side in channels (1 for short prompts)
+constexpr int G = 4;                    // tokens of a group: walked without a branch, kept in registers backwards
 
-template <int N>
+// SWAP: neighbouring quads of states hold their channels in opposite order
+template <int N_, int NP_, bool SWAP_>
 struct Tile {
-    static constexpr int NQ = N / 4, CQ = 32 / NQ, CW = 4 * CQ;
-    static constexpr int TT = N == 8 ? 8 : 16;
-    static constexpr int QPL = TT * CQ / 32;                        // a lane's quads of channels in a tile
-    static constexpr int MAPS = TT * N / 8, MPL = (MAPS + 31) / 32; // vectors of eight of B (or C); a lane's
-    static constexpr int X = TT * CW;                               // floats of a tile of channels
-    static constexpr int S = TT * N * 2;                            // floats of a tile of B or C, doubled
+    static constexpr int N = N_, NP = NP_;
+    static constexpr bool SWAP = SWAP_ && NP > 1;
+    static constexpr int NQ = N / 4, CQ = 32 / NQ;                  // quads of states; groups of channels
+    static constexpr int RC = 2 * NP, CW = RC * CQ;                 // channels of a thread, of a warp
+    static constexpr int TT = 512 / CW < 4 ? 4 : 512 / CW > 16 ? 16 : 512 / CW;
+    static constexpr int QR = CW / 4;                               // quads of channels in a token's row
+    static constexpr int QPL = TT * QR < 32 ? 1 : TT * QR / 32;     // of a tile, a lane
+    static constexpr int X = TT * CW, S = TT * N;                   // floats of a tile of channels, of B or C
+    static constexpr int MPL = (S / 8 + 31) / 32;                   // a lane's vectors of eight of B or C
+    static constexpr int OUT = RC > NQ ? RC / NQ : 1;               // a lane's values of a sum over states
 };
-inline int tile_tokens(int N) { return N == 8 ? 8 : 16; }
-inline int warp_channels(int N) { return 512 / N; }
+constexpr int tile_tokens(int N, int np) { return 512 / (256 * np / N) < 4 ? 4 : 512 / (256 * np / N) > 16 ? 16 : 512 / (256 * np / N); }
+constexpr int warp_channels(int N, int np) { return 256 * np / N; }
 
-// four states of four channels: [state][pair of channels]
-struct Quad {
-    pair_t v[4][2];
+// four states of a thread's channels: [state][pair of channels]
+template <class K>
+struct States {
+    pair_t v[4][K::NP];
     __device__ __forceinline__ void fill(float x) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) v[n][0] = v[n][1] = pk(x, x);
-    }
-    // channel c, state n of an array [P][N] from `p` on (in: these channels exist)
-    template <int N>
-    __device__ __forceinline__ void load(const float *p, bool in) {
-        float4 r[4];
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) r[c] = in ? *reinterpret_cast<const float4 *>(p + c * N) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            v[0][k] = pk(r[2 * k].x, r[2 * k + 1].x);
-            v[1][k] = pk(r[2 * k].y, r[2 * k + 1].y);
-            v[2][k] = pk(r[2 * k].z, r[2 * k + 1].z);
-            v[3][k] = pk(r[2 * k].w, r[2 * k + 1].w);
-        }
-    }
-    template <int N>
-    __device__ __forceinline__ void store(float *p, bool in) const {
-        if (!in) return;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float4 x, y;
-            upk(v[0][k], x.x, y.x);
-            upk(v[1][k], x.y, y.y);
-            upk(v[2][k], x.z, y.z);
-            upk(v[3][k], x.w, y.w);
-            *reinterpret_cast<float4 *>(p + 2 * k * N) = x;
-            *reinterpret_cast<float4 *>(p + (2 * k + 1) * N) = y;
-        }
+            for (int k = 0; k < K::NP; ++k) v[n][k] = pk(x, x);
     }
 };
 
 __device__ __forceinline__ ulonglong2 lds2(const float *p) { return *reinterpret_cast<const ulonglong2 *>(p); }
+__device__ __forceinline__ pair_t lds1(const float *p) { return *reinterpret_cast<const pair_t *>(p); }
+__device__ __forceinline__ void put4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ float4 get4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ pair_t twice(float x) { return pk(x, x); }
+__device__ __forceinline__ pair_t shfl2(pair_t v, int d) {
+    float x, y;
+    upk(v, x, y);
+    return pk(__shfl_xor_sync(~0u, x, d), __shfl_xor_sync(~0u, y, d));
+}
 
 // A warp's place: its channels, segment and lanes
-template <int N>
+template <class K>
 struct Lane {
-    typedef Tile<N> K;
     int lane, nq, cq, warp, c0;         // c0: the warp's first channel
     int64_t seg, col;                   // segment, block of channels
     int64_t t0, t1, lo, hi;             // the segment's tokens; those that belong to sequences
-    bool in;                            // this thread's four channels exist
+    bool in;                            // this thread's channels exist
     __device__ Lane(const SsmArgs &a, int64_t block, int64_t cols) {
         lane = threadIdx.x & 31;
         warp = threadIdx.x >> 5;
@@ -103,8 +92,8 @@ struct Lane {
         cq = lane / K::NQ;
         seg = block / cols;
         col = block - seg * cols;
-        c0 = int(col * WPB + warp) * K::CW;
-        in = c0 + cq * 4 < a.P;
+        c0 = int(col * (blockDim.x >> 5) + warp) * K::CW;
+        in = c0 + cq * K::RC < a.P;
         t0 = seg * a.seglen;
         t1 = min(t0 + a.seglen, a.q.rows);
         lo = t0;
@@ -114,11 +103,91 @@ struct Lane {
             hi = min(t1, a.q.at(a.q.B));
         }
     }
-    __device__ __forceinline__ int64_t state(const SsmArgs &a) const { return int64_t(c0 + cq * 4) * N + nq * 4; }
-    __device__ __forceinline__ const float *of(const SsmArgs &a, const float *base, int64_t i) const {
-        return base + i * a.P * N + state(a);
+    // first of the two channels of pair p, inside the warp's
+    __device__ __forceinline__ int pair(int p) const {
+        if (K::NP == 2) return cq * 4 + 2 * (p ^ (K::SWAP ? nq & 1 : 0));
+        return cq * 2;
     }
-    __device__ __forceinline__ float *of(const SsmArgs &a, float *base, int64_t i) const { return base + i * a.P * N + state(a); }
+    // a row [CW] of shared memory: this thread's pairs
+    __device__ __forceinline__ void row(pair_t (&v)[K::NP], const float *p) const {
+        if (K::NP == 2 && !K::SWAP) {
+            const ulonglong2 x = lds2(p + pair(0));
+            v[0] = x.x;
+            v[K::NP - 1] = x.y;
+        } else {
+#pragma unroll
+            for (int k = 0; k < K::NP; ++k) v[k] = lds1(p + pair(k));
+        }
+    }
+    // four states of a row [N] of B or C
+    __device__ __forceinline__ void maps(float (&v)[4], const float *p) const {
+        const float4 x = get4(p + nq * 4);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    }
+    // this thread's part of entry i of an array [.][P][N]
+    __device__ __forceinline__ void load(States<K> &s, const SsmArgs &a, const float *base, int64_t i) const {
+        const float *p = base + (i * a.P + c0) * K::N + nq * 4;
+#pragma unroll
+        for (int k = 0; k < K::NP; ++k) {
+            const float4 x = in ? get4(p + pair(k) * K::N) : f4(0.f), y = in ? get4(p + (pair(k) + 1) * K::N) : f4(0.f);
+            s.v[0][k] = pk(x.x, y.x);
+            s.v[1][k] = pk(x.y, y.y);
+            s.v[2][k] = pk(x.z, y.z);
+            s.v[3][k] = pk(x.w, y.w);
+        }
+    }
+    __device__ __forceinline__ void store(const States<K> &s, const SsmArgs &a, float *base, int64_t i) const {
+        if (!in) return;
+        float *p = base + (i * a.P + c0) * K::N + nq * 4;
+#pragma unroll
+        for (int k = 0; k < K::NP; ++k) {
+            float4 x, y;
+            upk(s.v[0][k], x.x, y.x);
+            upk(s.v[1][k], x.y, y.y);
+            upk(s.v[2][k], x.z, y.z);
+            upk(s.v[3][k], x.w, y.w);
+            put4(p + pair(k) * K::N, x);
+            put4(p + (pair(k) + 1) * K::N, y);
+        }
+    }
+    // a value a channel, [.][P]: written by the first quad of states
+    __device__ __forceinline__ void store(const pair_t (&v)[K::NP], const SsmArgs &a, float *base, int64_t i) const {
+        if (!in || nq != 0) return;
+#pragma unroll
+        for (int k = 0; k < K::NP; ++k) *reinterpret_cast<pair_t *>(base + i * a.P + c0 + pair(k)) = v[k];
+    }
+    // Sums over the quads of states of a value a channel: OUT of them a lane, from channel sums_at() of a row on;
+    // lanes that hold() write them.
+    __device__ __forceinline__ void sums(pair_t (&v)[K::NP], float (&o)[K::OUT]) const {
+        constexpr int NQ = K::NQ;
+        int m = 1;
+        pair_t two = v[0];
+        if (K::NP == 2) {
+            two = add2(v[0], shfl2(v[K::NP - 1], 1));
+            m = 2;
+        }
+        float x, y;
+        upk(two, x, y);
+        if (m >= NQ) {
+            o[0] = x;
+            o[K::OUT - 1] = K::OUT > 1 ? y : x;
+            return;
+        }
+        const bool b = nq & m;
+        float one = (b ? y : x) + __shfl_xor_sync(~0u, b ? x : y, m);
+        for (m *= 2; m < NQ; m *= 2) one += __shfl_xor_sync(~0u, one, m);
+        o[0] = one;
+    }
+    __device__ __forceinline__ int sums_at() const {
+        if (K::NP == 2) return cq * 4 + 2 * (nq & 1) + (K::NQ > 2 ? nq >> 1 & 1 : 0);
+        return cq * 2 + (nq & 1);
+    }
+    __device__ __forceinline__ bool hold() const { return nq < K::RC; }
+    __device__ __forceinline__ void put_sums(float *row, const float (&o)[K::OUT]) const {
+        float *p = row + sums_at();
+        if (K::OUT == 2) *reinterpret_cast<float2 *>(p) = make_float2(o[0], o[K::OUT - 1]);
+        else if (hold()) *p = o[0];
+    }
 };
 
 // The sequences of a tile's tokens, bit i (lane i) for token i
@@ -157,59 +226,69 @@ struct Marks {
     __device__ __forceinline__ int64_t of(int i) const { return __shfl_sync(~0u, seq, i); }
 };
 
-// What a lane stages and finishes: quad j is token row + NQ j of the tile, always the same channels
-template <class T, int N>
+// What a lane stages and finishes: quad j of channels is of token tok(j), always the same channels
+template <class T, class K>
 struct Mine {
-    typedef Tile<N> K;
     int row, cl, c;                     // cl: channel inside the warp's, c: in the array
     bool in;
     float4 bias, D;
-    __device__ Mine(const SsmArgs &a, const Lane<N> &l) {
-        row = l.lane / K::CQ;
-        cl = l.lane % K::CQ * 4;
+    __device__ Mine(const SsmArgs &a, const Lane<K> &l) {
+        row = l.lane / K::QR;
+        cl = l.lane % K::QR * 4;
         c = l.c0 + cl;
-        in = c < a.P;
+        in = c < a.P && row < K::TT;
         bias = a.bias && in ? __ldg(reinterpret_cast<const float4 *>(a.bias + c)) : f4(0.f);
         D = a.D && in ? __ldg(reinterpret_cast<const float4 *>(a.D + c)) : f4(0.f);
     }
-    __device__ __forceinline__ int tok(int j) const { return row + K::NQ * j; }
-    __device__ __forceinline__ bool ok(const Lane<N> &l, int64_t t, int j) const {
-        const int64_t x = t + tok(j);
-        return in && x >= l.lo && x < l.hi;
+    __device__ __forceinline__ int tok(int j) const { return row + 32 / K::QR * j; }
+    __device__ __forceinline__ bool staged() const { return row < K::TT; }
+    // the tile's tokens that belong to sequences: from.. below to, counted from its first
+    int from, to;
+    __device__ __forceinline__ void at(const Lane<K> &l, int64_t t) {
+        from = l.lo > t ? int(min(l.lo - t, int64_t(K::TT))) : 0;
+        to = l.hi < t + K::TT ? int(max(l.hi - t, int64_t(0))) : K::TT;
     }
-    __device__ __forceinline__ void load(Raw4<T> (&r)[K::QPL], const void *p, int64_t ld, const Lane<N> &l, int64_t t) const {
+    __device__ __forceinline__ bool ok(int j) const { return in && tok(j) >= from && tok(j) < to; }
+    __device__ __forceinline__ void load(Raw4<T> (&r)[K::QPL], const void *p, int64_t ld, int64_t t) const {
+        const T *q = static_cast<const T *>(p) + (t + row) * ld + c;
+        const int64_t step = 32 / K::QR * ld;
 #pragma unroll
         for (int j = 0; j < K::QPL; ++j) {
-            if (ok(l, t, j)) r[j].load(static_cast<const T *>(p) + (t + tok(j)) * ld + c);
+            if (ok(j)) r[j].load(q + j * step);
             else r[j].zero();
         }
+    }
+    // quad j of row tok(j) of an array [.][P] with this pitch
+    __device__ __forceinline__ T *out(void *p, int64_t ld, int64_t t, int j) const {
+        return static_cast<T *>(p) + (t + row) * ld + c + j * (32 / K::QR * ld);
     }
 };
 
 __device__ __forceinline__ float4 softplus4(float4 v) {
-    return make_float4(softplus_f(v.x), softplus_f(v.y), softplus_f(v.z), softplus_f(v.w));
+    float4 d;
+    upk(softplus_2(v.x, v.y), d.x, d.y);
+    upk(softplus_2(v.z, v.w), d.z, d.w);
+    return d;
 }
-__device__ __forceinline__ void put4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
-__device__ __forceinline__ float4 get4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
 // steps and inputs of a tile: d and u = d x (zeros where there is no token)
-template <class T, int N>
-__device__ __forceinline__ void stage_steps(const Lane<N> &l, const Mine<T, N> &v, int64_t t, const Raw4<T> (&rx)[Tile<N>::QPL],
-                                            const Raw4<T> (&rdt)[Tile<N>::QPL], float *ds, float *us) {
-    typedef Tile<N> K;
+template <class T, class K>
+__device__ __forceinline__ void stage_steps(const Mine<T, K> &v, const Raw4<T> (&rx)[K::QPL], const Raw4<T> (&rdt)[K::QPL],
+                                            float *ds, float *us) {
+    if (!v.staged()) return;
 #pragma unroll
     for (int j = 0; j < K::QPL; ++j) {
-        const float4 d = v.ok(l, t, j) ? softplus4(rdt[j].get() + v.bias) : f4(0.f);
+        const float4 d = v.ok(j) ? softplus4(rdt[j].get() + v.bias) : f4(0.f);
         put4(ds + v.tok(j) * K::CW + v.cl, d);
         put4(us + v.tok(j) * K::CW + v.cl, d * rx[j].get());
     }
 }
 
 // the cotangent g of v: go, times z sigmoid(z) with a gate
-template <class T, int N>
-__device__ __forceinline__ void stage_cotangent(const SsmArgs &a, const Mine<T, N> &v, const Raw4<T> (&rg)[Tile<N>::QPL],
-                                                const Raw4<T> (&rz)[Tile<N>::QPL], float *gs) {
-    typedef Tile<N> K;
+template <class T, class K>
+__device__ __forceinline__ void stage_cotangent(const SsmArgs &a, const Mine<T, K> &v, const Raw4<T> (&rg)[K::QPL],
+                                                const Raw4<T> (&rz)[K::QPL], float *gs) {
+    if (!v.staged()) return;
 #pragma unroll
     for (int j = 0; j < K::QPL; ++j) {
         float4 g = rg[j].get();
@@ -221,166 +300,175 @@ __device__ __forceinline__ void stage_cotangent(const SsmArgs &a, const Mine<T, 
     }
 }
 
-// B or C of a tile: fetched, and staged with each value twice
-template <class T, int N>
+// B or C of a tile
+template <class T, class K>
 struct Maps {
-    typedef Tile<N> K;
     Raw8<T> r[K::MPL];
-    __device__ __forceinline__ void load(const void *p, int64_t ld, const Lane<N> &l, int64_t t) {
+    __device__ __forceinline__ void load(const void *p, int64_t ld, const Lane<K> &l, const Mine<T, K> &v, int64_t t) {
 #pragma unroll
         for (int j = 0; j < K::MPL; ++j) {
-            const int i = l.lane + 32 * j, tok = i / (N / 8), n = i % (N / 8) * 8;
-            if (tok < K::TT && t + tok >= l.lo && t + tok < l.hi) r[j].load(static_cast<const T *>(p) + (t + tok) * ld + n);
+            const int i = l.lane + 32 * j, tok = i / (K::N / 8), n = i % (K::N / 8) * 8;
+            if (tok >= v.from && tok < v.to) r[j].load(static_cast<const T *>(p) + (t + tok) * ld + n);
             else r[j].zero();
         }
     }
-    __device__ __forceinline__ void stage(const Lane<N> &l, float *s) const {
+    __device__ __forceinline__ void stage(const Lane<K> &l, float *s) const {
 #pragma unroll
         for (int j = 0; j < K::MPL; ++j) {
             const int i = l.lane + 32 * j;
             float x[8];
             r[j].get(x);
-            if (i < K::MAPS)
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) put4(s + (i * 8 + e) * 2, make_float4(x[e], x[e], x[e + 1], x[e + 1]));
+            if (i < K::S / 8) {
+                put4(s + i * 8, make_float4(x[0], x[1], x[2], x[3]));
+                put4(s + i * 8 + 4, make_float4(x[4], x[5], x[6], x[7]));
+            }
         }
     }
 };
-
-template <int N>
-__device__ __forceinline__ Quad decays(const SsmArgs &a, const Lane<N> &l) {
-    Quad A;
-    A.load<N>(a.A + l.state(a), l.in);
-    const pair_t e = pk(SEQ_LOG2E, SEQ_LOG2E);
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) A.v[n][k] = mul2(A.v[n][k], e);
-    return A;
-}
 
 // The exponential unit's results lie low by 2e-8 on average where the exponent is near zero (measured over
 // 0 to -1; 0.3 to 0.8 units of the last place at worst either way).  States that last for a
 // thousand tokens would show it, so exponents are raised by that much in the multiply-add that forms them.
 constexpr float EXP_UP = 2.5e-8f;
 
-// what a thread reads of a token: its channels' steps and inputs, its states' B (or C)
-template <int N>
+template <class K>
+__device__ __forceinline__ States<K> decays(const SsmArgs &a, const Lane<K> &l) {
+    States<K> A;
+    l.load(A, a, a.A, 0);
+    const pair_t e = twice(SEQ_LOG2E);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int k = 0; k < K::NP; ++k) A.v[n][k] = mul2(A.v[n][k], e);
+    return A;
+}
+
+// what a thread reads of a token to advance its states: its channels' steps and inputs, its states' B
+template <class K>
 struct Token {
-    pair_t d[2], u[2], B[4];
-    __device__ __forceinline__ void load(const float *ds, const float *us, const float *Bs, const Lane<N> &l, int i) {
-        const ulonglong2 x = lds2(ds + i * Tile<N>::CW + l.cq * 4), y = lds2(us + i * Tile<N>::CW + l.cq * 4);
-        d[0] = x.x; d[1] = x.y;
-        u[0] = y.x; u[1] = y.y;
-        maps(B, Bs, l, i);
-    }
-    __device__ __forceinline__ static void maps(pair_t (&b)[4], const float *s, const Lane<N> &l, int i) {
-        const ulonglong2 x = lds2(s + (i * N + l.nq * 4) * 2), y = lds2(s + (i * N + l.nq * 4) * 2 + 4);
-        b[0] = x.x; b[1] = x.y; b[2] = y.x; b[3] = y.y;
+    pair_t d[K::NP], u[K::NP];
+    float B[4];
+    __device__ __forceinline__ void load(const float *ds, const float *us, const float *Bs, const Lane<K> &l, int i) {
+        l.row(d, ds + i * K::CW);
+        l.row(u, us + i * K::CW);
+        l.maps(B, Bs + i * K::N);
     }
 };
 
 // h = exp(d A) h + u B for one token
-template <bool KEEP, int N>
-__device__ __forceinline__ void advance(const Quad &A, Quad &h, Quad *keep, const Token<N> &k) {
-    const pair_t up = pk(EXP_UP, EXP_UP);
+template <bool KEEP, class K>
+__device__ __forceinline__ void advance(const States<K> &A, States<K> &h, States<K> *keep, const Token<K> &k) {
+    const pair_t up = twice(EXP_UP);
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < 4; ++n) {
+        const pair_t B = twice(k.B[n]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < K::NP; ++c) {
             const pair_t e = exp2_2(fma2(k.d[c], A.v[n][c], up));
             if (KEEP) keep->v[n][c] = e;
-            h.v[n][c] = fma2(e, h.v[n][c], mul2(k.u[c], k.B[n]));
+            h.v[n][c] = fma2(e, h.v[n][c], mul2(k.u[c], B));
         }
+    }
+}
+
+// the state before a sequence's first token
+template <class K>
+__device__ __forceinline__ void begin_sequence(const SsmArgs &a, const Lane<K> &l, int64_t b, States<K> &h) {
+    if (a.s0) l.load(h, a, a.s0, b);
+    else h.fill(0.f);
 }
 
 // ---------------------------------------------------------------- segments from a state of zero
+template <class K, bool BWD>
+constexpr int state_floats() { return (BWD ? 3 : 2) * K::X + (BWD ? 2 : 1) * K::S; }
+
 template <class T, int N, bool BWD>
 __global__ __launch_bounds__(32 * WPB, 3) void k_ssm_state(const SsmArgs a, int64_t cols) {
-    typedef Tile<N> K;
+    typedef Tile<N, 2, false> K;
     extern __shared__ __align__(16) float sm[];
-    const Lane<N> l(a, blockIdx.x, cols);
-    const Mine<T, N> v(a, l);
-    float *ds = sm + l.warp * ((BWD ? 3 : 2) * K::X + (BWD ? 2 : 1) * K::S), *us = ds + K::X, *Bs = us + K::X;
+    const Lane<K> l(a, blockIdx.x, cols);
+    Mine<T, K> v(a, l);
+    float *ds = sm + l.warp * state_floats<K, BWD>(), *us = ds + K::X, *Bs = us + K::X;
     float *Cs = Bs + K::S, *gs = Cs + K::S;                         // BWD
-    const Quad A = decays<N>(a, l);
-    Quad h, P, m;
+    const States<K> A = decays<K>(a, l);
+    States<K> h, P, m;
     h.fill(0.f);
     P.fill(1.f);
     m.fill(0.f);
-    pair_t sum[2] = {pk(0.f, 0.f), pk(0.f, 0.f)};
+    pair_t sum[K::NP];
+#pragma unroll
+    for (int k = 0; k < K::NP; ++k) sum[k] = twice(0.f);
     bool fresh = false;                                             // a sequence has begun in this segment
     Marks mk;
     Raw4<T> rx[K::QPL], rdt[K::QPL];
-    Maps<T, N> rB;
-    v.load(rx, a.x, a.ldx, l, l.t0);
-    v.load(rdt, a.dt, a.lddt, l, l.t0);
-    rB.load(a.Bm, a.ldB, l, l.t0);
-    auto steps = [&](float *p) {                                    // [P] of the sums of steps
-        if (l.nq != 0 || !l.in) return;
-        float4 s;
-        upk(sum[0], s.x, s.y);
-        upk(sum[1], s.z, s.w);
-        put4(p + l.c0 + l.cq * 4, fresh ? f4(-1.f) : s);
+    Maps<T, K> rB;
+    auto fetch = [&](int64_t t) {
+        v.at(l, t);
+        v.load(rx, a.x, a.ldx, t);
+        v.load(rdt, a.dt, a.lddt, t);
+        rB.load(a.Bm, a.ldB, l, v, t);
+    };
+    fetch(l.t0);
+    auto steps = [&](float *p, int64_t i) {                         // [.][P]: the sums of steps
+        pair_t s[K::NP];
+#pragma unroll
+        for (int k = 0; k < K::NP; ++k) s[k] = fresh ? twice(-1.f) : sum[k];
+        l.store(s, a, p, i);
     };
     for (int64_t t = l.t0; t < l.t1; t += K::TT) {
         if (BWD) {
             const int64_t tile = t / K::TT;
-            h.store<N>(l.of(a, a.tile, tile), l.in);
-            steps(a.tstep + tile * a.P);
+            l.store(h, a, a.tile, tile);
+            steps(a.tstep, tile);
         }
         mk.at<K::TT>(a.q, t, l.lo, l.hi, true);
         __syncwarp();
-        stage_steps<T, N>(l, v, t, rx, rdt, ds, us);
+        stage_steps<T, K>(v, rx, rdt, ds, us);
         rB.stage(l, Bs);
         if (BWD) {
             Raw4<T> rg[K::QPL], rz[K::QPL];
-            Maps<T, N> rC;
-            v.load(rg, a.go, a.ldy, l, t);
-            if (a.z) v.load(rz, a.z, a.ldz, l, t);
-            rC.load(a.Cm, a.ldC, l, t);
-            stage_cotangent<T, N>(a, v, rg, rz, gs);
+            Maps<T, K> rC;
+            v.load(rg, a.go, a.ldy, t);
+            if (a.z) v.load(rz, a.z, a.ldz, t);
+            rC.load(a.Cm, a.ldC, l, v, t);
+            stage_cotangent<T, K>(a, v, rg, rz, gs);
             rC.stage(l, Cs);
         }
         __syncwarp();
-        v.load(rx, a.x, a.ldx, l, t + K::TT);
-        v.load(rdt, a.dt, a.lddt, l, t + K::TT);
-        rB.load(a.Bm, a.ldB, l, t + K::TT);
+        fetch(t + K::TT);
         auto walk = [&](auto events, int i0) {
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 const int i = i0 + j;
-                Token<N> k;
+                Token<K> k;
                 k.load(ds, us, Bs, l, i);
                 if (events && (mk.first >> i & 1u)) {
-                    const int64_t b = mk.of(i);
-                    if (a.s0) h.load<N>(l.of(a, a.s0, b), l.in);
-                    else h.fill(0.f);
+                    begin_sequence(a, l, mk.of(i), h);
                     fresh = true;
                 }
-                sum[0] = add2(sum[0], k.d[0]);
-                sum[1] = add2(sum[1], k.d[1]);
-                Quad e;
+#pragma unroll
+                for (int c = 0; c < K::NP; ++c) sum[c] = add2(sum[c], k.d[c]);
+                States<K> e;
                 advance<BWD>(A, h, &e, k);
                 if (BWD && !(events && fresh)) {
-                    const ulonglong2 g = lds2(gs + i * K::CW + l.cq * 4);
-                    const pair_t gg[2] = {g.x, g.y};
-                    pair_t C[4];
-                    Token<N>::maps(C, Cs, l, i);
+                    pair_t g[K::NP];
+                    float C[4];
+                    l.row(g, gs + i * K::CW);
+                    l.maps(C, Cs + i * N);
 #pragma unroll
                     for (int n = 0; n < 4; ++n)
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
+                        for (int c = 0; c < K::NP; ++c) {
                             P.v[n][c] = mul2(P.v[n][c], e.v[n][c]);
-                            m.v[n][c] = fma2(P.v[n][c], mul2(gg[c], C[n]), m.v[n][c]);
+                            m.v[n][c] = fma2(P.v[n][c], mul2(g[c], twice(C[n])), m.v[n][c]);
                         }
                     if (events && a.ds1 && (mk.last >> i & 1u)) {
-                        Quad s;
-                        s.load<N>(l.of(a, a.ds1, mk.of(i)), l.in);
+                        States<K> s;
+                        l.load(s, a, a.ds1, mk.of(i));
 #pragma unroll
                         for (int n = 0; n < 4; ++n)
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) m.v[n][c] = fma2(P.v[n][c], s.v[n][c], m.v[n][c]);
+                            for (int c = 0; c < K::NP; ++c) m.v[n][c] = fma2(P.v[n][c], s.v[n][c], m.v[n][c]);
                     }
                 }
             }
@@ -391,9 +479,9 @@ __global__ __launch_bounds__(32 * WPB, 3) void k_ssm_state(const SsmArgs a, int6
             else walk(std::false_type(), i);
         }
     }
-    h.store<N>(l.of(a, a.seg, l.seg), l.in);
-    steps(a.step + l.seg * a.P);
-    if (BWD) m.store<N>(l.of(a, a.adj, l.seg), l.in);
+    l.store(h, a, a.seg, l.seg);
+    steps(a.step, l.seg);
+    if (BWD) l.store(m, a, a.adj, l.seg);
 }
 
 // Over the segments in order: seg becomes the state that enters each; blockIdx.y 1: adj, from the right.
@@ -440,76 +528,75 @@ __device__ void pass_through(const SsmArgs &a, float *out, const float *in, int6
 }
 
 // ---------------------------------------------------------------- outputs
-template <class T, int N>
+template <class K>
+constexpr int out_floats() { return 3 * K::X + 2 * K::S; }
+
+template <class T, int N, int NP>
 __global__ __launch_bounds__(32 * WPB, 3) void k_ssm_out(const SsmArgs a, int64_t cols) {
-    typedef Tile<N> K;
+    typedef Tile<N, NP, true> K;
     extern __shared__ __align__(16) float sm[];
     const int64_t work = a.nseg * cols;
     if (int64_t(blockIdx.x) >= work) {
         pass_through(a, a.s1, a.s0, blockIdx.x - work, gridDim.x - work);
         return;
     }
-    const Lane<N> l(a, blockIdx.x, cols);
-    const Mine<T, N> v(a, l);
-    float *ds = sm + l.warp * (2 * K::X + 2 * K::S + K::TT * 128), *us = ds + K::X, *Bs = us + K::X, *Cs = Bs + K::S;
-    float *ys = Cs + K::S;                                          // [TT][NQ][CW]: sums over a quad of states
-    const Quad A = decays<N>(a, l);
-    Quad h;
+    const Lane<K> l(a, blockIdx.x, cols);
+    Mine<T, K> v(a, l);
+    float *ds = sm + l.warp * out_floats<K>(), *us = ds + K::X, *ys = us + K::X, *Bs = ys + K::X, *Cs = Bs + K::S;
+    const States<K> A = decays<K>(a, l);
+    States<K> h;
     h.fill(0.f);
-    if (a.nseg > 1) h.load<N>(l.of(a, a.seg, l.seg), l.in);
+    if (a.nseg > 1) l.load(h, a, a.seg, l.seg);
     Marks mk;
     Raw4<T> rx[K::QPL], rdt[K::QPL], rz[K::QPL], cx[K::QPL];
-    Maps<T, N> rB, rC;
+    Maps<T, K> rB, rC;
     auto fetch = [&](int64_t t) {
-        v.load(rx, a.x, a.ldx, l, t);
-        v.load(rdt, a.dt, a.lddt, l, t);
-        rB.load(a.Bm, a.ldB, l, t);
-        rC.load(a.Cm, a.ldC, l, t);
+        v.at(l, t);
+        v.load(rx, a.x, a.ldx, t);
+        v.load(rdt, a.dt, a.lddt, t);
+        rB.load(a.Bm, a.ldB, l, v, t);
+        rC.load(a.Cm, a.ldC, l, v, t);
     };
     fetch(l.t0);
     for (int64_t t = l.t0; t < l.t1; t += K::TT) {
         mk.at<K::TT>(a.q, t, l.lo, l.hi, true);
         __syncwarp();
-        stage_steps<T, N>(l, v, t, rx, rdt, ds, us);
+        stage_steps<T, K>(v, rx, rdt, ds, us);
         rB.stage(l, Bs);
         rC.stage(l, Cs);
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < K::QPL; ++j) cx[j] = rx[j];
-        if (a.z) v.load(rz, a.z, a.ldz, l, t);
+        if (a.z) v.load(rz, a.z, a.ldz, t);
         fetch(t + K::TT);
         // the sums of a group stay in registers until its end: a store to shared memory would hold up
         // the next token's loads
         auto walk = [&](auto events, int i0) {
-            ulonglong2 y[G];
+            float o[G][K::OUT];
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 const int i = i0 + j;
-                Token<N> k;
-                pair_t C[4];
+                Token<K> k;
+                float C[4];
                 k.load(ds, us, Bs, l, i);
-                Token<N>::maps(C, Cs, l, i);
-                if (events && (mk.first >> i & 1u)) {
-                    const int64_t b = mk.of(i);
-                    if (a.s0) h.load<N>(l.of(a, a.s0, b), l.in);
-                    else h.fill(0.f);
-                }
-                advance<false>(A, h, nullptr, k);
-                y[j].x = mul2(C[0], h.v[0][0]);
-                y[j].y = mul2(C[0], h.v[0][1]);
+                l.maps(C, Cs + i * N);
+                if (events && (mk.first >> i & 1u)) begin_sequence(a, l, mk.of(i), h);
+                advance<false>(A, h, &h, k);
+                pair_t y[K::NP];
 #pragma unroll
-                for (int n = 1; n < 4; ++n) {
-                    y[j].x = fma2(C[n], h.v[n][0], y[j].x);
-                    y[j].y = fma2(C[n], h.v[n][1], y[j].y);
+                for (int c = 0; c < K::NP; ++c) {
+                    y[c] = mul2(twice(C[0]), h.v[0][c]);
+#pragma unroll
+                    for (int n = 1; n < 4; ++n) y[c] = fma2(twice(C[n]), h.v[n][c], y[c]);
                 }
+                l.sums(y, o[j]);
                 if (events && a.s1 && (mk.last >> i & 1u)) {
                     const int64_t b = mk.of(i);
-                    h.store<N>(l.of(a, a.s1, b), l.in);
+                    l.store(h, a, a.s1, b);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < G; ++j)
-                *reinterpret_cast<ulonglong2 *>(ys + ((i0 + j) * K::NQ + l.nq) * K::CW + l.cq * 4) = y[j];
+            for (int j = 0; j < G; ++j) l.put_sums(ys + (i0 + j) * K::CW, o[j]);
         };
 #pragma unroll 1
         for (int i = 0; i < K::TT; i += G) {
@@ -517,19 +604,16 @@ __global__ __launch_bounds__(32 * WPB, 3) void k_ssm_out(const SsmArgs a, int64_
             else walk(std::false_type(), i);
         }
         __syncwarp();
+        v.at(l, t);
 #pragma unroll
         for (int j = 0; j < K::QPL; ++j) {
-            if (!v.ok(l, t, j)) continue;
-            const float *p = ys + v.tok(j) * 128 + v.cl;
-            float4 y = get4(p);
-#pragma unroll
-            for (int q = 1; q < K::NQ; ++q) y = y + get4(p + q * K::CW);
-            y = fma4(v.D, cx[j].get(), y);
+            if (!v.ok(j)) continue;
+            float4 y = fma4(v.D, cx[j].get(), get4(ys + v.tok(j) * K::CW + v.cl));
             if (a.z) {
                 const float4 z = rz[j].get();
                 y = y * (z * sigmoid4(z));
             }
-            st4(static_cast<T *>(a.y) + (t + v.tok(j)) * a.ldy + v.c, y);
+            st4(v.out(a.y, a.ldy, t, j), y);
         }
     }
 }
@@ -537,30 +621,30 @@ __global__ __launch_bounds__(32 * WPB, 3) void k_ssm_out(const SsmArgs a, int64_
 // ---------------------------------------------------------------- gradients
 template <int N>
 struct GradSm {                         // floats of a warp's part
-    typedef Tile<N> K;
+    typedef Tile<N, 2, true> K;
     static constexpr int CK = K::TT / G * 512;                      // states at every G-th token, [.][4][32] x 4
-    static constexpr int BC = G * 2 * 128, CH = G * 3 * 128;        // a group's sums: over channels, over states
     static constexpr int SUM = K::TT * 2 * N;                       // dB and dC of a tile over the warp's channels
-    static constexpr int ALL = 3 * K::X + 2 * K::S + CK + BC + CH + SUM;
+    static constexpr int ALL = 3 * K::X + 2 * K::S + CK + SUM;
 };
 
 template <class T, int N>
-__global__ __launch_bounds__(32 * WPB) void k_ssm_grad(const SsmArgs a, int64_t cols) {
-    typedef Tile<N> K;
+__global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64_t cols) {
+    typedef Tile<N, 2, true> K;
     typedef GradSm<N> M;
+    constexpr int NP = K::NP;
     extern __shared__ __align__(16) float sm[];
     const int64_t work = a.nseg * cols;
     if (int64_t(blockIdx.x) >= work) {
         pass_through(a, a.ds0, a.ds1, blockIdx.x - work, gridDim.x - work);
         return;
     }
-    const Lane<N> l(a, blockIdx.x, cols);
-    const Mine<T, N> v(a, l);
+    const Lane<K> l(a, blockIdx.x, cols);
+    Mine<T, K> v(a, l);
     float *ds = sm + l.warp * M::ALL, *us = ds + K::X, *gs = us + K::X, *Bs = gs + K::X, *Cs = Bs + K::S;
-    float *ck = Cs + K::S, *bc = ck + M::CK, *ch = bc + M::BC, *ws = ch + M::CH;
-    const Quad A = decays<N>(a, l);
-    Quad e, dA;                                                     // e: what reaches the state before
-    e.load<N>(l.of(a, a.adj, l.seg), l.in);
+    float *ck = Cs + K::S, *ws = ck + M::CK;
+    const States<K> A = decays<K>(a, l);
+    States<K> e, dA;                                                // e: what reaches the state before
+    l.load(e, a, a.adj, l.seg);
     dA.fill(0.f);
     float4 dD = f4(0.f), db = f4(0.f);
     Marks mk;
@@ -569,108 +653,110 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_grad(const SsmArgs a, int64_t 
         const int64_t t = l.t0 + int64_t(ti) * K::TT, tile = t / K::TT;
         mk.at<K::TT>(a.q, t, l.lo, l.hi, false);
         // the state before the tile
-        Quad h;
+        States<K> h;
         {
-            Quad in;
-            float4 s = make_float4(-1.f, -1.f, -1.f, -1.f);
-            h.load<N>(l.of(a, a.tile, tile), l.in);
-            in.load<N>(l.of(a, a.seg, l.seg), l.in);
-            if (l.in) s = *reinterpret_cast<const float4 *>(a.tstep + tile * a.P + l.c0 + l.cq * 4);
-            if (s.x >= 0.f) {
-                const pair_t d[2] = {pk(s.x, s.y), pk(s.z, s.w)};
+            Raw4<T> rx[K::QPL], rdt[K::QPL], rg[K::QPL], rz[K::QPL];
+            Maps<T, K> rB, rC;
+            v.at(l, t);
+            v.load(rx, a.x, a.ldx, t);
+            v.load(rdt, a.dt, a.lddt, t);
+            v.load(rg, a.go, a.ldy, t);
+            if (a.z) v.load(rz, a.z, a.ldz, t);
+            rB.load(a.Bm, a.ldB, l, v, t);
+            rC.load(a.Cm, a.ldC, l, v, t);
+            l.load(h, a, a.tile, tile);
+            pair_t s[NP];
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+                s[k] = l.in ? *reinterpret_cast<const pair_t *>(a.tstep + tile * a.P + l.c0 + l.pair(k)) : twice(-1.f);
+            float s0, s1;
+            upk(s[0], s0, s1);
+            if (s0 >= 0.f) {
+                States<K> in;
+                l.load(in, a, a.seg, l.seg);
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) h.v[n][k] = fma2(exp2_2(mul2(d[k], A.v[n][k])), in.v[n][k], h.v[n][k]);
+                    for (int k = 0; k < NP; ++k) h.v[n][k] = fma2(exp2_2(mul2(s[k], A.v[n][k])), in.v[n][k], h.v[n][k]);
             }
-        }
-        {
-            Raw4<T> rx[K::QPL], rdt[K::QPL], rg[K::QPL], rz[K::QPL];
-            Maps<T, N> rB, rC;
-            v.load(rx, a.x, a.ldx, l, t);
-            v.load(rdt, a.dt, a.lddt, l, t);
-            v.load(rg, a.go, a.ldy, l, t);
-            if (a.z) v.load(rz, a.z, a.ldz, l, t);
-            rB.load(a.Bm, a.ldB, l, t);
-            rC.load(a.Cm, a.ldC, l, t);
             __syncwarp();
-            stage_steps<T, N>(l, v, t, rx, rdt, ds, us);
-            stage_cotangent<T, N>(a, v, rg, rz, gs);
+            stage_steps<T, K>(v, rx, rdt, ds, us);
+            stage_cotangent<T, K>(a, v, rg, rz, gs);
             rB.stage(l, Bs);
             rC.stage(l, Cs);
             __syncwarp();
         }
-        auto begin = [&](int i, Quad &x) {                          // the state before a sequence's first token
-            const int64_t b = mk.of(i);
-            if (a.s0) x.load<N>(l.of(a, a.s0, b), l.in);
-            else x.fill(0.f);
-        };
-        auto keep = [&](int g, const Quad &x) {
+        auto keep = [&](int g, const States<K> &x) {
 #pragma unroll
             for (int n = 0; n < 4; ++n)
                 *reinterpret_cast<ulonglong2 *>(ck + ((g * 4 + n) * 32 + l.lane) * 4) = make_ulonglong2(x.v[n][0], x.v[n][1]);
         };
         keep(0, h);
+#pragma unroll 1
         for (int g = 1; g < K::TT / G; ++g) {
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 const int i = (g - 1) * G + j;
-                if (mk.first >> i & 1u) begin(i, h);
-                Token<N> k;
+                Token<K> k;
                 k.load(ds, us, Bs, l, i);
-                advance<false>(A, h, nullptr, k);
+                if (mk.first >> i & 1u) begin_sequence(a, l, mk.of(i), h);
+                advance<false>(A, h, &h, k);
             }
             keep(g, h);
         }
-        for (int g = K::TT / G - 1; g >= 0; --g) {
-            Quad hp[G], ea[G];                                      // the state before each token, its decay
+        auto group = [&](auto events, int g) {
+            States<K> hp[G + 1], ea[G];                             // the state before each token, its decay
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const ulonglong2 x = lds2(ck + ((g * 4 + n) * 32 + l.lane) * 4);
-                h.v[n][0] = x.x;
-                h.v[n][1] = x.y;
+                hp[0].v[n][0] = x.x;
+                hp[0].v[n][1] = x.y;
             }
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 const int i = g * G + j;
-                if (mk.first >> i & 1u) begin(i, h);
-                hp[j] = h;
-                Token<N> k;
+                Token<K> k;
                 k.load(ds, us, Bs, l, i);
-                advance<true>(A, h, &ea[j], k);
+                if (events && (mk.first >> i & 1u)) begin_sequence(a, l, mk.of(i), hp[j]);
+                hp[j + 1] = hp[j];
+                advance<true>(A, hp[j + 1], &ea[j], k);
             }
 #pragma unroll
             for (int j = G - 1; j >= 0; --j) {
                 const int i = g * G + j;
-                const float *Bi = Bs + (i * N + l.nq * 4) * 2, *Ci = Cs + (i * N + l.nq * 4) * 2;
-                const ulonglong2 d2 = lds2(ds + i * K::CW + l.cq * 4), u2 = lds2(us + i * K::CW + l.cq * 4);
-                const ulonglong2 g2 = lds2(gs + i * K::CW + l.cq * 4), b0 = lds2(Bi), b1 = lds2(Bi + 4), c0 = lds2(Ci), c1 = lds2(Ci + 4);
-                const pair_t d[2] = {d2.x, d2.y}, u[2] = {u2.x, u2.y}, gg[2] = {g2.x, g2.y};
-                const pair_t B[4] = {b0.x, b0.y, b1.x, b1.y}, C[4] = {c0.x, c0.y, c1.x, c1.y};
-                if (mk.last >> i & 1u) {
+                Token<K> k;
+                pair_t gg[NP];
+                float C[4];
+                k.load(ds, us, Bs, l, i);
+                l.row(gg, gs + i * K::CW);
+                l.maps(C, Cs + i * N);
+                if (events && (mk.last >> i & 1u)) {
                     const int64_t b = mk.of(i);
-                    if (a.ds1) e.load<N>(l.of(a, a.ds1, b), l.in);
+                    if (a.ds1) l.load(e, a, a.ds1, b);
                     else e.fill(0.f);
                 }
-                const pair_t zero = pk(0.f, 0.f);
-                pair_t vv[2] = {zero, zero}, mb[2] = {zero, zero}, sa[2] = {zero, zero};
+                const pair_t zero = twice(0.f);
+                pair_t vv[NP], mb[NP], sa[NP];
+#pragma unroll
+                for (int c = 0; c < NP; ++c) vv[c] = mb[c] = sa[c] = zero;
                 float dB[4], dC[4];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     pair_t xb = zero, xc = zero;
+                    const pair_t Bn = twice(k.B[n]), Cn = twice(C[n]);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        // the state after the token; the next one's is another sequence's where that begins
-                        const pair_t hn = fma2(ea[j].v[n][k], hp[j].v[n][k], mul2(u[k], B[n]));
-                        const pair_t m = fma2(gg[k], C[n], e.v[n][k]);
-                        vv[k] = fma2(C[n], hn, vv[k]);
-                        xc = fma2(gg[k], hn, xc);
-                        xb = fma2(u[k], m, xb);
-                        mb[k] = fma2(m, B[n], mb[k]);
-                        e.v[n][k] = mul2(ea[j].v[n][k], m);
-                        const pair_t w = mul2(e.v[n][k], hp[j].v[n][k]);
-                        dA.v[n][k] = fma2(w, d[k], dA.v[n][k]);
-                        sa[k] = fma2(w, A.v[n][k], sa[k]);
+                    for (int c = 0; c < NP; ++c) {
+                        // the state after the token: the next one's, but where another sequence begins there
+                        const pair_t hn = events ? fma2(ea[j].v[n][c], hp[j].v[n][c], mul2(k.u[c], Bn)) : hp[j + 1].v[n][c];
+                        const pair_t m = fma2(gg[c], Cn, e.v[n][c]);
+                        vv[c] = fma2(Cn, hn, vv[c]);
+                        xc = fma2(gg[c], hn, xc);
+                        xb = fma2(k.u[c], m, xb);
+                        mb[c] = fma2(m, Bn, mb[c]);
+                        e.v[n][c] = mul2(ea[j].v[n][c], m);
+                        const pair_t w = mul2(e.v[n][c], hp[j].v[n][c]);
+                        dA.v[n][c] = fma2(w, k.d[c], dA.v[n][c]);
+                        sa[c] = fma2(w, A.v[n][c], sa[c]);
                     }
                     float x, y;
                     upk(xb, x, y);
@@ -678,61 +764,73 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_grad(const SsmArgs a, int64_t 
                     upk(xc, x, y);
                     dC[n] = x + y;
                 }
-                *reinterpret_cast<float4 *>(bc + (j * 2 + 0) * 128 + l.cq * N + l.nq * 4) = make_float4(dB[0], dB[1], dB[2], dB[3]);
-                *reinterpret_cast<float4 *>(bc + (j * 2 + 1) * 128 + l.cq * N + l.nq * 4) = make_float4(dC[0], dC[1], dC[2], dC[3]);
-                *reinterpret_cast<ulonglong2 *>(ch + (j * 3 + 0) * 128 + l.nq * K::CW + l.cq * 4) = make_ulonglong2(mb[0], mb[1]);
-                *reinterpret_cast<ulonglong2 *>(ch + (j * 3 + 1) * 128 + l.nq * K::CW + l.cq * 4) = make_ulonglong2(sa[0], sa[1]);
-                *reinterpret_cast<ulonglong2 *>(ch + (j * 3 + 2) * 128 + l.nq * K::CW + l.cq * 4) = make_ulonglong2(vv[0], vv[1]);
-                if (mk.first >> i & 1u) {
+                if (events && (mk.first >> i & 1u)) {
                     const int64_t b = mk.of(i);
-                    if (a.ds0) e.store<N>(l.of(a, a.ds0, b), l.in);
+                    if (a.ds0) l.store(e, a, a.ds0, b);
                     e.fill(0.f);
                 }
-            }
-            __syncwarp();
-            // the group's sums: over states into ds, us, gs (done with), over channels into ws
-            for (int x = l.lane; x < G * 3 * K::CQ; x += 32) {
-                const int q = x % K::CQ, r = x / K::CQ, kind = r % 3, j = r / 3;
-                const float4 *p = reinterpret_cast<const float4 *>(ch + r * 128 + q * 4);
-                float4 s = p[0];
+                // Sums over states over what is done with: d by m B, u by A e h, g by v.  Every lane has read row i, as
+                // the exchanges need all lanes' sums.
+                float o[3][K::OUT];
+                l.sums(mb, o[0]);
+                l.sums(sa, o[1]);
+                l.sums(vv, o[2]);
+                l.put_sums(ds + i * K::CW, o[0]);
+                l.put_sums(us + i * K::CW, o[1]);
+                l.put_sums(gs + i * K::CW, o[2]);
+                // dB and dC over the groups of channels: half of the lanes keep the one, half the other
+                float q[4];
+                const bool odd = l.cq & 1;
 #pragma unroll
-                for (int y = 1; y < K::NQ; ++y) s = s + p[y * K::CW / 4];
-                float *to = kind == 0 ? ds : kind == 1 ? us : gs;
-                *reinterpret_cast<float4 *>(to + (g * G + j) * K::CW + q * 4) = s;
+                for (int n = 0; n < 4; ++n) q[n] = (odd ? dC[n] : dB[n]) + __shfl_xor_sync(~0u, odd ? dB[n] : dC[n], K::NQ);
+                float *to = ws + i * 2 * N + (odd ? N : 0) + l.nq * 4;
+                if (K::CQ == 2) {
+                    put4(to, make_float4(q[0], q[1], q[2], q[3]));
+                } else {
+                    const bool b2 = l.cq & 2;
+                    float r0 = (b2 ? q[2] : q[0]) + __shfl_xor_sync(~0u, b2 ? q[0] : q[2], 2 * K::NQ);
+                    float r1 = (b2 ? q[3] : q[1]) + __shfl_xor_sync(~0u, b2 ? q[1] : q[3], 2 * K::NQ);
+                    to += b2 ? 2 : 0;
+                    if (K::CQ == 4) {
+                        *reinterpret_cast<float2 *>(to) = make_float2(r0, r1);
+                    } else {
+                        const bool b4 = l.cq & 4;
+                        float r = (b4 ? r1 : r0) + __shfl_xor_sync(~0u, b4 ? r0 : r1, 4 * K::NQ & 31);
+                        if (K::CQ == 16) r += __shfl_xor_sync(~0u, r, 8 * K::NQ & 31);
+                        if (K::CQ == 8 || l.cq < 8) to[b4 ? 1 : 0] = r;
+                    }
+                }
             }
-            for (int x = l.lane; x < G * 2 * K::NQ; x += 32) {
-                const int q = x % K::NQ, r = x / K::NQ, kind = r % 2, j = r / 2;
-                const float4 *p = reinterpret_cast<const float4 *>(bc + r * 128 + q * 4);
-                float4 s = p[0];
-#pragma unroll
-                for (int y = 1; y < K::CQ; ++y) s = s + p[y * N / 4];
-                *reinterpret_cast<float4 *>(ws + (g * G + j) * 2 * N + kind * N + q * 4) = s;
-            }
-            __syncwarp();
+        };
+#pragma unroll 1
+        for (int g = K::TT / G - 1; g >= 0; --g) {
+            // the token behind a group may begin another sequence: that only touches its own state
+            if ((mk.first | mk.last) >> (g * G) & ((1u << G) - 1)) group(std::true_type(), g);
+            else group(std::false_type(), g);
         }
+        __syncwarp();
         // the tile's gradients of what each channel reads
         {
             Raw4<T> rx[K::QPL], rdt[K::QPL], rz[K::QPL], rg[K::QPL];
-            v.load(rx, a.x, a.ldx, l, t);
-            v.load(rdt, a.dt, a.lddt, l, t);
-            v.load(rg, a.go, a.ldy, l, t);
-            if (a.z) v.load(rz, a.z, a.ldz, l, t);
+            v.load(rx, a.x, a.ldx, t);
+            v.load(rdt, a.dt, a.lddt, t);
+            v.load(rg, a.go, a.ldy, t);
+            if (a.z) v.load(rz, a.z, a.ldz, t);
 #pragma unroll
             for (int j = 0; j < K::QPL; ++j) {
-                if (!v.ok(l, t, j)) continue;
-                const int64_t at = t + v.tok(j);
+                if (!v.ok(j)) continue;
                 const int sh = v.tok(j) * K::CW + v.cl;
                 const float4 x = rx[j].get(), raw = rdt[j].get() + v.bias, mb = get4(ds + sh);
                 float4 g = rg[j].get();
                 if (a.z) {
                     // v z s: its derivative for z is v s (1 + z (1 - s))
                     const float4 z = rz[j].get(), s = sigmoid4(z), val = fma4(v.D, x, get4(gs + sh));
-                    st4(static_cast<T *>(a.dz) + at * a.ldz + v.c, g * val * s * fma4(z, f4(1.f) - s, f4(1.f)));
+                    st4(v.out(a.dz, a.ldz, t, j), g * val * s * fma4(z, f4(1.f) - s, f4(1.f)));
                     g = g * (z * s);
                 }
                 const float4 ddt = fma4(x, mb, f4(SEQ_LN2) * get4(us + sh)) * sigmoid4(raw);
-                st4(static_cast<T *>(a.dx) + at * a.ldx + v.c, fma4(softplus4(raw), mb, v.D * g));
-                st4(static_cast<T *>(a.ddt) + at * a.lddt + v.c, ddt);
+                st4(v.out(a.dx, a.ldx, t, j), fma4(softplus4(raw), mb, v.D * g));
+                st4(v.out(a.ddt, a.lddt, t, j), ddt);
                 dD = fma4(g, x, dD);
                 db = db + ddt;
             }
@@ -742,17 +840,17 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_grad(const SsmArgs a, int64_t 
         for (int x = threadIdx.x; x < K::TT * N / 2; x += 32 * WPB) {
             const int tok = x / (N / 2), q = x % (N / 2) * 4;
             const float *p = sm + (M::ALL - M::SUM) + tok * 2 * N + q;
-            float4 s = *reinterpret_cast<const float4 *>(p);
+            float4 s = get4(p);
 #pragma unroll
-            for (int w = 1; w < WPB; ++w) s = s + *reinterpret_cast<const float4 *>(p + w * M::ALL);
-            if (t + tok < l.t1) *reinterpret_cast<float4 *>(a.bc + ((l.col * a.q.rows + t + tok) * 2 * N + q)) = s;
+            for (int w = 1; w < WPB; ++w) s = s + get4(p + w * M::ALL);
+            if (t + tok < l.t1) put4(a.bc + ((l.col * a.q.rows + t + tok) * 2 * N + q), s);
         }
         __syncthreads();
     }
     float *par = a.par + l.seg * a.P * (N + 2);
-    dA.store<N>(par + l.state(a), l.in);
+    l.store(dA, a, par, 0);
 #pragma unroll
-    for (int w = K::CQ; w < 32; w <<= 1) {
+    for (int w = K::QR; w < 32; w <<= 1) {
         auto join = [&](float4 &x) {
             x = x + make_float4(__shfl_xor_sync(~0u, x.x, w), __shfl_xor_sync(~0u, x.y, w), __shfl_xor_sync(~0u, x.z, w),
                                 __shfl_xor_sync(~0u, x.w, w));
@@ -760,7 +858,7 @@ __global__ __launch_bounds__(32 * WPB) void k_ssm_grad(const SsmArgs a, int64_t 
         join(dD);
         join(db);
     }
-    if (l.lane < K::CQ && v.in) {
+    if (l.lane < K::QR && v.in) {
         put4(par + int64_t(a.P) * N + v.c, dD);
         put4(par + int64_t(a.P) * (N + 1) + v.c, db);
     }
@@ -858,18 +956,24 @@ cudaError_t pick(int N, bool bf16, F f) {
     return bf16 ? sizes(__nv_bfloat16()) : sizes(0.f);
 }
 
-int64_t columns(const SsmArgs &a) { return seq_div(a.P, WPB * warp_channels(a.N)); }
+// Two channels a thread, not four, for a prompt so short that its walk is a matter of latency, unless its
+// channels fill the SMs by themselves.
+bool brief(const SsmArgs &a) { return a.q.rows <= 256 && seq_div(a.P, warp_channels(a.N, 2)) < 608; }
+int64_t columns(const SsmArgs &a, bool bwd) {
+    return bwd ? seq_div(a.P, WPB * warp_channels(a.N, 2)) : brief(a) ? seq_div(a.P, warp_channels(a.N, 1))
+                                                                     : seq_div(a.P, WPB * warp_channels(a.N, 2));
+}
 // blocks that look for sequences without tokens: only packed ones may have any, or all of them have none
 int64_t lookers(const SsmArgs &a, const float *out) {
     return out && a.q.B && (a.q.off || a.q.rows == 0) ? std::min<int64_t>(a.q.B, 152) : 0;
 }
 
 template <auto Kern>
-cudaError_t go(KernelId id, int64_t blocks, size_t smem, cudaStream_t st, const SsmArgs &a, int64_t cols) {
+cudaError_t go(KernelId id, int64_t blocks, int warps, size_t floats, cudaStream_t st, const SsmArgs &a, int64_t cols) {
     const cudaError_t e = allow_smem<Kern>();
     if (e != cudaSuccess) return e;
     ProfScope p(id, st);
-    Kern<<<unsigned(blocks), 32 * WPB, smem, st>>>(a, cols);
+    Kern<<<unsigned(blocks), 32 * warps, warps * floats * sizeof(float), st>>>(a, cols);
     return cudaGetLastError();
 }
 
@@ -882,12 +986,11 @@ cudaError_t carry(const SsmArgs &a, int dirs, cudaStream_t st) {
 }  // namespace
 
 size_t ssm_plan(SsmArgs &a, bool bwd, void *base) {
-    const int64_t tt = tile_tokens(a.N), cols = columns(a), tiles = seq_div(a.q.rows, tt);
-    // one turn of the machine: 3 blocks an SM forwards, 2 backwards; short prompts stay in one segment, as
-    // a walk of 256 tokens costs less than two more launches
+    const int64_t tt = tile_tokens(a.N, 2), cols = columns(a, bwd), tiles = seq_div(a.q.rows, tt);
+    // one turn of the machine: 3 blocks an SM forwards, 2 backwards, and 64 tokens a segment at least (32 backwards); a
+    // short prompt stays in one segment, as its walk costs less than two more launches
     const int64_t want = std::max<int64_t>(1, 152 * (bwd ? 2 : 3) / cols);
-    const int64_t least = bwd ? 2 : a.q.rows <= 256 ? 16 : 4;          // tiles of a segment
-    const int64_t per = std::max(least, seq_div(tiles, want));
+    const int64_t per = !bwd && brief(a) ? std::max<int64_t>(tiles, 1) : std::max((bwd ? 32 : 64) / tt, seq_div(tiles, want));
     a.seglen = per * tt;
     a.nseg = seq_div(a.q.rows, a.seglen);
     char *p = static_cast<char *>(base);
@@ -912,32 +1015,33 @@ size_t ssm_plan(SsmArgs &a, bool bwd, void *base) {
 }
 
 cudaError_t launch_ssm_fwd(const SsmArgs &a, bool bf16, cudaStream_t st) {
-    const int64_t cols = columns(a), look = lookers(a, a.s1);
+    const int64_t cols = columns(a, false), look = lookers(a, a.s1);
     return pick(a.N, bf16, [&](auto t, auto n) {
         typedef decltype(t) T;
         constexpr int N = decltype(n)::value;
-        typedef Tile<N> K;
+        typedef Tile<N, 2, true> K;
         if (a.nseg > 1) {
-            LIN_CUDA((go<k_ssm_state<T, N, false>>(K_SSM_STATE, a.nseg * cols, WPB * (2 * K::X + K::S) * 4, st, a, cols)));
+            LIN_CUDA((go<k_ssm_state<T, N, false>>(K_SSM_STATE, a.nseg * cols, WPB, state_floats<K, false>(), st, a, cols)));
             LIN_CUDA(carry(a, 1, st));
         }
         if (a.nseg * cols + look == 0) return cudaSuccess;
-        return go<k_ssm_out<T, N>>(K_SSM_OUT, a.nseg * cols + look, WPB * (2 * K::X + 2 * K::S + K::TT * 128) * 4, st, a, cols);
+        if (brief(a)) return go<k_ssm_out<T, N, 1>>(K_SSM_OUT, a.nseg * cols + look, 1, out_floats<Tile<N, 1, true>>(), st, a, cols);
+        return go<k_ssm_out<T, N, 2>>(K_SSM_OUT, a.nseg * cols + look, WPB, out_floats<K>(), st, a, cols);
     });
 }
 
 cudaError_t launch_ssm_bwd(const SsmArgs &a, bool bf16, cudaStream_t st) {
-    const int64_t cols = columns(a), look = lookers(a, a.ds0);
+    const int64_t cols = columns(a, true), look = lookers(a, a.ds0);
     return pick(a.N, bf16, [&](auto t, auto n) {
         typedef decltype(t) T;
         constexpr int N = decltype(n)::value;
-        typedef Tile<N> K;
+        typedef Tile<N, 2, false> K;
         if (a.nseg) {
-            LIN_CUDA((go<k_ssm_state<T, N, true>>(K_SSM_STATE, a.nseg * cols, WPB * (3 * K::X + 2 * K::S) * 4, st, a, cols)));
+            LIN_CUDA((go<k_ssm_state<T, N, true>>(K_SSM_STATE, a.nseg * cols, WPB, state_floats<K, true>(), st, a, cols)));
             LIN_CUDA(carry(a, 2, st));
         }
         if (a.nseg * cols + look)
-            LIN_CUDA((go<k_ssm_grad<T, N>>(K_SSM_GRAD, a.nseg * cols + look, WPB * GradSm<N>::ALL * 4, st, a, cols)));
+            LIN_CUDA((go<k_ssm_grad<T, N>>(K_SSM_GRAD, a.nseg * cols + look, WPB, GradSm<N>::ALL, st, a, cols)));
         const int64_t maps = seq_div(a.q.rows * (N / 2), 256), rest = seq_div(int64_t(a.P) * (N + 2), 256);
         ProfScope p(K_SSM_JOIN, st);
         k_ssm_join<T><<<unsigned(maps + rest), 256, 0, st>>>(a, cols, maps);
