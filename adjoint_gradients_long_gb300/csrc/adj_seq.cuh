@@ -44,6 +44,10 @@ struct Raw8<float> {
         a = __ldg(reinterpret_cast<const float4 *>(p));
         b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
     }
+    __device__ __forceinline__ void load_own(const float *p) {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
+    }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
@@ -53,6 +57,7 @@ template <>
 struct Raw8<__nv_bfloat16> {
     uint4 u;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void load_own(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -70,7 +75,7 @@ template <>
 struct Raw4<float> {
     float4 v;
     __device__ __forceinline__ void load(const float *p) { v = __ldg(reinterpret_cast<const float4 *>(p)); }
-    __device__ __forceinline__ void load_own(const float *p) { v = *reinterpret_cast<const float4 *>(p); }   // written by this launch too
+    __device__ __forceinline__ void load_own(const float *p) { v = *reinterpret_cast<const float4 *>(p); }   // not by way of the read-only cache
     __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float4 *>(p) = v; }
     __device__ __forceinline__ void zero() { v = f4(0.f); }
     __device__ __forceinline__ float4 get() const { return v; }

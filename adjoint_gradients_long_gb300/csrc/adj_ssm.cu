@@ -21,7 +21,7 @@
 // k_ssm_out or k_ssm_grad walk the segments again from there.  One segment needs the last alone.
 // The backward pass keeps the state at the start of every tile: the one that k_ssm_state makes from
 // zero, plus what enters the segment times exp(A sum d), so no third walk is needed; inside a
-// tile the states are formed forwards, kept for four tokens at a time, and used backwards.
+// tile the states are formed forwards, kept for two tokens at a time, and used backwards.
 //
 // Sequences may begin and end anywhere: a tile has a mask of the tokens that begin one (there the state
 // is loaded) and of those that end one (there it is stored).  Tokens of no sequence are staged as
@@ -36,7 +36,7 @@ namespace adj {
 namespace {
 
 constexpr int WPB = 4;                  // warps of a block, side by side in channels (1 for short prompts)
-constexpr int G = 4;                    // tokens of a group: walked without a branch, kept in registers backwards
+constexpr int G = 4;                    // tokens of a group, walked without a branch
 
 // SWAP: neighbouring quads of states hold their channels in opposite order
 template <int N_, int NP_, bool SWAP_>
@@ -622,16 +622,19 @@ __global__ __launch_bounds__(32 * WPB, 3) void k_ssm_out(const SsmArgs a, int64_
 template <int N>
 struct GradSm {                         // floats of a warp's part
     typedef Tile<N, 2, true> K;
-    static constexpr int CK = K::TT / G * 512;                      // states at every G-th token, [.][4][32] x 4
+    // tokens of a group, whose states and decays stay in registers: four spill (300 bytes, 672 us against 653 for the
+    // training batch below), but with 64 states the room for those of every second token is not there
+    static constexpr int GB = N == 64 ? 4 : 2;
+    static constexpr int CK = K::TT / GB * 512;                     // states at every GB-th token, [.][4][32] x 4
     static constexpr int SUM = K::TT * 2 * N;                       // dB and dC of a tile over the warp's channels
-    static constexpr int ALL = 3 * K::X + 2 * K::S + CK + SUM;
+    static constexpr int ALL = 4 * K::X + 2 * K::S + CK + SUM;
 };
 
 template <class T, int N>
 __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64_t cols) {
     typedef Tile<N, 2, true> K;
     typedef GradSm<N> M;
-    constexpr int NP = K::NP;
+    constexpr int NP = K::NP, GB = M::GB, RN = K::CQ == 2 ? 4 : K::CQ == 4 ? 2 : 1;
     extern __shared__ __align__(16) float sm[];
     const int64_t work = a.nseg * cols;
     if (int64_t(blockIdx.x) >= work) {
@@ -640,7 +643,7 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
     }
     const Lane<K> l(a, blockIdx.x, cols);
     Mine<T, K> v(a, l);
-    float *ds = sm + l.warp * M::ALL, *us = ds + K::X, *gs = us + K::X, *Bs = gs + K::X, *Cs = Bs + K::S;
+    float *ds = sm + l.warp * M::ALL, *us = ds + K::X, *gs = us + K::X, *ms = gs + K::X, *Bs = ms + K::X, *Cs = Bs + K::S;
     float *ck = Cs + K::S, *ws = ck + M::CK;
     const States<K> A = decays<K>(a, l);
     States<K> e, dA;                                                // e: what reaches the state before
@@ -657,6 +660,12 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
         {
             Raw4<T> rx[K::QPL], rdt[K::QPL], rg[K::QPL], rz[K::QPL];
             Maps<T, K> rB, rC;
+            States<K> in;
+            pair_t s[NP];
+            l.load(in, a, a.seg, l.seg);
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+                s[k] = l.in ? *reinterpret_cast<const pair_t *>(a.tstep + tile * a.P + l.c0 + l.pair(k)) : twice(-1.f);
             v.at(l, t);
             v.load(rx, a.x, a.ldx, t);
             v.load(rdt, a.dt, a.lddt, t);
@@ -665,25 +674,19 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
             rB.load(a.Bm, a.ldB, l, v, t);
             rC.load(a.Cm, a.ldC, l, v, t);
             l.load(h, a, a.tile, tile);
-            pair_t s[NP];
-#pragma unroll
-            for (int k = 0; k < NP; ++k)
-                s[k] = l.in ? *reinterpret_cast<const pair_t *>(a.tstep + tile * a.P + l.c0 + l.pair(k)) : twice(-1.f);
-            float s0, s1;
-            upk(s[0], s0, s1);
-            if (s0 >= 0.f) {
-                States<K> in;
-                l.load(in, a, a.seg, l.seg);
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int k = 0; k < NP; ++k) h.v[n][k] = fma2(exp2_2(mul2(s[k], A.v[n][k])), in.v[n][k], h.v[n][k]);
-            }
             __syncwarp();
             stage_steps<T, K>(v, rx, rdt, ds, us);
             stage_cotangent<T, K>(a, v, rg, rz, gs);
             rB.stage(l, Bs);
             rC.stage(l, Cs);
+            float s0, s1;
+            upk(s[0], s0, s1);
+            if (s0 >= 0.f) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) h.v[n][k] = fma2(exp2_2(mul2(s[k], A.v[n][k])), in.v[n][k], h.v[n][k]);
+            }
             __syncwarp();
         }
         auto keep = [&](int g, const States<K> &x) {
@@ -693,10 +696,10 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
         };
         keep(0, h);
 #pragma unroll 1
-        for (int g = 1; g < K::TT / G; ++g) {
+        for (int g = 1; g < K::TT / GB; ++g) {
 #pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const int i = (g - 1) * G + j;
+            for (int j = 0; j < GB; ++j) {
+                const int i = (g - 1) * GB + j;
                 Token<K> k;
                 k.load(ds, us, Bs, l, i);
                 if (mk.first >> i & 1u) begin_sequence(a, l, mk.of(i), h);
@@ -705,7 +708,8 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
             keep(g, h);
         }
         auto group = [&](auto events, int g) {
-            States<K> hp[G + 1], ea[G];                             // the state before each token, its decay
+            States<K> hp[GB], ea[GB];                               // the state before each token, its decay
+            float o[GB][3][K::OUT], r[GB][RN];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const ulonglong2 x = lds2(ck + ((g * 4 + n) * 32 + l.lane) * 4);
@@ -713,17 +717,24 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
                 hp[0].v[n][1] = x.y;
             }
 #pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const int i = g * G + j;
+            for (int j = 0; j < GB; ++j) {
+                const int i = g * GB + j;
                 Token<K> k;
                 k.load(ds, us, Bs, l, i);
                 if (events && (mk.first >> i & 1u)) begin_sequence(a, l, mk.of(i), hp[j]);
-                hp[j + 1] = hp[j];
-                advance<true>(A, hp[j + 1], &ea[j], k);
+                if (j + 1 < GB) {
+                    hp[j + 1] = hp[j];
+                    advance<true>(A, hp[j + 1], &ea[j], k);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int c = 0; c < NP; ++c) ea[j].v[n][c] = exp2_2(fma2(k.d[c], A.v[n][c], twice(EXP_UP)));
+                }
             }
 #pragma unroll
-            for (int j = G - 1; j >= 0; --j) {
-                const int i = g * G + j;
+            for (int j = GB - 1; j >= 0; --j) {
+                const int i = g * GB + j;
                 Token<K> k;
                 pair_t gg[NP];
                 float C[4];
@@ -746,8 +757,8 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
                     const pair_t Bn = twice(k.B[n]), Cn = twice(C[n]);
 #pragma unroll
                     for (int c = 0; c < NP; ++c) {
-                        // the state after the token: the next one's, but where another sequence begins there
-                        const pair_t hn = events ? fma2(ea[j].v[n][c], hp[j].v[n][c], mul2(k.u[c], Bn)) : hp[j + 1].v[n][c];
+                        // the state after the token: the next one's, but behind the group and where another sequence begins
+                        const pair_t hn = events || j == GB - 1 ? fma2(ea[j].v[n][c], hp[j].v[n][c], mul2(k.u[c], Bn)) : hp[(j + 1) % GB].v[n][c];
                         const pair_t m = fma2(gg[c], Cn, e.v[n][c]);
                         vv[c] = fma2(Cn, hn, vv[c]);
                         xc = fma2(gg[c], hn, xc);
@@ -769,43 +780,49 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
                     if (a.ds0) l.store(e, a, a.ds0, b);
                     e.fill(0.f);
                 }
-                // Sums over states over what is done with: d by m B, u by A e h, g by v.  Every lane has read row i, as
-                // the exchanges need all lanes' sums.
-                float o[3][K::OUT];
-                l.sums(mb, o[0]);
-                l.sums(sa, o[1]);
-                l.sums(vv, o[2]);
-                l.put_sums(ds + i * K::CW, o[0]);
-                l.put_sums(us + i * K::CW, o[1]);
-                l.put_sums(gs + i * K::CW, o[2]);
-                // dB and dC over the groups of channels: half of the lanes keep the one, half the other
+                // Sums over states, and of dB and dC over the groups of channels: half of the lanes keep the one,
+                // half the other, and so on
+                l.sums(mb, o[j][0]);
+                l.sums(sa, o[j][1]);
+                l.sums(vv, o[j][2]);
                 float q[4];
-                const bool odd = l.cq & 1;
+                const bool odd = l.cq & 1, b2 = l.cq & 2, b4 = l.cq & 4;
 #pragma unroll
                 for (int n = 0; n < 4; ++n) q[n] = (odd ? dC[n] : dB[n]) + __shfl_xor_sync(~0u, odd ? dB[n] : dC[n], K::NQ);
-                float *to = ws + i * 2 * N + (odd ? N : 0) + l.nq * 4;
                 if (K::CQ == 2) {
-                    put4(to, make_float4(q[0], q[1], q[2], q[3]));
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) r[j][n % RN] = q[n];
                 } else {
-                    const bool b2 = l.cq & 2;
-                    float r0 = (b2 ? q[2] : q[0]) + __shfl_xor_sync(~0u, b2 ? q[0] : q[2], 2 * K::NQ);
-                    float r1 = (b2 ? q[3] : q[1]) + __shfl_xor_sync(~0u, b2 ? q[1] : q[3], 2 * K::NQ);
-                    to += b2 ? 2 : 0;
+                    const float r0 = (b2 ? q[2] : q[0]) + __shfl_xor_sync(~0u, b2 ? q[0] : q[2], 2 * K::NQ & 31);
+                    const float r1 = (b2 ? q[3] : q[1]) + __shfl_xor_sync(~0u, b2 ? q[1] : q[3], 2 * K::NQ & 31);
                     if (K::CQ == 4) {
-                        *reinterpret_cast<float2 *>(to) = make_float2(r0, r1);
+                        r[j][0] = r0;
+                        r[j][1 % RN] = r1;
                     } else {
-                        const bool b4 = l.cq & 4;
-                        float r = (b4 ? r1 : r0) + __shfl_xor_sync(~0u, b4 ? r0 : r1, 4 * K::NQ & 31);
-                        if (K::CQ == 16) r += __shfl_xor_sync(~0u, r, 8 * K::NQ & 31);
-                        if (K::CQ == 8 || l.cq < 8) to[b4 ? 1 : 0] = r;
+                        r[j][0] = (b4 ? r1 : r0) + __shfl_xor_sync(~0u, b4 ? r0 : r1, 4 * K::NQ & 31);
+                        if (K::CQ == 16) r[j][0] += __shfl_xor_sync(~0u, r[j][0], 8 * K::NQ & 31);
                     }
                 }
             }
+            // To shared memory when the group is done, so that no store holds up a token's loads: m B, and over what is
+            // done with, A e h (u's rows) and v (g's).  Every lane has read those rows, as the exchanges need
+            // all lanes' sums.
+#pragma unroll
+            for (int j = 0; j < GB; ++j) {
+                const int i = g * GB + j;
+                l.put_sums(ms + i * K::CW, o[j][0]);
+                l.put_sums(us + i * K::CW, o[j][1]);
+                l.put_sums(gs + i * K::CW, o[j][2]);
+                float *to = ws + i * 2 * N + (l.cq & 1 ? N : 0) + l.nq * 4;
+                if (K::CQ == 2) put4(to, make_float4(r[j][0], r[j][1 % RN], r[j][2 % RN], r[j][3 % RN]));
+                else if (K::CQ == 4) *reinterpret_cast<float2 *>(to + (l.cq & 2)) = make_float2(r[j][0], r[j][1 % RN]);
+                else if (l.cq < 8) to[(l.cq & 2) + (l.cq >> 2)] = r[j][0];
+            }
         };
 #pragma unroll 1
-        for (int g = K::TT / G - 1; g >= 0; --g) {
+        for (int g = K::TT / GB - 1; g >= 0; --g) {
             // the token behind a group may begin another sequence: that only touches its own state
-            if ((mk.first | mk.last) >> (g * G) & ((1u << G) - 1)) group(std::true_type(), g);
+            if ((mk.first | mk.last) >> (g * GB) & ((1u << GB) - 1)) group(std::true_type(), g);
             else group(std::false_type(), g);
         }
         __syncwarp();
@@ -820,7 +837,7 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
             for (int j = 0; j < K::QPL; ++j) {
                 if (!v.ok(j)) continue;
                 const int sh = v.tok(j) * K::CW + v.cl;
-                const float4 x = rx[j].get(), raw = rdt[j].get() + v.bias, mb = get4(ds + sh);
+                const float4 x = rx[j].get(), raw = rdt[j].get() + v.bias, mb = get4(ms + sh);
                 float4 g = rg[j].get();
                 if (a.z) {
                     // v z s: its derivative for z is v s (1 + z (1 - s))
@@ -829,7 +846,7 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
                     g = g * (z * s);
                 }
                 const float4 ddt = fma4(x, mb, f4(SEQ_LN2) * get4(us + sh)) * sigmoid4(raw);
-                st4(v.out(a.dx, a.ldx, t, j), fma4(softplus4(raw), mb, v.D * g));
+                st4(v.out(a.dx, a.ldx, t, j), fma4(get4(ds + sh), mb, v.D * g));
                 st4(v.out(a.ddt, a.lddt, t, j), ddt);
                 dD = fma4(g, x, dD);
                 db = db + ddt;
@@ -987,9 +1004,10 @@ cudaError_t carry(const SsmArgs &a, int dirs, cudaStream_t st) {
 
 size_t ssm_plan(SsmArgs &a, bool bwd, void *base) {
     const int64_t tt = tile_tokens(a.N, 2), cols = columns(a, bwd), tiles = seq_div(a.q.rows, tt);
-    // one turn of the machine: 3 blocks an SM forwards, 2 backwards, and 64 tokens a segment at least (32 backwards); a
-    // short prompt stays in one segment, as its walk costs less than two more launches
-    const int64_t want = std::max<int64_t>(1, 152 * (bwd ? 2 : 3) / cols);
+    // whole turns of the machine: 3 blocks an SM, and backwards twice that, three turns of k_ssm_grad's 2 blocks; 64
+    // tokens a segment at least (32 backwards).  A short prompt stays in one segment, as its walk costs
+    // less than two more launches.
+    const int64_t want = std::max<int64_t>(1, 152 * (bwd ? 6 : 3) / cols);
     const int64_t per = !bwd && brief(a) ? std::max<int64_t>(tiles, 1) : std::max((bwd ? 32 : 64) / tt, seq_div(tiles, want));
     a.seglen = per * tt;
     a.nseg = seq_div(a.q.rows, a.seglen);
