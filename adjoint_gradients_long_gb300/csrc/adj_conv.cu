@@ -29,9 +29,31 @@ __device__ __forceinline__ const T *row(const void *p, int64_t i, int64_t ld, in
     return static_cast<const T *>(p) + i * ld + c;
 }
 
+using adj::operator+;                   // beside those of Four
+using adj::sigmoid4;
+
+// Four channels as two packed pairs: a multiply-add takes half the instructions
+struct Four {
+    pair_t a, b;
+    __device__ __forceinline__ Four() {}
+    __device__ __forceinline__ explicit Four(float x) : a(pk(x, x)), b(a) {}
+    __device__ __forceinline__ explicit Four(float4 v) : a(pk(v.x, v.y)), b(pk(v.z, v.w)) {}
+    __device__ __forceinline__ Four(pair_t a_, pair_t b_) : a(a_), b(b_) {}
+    __device__ __forceinline__ float4 get() const {
+        float4 v;
+        upk(a, v.x, v.y);
+        upk(b, v.z, v.w);
+        return v;
+    }
+};
+__device__ __forceinline__ Four operator*(Four x, Four y) { return Four(mul2(x.a, y.a), mul2(x.b, y.b)); }
+__device__ __forceinline__ Four operator+(Four x, Four y) { return Four(add2(x.a, y.a), add2(x.b, y.b)); }
+__device__ __forceinline__ Four fma4(Four x, Four y, Four z) { return Four(fma2(x.a, y.a, z.a), fma2(x.b, y.b, z.b)); }
+__device__ __forceinline__ Four sigmoid4(Four x) { return Four(sigmoid4(x.get())); }
+
 // Weights and bias of four channels; w is [P][W], so theirs are W vectors in a row
 template <int W>
-__device__ __forceinline__ void load_taps(const ConvArgs &a, int c, float4 (&w)[W], float4 &bias) {
+__device__ __forceinline__ void load_taps(const ConvArgs &a, int c, Four (&w)[W], Four &bias) {
     union {
         float4 v[W];
         float f[4 * W];
@@ -39,8 +61,8 @@ __device__ __forceinline__ void load_taps(const ConvArgs &a, int c, float4 (&w)[
 #pragma unroll
     for (int j = 0; j < W; ++j) u.v[j] = __ldg(reinterpret_cast<const float4 *>(a.w + int64_t(c) * W) + j);
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j] = make_float4(u.f[j], u.f[W + j], u.f[2 * W + j], u.f[3 * W + j]);
-    bias = a.bias ? __ldg(reinterpret_cast<const float4 *>(a.bias + c)) : f4(0.f);
+    for (int j = 0; j < W; ++j) w[j] = Four(make_float4(u.f[j], u.f[W + j], u.f[2 * W + j], u.f[3 * W + j]));
+    bias = Four(a.bias ? __ldg(reinterpret_cast<const float4 *>(a.bias + c)) : f4(0.f));
 }
 
 // Entry i of sequence b's list (its state, then its tokens from `begin` on)
@@ -51,6 +73,19 @@ __device__ __forceinline__ Raw4<T> entry(const ConvArgs &a, int64_t b, int64_t b
     else if (a.s0) r.load(row<T>(a.s0, b * (W - 1) + i, a.P, c));
     else r.zero();
     return r;
+}
+
+// Offsets of up to 256 sequences, read by the block together: the search for a run's sequence then waits for
+// shared memory, not five times for L2.  (All threads of the block.)
+constexpr int NEAR = 256;
+__device__ __forceinline__ Seqs near(const Seqs &q, int64_t *offs) {
+    Seqs n = q;
+    if (q.off && q.B <= NEAR) {
+        for (int i = threadIdx.x; i <= int(q.B); i += CT) offs[i] = q.off[i];
+        __syncthreads();
+        n.off = offs;
+    }
+    return n;
 }
 
 struct Place {
@@ -67,31 +102,33 @@ struct Place {
 
 // Blocks below `runs` take tokens, those above write the states after the last tokens.
 template <class T, int W>
-__global__ __launch_bounds__(CT, 3) void k_conv_fwd(const ConvArgs a, int vg, int tr, int64_t runs) {
+__global__ __launch_bounds__(CT, 4) void k_conv_fwd(const ConvArgs a, int vg, int tr, int64_t runs) {
+    __shared__ int64_t offs[NEAR + 1];
+    const Seqs q = near(a.q, offs);
     const Place at(vg, a.P);
     if (!at.in) return;
     const int c = at.c, rg = CT / vg;
     if (int64_t(blockIdx.x) >= runs) {
         const int64_t b = (blockIdx.x - runs) * rg + at.run;
-        if (b >= a.q.B) return;
-        const int64_t begin = a.q.begin(b), n = max(int64_t(0), a.q.end(b) - begin);
+        if (b >= q.B) return;
+        const int64_t begin = q.begin(b), n = max(int64_t(0), q.end(b) - begin);
         for (int i = 0; i < W - 1; ++i)
             entry<T, W>(a, b, begin, n + i, c).store(static_cast<T *>(a.s1) + (b * (W - 1) + i) * a.P + c);
         return;
     }
     int64_t t = (int64_t(blockIdx.x) * rg + at.run) * tr;
-    const int64_t stop = min(t + tr, a.q.rows);
+    const int64_t stop = min(t + tr, q.rows);
     if (t >= stop) return;
-    float4 w[W], bias, x[W];
+    Four w[W], bias, x[W];
     load_taps<W>(a, c, w, bias);
-    if (a.q.off) t = max(t, a.q.at(0));
+    if (q.off) t = max(t, q.at(0));
     while (t < stop) {
-        const int64_t b = a.q.find(t);
+        const int64_t b = q.find(t);
         if (b < 0) return;
-        const int64_t begin = a.q.begin(b), end = min(a.q.end(b), stop);
+        const int64_t begin = q.begin(b), end = min(q.end(b), stop);
         // x[1..W-1]: the W-1 entries before token t
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) x[j + 1] = entry<T, W>(a, b, begin, t - begin + j, c).get();
+        for (int j = 0; j < W - 1; ++j) x[j + 1] = Four(entry<T, W>(a, b, begin, t - begin + j, c).get());
         // pointers and counts inside the run: 64-bit comparisons a token cost more than its arithmetic
         const T *px = row<T>(a.x, t, a.ldx, c);
         T *py = static_cast<T *>(a.y) + t * a.ldy + c;
@@ -101,6 +138,16 @@ __global__ __launch_bounds__(CT, 3) void k_conv_fwd(const ConvArgs a, int vg, in
 #pragma unroll
         for (int u = 0; u < FU; ++u)
             if (u < n) next[u].load(px + u * a.ldx);
+        auto token = [&](const Raw4<T> &in) {
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) x[j] = x[j + 1];
+            x[W - 1] = Four(in.get());
+            Four p = bias;
+#pragma unroll
+            for (int j = 0; j < W; ++j) p = fma4(w[j], x[j], p);
+            st4(py, (a.act ? p * sigmoid4(p) : p).get());
+            py += a.ldy;
+        };
         for (int i = 0; i < n; i += FU) {
             Raw4<T> now[FU];
 #pragma unroll
@@ -109,17 +156,13 @@ __global__ __launch_bounds__(CT, 3) void k_conv_fwd(const ConvArgs a, int vg, in
 #pragma unroll
             for (int u = 0; u < FU; ++u)
                 if (i + FU + u < n) next[u].load(px + u * a.ldx);
+            if (i + FU <= n) {                                      // straight on: the window moves by names alone
 #pragma unroll
-            for (int u = 0; u < FU; ++u) {
-                if (i + u >= n) break;
+                for (int u = 0; u < FU; ++u) token(now[u]);
+            } else {
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) x[j] = x[j + 1];
-                x[W - 1] = now[u].get();
-                float4 p = bias;
-#pragma unroll
-                for (int j = 0; j < W; ++j) p = fma4(w[j], x[j], p);
-                st4(py, a.act ? p * sigmoid4(p) : p);
-                py += a.ldy;
+                for (int u = 0; u < FU; ++u)
+                    if (i + u < n) token(now[u]);
             }
         }
         t = end;
@@ -130,22 +173,25 @@ __global__ __launch_bounds__(CT, 3) void k_conv_fwd(const ConvArgs a, int vg, in
 template <class T, int W>
 __global__ __launch_bounds__(CT, 2) void k_conv_bwd(const ConvArgs a, int vg, int tr, int64_t runs) {
     __shared__ float4 sum[CT];
+    __shared__ int64_t offs[NEAR + 1];
+    const Seqs q = near(a.q, offs);
     const Place at(vg, a.P);
     const int c = at.c, rg = CT / vg;
-    float4 w[W], bias, x[W], dp[W], dw[W], db = f4(0.f);
+    Four w[W], bias, x[W], dp[W], dw[W], db(0.f);
     if (at.in) load_taps<W>(a, c, w, bias);
 #pragma unroll
-    for (int j = 0; j < W; ++j) dw[j] = dp[j] = f4(0.f);
+    for (int j = 0; j < W; ++j) dw[j] = dp[j] = Four(0.f);
     // one token: its entry joins x[W-1], the cotangent of its sum dp[W-1]
     auto token = [&](const Raw4<T> &in, const Raw4<T> &cot) {
-        x[W - 1] = in.get();
-        float4 g = cot.get();
+        x[W - 1] = Four(in.get());
+        Four g(cot.get());
         if (a.act) {
-            float4 p = bias;
+            Four p = bias;
 #pragma unroll
             for (int j = 0; j < W; ++j) p = fma4(w[j], x[j], p);
-            const float4 s = sigmoid4(p);
-            g = g * s * fma4(p, f4(1.f) - s, f4(1.f));
+            // s (1 + p (1 - s)) = s + (p s) (1 - s)
+            const Four s = sigmoid4(p);
+            g = g * fma4(p * s, fma4(s, Four(-1.f), Four(1.f)), s);
         }
         dp[W - 1] = g;
     };
@@ -156,20 +202,25 @@ __global__ __launch_bounds__(CT, 2) void k_conv_bwd(const ConvArgs a, int vg, in
             dp[j] = dp[j + 1];
         }
     };
+    auto sum_up = [&]() {
+        db = db + dp[W - 1];
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j] = fma4(dp[W - 1], x[j], dw[j]);
+    };
     if (int64_t(blockIdx.x) >= runs) {
         // dc of the entries of the state: from the first W-1 tokens, and from ds1 where a sequence is shorter
         const int64_t b = (blockIdx.x - runs) * rg + at.run;
-        if (!at.in || b >= a.q.B) return;
-        const int64_t begin = a.q.begin(b), n = max(int64_t(0), a.q.end(b) - begin);
+        if (!at.in || b >= q.B) return;
+        const int64_t begin = q.begin(b), n = max(int64_t(0), q.end(b) - begin);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) x[j + 1] = entry<T, W>(a, b, begin, j, c).get();
-        float4 ds[W - 1];
+        for (int j = 0; j < W - 1; ++j) x[j + 1] = Four(entry<T, W>(a, b, begin, j, c).get());
+        Four ds[W - 1];
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
             Raw4<T> r;
             r.zero();
             if (a.ds1 && i >= n) r.load(row<T>(a.ds1, b * (W - 1) + (i - n), a.P, c));
-            ds[i] = r.get();
+            ds[i] = Four(r.get());
         }
 #pragma unroll
         for (int t = 0; t < W - 1; ++t) {
@@ -183,20 +234,20 @@ __global__ __launch_bounds__(CT, 2) void k_conv_bwd(const ConvArgs a, int vg, in
             for (int j = 0; j < W - 1 - t; ++j) ds[t + j] = fma4(w[j], dp[W - 1], ds[t + j]);
         }
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) st4(static_cast<T *>(a.ds0) + (b * (W - 1) + i) * a.P + c, ds[i]);
+        for (int i = 0; i < W - 1; ++i) st4(static_cast<T *>(a.ds0) + (b * (W - 1) + i) * a.P + c, ds[i].get());
         return;
     }
     int64_t t = (int64_t(blockIdx.x) * rg + at.run) * tr;
-    const int64_t stop = at.in ? min(t + tr, a.q.rows) : 0;
-    if (a.q.off && t < stop) t = max(t, a.q.at(0));
+    const int64_t stop = at.in ? min(t + tr, q.rows) : 0;
+    if (q.off && t < stop) t = max(t, q.at(0));
     while (t < stop) {
-        const int64_t b = a.q.find(t);
+        const int64_t b = q.find(t);
         if (b < 0) break;
-        const int64_t begin = a.q.begin(b), end = a.q.end(b), last = min(end, stop), until = last + W - 1;
+        const int64_t begin = q.begin(b), end = q.end(b), last = min(end, stop), until = last + W - 1;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
-            x[j + 1] = entry<T, W>(a, b, begin, t - begin + j, c).get();
-            dp[j + 1] = f4(0.f);
+            x[j + 1] = Four(entry<T, W>(a, b, begin, t - begin + j, c).get());
+            dp[j + 1] = Four(0.f);
         }
         const T *px = row<T>(a.x, t, a.ldx, c), *pg = row<T>(a.go, t, a.ldy, c);
         T *pd = static_cast<T *>(a.dx) + t * a.ldx + c;
@@ -224,29 +275,40 @@ __global__ __launch_bounds__(CT, 2) void k_conv_bwd(const ConvArgs a, int vg, in
                 cg[u] = ng[u];
             }
             fetch(i + CU);
+            // dx of the token W-1 behind: complete now
+            auto emit = [&](Four d) {
 #pragma unroll
-            for (int u = 0; u < CU; ++u) {
-                const int k = i + u, s = k - (W - 1);               // dx of token s is complete after token k
-                if (k >= all) break;
-                shift();
-                if (k < left) token(cx[u], cg[u]);
-                else dp[W - 1] = f4(0.f);
-                if (k < own) {
-                    db = db + dp[W - 1];
+                for (int j = 0; j < W; ++j) d = fma4(w[W - 1 - j], dp[j], d);
+                st4(pd, d.get());
+                pd += a.ldx;
+            };
+            if (i >= W - 1 && i + CU <= own && !(a.ds1 && i + CU - W >= tail)) {
+                // straight on: the windows move by names alone
 #pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j] = fma4(dp[W - 1], x[j], dw[j]);
+                for (int u = 0; u < CU; ++u) {
+                    shift();
+                    token(cx[u], cg[u]);
+                    sum_up();
+                    emit(Four(0.f));
                 }
-                if (s >= 0) {
-                    float4 d = f4(0.f);
-                    if (a.ds1 && s >= tail) {
-                        Raw4<T> r;
-                        r.load(row<T>(a.ds1, b * (W - 1) + (s - tail), a.P, c));
-                        d = r.get();
-                    }
+            } else {
 #pragma unroll
-                    for (int j = 0; j < W; ++j) d = fma4(w[W - 1 - j], dp[j], d);
-                    st4(pd, d);
-                    pd += a.ldx;
+                for (int u = 0; u < CU; ++u) {
+                    const int k = i + u, s = k - (W - 1);
+                    if (k >= all) break;
+                    shift();
+                    if (k < left) token(cx[u], cg[u]);
+                    else dp[W - 1] = Four(0.f);
+                    if (k < own) sum_up();
+                    if (s >= 0) {
+                        Four d(0.f);
+                        if (a.ds1 && s >= tail) {
+                            Raw4<T> r;
+                            r.load(row<T>(a.ds1, b * (W - 1) + (s - tail), a.P, c));
+                            d = Four(r.get());
+                        }
+                        emit(d);
+                    }
                 }
             }
         }
@@ -256,7 +318,7 @@ __global__ __launch_bounds__(CT, 2) void k_conv_bwd(const ConvArgs a, int vg, in
 #pragma unroll
     for (int k = 0; k <= W; ++k) {
         __syncthreads();
-        sum[threadIdx.x] = k < W ? dw[k < W ? k : 0] : db;          // thread = run vg + quad
+        sum[threadIdx.x] = (k < W ? dw[k < W ? k : 0] : db).get();  // thread = run vg + quad
         __syncthreads();
         const int p = (int(blockIdx.y) * vg + int(threadIdx.x)) * 4;
         if (int(threadIdx.x) < vg && p < a.P) {
@@ -273,7 +335,7 @@ __global__ __launch_bounds__(CT) void k_conv_join(const ConvArgs a, int64_t bloc
     if (i >= n) return;
     const int k = int(i / a.P), p = int(i - int64_t(k) * a.P);
     float s = 0.f;
-#pragma unroll 8
+#pragma unroll 16
     for (int64_t b = 0; b < blocks; ++b) s += __ldg(a.part + b * n + i);
     if (k < a.W) a.dw[int64_t(p) * a.W + k] = s;
     else if (a.dbias) a.dbias[p] = s;
@@ -296,13 +358,13 @@ __global__ __launch_bounds__(CT) void k_conv_step(const ConvArgs a, T *state, in
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) r[j].load_own(s + int64_t(j) * a.P);
     r[W - 1].load(row<T>(a.x, b, a.ldx, c));
-    float4 w[W], p;
+    Four w[W], p;
     load_taps<W>(a, c, w, p);
 #pragma unroll
-    for (int j = 0; j < W; ++j) p = fma4(w[j], r[j].get(), p);
+    for (int j = 0; j < W; ++j) p = fma4(w[j], Four(r[j].get()), p);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) r[j + 1].store(s + int64_t(j) * a.P);
-    st4(y, a.act ? p * sigmoid4(p) : p);
+    st4(y, (a.act ? p * sigmoid4(p) : p).get());
 }
 
 // quads side by side in a block, runs of `tr` tokens, blocks of runs
@@ -320,8 +382,8 @@ ConvGrid conv_grid(const ConvArgs &a, int longest, int shortest, int64_t want) {
     g.runs = seq_div(a.q.rows, int64_t(g.tr) * (CT / g.vg));
     return g;
 }
-ConvGrid fwd_grid(const ConvArgs &a) { return conv_grid(a, 32, 4, 152 * 1024); }
-ConvGrid bwd_grid(const ConvArgs &a) { return conv_grid(a, 64, 8, 152 * 384); }
+ConvGrid fwd_grid(const ConvArgs &a) { return conv_grid(a, 64, 4, 152 * 1024); }
+ConvGrid bwd_grid(const ConvArgs &a) { return conv_grid(a, 128, 8, 152 * 384); }
 
 // f(type, taps) for the call's type and taps
 template <class F>

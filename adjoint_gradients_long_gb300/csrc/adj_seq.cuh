@@ -16,15 +16,15 @@ struct Seqs {
     int64_t B, T, rows;
 
     __device__ __forceinline__ int64_t at(int64_t i) const {
-        const int64_t v = __ldg(off + i);
+        const int64_t v = off[i];
         return v < 0 ? 0 : v > rows ? rows : v;
     }
     __device__ __forceinline__ int64_t begin(int64_t b) const { return off ? at(b) : b * T; }
     __device__ __forceinline__ int64_t end(int64_t b) const { return off ? at(b + 1) : (b + 1) * T; }
     // the sequence that holds token t, or -1
     __device__ __forceinline__ int64_t find(int64_t t) const {
-        if (!off) return t < rows ? t / T : -1;
-        int64_t lo = 0, hi = B + 1;                     // entries at most t lie below lo, larger ones from hi on
+        if (!off) return t < rows ? int64_t(uint32_t(t) / uint32_t(T)) : -1;       // rows < 2^31
+        int64_t lo = 0, hi = B + 1;                     // entries below lo are at most t, those from hi on larger
         while (lo < hi) {
             const int64_t mid = (lo + hi) >> 1;
             if (at(mid) <= t) lo = mid + 1;
