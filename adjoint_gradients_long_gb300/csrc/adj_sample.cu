@@ -8,10 +8,11 @@
 //
 // The kept tokens are a prefix of the order by x, so a limit is a key (the order of the fp32 values as
 // unsigned integers) and a number of tokens that equal it.  Top-k and top-p are found without sorting:
-// counts or weights over bins of the distance from the maximum, 24 to a power of two, say in which bin
-// a limit lies.  One value alone there (as often with bf16) is the limit; up to 512 tokens are compared
-// with one another; the keys of more are cut into 1024 parts again until one is left, three
-// times at most.  Top-k goes first and counts only, so that weights are formed for what it keeps.
+// counts or weights over bins in falling order say in which bin a limit lies.  bf16 has a bin for each of its
+// values, nearly, and is done.  fp32 has 24 bins to a power of two of the distance from the maximum: one
+// value alone there is the limit; up to 512 tokens are compared with one another; the keys of more are
+// cut into 1024 parts again until one is left, three times at most.  Top-k goes first and counts only, so
+// that weights are formed for what it keeps.
 // The token is then found by index: sums of the kept weights of every warp's part, of every thread's
 // share of the part that holds it, and along that share.
 //
@@ -98,6 +99,31 @@ struct Weigh {
     }
 };
 
+// bf16 has few values, so a row repeats them: those of 2^-8 to 2^7 and their negatives have a bin each, in
+// falling order, with smaller and larger ones in three bins that several values share.  Counts are
+// then all that a pass has to add up, and a weight is formed once a value, not once a token.
+constexpr int KEY_LOW = (119 << 7) - 1, KEY_SPAN = 15 * 128 + 1;    // 0: below; 1..: a value each; KEY_SPAN: above
+constexpr int KEYS = 2 * KEY_SPAN + 1;
+__device__ __forceinline__ int key_bin(float x) {
+    const int bits = __float_as_int(x) >> 16, q = min(max(bits & 0x7FFF, KEY_LOW), KEY_LOW + KEY_SPAN) - KEY_LOW;
+    return bits < 0 ? KEY_SPAN + q : KEY_SPAN - q;
+}
+__device__ __forceinline__ bool one_value(int bin) { return bin != 0 && bin != KEY_SPAN && bin != KEYS - 1; }
+__device__ __forceinline__ float bin_value(int bin) {
+    const int q = bin > KEY_SPAN ? bin - KEY_SPAN : KEY_SPAN - bin;
+    return __int_as_float((q + KEY_LOW) << 16 | (bin > KEY_SPAN ? int(0x80000000u) : 0));
+}
+template <class T>
+constexpr bool KEYED = sizeof(T) == 2;
+
+template <class T>
+struct KeyTable {};
+template <>
+struct KeyTable<__nv_bfloat16> {
+    unsigned long long weight[KEYS + 1];                // kept weight of a bin of one value
+    uint32_t tokens[KEYS + 1], shared_low[3], shared_high[3];
+};
+
 struct Shared {
     Step steps[256];
     uint32_t count[BINS], low[BINS], high[BINS];        // tokens of a bin; the halves of their weights' sum
@@ -116,10 +142,10 @@ struct Shared {
 
 // A 64-bit sum in two native 32-bit additions (64 bits in shared memory are a loop of compare and
 // exchange, which tokens of one bin hold up); few weights reach 2^32, so the second is rare.
-__device__ __forceinline__ void add_weight(Shared &s, int bin, uint64_t w) {
-    const uint32_t lo = uint32_t(w), old = atomicAdd(&s.low[bin], lo);
+__device__ __forceinline__ void add_weight(uint32_t *low, uint32_t *high, uint64_t w) {
+    const uint32_t lo = uint32_t(w), old = atomicAdd(low, lo);
     const uint32_t hi = uint32_t(w >> 32) + (old + lo < old ? 1u : 0u);
-    if (hi) atomicAdd(&s.high[bin], hi);
+    if (hi) atomicAdd(high, hi);
 }
 
 // Exclusive sums over the block's threads, in their order; totals in every thread.
@@ -188,6 +214,40 @@ struct Level {
     }
 };
 
+// The same over the bins of bf16 values; forms the weights of those of one value
+template <int ST>
+struct KeyLevel {
+    static constexpr int PER = (KEYS + ST - 1) / ST;
+    uint32_t c[PER], before_c, all_c;
+    uint64_t w[PER], before_w, all_w;
+    __device__ void read(Shared &s, KeyTable<__nv_bfloat16> &k, const Weigh &weigh, int blocks) {
+        uint32_t sc = 0;
+        uint64_t sw = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int bin = int(threadIdx.x) * PER + i;
+            c[i] = 0;
+            w[i] = 0;
+            if (bin >= KEYS) continue;
+            for (int b = 0; b < blocks; ++b) c[i] += blocks > 1 ? peer(k.tokens + bin, b) : k.tokens[bin];
+            if (one_value(bin)) {
+                const uint64_t one = weigh.kept(bin_value(bin));
+                k.weight[bin] = one;
+                if (one == 0) c[i] = 0;
+                w[i] = c[i] * one;
+            } else {
+                const int at = bin == 0 ? 0 : bin == KEY_SPAN ? 1 : 2;
+                for (int b = 0; b < blocks; ++b)
+                    w[i] += (uint64_t(blocks > 1 ? peer(k.shared_high + at, b) : k.shared_high[at]) << 32) +
+                            (blocks > 1 ? peer(k.shared_low + at, b) : k.shared_low[at]);
+            }
+            sc += c[i];
+            sw += w[i];
+        }
+        block_scan<ST>(s, sc, sw, before_c, before_w, all_c, all_w);
+    }
+};
+
 // A limit being looked for: the first `k` tokens, or those before which less than `mass` lies
 struct Goal {
     bool by_count;
@@ -197,15 +257,15 @@ struct Goal {
 };
 
 // The last bin whose beginning is inside the goal, given what lies before the whole level.
-template <int ST>
-__device__ void cross(Shared &s, const Level<ST> &l, const Goal &g, uint32_t over_c, uint64_t over_w) {
+template <class L>
+__device__ void cross(Shared &s, const L &l, const Goal &g, uint32_t over_c, uint64_t over_w) {
     uint32_t c = over_c + l.before_c;
     uint64_t w = over_w + l.before_w;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < Level<ST>::PER; ++i) {
+    for (int i = 0; i < L::PER; ++i) {
         if (l.c[i] && g.inside(c, w) && !g.inside(c + l.c[i], w + l.w[i])) {
-            s.bin = threadIdx.x * Level<ST>::PER + i;
+            s.bin = threadIdx.x * L::PER + i;
             s.here_c = l.c[i];
             s.before_c = c;
             s.before_w = w;
@@ -216,10 +276,17 @@ __device__ void cross(Shared &s, const Level<ST> &l, const Goal &g, uint32_t ove
     __syncthreads();
 }
 
-// A limit: tokens above `x`, and the first `ties` of those that equal it
+// A limit: tokens above `x`, and the first `ties` of those that equal it; their weight (where weights were added)
 struct Cut {
     float x;
     uint32_t ties;
+    uint64_t weight;
+    // that of equal tokens, of weight w each, which begin with `c` tokens and weight `over` before them
+    __device__ __forceinline__ static Cut among(float x, uint64_t w, const Goal &g, uint32_t c, uint64_t over) {
+        // a bin that is crossed holds a token: w > 0
+        const uint32_t n = w == 0 ? 0 : g.by_count ? g.k - c : uint32_t((g.mass - over + w - 1) / w);
+        return Cut{x, n, over + n * w};
+    }
 };
 
 // A block's part of a row: 16-byte vectors in shared memory, minus infinity where they reach over the row
@@ -270,11 +337,11 @@ __device__ __forceinline__ void clear(Shared &s) {
     }
 }
 
-// The limit in bin s.bin of the distances, among tokens of at least `floor`.
+// The limit in bin s.bin, of the distances or of bf16's shared ones, among tokens of at least `floor`.
 template <class T, int ST>
 __device__ Cut narrow(Shared &s, const Row<T, ST> &row, const Weigh &weigh, const Goal &g, float floor, int blocks) {
     const int tid = threadIdx.x, bin = int(s.bin);
-    const bool few = s.here_c <= LIST;
+    const bool few = s.here_c <= LIST, weights = KEYED<T> || !g.by_count;
     uint32_t over_c = s.before_c, lo = ~0u, hi = 0;
     uint64_t over_w = s.before_w;
     meet(blocks);                                                   // everyone has read what a call before left
@@ -284,7 +351,7 @@ __device__ Cut narrow(Shared &s, const Row<T, ST> &row, const Weigh &weigh, cons
     }
     __syncthreads();
     row.each([&](float x) {
-        if (!(x >= floor) || weigh.bin(x) != bin) return;
+        if (!(x >= floor) || (KEYED<T> ? key_bin(x) != bin || weigh.kept(x) == 0 : weigh.bin(x) != bin)) return;
         const uint32_t k = order_key(x);
         lo = min(lo, k);
         hi = max(hi, k);
@@ -315,7 +382,7 @@ __device__ Cut narrow(Shared &s, const Row<T, ST> &row, const Weigh &weigh, cons
         if (tid == 0) s.limit = ~0u;
         __syncthreads();
         const uint32_t mine = tid < n ? s.all_list[tid] : 0u;
-        if (tid < n) s.list_w[tid] = g.by_count ? 0 : weigh(key_value(mine));
+        if (tid < n) s.list_w[tid] = weights ? weigh(key_value(mine)) : 0;
         __syncthreads();
         uint32_t c = over_c;
         uint64_t w = over_w;
@@ -348,7 +415,7 @@ __device__ Cut narrow(Shared &s, const Row<T, ST> &row, const Weigh &weigh, cons
             const uint64_t w = weigh.kept(x);
             if (w == 0) return;
             atomicAdd(&s.count[(hi - k) >> shift], 1u);
-            if (!g.by_count) add_weight(s, (hi - k) >> shift, w);
+            if (weights) add_weight(&s.low[(hi - k) >> shift], &s.high[(hi - k) >> shift], w);
         });
         meet(blocks);
         Level<ST> l;
@@ -359,11 +426,13 @@ __device__ Cut narrow(Shared &s, const Row<T, ST> &row, const Weigh &weigh, cons
         hi -= s.bin << shift;
         lo = max(lo, hi - ((1u << shift) - 1));
     }
-    Cut c{key_value(hi), 0};
-    const uint64_t w = weigh(c.x);
-    if (w) c.ties = g.by_count ? g.k - over_c : uint32_t((g.mass - over_w + w - 1) / w);    // the limit holds a token: w > 0
-    return c;
+    const float x = key_value(hi);
+    return Cut::among(x, weigh(x), g, over_c, over_w);
 }
+
+// bytes of shared memory before the row
+template <class T>
+constexpr size_t FIXED = sizeof(Shared) + (KEYED<T> ? sizeof(KeyTable<T>) + 15 & ~size_t(15) : 0);
 
 template <class T, int ST>
 __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
@@ -380,7 +449,11 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
     if (tid < 256) s.steps[tid] = g_steps.s[tid];
     clear<ST>(s);
     if (tid == 0) s.bad = 0;
-    const Row<T, ST> row(a, n, blocks, rank, reinterpret_cast<uint4 *>(raw + sizeof(Shared)));
+    KeyTable<T> &keys = *reinterpret_cast<KeyTable<T> *>(raw + sizeof(Shared));     // bf16
+    if constexpr (KEYED<T>) {
+        for (int i = tid; i < KEYS + 1 + 6; i += ST) keys.tokens[i] = 0;            // the shared sums behind them, too
+    }
+    const Row<T, ST> row(a, n, blocks, rank, reinterpret_cast<uint4 *>(raw + FIXED<T>));
     __syncthreads();
     float top = -INFINITY;
     bool bad = !(temperature >= 0.f) || top_p != top_p || min_p != min_p;
@@ -430,10 +503,46 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
         weigh.sure = fminf(weigh.sure, t - out);
         weigh.never = fminf(weigh.never, t + out);
     }
-    Cut cut{-INFINITY, 0};                                          // everything
+    Cut cut{-INFINITY, 0, 0};                                       // everything
     const bool by_k = top_k > 0 && top_k < a.V, by_p = top_p < 1.f;
     if (temperature == 0.f || (by_k && top_k == 1)) {
-        cut = Cut{top, 1};
+        cut = Cut{top, 1, 0};
+    } else if constexpr (KEYED<T>) {
+        if (by_k || by_p) {
+            row.each([&](float x) {
+                if (!((top - x) * weigh.hi < DEAD)) return;
+                const int bin = key_bin(x);
+                if (one_value(bin)) {
+                    atomicAdd(&keys.tokens[bin], 1u);
+                } else if (const uint64_t w = weigh.kept(x)) {
+                    const int at = bin == 0 ? 0 : bin == KEY_SPAN ? 1 : 2;
+                    atomicAdd(&keys.tokens[bin], 1u);
+                    add_weight(&keys.shared_low[at], &keys.shared_high[at], w);
+                }
+            });
+            meet(blocks);
+            KeyLevel<ST> l;
+            l.read(s, keys, weigh, blocks);
+            uint64_t Z = l.all_w;
+#pragma unroll 1
+            for (int phase = by_k && uint32_t(top_k) < l.all_c ? 0 : 1; phase < (by_p ? 2 : 1); ++phase) {
+                Goal g{phase == 0, uint32_t(top_k), 0};
+                if (phase == 1) {
+                    // one token at least: the first begins below one unit.  One thread alone in 64-bit floating point.
+                    if (tid == 0) s.mass = uint64_t(ceil(fmax(double(top_p) * double(Z), 1.0)));
+                    __syncthreads();
+                    g.mass = s.mass;
+                }
+                cross(s, l, g, 0, 0);
+                const int bin = int(s.bin);
+                if (one_value(bin)) cut = Cut::among(bin_value(bin), keys.weight[bin], g, s.before_c, s.before_w);
+                else cut = narrow(s, row, weigh, g, -INFINITY, blocks);
+                Z = cut.weight;
+            }
+        } else {
+            for (int i = tid; i < KEYS; i += ST) keys.weight[i] = one_value(i) ? weigh.kept(bin_value(i)) : 0;
+            __syncthreads();
+        }
     } else {
         // Top-k first, then top-p among what is left.  Tokens that equal top-k's limit count in full there,
         // which moves nothing: what top_p asks for lies within the kept ones.
@@ -449,7 +558,7 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
                 const int bin = x >= cut.x ? weigh.bin(x) : -1;
                 if (bin < 0) return;
                 atomicAdd(&s.count[bin], 1u);
-                if (mass) add_weight(s, bin, weigh(x));
+                if (mass) add_weight(&s.low[bin], &s.high[bin], weigh(x));
             });
             meet(blocks);
             Level<ST> l;
@@ -477,8 +586,15 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
     const int per = (row.nv + SW - 1) / SW, i0 = min(row.nv, warp * per), i1 = min(row.nv, i0 + per);
     uint64_t w = 0;
     uint32_t t = 0;
+    auto weight_of = [&](float x) -> uint64_t {
+        if constexpr (KEYED<T>) {
+            const int bin = key_bin(x);
+            if (one_value(bin)) return keys.weight[bin];
+        }
+        return weigh.kept(x);
+    };
     auto add = [&](float x) {
-        if (x > cut.x) w += weigh.kept(x);
+        if (x > cut.x) w += weight_of(x);
         else t += x == cut.x;
     };
     row.each_of(i0 + lane, i1, 32, add);
@@ -544,7 +660,7 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
                 for (int e = 0; e < N; ++e) {
                     uint64_t x = 0;
                     if (v[e] > cut.x) {
-                        x = weigh.kept(v[e]);
+                        x = weight_of(v[e]);
                     } else if (v[e] == cut.x) {
                         x = bt < cut.ties ? tie_w : 0;
                         ++bt;
@@ -568,8 +684,10 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
     }
 }
 
-constexpr size_t MOST_SMEM = 232448 - sizeof(Shared) - 64;          // for a part of a row
-static_assert(int64_t(ADJ_SAMPLE_MAX_V) / 8 * 4 + 32 <= int64_t(MOST_SMEM), "a row has to fit eight blocks");
+template <class T>
+constexpr size_t MOST = 232448 - FIXED<T> - 64;                     // for a part of a row
+static_assert(ADJ_SAMPLE_MAX_V / 8 * 4 + 32 <= MOST<float> && ADJ_SAMPLE_MAX_V / 8 * 2 + 32 <= MOST<__nv_bfloat16>,
+              "a row has to fit eight blocks");
 
 template <class T, int ST>
 cudaError_t launch_as(const SampleArgs &a, int blocks, size_t smem, cudaStream_t st) {
@@ -595,9 +713,9 @@ cudaError_t launch(const SampleArgs &a, cudaStream_t st) {
     // the fewest blocks whose parts fit; then more, while every block keeps 4096 values and there are SMs for all
     auto part = [&](int blocks) { return size_t((a.V * sizeof(T) / 16 + 2 + blocks - 1) / blocks) * 16; };
     int blocks = 1;
-    while (blocks < 8 && part(blocks) > MOST_SMEM) blocks *= 2;
+    while (blocks < 8 && part(blocks) > MOST<T>) blocks *= 2;
     while (blocks < 8 && a.N * blocks * 2 <= 152 && a.V / (blocks * 2) >= 4096) blocks *= 2;
-    const size_t smem = sizeof(Shared) + part(blocks);
+    const size_t smem = FIXED<T> + part(blocks);
     // a part that leaves no room for a second block beside it gets all the SM's threads
     return smem > 113 * 1024 ? launch_as<T, 1024>(a, blocks, smem, st) : launch_as<T, 512>(a, blocks, smem, st);
 }
