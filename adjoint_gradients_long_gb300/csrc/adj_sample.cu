@@ -34,24 +34,21 @@ constexpr int LIST = 512;               // tokens of a bin that are compared one
 constexpr float DEAD = 41.5f;           // 2^-41.5 is less than half a unit
 constexpr float PARTS = 24.f;           // bins a power of two: DEAD of them fit
 
-// 2^(-i / 256): as a whole number of 2^-42, and as a pair of fp32
-struct alignas(16) Step {
-    unsigned long long fixed;
-    float hi, lo;
-};
+// 2^(-(i + 1) / 256), from 1/2 to below 1, as pairs of fp32
 struct StepTable {
-    Step s[256];
+    float2 s[256];
 };
 constexpr StepTable make_steps() {
     StepTable t{};
     const double root = 0.99729605608547012625;         // 2^(-1/256)
     double v = 1.0;
     for (int i = 0; i < 256; ++i) {
-        t.s[i].fixed = static_cast<unsigned long long>(v * 4398046511104.0 + 0.5);
-        t.s[i].hi = static_cast<float>(v);
-        t.s[i].lo = static_cast<float>(v - static_cast<double>(t.s[i].hi));
         v *= root;
+        t.s[i].x = static_cast<float>(v);
+        t.s[i].y = static_cast<float>(v - static_cast<double>(t.s[i].x));
     }
+    t.s[255].x = 0.5f;
+    t.s[255].y = 0.f;
     return t;
 }
 __device__ const StepTable g_steps = make_steps();
@@ -59,7 +56,7 @@ __device__ const StepTable g_steps = make_steps();
 // A row's weights
 struct Weigh {
     float m, hi, lo;                    // the largest logit; log2 e / temperature as a pair, finite
-    const Step *steps;
+    const float2 *steps;
     uint64_t least;                     // the smallest weight that min-p keeps, one unit at least
     float sure, never;                  // distances up to which a weight is above `least`, from which below
 
@@ -69,22 +66,29 @@ struct Weigh {
         const float d = m - x, t = d * hi;
         const float b = d - m, dl = (m - (d - b)) - (x + b);
         const float e = fmaf(d, hi, -t) + fmaf(d, lo, dl * hi);
-        const float MAGIC = 12582912.f;                 // 1.5 2^23: rounds to whole numbers
-        const float kf = fmaf(t, 256.f, MAGIC);
-        const int k = __float_as_int(kf) - __float_as_int(MAGIC);
-        const float r = fmaf(kf - MAGIC, -1.f / 256.f, t);      // exact
+        constexpr float MAGIC = 12582912.f;             // 1.5 2^23: rounds to whole numbers, its bits' low 22 are zero
+        constexpr uint32_t BITS = 0x4B400000u;
+        // t = (256 n + i + 1) / 256 + r, i of 0 to 255 and n from -1 on: the bits of kf end in those of 256 n + i
+        const float kf = fmaf(t, 256.f, MAGIC - 1.f);
+        const uint32_t kb = __float_as_uint(kf);
+        const float r = fmaf(kf - (MAGIC - 1.f), -1.f / 256.f, t);      // exact
         constexpr float L = 0.693147182464599609375f, LL = -1.904654323148236017e-9f;
         const float ph = -r * L, pl = fmaf(-r, L, -ph);
-        const float sq = ph * ph, tail = fmaf(sq, fmaf(ph, fmaf(ph, 1.f / 24.f, 1.f / 6.f), 0.5f), fmaf(-e, L, fmaf(-r, LL, pl)));
-        const Step s = steps[k & 255];
-        const float q = s.hi * ph, low = fmaf(s.hi, ph, -q) + fmaf(s.lo, ph, s.hi * tail);
-        const float qa = fmaf(q, 1048576.f, MAGIC);             // 2^20
-        const float rest = fmaf(qa - MAGIC, -1.f / 1048576.f, q) + low;
-        const float qb = fmaf(rest, 4398046511104.f, MAGIC);    // 2^42, below 2^22 of it
-        const long long whole = (long long)s.fixed + ((long long)(__float_as_int(qa) - __float_as_int(MAGIC)) << 22) +
-                                (__float_as_int(qb) - __float_as_int(MAGIC));
-        const int n = ((k >> 8) + 2) & 63;
-        const uint64_t w = uint64_t(whole + (1ll << (n - 1))) >> n;
+        // 2^-(r + e) - 1 = y + y^2 / 2 + y^3 / 6, y = ph + rest (the fourth power is below 2^-42)
+        const float rest = fmaf(-e, L, fmaf(-r, LL, pl)), tail = fmaf(ph, fmaf(ph, fmaf(ph, 1.f / 6.f, 0.5f), rest), rest);
+        const float2 s = steps[kb & 255];
+        const float q = s.x * ph, low = fmaf(s.x, ph, -q) + fmaf(s.y, ph, fmaf(s.x, tail, s.y));
+        // s.x + q + low in units of 2^-42: s.x is 24 bits of 2^-24, the others go in units of 2^-20, and what that
+        // leaves, below 2^21 units, by itself
+        const float sum = q + low, lost = low - (sum - q);
+        const float qa = fmaf(sum, 1048576.f, MAGIC);
+        const float qb = fmaf(fmaf(qa - MAGIC, -1.f / 1048576.f, sum) + lost, 4398046511104.f, MAGIC);
+        const uint32_t upper = ((__float_as_uint(s.x) & 0x7FFFFFu) | 0x800000u) + (__float_as_uint(qa) << 4) - (BITS << 4) -
+                               (BITS >> 18);
+        uint64_t whole = uint64_t(upper) * (1u << 18) + __float_as_uint(qb);
+        // 2^-n of it in units of 2^-40, to the nearest
+        whole >>= (kb >> 8) + 1 & 63;
+        const uint64_t w = (whole + 1) >> 1;
         return t < DEAD ? w : 0;
     }
     // a part of the distances from the largest: never falls as x does; -1: not kept by min-p, or too far
@@ -125,7 +129,7 @@ struct KeyTable<__nv_bfloat16> {
 };
 
 struct Shared {
-    Step steps[256];
+    float2 steps[256];
     uint32_t count[BINS], low[BINS], high[BINS];        // tokens of a bin; the halves of their weights' sum
     // what the blocks of a cluster read of one another
     float top;
@@ -136,7 +140,7 @@ struct Shared {
     unsigned long long red64[MOST_WARPS], list_w[LIST];
     uint32_t red32[MOST_WARPS], all_list[LIST];
     // a crossing: its bin, what it holds and what lies before it
-    uint32_t bin, here_c, before_c, owner, owner_ties, limit;
+    uint32_t bin, before_c, owner, owner_ties, limit;
     unsigned long long before_w, owner_w, total, mass;
 };
 
@@ -264,9 +268,8 @@ __device__ void cross(Shared &s, const L &l, const Goal &g, uint32_t over_c, uin
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < L::PER; ++i) {
-        if (l.c[i] && g.inside(c, w) && !g.inside(c + l.c[i], w + l.w[i])) {
+        if ((g.by_count ? l.c[i] != 0 : l.w[i] != 0) && g.inside(c, w) && !g.inside(c + l.c[i], w + l.w[i])) {
             s.bin = threadIdx.x * L::PER + i;
-            s.here_c = l.c[i];
             s.before_c = c;
             s.before_w = w;
         }
@@ -341,7 +344,7 @@ __device__ __forceinline__ void clear(Shared &s) {
 template <class T, int ST>
 __device__ Cut narrow(Shared &s, const Row<T, ST> &row, const Weigh &weigh, const Goal &g, float floor, int blocks) {
     const int tid = threadIdx.x, bin = int(s.bin);
-    const bool few = s.here_c <= LIST, weights = KEYED<T> || !g.by_count;
+    const bool weights = KEYED<T> || !g.by_count;
     uint32_t over_c = s.before_c, lo = ~0u, hi = 0;
     uint64_t over_w = s.before_w;
     meet(blocks);                                                   // everyone has read what a call before left
@@ -355,7 +358,8 @@ __device__ Cut narrow(Shared &s, const Row<T, ST> &row, const Weigh &weigh, cons
         const uint32_t k = order_key(x);
         lo = min(lo, k);
         hi = max(hi, k);
-        if (few) s.list[atomicAdd(&s.listed, 1u)] = k;              // here_c of them over all blocks
+        const uint32_t at = atomicAdd(&s.listed, 1u);
+        if (at < LIST) s.list[at] = k;
     });
     lo = __reduce_min_sync(~0u, lo);
     hi = __reduce_max_sync(~0u, hi);
@@ -366,11 +370,13 @@ __device__ Cut narrow(Shared &s, const Row<T, ST> &row, const Weigh &weigh, cons
     meet(blocks);
     lo = s.kmin;
     hi = s.kmax;
+    uint32_t total = blocks > 1 ? 0 : s.listed;
     for (int b = 0; blocks > 1 && b < blocks; ++b) {
         lo = min(lo, peer(&s.kmin, b));
         hi = max(hi, peer(&s.kmax, b));
+        total += peer(&s.listed, b);
     }
-    if (few && lo < hi) {
+    if (total <= LIST && lo < hi) {
         // every token of the bin with all others: what lies above it; the lowest one inside the goal
         int n = 0;
         for (int b = 0; b < blocks; ++b) {
@@ -414,7 +420,7 @@ __device__ Cut narrow(Shared &s, const Row<T, ST> &row, const Weigh &weigh, cons
             if (k < lo || k > hi) return;
             const uint64_t w = weigh.kept(x);
             if (w == 0) return;
-            atomicAdd(&s.count[(hi - k) >> shift], 1u);
+            if (g.by_count) atomicAdd(&s.count[(hi - k) >> shift], 1u);
             if (weights) add_weight(&s.low[(hi - k) >> shift], &s.high[(hi - k) >> shift], w);
         });
         meet(blocks);
@@ -554,12 +560,18 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
                 clear<ST>(s);
                 __syncthreads();
             }
+            uint32_t equal = 0;                                     // tokens at top-k's limit
+            if (tid == 0) s.listed = 0;
+            __syncthreads();
             row.each([&](float x) {
                 const int bin = x >= cut.x ? weigh.bin(x) : -1;
                 if (bin < 0) return;
-                atomicAdd(&s.count[bin], 1u);
+                equal += x == cut.x;
                 if (mass) add_weight(&s.low[bin], &s.high[bin], weigh(x));
+                else atomicAdd(&s.count[bin], 1u);
             });
+            equal = __reduce_add_sync(~0u, equal);
+            if (lane == 0 && equal) atomicAdd(&s.listed, equal);
             meet(blocks);
             Level<ST> l;
             l.read(s, blocks);
@@ -568,7 +580,9 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
                 // one token at least: the first begins below one unit.  One thread alone in 64-bit floating point.
                 if (tid == 0) {
                     uint64_t Z = l.all_w;
-                    if (cut.ties) Z -= (uint64_t(l.all_c) - uint32_t(top_k)) * weigh(cut.x);
+                    uint32_t all = blocks > 1 ? 0 : s.listed;
+                    for (int b = 0; blocks > 1 && b < blocks; ++b) all += peer(&s.listed, b);
+                    if (cut.ties) Z -= uint64_t(all - cut.ties) * weigh(cut.x);
                     s.mass = uint64_t(ceil(fmax(double(top_p) * double(Z), 1.0)));
                 }
                 __syncthreads();
