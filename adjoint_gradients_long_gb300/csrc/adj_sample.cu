@@ -91,11 +91,15 @@ struct Weigh {
         const uint64_t w = (whole + 1) >> 1;
         return t < DEAD ? w : 0;
     }
-    // a part of the distances from the largest: never falls as x does; -1: not kept by min-p, or too far
+    // A part of the distances from the largest: never falls as x does; -1: not kept by min-p, or too far.  The weight
+    // itself is looked at on the border alone, out of line: inlined, it would be formed for every value.
     __device__ __forceinline__ int bin(float x) const {
         const float t = (m - x) * hi;
-        if (!(t < never) || (t > sure && (*this)(x) < least)) return -1;
+        if (!(t < never) || (t > sure && far_weight(m, hi, lo, steps, x) < least)) return -1;
         return int(t * PARTS);
+    }
+    __device__ __noinline__ static uint64_t far_weight(float m, float hi, float lo, const float2 *steps, float x) {
+        return Weigh{m, hi, lo, steps, 1, 0.f, 0.f}(x);
     }
     __device__ __forceinline__ uint64_t kept(float x) const {
         const uint64_t w = (*this)(x);
@@ -173,19 +177,23 @@ __device__ void block_scan(Shared &s, uint32_t c, uint64_t w, uint32_t &ec, uint
         s.red64[warp] = iw;
     }
     __syncthreads();
-    uint32_t bc = 0;
-    uint64_t bw = 0;
-    tc = 0;
-    tw = 0;
+    // every warp sums up the warps' totals by itself
+    const bool there = lane < ST / 32;
+    uint32_t wc = there ? s.red32[lane] : 0;
+    uint64_t ww = there ? s.red64[lane] : 0;
 #pragma unroll
-    for (int i = 0; i < ST / 32; ++i) {
-        if (i < warp) {
-            bc += s.red32[i];
-            bw += s.red64[i];
+    for (int d = 1; d < ST / 32; d <<= 1) {
+        const uint32_t x = __shfl_up_sync(~0u, wc, d);
+        const uint64_t y = __shfl_up_sync(~0u, ww, d);
+        if (lane >= d) {
+            wc += x;
+            ww += y;
         }
-        tc += s.red32[i];
-        tw += s.red64[i];
     }
+    tc = __shfl_sync(~0u, wc, ST / 32 - 1);
+    tw = __shfl_sync(~0u, ww, ST / 32 - 1);
+    const uint32_t bc = warp ? __shfl_sync(~0u, wc, warp - 1 & 31) : 0;
+    const uint64_t bw = warp ? __shfl_sync(~0u, ww, warp - 1 & 31) : 0;
     ec = bc + ic - c;
     ew = bw + iw - w;
 }
@@ -201,14 +209,23 @@ struct Level {
         uint64_t sw = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) c[i] = 0, w[i] = 0;
-        for (int b = 0; b < blocks; ++b)
+        // a block's values are on their way together: one at a time, each would wait for the other block
+        for (int b = 0; b < blocks; ++b) {
+            uint32_t n[PER], lo[PER], hi[PER];
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int bin = int(threadIdx.x) * PER + i;
                 const bool own = blocks == 1;
-                c[i] += own ? s.count[bin] : peer(s.count + bin, b);
-                w[i] += (uint64_t(own ? s.high[bin] : peer(s.high + bin, b)) << 32) + (own ? s.low[bin] : peer(s.low + bin, b));
+                n[i] = own ? s.count[bin] : peer(s.count + bin, b);
+                lo[i] = own ? s.low[bin] : peer(s.low + bin, b);
+                hi[i] = own ? s.high[bin] : peer(s.high + bin, b);
             }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                c[i] += n[i];
+                w[i] += (uint64_t(hi[i]) << 32) + lo[i];
+            }
+        }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             sc += c[i];
@@ -227,13 +244,27 @@ struct KeyLevel {
     __device__ void read(Shared &s, KeyTable<__nv_bfloat16> &k, const Weigh &weigh, int blocks) {
         uint32_t sc = 0;
         uint64_t sw = 0;
+        // Over the blocks first, by threads side by side: a thread's own bins lie apart from its neighbours', and
+        // the other blocks' memory takes that ill.  The sums stand where the weights go afterwards.
+        uint32_t *all = reinterpret_cast<uint32_t *>(k.weight);
+        if (blocks > 1) {
+            for (int bin = threadIdx.x; bin < KEYS; bin += ST) {
+                uint32_t n = 0;
+                for (int b = 0; b < blocks; ++b) n += peer(k.tokens + bin, b);
+                all[bin] = n;
+            }
+            __syncthreads();
+        } else {
+            all = k.tokens;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) c[i] = all[min(int(threadIdx.x) * PER + i, KEYS)];
+        if (blocks > 1) __syncthreads();
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int bin = int(threadIdx.x) * PER + i;
-            c[i] = 0;
             w[i] = 0;
             if (bin >= KEYS) continue;
-            for (int b = 0; b < blocks; ++b) c[i] += blocks > 1 ? peer(k.tokens + bin, b) : k.tokens[bin];
             if (one_value(bin)) {
                 const uint64_t one = weigh.kept(bin_value(bin));
                 k.weight[bin] = one;
@@ -724,7 +755,8 @@ cudaError_t launch_as(const SampleArgs &a, int blocks, size_t smem, cudaStream_t
 
 template <class T>
 cudaError_t launch(const SampleArgs &a, cudaStream_t st) {
-    // the fewest blocks whose parts fit; then more, while every block keeps 4096 values and there are SMs for all
+    // The fewest blocks whose parts fit; then more, while every block keeps 4096 values and there are SMs for all: a row
+    // of 32000 bf16 with top-k and top-p takes 19.6 us in four blocks, 21.2 in two, 23.9 in one.
     auto part = [&](int blocks) { return size_t((a.V * sizeof(T) / 16 + 2 + blocks - 1) / blocks) * 16; };
     int blocks = 1;
     while (blocks < 8 && part(blocks) > MOST<T>) blocks *= 2;
