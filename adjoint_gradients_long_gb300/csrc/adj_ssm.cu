@@ -492,7 +492,7 @@ __global__ __launch_bounds__(128) void k_ssm_carry(const SsmArgs a) {
     const int p = int(i / (a.N / 4));
     const float4 A = f4(SEQ_LOG2E) * __ldg(reinterpret_cast<const float4 *>(a.A) + i);
     float4 *x = reinterpret_cast<float4 *>(right ? a.adj : a.seg) + i, cur = f4(0.f);
-    constexpr int U = 8;
+    constexpr int U = 16;
     for (int64_t s0 = 0; s0 < a.nseg; s0 += U) {
         float4 v[U];
         float d[U];
@@ -1005,10 +1005,10 @@ cudaError_t carry(const SsmArgs &a, int dirs, cudaStream_t st) {
 size_t ssm_plan(SsmArgs &a, bool bwd, void *base) {
     const int64_t tt = tile_tokens(a.N, 2), cols = columns(a, bwd), tiles = seq_div(a.q.rows, tt);
     // whole turns of the machine: 3 blocks an SM, and backwards twice that, three turns of k_ssm_grad's 2 blocks; 64
-    // tokens a segment at least (32 backwards).  A short prompt stays in one segment, as its walk costs
-    // less than two more launches.
+    // tokens a segment at least (two tiles backwards: 2048 x 512 x 16 take 52 us so, 65 with one and 60 with four).
+    // A short prompt stays in one segment, as its walk costs less than two more launches.
     const int64_t want = std::max<int64_t>(1, 152 * (bwd ? 6 : 3) / cols);
-    const int64_t per = !bwd && brief(a) ? std::max<int64_t>(tiles, 1) : std::max((bwd ? 32 : 64) / tt, seq_div(tiles, want));
+    const int64_t per = !bwd && brief(a) ? std::max<int64_t>(tiles, 1) : std::max<int64_t>(bwd ? 2 : 64 / tt, seq_div(tiles, want));
     a.seglen = per * tt;
     a.nseg = seq_div(a.q.rows, a.seglen);
     char *p = static_cast<char *>(base);

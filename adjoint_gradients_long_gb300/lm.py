@@ -331,6 +331,12 @@ class _Seq:
             self._strided[at] = y.zero_()
         return self._strided[at]
 
+    @staticmethod
+    def _other(pair, given):
+        """Of two arrays of states the one that the call was not given: a sequence is carried on from call to
+        call with what the object returned."""
+        return pair[1] if given is not None and given == pair[0].data_ptr() else pair[0]
+
 
 class ShortConv(_Seq):
     """A causal convolution of W (2 to 4) taps for each of P channels (a multiple of 8) over B sequences:
@@ -346,7 +352,7 @@ class ShortConv(_Seq):
         need = lib.conv_workspace_bytes(self.dims)
         if need == 0:
             raise ValueError("unsupported convolution sizes")
-        self.y, self.s1 = self._new(self.x), self._new(self.states)
+        self.y, self._s1 = self._new(self.x), (self._new(self.states), self._new(self.states))
         pd = ctypes.byref(self.dims)
         self._fwd, self._bwd = lib.bind("adj_conv_fwd", pd), lib.bind("adj_conv_bwd", pd)
         self.has_backward = backward
@@ -354,7 +360,8 @@ class ShortConv(_Seq):
             self.ws_bytes = need
             self.ws = _workspace(need, self.device)
             self.dw, self.dbias = self._new(self.w, torch.float32), self._new((P,), torch.float32)
-            self.ds0 = self._new(self.states)
+            self._ds0 = self._new(self.states), self._new(self.states)
+            self._strided["x", None] = self._new(self.x)
 
     def _inputs(self, x, w, bias, s0, offsets):
         self.dims.ldx = self._pitch("x", x, self.x)
@@ -365,20 +372,24 @@ class ShortConv(_Seq):
         return None if s is None else _dense(name, s, self.states, self.xt, self.device)
 
     def forward(self, x, w, bias=None, s0=None, offsets=None):
-        """(y, s1 [B,W-1,P]): the outputs, and the last W-1 inputs of every sequence."""
-        self._fwd(*self._inputs(x, w, bias, s0, offsets), self.y.data_ptr(), self.s1.data_ptr(), raw_stream(self.device))
-        return self.y, self.s1
+        """(y, s1 [B,W-1,P]): the outputs, and the last W-1 inputs of every sequence.  s0 may be the s1 of the
+        call before: there are two arrays, by turns."""
+        at = self._inputs(x, w, bias, s0, offsets)
+        s1 = self._other(self._s1, at[3])
+        self._fwd(*at, self.y.data_ptr(), s1.data_ptr(), raw_stream(self.device))
+        return self.y, s1
 
     def backward(self, x, w, go, bias=None, s0=None, ds1=None, offsets=None):
-        """(dx, dw, dbias, ds0) for the cotangents go of y and ds1 of s1; dx has the layout of x."""
+        """(dx, dw, dbias, ds0) for the cotangents go of y and ds1 of s1; dx has the layout of x.  ds1 may be
+        the ds0 of the call before."""
         if not self.has_backward:
             raise ValueError("this ShortConv was made without backward=True")
         at = self._inputs(x, w, bias, s0, offsets)
         at += _dense("go", go, self.x, self.xt, self.device), self._state("ds1", ds1)
-        dx = self._like("x", x)
-        self._bwd(*at, dx.data_ptr(), self.dw.data_ptr(), self.dbias.data_ptr(), self.ds0.data_ptr(), self.ws.data_ptr(),
+        dx, ds0 = self._like("x", x), self._other(self._ds0, at[-1])
+        self._bwd(*at, dx.data_ptr(), self.dw.data_ptr(), self.dbias.data_ptr(), ds0.data_ptr(), self.ws.data_ptr(),
                   self.ws_bytes, raw_stream(self.device))
-        return dx, self.dw, self.dbias, self.ds0
+        return dx, self.dw, self.dbias, ds0
 
 
 class ShortConvStep(_Seq):
@@ -442,12 +453,14 @@ class SelScan(_Sel):
         self.ws = _workspace(need, self.device)
         f32 = torch.float32
         self.states = (B, P, N)
-        self.y, self.s1 = self._new(self.x), self._new(self.states, f32)
+        self.y, self._s1 = self._new(self.x), (self._new(self.states, f32), self._new(self.states, f32))
         pd = ctypes.byref(self.dims)
         self._fwd, self._bwd = lib.bind("adj_ssm_fwd", pd), lib.bind("adj_ssm_bwd", pd)
         self.has_backward = backward
         if backward:
-            self.dA, self.ds0 = self._new(self.A, f32), self._new(self.states, f32)
+            self.dA, self._ds0 = self._new(self.A, f32), (self._new(self.states, f32), self._new(self.states, f32))
+            for name, shape in (("x", self.x), ("dt", self.x), ("Bm", self.maps), ("Cm", self.maps), ("z", self.x)):
+                self._strided[name, None] = self._new(shape)
             self.dD, self.ddt_bias = self._new(self.P, f32), self._new(self.P, f32)
 
     def _inputs(self, x, dt, A, Bm, Cm, D, z, dt_bias, s0, offsets):
@@ -455,21 +468,23 @@ class SelScan(_Sel):
                 self._offsets(offsets))
 
     def forward(self, x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, s0=None, offsets=None):
-        """(y, s1 [B,P,N]): the outputs, and the state after every sequence's last token."""
-        self._fwd(*self._inputs(x, dt, A, Bm, Cm, D, z, dt_bias, s0, offsets), self.y.data_ptr(), self.s1.data_ptr(),
-                  self.ws.data_ptr(), self.ws_bytes, raw_stream(self.device))
-        return self.y, self.s1
+        """(y, s1 [B,P,N]): the outputs, and the state after every sequence's last token.  s0 may be the s1 of
+        the call before: there are two arrays, by turns."""
+        at = self._inputs(x, dt, A, Bm, Cm, D, z, dt_bias, s0, offsets)
+        s1 = self._other(self._s1, at[8])
+        self._fwd(*at, self.y.data_ptr(), s1.data_ptr(), self.ws.data_ptr(), self.ws_bytes, raw_stream(self.device))
+        return self.y, s1
 
     def backward(self, x, dt, A, Bm, Cm, go, D=None, z=None, dt_bias=None, s0=None, ds1=None, offsets=None):
         """SelGrads for the cotangents go of y and ds1 of s1; dx, ddt, dB, dC and dz have the layouts of
-        x, dt, Bm, Cm and z.  dz is None without z."""
+        x, dt, Bm, Cm and z.  dz is None without z.  ds1 may be the ds0 of the call before."""
         if not self.has_backward:
             raise ValueError("this SelScan was made without backward=True")
         at = self._inputs(x, dt, A, Bm, Cm, D, z, dt_bias, s0, offsets)
         at += _dense("go", go, self.x, self.xt, self.device), self._f32("ds1", ds1, self.states)
         like = self._like
         r = SelGrads(like("x", x), like("dt", dt), self.dA, like("Bm", Bm), like("Cm", Cm), self.dD,
-                     None if z is None else like("z", z), self.ddt_bias, self.ds0)
+                     None if z is None else like("z", z), self.ddt_bias, self._other(self._ds0, at[-1]))
         self._bwd(*at, *(None if g is None else g.data_ptr() for g in r), self.ws.data_ptr(), self.ws_bytes,
                   raw_stream(self.device))
         return r

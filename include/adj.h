@@ -371,7 +371,8 @@ adj_status adj_grad_clip(const adj_grad_seg *segs, int64_t nseg, float max_norm,
  * reaches from one sequence into another, values that are not finite included (but for
  * gradients of parameters, which sum over all).
  * ld*: elements from one token to the next (so that arrays may be column slices of one
- * projection), multiples of 16 bytes.  A pool of states has n_slots entries; slots [B] int32
+ * projection), multiples of 16 bytes.  Prompts and gradients: no output may overlap an input (s1 with s0,
+ * ds0 with ds1 included); the same address twice is refused.  A pool of states has n_slots entries; slots [B] int32
  * gives the entry of each sequence (NULL: entry b, needs n_slots >= B).  A slot outside
  * [0, n_slots) leaves the pool untouched and gives a row of zeros (the padding of a batch); a
  * slot given twice is a race.
@@ -391,7 +392,7 @@ typedef struct {
     int32_t reserved;            /* zero */
 } adj_conv_dims;
 
-/* s0 NULL: zeros; s1 NULL: not written.  y may not alias an input.  No workspace. */
+/* s0 NULL: zeros; s1 NULL: not written.  No workspace. */
 adj_status adj_conv_fwd(const adj_conv_dims *dims, const void *x, const float *w, const float *bias, const void *s0,
                         const int64_t *offsets, void *y, void *s1, void *stream);
 
@@ -400,7 +401,7 @@ size_t adj_conv_workspace_bytes(const adj_conv_dims *dims);
 
 /* Gradients for the cotangents go [rows,P] of y (pitch ldy) and ds1 [B,W-1,P] of s1 (both
  * x_dtype; ds1 NULL: zeros): dx (pitch ldx), dw [P,W] fp32, dbias [P] fp32 (NULL: not written),
- * ds0 [B,W-1,P] x_dtype (NULL: not written).  No output may alias an input.  Sums in a fixed order. */
+ * ds0 [B,W-1,P] x_dtype (NULL: not written).  Sums in a fixed order. */
 adj_status adj_conv_bwd(const adj_conv_dims *dims, const void *x, const float *w, const float *bias, const void *s0,
                         const int64_t *offsets, const void *go, const void *ds1, void *dx, float *dw, float *dbias,
                         void *ds0, void *ws, size_t ws_bytes, void *stream);
@@ -428,15 +429,15 @@ typedef struct {
 /* Workspace bytes of ADJ_OP_SSM_FWD or ADJ_OP_SSM_BWD (0 for sizes the calls reject). */
 size_t adj_ssm_workspace_bytes(const adj_ssm_dims *dims, int op);
 
-/* D, z, dt_bias, s0 NULL: zeros (z: no gate); s1 NULL: not written.  y may not alias an input. */
+/* D, z, dt_bias, s0 NULL: zeros (z: no gate); s1 NULL: not written. */
 adj_status adj_ssm_fwd(const adj_ssm_dims *dims, const void *x, const void *dt, const float *A, const void *Bm,
                        const void *Cm, const float *D, const void *z, const float *dt_bias, const float *s0,
                        const int64_t *offsets, void *y, float *s1, void *ws, size_t ws_bytes, void *stream);
 
 /* Gradients for the cotangents go [rows,P] of y (x_dtype, pitch ldy) and ds1 of s1 (NULL: zeros).
  * dx, ddt, dz, dB, dC have the type and pitch of x, dt, z, Bm, Cm; dA, dD, ddt_bias, ds0 are fp32.
- * dD, ddt_bias, ds0 NULL: not written; dz is needed where z is given, and NULL without.  No output
- * may alias an input.  Sums in a fixed order. */
+ * dD, ddt_bias, ds0 NULL: not written; dz is needed where z is given, and NULL without.  Sums in a
+ * fixed order. */
 adj_status adj_ssm_bwd(const adj_ssm_dims *dims, const void *x, const void *dt, const float *A, const void *Bm,
                        const void *Cm, const float *D, const void *z, const float *dt_bias, const float *s0,
                        const int64_t *offsets, const void *go, const float *ds1, void *dx, void *ddt, float *dA,

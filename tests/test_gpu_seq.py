@@ -374,3 +374,86 @@ def test_same_bits_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(kept, first))
+
+
+def test_carried_on_with_the_objects_own_states():
+    """A long prompt in pieces through one object, its s1 given back as s0, and the gradients from the last
+    piece to the first, ds0 given back as ds1: as in one call."""
+    from adjoint_gradients_long_gb300 import lm
+    n, k = 96, 3                                           # whole tiles, so that states are summed up alike
+    x, _ = scan_case(6, 2, n * k, 40, 16, False)
+    s, whole = (lm.SelScan(2, t, 40, 16, x_bf16=False, backward=True) for t in (n, n * k))
+    y, s1, r = scan_run(whole, x)
+    piece = lambda i: {m: v[:, i * n:(i + 1) * n].contiguous() if v is not None and v.dim() == 3 and v.shape[1] == n * k else v  # noqa: E731
+                       for m, v in x.items()}
+    st, states, ys = x["s0"], [], []
+    for i in range(k):
+        p = piece(i)
+        states.append(st.clone())
+        got, st = s.forward(*(p[m] for m in FWD), p["D"], p["z"], p["dt_bias"], st)
+        ys.append(got.clone())
+    assert rel_fro(np64(torch.cat(ys, 1)), np64(y)) <= SCAN and rel_fro(np64(st), np64(s1)) <= SCAN
+    ds, dxs = x["ds1"], []
+    for i in reversed(range(k)):
+        p = piece(i)
+        g = s.backward(*(p[m] for m in FWD), p["go"], p["D"], p["z"], p["dt_bias"], states[i], ds)
+        ds = g.ds0
+        dxs.append(g.dx.clone())
+    assert rel_fro(np64(torch.cat(dxs[::-1], 1)), np64(r.dx)) <= SCAN_G and rel_fro(np64(ds), np64(r.ds0)) <= SCAN_G
+    cx, _ = conv_case(6, 2, 40 * 3, 48, 4, True)
+    c, whole = (lm.ShortConv(2, t, 48, 4, backward=True) for t in (40, 120))
+    y, s1 = (o.clone() for o in whole.forward(cx["x"], cx["w"], cx["bias"], cx["s0"]))
+    dx, _, _, ds0 = whole.backward(cx["x"], cx["w"], cx["go"], cx["bias"], cx["s0"], cx["ds1"])
+    st, states, ys, dxs, ds = cx["s0"], [], [], [], cx["ds1"]
+    for i in range(3):
+        states.append(st.clone())
+        got, st = c.forward(cx["x"][:, 40 * i:40 * i + 40].contiguous(), cx["w"], cx["bias"], st)
+        ys.append(got.clone())
+    for i in reversed(range(3)):
+        at = slice(40 * i, 40 * i + 40)
+        g, _, _, ds = c.backward(cx["x"][:, at].contiguous(), cx["w"], cx["go"][:, at].contiguous(), cx["bias"], states[i], ds)
+        dxs.append(g.clone())
+    assert torch.equal(torch.cat(ys, 1), y) and torch.equal(st, s1)
+    assert rel_fro(np64(torch.cat(dxs[::-1], 1)), np64(dx)) <= 2 * HALF     # ds0 between two pieces is rounded
+    assert rel_fro(np64(ds), np64(ds0)) <= 2 * HALF
+
+
+def test_outputs_given_as_inputs_are_refused():
+    from adjoint_gradients_long_gb300 import lib, lm
+    x, _ = scan_case(6, 1, 32, 16, 16, True)
+    s = lm.SelScan(1, 32, 16, 16, backward=True)
+    y, _ = s.forward(*(x[m] for m in FWD))
+    with pytest.raises(lib.AdjError):
+        s.forward(y, *(x[m] for m in FWD[1:]))
+    with pytest.raises(lib.AdjError):
+        s.forward(*(x[m] for m in FWD), None, y)
+    dx = s.backward(*(x[m] for m in FWD), x["go"]).dx
+    with pytest.raises(lib.AdjError):
+        s.backward(*(x[m] for m in FWD), dx)
+    c = lm.ShortConv(1, 32, 16, backward=True)
+    w = torch.zeros(16, 4, device="cuda")
+    y, _ = c.forward(x["x"], w)
+    with pytest.raises(lib.AdjError):
+        c.forward(y, w)
+    with pytest.raises(lib.AdjError):
+        c.backward(x["x"], w, c.backward(x["x"], w, x["go"])[0])
+
+
+def test_graph_takes_new_offsets():
+    """Offsets are read on the device: a captured call follows what they hold when it is replayed."""
+    from adjoint_gradients_long_gb300 import lm
+    x, _ = scan_case(12, 3, 160, 24, 8, True, lengths=[50, 60, 50])
+    s = lm.SelScan(3, 160, 24, 8, packed=True, backward=True)
+    scan_run(s, x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, s1, r = scan_run(s, x)
+    for lengths in ([1, 0, 159], [100, 30, 30]):
+        x["offsets"].copy_(offsets_of(lengths))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in (y, s1, *r)]
+        fresh = lm.SelScan(3, 160, 24, 8, packed=True, backward=True)
+        a, b, g = scan_run(fresh, x)
+        assert all(torch.equal(o, p) for o, p in zip(got, (a, b, *g)))

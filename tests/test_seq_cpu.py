@@ -109,8 +109,11 @@ def test_conv_dims_refused(L, bad, status):
     assert L.adj_conv_workspace_bytes(conv(**bad)) == 0
 
 
+A1, A2 = FAKE + (1 << 20), FAKE + (2 << 20)
+
+
 def test_conv_pointers_refused(L):
-    args = dict(x=FAKE, w=FAKE, bias=None, s0=None, off=None, y=FAKE, s1=None)
+    args = dict(x=FAKE, w=FAKE, bias=None, s0=None, off=None, y=A1, s1=None)
 
     def fwd(d=None, **kw):
         return L.adj_conv_fwd(d or conv(), *{**args, **kw}.values(), None)
@@ -119,10 +122,11 @@ def test_conv_pointers_refused(L):
     for n in ("bias", "s0", "s1"):
         assert fwd(**{n: FAKE + 8}) == 3
     assert fwd(off=FAKE) == 1 and fwd(conv(packed=1)) == 1                 # offsets and packed together
+    assert fwd(y=FAKE) == 1 and fwd(s0=A2, s1=A2) == 1                      # an output that is an input
     assert fwd(conv(packed=1), off=FAKE + 4) == 3
     assert fwd(conv(B=0)) == 0
     need = L.adj_conv_workspace_bytes(conv())
-    back = dict(x=FAKE, w=FAKE, bias=None, s0=None, off=None, go=FAKE, ds1=None, dx=FAKE, dw=FAKE, dbias=None, ds0=None, ws=FAKE)
+    back = dict(x=FAKE, w=FAKE, bias=None, s0=None, off=None, go=FAKE, ds1=None, dx=A1, dw=A1, dbias=None, ds0=None, ws=FAKE)
 
     def bwd(ws_bytes=BIG, **kw):
         return L.adj_conv_bwd(conv(), *{**back, **kw}.values(), ws_bytes, None)
@@ -131,6 +135,7 @@ def test_conv_pointers_refused(L):
     for n in ("ds1", "dbias", "ds0", "dw"):
         assert bwd(**{n: FAKE + 8}) == 3, n
     assert bwd(ws=FAKE + 64) == 3 and bwd(ws_bytes=need - 1) == 5
+    assert bwd(dx=FAKE) == 1 and bwd(ds1=A2, ds0=A2) == 1 and bwd(s0=A2, ds0=A2) == 1
 
     def step(d=None, x=FAKE, state=FAKE, n=4, slots=FAKE):
         return L.adj_conv_step(d or conv(), x, FAKE, None, state, n, slots, FAKE, None)
@@ -157,7 +162,7 @@ def test_scan_dims_refused(L, bad, status):
 
 
 def test_scan_pointers_refused(L):
-    args = dict(x=FAKE, dt=FAKE, A=FAKE, Bm=FAKE, Cm=FAKE, D=None, z=None, bias=None, s0=None, off=None, y=FAKE, s1=None, ws=FAKE)
+    args = dict(x=FAKE, dt=FAKE, A=FAKE, Bm=FAKE, Cm=FAKE, D=None, z=None, bias=None, s0=None, off=None, y=A1, s1=None, ws=FAKE)
 
     def fwd(d=None, ws_bytes=BIG, **kw):
         return L.adj_ssm_fwd(d or ssm(), *{**args, **kw}.values(), ws_bytes, None)
@@ -166,11 +171,12 @@ def test_scan_pointers_refused(L):
     for n in ("D", "z", "bias", "s0", "s1"):
         assert fwd(**{n: FAKE + 8}) == 3, n
     assert fwd(off=FAKE) == 1 and fwd(ssm(packed=1)) == 1 and fwd(ssm(B=0)) == 0
+    assert fwd(y=FAKE) == 1 and fwd(z=A1) == 1 and fwd(s0=A2, s1=A2) == 1
     need = L.adj_ssm_workspace_bytes(ssm(), lib.OP_SSM_FWD)
     assert fwd(ws_bytes=need - 1) == 5
     assert L.adj_ssm_workspace_bytes(ssm(), lib.OP_SSM_BWD) > need and L.adj_ssm_workspace_bytes(ssm(), lib.OP_FWD) == 0
-    back = dict(x=FAKE, dt=FAKE, A=FAKE, Bm=FAKE, Cm=FAKE, D=None, z=None, bias=None, s0=None, off=None, go=FAKE, ds1=None, dx=FAKE,
-                ddt=FAKE, dA=FAKE, dB=FAKE, dC=FAKE, dD=None, dz=None, dbias=None, ds0=None, ws=FAKE)
+    back = dict(x=FAKE, dt=FAKE, A=FAKE, Bm=FAKE, Cm=FAKE, D=None, z=None, bias=None, s0=None, off=None, go=FAKE, ds1=None, dx=A1,
+                ddt=A1, dA=A1, dB=A1, dC=A1, dD=None, dz=None, dbias=None, ds0=None, ws=FAKE)
 
     def bwd(ws_bytes=BIG, **kw):
         return L.adj_ssm_bwd(ssm(), *{**back, **kw}.values(), ws_bytes, None)
@@ -178,7 +184,8 @@ def test_scan_pointers_refused(L):
         assert bwd(**{n: None}) == 1, n
     for n in ("ds1", "dD", "dbias", "ds0"):
         assert bwd(**{n: FAKE + 8}) == 3, n
-    assert bwd(z=FAKE) == 1 and bwd(dz=FAKE) == 1                          # z and dz together
+    assert bwd(z=FAKE) == 1 and bwd(dz=A1) == 1                            # z and dz together
+    assert bwd(dx=FAKE) == 1 and bwd(dB=FAKE) == 1 and bwd(ds1=A2, ds0=A2) == 1
     assert bwd(ws_bytes=L.adj_ssm_workspace_bytes(ssm(), lib.OP_SSM_BWD) - 1) == 5
 
     def step(d=None, x=FAKE, state=FAKE, n=4, slots=FAKE):
