@@ -5,7 +5,8 @@
 // the sums of a token in registers, so each value is read once (and W-1 of them again by the run
 // after it, mostly from L2) and written once.  Bound by HBM: the arithmetic is W multiply-adds and
 // one sigmoid a value.  Four channels, not eight: eight took 162 registers forwards and 255 backwards,
-// too few warps to cover HBM's latency.  A block holds VG quads of channels side by side and
+// too few warps to cover HBM's latency.  Measured: 32768 tokens x 2048 channels bf16 51 us (0.77 of the copy
+// bandwidth), gradients of 16384 tokens 54 us (0.55).  A block holds VG quads of channels side by side and
 // 256 / VG runs, VG the power of two that covers the channels, 64 at most: neighbouring threads
 // read neighbouring quads.
 //
@@ -20,9 +21,21 @@ namespace adj {
 namespace {
 
 constexpr int CT = 256;         // threads of a block
-// tokens that a thread fetches together (and as many are on their way behind them)
-template <class T>
-constexpr int FETCH = sizeof(T) == 2 ? 4 : 2;
+// A thread's next tokens, on their way to its own places in shared memory, 32 KB a block: as many in registers
+// would leave too few warps.  It waits for its own copies alone.
+template <class T, int ARRAYS>
+struct Ring {
+    static constexpr int TOKENS = int(32768 / (CT * sizeof(Raw4<T>) * ARRAYS));     // a power of two
+    Raw4<T> v[TOKENS][ARRAYS][CT];
+    __device__ __forceinline__ Raw4<T> get(int i, int array) const { return v[i & (TOKENS - 1)][array][threadIdx.x]; }
+    __device__ __forceinline__ void start(int i, int array, const T *p) {
+        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&v[i & (TOKENS - 1)][array][threadIdx.x]));
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(p), "n"(sizeof(Raw4<T>)) : "memory");
+    }
+    __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    template <int N>
+    __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+};
 
 template <class T>
 __device__ __forceinline__ const T *row(const void *p, int64_t i, int64_t ld, int c) {
@@ -103,6 +116,8 @@ struct Place {
 // Blocks below `runs` take tokens, those above write the states after the last tokens.
 template <class T, int W>
 __global__ __launch_bounds__(CT, 4) void k_conv_fwd(const ConvArgs a, int vg, int tr, int64_t runs) {
+    typedef Ring<T, 1> R;
+    __shared__ R ring;
     __shared__ int64_t offs[NEAR + 1];
     const Seqs q = near(a.q, offs);
     const Place at(vg, a.P);
@@ -133,11 +148,16 @@ __global__ __launch_bounds__(CT, 4) void k_conv_fwd(const ConvArgs a, int vg, in
         const T *px = row<T>(a.x, t, a.ldx, c);
         T *py = static_cast<T *>(a.y) + t * a.ldy + c;
         const int n = int(end - t);
-        constexpr int FU = FETCH<T>;
-        Raw4<T> next[FU];
+        constexpr int FU = 4, AHEAD = R::TOKENS / FU - 1;
+        auto fetch = [&](int i) {
 #pragma unroll
-        for (int u = 0; u < FU; ++u)
-            if (u < n) next[u].load(px + u * a.ldx);
+            for (int u = 0; u < FU; ++u)
+                if (i + u < n) ring.start(i + u, 0, px + u * a.ldx);
+            px += FU * a.ldx;
+            ring.commit();
+        };
+#pragma unroll
+        for (int g = 0; g < AHEAD; ++g) fetch(g * FU);
         auto token = [&](const Raw4<T> &in) {
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) x[j] = x[j + 1];
@@ -149,13 +169,11 @@ __global__ __launch_bounds__(CT, 4) void k_conv_fwd(const ConvArgs a, int vg, in
             py += a.ldy;
         };
         for (int i = 0; i < n; i += FU) {
+            fetch(i + AHEAD * FU);
+            ring.template wait<AHEAD>();
             Raw4<T> now[FU];
 #pragma unroll
-            for (int u = 0; u < FU; ++u) now[u] = next[u];
-            px += FU * a.ldx;
-#pragma unroll
-            for (int u = 0; u < FU; ++u)
-                if (i + FU + u < n) next[u].load(px + u * a.ldx);
+            for (int u = 0; u < FU; ++u) now[u] = ring.get(i + u, 0);
             if (i + FU <= n) {                                      // straight on: the window moves by names alone
 #pragma unroll
                 for (int u = 0; u < FU; ++u) token(now[u]);
@@ -172,6 +190,8 @@ __global__ __launch_bounds__(CT, 4) void k_conv_fwd(const ConvArgs a, int vg, in
 // Blocks below `runs` take tokens, those above write ds0.
 template <class T, int W>
 __global__ __launch_bounds__(CT, 2) void k_conv_bwd(const ConvArgs a, int vg, int tr, int64_t runs) {
+    typedef Ring<T, 2> R;
+    __shared__ R ring;
     __shared__ float4 sum[CT];
     __shared__ int64_t offs[NEAR + 1];
     const Seqs q = near(a.q, offs);
@@ -254,27 +274,29 @@ __global__ __launch_bounds__(CT, 2) void k_conv_bwd(const ConvArgs a, int vg, in
         // counted from the first token here: tokens that exist, that this run sums up and emits, that it walks
         const int left = int(min(end - t, int64_t(tr + W))), own = int(last - t), all = int(until - t);
         const int64_t tail = end - (W - 1) - t;                     // the first token that s1 holds
-        constexpr int CU = FETCH<T> / 2;
-        Raw4<T> nx[CU], ng[CU];
+        constexpr int CU = R::TOKENS / 2, AHEAD = R::TOKENS / CU - 1;
         auto fetch = [&](int i) {
 #pragma unroll
             for (int u = 0; u < CU; ++u)
                 if (i + u < left && i + u < all) {
-                    nx[u].load(px + u * a.ldx);
-                    ng[u].load(pg + u * a.ldy);
+                    ring.start(i + u, 0, px + u * a.ldx);
+                    ring.start(i + u, 1, pg + u * a.ldy);
                 }
             px += CU * a.ldx;
             pg += CU * a.ldy;
+            ring.commit();
         };
-        fetch(0);
+#pragma unroll
+        for (int g = 0; g < AHEAD; ++g) fetch(g * CU);
         for (int i = 0; i < all; i += CU) {
+            fetch(i + AHEAD * CU);
+            ring.template wait<AHEAD>();
             Raw4<T> cx[CU], cg[CU];
 #pragma unroll
             for (int u = 0; u < CU; ++u) {
-                cx[u] = nx[u];
-                cg[u] = ng[u];
+                cx[u] = ring.get(i + u, 0);
+                cg[u] = ring.get(i + u, 1);
             }
-            fetch(i + CU);
             // dx of the token W-1 behind: complete now
             auto emit = [&](Four d) {
 #pragma unroll
