@@ -911,11 +911,12 @@ __global__ __launch_bounds__(256) void k_ssm_join(const SsmArgs a, int64_t cols,
 // ---------------------------------------------------------------- single tokens
 // A thread takes four states of each of K channels, K the number of quads of states, 4 at most: its K loads of
 // the state are in flight together, and the steps of the K channels are formed by one lane each.
-// The state is read and written once, bound by HBM.
+// The state is read and written once, bound by HBM; blocks of 128, not 256: 20.7 us against 22.7 for 256 sequences
+// of 2048 x 16 out of cold memory, where all blocks together are three turns of the machine.
 template <class T, int N>
-__global__ __launch_bounds__(256) void k_ssm_step(const SsmArgs a, float *state, int64_t n_slots, const int32_t *slots) {
+__global__ __launch_bounds__(128) void k_ssm_step(const SsmArgs a, float *state, int64_t n_slots, const int32_t *slots) {
     constexpr int NQ = N / 4, K = NQ < 4 ? NQ : 4;
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, per = int64_t(a.P) / K * NQ, b = i / per;
+    const int64_t i = int64_t(blockIdx.x) * 128 + threadIdx.x, per = int64_t(a.P) / K * NQ, b = i / per;
     if (b >= a.q.B) return;                                         // whole groups of NQ lanes
     const int r = int(i - b * per), nq = r % NQ, c0 = r / NQ * K, k0 = nq % K, p = c0 + k0;
     const uint32_t group = (NQ == 32 ? ~0u : (1u << NQ) - 1) << (threadIdx.x & 31 & ~(NQ - 1));
@@ -1073,7 +1074,7 @@ cudaError_t launch_ssm_step(const SsmArgs &a, bool bf16, float *state, int64_t n
         typedef decltype(t) T;
         constexpr int N = decltype(n)::value;
         ProfScope p(K_SSM_STEP, st);
-        k_ssm_step<T, N><<<unsigned(seq_div(a.q.B * (a.P / std::min(4, N / 4)) * (N / 4), 256)), 256, 0, st>>>(a, state, n_slots, slots);
+        k_ssm_step<T, N><<<unsigned(seq_div(a.q.B * (a.P / std::min(4, N / 4)) * (N / 4), 128)), 128, 0, st>>>(a, state, n_slots, slots);
         return cudaGetLastError();
     });
 }
