@@ -39,10 +39,10 @@ def _check(name, x, shape, dtype, device):
 
 def _dense(name, x, shape, dtype, device):
     """The address of a dense tensor."""
+    if x.dtype is dtype and x.shape == shape and x.device == device and x.is_contiguous():
+        return x.data_ptr()
     _check(name, x, shape, dtype, device)
-    if not x.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor, got strides {x.stride()}")
-    return x.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous tensor, got strides {x.stride()}")
 
 
 def _device(device):
@@ -290,7 +290,8 @@ class _Seq:
 
     def _pitch(self, name, x, shape):
         """The distance of two tokens in x."""
-        _check(name, x, shape, self.xt, self.device)
+        if x.dtype is not self.xt or x.shape != shape or x.device != self.device:
+            _check(name, x, shape, self.xt, self.device)
         if x.is_contiguous():
             return shape[-1]
         s = x.stride()
@@ -403,14 +404,14 @@ class ShortConvStep(_Seq):
         if lib.conv_workspace_bytes(self.dims) == 0:
             raise ValueError("unsupported convolution sizes")
         self.y = self._new(self.x)
-        self._step = lib.bind("adj_conv_step", ctypes.byref(self.dims))
+        self._step, self._out = lib.bind("adj_conv_step", ctypes.byref(self.dims)), self.y.data_ptr()
 
     def step(self, x, w, state, bias=None, slots=None):
         """y [B,P].  slots [B] int32: sequence b's state is state[slots[b]] (a slot outside the pool:
         padding, a row of zeros); None: state[b]."""
         self.dims.ldx = self._pitch("x", x, self.x)
         self._step(x.data_ptr(), self._f32("w", w, self.w), self._f32("bias", bias, self.w[:1]),
-                   *self._pool(state, (self.w[1] - 1, self.w[0]), self.xt, slots), self.y.data_ptr(), raw_stream(self.device))
+                   *self._pool(state, (self.w[1] - 1, self.w[0]), self.xt, slots), self._out, raw_stream(self.device))
         return self.y
 
 
@@ -499,13 +500,13 @@ class SelScanStep(_Sel):
         if lib.ssm_workspace_bytes(self.dims, lib.OP_SSM_FWD) == 0:
             raise ValueError("unsupported selective-scan sizes")
         self.y = self._new(self.x)
-        self._step = lib.bind("adj_ssm_step", ctypes.byref(self.dims))
+        self._step, self._out = lib.bind("adj_ssm_step", ctypes.byref(self.dims)), self.y.data_ptr()
 
     def step(self, x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, slots=None):
         """y [B,P].  slots [B] int32: sequence b's state is state[slots[b]] (a slot outside the pool:
         padding, a row of zeros); None: state[b]."""
         self._step(*self._tokens(x, dt, A, Bm, Cm), *self._extras(D, z, dt_bias),
-                   *self._pool(state, self.A, torch.float32, slots), self.y.data_ptr(), raw_stream(self.device))
+                   *self._pool(state, self.A, torch.float32, slots), self._out, raw_stream(self.device))
         return self.y
 
 
