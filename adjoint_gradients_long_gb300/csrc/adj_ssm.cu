@@ -564,6 +564,7 @@ __global__ __launch_bounds__(32 * WPB, 3) void k_ssm_out(const SsmArgs a, int64_
     };
     fetch(l.t0);
     for (int64_t t = l.t0; t < l.t1; t += K::TT) {
+        v.at(l, t);
         mk.at<K::TT>(a.q, t, l.lo, l.hi, true);
         __syncwarp();
         stage_steps<T, K>(v, rx, rdt, ds, us);

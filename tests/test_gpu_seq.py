@@ -248,6 +248,15 @@ def test_scan_rows_of_no_sequence_stay():
         assert all(torch.isfinite(o).all() for o in (s1, r.dA, r.dD, r.ddt_bias, r.ds0))
 
 
+@pytest.mark.parametrize("before", [1, 3, 20, 37])
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+def test_scan_sequences_within_the_tokens(N, before):
+    """Tokens of no sequence on both sides, at places inside a tile."""
+    for T, lengths in ((200, [50, 0, 77]), (700, [5, 300, 301])):
+        for bf16 in (False, True):
+            scan_check(N + before, 3, T, 40, N, bf16, lengths=lengths, before=before)
+
+
 def test_scan_values_that_are_not_finite_stay_in_their_sequence():
     from adjoint_gradients_long_gb300 import lm
     for N in (8, 16):
@@ -437,6 +446,44 @@ def test_outputs_given_as_inputs_are_refused():
         c.forward(y, w)
     with pytest.raises(lib.AdjError):
         c.backward(x["x"], w, c.backward(x["x"], w, x["go"])[0])
+
+
+def test_addresses_past_32_bits():
+    """Rows and slots behind the first 2^31 elements give what dense copies of them give."""
+    from adjoint_gradients_long_gb300 import lm
+    T, P, N, ld = 1100, 16, 8, 1 << 21
+    g = torch.Generator(device="cuda").manual_seed(0)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=g)                    # noqa: E731
+    base = torch.empty(T, ld, dtype=torch.bfloat16, device="cuda")
+    cols = [base[:, -c - 64:][:, :n] for c, n in ((0, P), (128, P), (256, P), (384, N), (512, N))]
+    for c in cols:
+        c.copy_(rand(*c.shape))
+    w, b, A, D = rand(P, 4), rand(P), -rand(P, N).abs(), rand(P)
+    go, off = rand(T, P).bfloat16(), torch.tensor([0, 500, T], device="cuda")
+    assert T * ld > 2 ** 31
+    got = []
+    for x, dt, z, Bm, Cm in (cols, [c.contiguous() for c in cols]):
+        conv, scan = (k(2, T, P, n, packed=True, backward=True) for k, n in ((lm.ShortConv, 4), (lm.SelScan, N)))
+        got.append((*conv.forward(x, w, b, None, off), *conv.backward(x, w, go, b, None, None, off),
+                    *scan.forward(x, dt, A, Bm, Cm, D, z, b, None, off), *scan.backward(x, dt, A, Bm, Cm, go, D, z, b, None, None, off)))
+        del conv, scan
+    assert all(same_bits(a, c) for a, c in zip(*got))
+    del base, cols, got
+    slots = torch.tensor([5, 0], dtype=torch.int32, device="cuda")
+    for dtype, entry in ((torch.bfloat16, (3, 8192)), (torch.float32, (8192, 64))):
+        n = 2 ** 31 // (entry[0] * entry[1]) + 8
+        pool, small = torch.empty(n, *entry, dtype=dtype, device="cuda"), rand(8, *entry).to(dtype)
+        pool[n - 8:] = small
+        x = rand(2, 8192).bfloat16()
+        ys = []
+        for at, s in ((pool, slots + (n - 8)), (small, slots)):
+            if dtype is torch.bfloat16:
+                ys.append(lm.ShortConvStep(2, 8192).step(x, b.new_ones(8192, 4), at, None, s))
+            else:
+                m = x[:, :64].contiguous()
+                ys.append(lm.SelScanStep(2, 8192, 64).step(x, x, -b.new_ones(entry), m, m, at, None, x, None, s))
+        assert same_bits(*ys) and same_bits(pool[n - 8:], small)
+        del pool
 
 
 def test_graph_takes_new_offsets():
