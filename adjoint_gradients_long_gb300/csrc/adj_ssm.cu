@@ -687,7 +687,7 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
             rC.stage(l, Cs);
             float s0, s1;
             upk(s[0], s0, s1);
-            if (s0 >= 0.f) {
+            if (!(s0 < 0.f)) {                                      // a NaN is its own channel's alone
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
 #pragma unroll

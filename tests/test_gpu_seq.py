@@ -277,6 +277,29 @@ def test_scan_values_that_are_not_finite_stay_in_their_sequence():
                 assert all(same_bits(got[i][b], clean[i][b]) for b in (0, 2, 3)), (n, i)
 
 
+def test_scan_a_channel_that_is_not_finite_stays_alone():
+    """In all that belongs to one channel the others keep their bits (B and C are read by all)."""
+    from adjoint_gradients_long_gb300 import lm
+    for N in (8, 16, 32, 64):
+        for bad in (0, 5, 39):
+            x, _ = scan_case(4, 2, 700, 40, N, True)
+            s = lm.SelScan(2, 700, 40, N, backward=True)
+            keep = [c for c in range(40) if c != bad]
+            clean = [o.clone() for o in (lambda y, s1, r: (y, s1, *r))(*scan_run(s, x))]
+            for n in ("x", "dt", "z", "go"):
+                dirty = dict(x)
+                dirty[n] = x[n].clone()
+                dirty[n][0, 20, bad] = float("nan")
+                y, s1, r = scan_run(s, dirty)
+                got = (y, s1, *r)
+                for i in (0, 2, 3, 8):                      # y, dx, ddt, dz
+                    assert same_bits(got[i][..., keep], clean[i][..., keep]), (N, bad, n, i)
+                for i in (1, 10):                           # s1, ds0
+                    assert same_bits(got[i][:, keep], clean[i][:, keep]), (N, bad, n, i)
+                for i in (4, 7, 9):                         # dA, dD, ddt_bias
+                    assert same_bits(got[i][keep], clean[i][keep]), (N, bad, n, i)
+
+
 def test_scan_step_of_zero_keeps_the_state():
     """dt of minus infinity: the decay is one and nothing comes in, bit for bit."""
     from adjoint_gradients_long_gb300 import lm
