@@ -530,7 +530,7 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
     {
         // log2 e / temperature as a pair: the quotient, and the quotient of what it leaves
         constexpr float H = 1.44269502162933349609375f, L = 1.925963033500011079e-8f;
-        weigh.hi = fminf(H / temperature, 3.402823466e38f);
+        weigh.hi = temperature == 0.f ? 3.402823466e38f : fminf(H / temperature, 3.402823466e38f);     // -0 too
         // none for an infinite temperature, nor for one near zero (a difference of logits is far there)
         weigh.lo = weigh.hi == 0.f || weigh.hi > 1e37f ? 0.f : (fmaf(-weigh.hi, temperature, H) + L) / temperature;
     }
@@ -539,7 +539,7 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
     weigh.never = DEAD;
     if (min_p > 0.f) {
         const float p = fminf(min_p, 1.f), t = -log2f(p);
-        weigh.least = max(uint64_t(1), uint64_t(ceilf(p * 1099511627776.f)))      /* 2^40: exact */;
+        weigh.least = max(uint64_t(1), uint64_t(ceilf(p * 1099511627776.f)));     // 2^40 p: exact
         const float out = weigh.least < 1024 ? 2.f : 0.01f;         // outside log2f's error and the weights' rounding
         weigh.sure = fminf(weigh.sure, t - out);
         weigh.never = fminf(weigh.never, t + out);

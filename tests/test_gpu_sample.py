@@ -1,6 +1,6 @@
 """GPU sampling against the definition with Python's whole numbers (oracle/seq.py).
 
-Tokens are equal: the kernel's weights are off by a few units of 2^-40, so a draw differs where u lies
+Tokens are equal: the kernel's weights are off by one unit of 2^-40 at most, so a draw differs where u lies
 that close to a border, which for the seeded rows here has a chance below 1e-6.  logp: the distance and a
 logarithm, each to 2^-23 of values up to 30, and the total's 2^-24: 1e-5.
 """
@@ -123,6 +123,15 @@ def test_settings_at_their_ends():
     check(x, [0.0, 1.0, -1.0, 2.0, nan, 1 - 2.0 ** -24, 0.5, 1e-40, math.inf, -math.inf], top_p=[0.9] * 10)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_temperature_of_either_zero(bf16):
+    for V in (3, 500, 20000):
+        x, u = logits(2, V, bf16, 8)
+        want = check(x, u, temperature=[0.0] * 2)
+        assert check(x, u, temperature=[-0.0] * 2) == want == x.argmax(1).tolist()
+        check(x, u, temperature=[-0.0] * 2, top_k=[2] * 2, top_p=[0.5] * 2, min_p=[0.1] * 2)
+
+
 def test_rows_strided_and_ragged():
     """Rows at every alignment, and a row alone or in a batch: the same token."""
     from adjoint_gradients_long_gb300 import lm
@@ -137,6 +146,19 @@ def test_rows_strided_and_ragged():
         one = lm.Sampler(1, 9000, x_bf16=bf16)
         for i in (0, 17, 299):
             assert one.sample(x[i:i + 1], t(u[i:i + 1]), **{n: v[i:i + 1] for n, v in kw})[0].item() == all_rows[i]
+
+
+def test_rows_past_32_bits():
+    from adjoint_gradients_long_gb300 import lm
+    N, V, ld = 1100, 50, 1 << 21
+    wide = torch.empty(N, ld, dtype=torch.bfloat16, device="cuda")[:, ld - 99:][:, :V]
+    x, u = logits(N, V, True, 9)
+    wide.copy_(x)
+    assert (N - 1) * ld > 2 ** 31
+    s, p, u = lm.Sampler(N, V), torch.full((N,), 0.9, device="cuda"), torch.tensor(u, dtype=torch.float32, device="cuda")
+    token, logp = (o.clone() for o in s.sample(x, u, top_p=p))
+    again, logp2 = s.sample(wide, u, top_p=p)
+    assert torch.equal(token, again) and torch.equal(logp, logp2)
 
 
 def test_graph_takes_new_numbers():
