@@ -156,6 +156,8 @@ adj_status adj_conv_step(const adj_conv_dims *dims, const void *x, const float *
     ADJ_TRY(may({bias}));
     ADJ_TRY(check_slots(a.q.B, n_slots, slots));
     if (a.q.B == 0) return ADJ_OK;
+    ADJ_TRY(apart({y, state}, {x, w, bias, slots}));
+    if (y == state) return ADJ_EINVAL;
     a.x = x; a.w = w; a.bias = bias; a.y = y;
     return done(launch_conv_step(a, dims->x_dtype == ADJ_BF16, state, n_slots, slots, static_cast<cudaStream_t>(stream)));
 }
@@ -212,6 +214,8 @@ adj_status adj_ssm_step(const adj_ssm_dims *dims, const void *x, const void *dt,
     ADJ_TRY(may({D, z, dt_bias}));
     ADJ_TRY(check_slots(a.q.B, n_slots, slots));
     if (a.q.B == 0) return ADJ_OK;
+    ADJ_TRY(apart({y, state}, {x, dt, A, Bm, Cm, D, z, dt_bias, slots}));
+    if (y == state) return ADJ_EINVAL;
     a.x = x; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.D = D; a.z = z; a.bias = dt_bias; a.y = y;
     return done(launch_ssm_step(a, dims->x_dtype == ADJ_BF16, state, n_slots, slots, static_cast<cudaStream_t>(stream)));
 }

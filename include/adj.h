@@ -371,8 +371,8 @@ adj_status adj_grad_clip(const adj_grad_seg *segs, int64_t nseg, float max_norm,
  * reaches from one sequence into another, values that are not finite included (but for
  * gradients of parameters, which sum over all).
  * ld*: elements from one token to the next (so that arrays may be column slices of one
- * projection), multiples of 16 bytes.  Prompts and gradients: no output may overlap an input (s1 with s0,
- * ds0 with ds1 included); the same address twice is refused.  A pool of states has n_slots entries; slots [B] int32
+ * projection), multiples of 16 bytes.  No output may overlap an input (s1 with s0, ds0
+ * with ds1, a step's y with what it reads) or another output; an input's address as an output is refused.  A pool of states has n_slots entries; slots [B] int32
  * gives the entry of each sequence (NULL: entry b, needs n_slots >= B).  A slot outside
  * [0, n_slots) leaves the pool untouched and gives a row of zeros (the padding of a batch); a
  * slot given twice is a race.
@@ -460,7 +460,7 @@ adj_status adj_ssm_step(const adj_ssm_dims *dims, const void *x, const void *dt,
  *   logp      log(w_j / total), from (x_j - m) / temperature itself
  * u [N] fp32 in [0, 1) (others are taken as the nearest such number, NaN as 0).  Temperature 0 takes
  * the largest logit, the lowest index first; top_p >= 1 and min_p <= 0 keep all, min_p > 1 and top_p <= 0
- * the largest alone.  Minus infinity is a masked token.  Weights are off by a few units of 2^-40; as they
+ * the largest alone.  Minus infinity is a masked token.  Weights are off by one unit at most; as they
  * are whole numbers the result does not depend on the order of sums, and equal rows give equal tokens.
  * token [N] int64 and logp [N] fp32 (NULL: not written).  Without a finite value a row gives token -1 and
  * logp -inf; with a NaN or +inf in it, or a setting that is NaN or a negative temperature, token -1 and

@@ -194,6 +194,19 @@ def test_scan_pointers_refused(L):
     assert step(n=1, slots=None) == 2 and step(n=-1) == 2 and step(ssm(B=0)) == 0
 
 
+def test_steps_outputs_apart(L):
+    """A step's y is none of what it reads, and neither is its pool."""
+    def conv_step(x=FAKE, w=FAKE, bias=None, state=A1, slots=None, y=A2):
+        return L.adj_conv_step(conv(), x, w, bias, state, 4, slots, y, None)
+
+    def scan_step(x=FAKE, dt=FAKE, A=FAKE, Bm=FAKE, Cm=FAKE, D=None, z=None, bias=None, state=A1, slots=None, y=A2):
+        return L.adj_ssm_step(ssm(), x, dt, A, Bm, Cm, D, z, bias, state, 4, slots, y, None)
+    for step, names in ((conv_step, "x w bias slots"), (scan_step, "x dt A Bm Cm D z bias slots")):
+        for n in names.split():
+            assert step(**{n: A1}) == 1 and step(**{n: A2}) == 1, n
+        assert step(state=A2) == 1
+
+
 def test_scan_workspace_is_bounded(L):
     """Backwards: a state for every tile of tokens, the segments', and partial sums of dB and dC."""
     for P, N, T in ((1024, 16, 65536), (2048, 16, 16384), (8, 64, 100000), (4096, 8, 777)):
