@@ -44,10 +44,6 @@ struct Raw8<float> {
         a = __ldg(reinterpret_cast<const float4 *>(p));
         b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
     }
-    __device__ __forceinline__ void load_own(const float *p) {
-        a = reinterpret_cast<const float4 *>(p)[0];
-        b = reinterpret_cast<const float4 *>(p)[1];
-    }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
@@ -57,7 +53,6 @@ template <>
 struct Raw8<__nv_bfloat16> {
     uint4 u;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void load_own(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -68,6 +63,7 @@ struct Raw8<__nv_bfloat16> {
         }
     }
 };
+
 // ---------------------------------------------------------------- four channels, as they are stored
 template <class T>
 struct Raw4;

@@ -628,8 +628,8 @@ __global__ __launch_bounds__(32 * WPB, 3) void k_ssm_out(const SsmArgs a, int64_
 template <int N>
 struct GradSm {                         // floats of a warp's part
     typedef Tile<N, 2, true> K;
-    // tokens of a group, whose states and decays stay in registers: four spill (300 bytes, 672 us against 653 for the
-    // training batch below), but with 64 states the room for those of every second token is not there
+    // tokens of a group, whose states and decays stay in registers: four spill (300 bytes; 672 us against 653 for
+    // 16384 x 2048 x 16 when this was chosen), but with 64 states the room for those of every second token is not there
     static constexpr int GB = N == 64 ? 4 : 2;
     static constexpr int CK = K::TT / GB * 512;                     // states at every GB-th token, [.][4][32] x 4
     static constexpr int SUM = K::TT * 2 * N;                       // dB and dC of a tile over the warp's channels
@@ -811,8 +811,8 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
                 }
             }
             // To shared memory when the group is done, so that no store holds up a token's loads: m B, and over what is
-            // done with, A e h (u's rows) and v (g's).  Every lane has read those rows, as the exchanges need
-            // all lanes' sums.
+            // done with, A e h (u's rows) and v (g's)
+            __syncwarp();
 #pragma unroll
             for (int j = 0; j < GB; ++j) {
                 const int i = g * GB + j;
@@ -925,7 +925,7 @@ __global__ __launch_bounds__(128) void k_ssm_step(const SsmArgs a, float *state,
     const int64_t i = int64_t(blockIdx.x) * 128 + threadIdx.x, per = int64_t(a.P) / K * NQ, b = i / per;
     if (b >= a.q.B) return;                                         // whole groups of NQ lanes
     const int r = int(i - b * per), nq = r % NQ, c0 = r / NQ * K, k0 = nq % K, p = c0 + k0;
-    const uint32_t group = (NQ == 32 ? ~0u : (1u << NQ) - 1) << (threadIdx.x & 31 & ~(NQ - 1));
+    const uint32_t group = ((1u << NQ) - 1) << (threadIdx.x & 31 & ~(NQ - 1));
     T *y = static_cast<T *>(a.y) + b * a.ldy + p;
     const int64_t slot = slots ? int64_t(__ldg(slots + b)) : b;
     if (slot < 0 || slot >= n_slots) {                              // the whole group

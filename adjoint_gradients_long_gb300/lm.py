@@ -319,8 +319,9 @@ class _Seq:
         return at, n, slots
 
     def _new(self, shape, dtype=None):
-        """An output.  Zeros at first: rows of no sequence are not written."""
-        return torch.zeros(shape, dtype=dtype or self.xt, device=self.device)
+        """An output.  Packed, zeros at first: rows of no sequence are not written."""
+        make = torch.zeros if self.packed else torch.empty
+        return make(shape, dtype=dtype or self.xt, device=self.device)
 
     def _like(self, name, x):
         """The gradient of x, in x's layout: one array for each layout that has been met, kept with
@@ -329,7 +330,7 @@ class _Seq:
         if at not in self._strided:
             y = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if at[1] is None
                  else torch.empty_strided(x.shape, at[1], dtype=x.dtype, device=x.device))
-            self._strided[at] = y.zero_()
+            self._strided[at] = y.zero_() if self.packed else y
         return self._strided[at]
 
     @staticmethod
