@@ -88,7 +88,8 @@ template <class K>
 struct Lane {
     int lane, nq, cq, warp, c0;         // c0: the warp's first channel
     int64_t seg, col;                   // segment, block of channels
-    int64_t t0, t1, lo, hi;             // the segment's tokens; those that belong to sequences
+    int64_t t0, t1;                     // the segment's tokens
+    int lo, hi;                         // those that belong to sequences, counted from t0
     bool in;                            // this thread's channels exist
     __device__ Lane(const SsmArgs &a, int64_t block, int64_t cols) {
         lane = threadIdx.x & 31;
@@ -101,11 +102,11 @@ struct Lane {
         in = c0 + cq * K::RC < a.P;
         t0 = seg * a.seglen;
         t1 = min(t0 + a.seglen, a.q.rows);
-        lo = t0;
-        hi = t1;
+        lo = 0;
+        hi = int(t1 - t0);
         if (a.q.off) {
-            lo = max(t0, a.q.at(0));
-            hi = min(t1, a.q.at(a.q.B));
+            lo = int(max(t0, a.q.at(0)) - t0);
+            hi = int(max(t0, min(t1, a.q.at(a.q.B))) - t0);
         }
     }
     // first of the two channels of pair p, inside the warp's
@@ -202,17 +203,17 @@ struct Marks {
     int64_t seq;                        // of this lane's token
     __device__ Marks() : b(-1), begin(0), end(0) {}
     // forwards: the sequence of the last token is remembered, else that of the first
-    template <int TT>
-    __device__ void at(const Seqs &q, int64_t t, int64_t lo, int64_t hi, bool forwards) {
+    template <int TT, class L>
+    __device__ void at(const Seqs &q, const L &l, int64_t t, bool forwards) {
         if (b >= 0 && begin <= t && t + TT <= end) {
             first = begin == t ? 1u : 0u;
             last = end == t + TT ? 1u << (TT - 1) : 0u;
             seq = b;
             return;
         }
-        const int lane = threadIdx.x & 31;
+        const int lane = threadIdx.x & 31, i = int(t - l.t0) + lane;
         const int64_t x = t + lane;
-        int64_t s = lane < TT && x >= lo && x < hi ? q.find(x) : -1, s0 = 0, s1 = 0;
+        int64_t s = lane < TT && i >= l.lo && i < l.hi ? q.find(x) : -1, s0 = 0, s1 = 0;
         if (s >= 0) {
             s0 = q.begin(s);
             s1 = q.end(s);
@@ -222,10 +223,10 @@ struct Marks {
         const uint32_t any = __ballot_sync(~0u, s >= 0);
         seq = s >= 0 ? s : 0;
         if (any) {
-            const int l = forwards ? 31 - __clz(any) : __ffs(any) - 1;
-            b = __shfl_sync(~0u, s, l);
-            begin = __shfl_sync(~0u, s0, l);
-            end = __shfl_sync(~0u, s1, l);
+            const int k = forwards ? 31 - __clz(any) : __ffs(any) - 1;
+            b = __shfl_sync(~0u, s, k);
+            begin = __shfl_sync(~0u, s0, k);
+            end = __shfl_sync(~0u, s1, k);
         }
     }
     __device__ __forceinline__ int64_t of(int i) const { return __shfl_sync(~0u, seq, i); }
@@ -250,8 +251,9 @@ struct Mine {
     // the tile's tokens that belong to sequences: from.. below to, counted from its first
     int from, to;
     __device__ __forceinline__ void at(const Lane<K> &l, int64_t t) {
-        from = l.lo > t ? int(min(l.lo - t, int64_t(K::TT))) : 0;
-        to = l.hi < t + K::TT ? int(max(l.hi - t, int64_t(0))) : K::TT;
+        const int i = int(t - l.t0);
+        from = max(l.lo - i, 0);
+        to = min(l.hi - i, K::TT);
     }
     __device__ __forceinline__ bool ok(int j) const { return in && tok(j) >= from && tok(j) < to; }
     __device__ __forceinline__ void load(Raw4<T> (&r)[K::QPL], const void *p, int64_t ld, int64_t t) const {
@@ -426,7 +428,7 @@ __global__ __launch_bounds__(32 * WPB, 3) void k_ssm_state(const SsmArgs a, int6
             l.store(h, a, a.tile, tile);
             steps(a.tstep, tile);
         }
-        mk.at<K::TT>(a.q, t, l.lo, l.hi, true);
+        mk.at<K::TT>(a.q, l, t, true);
         __syncwarp();
         stage_steps<T, K>(v, rx, rdt, ds, us);
         rB.stage(l, Bs);
@@ -565,7 +567,7 @@ __global__ __launch_bounds__(32 * WPB, 3) void k_ssm_out(const SsmArgs a, int64_
     fetch(l.t0);
     for (int64_t t = l.t0; t < l.t1; t += K::TT) {
         v.at(l, t);
-        mk.at<K::TT>(a.q, t, l.lo, l.hi, true);
+        mk.at<K::TT>(a.q, l, t, true);
         __syncwarp();
         stage_steps<T, K>(v, rx, rdt, ds, us);
         rB.stage(l, Bs);
@@ -660,7 +662,7 @@ __global__ __launch_bounds__(32 * WPB, 2) void k_ssm_grad(const SsmArgs a, int64
     const int tiles = int((l.t1 - l.t0 + K::TT - 1) / K::TT);
     for (int ti = tiles - 1; ti >= 0; --ti) {
         const int64_t t = l.t0 + int64_t(ti) * K::TT, tile = t / K::TT;
-        mk.at<K::TT>(a.q, t, l.lo, l.hi, false);
+        mk.at<K::TT>(a.q, l, t, false);
         // the state before the tile
         States<K> h;
         {
