@@ -544,7 +544,9 @@ __global__ __launch_bounds__(ST) void k_sample(const SampleArgs a, int blocks) {
         weigh.sure = fminf(weigh.sure, t - out);
         weigh.never = fminf(weigh.never, t + out);
     }
-    Cut cut{-INFINITY, 0, 0};                                       // everything
+    // Everything above what has no weight for certain, rounded away from it: a warp whose values all lie below forms none
+    // (152 rows of 50001 fp32 with min-p 0.05: 20 us, against 30)
+    Cut cut{__fsub_rd(top, weigh.never * 1.001f / weigh.hi), 0, 0};
     const bool by_k = top_k > 0 && top_k < a.V, by_p = top_p < 1.f;
     if (temperature == 0.f || (by_k && top_k == 1)) {
         cut = Cut{top, 1, 0};
