@@ -20,7 +20,7 @@
 // read once, and every later pass finds them there.
 //
 // Measured: one row of 32000 bf16 with top-k and top-p 20 us, a chain of meetings of its four blocks; 64 rows of 131072
-// bf16 with top-p 40 us; 152 rows of 50001 fp32 with top-p 67 us, bound by the instructions of the weights
+// bf16 with top-p 40 us; 152 rows of 50001 fp32 with top-p 63 us, bound by the instructions of the weights
 // (55 a token, formed for the bins and again for the draw), without a limit 30 us.
 #include <algorithm>
 

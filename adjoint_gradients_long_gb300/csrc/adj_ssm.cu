@@ -30,7 +30,7 @@
 // Bound by issue: a token of 32 channels of 16 states takes 83 instructions in k_ssm_state, 124 in k_ssm_out and
 // about 370 in k_ssm_grad, of which a packed one holds the issue for nearly two cycles.  16 are exponentials, at 32 a
 // cycle and SM (measured), which alone would take 115 us of a walk over 65536 x 1024 x 16.  Measured there, bf16
-// with gate: 228 + 15 + 319 us; gradients of 16384 x 2048 x 16: 224 + 15 + 622 + 15 us.
+// with gate: 224 + 14 + 322 us; gradients of 16384 x 2048 x 16: 224 + 15 + 614 + 15 us.
 #include <algorithm>
 
 #include "adj_lin.cuh"

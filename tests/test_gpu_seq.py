@@ -117,6 +117,13 @@ def test_conv_forms(kw, bf16):
     conv_check(9, B, sum(kw["lengths"]) if "lengths" in kw else 161, 72, 4, bf16, **kw)
 
 
+@pytest.mark.parametrize("before", [1, 20, 37])
+def test_conv_sequences_within_the_tokens(before):
+    for W in (2, 3, 4):
+        conv_check(13, 3, 200, 72, W, True, lengths=[50, 0, 77], before=before)
+        conv_check(14, 2, 700, 40, W, False, lengths=[1, 633], before=before)
+
+
 def test_conv_long():
     conv_check(4, 1, 3000, 64, 4, True)
 
@@ -448,6 +455,13 @@ def test_carried_on_with_the_objects_own_states():
     assert torch.equal(torch.cat(ys, 1), y) and torch.equal(st, s1)
     assert rel_fro(np64(torch.cat(dxs[::-1], 1)), np64(dx)) <= 2 * HALF     # ds0 between two pieces is rounded
     assert rel_fro(np64(ds), np64(ds0)) <= 2 * HALF
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_more_sequences_than_a_block_reads_together(bf16):
+    lengths = [1, 0, 3, 9] * 65
+    conv_check(10, 260, sum(lengths), 40, 4, bf16, lengths=lengths)
+    scan_check(11, 260, sum(lengths), 24, 16, bf16, lengths=lengths)
 
 
 def test_outputs_given_as_inputs_are_refused():
