@@ -319,7 +319,7 @@ class _Seq:
         return at, n, slots
 
     def _new(self, shape, dtype=None):
-        """An output.  Packed, zeros at first: rows of no sequence are not written."""
+        """An output.  Packed, zeros at first: rows of no sequence are not written, and hold what an older call left."""
         make = torch.zeros if self.packed else torch.empty
         return make(shape, dtype=dtype or self.xt, device=self.device)
 
@@ -344,7 +344,8 @@ class ShortConv(_Seq):
     """A causal convolution of W (2 to 4) taps for each of P channels (a multiple of 8) over B sequences:
     p_t = bias + sum_j w[:, j] c_{t+j}, c the sequence's last W-1 inputs before and its tokens,
     y = p sigmoid(p) with act, else p.  x [B,T,P]; packed: T tokens of all sequences together, x [T,P],
-    and offsets [B+1] int64 where each begins (include/adj.h, "Sequences").  w [P,W] and bias [P]
+    and offsets [B+1] int64 where each begins (include/adj.h, "Sequences"); rows of no sequence are
+    neither read nor written: in the outputs they keep an older call's values.  w [P,W] and bias [P]
     fp32.  backward: also hold what the gradients need."""
 
     def __init__(self, B, T, P, W=4, x_bf16=True, act=True, packed=False, backward=False, device="cuda"):
@@ -441,7 +442,8 @@ class SelScan(_Sel):
     d = softplus(dt + dt_bias), h_t = exp(d A) h_{t-1} + d x B_t, v_t = sum_n C_t h_t + D x_t,
     y = v z sigmoid(z) with z, else v.  x, dt, z [B,T,P], Bm, Cm [B,T,N]; packed: T tokens of all
     sequences together, [T,P] and [T,N], and offsets [B+1] int64 where each begins (include/adj.h,
-    "Sequences").  A [P,N], D, dt_bias [P] and states [B,P,N] fp32.  backward: also hold what the
+    "Sequences"); rows of no sequence are neither read nor written: in the outputs they keep an older
+    call's values, so products over all rows leave them out or clear them.  A [P,N], D, dt_bias [P] and states [B,P,N] fp32.  backward: also hold what the
     gradients need."""
 
     def __init__(self, B, T, P, N, x_bf16=True, packed=False, backward=False, device="cuda"):

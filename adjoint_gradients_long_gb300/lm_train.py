@@ -164,15 +164,19 @@ class SelLm:
 
     def loss_and_grads(self, tokens, targets, offsets):
         """Mean negative log probability of the targets (a device scalar) over packed tokens [T], targets
-        [T] (-1: none, as for rows behind the last document) and offsets [B+1]; fills self.grads."""
+        [T] (-1: none, as for rows of no document) and offsets [B+1]; fills self.grads."""
         P, T = self.P, self.T
+        # The operators leave rows of no document as they were: an older batch's values, which the products below, over
+        # all rows, must not see
+        t = torch.arange(T, device=self.device)
+        nobody = ((t < offsets[0]) | (t >= offsets[-1]))[:, None]
         x = self.E[tokens]
         uz = (x @ self.W_in).bfloat16()
         u, z = uz[:, :P], uz[:, P:]
-        c = self.conv.forward(u, self.w, self.b, None, offsets)[0]
+        c = self.conv.forward(u, self.w, self.b, None, offsets)[0].masked_fill(nobody, 0)
         cf = c.float()
         dt, Bm, Cm = self._split((cf @ self.W_x).bfloat16())
-        s = self.scan.forward(c, dt, self.A, Bm, Cm, self.D, z, self.dt_bias, None, offsets)[0].float()
+        s = self.scan.forward(c, dt, self.A, Bm, Cm, self.D, z, self.dt_bias, None, offsets)[0].float().masked_fill_(nobody, 0)
         y = x + s @ self.W_o
         logits = (y @ self.E.T).bfloat16()
         count = (targets >= 0).sum()
@@ -185,12 +189,12 @@ class SelLm:
         torch.mm(s.T, dy, out=dW_o)
         g = self.scan.backward(c, dt, self.A, Bm, Cm, (dy @ self.W_o.T).bfloat16(), self.D, z, self.dt_bias, None, None, offsets)
         dA.copy_(g.dA), dD.copy_(g.dD), ddt_bias.copy_(g.ddt_bias)
-        dh = torch.cat([g.ddt.float(), g.dB.float(), g.dC.float()], -1)
+        dh = torch.cat([g.ddt.float(), g.dB.float(), g.dC.float()], -1).masked_fill_(nobody, 0)
         torch.mm(cf.T, dh, out=dW_x)
         dc = (g.dx.float() + dh @ self.W_x.T).bfloat16()
         du, gw, gb, _ = self.conv.backward(u, self.w, dc, self.b, None, None, offsets)
         dw.copy_(gw), db.copy_(gb)
-        duz = torch.cat([du.float(), g.dz.float()], -1)
+        duz = torch.cat([du.float(), g.dz.float()], -1).masked_fill_(nobody, 0)
         torch.mm(x.T, duz, out=dW_in)
         dx = dy + duz @ self.W_in.T
         # sorted sums: a token that occurs often gets the same bits every time
