@@ -262,7 +262,10 @@ struct KeyLevel {
             all = k.tokens;
         }
 #pragma unroll
-        for (int i = 0; i < PER; ++i) c[i] = all[min(int(threadIdx.x) * PER + i, KEYS)];
+        for (int i = 0; i < PER; ++i) {
+            const int bin = int(threadIdx.x) * PER + i;
+            c[i] = bin < KEYS ? all[bin] : 0;           // the last threads have fewer bins: nothing there may be crossed
+        }
         if (blocks > 1) __syncthreads();
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
