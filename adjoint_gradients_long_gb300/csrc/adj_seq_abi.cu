@@ -63,7 +63,9 @@ adj_status check_offsets(int32_t packed, const int64_t *offsets) {
     if ((packed != 0) != (offsets != nullptr)) return ADJ_EINVAL;
     return aligned(offsets, 8) ? ADJ_OK : ADJ_EALIGN;
 }
-adj_status check_slots(int64_t B, int64_t n_slots, const int32_t *slots) {
+// a pool without entries needs no address: every slot is outside it
+adj_status check_pool(int64_t B, const void *state, int64_t n_slots, const int32_t *slots) {
+    ADJ_TRY(B && n_slots ? need({state}) : may({state}));
     if (slots && !aligned(slots, 4)) return ADJ_EALIGN;
     return n_slots < 0 || (!slots && n_slots < B) ? ADJ_ESHAPE : ADJ_OK;
 }
@@ -152,9 +154,9 @@ adj_status adj_conv_step(const adj_conv_dims *dims, const void *x, const float *
                          int64_t n_slots, const int32_t *slots, void *y, void *stream) {
     ConvArgs a;
     ADJ_TRY(check_conv(dims, true, a));
-    if (a.q.B) ADJ_TRY(need({x, w, state, y}));
+    if (a.q.B) ADJ_TRY(need({x, w, y}));
     ADJ_TRY(may({bias}));
-    ADJ_TRY(check_slots(a.q.B, n_slots, slots));
+    ADJ_TRY(check_pool(a.q.B, state, n_slots, slots));
     if (a.q.B == 0) return ADJ_OK;
     ADJ_TRY(apart({y, state}, {x, w, bias, slots}));
     if (y == state) return ADJ_EINVAL;
@@ -210,9 +212,9 @@ adj_status adj_ssm_step(const adj_ssm_dims *dims, const void *x, const void *dt,
                         int64_t n_slots, const int32_t *slots, void *y, void *stream) {
     SsmArgs a;
     ADJ_TRY(check_ssm(dims, true, a));
-    if (a.q.B) ADJ_TRY(need({x, dt, A, Bm, Cm, state, y}));
+    if (a.q.B) ADJ_TRY(need({x, dt, A, Bm, Cm, y}));
     ADJ_TRY(may({D, z, dt_bias}));
-    ADJ_TRY(check_slots(a.q.B, n_slots, slots));
+    ADJ_TRY(check_pool(a.q.B, state, n_slots, slots));
     if (a.q.B == 0) return ADJ_OK;
     ADJ_TRY(apart({y, state}, {x, dt, A, Bm, Cm, D, z, dt_bias, slots}));
     if (y == state) return ADJ_EINVAL;

@@ -374,8 +374,8 @@ adj_status adj_grad_clip(const adj_grad_seg *segs, int64_t nseg, float max_norm,
  * projection), multiples of 16 bytes.  No output may overlap an input (s1 with s0, ds0
  * with ds1, a step's y with what it reads) or another output; an input's address as an output is refused.  A pool of states has n_slots entries; slots [B] int32
  * gives the entry of each sequence (NULL: entry b, needs n_slots >= B).  A slot outside
- * [0, n_slots) leaves the pool untouched and gives a row of zeros (the padding of a batch); a
- * slot given twice is a race.
+ * [0, n_slots) leaves the pool untouched and gives a row of zeros (the padding of a batch; a pool without
+ * entries may be NULL); a slot given twice is a race.
  * ------------------------------------------------------------------------- */
 
 /* Short causal convolution, each channel with its own W taps.  With the list
