@@ -46,7 +46,7 @@ constexpr int32_t MOST_CHANNELS = 1 << 20;
 adj_status check_rows(int64_t B, int64_t T, int32_t P, int32_t packed, bool step, int64_t &rows) {
     rows = 0;
     if (B < 0 || B >= MOST_ROWS || (!step && (T < 0 || T >= MOST_ROWS))) return ADJ_ESHAPE;
-    if (packed != 0 && packed != 1) return ADJ_EINVAL;
+    if (!step && packed != 0 && packed != 1) return ADJ_EINVAL;
     if (P < 8 || P % 8 || P > MOST_CHANNELS) return ADJ_ESHAPE;
     rows = step ? B : packed ? T : B * T;
     return rows < MOST_ROWS ? ADJ_OK : ADJ_ESHAPE;
