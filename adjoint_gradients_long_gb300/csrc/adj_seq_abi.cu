@@ -118,7 +118,7 @@ adj_status adj_conv_fwd(const adj_conv_dims *dims, const void *x, const float *w
     ADJ_TRY(check_offsets(dims->packed, offsets));
     if (a.q.rows) ADJ_TRY(need({x, w, y}));
     ADJ_TRY(may({bias, s0, s1}));
-    ADJ_TRY(apart({y, s1}, {x, w, bias, s0}));
+    ADJ_TRY(apart({y, s1}, {x, w, bias, s0, offsets}));
     a.q.off = offsets;
     a.x = x; a.w = w; a.bias = bias; a.s0 = s0; a.y = y; a.s1 = s1;
     if (a.q.B == 0) return ADJ_OK;
@@ -139,7 +139,7 @@ adj_status adj_conv_bwd(const adj_conv_dims *dims, const void *x, const float *w
     if (a.q.rows) ADJ_TRY(need({x, go, dx}));
     ADJ_TRY(need({w, dw}));
     ADJ_TRY(may({bias, s0, ds1, dbias, ds0}));
-    ADJ_TRY(apart({dx, dw, dbias, ds0}, {x, w, bias, s0, go, ds1}));
+    ADJ_TRY(apart({dx, dw, dbias, ds0}, {x, w, bias, s0, offsets, go, ds1}));
     if (!ws) return ADJ_EINVAL;
     if (!aligned(ws, 256)) return ADJ_EALIGN;
     if (ws_bytes < WS_HEADER + conv_ws_bytes(a)) return ADJ_EWORKSPACE;
@@ -178,7 +178,7 @@ adj_status adj_ssm_fwd(const adj_ssm_dims *dims, const void *x, const void *dt, 
     ADJ_TRY(check_offsets(dims->packed, offsets));
     if (a.q.rows) ADJ_TRY(need({x, dt, A, Bm, Cm, y}));
     ADJ_TRY(may({D, z, dt_bias, s0, s1}));
-    ADJ_TRY(apart({y, s1}, {x, dt, A, Bm, Cm, D, z, dt_bias, s0}));
+    ADJ_TRY(apart({y, s1}, {x, dt, A, Bm, Cm, D, z, dt_bias, s0, offsets}));
     ADJ_TRY(plan(a, false, ws, ws_bytes));
     if (a.q.B == 0) return ADJ_OK;
     a.q.off = offsets;
@@ -198,7 +198,7 @@ adj_status adj_ssm_bwd(const adj_ssm_dims *dims, const void *x, const void *dt, 
     ADJ_TRY(need({A, dA}));
     if ((z != nullptr) != (dz != nullptr)) return ADJ_EINVAL;
     ADJ_TRY(may({D, z, dt_bias, s0, ds1, dD, dz, ddt_bias, ds0}));
-    ADJ_TRY(apart({dx, ddt, dA, dB, dC, dD, dz, ddt_bias, ds0}, {x, dt, A, Bm, Cm, D, z, dt_bias, s0, go, ds1}));
+    ADJ_TRY(apart({dx, ddt, dA, dB, dC, dD, dz, ddt_bias, ds0}, {x, dt, A, Bm, Cm, D, z, dt_bias, s0, offsets, go, ds1}));
     ADJ_TRY(plan(a, true, ws, ws_bytes));
     a.q.off = offsets;
     a.x = x; a.dt = dt; a.A = A; a.Bm = Bm; a.Cm = Cm; a.D = D; a.z = z; a.bias = dt_bias; a.s0 = s0;
