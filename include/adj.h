@@ -417,7 +417,7 @@ adj_status adj_conv_step(const adj_conv_dims *dims, const void *x, const float *
  *   x, dt, z, y [rows,P], Bm, Cm [rows,N] x_dtype; A [P,N], D, dt_bias [P] fp32
  *   s0, s1 [B,P,N] fp32: the states before the first and after the last token
  * A is expected <= 0; larger ones are allowed as long as products of exp(d A) over a sequence stay
- * finite.  dt of minus infinity is a step of zero: the token leaves the state as it is.
+ * finite.  dt of minus infinity is a step of zero: a token of finite x and B leaves the state as it is.
  * P a multiple of 8; N 8, 16, 32 or 64; states and sums in fp32. */
 typedef struct {
     int64_t B, T;
@@ -459,8 +459,9 @@ adj_status adj_ssm_step(const adj_ssm_dims *dims, const void *x, const void *dt,
  *   token     the first kept j, by index, with sum of the kept w_i, i <= j, > u[n] * their total
  *   logp      log(w_j / total), from (x_j - m) / temperature itself
  * u [N] fp32 in [0, 1) (others are taken as the nearest such number, NaN as 0).  Temperature 0 takes
- * the largest logit, the lowest index first; top_p >= 1 and min_p <= 0 keep all, min_p > 1 and top_p <= 0
- * the largest alone.  Minus infinity is a masked token.  Weights are off by one unit at most; as they
+ * the largest logit, the lowest index first; top_p >= 1 and min_p <= 0 keep all, min_p > 1 is taken as 1
+ * (the weights of 2^40, equals of the largest logit among them), top_p <= 0 keeps the first alone.  Minus infinity
+ * is a masked token, and so is one whose distance from m is beyond fp32.  Weights are off by one unit at most; as they
  * are whole numbers the result does not depend on the order of sums, and equal rows give equal tokens.
  * token [N] int64 and logp [N] fp32 (NULL: not written).  Without a finite value a row gives token -1 and
  * logp -inf; with a NaN or +inf in it, or a setting that is NaN or a negative temperature, token -1 and
