@@ -5,8 +5,10 @@
 // the sums of a token in registers, so each value is read once (and W-1 of them again by the run
 // after it, mostly from L2) and written once.  Bound by HBM: the arithmetic is W multiply-adds and
 // one sigmoid a value.  Four channels, not eight: eight took 162 registers forwards and 255 backwards,
-// too few warps to cover HBM's latency.  Measured: 32768 tokens x 2048 channels bf16 51 us (0.77 of the copy
-// bandwidth), gradients of 16384 tokens 54 us (0.55).  A block holds VG quads of channels side by side and
+// too few warps to cover HBM's latency.  With W = 4 the gradients still spill (60 bytes stored and 164 loaded
+// a thread in bf16, 80 and 160 in fp32), and so do the outputs in fp32 (52 and 68).  Measured: 32768 tokens x
+// 2048 channels bf16 50 us (0.80 of the copy bandwidth), fp32 96 (0.83); gradients of 16384 tokens bf16 54 us
+// (0.55), fp32 78 (0.76).  A block holds VG quads of channels side by side and
 // 256 / VG runs, VG the power of two that covers the channels, 64 at most: neighbouring threads
 // read neighbouring quads.
 //
@@ -395,7 +397,11 @@ struct ConvGrid {
     int64_t runs;
 };
 // The longest runs (the fewest tokens read twice) of which there are still `want` threads' worth for
-// the loads in flight to cover HBM's latency.
+// the loads in flight to cover HBM's latency.  Measured with 2048 channels, bf16, us (tokens: as it is; half of `want`;
+// twice): outputs 16384: 27.9; 28.6; 31.8, 4096: 9.9; 9.2; 13.7.  Gradients 16384: 54.7; 54.7; 65.3, 4096: 20.9; 20.2;
+// 27.3.  Half the longest run: outputs 32768 50.0 against 48.2, gradients 16384 65.2 against 54.7; twice: the same, but
+// gradients 32768 97 against 108.  Twice the shortest: outputs 77 3.9 against 3.4, gradients 512 12.4 against 9.9; half
+// (gradients): 11.4 against 9.9.
 ConvGrid conv_grid(const ConvArgs &a, int longest, int shortest, int64_t want) {
     const int pv = a.P / 4;
     ConvGrid g{1, longest, 0};

@@ -919,8 +919,10 @@ __global__ __launch_bounds__(256) void k_ssm_join(const SsmArgs a, int64_t cols,
 // ---------------------------------------------------------------- single tokens
 // A thread takes four states of each of K channels, K the number of quads of states, 4 at most: its K loads of
 // the state are in flight together, and the steps of the K channels are formed by one lane each.
-// The state is read and written once, bound by HBM; blocks of 128, not 256: 20.7 us against 22.7 for 256 sequences
-// of 2048 x 16 out of cold memory, where all blocks together are three turns of the machine.
+// The state is read and written once.  256 sequences of 2048 x 16 bf16 (34 MB of states): 11.4 us where the pool stays in
+// L2 between calls, 13.9 with twelve pools by turns, 20.7 behind a write over all of L2, which has to leave it first;
+// the copy bandwidth gives 10.5.  Blocks of 128, not 256: 20.7 us against 22.7 in the last case; all blocks together are
+// three turns of the machine, and nothing is in flight between two of them.
 template <class T, int N>
 __global__ __launch_bounds__(128) void k_ssm_step(const SsmArgs a, float *state, int64_t n_slots, const int32_t *slots) {
     constexpr int NQ = N / 4, K = NQ < 4 ? NQ : 4;
@@ -982,8 +984,11 @@ cudaError_t pick(int N, bool bf16, F f) {
     return bf16 ? sizes(__nv_bfloat16()) : sizes(0.f);
 }
 
-// Two channels a thread, not four, for a prompt so short that its walk is a matter of latency, unless its
-// channels fill the SMs by themselves.
+// Two channels a thread, not four, and one segment, for a prompt so short that its walk is a matter of latency, unless
+// its channels fill the SMs by themselves.  The border, 2048 x 16 bf16, us so and with four channels and segments
+// of 64 tokens: 64 tokens 8.2 and 11.9, 128 14.0 and 23.7, 192 19.9 and 24.3, 256 25.3 and 24.3, 384 36.8 and 24.7;
+// 2048 x 64: 192 tokens 24.4 and 29.8, 256 31.5 and 30.1, 384 45.6 and 38.2; 8192 x 16: 256 27.2 and 31.6, 384 39.2
+// and 40.0.
 bool brief(const SsmArgs &a) { return a.q.rows <= 256 && seq_div(a.P, warp_channels(a.N, 2)) < 608; }
 int64_t columns(const SsmArgs &a, bool bwd) {
     return bwd ? seq_div(a.P, WPB * warp_channels(a.N, 2)) : brief(a) ? seq_div(a.P, warp_channels(a.N, 1))
