@@ -443,8 +443,8 @@ class SelScan(_Sel):
     y = v z sigmoid(z) with z, else v.  x, dt, z [B,T,P], Bm, Cm [B,T,N]; packed: T tokens of all
     sequences together, [T,P] and [T,N], and offsets [B+1] int64 where each begins (include/adj.h,
     "Sequences"); rows of no sequence are neither read nor written: in the outputs they keep an older
-    call's values, so products over all rows leave them out or clear them.  A [P,N], D, dt_bias [P] and states [B,P,N] fp32.  backward: also hold what the
-    gradients need."""
+    call's values, so products over all rows leave them out or clear them.  A [P,N], D, dt_bias [P] and
+    states [B,P,N] fp32.  backward: also hold what the gradients need."""
 
     def __init__(self, B, T, P, N, x_bf16=True, packed=False, backward=False, device="cuda"):
         super().__init__(B, T, P, N, packed, x_bf16, device)
